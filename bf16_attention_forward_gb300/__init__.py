@@ -1,12 +1,13 @@
 """bf16 attention forward for GB300 (sm_103a): Python binding of the C-ABI library.
 
 The binding only marshals arguments: every step of the computation runs in the library's
-CUDA kernels (``csrc/attn_fwd.cu``, ABI in ``include/bf16_attn.h``).  PyTorch supplies
+CUDA kernels (``csrc/*.cu``, ABI in ``include/bf16_attn.h``).  PyTorch supplies
 device memory and the current stream.  There is no CPU fallback: if the compiled library
 is missing, importing the binding's entry points raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -14,6 +15,7 @@ import threading
 from . import build as _build
 
 LAYOUTS = {"bshd": 0, "bhsd": 1}
+PAIRINGS = {"adjacent": 0, "halves": 1}
 MODES = {"rtne": 0, "rtna": 1, "rtz": 2}
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
           3: "ATTN_ERR_MISALIGNED", 4: "ATTN_ERR_ALIAS", 5: "ATTN_ERR_NO_DEVICE",
@@ -23,7 +25,9 @@ EXPORTS = ("attn_fwd", "attn_fwd_ws", "attn_fwd_noalloc", "attn_fwd_ex", "attn_f
            "attn_plan_ex", "attn_get_device_status", "attn_status_string", "attn_version",
            "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_get_device_status",
            "attn_fwd_varlen", "attn_fwd_varlen_workspace_size", "attn_fwd_paged",
-           "attn_fwd_paged_workspace_size", "attn_bwd_varlen", "attn_bwd_varlen_workspace_size")
+           "attn_fwd_paged_workspace_size", "attn_bwd_varlen", "attn_bwd_varlen_workspace_size",
+           "attn_rope", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size",
+           "attn_paged_evict", "attn_paged_evict_workspace_size", "attn_cache_get_device_status")
 
 
 class AttnError(RuntimeError):
@@ -79,6 +83,42 @@ class BwdVarlenArgs(ctypes.Structure):
                                                "cu_seqlens_q", "cu_seqlens_k")] + \
                [(n, ctypes.c_int64) for n in ("B", "H", "Hkv", "total_q", "total_k", "d")] + \
                [(n, ctypes.c_int32) for n in ("causal", "wait_limit_ms", "reserved", "reserved2")]
+
+
+class RopeArgs(ctypes.Structure):
+    """attn_rope_args_t: the argument set of attn_rope."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_out", "k", "k_out", "positions", "freqs", "axes")] + \
+               [(n, ctypes.c_int64) for n in ("B", "S", "H", "Hkv", "d")] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "q_out_stride", "k_stride", "k_out_stride")] + \
+               [(n, ctypes.c_int64) for n in ("pos_axis_stride", "pos_batch_stride")] + \
+               [(n, ctypes.c_int32) for n in ("pairs", "num_axes", "pairing", "inverse")]
+
+
+class AppendArgs(ctypes.Structure):
+    """attn_append_args_t: the argument set of attn_paged_append."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_cache", "v_cache", "q", "q_out", "cu_seqlens_new",
+                                               "seqlens_k", "block_table", "positions", "freqs", "axes")] + \
+               [(n, ctypes.c_int64) for n in ("B", "H", "Hkv", "total", "num_pages", "page_size", "max_pages",
+                                              "d")] + \
+               [(n, ctypes.c_int64 * 2) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [("pos_axis_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("pairs", "num_axes", "pairing", "reserved")]
+
+
+class DecodeArgs(ctypes.Structure):
+    """attn_decode_args_t: the argument set of attn_paged_decode."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache", "o", "lse", "weights", "seqlens_k",
+                                               "block_table")] + \
+               [(n, ctypes.c_int64) for n in ("B", "H", "Hkv", "num_pages", "page_size", "max_pages", "d")] + \
+               [(n, ctypes.c_int32) for n in ("round_mode", "reserved")]
+
+
+class EvictArgs(ctypes.Structure):
+    """attn_evict_args_t: the argument set of attn_paged_evict."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "weights", "weights_out", "seqlens_k",
+                                               "seqlens_out", "block_table")] + \
+               [(n, ctypes.c_int64) for n in ("B", "Hkv", "num_pages", "page_size", "max_pages", "d", "budget",
+                                              "sinks", "recent")]
 
 
 class Plan(ctypes.Structure):
@@ -148,6 +188,16 @@ def load(path: str | None = None):
         lib.attn_bwd_varlen.argtypes = [ctypes.POINTER(BwdVarlenArgs), vp, ctypes.c_size_t, vp]
         lib.attn_bwd_varlen_workspace_size.restype = ctypes.c_size_t
         lib.attn_bwd_varlen_workspace_size.argtypes = [ctypes.POINTER(BwdVarlenArgs)]
+        for name, args in (("attn_rope", RopeArgs), ("attn_paged_append", AppendArgs)):
+            getattr(lib, name).restype = i32
+            getattr(lib, name).argtypes = [ctypes.POINTER(args), vp]
+        for name, args in (("attn_paged_decode", DecodeArgs), ("attn_paged_evict", EvictArgs)):
+            getattr(lib, name).restype = i32
+            getattr(lib, name).argtypes = [ctypes.POINTER(args), vp, ctypes.c_size_t, vp]
+            getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
+            getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args)]
+        lib.attn_cache_get_device_status.restype = i32
+        lib.attn_cache_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         lib.attn_plan.restype = i32
         lib.attn_plan.argtypes = [i64] * 6 + [ctypes.POINTER(Options), ctypes.POINTER(Plan)]
         lib.attn_get_device_status.restype = i32
@@ -580,4 +630,313 @@ def bwd_device_status(stream=None) -> tuple:
     s = stream if stream is not None else torch.cuda.current_stream()
     site = ctypes.c_int32(0)
     st = load().attn_bwd_get_device_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(site))
+    return int(st), int(site.value)
+
+
+# ------------------------------------------------------------- around the paged K/V cache
+def _on(device, stream):
+    """Context in which a call's tensors are allocated and its kernels launched: the tensors' device, and
+    `stream` (an allocation belongs to the stream that uses it)."""
+    import torch
+    if stream is not None:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+        return torch.cuda.stream(s)
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _tensor(t, name, dtype, dim, device=None, contiguous=True):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.dim() != dim:
+        raise TypeError("%s must be a CUDA %s tensor of %d dimension(s)" % (name, str(dtype)[6:], dim))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if device is not None and t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    return t
+
+
+def _heads(t, name, dim, device=None):
+    """A bf16 tensor whose heads are contiguous; any strides else."""
+    import torch
+    _tensor(t, name, torch.bfloat16, dim, device, contiguous=False)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the head dimension of %s must be contiguous" % name)
+    return t
+
+
+def rope_freqs(axis_dims, base: float = 10000.0, spectrum: str = "axis", scale=None, device="cuda"):
+    """(freqs, axes) of :func:`attn_rope` for rotated dimensions split over axes: ``axis_dims`` gives
+    each axis its (even) number of dimensions.  ``spectrum``: "axis", pair i of an axis with n
+    dimensions turns at base ** (-2 i / n) radians per position; "shared", pair p of all P pairs at
+    base ** (-p / P), whatever axis it takes its position from.  ``scale``: optional factor on
+    each axis's positions (interpolation)."""
+    import torch
+    dims = [int(n) for n in axis_dims]
+    if not dims or any(n < 2 or n % 2 for n in dims):
+        raise ValueError("axis_dims must be even numbers >= 2")
+    if spectrum not in ("axis", "shared") or not base > 0:
+        raise ValueError("spectrum must be axis/shared and base positive")
+    scale = [1.0] * len(dims) if scale is None else [float(x) for x in scale]
+    if len(scale) != len(dims):
+        raise ValueError("scale must give one factor per axis")
+    freqs, axes, pairs = [], [], sum(dims) // 2
+    for a, n in enumerate(dims):
+        for i in range(n // 2):
+            e = 2.0 * i / n if spectrum == "axis" else len(freqs) / pairs
+            freqs.append(scale[a] * float(base) ** -e)
+            axes.append(a)
+    return (torch.tensor(freqs, dtype=torch.float64, device=device),
+            torch.tensor(axes, dtype=torch.int32, device=device))
+
+
+def _rope_tables(positions, freqs, axes, pairing, device, pos_dims):
+    import torch
+    if pairing not in PAIRINGS:
+        raise ValueError("pairing must be adjacent or halves")
+    _tensor(freqs, "freqs", torch.float64, 1, device)
+    _tensor(axes, "axes", torch.int32, 1, device)
+    if freqs.numel() != axes.numel():
+        raise ValueError("freqs and axes must have one entry per pair")
+    _tensor(positions, "positions", torch.int32, positions.dim() if positions.dim() in pos_dims else pos_dims[0], device,
+            contiguous=False)
+    if positions.shape[-1] > 1 and positions.stride(-1) != 1:
+        raise ValueError("the token dimension of positions must be contiguous")
+
+
+def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str = "adjacent", q_out=None, k_out=None,
+              inverse: bool = False, stream=None):
+    """Rotary positions with several axes: q (and k, unless it is None) with pair p of every head turned
+    by positions[axes[p]] * freqs[p] radians.
+
+    ``q``/``k``: CUDA bf16, 4-D in ``layout`` or packed [total, heads, d]; any strides that keep a head
+    contiguous and rows 16-byte aligned (views of a fused projection).  ``positions``: CUDA int32
+    [axes, S] (one grid for every batch entry), [axes, B, S], or [axes, total] for packed tensors.
+    ``freqs``/``axes``: float64 and int32 [pairs], as :func:`rope_freqs` makes them; elements past
+    2 * pairs pass through.  ``pairing``: "adjacent" elements (2p, 2p + 1) or "halves" (p, p + pairs).
+    ``q_out``/``k_out``: optional outputs (q and k themselves: in place).  ``inverse`` turns by the negative
+    angles.  Returns ``(q_out, k_out)``, or ``q_out`` when k is None."""
+    import torch
+    if layout not in LAYOUTS:
+        raise ValueError("layout must be bshd or bhsd")
+    dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+    _heads(q, "q", dim)
+    dev = q.device
+    _rope_tables(positions, freqs, axes, pairing, dev, (2, 3) if dim == 4 else (2,))
+    order = (0, 1) if dim == 3 else (0, 1, 2) if layout == "bshd" else (0, 2, 1)     # (batch,) token, head
+
+    def shape(t):
+        return tuple(t.shape[i] for i in order)
+
+    def strides(t):
+        s = tuple(t.stride(i) for i in order)
+        return s if dim == 4 else (0,) + s
+
+    B, S, H = shape(q) if dim == 4 else (1,) + shape(q)
+    if k is not None:
+        _heads(k, "k", dim, dev)
+        if k.shape[-1] != q.shape[-1] or shape(k)[:-1] != shape(q)[:-1]:
+            raise ValueError("q and k must agree in all but their heads")
+    if positions.shape[-1] != S or (positions.dim() == 3 and positions.shape[1] != B):
+        raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
+    with _on(dev, stream):
+        outs = []
+        for t, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+            if t is None:
+                outs.append(None)
+                continue
+            if o is None:
+                o = torch.empty(t.shape, dtype=t.dtype, device=dev)
+            elif tuple(_heads(o, name, dim, dev).shape) != tuple(t.shape):
+                raise ValueError("%s must have its input's shape" % name)
+            outs.append(o)
+        qo, ko = outs
+        none = (0, 0, 0)
+        a = RopeArgs(q.data_ptr(), qo.data_ptr(), 0 if k is None else k.data_ptr(), 0 if k is None else ko.data_ptr(),
+                     positions.data_ptr(), freqs.data_ptr(), axes.data_ptr(), B, S, H,
+                     0 if k is None else k.shape[order[-1]], q.shape[-1], strides(q), strides(qo),
+                     none if k is None else strides(k), none if k is None else strides(ko), positions.stride(0),
+                     positions.stride(1) if positions.dim() == 3 else 0, freqs.numel(), positions.shape[0],
+                     PAIRINGS[pairing], int(bool(inverse)))
+        if S > 0:
+            st = load().attn_rope(ctypes.byref(a), _stream_ptr(stream, dev))
+            if st != 0:
+                raise AttnError(st, "attn_rope")
+    return qo if k is None else (qo, ko)
+
+
+def attn_rope_bwd(dq, dk, positions, freqs, axes, layout: str = "bshd", pairing: str = "adjacent", dq_out=None,
+                  dk_out=None, stream=None):
+    """Gradients with respect to :func:`attn_rope`'s inputs from those with respect to its outputs (the rotation
+    by the negative angles; a rotation's inverse is its transpose).  Arguments as there."""
+    return attn_rope(dq, dk, positions, freqs, axes, layout, pairing, dq_out, dk_out, inverse=True, stream=stream)
+
+
+def _check_cache(k_cache, v_cache, block_table, seqlens_k):
+    import torch
+    dev = _tensor(k_cache, "k_cache", torch.bfloat16, 4).device
+    _tensor(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    _tensor(seqlens_k, "seqlens_k", torch.int32, 1, dev)
+    _tensor(block_table, "block_table", torch.int32, 2, dev)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if seqlens_k.numel() != block_table.shape[0]:
+        raise ValueError("seqlens_k must hold one length per row of block_table")
+    return dev
+
+
+def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_table, q=None, q_out=None,
+                      positions=None, freqs=None, axes=None, pairing: str = "adjacent", stream=None):
+    """Write new tokens' keys and values to their slots of a paged cache; with ``positions``, ``freqs`` and
+    ``axes`` (as in :func:`attn_rope`, positions [axes, total]) the keys, and the queries ``q`` if given,
+    are rotated on the way.
+
+    ``k``/``v``: [total, Hkv, d], ``q``: [total, H, d] (CUDA bf16, heads contiguous, token strides free);
+    ``cu_seqlens_new``: CUDA int32 [B + 1] row offsets of each sequence's new tokens;
+    ``seqlens_k``: int32 [B] lengths WITH the new tokens, as :func:`attn_fwd_paged` and
+    :func:`attn_paged_decode` then take them; ``block_table``: int32 [B, max_pages].  Tokens whose slot or
+    page the cache does not have are not written and are reported by :func:`cache_device_status`.
+    Returns ``q_out`` (dense [total, H, d]; rows outside every sequence are left as they were), or None
+    without ``q``."""
+    import torch
+    dev = _check_cache(k_cache, v_cache, block_table, seqlens_k)
+    _heads(k, "k", 3, dev)
+    _heads(v, "v", 3, dev)
+    _tensor(cu_seqlens_new, "cu_seqlens_new", torch.int32, 1, dev)
+    B, (total, Hkv, d) = seqlens_k.numel(), k.shape
+    if v.shape != k.shape or k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("k and v must be [total, Hkv, d] with the cache's Hkv and d")
+    if cu_seqlens_new.numel() != B + 1:
+        raise ValueError("cu_seqlens_new must hold B + 1 offsets")
+    rotate = positions is not None
+    if (freqs is not None) != rotate or (axes is not None) != rotate:
+        raise ValueError("positions, freqs and axes go together")
+    if rotate:
+        _rope_tables(positions, freqs, axes, pairing, dev, (2,))
+        if positions.shape[1] != total:
+            raise ValueError("positions must be [axes, total]")
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    H = 0
+    if q is not None:
+        _heads(q, "q", 3, dev)
+        H = q.shape[1]
+        if q.shape[0] != total or q.shape[2] != d:
+            raise ValueError("q must be [total, H, d]")
+        if q_out is not None and (tuple(_tensor(q_out, "q_out", torch.bfloat16, 3, dev).shape) != tuple(q.shape)):
+            raise ValueError("q_out must have q's shape")
+    with _on(dev, stream):
+        if q is not None and q_out is None:
+            q_out = torch.zeros((total, H, d), dtype=torch.bfloat16, device=dev)
+        a = AppendArgs(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                       0 if q is None else q.data_ptr(), 0 if q is None else q_out.data_ptr(), cu_seqlens_new.data_ptr(),
+                       seqlens_k.data_ptr(), block_table.data_ptr(), positions.data_ptr() if rotate else 0,
+                       freqs.data_ptr() if rotate else 0, axes.data_ptr() if rotate else 0, B, H, Hkv, total,
+                       k_cache.shape[0], k_cache.shape[1], block_table.shape[1], d,
+                       (0, 0) if q is None else (q.stride(0), q.stride(1)), (k.stride(0), k.stride(1)),
+                       (v.stride(0), v.stride(1)), positions.stride(0) if rotate else 0,
+                       freqs.numel() if rotate else 0, positions.shape[0] if rotate else 1, PAIRINGS[pairing], 0)
+        if total > 0:
+            st = load().attn_paged_append(ctypes.byref(a), _stream_ptr(stream, dev))
+            if st != 0:
+                raise AttnError(st, "attn_paged_append")
+    return q_out
+
+
+def _workspace(lib_call, a, workspace, device):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(int(lib_call(ctypes.byref(a))), 16), dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None, o=None, lse=None,
+                      round: str = "rtne", return_lse: bool = False, stream=None, workspace=None):
+    """Attention of one new token per sequence over a paged K/V cache.
+
+    ``q``: [B, H, d]; ``k_cache``/``v_cache``: [num_pages, page_size, Hkv, d] (CUDA bf16, contiguous; any
+    page_size; Hkv divides H); ``seqlens_k``: CUDA int32 [B] (a sequence without keys gets NaN outputs and
+    -inf lse); ``block_table``: CUDA int32 [B, max_pages].  ``weights``: optional fp32
+    [B, Hkv, max_pages * page_size]; each key's softmax weight, summed over the query heads of its K/V
+    head, is added to it (what :func:`attn_paged_evict` goes by).  The work is split evenly over the SMs
+    whatever the lengths are.  A sequence with a bad length or page index is not written and is reported by
+    :func:`cache_device_status`.  ``workspace``: optional caller tensor (calls that may run at the same
+    time need one each); without it one is allocated here.  Returns ``o`` or ``(o, lse)`` (lse fp32 [B, H])."""
+    import torch
+    if round not in MODES:
+        raise ValueError("round must be rtne/rtna/rtz")
+    dev = _check_cache(k_cache, v_cache, block_table, seqlens_k)
+    _tensor(q, "q", torch.bfloat16, 3, dev)
+    B, H, d = q.shape
+    P, ps, Hkv, dk = k_cache.shape
+    if B != seqlens_k.numel() or d != dk:
+        raise ValueError("q must be [B, H, d] with seqlens_k's B and the cache's d")
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError("k/v heads (%d) must divide the query heads (%d)" % (Hkv, H))
+    if weights is not None and tuple(_tensor(weights, "weights", torch.float32, 3, dev).shape) != (
+            B, Hkv, block_table.shape[1] * ps):
+        raise ValueError("weights must be [B, Hkv, max_pages * page_size]")
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty_like(q)
+        elif tuple(_tensor(o, "o", torch.bfloat16, 3, dev).shape) != tuple(q.shape):
+            raise ValueError("o must be a contiguous CUDA bf16 tensor shaped like q")
+        if lse is None and return_lse:
+            lse = torch.empty((B, H), dtype=torch.float32, device=dev)
+        if lse is not None and tuple(_tensor(lse, "lse", torch.float32, 2, dev).shape) != (B, H):
+            raise ValueError("lse must be a contiguous CUDA fp32 tensor [B, H]")
+        a = DecodeArgs(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                       0 if lse is None else lse.data_ptr(), 0 if weights is None else weights.data_ptr(),
+                       seqlens_k.data_ptr(), block_table.data_ptr(), B, H, Hkv, P, ps, block_table.shape[1], d,
+                       MODES[round], 0)
+        lib = load()
+        ws, nbytes = _workspace(lib.attn_paged_decode_workspace_size, a, workspace, dev)
+        st = lib.attn_paged_decode(ctypes.byref(a), ws.data_ptr(), nbytes, _stream_ptr(stream, dev))
+        if st != 0:
+            raise AttnError(st, "attn_paged_decode")
+    return (o, lse) if (return_lse or lse is not None) else o
+
+
+def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: int, sinks: int = 0,
+                     recent: int = 0, seqlens_out=None, weights_out=None, stream=None, workspace=None):
+    """Cut every sequence longer than ``budget`` to ``budget`` keys, for each K/V head on its own: the first
+    ``sinks`` slots, the last ``recent`` ones, and the keys of largest ``weights`` between them (of
+    equal weights the lower slots; NaN ranks lowest).
+
+    Survivors below slot budget - recent stay where they are, those past it move into the freed slots in
+    order, and the recent keys follow up to the budget's end.  ``k_cache``/``v_cache`` (as in
+    :func:`attn_paged_decode`) are rewritten in place; ``weights`` [B, Hkv, max_pages * page_size] and
+    ``seqlens_k`` too, unless ``weights_out`` / ``seqlens_out`` take the new ones.  A sequence with a bad
+    length or page, or with a page that the table holds more than once, stays as it is and is reported
+    by :func:`cache_device_status`.  Returns ``seqlens_out``."""
+    import torch
+    dev = _check_cache(k_cache, v_cache, block_table, seqlens_k)
+    P, ps, Hkv, d = k_cache.shape
+    B, max_pages = block_table.shape
+    weights_out = weights if weights_out is None else weights_out
+    seqlens_out = seqlens_k if seqlens_out is None else seqlens_out
+    for t, name in ((weights, "weights"), (weights_out, "weights_out")):
+        if tuple(_tensor(t, name, torch.float32, 3, dev).shape) != (B, Hkv, max_pages * ps):
+            raise ValueError("%s must be [B, Hkv, max_pages * page_size]" % name)
+    if _tensor(seqlens_out, "seqlens_out", torch.int32, 1, dev).numel() != B:
+        raise ValueError("seqlens_out must hold B lengths")
+    with _on(dev, stream):
+        a = EvictArgs(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
+                      seqlens_k.data_ptr(), seqlens_out.data_ptr(), block_table.data_ptr(), B, Hkv, P, ps, max_pages, d,
+                      int(budget), int(sinks), int(recent))
+        lib = load()
+        ws, nbytes = _workspace(lib.attn_paged_evict_workspace_size, a, workspace, dev)
+        st = lib.attn_paged_evict(ctypes.byref(a), ws.data_ptr(), nbytes, _stream_ptr(stream, dev))
+        if st != 0:
+            raise AttnError(st, "attn_paged_evict")
+    return seqlens_out
+
+
+def cache_device_status(stream=None) -> tuple:
+    """Synchronize and read/clear the status word of the rope, append, decode and evict kernels: (status, check)."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream()
+    site = ctypes.c_int32(0)
+    st = load().attn_cache_get_device_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(site))
     return int(st), int(site.value)

@@ -7,9 +7,9 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, "attn_fwd.cu"), os.path.join(CSRC, "attn_bwd.cu")]
-HEADERS = [os.path.join(CSRC, "ptx.cuh"),
-           os.path.join(os.path.dirname(HERE), "include", "bf16_attn.h")]
+SOURCES = [os.path.join(CSRC, n) for n in ("attn_fwd.cu", "attn_bwd.cu", "attn_cache.cu")]
+HEADERS = [os.path.join(CSRC, n) for n in ("ptx.cuh", "cache_common.cuh", "rope.cuh", "decode.cuh", "evict.cuh")] + \
+          [os.path.join(os.path.dirname(HERE), "include", "bf16_attn.h")]
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libbf16attn.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -35,7 +35,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC", "-t", "0",
            "-cudart", "static", "-o", tmp, *SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

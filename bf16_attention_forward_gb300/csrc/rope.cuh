@@ -1,0 +1,187 @@
+// rope.cuh -- rotary positions with several axes, and their form that writes a paged cache.
+//
+// Mathematics.  Pair p of a head's rotated dimensions turns by theta = pos[axis[p]] * freq[p]:
+//   y0 = x0 cos(theta) - x1 sin(theta),  y1 = x1 cos(theta) + x0 sin(theta),
+// with (x0, x1) = (x[2p], x[2p+1]) ("adjacent") or (x[p], x[p+P]) ("halves", P pairs); the
+// backward is the rotation by -theta.  The remaining dimensions pass through bit for bit.
+//
+// Angles.  Positions reach 2^31, where pos * freq in fp32 has no correct digit left.  The
+// kernel keeps freq / 2pi as a 64-bit binary fraction of a turn; an integer position times it,
+// modulo 2^64, is the fraction of a turn (whole turns drop out of the high end), exact
+// but for the fraction's own last bit: pos * 2^-64 turns, and pos * 2^-53 relative to the
+// frequency from its fp64 value.  The top 32 bits of the product, read as a signed number of
+// half turns in [-1, 1), go to sincospi.
+//
+// Bound: HBM bytes (each element read and written once).  One thread holds the cosines and
+// sines of the 8 pairs of 16 elements and applies them to those elements of several heads, so that
+// the sincospi work is shared by the heads of a token.
+#pragma once
+#include "cache_common.cuh"
+
+namespace cache {
+
+struct RopeTensor {       // byte strides
+    const char* src;
+    char* dst;
+    long long src_b, src_t, src_h, dst_b, dst_t, dst_h;
+    int heads;
+};
+
+struct RopeParams {
+    RopeTensor x[3];               // q, k, v (v is copied; only when appending)
+    const int32_t* positions;
+    const double* freqs;
+    const int32_t* axes;
+    long long pos_axis, pos_b;     // element strides of positions
+    long long S, tokens;           // tokens per batch entry, and in all
+    int pairs, num_axes, inverse, heads_per_thread, heads;
+    // appending
+    Pages pages;
+    const int32_t* cu_new;
+    const int32_t* seqlens_k;
+    int B;
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;
+constexpr int kCuStage = 1024;     // sequence offsets that a block searches in shared memory
+
+// bf16 pair (x0 in the low half) turned by (c, s)
+__device__ __forceinline__ uint32_t rotate_word(uint32_t w, float c, float s) {
+    const float x0 = __uint_as_float(w << 16), x1 = __uint_as_float(w & 0xFFFF0000u);
+    return ptx::pack_bf16x2(x0 * c - x1 * s, x1 * c + x0 * s);
+}
+
+template <int D, bool kHalves, bool kAppend>
+__global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kL = D / 16;     // threads of a token: 16 elements (two 16-byte chunks) of a head each
+    __shared__ unsigned long long turn[D / 2];
+    __shared__ int axis[D / 2];
+    __shared__ int cu_s[kAppend ? kCuStage : 1];
+    pdl_wait();
+    pdl_launch();
+    int bad = 0;
+    for (int i = threadIdx.x; i < p.pairs; i += kRopeThreads) {
+        double t = p.freqs[i] * 0.15915494309189533577;    // 1 / 2pi
+        t -= floor(t);
+        turn[i] = (unsigned long long)(t * 18446744073709551616.0);
+        axis[i] = p.axes[i];
+        bad |= (unsigned)axis[i] >= (unsigned)p.num_axes;
+    }
+    const bool staged = kAppend && p.B < kCuStage;
+    if constexpr (kAppend)
+        if (staged)
+            for (int i = threadIdx.x; i <= p.B; i += kRopeThreads) cu_s[i] = __ldg(p.cu_new + i);
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_AXES);
+        return;
+    }
+    const int l = threadIdx.x % kL;
+    const long long token = (long long)blockIdx.x * (kRopeThreads / kL) + threadIdx.x / kL;
+    if (token >= p.tokens) return;
+    const long long b = kAppend ? 0 : token / p.S, s = kAppend ? token : token - b * p.S;
+
+    long long row = -1;            // the token's row of the cache
+    if constexpr (kAppend) {
+        const int* cu = staged ? cu_s : p.cu_new;
+        // the last sequence that starts at or before the token (a later one, empty, may start there too)
+        int lo = 0, hi = p.B;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cu[mid] <= token) lo = mid; else hi = mid - 1;
+        }
+        if (lo >= p.B || cu[lo] > token) return;           // in front of the first sequence or behind the last
+        const int end = cu[lo + 1];
+        const long long len = __ldg(p.seqlens_k + lo), first = len - ((long long)end - cu[lo]);
+        const long long at = len - end + token;            // its slot in the sequence
+        if (first >= 0 && at >= 0 && at < (long long)p.pages.max_pages * p.pages.page_size)
+            row = page_row(p.pages, p.pages.table + (long long)lo * p.pages.max_pages, (int)at);
+        if (row < 0 && l == 0) report_invalid(ATTN_CACHE_SITE_APPEND);
+    }
+
+    // the two chunks of this thread, and the first pair of each
+    int ca, cb, pa, pb;
+    if constexpr (kHalves) {
+        const int rot = p.pairs / 8;
+        ca = l < rot ? l : 2 * rot + 2 * (l - rot);
+        cb = l < rot ? l + rot : ca + 1;
+        pa = l < rot ? 8 * l : p.pairs;
+        pb = pa + 4;
+    } else {
+        ca = l;
+        cb = l + kL;
+        pa = 4 * ca;
+        pb = 4 * cb;
+    }
+    float c[8], sn[8];
+    bool turned[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int pr = e < 4 ? pa + e : pb + e - 4;
+        turned[e] = pr < p.pairs;
+        c[e] = 1.0f;
+        sn[e] = 0.0f;
+        if (turned[e]) {
+            const long long pos = __ldg(p.positions + axis[pr] * p.pos_axis + b * p.pos_b + s);
+            const unsigned long long at = turn[pr] * (unsigned long long)pos;
+            sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn[e], &c[e]);
+            if (p.inverse) sn[e] = -sn[e];
+        }
+    }
+    const int h_begin = blockIdx.y * p.heads_per_thread;
+    const int h_end = min(h_begin + p.heads_per_thread, p.heads);
+    for (int h0 = h_begin; h0 < h_end; h0 += kRopeUnroll) {
+        uint4 xa[kRopeUnroll], xb[kRopeUnroll];
+        char* dst[kRopeUnroll];
+        bool copy[kRopeUnroll];
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            int h = h0 + u, t = 0;
+            dst[u] = nullptr;
+            copy[u] = false;
+            if (h >= h_end) continue;
+            if (h >= p.x[0].heads) { h -= p.x[0].heads; t = 1; }
+            if (kAppend && t == 1 && h >= p.x[1].heads) { h -= p.x[1].heads; t = 2; }
+            const RopeTensor& x = p.x[t];
+            if (kAppend && t > 0 && row < 0) continue;
+            const char* src = x.src + b * x.src_b + s * x.src_t + h * x.src_h;
+            dst[u] = x.dst + b * x.dst_b + (kAppend && t > 0 ? row : s) * x.dst_t + h * x.dst_h;
+            copy[u] = t == 2;
+            xa[u] = *reinterpret_cast<const uint4*>(src + ca * 16);
+            xb[u] = *reinterpret_cast<const uint4*>(src + cb * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            if (!dst[u]) continue;
+            if (!kAppend || !copy[u]) {
+                uint32_t wa[4] = {xa[u].x, xa[u].y, xa[u].z, xa[u].w}, wb[4] = {xb[u].x, xb[u].y, xb[u].z, xb[u].w};
+                if constexpr (kHalves) {
+                    if (turned[0]) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // elements 2i and 2i + 1 of both chunks
+                            const float a0 = __uint_as_float(wa[i] << 16), a1 = __uint_as_float(wa[i] & 0xFFFF0000u);
+                            const float b0 = __uint_as_float(wb[i] << 16), b1 = __uint_as_float(wb[i] & 0xFFFF0000u);
+                            wa[i] = ptx::pack_bf16x2(a0 * c[2 * i] - b0 * sn[2 * i],
+                                                     a1 * c[2 * i + 1] - b1 * sn[2 * i + 1]);
+                            wb[i] = ptx::pack_bf16x2(b0 * c[2 * i] + a0 * sn[2 * i],
+                                                     b1 * c[2 * i + 1] + a1 * sn[2 * i + 1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (turned[i]) wa[i] = rotate_word(wa[i], c[i], sn[i]);
+                        if (turned[4 + i]) wb[i] = rotate_word(wb[i], c[4 + i], sn[4 + i]);
+                    }
+                }
+                xa[u] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                xb[u] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+            }
+            *reinterpret_cast<uint4*>(dst[u] + ca * 16) = xa[u];
+            *reinterpret_cast<uint4*>(dst[u] + cb * 16) = xb[u];
+        }
+    }
+}
+
+}  // namespace cache

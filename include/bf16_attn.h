@@ -443,6 +443,164 @@ size_t attn_bwd_varlen_workspace_size(const attn_bwd_varlen_args_t* args);
 int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t workspace_bytes,
                     attn_stream_t stream);
 
+/*
+ * Around the paged K/V cache: rotary positions, appending, attention of one new token, eviction.
+ *
+ * Common to the four calls.  Tensors are bf16 with head dimension d = 128 or 64 unless said
+ * otherwise, device pointers 16-byte aligned (int32 and fp32 tensors 4-byte, fp64 8-byte).  The
+ * cache is k_cache, v_cache bf16 [num_pages][page_size][Hkv][d] with any page_size >= 1; key j of
+ * sequence b is slot j % page_size of page block_table[b * max_pages + j / page_size], as in
+ * attn_fwd_paged (which itself wants a page_size that is a multiple of 128).  All calls run on
+ * `stream`, allocate nothing and keep nothing between calls; a workspace is the caller's, and calls
+ * that may run at the same time need workspaces of their own.  Argument errors are returned as by
+ * attn_fwd; what only the device can see (lengths, page indices, axes) is reported through
+ * attn_cache_get_device_status() as ATTN_ERR_INVALID_ARG at the site given below.
+ */
+#define ATTN_CACHE_SITE_AXES 20     /* an axis outside 0 .. num_axes - 1: nothing is written           */
+#define ATTN_CACHE_SITE_APPEND 21   /* a new token's slot or page is not in the cache: k, v not written  */
+#define ATTN_CACHE_SITE_DECODE 22   /* a bad length or page: that sequence's outputs are not written    */
+#define ATTN_CACHE_SITE_EVICT 23    /* a bad length or page, or a page used twice: the sequence stays    */
+
+/* Which elements of a head form pair p of `pairs`: 2p and 2p + 1, or p and p + pairs. */
+typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_t;
+
+/*
+ * attn_rope -- rotary positions with several axes on queries and keys, before the attention; with
+ * `inverse` the rotation by the negative angles, which is the gradient (dq, dk from the gradients of
+ * the rotated q, k).  Pair p turns by positions[axes[p]] * freqs[p] radians; elements past
+ * 2 * pairs pass through unchanged.  Angles are exact to fp32 for every int32 position; the
+ * rotation is computed in fp32 and rounded once (nearest even).  A NaN stays some NaN.
+ *   q, k          [B][S][H or Hkv][d] as strides say: element (b, s, h, x) at b * stride[0] +
+ *                 s * stride[1] + h * stride[2] + x (elements; multiples of 8), so BSHD, BHSD and
+ *                 views of a fused projection are all taken.  k may be NULL (Hkv is then ignored)
+ *   q_out, k_out  likewise with strides of their own (no two elements on one address); each may be
+ *                 its input itself (same pointer and strides), and otherwise overlaps no input or output
+ *   positions     int32: axis a of token (b, s) at a * pos_axis_stride + b * pos_batch_stride + s
+ *   freqs, axes   fp64 and int32 [pairs]: radians per unit of position, and the axis of each pair
+ *   pairs         1 .. d / 2 (ATTN_ROPE_HALVES: a multiple of 8);  num_axes >= 1
+ *   B >= 1, S >= 0;  inverse 0 or 1
+ */
+typedef struct {
+    const void* q;
+    void* q_out;
+    const void* k;
+    void* k_out;
+    const int32_t* positions;
+    const double* freqs;
+    const int32_t* axes;
+    int64_t B, S, H, Hkv, d;
+    int64_t q_stride[3], q_out_stride[3], k_stride[3], k_out_stride[3];
+    int64_t pos_axis_stride, pos_batch_stride;
+    int32_t pairs, num_axes, pairing, inverse;
+} attn_rope_args_t;
+
+int attn_rope(const attn_rope_args_t* args, attn_stream_t stream);
+
+/*
+ * attn_paged_append -- writes new tokens' keys and values to their slots of a paged cache, the keys
+ * (and the queries) rotated on the way: the step between a projection and attn_fwd_paged or
+ * attn_paged_decode.
+ *   k, v             [total][Hkv][d], token and head strides in elements (multiples of 8)
+ *   q, q_out         optional queries [total][H][d] (strided) and their rotated copy (dense; may be q
+ *                    itself if q is dense).  NULL: none
+ *   cu_seqlens_new   device int32 [B + 1]: sequence b's new tokens are rows cu[b] .. cu[b+1] - 1 (a
+ *                    sequence may have none); rows outside every sequence are not read or written
+ *   seqlens_k        device int32 [B]: lengths WITH the new tokens (as the attention takes them), so row
+ *                    cu[b] + i goes to slot seqlens_k[b] - (cu[b+1] - cu[b]) + i
+ *   positions, freqs, axes, pairs, num_axes, pairing   as in attn_rope, positions [num_axes] x [total]
+ *                    (axis stride pos_axis_stride); pairs = 0: no rotation, the three are ignored
+ * A page that receives tokens belongs to one sequence: two tokens for one slot leave either's data.
+ */
+typedef struct {
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    const void* q;
+    void* q_out;
+    const int32_t* cu_seqlens_new;
+    const int32_t* seqlens_k;
+    const int32_t* block_table;
+    const int32_t* positions;
+    const double* freqs;
+    const int32_t* axes;
+    int64_t B, H, Hkv, total, num_pages, page_size, max_pages, d;
+    int64_t q_stride[2], k_stride[2], v_stride[2];
+    int64_t pos_axis_stride;
+    int32_t pairs, num_axes, pairing, reserved;
+} attn_append_args_t;
+
+int attn_paged_append(const attn_append_args_t* args, attn_stream_t stream);
+
+/*
+ * attn_paged_decode -- attention of one new token per sequence over the paged cache (its own key is
+ * the last of seqlens_k[b]): the decoding step for any page size and any number of query heads per
+ * K/V head, its work split evenly over the SMs whatever the lengths are.
+ *   q, o          bf16 [B][H][d];  lse  optional fp32 [B][H], as in attn_fwd_ex
+ *   seqlens_k     device int32 [B], 0 .. max_pages * page_size; a sequence without keys gets NaN and
+ *                 -inf.  Table entries past a sequence's last used page, and slots past its length, are
+ *                 not read.  Pages may be shared between sequences
+ *   weights       optional fp32 [B][Hkv][max_pages * page_size]: each visible key's softmax weight, summed
+ *                 over the query heads of its K/V head, is added (the accumulated weight that
+ *                 attn_paged_evict goes by).  A NaN row adds NaN to its keys
+ *   round_mode    as in attn_fwd.  Non-finite values are treated as there
+ * Results are bitwise reproducible for the same lengths on the same GPU model.  workspace: caller device
+ * memory of at least attn_paged_decode_workspace_size() bytes, 16-byte aligned: the parts of split rows,
+ * and with weights the logits (4 bytes per query head and table slot).  The size query returns
+ * 0 for invalid arguments or without a usable device.
+ */
+typedef struct {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    void* o;
+    float* lse;
+    float* weights;
+    const int32_t* seqlens_k;
+    const int32_t* block_table;
+    int64_t B, H, Hkv, num_pages, page_size, max_pages, d;
+    int32_t round_mode, reserved;
+} attn_decode_args_t;
+
+size_t attn_paged_decode_workspace_size(const attn_decode_args_t* args);
+int attn_paged_decode(const attn_decode_args_t* args, void* workspace, size_t workspace_bytes,
+                      attn_stream_t stream);
+
+/*
+ * attn_paged_evict -- cuts the caches of sequences longer than `budget` to `budget` keys, by
+ * accumulated attention weight, for each K/V head on its own.  Kept are slots 0 .. sinks - 1, the last
+ * `recent` slots, and of those between them the ones of largest weight (of equal weights the lower
+ * slots; -0 equals 0; a NaN ranks below every number).  Survivors below slot budget - recent stay where
+ * they are, the i-th survivor past it moves into the i-th freed slot, and the recent keys follow in order
+ * up to slot budget - 1: attention does not depend on the order of keys, and the recent window stays
+ * last for the tokens to come.  Shorter sequences stay as they are.
+ *   k_cache, v_cache   rewritten in place.  A page that a rewritten sequence uses must be used once in
+ *                      the whole table (checked: such a sequence is left as it was and reported)
+ *   weights            fp32 [B][Hkv][max_pages * page_size], as attn_paged_decode accumulates them
+ *   weights_out        the weights of the slots after the call, freed slots up to the old length zero; may be
+ *                      `weights` itself, else overlaps nothing.  Entries past the old length are not written
+ *   seqlens_k, seqlens_out   device int32 [B]: lengths before and after; may be the same
+ *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget
+ * workspace: caller device memory of at least attn_paged_evict_workspace_size() bytes, 16-byte aligned.
+ */
+typedef struct {
+    void* k_cache;
+    void* v_cache;
+    const float* weights;
+    float* weights_out;
+    const int32_t* seqlens_k;
+    int32_t* seqlens_out;
+    const int32_t* block_table;
+    int64_t B, Hkv, num_pages, page_size, max_pages, d, budget, sinks, recent;
+} attn_evict_args_t;
+
+size_t attn_paged_evict_workspace_size(const attn_evict_args_t* args);
+int attn_paged_evict(const attn_evict_args_t* args, void* workspace, size_t workspace_bytes,
+                     attn_stream_t stream);
+
+/* Synchronize `stream`, then read and clear the status word of these four calls' kernels. */
+int attn_cache_get_device_status(attn_stream_t stream, int32_t* site);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -188,14 +189,15 @@ def load(path: str | None = None):
         lib.attn_bwd_varlen.argtypes = [ctypes.POINTER(BwdVarlenArgs), vp, ctypes.c_size_t, vp]
         lib.attn_bwd_varlen_workspace_size.restype = ctypes.c_size_t
         lib.attn_bwd_varlen_workspace_size.argtypes = [ctypes.POINTER(BwdVarlenArgs)]
-        for name, args in (("attn_rope", RopeArgs), ("attn_paged_append", AppendArgs)):
+        # the argument sets of these calls travel as packed bytes or as structures
+        for name in ("attn_rope", "attn_paged_append"):
             getattr(lib, name).restype = i32
-            getattr(lib, name).argtypes = [ctypes.POINTER(args), vp]
-        for name, args in (("attn_paged_decode", DecodeArgs), ("attn_paged_evict", EvictArgs)):
+            getattr(lib, name).argtypes = [vp, vp]
+        for name in ("attn_paged_decode", "attn_paged_evict"):
             getattr(lib, name).restype = i32
-            getattr(lib, name).argtypes = [ctypes.POINTER(args), vp, ctypes.c_size_t, vp]
+            getattr(lib, name).argtypes = [vp, vp, ctypes.c_size_t, vp]
             getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
-            getattr(lib, name + "_workspace_size").argtypes = [ctypes.POINTER(args)]
+            getattr(lib, name + "_workspace_size").argtypes = [vp]
         lib.attn_cache_get_device_status.restype = i32
         lib.attn_cache_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         lib.attn_plan.restype = i32
@@ -634,34 +636,58 @@ def bwd_device_status(stream=None) -> tuple:
 
 
 # ------------------------------------------------------------- around the paged K/V cache
-def _on(device, stream):
+# These calls sit in decoding loops, where a call's time on the host counts: arguments are checked with few
+# attribute reads, packed in one go, and shapes and strides are read once.
+def _packer(cls):
+    """struct.pack for the fields of an argument structure, arrays flattened."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i"}
+    fmt = "@" + "".join(codes[t] if t in codes else "%d%s" % (t._length_, codes[t._type_]) for _, t in cls._fields_)
+    packed = struct.Struct(fmt)
+    assert packed.size <= ctypes.sizeof(cls) <= packed.size + 4      # the structure may end in padding
+    return packed.pack
+
+
+_pack_rope, _pack_append, _pack_decode, _pack_evict = map(_packer, (RopeArgs, AppendArgs, DecodeArgs, EvictArgs))
+
+
+def _on(index, stream):
     """Context in which a call's tensors are allocated and its kernels launched: the tensors' device, and
-    `stream` (an allocation belongs to the stream that uses it)."""
+    `stream` (an allocation belongs to the stream that uses it); None where both are current."""
     import torch
     if stream is not None:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=index)
         return torch.cuda.stream(s)
-    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+    return None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
-def _tensor(t, name, dtype, dim, device=None, contiguous=True):
+def _wrong(t, name, dtype, dim, index):
+    """Raise what is wrong with a tensor (a contiguous one was wanted, and it has passed or failed all else)."""
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.dim() != dim:
         raise TypeError("%s must be a CUDA %s tensor of %d dimension(s)" % (name, str(dtype)[6:], dim))
-    if contiguous and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if device is not None and t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    return t
+    if index is not None and t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d" % (name, index))
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _heads(t, name, dim, device=None):
-    """A bf16 tensor whose heads are contiguous; any strides else."""
+def _tensor(t, name, dtype, dim, index=None):
+    """A contiguous CUDA tensor; returns its device's index."""
     import torch
-    _tensor(t, name, torch.bfloat16, dim, device, contiguous=False)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim or not t.is_contiguous()
+            or not t.is_cuda or (index is not None and t.get_device() != index)):
+        _wrong(t, name, dtype, dim, index)
+    return t.get_device()
+
+
+def _heads(t, name, dim, index=None):
+    """A bf16 tensor whose heads are contiguous, with any strides else; returns its device's index."""
+    import torch
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dim or not t.is_cuda
+            or (index is not None and t.get_device() != index)):
+        _wrong(t, name, torch.bfloat16, dim, index)
+    if t.stride()[-1] != 1 and t.shape[-1] > 1:
         raise ValueError("the head dimension of %s must be contiguous" % name)
-    return t
+    return t.get_device()
 
 
 def rope_freqs(axis_dims, base: float = 10000.0, spectrum: str = "axis", scale=None, device="cuda"):
@@ -689,18 +715,22 @@ def rope_freqs(axis_dims, base: float = 10000.0, spectrum: str = "axis", scale=N
             torch.tensor(axes, dtype=torch.int32, device=device))
 
 
-def _rope_tables(positions, freqs, axes, pairing, device, pos_dims):
+def _rope_tables(positions, freqs, axes, pairing, index, pos_dim):
+    """Checks the tables; returns the number of pairs."""
     import torch
     if pairing not in PAIRINGS:
         raise ValueError("pairing must be adjacent or halves")
-    _tensor(freqs, "freqs", torch.float64, 1, device)
-    _tensor(axes, "axes", torch.int32, 1, device)
-    if freqs.numel() != axes.numel():
+    _tensor(freqs, "freqs", torch.float64, 1, index)
+    _tensor(axes, "axes", torch.int32, 1, index)
+    pairs = freqs.numel()
+    if pairs != axes.numel():
         raise ValueError("freqs and axes must have one entry per pair")
-    _tensor(positions, "positions", torch.int32, positions.dim() if positions.dim() in pos_dims else pos_dims[0], device,
-            contiguous=False)
-    if positions.shape[-1] > 1 and positions.stride(-1) != 1:
+    if (not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.dim() != pos_dim
+            or not positions.is_cuda or positions.get_device() != index):
+        _wrong(positions, "positions", torch.int32, pos_dim, index)
+    if positions.stride()[-1] != 1 and positions.shape[-1] > 1:
         raise ValueError("the token dimension of positions must be contiguous")
+    return pairs
 
 
 def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str = "adjacent", q_out=None, k_out=None,
@@ -719,49 +749,53 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     if layout not in LAYOUTS:
         raise ValueError("layout must be bshd or bhsd")
     dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
-    _heads(q, "q", dim)
-    dev = q.device
-    _rope_tables(positions, freqs, axes, pairing, dev, (2, 3) if dim == 4 else (2,))
-    order = (0, 1) if dim == 3 else (0, 1, 2) if layout == "bshd" else (0, 2, 1)     # (batch,) token, head
+    dev = _heads(q, "q", dim)
+    per_batch = dim == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 3
+    pairs = _rope_tables(positions, freqs, axes, pairing, dev, 3 if per_batch else 2)
+    swap = dim == 4 and layout == "bhsd"
 
-    def shape(t):
-        return tuple(t.shape[i] for i in order)
+    def geometry(t):
+        """(B, S, heads, d) and the (batch, token, head) strides."""
+        n, st = t.shape, t.stride()
+        if dim == 3:
+            return (1, n[0], n[1], n[2]), (0, st[0], st[1])
+        if swap:
+            return (n[0], n[2], n[1], n[3]), (st[0], st[2], st[1])
+        return tuple(n), st[:3]
 
-    def strides(t):
-        s = tuple(t.stride(i) for i in order)
-        return s if dim == 4 else (0,) + s
-
-    B, S, H = shape(q) if dim == 4 else (1,) + shape(q)
+    (B, S, H, d), qs = geometry(q)
+    Hkv, ks = 0, (0, 0, 0)
     if k is not None:
         _heads(k, "k", dim, dev)
-        if k.shape[-1] != q.shape[-1] or shape(k)[:-1] != shape(q)[:-1]:
+        (Bk, Sk, Hkv, dk), ks = geometry(k)
+        if Bk != B or Sk != S or dk != d:
             raise ValueError("q and k must agree in all but their heads")
-    if positions.shape[-1] != S or (positions.dim() == 3 and positions.shape[1] != B):
+    pn, pst = positions.shape, positions.stride()
+    if pn[-1] != S or (per_batch and pn[1] != B):
         raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
-    with _on(dev, stream):
-        outs = []
-        for t, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-            if t is None:
-                outs.append(None)
-                continue
-            if o is None:
-                o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-            elif tuple(_heads(o, name, dim, dev).shape) != tuple(t.shape):
-                raise ValueError("%s must have its input's shape" % name)
-            outs.append(o)
-        qo, ko = outs
-        none = (0, 0, 0)
-        a = RopeArgs(q.data_ptr(), qo.data_ptr(), 0 if k is None else k.data_ptr(), 0 if k is None else ko.data_ptr(),
-                     positions.data_ptr(), freqs.data_ptr(), axes.data_ptr(), B, S, H,
-                     0 if k is None else k.shape[order[-1]], q.shape[-1], strides(q), strides(qo),
-                     none if k is None else strides(k), none if k is None else strides(ko), positions.stride(0),
-                     positions.stride(1) if positions.dim() == 3 else 0, freqs.numel(), positions.shape[0],
-                     PAIRINGS[pairing], int(bool(inverse)))
+    for o, t, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if o is not None and (t is None or _heads(o, name, dim, dev) != dev or o.shape != t.shape):
+            raise ValueError("%s must have its input's shape" % name)
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
         if S > 0:
-            st = load().attn_rope(ctypes.byref(a), _stream_ptr(stream, dev))
+            kp, ko, kos = (0, 0, ks) if k is None else (k.data_ptr(), k_out.data_ptr(), geometry(k_out)[1])
+            a = _pack_rope(q.data_ptr(), q_out.data_ptr(), kp, ko, positions.data_ptr(), freqs.data_ptr(),
+                           axes.data_ptr(), B, S, H, Hkv, d, *qs, *geometry(q_out)[1], *ks, *kos, pst[0],
+                           pst[1] if per_batch else 0, pairs, pn[0], PAIRINGS[pairing], 1 if inverse else 0)
+            st = load().attn_rope(a, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_rope")
-    return qo if k is None else (qo, ko)
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return q_out if k is None else (q_out, k_out)
 
 
 def attn_rope_bwd(dq, dk, positions, freqs, axes, layout: str = "bshd", pairing: str = "adjacent", dq_out=None,
@@ -772,16 +806,18 @@ def attn_rope_bwd(dq, dk, positions, freqs, axes, layout: str = "bshd", pairing:
 
 
 def _check_cache(k_cache, v_cache, block_table, seqlens_k):
+    """Checks the cache's tensors; returns (device index, pages, page size, Hkv, d, B, max pages)."""
     import torch
-    dev = _tensor(k_cache, "k_cache", torch.bfloat16, 4).device
+    dev = _tensor(k_cache, "k_cache", torch.bfloat16, 4)
     _tensor(v_cache, "v_cache", torch.bfloat16, 4, dev)
     _tensor(seqlens_k, "seqlens_k", torch.int32, 1, dev)
     _tensor(block_table, "block_table", torch.int32, 2, dev)
-    if k_cache.shape != v_cache.shape:
+    shape, (B, most) = k_cache.shape, block_table.shape
+    if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    if seqlens_k.numel() != block_table.shape[0]:
+    if seqlens_k.numel() != B:
         raise ValueError("seqlens_k must hold one length per row of block_table")
-    return dev
+    return (dev, *shape, B, most)
 
 
 def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_table, q=None, q_out=None,
@@ -795,60 +831,74 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
     ``seqlens_k``: int32 [B] lengths WITH the new tokens, as :func:`attn_fwd_paged` and
     :func:`attn_paged_decode` then take them; ``block_table``: int32 [B, max_pages].  Tokens whose slot or
     page the cache does not have are not written and are reported by :func:`cache_device_status`.
-    Returns ``q_out`` (dense [total, H, d]; rows outside every sequence are left as they were), or None
-    without ``q``."""
+    Returns ``q_out`` (dense [total, H, d]; rows outside every sequence are left as they were, zero where
+    it is allocated here), or None without ``q``."""
     import torch
-    dev = _check_cache(k_cache, v_cache, block_table, seqlens_k)
+    dev, pages, ps, Hkv, d, B, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
     _heads(k, "k", 3, dev)
     _heads(v, "v", 3, dev)
     _tensor(cu_seqlens_new, "cu_seqlens_new", torch.int32, 1, dev)
-    B, (total, Hkv, d) = seqlens_k.numel(), k.shape
-    if v.shape != k.shape or k_cache.shape[2:] != k.shape[1:]:
+    shape = k.shape
+    total = shape[0]
+    if v.shape != shape or shape[1] != Hkv or shape[2] != d:
         raise ValueError("k and v must be [total, Hkv, d] with the cache's Hkv and d")
     if cu_seqlens_new.numel() != B + 1:
         raise ValueError("cu_seqlens_new must hold B + 1 offsets")
-    rotate = positions is not None
-    if (freqs is not None) != rotate or (axes is not None) != rotate:
-        raise ValueError("positions, freqs and axes go together")
-    if rotate:
-        _rope_tables(positions, freqs, axes, pairing, dev, (2,))
+    pairs, num_axes, pos, pos_stride, fp, ap = 0, 1, 0, 0, 0, 0
+    if positions is not None and freqs is not None and axes is not None:
+        pairs = _rope_tables(positions, freqs, axes, pairing, dev, 2)
+        num_axes = positions.shape[0]
         if positions.shape[1] != total:
             raise ValueError("positions must be [axes, total]")
-    if q is None and q_out is not None:
-        raise ValueError("q_out needs q")
-    H = 0
+        pos, pos_stride, fp, ap = positions.data_ptr(), positions.stride()[0], freqs.data_ptr(), axes.data_ptr()
+    elif positions is not None or freqs is not None or axes is not None:
+        raise ValueError("positions, freqs and axes go together")
+    elif pairing not in PAIRINGS:
+        raise ValueError("pairing must be adjacent or halves")
+    H, qs = 0, (0, 0)
     if q is not None:
         _heads(q, "q", 3, dev)
-        H = q.shape[1]
-        if q.shape[0] != total or q.shape[2] != d:
+        qt, H, qd = q.shape
+        qs = q.stride()[:2]
+        if qt != total or qd != d:
             raise ValueError("q must be [total, H, d]")
-        if q_out is not None and (tuple(_tensor(q_out, "q_out", torch.bfloat16, 3, dev).shape) != tuple(q.shape)):
+        if q_out is not None and (_tensor(q_out, "q_out", torch.bfloat16, 3, dev) != dev or q_out.shape != q.shape):
             raise ValueError("q_out must have q's shape")
-    with _on(dev, stream):
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
         if q is not None and q_out is None:
-            q_out = torch.zeros((total, H, d), dtype=torch.bfloat16, device=dev)
-        a = AppendArgs(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                       0 if q is None else q.data_ptr(), 0 if q is None else q_out.data_ptr(), cu_seqlens_new.data_ptr(),
-                       seqlens_k.data_ptr(), block_table.data_ptr(), positions.data_ptr() if rotate else 0,
-                       freqs.data_ptr() if rotate else 0, axes.data_ptr() if rotate else 0, B, H, Hkv, total,
-                       k_cache.shape[0], k_cache.shape[1], block_table.shape[1], d,
-                       (0, 0) if q is None else (q.stride(0), q.stride(1)), (k.stride(0), k.stride(1)),
-                       (v.stride(0), v.stride(1)), positions.stride(0) if rotate else 0,
-                       freqs.numel() if rotate else 0, positions.shape[0] if rotate else 1, PAIRINGS[pairing], 0)
+            q_out = torch.zeros((total, H, d), dtype=torch.bfloat16, device=q.device)
         if total > 0:
-            st = load().attn_paged_append(ctypes.byref(a), _stream_ptr(stream, dev))
+            a = _pack_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                             0 if q is None else q.data_ptr(), 0 if q is None else q_out.data_ptr(),
+                             cu_seqlens_new.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), pos, fp, ap, B, H,
+                             Hkv, total, pages, ps, most, d, *qs, *k.stride()[:2], *v.stride()[:2], pos_stride, pairs,
+                             num_axes, PAIRINGS[pairing], 0)
+            st = load().attn_paged_append(a, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_paged_append")
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return q_out
 
 
-def _workspace(lib_call, a, workspace, device):
+def _with_workspace(name, a, workspace, tensor, index):
+    """Calls an entry point that wants a workspace: the caller's, or one allocated on the current stream."""
     import torch
+    lib = load()
     if workspace is None:
-        workspace = torch.empty(max(int(lib_call(ctypes.byref(a))), 16), dtype=torch.uint8, device=device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
-    return workspace, workspace.numel() * workspace.element_size()
+        workspace = torch.empty(max(getattr(lib, name + "_workspace_size")(a), 16), dtype=torch.uint8, device=tensor.device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != tensor.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+    st = getattr(lib, name)(a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise AttnError(st, name)
 
 
 def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None, o=None, lse=None,
@@ -866,36 +916,37 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
     import torch
     if round not in MODES:
         raise ValueError("round must be rtne/rtna/rtz")
-    dev = _check_cache(k_cache, v_cache, block_table, seqlens_k)
+    dev, pages, ps, Hkv, dc, Bc, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
     _tensor(q, "q", torch.bfloat16, 3, dev)
     B, H, d = q.shape
-    P, ps, Hkv, dk = k_cache.shape
-    if B != seqlens_k.numel() or d != dk:
+    if B != Bc or d != dc:
         raise ValueError("q must be [B, H, d] with seqlens_k's B and the cache's d")
     if Hkv < 1 or H % Hkv != 0:
         raise ValueError("k/v heads (%d) must divide the query heads (%d)" % (Hkv, H))
-    if weights is not None and tuple(_tensor(weights, "weights", torch.float32, 3, dev).shape) != (
-            B, Hkv, block_table.shape[1] * ps):
-        raise ValueError("weights must be [B, Hkv, max_pages * page_size]")
-    with _on(dev, stream):
+    if weights is not None:
+        _tensor(weights, "weights", torch.float32, 3, dev)
+        if weights.shape != (B, Hkv, most * ps):
+            raise ValueError("weights must be [B, Hkv, max_pages * page_size]")
+    if o is not None and (_tensor(o, "o", torch.bfloat16, 3, dev) != dev or o.shape != q.shape):
+        raise ValueError("o must be shaped like q")
+    if lse is not None and (_tensor(lse, "lse", torch.float32, 2, dev) != dev or lse.shape != (B, H)):
+        raise ValueError("lse must be [B, H]")
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
         if o is None:
             o = torch.empty_like(q)
-        elif tuple(_tensor(o, "o", torch.bfloat16, 3, dev).shape) != tuple(q.shape):
-            raise ValueError("o must be a contiguous CUDA bf16 tensor shaped like q")
         if lse is None and return_lse:
-            lse = torch.empty((B, H), dtype=torch.float32, device=dev)
-        if lse is not None and tuple(_tensor(lse, "lse", torch.float32, 2, dev).shape) != (B, H):
-            raise ValueError("lse must be a contiguous CUDA fp32 tensor [B, H]")
-        a = DecodeArgs(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
-                       0 if lse is None else lse.data_ptr(), 0 if weights is None else weights.data_ptr(),
-                       seqlens_k.data_ptr(), block_table.data_ptr(), B, H, Hkv, P, ps, block_table.shape[1], d,
-                       MODES[round], 0)
-        lib = load()
-        ws, nbytes = _workspace(lib.attn_paged_decode_workspace_size, a, workspace, dev)
-        st = lib.attn_paged_decode(ctypes.byref(a), ws.data_ptr(), nbytes, _stream_ptr(stream, dev))
-        if st != 0:
-            raise AttnError(st, "attn_paged_decode")
-    return (o, lse) if (return_lse or lse is not None) else o
+            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        a = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                         0 if lse is None else lse.data_ptr(), 0 if weights is None else weights.data_ptr(),
+                         seqlens_k.data_ptr(), block_table.data_ptr(), B, H, Hkv, pages, ps, most, d, MODES[round], 0)
+        _with_workspace("attn_paged_decode", a, workspace, q, dev)
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return o if lse is None else (o, lse)
 
 
 def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: int, sinks: int = 0,
@@ -911,25 +962,27 @@ def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: 
     length or page, or with a page that the table holds more than once, stays as it is and is reported
     by :func:`cache_device_status`.  Returns ``seqlens_out``."""
     import torch
-    dev = _check_cache(k_cache, v_cache, block_table, seqlens_k)
-    P, ps, Hkv, d = k_cache.shape
-    B, max_pages = block_table.shape
+    dev, pages, ps, Hkv, d, B, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
     weights_out = weights if weights_out is None else weights_out
     seqlens_out = seqlens_k if seqlens_out is None else seqlens_out
     for t, name in ((weights, "weights"), (weights_out, "weights_out")):
-        if tuple(_tensor(t, name, torch.float32, 3, dev).shape) != (B, Hkv, max_pages * ps):
+        _tensor(t, name, torch.float32, 3, dev)
+        if t.shape != (B, Hkv, most * ps):
             raise ValueError("%s must be [B, Hkv, max_pages * page_size]" % name)
-    if _tensor(seqlens_out, "seqlens_out", torch.int32, 1, dev).numel() != B:
+    _tensor(seqlens_out, "seqlens_out", torch.int32, 1, dev)
+    if seqlens_out.numel() != B:
         raise ValueError("seqlens_out must hold B lengths")
-    with _on(dev, stream):
-        a = EvictArgs(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
-                      seqlens_k.data_ptr(), seqlens_out.data_ptr(), block_table.data_ptr(), B, Hkv, P, ps, max_pages, d,
-                      int(budget), int(sinks), int(recent))
-        lib = load()
-        ws, nbytes = _workspace(lib.attn_paged_evict_workspace_size, a, workspace, dev)
-        st = lib.attn_paged_evict(ctypes.byref(a), ws.data_ptr(), nbytes, _stream_ptr(stream, dev))
-        if st != 0:
-            raise AttnError(st, "attn_paged_evict")
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        a = _pack_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
+                        seqlens_k.data_ptr(), seqlens_out.data_ptr(), block_table.data_ptr(), B, Hkv, pages, ps, most, d,
+                        int(budget), int(sinks), int(recent))
+        _with_workspace("attn_paged_evict", a, workspace, k_cache, dev)
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return seqlens_out
 
 

@@ -52,7 +52,9 @@ int device(int* sms) {
         if (d.major == 10 && d.minor == 3 &&
             (set_decode_attr<128, 1>() != cudaSuccess || set_decode_attr<128, 2>() != cudaSuccess ||
              set_decode_attr<128, 4>() != cudaSuccess || set_decode_attr<64, 1>() != cudaSuccess ||
-             set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess)) {
+             set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess ||
+             cudaFuncSetAttribute(attn_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kMostStaged * 4) != cudaSuccess)) {
             cudaGetLastError();
             return ATTN_ERR_CUDA;
         }
@@ -435,7 +437,7 @@ int check_evict_shape(const attn_evict_args_t& a) {
 }
 
 struct EvictLayout {
-    size_t owner, lens, moves, list, bytes;
+    size_t owner, lens, moves, list, rows, bytes;
     int64_t most_moves;
 };
 EvictLayout evict_layout(const attn_evict_args_t& a) {
@@ -446,8 +448,29 @@ EvictLayout evict_layout(const attn_evict_args_t& a) {
     l.lens = align256((size_t)a.num_pages * 4);
     l.moves = l.lens + align256((size_t)a.B * 4);
     l.list = l.moves + align256((size_t)(a.B * a.Hkv) * 4);
-    l.bytes = l.list + (size_t)(a.B * a.Hkv) * (size_t)(2 * l.most_moves) * 4;
+    l.rows = l.list + align256((size_t)(a.B * a.Hkv) * (size_t)(2 * l.most_moves) * 4);
+    l.bytes = l.rows + (size_t)(a.B * a.Hkv) * (size_t)(2 * l.most_moves) * 4;
     return l;
+}
+
+// a cluster launch behind the memset, which a programmatic dependence does not cover
+int launch_select(const EvictParams& p, int64_t rows, cudaStream_t stream) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)p.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(rows * p.cluster));
+    lc.blockDim = dim3(kSelThreads);
+    lc.dynamicSmemBytes = (size_t)p.staged * 4;
+    lc.stream = stream;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, attn_evict_select_kernel, p) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    return ATTN_OK;
 }
 
 int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -495,14 +518,26 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     p.lens = reinterpret_cast<int32_t*>(ws + l.lens);
     p.moves = reinterpret_cast<int32_t*>(ws + l.moves);
     p.list = reinterpret_cast<int32_t*>(ws + l.list);
+    p.rows = reinterpret_cast<int32_t*>(ws + l.rows);
     p.most_moves = l.most_moves;
-    const int64_t rows = a.B * a.Hkv;
+    const int64_t rows = a.B * a.Hkv, room = a.max_pages * a.page_size;
+    // select: a cluster per row that holds its keys in shared memory where 8 CTAs can (else they are read again
+    // for each pass), and that gives every SM two CTAs where a CTA keeps 4096 keys
+    p.cluster = 1;
+    while (p.cluster < 8 && (room > (int64_t)p.cluster * kMostStaged || (rows * p.cluster < 2 * sms && room > p.cluster * 4096)))
+        p.cluster *= 2;
+    p.staged = (int)(cdiv(room, p.cluster) < kMostStaged ? cdiv(room, p.cluster) : kMostStaged);
     // column pieces of 32 bytes at least (a DRAM sector), until there is a CTA for every SM
     p.pieces = 1;
     while (2 * rows * p.pieces < sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
     if (cudaMemsetAsync(p.owner, 0xFF, (size_t)a.num_pages * 4, stream) != cudaSuccess) { cudaGetLastError(); return ATTN_ERR_CUDA; }
-    if ((st = launch(attn_evict_select_kernel, rows, 1, kSelThreads, 0, false, stream, p)) != ATTN_OK) return st;
-    return launch(attn_evict_move_kernel, rows * (2 * p.pieces + 1), 1, kMoveThreads, 0, true, stream, p);
+    if ((st = launch_select(p, rows, stream)) != ATTN_OK) return st;
+    if (l.most_moves > 0) {
+        st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, true, stream, p)
+                        : launch(attn_evict_fill_kernel<64>, 4 * sms, 1, kFillThreads, 0, true, stream, p);
+        if (st != ATTN_OK) return st;
+    }
+    return launch(attn_evict_shift_kernel, rows * (2 * p.pieces + 1), 1, kShiftThreads, 0, true, stream, p);
 }
 
 }  // namespace

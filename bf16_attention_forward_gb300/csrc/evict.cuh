@@ -8,15 +8,17 @@
 // budget - 1.  Attention does not depend on the order of the keys, and the recent window stays at the end for
 // the next call.  No more rows move than have to: min(evicted, kept) at most, and the recent ones.
 //
-// Select kernel (a CTA per (sequence, K/V head)): the threshold weight by a radix select over the
-// order-preserving 32-bit keys, then one ordered pass that lists freed slots and late survivors.
-// Move kernel: the rows.  A source slot of one move can be the target of another only from the late
-// survivors to the recent block, and inside the recent block from a later to an earlier slot, so one CTA
-// moves a (tensor, sequence, head) in that order; columns are independent, and a few long
-// caches split their rows into column pieces for more CTAs.
+// Select kernel (a cluster of 1 to 8 CTAs per (sequence, K/V head)): the weights are read once, as
+// order-preserving 32-bit keys that stay in shared memory; a radix select of 11 + 11 + 10 bits over the
+// cluster's summed histograms gives the threshold, and an ordered pass lists freed slots and late survivors.
+// Fill kernel: the rows that move into freed slots.  Their sources and targets are disjoint, so all
+// sequences' moves form one line that the CTAs divide evenly.
+// Shift kernel: the recent block, and the weights.  Its rows may overlap their targets, so one CTA
+// moves a (tensor, sequence, head) in ascending order, each step's reads before its writes; columns are
+// independent, and a few long caches split their rows into column pieces for more CTAs.
 //
 // Bound: the moved rows' bytes (K and V, read and written) and 4 bytes per key; below a few
-// MB the two launches' latency.
+// MB the launches' latency.
 #pragma once
 #include "cache_common.cuh"
 
@@ -32,17 +34,24 @@ struct EvictParams {
     Pages pages;
     int B, Hkv, row_bytes;
     int budget, sinks, recent;
-    int pieces;                // column pieces of a row
+    int cluster;               // CTAs of a (sequence, K/V head) in the select kernel
+    int pieces;                // column pieces of a row in the shift kernel
+    int staged;                // keys that a select CTA has room for in shared memory
     // workspace
     int32_t* owner;            // [num_pages]: -1, the sequence that uses the page, or -2 for several uses
     int32_t* lens;             // [B]
     int32_t* moves;            // [B][Hkv]: rows that move into freed slots
     int32_t* list;             // [B][Hkv][2 * most_moves]: freed slots, then the survivors that fill them
+    int32_t* rows;             // the same as rows of the cache
     long long most_moves;
 };
 
-constexpr int kSelThreads = 1024;
-constexpr int kMoveThreads = 256;
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMostStaged = 16384;     // 64 KB: three CTAs an SM
+constexpr int kFillThreads = 256;
+constexpr int kShiftThreads = 256;
 
 // order-preserving: a < b as numbers iff key(a) < key(b); -0 equals +0; NaN is 0, below -inf
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -55,103 +64,265 @@ __device__ __forceinline__ bool valid_len(const EvictParams& p, int n) {
     return n >= 0 && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size;
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int hist[256];
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ int4 cluster_ld4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ int cluster_ld(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
+    extern __shared__ uint32_t key_s[];
+    __shared__ __align__(16) int hist[3][kBins];
+    __shared__ int warp_n[3][kSelWarps];
+    __shared__ int total_s[2];             // ties and listed slots of this CTA, read by the cluster
     __shared__ uint32_t prefix_s;
-    __shared__ int want_s;
-    __shared__ int warp_n[2][32];
+    __shared__ int want_s, tied_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const unsigned below = (1u << lane) - 1;
     pdl_wait();
     pdl_launch();
-    const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
+    const int C = p.cluster, rank = blockIdx.x % C, bh = blockIdx.x / C;
+    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
     const int n = __ldg(p.seqlens_k + b);
     const long long room = (long long)p.pages.max_pages * p.pages.page_size;
+    const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
     const bool ok = valid_len(p, n);
-    if (h == 0) {
+    if (h == 0 && rank == 0) {
         if (tid == 0) p.lens[b] = n;
         if (ok) {
             const int used = n > 0 ? (n - 1) / p.pages.page_size + 1 : 0;
             for (int i = tid; i < used; i += kSelThreads) {
-                const int pg = __ldg(p.pages.table + (long long)b * p.pages.max_pages + i);
+                const int pg = __ldg(table + i);
                 if ((unsigned)pg < (unsigned)p.pages.num_pages && atomicCAS(p.owner + pg, -1, b) != -1)
                     atomicExch(p.owner + pg, -2);
             }
         }
     }
-    if (!ok || n <= p.budget) return;
-    const float* w = p.weights + blockIdx.x * room;
-    const int lo = p.sinks, hi = n - p.recent, keep = p.budget - p.sinks - p.recent, end = p.budget - p.recent;
-    // the keep-th largest key of [lo, hi), and how many equal to it are kept
+    if (!ok || n <= p.budget) {            // (the whole cluster)
+        if (rank == 0 && tid == 0) p.moves[bh] = 0;
+        return;
+    }
+    const float* w = p.weights + bh * room;
+    const int keep = p.budget - p.sinks - p.recent, end = p.budget - p.recent;
+    // this CTA's slots, and each warp's
+    const int per = (n - p.recent - p.sinks - 1) / C + 1;
+    const int lo = p.sinks + min(rank * per, n - p.recent - p.sinks), hi = min(lo + per, n - p.recent);
+    const bool staged = hi - lo <= p.staged;
+    const int per_warp = ((hi - lo - 1) / kSelThreads + 1) * 32;
+    const int wlo = min(lo + warp * per_warp, hi), whi = min(wlo + per_warp, hi);
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+
+    // the keep-th largest key of the row, and how many equal to it are kept
     uint32_t prefix = 0;
-    int want = keep;
-    if (keep > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            for (int j = lo + tid; j < hi; j += kSelThreads) {
-                const uint32_t key = weight_key(w[j]);
-                if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+    int want = keep, tied = 0;
+    for (int pass = 0; pass < 3 && keep > 0; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        for (int j = lo + tid; j < hi; j += kSelThreads) {
+            uint32_t key;
+            if (pass > 0 && staged) {
+                key = key_s[j - lo];
+            } else {
+                key = weight_key(w[j]);
+                if (staged) key_s[j - lo] = key;
             }
-            __syncthreads();
-            if (warp == 0) {
-                // lane i holds bins 8i .. 8i + 7; counts of larger bins from the top
-                int mine = 0;
-                for (int e = 0; e < 8; ++e) mine += hist[lane * 8 + e];
-                int above = mine;
+            if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
+        }
+        if (C > 1) cluster_sync(); else __syncthreads();
+        // thread t: bins 4t .. 4t + 3, summed over the cluster, and the count of larger bins
+        int4 sum = make_int4(0, 0, 0, 0);
+        for (int r = 0; r < C; ++r) {
+            const int4 x = C > 1 ? cluster_ld4(cluster_map(ptx::smem_u32(&hist[pass][4 * tid]), r))
+                                 : *reinterpret_cast<const int4*>(&hist[pass][4 * tid]);
+            sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+        }
+        const int mine = sum.x + sum.y + sum.z + sum.w;
+        int above = mine;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int x = __shfl_down_sync(0xFFFFFFFFu, above, off);
-                    if (lane + off < 32) above += x;
-                }
-                above -= mine;
-                if (above < want && above + mine >= want) {
-                    int e = 7;
-                    while (above + hist[lane * 8 + e] < want) above += hist[lane * 8 + e--];
-                    prefix_s = (prefix << 8) | (uint32_t)(lane * 8 + e);
-                    want_s = want - above;
-                }
-            }
-            __syncthreads();
-            prefix = prefix_s;
-            want = want_s;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_down_sync(0xFFFFFFFFu, above, off);
+            if (lane + off < 32) above += x;
         }
-    }
-    // freed slots below `end`, then survivors past it, in order
-    int32_t* list = p.list + blockIdx.x * 2 * p.most_moves;
-    int listed = 0, ties = 0;
-    for (int base = lo; base < hi; base += kSelThreads) {
-        const int j = base + tid;
-        const uint32_t key = j < hi ? weight_key(w[j]) : 0u;
-        const bool in = j < hi && keep > 0, tie = in && key == prefix;
-        const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
-        if (lane == 0) warp_n[0][warp] = __popc(tb);
+        if (lane == 0) warp_n[pass][warp] = above;
         __syncthreads();
-        int before = 0, all = 0;
-        for (int i = 0; i < 32; ++i) {
+        above -= mine;
+        for (int i = warp + 1; i < kSelWarps; ++i) above += warp_n[pass][i];
+        if (above < want && above + mine >= want) {
+            const int bin[4] = {sum.x, sum.y, sum.z, sum.w};
+            int e = 3;
+            while (above + bin[e] < want) above += bin[e--];
+            prefix_s = (prefix << bits) | (uint32_t)(4 * tid + e);
+            want_s = want - above;
+            tied_s = bin[e];
+        }
+        __syncthreads();
+        prefix = prefix_s;
+        want = want_s;
+        tied = tied_s;
+    }
+
+    auto key_at = [&](int j) { return staged ? key_s[j - lo] : weight_key(w[j]); };
+    // of the keys equal to the threshold the first `want` are kept: where not all are, their ranks count
+    int ties = 0;                          // ties before this warp's slots
+    const bool some = tied > want;
+    if (some) {
+        int count = 0;
+        for (int j0 = wlo; j0 < whi; j0 += 32)
+            count += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < whi && key_at(min(j0 + lane, hi - 1)) == prefix));
+        if (lane == 0) warp_n[0][warp] = count;
+        __syncthreads();
+        int all = 0;
+        for (int i = 0; i < kSelWarps; ++i) {
             const int x = warp_n[0][i];
-            before += i < warp ? x : 0;
+            ties += i < warp ? x : 0;
             all += x;
         }
-        const bool kept = in && (key > prefix || (tie && ties + before + __popc(tb & ((1u << lane) - 1)) < want));
-        ties += all;
-        const bool out = j < hi && (j < end ? !kept : kept);
-        const unsigned ob = __ballot_sync(0xFFFFFFFFu, out);
-        if (lane == 0) warp_n[1][warp] = __popc(ob);
-        __syncthreads();
-        before = all = 0;
-        for (int i = 0; i < 32; ++i) {
-            const int x = warp_n[1][i];
-            before += i < warp ? x : 0;
-            all += x;
+        if (C > 1) {
+            if (tid == 0) total_s[0] = all;
+            cluster_sync();
+            for (int r = 0; r < rank; ++r) ties += cluster_ld(cluster_map(ptx::smem_u32(&total_s[0]), r));
         }
-        if (out) list[listed + before + __popc(ob & ((1u << lane) - 1))] = j;
-        listed += all;
     }
-    if (tid == 0) p.moves[blockIdx.x] = listed >> 1;
+    // freed slots below `end`, and survivors at or past it, counted and then listed in order
+    auto out_at = [&](int j0, int& seen) {
+        const int j = j0 + lane;
+        const bool in = j < whi;
+        const uint32_t key = in ? key_at(j) : 0u;
+        const bool tie = in && keep > 0 && key == prefix;
+        bool kept = in && keep > 0 && (key > prefix || tie);
+        if (some) {
+            const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
+            if (tie) kept = seen + __popc(tb & below) < want;
+            seen += __popc(tb);
+        }
+        return in && (j < end ? !kept : kept);
+    };
+    int count = 0, seen = ties;
+    for (int j0 = wlo; j0 < whi; j0 += 32) count += __popc(__ballot_sync(0xFFFFFFFFu, out_at(j0, seen)));
+    if (lane == 0) warp_n[1][warp] = count;
+    __syncthreads();
+    int at = 0, all = 0;
+    for (int i = 0; i < kSelWarps; ++i) {
+        const int x = warp_n[1][i];
+        at += i < warp ? x : 0;
+        all += x;
+    }
+    if (C > 1) {
+        if (tid == 0) total_s[1] = all;
+        cluster_sync();
+        all = 0;
+        for (int r = 0; r < C; ++r) {
+            const int x = cluster_ld(cluster_map(ptx::smem_u32(&total_s[1]), r));
+            at += r < rank ? x : 0;
+            all += x;
+        }
+    }
+    int32_t* list = p.list + bh * 2 * p.most_moves;
+    int32_t* rows = p.rows + bh * 2 * p.most_moves;
+    seen = ties;
+    for (int j0 = wlo; j0 < whi; j0 += 32) {
+        const bool out = out_at(j0, seen);
+        const unsigned ob = __ballot_sync(0xFFFFFFFFu, out);
+        if (out) {
+            const int i = at + __popc(ob & below);
+            list[i] = j0 + lane;
+            rows[i] = page_row(p.pages, table, j0 + lane);
+        }
+        at += __popc(ob);
+    }
+    if (rank == 0 && tid == 0) p.moves[bh] = all >> 1;
+    if (C > 1) cluster_sync();             // no CTA leaves while its shared memory may be read
 }
 
-// One CTA per (sequence, K/V head) and task: a column piece of K or V, or the weights.
-__global__ void __launch_bounds__(kMoveThreads) attn_evict_move_kernel(const __grid_constant__ EvictParams p) {
+// Whether a sequence that is to be cut has to stay: a page outside the cache, or one that the table
+// holds more than once.  Every thread of the block calls it.
+__device__ __forceinline__ bool refused(const EvictParams& p, int b, int n) {
+    const int used = (n - 1) / p.pages.page_size + 1;
+    int wrong = 0;
+    for (int i = threadIdx.x; i < used; i += blockDim.x) {
+        const int pg = __ldg(p.pages.table + (long long)b * p.pages.max_pages + i);
+        wrong |= (unsigned)pg >= (unsigned)p.pages.num_pages || p.owner[pg] != b;
+    }
+    return __syncthreads_or(wrong);
+}
+
+// K and V rows into freed slots: 16 bytes a lane, a warp takes 512 bytes of rows at a time, 8 of them in flight.
+template <int D>
+__global__ void __launch_bounds__(kFillThreads) attn_evict_fill_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kLanes = 2 * D / 16;                 // lanes of a K (or V) row
+    constexpr int kPer = 16 / kLanes;                  // moves of a warp's instruction: 1 or 2
+    constexpr int kU = 8;
+    pdl_wait();
+    pdl_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = p.B * p.Hkv;
+    long long total = 0;
+    for (int i = lane; i < rows; i += 32) total += p.moves[i];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
+    const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (u0 >= u1) return;
+    char* base = (lane < 16 ? p.k : p.v) + (lane % kLanes) * 16;   // lanes 0-15: K, 16-31: V
+    const int sub = (lane % 16) / kLanes;
+    const long long stride = (long long)p.Hkv * p.row_bytes;
+    long long begin = 0;                               // of row bh on the line of moves
+    int last = -1;
+    bool stay = false;
+    for (int base_bh = 0; base_bh < rows && begin < u1; base_bh += 32) {
+        const int mine = base_bh + lane < rows ? p.moves[base_bh + lane] : 0;
+        for (int i = 0; i < 32 && base_bh + i < rows; ++i) {
+            const int n = __shfl_sync(0xFFFFFFFFu, mine, i), bh = base_bh + i;
+            const long long first = begin;
+            begin += n;
+            if (begin <= u0 || n == 0) continue;
+            if (first >= u1) break;
+            const int b = bh / p.Hkv, h = bh - b * p.Hkv;
+            if (b != last) {
+                stay = refused(p, b, p.lens[b]);
+                last = b;
+            }
+            if (stay) continue;
+            const int32_t* to = p.rows + bh * 2 * p.most_moves;
+            const int32_t* from = to + n;
+            const int m0 = (int)(u0 > first ? u0 - first : 0), m1 = (int)(u1 < begin ? u1 - first : n);
+            char* at = base + (long long)h * p.row_bytes;
+            for (int m = m0 + warp * kU * kPer; m < m1; m += (kFillThreads / 32) * kU * kPer) {
+                int t = 0, f = 0;
+                if (lane < kU * kPer && m + lane < m1) {
+                    t = to[m + lane];
+                    f = from[m + lane];
+                }
+                uint4 x[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int src = __shfl_sync(0xFFFFFFFFu, f, u * kPer + sub);
+                    if (m + u * kPer + sub < m1) x[u] = *reinterpret_cast<const uint4*>(at + src * stride);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int dst = __shfl_sync(0xFFFFFFFFu, t, u * kPer + sub);
+                    if (m + u * kPer + sub < m1) *reinterpret_cast<uint4*>(at + dst * stride) = x[u];
+                }
+            }
+        }
+    }
+}
+
+// The recent block, the weights and the lengths.  One CTA per (sequence, K/V head) and task: a column piece of
+// K or V, or the weights.
+__global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const __grid_constant__ EvictParams p) {
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch();
@@ -165,85 +336,61 @@ __global__ void __launch_bounds__(kMoveThreads) attn_evict_move_kernel(const __g
     bool bad = !valid_len(p, n);
     const bool over = !bad && n > p.budget;
     const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
-    if (over) {
-        // every used page has to be the sequence's alone
-        const int used = (n - 1) / p.pages.page_size + 1;
-        int wrong = 0;
-        for (int i = tid; i < used; i += kMoveThreads) {
-            const int pg = __ldg(table + i);
-            wrong |= (unsigned)pg >= (unsigned)p.pages.num_pages || p.owner[pg] != b;
-        }
-        bad = __syncthreads_or(wrong);
-    }
+    if (over) bad = refused(p, b, n);
     if (weights && h == 0 && tid == 0) {
         if (bad) report_invalid(ATTN_CACHE_SITE_EVICT);
         p.seqlens_out[b] = over && !bad ? p.budget : n;
     }
     if (bad) return;
     const int end = p.budget - p.recent, shift = n - p.budget;
-    const int moves = over ? p.moves[bh] : 0;
-    const int32_t* freed = p.list + bh * 2 * p.most_moves;
-    const int32_t* late = freed + moves;
 
     if (weights) {
         const float* w = p.weights + bh * room;
         float* out = p.weights_out + bh * room;
         if (out != w)
-            for (int j = tid; j < (over ? end : n); j += kMoveThreads) out[j] = w[j];
+            for (int j = tid; j < (over ? end : n); j += kShiftThreads) out[j] = w[j];
         if (!over) return;
+        const int moves = p.moves[bh];
+        const int32_t* freed = p.list + bh * 2 * p.most_moves;
+        const int32_t* late = freed + moves;
         __syncthreads();
-        for (int i = tid; i < moves; i += kMoveThreads) out[freed[i]] = w[late[i]];
+        for (int i = tid; i < moves; i += kShiftThreads) out[freed[i]] = w[late[i]];
         __syncthreads();
-        for (int i0 = 0; i0 < p.recent; i0 += kMoveThreads) {
+        for (int i0 = 0; i0 < p.recent; i0 += kShiftThreads) {
             const int i = i0 + tid;
             const float x = i < p.recent ? w[n - p.recent + i] : 0.0f;
             __syncthreads();           // (a slot is read before it is written: targets lie below the sources left)
             if (i < p.recent) out[end + i] = x;
         }
         __syncthreads();
-        for (int j = p.budget + tid; j < n; j += kMoveThreads) out[j] = 0.0f;
+        for (int j = p.budget + tid; j < n; j += kShiftThreads) out[j] = 0.0f;
         return;
     }
     if (!over) return;
 
     const int piece = task % p.pieces, bytes = p.row_bytes / p.pieces;   // 32 .. 256 bytes
-    const int lanes = bytes / 16, rows = kMoveThreads / lanes;
+    const int lanes = bytes / 16, rows = kShiftThreads / lanes;
     char* base = (task < p.pieces ? p.k : p.v) + (long long)h * p.row_bytes + piece * bytes + (tid % lanes) * 16;
     const long long stride = (long long)p.Hkv * p.row_bytes;
     const int r = tid / lanes;
-    constexpr int kU = 4;
-    for (int i0 = 0; i0 < moves; i0 += rows * kU) {
+    constexpr int kU = 8;
+    for (int i0 = 0; i0 < p.recent; i0 += rows * kU) {
         uint4 x[kU];
         int to[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int i = i0 + u * rows + r;
             to[u] = -1;
-            if (i < moves) {
-                to[u] = page_row(p.pages, table, freed[i]);
-                x[u] = *reinterpret_cast<const uint4*>(base + page_row(p.pages, table, late[i]) * stride);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u] * stride) = x[u];
-    }
-    __syncthreads();                   // the late survivors are out before the recent block covers their slots
-    for (int i0 = 0; i0 < p.recent; i0 += rows * kU) {
-        uint4 x[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = i0 + u * rows + r;
-            if (i < p.recent)
+            if (i < p.recent) {
                 x[u] = *reinterpret_cast<const uint4*>(base + page_row(p.pages, table, n - p.recent + i) * stride);
+                to[u] = page_row(p.pages, table, end + i);
+            }
         }
         // this step's reads before its writes; its targets lie below every later step's sources
         if (shift < p.recent) __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = i0 + u * rows + r;
-            if (i < p.recent) *reinterpret_cast<uint4*>(base + page_row(p.pages, table, end + i) * stride) = x[u];
-        }
+        for (int u = 0; u < kU; ++u)
+            if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u] * stride) = x[u];
     }
 }
 

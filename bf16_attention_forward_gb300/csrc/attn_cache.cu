@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "cache_common.cuh"
 #include "decode.cuh"
@@ -65,25 +66,34 @@ int device(int* sms) {
     return ATTN_OK;
 }
 
-// every kernel waits for the one before it before it touches global memory
-template <class... P, class... A>
-int launch(void (*kernel)(P...), int64_t grid_x, int grid_y, int threads, size_t smem, bool pdl, cudaStream_t stream,
-           A&&... args) {
-    cudaLaunchAttribute at[1];
+// Every kernel waits for the one before it before it touches global memory, so each is launched as its programmatic
+// dependent.  cluster: CTAs of a cluster.
+template <class P>
+int launch_clusters(void (*kernel)(P), int64_t grid, int cluster, int threads, size_t smem, cudaStream_t stream,
+                    const std::remove_const_t<P>& args, int grid_y = 1) {
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)grid_x, (unsigned)grid_y);
+    lc.gridDim = dim3((unsigned)grid, (unsigned)grid_y);
     lc.blockDim = dim3((unsigned)threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
     lc.attrs = at;
-    lc.numAttrs = pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&lc, kernel, args...) != cudaSuccess) {
+    lc.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&lc, kernel, args) != cudaSuccess) {
         cudaGetLastError();
         return ATTN_ERR_CUDA;
     }
     return ATTN_OK;
+}
+template <class P>
+int launch(void (*kernel)(P), int64_t grid, int grid_y, int threads, size_t smem, cudaStream_t stream,
+           const std::remove_const_t<P>& args) {
+    return launch_clusters(kernel, grid, 1, threads, smem, stream, args, grid_y);
 }
 
 // ------------------------------------------------------------------------------ memory ranges
@@ -212,14 +222,14 @@ int launch_rope(RopeParams& p, int64_t d, bool halves, bool append, int sms, cud
     const int gy = (int)cdiv(p.heads, p.heads_per_thread);
     if (gy > 65535) return ATTN_ERR_UNSUPPORTED;
     if (d == 128)
-        return append ? (halves ? launch(attn_rope_kernel<128, true, true>, grid, gy, kRopeThreads, 0, true, stream, p)
-                                : launch(attn_rope_kernel<128, false, true>, grid, gy, kRopeThreads, 0, true, stream, p))
-                      : (halves ? launch(attn_rope_kernel<128, true, false>, grid, gy, kRopeThreads, 0, true, stream, p)
-                                : launch(attn_rope_kernel<128, false, false>, grid, gy, kRopeThreads, 0, true, stream, p));
-    return append ? (halves ? launch(attn_rope_kernel<64, true, true>, grid, gy, kRopeThreads, 0, true, stream, p)
-                            : launch(attn_rope_kernel<64, false, true>, grid, gy, kRopeThreads, 0, true, stream, p))
-                  : (halves ? launch(attn_rope_kernel<64, true, false>, grid, gy, kRopeThreads, 0, true, stream, p)
-                            : launch(attn_rope_kernel<64, false, false>, grid, gy, kRopeThreads, 0, true, stream, p));
+        return append ? (halves ? launch(attn_rope_kernel<128, true, true>, grid, gy, kRopeThreads, 0, stream, p)
+                                : launch(attn_rope_kernel<128, false, true>, grid, gy, kRopeThreads, 0, stream, p))
+                      : (halves ? launch(attn_rope_kernel<128, true, false>, grid, gy, kRopeThreads, 0, stream, p)
+                                : launch(attn_rope_kernel<128, false, false>, grid, gy, kRopeThreads, 0, stream, p));
+    return append ? (halves ? launch(attn_rope_kernel<64, true, true>, grid, gy, kRopeThreads, 0, stream, p)
+                            : launch(attn_rope_kernel<64, false, true>, grid, gy, kRopeThreads, 0, stream, p))
+                  : (halves ? launch(attn_rope_kernel<64, true, false>, grid, gy, kRopeThreads, 0, stream, p)
+                            : launch(attn_rope_kernel<64, false, false>, grid, gy, kRopeThreads, 0, stream, p));
 }
 
 int run_rope(const attn_rope_args_t& a, cudaStream_t stream) {
@@ -356,12 +366,12 @@ template <int D, int NH>
 int launch_decode(const DecodeParams& p, cudaStream_t stream) {
     int st;
     if (p.weights) {
-        if ((st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, true, stream, p)) != ATTN_OK) return st;
-        if ((st = launch(attn_decode_join_kernel<D, NH, true>, p.grid, 1, 256, 0, true, stream, p)) != ATTN_OK) return st;
-        return launch(attn_decode_weights_kernel<NH>, 4 * p.grid, 1, 256, 0, true, stream, p);
+        if ((st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
+        if ((st = launch(attn_decode_join_kernel<D, NH, true>, p.grid, 1, 256, 0, stream, p)) != ATTN_OK) return st;
+        return launch(attn_decode_weights_kernel<NH>, 4 * p.grid, 1, 256, 0, stream, p);
     }
-    if ((st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, true, stream, p)) != ATTN_OK) return st;
-    return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, true, stream, p);
+    if ((st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
+    return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);
 }
 
 int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -432,45 +442,30 @@ int check_evict_shape(const attn_evict_args_t& a) {
     if (a.budget < 1 || a.sinks < 0 || a.recent < 0 || a.sinks > a.budget || a.recent > a.budget ||
         a.sinks + a.recent > a.budget)
         return ATTN_ERR_INVALID_ARG;
-    if (a.budget > kLim || a.B * a.Hkv > kLim / 32) return ATTN_ERR_UNSUPPORTED;     // 17 tasks a head at most
+    // 17 tasks a head at most; moves are counted, and rows of a head numbered, in int32
+    if (a.budget > kLim || a.B * a.Hkv > kLim / 32 || a.num_pages * a.page_size > 2 * kLim / a.Hkv ||
+        a.max_pages * a.page_size > 2 * kLim / (a.B * a.Hkv))
+        return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
 struct EvictLayout {
-    size_t owner, lens, moves, list, rows, bytes;
+    size_t uses, cut, total, moves, list, fill, bytes;
     int64_t most_moves;
 };
 EvictLayout evict_layout(const attn_evict_args_t& a) {
     const int64_t keep = a.budget - a.sinks - a.recent, over = a.max_pages * a.page_size - a.budget;
     EvictLayout l;
     l.most_moves = over < 0 ? 0 : keep < over ? keep : over;
-    l.owner = 0;
-    l.lens = align256((size_t)a.num_pages * 4);
-    l.moves = l.lens + align256((size_t)a.B * 4);
+    const size_t all = (size_t)(a.B * a.Hkv) * (size_t)l.most_moves;
+    l.uses = 0;
+    l.cut = align256((size_t)a.num_pages * 4);
+    l.total = l.cut + align256((size_t)a.B * 4);
+    l.moves = l.total + 256;
     l.list = l.moves + align256((size_t)(a.B * a.Hkv) * 4);
-    l.rows = l.list + align256((size_t)(a.B * a.Hkv) * (size_t)(2 * l.most_moves) * 4);
-    l.bytes = l.rows + (size_t)(a.B * a.Hkv) * (size_t)(2 * l.most_moves) * 4;
+    l.fill = l.list + align256(all * 8);
+    l.bytes = l.fill + all * 8;
     return l;
-}
-
-// a cluster launch behind the memset, which a programmatic dependence does not cover
-int launch_select(const EvictParams& p, int64_t rows, cudaStream_t stream) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)p.cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)(rows * p.cluster));
-    lc.blockDim = dim3(kSelThreads);
-    lc.dynamicSmemBytes = (size_t)p.staged * 4;
-    lc.stream = stream;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&lc, attn_evict_select_kernel, p) != cudaSuccess) {
-        cudaGetLastError();
-        return ATTN_ERR_CUDA;
-    }
-    return ATTN_OK;
 }
 
 int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -514,11 +509,12 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     p.budget = (int)a.budget;
     p.sinks = (int)a.sinks;
     p.recent = (int)a.recent;
-    p.owner = reinterpret_cast<int32_t*>(ws + l.owner);
-    p.lens = reinterpret_cast<int32_t*>(ws + l.lens);
+    p.uses = reinterpret_cast<int32_t*>(ws + l.uses);
+    p.cut = reinterpret_cast<int32_t*>(ws + l.cut);
+    p.total = reinterpret_cast<int32_t*>(ws + l.total);
     p.moves = reinterpret_cast<int32_t*>(ws + l.moves);
     p.list = reinterpret_cast<int32_t*>(ws + l.list);
-    p.rows = reinterpret_cast<int32_t*>(ws + l.rows);
+    p.fill = reinterpret_cast<int2*>(ws + l.fill);
     p.most_moves = l.most_moves;
     const int64_t rows = a.B * a.Hkv, room = a.max_pages * a.page_size;
     // select: a cluster per row that holds its keys in shared memory where 8 CTAs can (else they are read again
@@ -530,14 +526,15 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     // column pieces of 32 bytes at least (a DRAM sector), until there is a CTA for every SM
     p.pieces = 1;
     while (2 * rows * p.pieces < sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
-    if (cudaMemsetAsync(p.owner, 0xFF, (size_t)a.num_pages * 4, stream) != cudaSuccess) { cudaGetLastError(); return ATTN_ERR_CUDA; }
-    if ((st = launch_select(p, rows, stream)) != ATTN_OK) return st;
+    if ((st = launch_clusters(attn_evict_prep_kernel, kPrepCtas, kPrepCtas, kPrepThreads, 0, stream, p)) != ATTN_OK) return st;
+    if ((st = launch_clusters(attn_evict_select_kernel, rows * p.cluster, p.cluster, kSelThreads, (size_t)p.staged * 4, stream, p)) != ATTN_OK)
+        return st;
     if (l.most_moves > 0) {
-        st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, true, stream, p)
-                        : launch(attn_evict_fill_kernel<64>, 4 * sms, 1, kFillThreads, 0, true, stream, p);
+        st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, stream, p)
+                        : launch(attn_evict_fill_kernel<64>, 4 * sms, 1, kFillThreads, 0, stream, p);
         if (st != ATTN_OK) return st;
     }
-    return launch(attn_evict_shift_kernel, rows * (2 * p.pieces + 1), 1, kShiftThreads, 0, true, stream, p);
+    return launch(attn_evict_shift_kernel, rows * (2 * p.pieces + 1), 1, kShiftThreads, 0, stream, p);
 }
 
 }  // namespace

@@ -8,11 +8,13 @@
 // budget - 1.  Attention does not depend on the order of the keys, and the recent window stays at the end for
 // the next call.  No more rows move than have to: min(evicted, kept) at most, and the recent ones.
 //
+// Prepare kernel (one cluster of 8 CTAs): counts each page's uses in the table and decides which sequences are
+// cut: over the budget, a valid length, every page in the cache and used once.
 // Select kernel (a cluster of 1 to 8 CTAs per (sequence, K/V head)): the weights are read once, as
 // order-preserving 32-bit keys that stay in shared memory; a radix select of 11 + 11 + 10 bits over the
 // cluster's summed histograms gives the threshold, and an ordered pass lists freed slots and late survivors.
 // Fill kernel: the rows that move into freed slots.  Their sources and targets are disjoint, so all
-// sequences' moves form one line that the CTAs divide evenly.
+// sequences' moves lie on one list (in no fixed order) that the warps share evenly.
 // Shift kernel: the recent block, and the weights.  Its rows may overlap their targets, so one CTA
 // moves a (tensor, sequence, head) in ascending order, each step's reads before its writes; columns are
 // independent, and a few long caches split their rows into column pieces for more CTAs.
@@ -38,14 +40,17 @@ struct EvictParams {
     int pieces;                // column pieces of a row in the shift kernel
     int staged;                // keys that a select CTA has room for in shared memory
     // workspace
-    int32_t* owner;            // [num_pages]: -1, the sequence that uses the page, or -2 for several uses
-    int32_t* lens;             // [B]
+    int32_t* uses;             // [num_pages]: table entries of used pages that name the page
+    int32_t* cut;              // [B]: the length n of a sequence that is cut, -1 - n of one that fits, 0: refused
+    int32_t* total;            // moves on the fill list
     int32_t* moves;            // [B][Hkv]: rows that move into freed slots
     int32_t* list;             // [B][Hkv][2 * most_moves]: freed slots, then the survivors that fill them
-    int32_t* rows;             // the same as rows of the cache
+    int2* fill;                // [B * Hkv * most_moves]: (to, from) as rows of [cache rows * Hkv]
     long long most_moves;
 };
 
+constexpr int kPrepThreads = 1024;
+constexpr int kPrepCtas = 8;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
@@ -72,6 +77,7 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// (a CTA that is not launched in a cluster is one of size 1)
 __device__ __forceinline__ int4 cluster_ld4(uint32_t addr) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -83,11 +89,54 @@ __device__ __forceinline__ int cluster_ld(uint32_t addr) {
     return v;
 }
 
+__global__ void __launch_bounds__(kPrepThreads, 1) attn_evict_prep_kernel(const __grid_constant__ EvictParams p) {
+    const int tid = blockIdx.x * kPrepThreads + threadIdx.x, lane = threadIdx.x & 31, warp = tid >> 5;
+    constexpr int kThreads = kPrepThreads * kPrepCtas;
+    pdl_wait();
+    pdl_launch();
+    for (int i = tid; i < p.pages.num_pages; i += kThreads) p.uses[i] = 0;
+    if (tid == 0) *p.total = 0;
+    cluster_sync();
+    // a warp per sequence
+    for (int b = warp; b < p.B; b += kThreads / 32) {
+        const int n = __ldg(p.seqlens_k + b);
+        if (n < 1 || !valid_len(p, n)) continue;
+        const int used = (n - 1) / p.pages.page_size + 1;
+#pragma unroll 4
+        for (int i = lane; i < used; i += 32) {
+            const int pg = __ldg(p.pages.table + (long long)b * p.pages.max_pages + i);
+            if ((unsigned)pg < (unsigned)p.pages.num_pages) atomicAdd(p.uses + pg, 1);
+        }
+    }
+    cluster_sync();
+    for (int b = warp; b < p.B; b += kThreads / 32) {
+        const int n = __ldg(p.seqlens_k + b);
+        const bool valid = valid_len(p, n), over = valid && n > p.budget;
+        bool bad = !valid;
+        if (over) {
+            const int used = (n - 1) / p.pages.page_size + 1;
+#pragma unroll 4
+            for (int i = lane; i < used; i += 32) {
+                const int pg = __ldg(p.pages.table + (long long)b * p.pages.max_pages + i);
+                bad |= (unsigned)pg >= (unsigned)p.pages.num_pages || __ldcg(p.uses + pg) != 1;
+            }
+            bad = __any_sync(0xFFFFFFFFu, bad);
+        }
+        __syncwarp();                      // seqlens_out may be seqlens_k: every lane has read it
+        if (lane == 0) {
+            if (bad) report_invalid(ATTN_CACHE_SITE_EVICT);
+            p.cut[b] = bad ? 0 : over ? n : -1 - n;
+            p.seqlens_out[b] = over && !bad ? p.budget : n;
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
     extern __shared__ uint32_t key_s[];
     __shared__ __align__(16) int hist[3][kBins];
     __shared__ int warp_n[3][kSelWarps];
     __shared__ int total_s[2];             // ties and listed slots of this CTA, read by the cluster
+    __shared__ int start_s;                // rank 0: the row's place on the fill list
     __shared__ uint32_t prefix_s;
     __shared__ int want_s, tied_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -96,25 +145,10 @@ __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __
     pdl_launch();
     const int C = p.cluster, rank = blockIdx.x % C, bh = blockIdx.x / C;
     const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-    const int n = __ldg(p.seqlens_k + b);
+    const int n = p.cut[b];
+    if (n <= 0) return;                    // (the whole cluster)
     const long long room = (long long)p.pages.max_pages * p.pages.page_size;
     const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
-    const bool ok = valid_len(p, n);
-    if (h == 0 && rank == 0) {
-        if (tid == 0) p.lens[b] = n;
-        if (ok) {
-            const int used = n > 0 ? (n - 1) / p.pages.page_size + 1 : 0;
-            for (int i = tid; i < used; i += kSelThreads) {
-                const int pg = __ldg(table + i);
-                if ((unsigned)pg < (unsigned)p.pages.num_pages && atomicCAS(p.owner + pg, -1, b) != -1)
-                    atomicExch(p.owner + pg, -2);
-            }
-        }
-    }
-    if (!ok || n <= p.budget) {            // (the whole cluster)
-        if (rank == 0 && tid == 0) p.moves[bh] = 0;
-        return;
-    }
     const float* w = p.weights + bh * room;
     const int keep = p.budget - p.sinks - p.recent, end = p.budget - p.recent;
     // this CTA's slots, and each warp's
@@ -131,15 +165,27 @@ __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __
     int want = keep, tied = 0;
     for (int pass = 0; pass < 3 && keep > 0; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-            uint32_t key;
-            if (pass > 0 && staged) {
-                key = key_s[j - lo];
-            } else {
-                key = weight_key(w[j]);
-                if (staged) key_s[j - lo] = key;
+        if (pass > 0 && staged) {
+            for (int j = tid; j < hi - lo; j += kSelThreads) {
+                const uint32_t key = key_s[j];
+                if ((key >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
             }
-            if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
+        } else {
+            constexpr int kU = 8;          // loads in flight
+            for (int j0 = lo + tid; j0 < hi; j0 += kU * kSelThreads) {
+                float x[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (j0 + u * kSelThreads < hi) x[u] = w[j0 + u * kSelThreads];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int j = j0 + u * kSelThreads;
+                    if (j >= hi) break;
+                    const uint32_t key = weight_key(x[u]);
+                    if (staged) key_s[j - lo] = key;
+                    if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
+                }
+            }
         }
         if (C > 1) cluster_sync(); else __syncthreads();
         // thread t: bins 4t .. 4t + 3, summed over the cluster, and the count of larger bins
@@ -230,99 +276,62 @@ __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __
             all += x;
         }
     }
+    const int moves = all >> 1;
+    if (rank == 0 && tid == 0) {
+        p.moves[bh] = moves;
+        start_s = atomicAdd(p.total, moves);
+    }
+    if (C > 1) cluster_sync(); else __syncthreads();
+    int2* fill = p.fill + cluster_ld(cluster_map(ptx::smem_u32(&start_s), 0));
     int32_t* list = p.list + bh * 2 * p.most_moves;
-    int32_t* rows = p.rows + bh * 2 * p.most_moves;
     seen = ties;
     for (int j0 = wlo; j0 < whi; j0 += 32) {
         const bool out = out_at(j0, seen);
         const unsigned ob = __ballot_sync(0xFFFFFFFFu, out);
         if (out) {
-            const int i = at + __popc(ob & below);
+            const int i = at + __popc(ob & below), row = page_row(p.pages, table, j0 + lane) * p.Hkv + h;
             list[i] = j0 + lane;
-            rows[i] = page_row(p.pages, table, j0 + lane);
+            if (i < moves) fill[i].x = row; else fill[i - moves].y = row;
         }
         at += __popc(ob);
     }
-    if (rank == 0 && tid == 0) p.moves[bh] = all >> 1;
     if (C > 1) cluster_sync();             // no CTA leaves while its shared memory may be read
-}
-
-// Whether a sequence that is to be cut has to stay: a page outside the cache, or one that the table
-// holds more than once.  Every thread of the block calls it.
-__device__ __forceinline__ bool refused(const EvictParams& p, int b, int n) {
-    const int used = (n - 1) / p.pages.page_size + 1;
-    int wrong = 0;
-    for (int i = threadIdx.x; i < used; i += blockDim.x) {
-        const int pg = __ldg(p.pages.table + (long long)b * p.pages.max_pages + i);
-        wrong |= (unsigned)pg >= (unsigned)p.pages.num_pages || p.owner[pg] != b;
-    }
-    return __syncthreads_or(wrong);
 }
 
 // K and V rows into freed slots: 16 bytes a lane, a warp takes 512 bytes of rows at a time, 8 of them in flight.
 template <int D>
-__global__ void __launch_bounds__(kFillThreads) attn_evict_fill_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kFillThreads, 4) attn_evict_fill_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kLanes = 2 * D / 16;                 // lanes of a K (or V) row
     constexpr int kPer = 16 / kLanes;                  // moves of a warp's instruction: 1 or 2
     constexpr int kU = 8;
     pdl_wait();
     pdl_launch();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = p.B * p.Hkv;
-    long long total = 0;
-    for (int i = lane; i < rows; i += 32) total += p.moves[i];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
-    const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
-    if (u0 >= u1) return;
-    char* base = (lane < 16 ? p.k : p.v) + (lane % kLanes) * 16;   // lanes 0-15: K, 16-31: V
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (kFillThreads / 32);
+    const int total = *p.total;
+    char* base = (lane < 16 ? p.k : p.v) + (lane % kLanes) * 16;       // lanes 0-15: K, 16-31: V
     const int sub = (lane % 16) / kLanes;
-    const long long stride = (long long)p.Hkv * p.row_bytes;
-    long long begin = 0;                               // of row bh on the line of moves
-    int last = -1;
-    bool stay = false;
-    for (int base_bh = 0; base_bh < rows && begin < u1; base_bh += 32) {
-        const int mine = base_bh + lane < rows ? p.moves[base_bh + lane] : 0;
-        for (int i = 0; i < 32 && base_bh + i < rows; ++i) {
-            const int n = __shfl_sync(0xFFFFFFFFu, mine, i), bh = base_bh + i;
-            const long long first = begin;
-            begin += n;
-            if (begin <= u0 || n == 0) continue;
-            if (first >= u1) break;
-            const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-            if (b != last) {
-                stay = refused(p, b, p.lens[b]);
-                last = b;
-            }
-            if (stay) continue;
-            const int32_t* to = p.rows + bh * 2 * p.most_moves;
-            const int32_t* from = to + n;
-            const int m0 = (int)(u0 > first ? u0 - first : 0), m1 = (int)(u1 < begin ? u1 - first : n);
-            char* at = base + (long long)h * p.row_bytes;
-            for (int m = m0 + warp * kU * kPer; m < m1; m += (kFillThreads / 32) * kU * kPer) {
-                int t = 0, f = 0;
-                if (lane < kU * kPer && m + lane < m1) {
-                    t = to[m + lane];
-                    f = from[m + lane];
-                }
-                uint4 x[kU];
+    for (long long m = (long long)(blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5)) * kU * kPer; m < total;
+         m += (long long)warps * kU * kPer) {
+        int2 mv = make_int2(0, 0);
+        if (lane < kU * kPer && m + lane < total) mv = p.fill[m + lane];
+        uint4 x[kU];
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int src = __shfl_sync(0xFFFFFFFFu, f, u * kPer + sub);
-                    if (m + u * kPer + sub < m1) x[u] = *reinterpret_cast<const uint4*>(at + src * stride);
-                }
+        for (int u = 0; u < kU; ++u) {
+            const int src = __shfl_sync(0xFFFFFFFFu, mv.y, u * kPer + sub);
+            if (m + u * kPer + sub < total) x[u] = *reinterpret_cast<const uint4*>(base + (long long)src * (2 * D));
+        }
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int dst = __shfl_sync(0xFFFFFFFFu, t, u * kPer + sub);
-                    if (m + u * kPer + sub < m1) *reinterpret_cast<uint4*>(at + dst * stride) = x[u];
-                }
-            }
+        for (int u = 0; u < kU; ++u) {
+            const int dst = __shfl_sync(0xFFFFFFFFu, mv.x, u * kPer + sub);
+            if (m + u * kPer + sub < total) *reinterpret_cast<uint4*>(base + (long long)dst * (2 * D)) = x[u];
         }
     }
 }
 
-// The recent block, the weights and the lengths.  One CTA per (sequence, K/V head) and task: a column piece of
-// K or V, or the weights.
+// The recent block and the weights.  One CTA per (sequence, K/V head) and task: a column piece of K or V, or the
+// weights.
 __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kU = 8;                              // loads in flight
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch();
@@ -330,37 +339,56 @@ __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const _
     const long long bh = blockIdx.x / tasks;
     const int task = (int)(blockIdx.x - bh * tasks);
     const int b = (int)(bh / p.Hkv), h = (int)(bh - (long long)b * p.Hkv);
-    const int n = p.lens[b];
     const long long room = (long long)p.pages.max_pages * p.pages.page_size;
-    const bool weights = task == tasks - 1;
-    bool bad = !valid_len(p, n);
-    const bool over = !bad && n > p.budget;
-    const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
-    if (over) bad = refused(p, b, n);
-    if (weights && h == 0 && tid == 0) {
-        if (bad) report_invalid(ATTN_CACHE_SITE_EVICT);
-        p.seqlens_out[b] = over && !bad ? p.budget : n;
-    }
-    if (bad) return;
-    const int end = p.budget - p.recent, shift = n - p.budget;
+    const int cut = p.cut[b];
+    if (cut == 0) return;
+    const bool over = cut > 0;
+    const int n = over ? cut : -1 - cut, end = p.budget - p.recent, shift = n - p.budget;
 
-    if (weights) {
+    if (task == tasks - 1) {
         const float* w = p.weights + bh * room;
         float* out = p.weights_out + bh * room;
-        if (out != w)
-            for (int j = tid; j < (over ? end : n); j += kShiftThreads) out[j] = w[j];
+        if (out != w) {
+            const int upto = over ? end : n;
+            for (int j0 = tid; j0 < upto; j0 += kU * kShiftThreads) {
+                float x[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (j0 + u * kShiftThreads < upto) x[u] = w[j0 + u * kShiftThreads];
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (j0 + u * kShiftThreads < upto) out[j0 + u * kShiftThreads] = x[u];
+            }
+        }
         if (!over) return;
         const int moves = p.moves[bh];
         const int32_t* freed = p.list + bh * 2 * p.most_moves;
-        const int32_t* late = freed + moves;
         __syncthreads();
-        for (int i = tid; i < moves; i += kShiftThreads) out[freed[i]] = w[late[i]];
+        for (int i0 = tid; i0 < moves; i0 += kU * kShiftThreads) {
+            float x[kU];
+            int to[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int i = i0 + u * kShiftThreads;
+                if (i < moves) {
+                    to[u] = freed[i];
+                    x[u] = w[freed[moves + i]];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (i0 + u * kShiftThreads < moves) out[to[u]] = x[u];
+        }
         __syncthreads();
-        for (int i0 = 0; i0 < p.recent; i0 += kShiftThreads) {
-            const int i = i0 + tid;
-            const float x = i < p.recent ? w[n - p.recent + i] : 0.0f;
+        for (int i0 = 0; i0 < p.recent; i0 += kU * kShiftThreads) {
+            float x[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (i0 + u * kShiftThreads + tid < p.recent) x[u] = w[n - p.recent + i0 + u * kShiftThreads + tid];
             __syncthreads();           // (a slot is read before it is written: targets lie below the sources left)
-            if (i < p.recent) out[end + i] = x;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (i0 + u * kShiftThreads + tid < p.recent) out[end + i0 + u * kShiftThreads + tid] = x[u];
         }
         __syncthreads();
         for (int j = p.budget + tid; j < n; j += kShiftThreads) out[j] = 0.0f;
@@ -370,10 +398,10 @@ __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const _
 
     const int piece = task % p.pieces, bytes = p.row_bytes / p.pieces;   // 32 .. 256 bytes
     const int lanes = bytes / 16, rows = kShiftThreads / lanes;
+    const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
     char* base = (task < p.pieces ? p.k : p.v) + (long long)h * p.row_bytes + piece * bytes + (tid % lanes) * 16;
     const long long stride = (long long)p.Hkv * p.row_bytes;
     const int r = tid / lanes;
-    constexpr int kU = 8;
     for (int i0 = 0; i0 < p.recent; i0 += rows * kU) {
         uint4 x[kU];
         int to[kU];

@@ -54,7 +54,9 @@ int device(int* sms) {
             (set_decode_attr<128, 1>() != cudaSuccess || set_decode_attr<128, 2>() != cudaSuccess ||
              set_decode_attr<128, 4>() != cudaSuccess || set_decode_attr<64, 1>() != cudaSuccess ||
              set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess ||
-             cudaFuncSetAttribute(attn_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+             cudaFuncSetAttribute(attn_evict_select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kMostStaged * 4) != cudaSuccess ||
+             cudaFuncSetAttribute(attn_evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   kMostStaged * 4) != cudaSuccess)) {
             cudaGetLastError();
             return ATTN_ERR_CUDA;
@@ -196,6 +198,10 @@ Pages make_pages(const int32_t* table, int64_t num_pages, int64_t page_size, int
     c.num_pages = (int)num_pages;
     c.page_size = (int)page_size;
     c.max_pages = (int)max_pages;
+    uint32_t log2 = 0;
+    while (((int64_t)1 << log2) < page_size) ++log2;
+    c.shift = 30 + log2;
+    c.mul = (uint32_t)(((((uint64_t)1 << c.shift) - 1) / (uint64_t)page_size) + 1);
     return c;
 }
 
@@ -450,7 +456,7 @@ int check_evict_shape(const attn_evict_args_t& a) {
 }
 
 struct EvictLayout {
-    size_t uses, cut, total, moves, list, fill, bytes;
+    size_t uses, cut, lens, total, fill, fill_w, bytes;
     int64_t most_moves;
 };
 EvictLayout evict_layout(const attn_evict_args_t& a) {
@@ -460,11 +466,11 @@ EvictLayout evict_layout(const attn_evict_args_t& a) {
     const size_t all = (size_t)(a.B * a.Hkv) * (size_t)l.most_moves;
     l.uses = 0;
     l.cut = align256((size_t)a.num_pages * 4);
-    l.total = l.cut + align256((size_t)a.B * 4);
-    l.moves = l.total + 256;
-    l.list = l.moves + align256((size_t)(a.B * a.Hkv) * 4);
-    l.fill = l.list + align256(all * 8);
-    l.bytes = l.fill + all * 8;
+    l.lens = l.cut + align256((size_t)a.B * 4);
+    l.total = l.lens + align256((size_t)a.B * 4);
+    l.fill = l.total + 256;
+    l.fill_w = l.fill + align256(all * 8);
+    l.bytes = l.fill_w + all * 8;
     return l;
 }
 
@@ -511,24 +517,25 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     p.recent = (int)a.recent;
     p.uses = reinterpret_cast<int32_t*>(ws + l.uses);
     p.cut = reinterpret_cast<int32_t*>(ws + l.cut);
+    p.lens = reinterpret_cast<int32_t*>(ws + l.lens);
     p.total = reinterpret_cast<int32_t*>(ws + l.total);
-    p.moves = reinterpret_cast<int32_t*>(ws + l.moves);
-    p.list = reinterpret_cast<int32_t*>(ws + l.list);
     p.fill = reinterpret_cast<int2*>(ws + l.fill);
-    p.most_moves = l.most_moves;
+    p.fill_w = reinterpret_cast<uint2*>(ws + l.fill_w);
     const int64_t rows = a.B * a.Hkv, room = a.max_pages * a.page_size;
-    // select: a cluster per row that holds its keys in shared memory where 8 CTAs can (else they are read again
-    // for each pass), and that gives every SM two CTAs where a CTA keeps 4096 keys
+    // select: the CTAs of a row hold its keys in shared memory where 8 of them can (else the keys are read again for
+    // each pass), and more of them share a row while every CTA has an SM and 2048 keys
     p.cluster = 1;
-    while (p.cluster < 8 && (room > (int64_t)p.cluster * kMostStaged || (rows * p.cluster < 2 * sms && room > p.cluster * 4096)))
+    while (p.cluster < kMostCluster && (room > (int64_t)p.cluster * kMostStaged || (2 * rows * p.cluster <= sms && room > p.cluster * 2048)))
         p.cluster *= 2;
     p.staged = (int)(cdiv(room, p.cluster) < kMostStaged ? cdiv(room, p.cluster) : kMostStaged);
     // column pieces of 32 bytes at least (a DRAM sector), until there is a CTA for every SM
     p.pieces = 1;
     while (2 * rows * p.pieces < sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
     if ((st = launch_clusters(attn_evict_prep_kernel, kPrepCtas, kPrepCtas, kPrepThreads, 0, stream, p)) != ATTN_OK) return st;
-    if ((st = launch_clusters(attn_evict_select_kernel, rows * p.cluster, p.cluster, kSelThreads, (size_t)p.staged * 4, stream, p)) != ATTN_OK)
-        return st;
+    // threads: two keys each at least, 512 or 1024
+    st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024>, rows * p.cluster, p.cluster, 1024, (size_t)p.staged * 4, stream, p)
+                         : launch_clusters(attn_evict_select_kernel<512>, rows * p.cluster, p.cluster, 512, (size_t)p.staged * 4, stream, p);
+    if (st != ATTN_OK) return st;
     if (l.most_moves > 0) {
         st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, stream, p)
                         : launch(attn_evict_fill_kernel<64>, 4 * sms, 1, kFillThreads, 0, stream, p);

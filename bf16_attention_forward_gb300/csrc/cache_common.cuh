@@ -25,12 +25,19 @@ __device__ __forceinline__ void report_invalid(uint32_t site) {
 struct Pages {
     const int32_t* table;
     int page_size, max_pages, num_pages;
+    uint32_t mul, shift;           // j / page_size = j * mul >> shift for 0 <= j < 2^30
 };
+
+// With 2^(L-1) < page_size <= 2^L and mul = ceil(2^(30+L) / page_size) < 2^31 the excess mul * page_size - 2^(30+L) is
+// below 2^L, so for j < 2^30 it never carries the quotient to the next integer.
+__device__ __forceinline__ int page_of(const Pages& c, int j) {
+    return (int)(((unsigned long long)(uint32_t)j * c.mul) >> c.shift);
+}
 
 // row of slot j of a sequence whose table row is `t` (j inside the table), -1 for a page that
 // the cache does not have
 __device__ __forceinline__ int page_row(const Pages& c, const int32_t* t, int j) {
-    const int pg = j / c.page_size;
+    const int pg = page_of(c, j);
     const int phys = __ldg(t + pg);
     return (unsigned)phys < (unsigned)c.num_pages ? phys * c.page_size + (j - pg * c.page_size) : -1;
 }

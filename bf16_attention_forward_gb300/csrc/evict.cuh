@@ -11,8 +11,10 @@
 // Prepare kernel (one cluster of 8 CTAs): counts each page's uses in the table and decides which sequences are
 // cut: over the budget, a valid length, every page in the cache and used once.
 // Select kernel (a cluster of 1 to 8 CTAs per (sequence, K/V head)): the weights are read once, as
-// order-preserving 32-bit keys that stay in shared memory; a radix select of 11 + 11 + 10 bits over the
-// cluster's summed histograms gives the threshold, and an ordered pass lists freed slots and late survivors.
+// order-preserving 32-bit keys that stay in shared memory.  A histogram of the upper 11 bits, summed over
+// the cluster, gives the bin of the threshold; a bin of up to 1024 keys is gathered, a key or two a
+// thread, and searched bit by bit with block-wide counts (0.04 us a bit), a larger one by two more
+// histograms.  An ordered pass then lists freed slots and late survivors.
 // Fill kernel: the rows that move into freed slots.  Their sources and targets are disjoint, so all
 // sequences' moves lie on one list (in no fixed order) that the warps share evenly.
 // Shift kernel: the recent block, and the weights.  Its rows may overlap their targets, so one CTA
@@ -42,18 +44,17 @@ struct EvictParams {
     // workspace
     int32_t* uses;             // [num_pages]: table entries of used pages that name the page
     int32_t* cut;              // [B]: the length n of a sequence that is cut, -1 - n of one that fits, 0: refused
+    int32_t* lens;             // [B]: lengths after the call (seqlens_out may be seqlens_k, which the select kernel reads)
     int32_t* total;            // moves on the fill list
-    int32_t* moves;            // [B][Hkv]: rows that move into freed slots
-    int32_t* list;             // [B][Hkv][2 * most_moves]: freed slots, then the survivors that fill them
     int2* fill;                // [B * Hkv * most_moves]: (to, from) as rows of [cache rows * Hkv]
-    long long most_moves;
+    uint2* fill_w;             // the same as elements of weights
 };
 
 constexpr int kPrepThreads = 1024;
 constexpr int kPrepCtas = 8;
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMostCluster = 8;
 constexpr int kBins = 2048;
+constexpr int kMostGathered = 1024;    // keys of the threshold's bin that are searched in registers
 constexpr int kMostStaged = 16384;     // 64 KB: three CTAs an SM
 constexpr int kFillThreads = 256;
 constexpr int kShiftThreads = 256;
@@ -82,6 +83,9 @@ __device__ __forceinline__ int4 cluster_ld4(uint32_t addr) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ void cluster_add(uint32_t addr, int v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ int cluster_ld(uint32_t addr) {
     int v;
@@ -122,43 +126,63 @@ __global__ void __launch_bounds__(kPrepThreads, 1) attn_evict_prep_kernel(const 
             }
             bad = __any_sync(0xFFFFFFFFu, bad);
         }
-        __syncwarp();                      // seqlens_out may be seqlens_k: every lane has read it
         if (lane == 0) {
             if (bad) report_invalid(ATTN_CACHE_SITE_EVICT);
             p.cut[b] = bad ? 0 : over ? n : -1 - n;
-            p.seqlens_out[b] = over && !bad ? p.budget : n;
+            p.lens[b] = over && !bad ? p.budget : n;
         }
     }
 }
 
-__global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
+// It starts while the prepare kernel runs, and waits for that before it touches what it writes.
+template <int T>
+__global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kWarps = T / 32, kU = 8;             // kU: loads in flight
     extern __shared__ uint32_t key_s[];
-    __shared__ __align__(16) int hist[3][kBins];
-    __shared__ int warp_n[3][kSelWarps];
+    __shared__ __align__(16) int hist[kBins], sum_s[3][kBins];   // this CTA's counts, and the cluster's of each pass
+    __shared__ uint32_t near_s[kMostGathered];         // this CTA's keys of the threshold's bin
+    __shared__ int near_n, warp_n[2][kWarps];
     __shared__ int total_s[2];             // ties and listed slots of this CTA, read by the cluster
     __shared__ int start_s;                // rank 0: the row's place on the fill list
     __shared__ uint32_t prefix_s;
     __shared__ int want_s, tied_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned below = (1u << lane) - 1;
-    pdl_wait();
-    pdl_launch();
     const int C = p.cluster, rank = blockIdx.x % C, bh = blockIdx.x / C;
     const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-    const int n = p.cut[b];
-    if (n <= 0) return;                    // (the whole cluster)
+    pdl_launch();
+    const int n = __ldg(p.seqlens_k + b);
     const long long room = (long long)p.pages.max_pages * p.pages.page_size;
-    const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
     const float* w = p.weights + bh * room;
+    float* out = p.weights_out + bh * room;
+    // slots [j0, j1) of the weights as they are, where the new ones have a buffer of their own
+    auto copy_weights = [&](int j0, int j1) {
+        for (int j = j0 + tid; j < j1; j += kU * T) {
+            float x[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (j + u * T < j1) x[u] = w[j + u * T];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (j + u * T < j1) out[j + u * T] = x[u];
+        }
+    };
+    if (!valid_len(p, n) || n <= p.budget) {           // (the whole cluster)
+        pdl_wait();                                    // the kernels behind this one rely on the one before it too
+        if (out != w && rank == 0 && valid_len(p, n)) copy_weights(0, n);
+        return;
+    }
+    const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
     const int keep = p.budget - p.sinks - p.recent, end = p.budget - p.recent;
     // this CTA's slots, and each warp's
     const int per = (n - p.recent - p.sinks - 1) / C + 1;
     const int lo = p.sinks + min(rank * per, n - p.recent - p.sinks), hi = min(lo + per, n - p.recent);
-    const bool staged = hi - lo <= p.staged;
-    const int per_warp = ((hi - lo - 1) / kSelThreads + 1) * 32;
+    const bool staged = per <= p.staged;               // (the same for the whole cluster)
+    const int per_warp = ((hi - lo - 1) / T + 1) * 32;
     const int wlo = min(lo + warp * per_warp, hi), whi = min(wlo + per_warp, hi);
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
-    __syncthreads();
+    for (int i = tid; i < kBins; i += T) hist[i] = sum_s[0][i] = sum_s[1][i] = sum_s[2][i] = 0;
+    if (tid == 0) near_n = 0;
+    if (C > 1) cluster_sync(); else __syncthreads();   // no CTA adds to another's counts before they are zero
 
     // the keep-th largest key of the row, and how many equal to it are kept
     uint32_t prefix = 0;
@@ -166,58 +190,118 @@ __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __
     for (int pass = 0; pass < 3 && keep > 0; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         if (pass > 0 && staged) {
-            for (int j = tid; j < hi - lo; j += kSelThreads) {
+#pragma unroll 4
+            for (int j = tid; j < hi - lo; j += T) {
                 const uint32_t key = key_s[j];
-                if ((key >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
+                if ((key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
             }
         } else {
-            constexpr int kU = 8;          // loads in flight
-            for (int j0 = lo + tid; j0 < hi; j0 += kU * kSelThreads) {
+            for (int j0 = lo + tid; j0 < hi; j0 += kU * T) {
                 float x[kU];
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    if (j0 + u * kSelThreads < hi) x[u] = w[j0 + u * kSelThreads];
+                    if (j0 + u * T < hi) x[u] = w[j0 + u * T];
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const int j = j0 + u * kSelThreads;
-                    if (j >= hi) break;
-                    const uint32_t key = weight_key(x[u]);
-                    if (staged) key_s[j - lo] = key;
-                    if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
+                    const int j = j0 + u * T;
+                    if (j < hi) {
+                        const uint32_t key = weight_key(x[u]);
+                        if (staged) key_s[j - lo] = key;
+                        if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
+                    }
                 }
             }
         }
-        if (C > 1) cluster_sync(); else __syncthreads();
-        // thread t: bins 4t .. 4t + 3, summed over the cluster, and the count of larger bins
-        int4 sum = make_int4(0, 0, 0, 0);
-        for (int r = 0; r < C; ++r) {
-            const int4 x = C > 1 ? cluster_ld4(cluster_map(ptx::smem_u32(&hist[pass][4 * tid]), r))
-                                 : *reinterpret_cast<const int4*>(&hist[pass][4 * tid]);
-            sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
-        }
-        const int mine = sum.x + sum.y + sum.z + sum.w;
-        int above = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int x = __shfl_down_sync(0xFFFFFFFFu, above, off);
-            if (lane + off < 32) above += x;
-        }
-        if (lane == 0) warp_n[pass][warp] = above;
         __syncthreads();
-        above -= mine;
-        for (int i = warp + 1; i < kSelWarps; ++i) above += warp_n[pass][i];
-        if (above < want && above + mine >= want) {
-            const int bin[4] = {sum.x, sum.y, sum.z, sum.w};
-            int e = 3;
-            while (above + bin[e] < want) above += bin[e--];
-            prefix_s = (prefix << bits) | (uint32_t)(4 * tid + e);
-            want_s = want - above;
-            tied_s = bin[e];
+        // of the first 512 threads thread t takes bins 4t .. 4t + 3: few are not empty, and those go to every CTA
+        int4 mine = make_int4(0, 0, 0, 0);
+        int* to = &sum_s[pass][4 * tid];
+        if (tid < kBins / 4) {
+            int4* from = reinterpret_cast<int4*>(&hist[4 * tid]);
+            mine = *from;
+            *from = make_int4(0, 0, 0, 0);
+            if (C > 1)
+                for (int r = 0; r < C; ++r) {
+                    const uint32_t at = cluster_map(ptx::smem_u32(to), r);
+                    if (mine.x) cluster_add(at, mine.x);
+                    if (mine.y) cluster_add(at + 4, mine.y);
+                    if (mine.z) cluster_add(at + 8, mine.z);
+                    if (mine.w) cluster_add(at + 12, mine.w);
+                }
+        }
+        if (C > 1) {
+            cluster_sync();
+            if (tid < kBins / 4) mine = *reinterpret_cast<const int4*>(to);
+        }
+        // larger bins: of the warps behind this one, then (in the one warp that holds the threshold) of the lanes
+        const int count = mine.x + mine.y + mine.z + mine.w, in_warp = __reduce_add_sync(0xFFFFFFFFu, count);
+        if (lane == 0) warp_n[pass & 1][warp] = in_warp;
+        __syncthreads();
+        const int behind = __reduce_add_sync(0xFFFFFFFFu, lane < kBins / 4 / 32 && lane > warp ? warp_n[pass & 1][lane] : 0);
+        if (behind < want && behind + in_warp >= want) {
+            int above = count;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_down_sync(0xFFFFFFFFu, above, off);
+                if (lane + off < 32) above += x;
+            }
+            above += behind - count;
+            if (above < want && above + count >= want) {
+                int e = 3, c = mine.w;
+                if (above + c < want) { above += c; e = 2; c = mine.z; }
+                if (e == 2 && above + c < want) { above += c; e = 1; c = mine.y; }
+                if (e == 1 && above + c < want) { above += c; e = 0; c = mine.x; }
+                prefix_s = (prefix << bits) | (uint32_t)(4 * tid + e);
+                want_s = want - above;
+                tied_s = c;
+            }
         }
         __syncthreads();
         prefix = prefix_s;
         want = want_s;
         tied = tied_s;
+        if (pass > 0 || !staged || tied > kMostGathered) continue;
+
+        // gather the bin's keys, of every CTA, a key or two a thread
+#pragma unroll 4
+        for (int j = tid; j < hi - lo; j += T) {
+            const uint32_t key = key_s[j];
+            if ((key >> 21) == prefix) near_s[atomicAdd(&near_n, 1)] = key;
+        }
+        if (C > 1) cluster_sync(); else __syncthreads();
+        constexpr int kEach = kMostGathered / T;
+        uint32_t key[kEach];
+        int first = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) key[e] = 0;
+        for (int r = 0; r < C; ++r) {
+            const int m = C > 1 ? cluster_ld(cluster_map(ptx::smem_u32(&near_n), r)) : near_n;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int i = tid + e * T - first;
+                if (i >= 0 && i < m)
+                    key[e] = C > 1 ? (uint32_t)cluster_ld(cluster_map(ptx::smem_u32(&near_s[0]) + 4 * i, r)) : near_s[i];
+            }
+            first += m;
+        }
+        // the largest x with at least `want` keys >= x (places without a key hold 0 and never count: x > 0, or all count)
+        uint32_t x = prefix << 21;
+#pragma unroll 1
+        for (int bit = 20; bit >= 0; --bit) {
+            const uint32_t at = x | (1u << bit);
+            int n_at = __syncthreads_count(key[0] >= at);
+            if (kEach > 1) n_at += __syncthreads_count(key[kEach - 1] >= at);
+            if (n_at >= want) x = at;
+        }
+        int larger = __syncthreads_count(key[0] > x && tid < tied), equal = __syncthreads_count(key[0] == x && tid < tied);
+        if (kEach > 1) {
+            larger += __syncthreads_count(key[kEach - 1] > x && tid + T < tied);
+            equal += __syncthreads_count(key[kEach - 1] == x && tid + T < tied);
+        }
+        prefix = x;
+        want -= larger;
+        tied = equal;
+        break;
     }
 
     auto key_at = [&](int j) { return staged ? key_s[j - lo] : weight_key(w[j]); };
@@ -226,12 +310,14 @@ __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __
     const bool some = tied > want;
     if (some) {
         int count = 0;
+#pragma unroll 4
         for (int j0 = wlo; j0 < whi; j0 += 32)
             count += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < whi && key_at(min(j0 + lane, hi - 1)) == prefix));
+        __syncthreads();
         if (lane == 0) warp_n[0][warp] = count;
         __syncthreads();
         int all = 0;
-        for (int i = 0; i < kSelWarps; ++i) {
+        for (int i = 0; i < kWarps; ++i) {
             const int x = warp_n[0][i];
             ties += i < warp ? x : 0;
             all += x;
@@ -242,63 +328,100 @@ __global__ void __launch_bounds__(kSelThreads) attn_evict_select_kernel(const __
             for (int r = 0; r < rank; ++r) ties += cluster_ld(cluster_map(ptx::smem_u32(&total_s[0]), r));
         }
     }
-    // freed slots below `end`, and survivors at or past it, counted and then listed in order
-    auto out_at = [&](int j0, int& seen) {
-        const int j = j0 + lane;
-        const bool in = j < whi;
-        const uint32_t key = in ? key_at(j) : 0u;
-        const bool tie = in && keep > 0 && key == prefix;
-        bool kept = in && keep > 0 && (key > prefix || tie);
+    // Listed are freed slots below `end` and survivors at or past it: a bit each, counted here and listed below.
+    // The bits of 32 slots take the place of their first key (the warp has read all 32 by then); without
+    // staged keys they are worked out twice.
+    const uint32_t least = keep > 0 ? prefix : 0xFFFFFFFFu;      // (above every key)
+    auto listed = [&](int j0, uint32_t key, int& seen) {
+        const bool in = j0 + lane < whi;
+        unsigned kept = __ballot_sync(0xFFFFFFFFu, in && key >= least);
         if (some) {
-            const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
-            if (tie) kept = seen + __popc(tb & below) < want;
+            const unsigned tb = __ballot_sync(0xFFFFFFFFu, in && key == prefix);
+            const bool late = ((tb >> lane) & 1) && seen + __popc(tb & below) >= want;
+            kept &= ~__ballot_sync(0xFFFFFFFFu, late);
             seen += __popc(tb);
         }
-        return in && (j < end ? !kept : kept);
+        // of the slots from j0 on `freed` lie below end, and `all` are the warp's
+        const int freed = min(max(end - j0, 0), 32), all = min(max(whi - j0, 0), 32);
+        const unsigned low = freed == 32 ? 0xFFFFFFFFu : (1u << freed) - 1, mine = all == 32 ? 0xFFFFFFFFu : (1u << all) - 1;
+        return (kept ^ low) & mine;
     };
+    constexpr int kR = 4;                  // rows of 32 slots at a time
     int count = 0, seen = ties;
-    for (int j0 = wlo; j0 < whi; j0 += 32) count += __popc(__ballot_sync(0xFFFFFFFFu, out_at(j0, seen)));
+    for (int j0 = wlo; j0 < whi; j0 += 32 * kR) {
+        uint32_t key[kR];
+        unsigned bits[kR];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) key[r] = j0 + 32 * r + lane < whi ? key_at(j0 + 32 * r + lane) : 0u;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            bits[r] = listed(j0 + 32 * r, key[r], seen);
+            count += __popc(bits[r]);
+        }
+        if (staged && lane == 0)
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+                if (j0 + 32 * r < whi) key_s[j0 + 32 * r - lo] = bits[r];
+    }
+    __syncthreads();
     if (lane == 0) warp_n[1][warp] = count;
     __syncthreads();
-    int at = 0, all = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
-        const int x = warp_n[1][i];
-        at += i < warp ? x : 0;
-        all += x;
-    }
+    const int warps_n = lane < kWarps ? warp_n[1][lane] : 0;
+    int at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warps_n : 0), all = __reduce_add_sync(0xFFFFFFFFu, warps_n);
+    pdl_wait();                            // the prepare kernel's verdict, and its zero in p.total
+    const bool stays = p.cut[b] == 0;
     if (C > 1) {
         if (tid == 0) total_s[1] = all;
         cluster_sync();
-        all = 0;
-        for (int r = 0; r < C; ++r) {
-            const int x = cluster_ld(cluster_map(ptx::smem_u32(&total_s[1]), r));
-            at += r < rank ? x : 0;
-            all += x;
-        }
+        const int x = lane < C ? cluster_ld(cluster_map(ptx::smem_u32(&total_s[1]), lane)) : 0;
+        at += __reduce_add_sync(0xFFFFFFFFu, lane < rank ? x : 0);
+        all = __reduce_add_sync(0xFFFFFFFFu, x);
     }
-    const int moves = all >> 1;
-    if (rank == 0 && tid == 0) {
-        p.moves[bh] = moves;
-        start_s = atomicAdd(p.total, moves);
+    const int moves = stays ? 0 : all >> 1;
+    if (rank == 0 && tid == 0) start_s = atomicAdd(p.total, moves);
+    if (out != w && !stays) {
+        if (rank == 0) copy_weights(0, p.sinks);
+        copy_weights(lo, min(hi, end));
+        for (int j = p.budget + rank * T + tid; j < n; j += C * T) out[j] = 0.0f;
     }
     if (C > 1) cluster_sync(); else __syncthreads();
-    int2* fill = p.fill + cluster_ld(cluster_map(ptx::smem_u32(&start_s), 0));
-    int32_t* list = p.list + bh * 2 * p.most_moves;
+    const int start = C > 1 ? cluster_ld(cluster_map(ptx::smem_u32(&start_s), 0)) : start_s;
+    int2* fill = p.fill + start;
+    uint2* fill_w = p.fill_w + start;
+    const uint32_t w0 = (uint32_t)(bh * room);
     seen = ties;
-    for (int j0 = wlo; j0 < whi; j0 += 32) {
-        const bool out = out_at(j0, seen);
-        const unsigned ob = __ballot_sync(0xFFFFFFFFu, out);
-        if (out) {
-            const int i = at + __popc(ob & below), row = page_row(p.pages, table, j0 + lane) * p.Hkv + h;
-            list[i] = j0 + lane;
-            if (i < moves) fill[i].x = row; else fill[i - moves].y = row;
+    if (moves > 0)
+        for (int j0 = wlo; j0 < whi; j0 += 32 * kR) {
+            unsigned bits[kR];
+            int row[kR];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                const int j = j0 + 32 * r;
+                if (j >= whi) bits[r] = 0;
+                else if (staged) bits[r] = key_s[j - lo];
+                else bits[r] = listed(j, j + lane < whi ? key_at(j + lane) : 0u, seen);
+                if ((bits[r] >> lane) & 1) row[r] = page_row(p.pages, table, j + lane) * p.Hkv + h;
+            }
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                if ((bits[r] >> lane) & 1) {
+                    const int i = at + __popc(bits[r] & below);
+                    const uint32_t we = w0 + (uint32_t)(j0 + 32 * r + lane);
+                    if (i < moves) {
+                        fill[i].x = row[r];
+                        fill_w[i].x = we;
+                    } else {
+                        fill[i - moves].y = row[r];
+                        fill_w[i - moves].y = we;
+                    }
+                }
+                at += __popc(bits[r]);
+            }
         }
-        at += __popc(ob);
-    }
     if (C > 1) cluster_sync();             // no CTA leaves while its shared memory may be read
 }
 
-// K and V rows into freed slots: 16 bytes a lane, a warp takes 512 bytes of rows at a time, 8 of them in flight.
+// K and V rows and weights into freed slots: 16 bytes a lane, a warp takes 512 bytes of rows at a time, 8 of them in flight.
 template <int D>
 __global__ void __launch_bounds__(kFillThreads, 4) attn_evict_fill_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kLanes = 2 * D / 16;                 // lanes of a K (or V) row
@@ -313,7 +436,11 @@ __global__ void __launch_bounds__(kFillThreads, 4) attn_evict_fill_kernel(const 
     for (long long m = (long long)(blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5)) * kU * kPer; m < total;
          m += (long long)warps * kU * kPer) {
         int2 mv = make_int2(0, 0);
-        if (lane < kU * kPer && m + lane < total) mv = p.fill[m + lane];
+        if (lane < kU * kPer && m + lane < total) {
+            mv = p.fill[m + lane];
+            const uint2 we = p.fill_w[m + lane];
+            p.weights_out[we.x] = p.weights[we.y];
+        }
         uint4 x[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -341,45 +468,15 @@ __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const _
     const int b = (int)(bh / p.Hkv), h = (int)(bh - (long long)b * p.Hkv);
     const long long room = (long long)p.pages.max_pages * p.pages.page_size;
     const int cut = p.cut[b];
+    if (task == tasks - 1 && h == 0 && tid == 0) p.seqlens_out[b] = p.lens[b];
     if (cut == 0) return;
     const bool over = cut > 0;
     const int n = over ? cut : -1 - cut, end = p.budget - p.recent, shift = n - p.budget;
 
     if (task == tasks - 1) {
+        if (!over) return;
         const float* w = p.weights + bh * room;
         float* out = p.weights_out + bh * room;
-        if (out != w) {
-            const int upto = over ? end : n;
-            for (int j0 = tid; j0 < upto; j0 += kU * kShiftThreads) {
-                float x[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    if (j0 + u * kShiftThreads < upto) x[u] = w[j0 + u * kShiftThreads];
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    if (j0 + u * kShiftThreads < upto) out[j0 + u * kShiftThreads] = x[u];
-            }
-        }
-        if (!over) return;
-        const int moves = p.moves[bh];
-        const int32_t* freed = p.list + bh * 2 * p.most_moves;
-        __syncthreads();
-        for (int i0 = tid; i0 < moves; i0 += kU * kShiftThreads) {
-            float x[kU];
-            int to[kU];
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int i = i0 + u * kShiftThreads;
-                if (i < moves) {
-                    to[u] = freed[i];
-                    x[u] = w[freed[moves + i]];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (i0 + u * kShiftThreads < moves) out[to[u]] = x[u];
-        }
-        __syncthreads();
         for (int i0 = 0; i0 < p.recent; i0 += kU * kShiftThreads) {
             float x[kU];
 #pragma unroll
@@ -391,7 +488,8 @@ __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const _
                 if (i0 + u * kShiftThreads + tid < p.recent) out[end + i0 + u * kShiftThreads + tid] = x[u];
         }
         __syncthreads();
-        for (int j = p.budget + tid; j < n; j += kShiftThreads) out[j] = 0.0f;
+        if (out == w)
+            for (int j = p.budget + tid; j < n; j += kShiftThreads) out[j] = 0.0f;
         return;
     }
     if (!over) return;

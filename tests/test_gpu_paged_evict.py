@@ -137,6 +137,21 @@ def test_weights_of_every_kind(attn, weights, protected):
     run(attn, [400, 1300, 130], 11, 128, 2, 64, 129, *protected, seed=3, weights=weights)
 
 
+def spread(rng, shape):
+    return (rng.standard_normal(shape) * 10.0 ** rng.integers(-30, 30, shape)).astype(np.float32)
+
+
+def near(rng, shape):
+    return (1.0 + rng.random(shape) / 16).astype(np.float32)      # all in one bin of the upper bits
+
+
+@pytest.mark.parametrize("weights", [ties, zeros, odd, spread, near], ids=lambda f: f.__name__)
+@pytest.mark.parametrize("n", [9000, 40000, 140000])
+def test_long_caches(attn, n, weights):
+    # a few CTAs a head that hold the keys; 140,000 slots are more than they hold
+    run(attn, [n, n // 3], -(-n // 512), 512, 1, 64, n // 4, 5, n // 9, seed=n, weights=weights, inplace=n != 40000)
+
+
 def test_again_and_again(attn):
     # a cache that grows by a chunk and is cut, with the recent window kept in order at the end
     P, Hkv, d, budget, recent, chunk, most = 16, 2, 64, 100, 20, 17, 8

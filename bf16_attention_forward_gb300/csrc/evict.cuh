@@ -12,9 +12,10 @@
 // cut: over the budget, a valid length, every page in the cache and used once.
 // Select kernel (a cluster of 1 to 8 CTAs per (sequence, K/V head)): the weights are read once, as
 // order-preserving 32-bit keys that stay in shared memory.  A histogram of the upper 11 bits, summed over
-// the cluster, gives the bin of the threshold; a bin of up to 1024 keys is gathered, a key or two a
-// thread, and searched bit by bit with block-wide counts (0.04 us a bit), a larger one by two more
-// histograms.  An ordered pass then lists freed slots and late survivors.
+// the cluster, gives the bin of the threshold, and two more histograms (of 11 and 10 bits) of that bin's keys the
+// threshold itself; a bin of up to 4096 keys is gathered into every CTA's registers for that, which spares
+// those two the cluster's exchange and the walk over all keys.  An ordered pass then lists freed slots and
+// late survivors.
 // Fill kernel: the rows that move into freed slots.  Their sources and targets are disjoint, so all
 // sequences' moves lie on one list (in no fixed order) that the warps share evenly.
 // Shift kernel: the recent block, and the weights.  Its rows may overlap their targets, so one CTA
@@ -52,9 +53,11 @@ struct EvictParams {
 
 constexpr int kPrepThreads = 1024;
 constexpr int kPrepCtas = 8;
-constexpr int kMostCluster = 8;
+constexpr int kMostCluster = 8;        // (16 took 25 us longer to start, for 1 us less in the select kernel)
 constexpr int kBins = 2048;
-constexpr int kMostGathered = 1024;    // keys of the threshold's bin that are searched in registers
+constexpr int kMostGathered = 2 * kBins;   // keys of the threshold's bin that are searched in registers
+constexpr int kMostRanked = 128;       // ... and up to which each key's rank says it (0.6 us less than the two passes)
+constexpr int kListRows = 8;           // rows of 32 slots that a warp lists at a time
 constexpr int kMostStaged = 16384;     // 64 KB: three CTAs an SM
 constexpr int kFillThreads = 256;
 constexpr int kShiftThreads = 256;
@@ -137,10 +140,16 @@ __global__ void __launch_bounds__(kPrepThreads, 1) attn_evict_prep_kernel(const 
 // It starts while the prepare kernel runs, and waits for that before it touches what it writes.
 template <int T>
 __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
-    constexpr int kWarps = T / 32, kU = 8;             // kU: loads in flight
+    constexpr int kWarps = T / 32, kU = 16;            // kU: loads in flight
+    constexpr int kEach = kMostGathered / T;
     extern __shared__ uint32_t key_s[];
-    __shared__ __align__(16) int hist[kBins], sum_s[3][kBins];   // this CTA's counts, and the cluster's of each pass
-    __shared__ uint32_t near_s[kMostGathered];         // this CTA's keys of the threshold's bin
+    __shared__ __align__(16) int pool[4][kBins];
+    int* const hist = pool[0];                         // this CTA's counts,
+    int(* const sum_s)[kBins] = &pool[1];              // and the cluster's of each pass;
+    uint32_t* const near_s = reinterpret_cast<uint32_t*>(pool[2]);   // instead of the last two, its keys of the
+                                                                     // threshold's bin;
+    static_assert(kWarps * kListRows * 32 * 2 <= 2 * sizeof pool[0], "the warps' lists take the place of the first two");
+    uint16_t* const slot_s = reinterpret_cast<uint16_t*>(pool[0]) + (threadIdx.x >> 5) * (kListRows * 32);
     __shared__ int near_n, warp_n[2][kWarps];
     __shared__ int total_s[2];             // ties and listed slots of this CTA, read by the cluster
     __shared__ int start_s;                // rank 0: the row's place on the fill list
@@ -180,16 +189,24 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
     const bool staged = per <= p.staged;               // (the same for the whole cluster)
     const int per_warp = ((hi - lo - 1) / T + 1) * 32;
     const int wlo = min(lo + warp * per_warp, hi), whi = min(wlo + per_warp, hi);
-    for (int i = tid; i < kBins; i += T) hist[i] = sum_s[0][i] = sum_s[1][i] = sum_s[2][i] = 0;
+    for (int i = tid; i < 4 * kBins; i += T) pool[0][i] = 0;
     if (tid == 0) near_n = 0;
     if (C > 1) cluster_sync(); else __syncthreads();   // no CTA adds to another's counts before they are zero
 
     // the keep-th largest key of the row, and how many equal to it are kept
     uint32_t prefix = 0;
     int want = keep, tied = 0;
+    bool gathered = false;
+    int first_tied = 0;
+    uint32_t near[kEach];
     for (int pass = 0; pass < 3 && keep > 0; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        if (pass > 0 && staged) {
+        if (gathered) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                if (tid + e * T < first_tied && (near[e] >> (shift + bits)) == prefix)
+                    atomicAdd(&hist[(near[e] >> shift) & ((1u << bits) - 1)], 1);
+        } else if (pass > 0 && staged) {
 #pragma unroll 4
             for (int j = tid; j < hi - lo; j += T) {
                 const uint32_t key = key_s[j];
@@ -220,7 +237,7 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
             int4* from = reinterpret_cast<int4*>(&hist[4 * tid]);
             mine = *from;
             *from = make_int4(0, 0, 0, 0);
-            if (C > 1)
+            if (C > 1 && !gathered)
                 for (int r = 0; r < C; ++r) {
                     const uint32_t at = cluster_map(ptx::smem_u32(to), r);
                     if (mine.x) cluster_add(at, mine.x);
@@ -229,7 +246,7 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
                     if (mine.w) cluster_add(at + 12, mine.w);
                 }
         }
-        if (C > 1) {
+        if (C > 1 && !gathered) {
             cluster_sync();
             if (tid < kBins / 4) mine = *reinterpret_cast<const int4*>(to);
         }
@@ -262,46 +279,46 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
         tied = tied_s;
         if (pass > 0 || !staged || tied > kMostGathered) continue;
 
-        // gather the bin's keys, of every CTA, a key or two a thread
+        // gather the bin's keys, of every CTA
 #pragma unroll 4
         for (int j = tid; j < hi - lo; j += T) {
             const uint32_t key = key_s[j];
             if ((key >> 21) == prefix) near_s[atomicAdd(&near_n, 1)] = key;
         }
         if (C > 1) cluster_sync(); else __syncthreads();
-        constexpr int kEach = kMostGathered / T;
-        uint32_t key[kEach];
-        int first = 0;
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) key[e] = 0;
+        if (C == 1 && tied <= kMostRanked) {           // each key's rank among them
+            if (tid < tied) {
+                const uint32_t key = near_s[tid];
+                int larger = 0, equal = 0;
+#pragma unroll 4
+                for (int i = 0; i < tied; ++i) {
+                    larger += near_s[i] > key;
+                    equal += near_s[i] == key;
+                }
+                if (larger < want && larger + equal >= want) {       // (keys equal to the threshold write the same)
+                    prefix_s = key;
+                    want_s = want - larger;
+                    tied_s = equal;
+                }
+            }
+            __syncthreads();
+            prefix = prefix_s;
+            want = want_s;
+            tied = tied_s;
+            break;
+        }
+        gathered = true;
+        first_tied = tied;
+        int before = 0;
         for (int r = 0; r < C; ++r) {
-            const int m = C > 1 ? cluster_ld(cluster_map(ptx::smem_u32(&near_n), r)) : near_n;
+            const int m = cluster_ld(cluster_map(ptx::smem_u32(&near_n), r));
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-                const int i = tid + e * T - first;
-                if (i >= 0 && i < m)
-                    key[e] = C > 1 ? (uint32_t)cluster_ld(cluster_map(ptx::smem_u32(&near_s[0]) + 4 * i, r)) : near_s[i];
+                const int i = tid + e * T - before;
+                if (i >= 0 && i < m) near[e] = (uint32_t)cluster_ld(cluster_map(ptx::smem_u32(near_s) + 4 * i, r));
             }
-            first += m;
+            before += m;
         }
-        // the largest x with at least `want` keys >= x (places without a key hold 0 and never count: x > 0, or all count)
-        uint32_t x = prefix << 21;
-#pragma unroll 1
-        for (int bit = 20; bit >= 0; --bit) {
-            const uint32_t at = x | (1u << bit);
-            int n_at = __syncthreads_count(key[0] >= at);
-            if (kEach > 1) n_at += __syncthreads_count(key[kEach - 1] >= at);
-            if (n_at >= want) x = at;
-        }
-        int larger = __syncthreads_count(key[0] > x && tid < tied), equal = __syncthreads_count(key[0] == x && tid < tied);
-        if (kEach > 1) {
-            larger += __syncthreads_count(key[kEach - 1] > x && tid + T < tied);
-            equal += __syncthreads_count(key[kEach - 1] == x && tid + T < tied);
-        }
-        prefix = x;
-        want -= larger;
-        tied = equal;
-        break;
     }
 
     auto key_at = [&](int j) { return staged ? key_s[j - lo] : weight_key(w[j]); };
@@ -328,41 +345,21 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
             for (int r = 0; r < rank; ++r) ties += cluster_ld(cluster_map(ptx::smem_u32(&total_s[0]), r));
         }
     }
-    // Listed are freed slots below `end` and survivors at or past it: a bit each, counted here and listed below.
-    // The bits of 32 slots take the place of their first key (the warp has read all 32 by then); without
-    // staged keys they are worked out twice.
+    // listed are freed slots below `end` and survivors at or past it: counted here, and listed below
     const uint32_t least = keep > 0 ? prefix : 0xFFFFFFFFu;      // (above every key)
-    auto listed = [&](int j0, uint32_t key, int& seen) {
-        const bool in = j0 + lane < whi;
-        unsigned kept = __ballot_sync(0xFFFFFFFFu, in && key >= least);
+    auto listed = [&](int j, uint32_t key, int& seen) {
+        bool kept = key >= least;
         if (some) {
-            const unsigned tb = __ballot_sync(0xFFFFFFFFu, in && key == prefix);
-            const bool late = ((tb >> lane) & 1) && seen + __popc(tb & below) >= want;
-            kept &= ~__ballot_sync(0xFFFFFFFFu, late);
+            const bool tie = j < whi && key == prefix;
+            const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
+            if (tie) kept = seen + __popc(tb & below) < want;
             seen += __popc(tb);
         }
-        // of the slots from j0 on `freed` lie below end, and `all` are the warp's
-        const int freed = min(max(end - j0, 0), 32), all = min(max(whi - j0, 0), 32);
-        const unsigned low = freed == 32 ? 0xFFFFFFFFu : (1u << freed) - 1, mine = all == 32 ? 0xFFFFFFFFu : (1u << all) - 1;
-        return (kept ^ low) & mine;
+        return __ballot_sync(0xFFFFFFFFu, j < whi && kept == (j >= end));
     };
-    constexpr int kR = 4;                  // rows of 32 slots at a time
     int count = 0, seen = ties;
-    for (int j0 = wlo; j0 < whi; j0 += 32 * kR) {
-        uint32_t key[kR];
-        unsigned bits[kR];
-#pragma unroll
-        for (int r = 0; r < kR; ++r) key[r] = j0 + 32 * r + lane < whi ? key_at(j0 + 32 * r + lane) : 0u;
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            bits[r] = listed(j0 + 32 * r, key[r], seen);
-            count += __popc(bits[r]);
-        }
-        if (staged && lane == 0)
-#pragma unroll
-            for (int r = 0; r < kR; ++r)
-                if (j0 + 32 * r < whi) key_s[j0 + 32 * r - lo] = bits[r];
-    }
+#pragma unroll 4
+    for (int j0 = wlo; j0 < whi; j0 += 32) count += __popc(listed(j0 + lane, j0 + lane < whi ? key_at(j0 + lane) : 0u, seen));
     __syncthreads();
     if (lane == 0) warp_n[1][warp] = count;
     __syncthreads();
@@ -391,32 +388,42 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
     const uint32_t w0 = (uint32_t)(bh * room);
     seen = ties;
     if (moves > 0)
-        for (int j0 = wlo; j0 < whi; j0 += 32 * kR) {
-            unsigned bits[kR];
-            int row[kR];
-#pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                const int j = j0 + 32 * r;
-                if (j >= whi) bits[r] = 0;
-                else if (staged) bits[r] = key_s[j - lo];
-                else bits[r] = listed(j, j + lane < whi ? key_at(j + lane) : 0u, seen);
-                if ((bits[r] >> lane) & 1) row[r] = page_row(p.pages, table, j + lane) * p.Hkv + h;
+        for (int j0 = wlo; j0 < whi; j0 += 32 * kListRows) {
+            // slots (from j0 on) that are listed, close together: about one in four is, and each costs a page lookup
+            int m = 0;
+#pragma unroll 4
+            for (int r = 0; r < kListRows; ++r) {
+                const int j = j0 + 32 * r + lane;
+                const unsigned bits = listed(j, j < whi ? key_at(j) : 0u, seen);
+                if ((bits >> lane) & 1) slot_s[m + __popc(bits & below)] = (uint16_t)(32 * r + lane);
+                m += __popc(bits);
             }
+            __syncwarp();
+            constexpr int kE = 4;              // page lookups in flight
+            for (int e0 = lane; e0 < m; e0 += 32 * kE) {
+                int j[kE], row[kE];
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                if ((bits[r] >> lane) & 1) {
-                    const int i = at + __popc(bits[r] & below);
-                    const uint32_t we = w0 + (uint32_t)(j0 + 32 * r + lane);
+                for (int u = 0; u < kE; ++u)
+                    if (e0 + 32 * u < m) {
+                        j[u] = j0 + slot_s[e0 + 32 * u];
+                        row[u] = page_row(p.pages, table, j[u]) * p.Hkv + h;
+                    }
+#pragma unroll
+                for (int u = 0; u < kE; ++u) {
+                    const int i = at + e0 + 32 * u;
+                    if (e0 + 32 * u >= m) continue;
+                    const uint32_t we = w0 + (uint32_t)j[u];
                     if (i < moves) {
-                        fill[i].x = row[r];
+                        fill[i].x = row[u];
                         fill_w[i].x = we;
                     } else {
-                        fill[i - moves].y = row[r];
+                        fill[i - moves].y = row[u];
                         fill_w[i - moves].y = we;
                     }
                 }
-                at += __popc(bits[r]);
             }
+            at += m;
+            __syncwarp();
         }
     if (C > 1) cluster_sync();             // no CTA leaves while its shared memory may be read
 }

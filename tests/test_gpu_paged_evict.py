@@ -146,9 +146,9 @@ def near(rng, shape):
 
 
 @pytest.mark.parametrize("weights", [ties, zeros, odd, spread, near], ids=lambda f: f.__name__)
-@pytest.mark.parametrize("n", [9000, 40000, 140000])
+@pytest.mark.parametrize("n", [9000, 40000, 140000, 300000])
 def test_long_caches(attn, n, weights):
-    # a few CTAs a head that hold the keys; 140,000 slots are more than they hold
+    # a few CTAs a head that hold the keys; 300,000 slots are more than sixteen hold
     run(attn, [n, n // 3], -(-n // 512), 512, 1, 64, n // 4, 5, n // 9, seed=n, weights=weights, inplace=n != 40000)
 
 

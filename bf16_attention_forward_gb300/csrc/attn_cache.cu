@@ -528,9 +528,9 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     while (p.cluster < kMostCluster && (room > (int64_t)p.cluster * kMostStaged || (2 * rows * p.cluster <= sms && room > p.cluster * 2048)))
         p.cluster *= 2;
     p.staged = (int)(cdiv(room, p.cluster) < kMostStaged ? cdiv(room, p.cluster) : kMostStaged);
-    // column pieces of 32 bytes at least (a DRAM sector), until there is a CTA for every SM
+    // column pieces of 32 bytes at least (a DRAM sector), until there are three CTAs for every SM
     p.pieces = 1;
-    while (2 * rows * p.pieces < sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
+    while (2 * rows * p.pieces < 3 * sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
     if ((st = launch_clusters(attn_evict_prep_kernel, kPrepCtas, kPrepCtas, kPrepThreads, 0, stream, p)) != ATTN_OK) return st;
     // threads: two keys each at least, 512 or 1024
     st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024>, rows * p.cluster, p.cluster, 1024, (size_t)p.staged * 4, stream, p)

@@ -345,14 +345,15 @@ int run_append(const attn_append_args_t& a, cudaStream_t stream) {
 int head_tiles(int64_t group) { return group <= 8 ? 1 : group <= 16 ? 2 : 4; }
 
 struct DecodeLayout {
-    size_t part_o, part_ml, row_ml, scores, bytes;
+    size_t part_o, part_ml, split, row_ml, scores, bytes;
 };
 DecodeLayout decode_layout(const attn_decode_args_t& a, int sms) {
     const int64_t heads = 8 * head_tiles(a.H / a.Hkv), blocks = cdiv(a.H / a.Hkv, heads);
     DecodeLayout l;
     l.part_o = 0;
     l.part_ml = align256((size_t)(2 * sms * heads * a.d) * 4);
-    l.row_ml = l.part_ml + align256((size_t)(2 * sms * heads) * 8);
+    l.split = l.part_ml + align256((size_t)(2 * sms * heads) * 8);
+    l.row_ml = l.split + align256((size_t)sms * 16);
     l.scores = l.row_ml + (a.weights ? align256((size_t)(a.B * a.Hkv * blocks * heads) * 8) : 0);
     l.bytes = l.scores + (a.weights ? (size_t)a.B * a.H * (size_t)(a.max_pages * a.page_size) * 4 : 0);
     return l;
@@ -371,10 +372,10 @@ int check_decode_shape(const attn_decode_args_t& a) {
 template <int D, int NH>
 int launch_decode(const DecodeParams& p, cudaStream_t stream) {
     int st;
+    // the weights' blocks: four an SM
     if (p.weights) {
         if ((st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
-        if ((st = launch(attn_decode_join_kernel<D, NH, true>, p.grid, 1, 256, 0, stream, p)) != ATTN_OK) return st;
-        return launch(attn_decode_weights_kernel<NH>, 4 * p.grid, 1, 256, 0, stream, p);
+        return launch(attn_decode_join_kernel<D, NH, true>, 5 * p.grid, 1, 256, 0, stream, p);
     }
     if ((st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
     return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);
@@ -435,6 +436,7 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     p.scale_log2 = (float)((1.0 / std::sqrt((double)a.d)) * 1.4426950408889634);
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+    p.split = reinterpret_cast<int4*>(ws + l.split);
     p.row_ml = reinterpret_cast<float2*>(ws + l.row_ml);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     if (a.d == 128) return nh == 1 ? launch_decode<128, 1>(p, stream) : nh == 2 ? launch_decode<128, 2>(p, stream) : launch_decode<128, 4>(p, stream);

@@ -18,7 +18,8 @@
 // ends inside it.  Each warp streams 16 keys of a tile through a ring of its own (cp.async, no
 // barrier between warps) and keeps its own m, l and o; the warps are joined at the end of a row.
 // A range holds at most one part that begins before it and one that ends behind it, so two part
-// slots per CTA suffice; attn_decode_join_kernel merges a split row's parts.
+// slots per CTA suffice; attn_decode_join_kernel merges a split row's parts, and beside that adds the
+// weights from the logits that the attention kernel kept.
 #pragma once
 #include "cache_common.cuh"
 
@@ -42,8 +43,9 @@ struct DecodeParams {
     // workspace
     float* part_o;                 // [2 * grid][heads of a block][d]
     float2* part_ml;               // [2 * grid][heads of a block]: (m in logits, l); l = -1: a bad page
-    float2* row_ml;                // [B][Hkv][head_blocks][heads of a block] (weights only)
-    float* scores;                 // [B][Hkv][max_pages * page_size][group] logits (weights only)
+    int4* split;                   // [grid]: (b, row, first and last CTA) of a row whose second part is the CTA's, else b = -1
+    float2* row_ml;                // [B][Hkv][head_blocks][heads of a block] of unsplit rows (weights only)
+    float* scores;                 // [B][H][max_pages * page_size] logits (weights only)
 };
 
 constexpr int kDecWarps = 8;
@@ -58,7 +60,8 @@ struct DecGeo {
     static constexpr int kStageBytes = 2 * kDecKeys * kRow;       // K then V of 16 keys: 8 KB or 4 KB
     static constexpr int kStages = D == 128 ? 3 : 6;              // 24 KB of ring per warp
     static constexpr int kRing = kDecWarps * kStages * kStageBytes;
-    static constexpr int kRed = kDecWarps * 8 * (D / 2) * 4;      // 8 heads, half of d, per warp
+    static constexpr int kRedRow = D / 2 + 4;                     // floats of a head's half row, padded against bank conflicts
+    static constexpr int kRed = kDecWarps * 8 * kRedRow * 4;      // 8 heads, half of d, per warp
     static constexpr int kSmem = kRing + kRed;
 };
 
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     constexpr int kChunks = G::kRow / 16;              // 16-byte chunks of a key
     constexpr int kRowsPerCopy = 32 / kChunks;         // keys that one cp.async of the warp takes
     extern __shared__ __align__(128) char smem[];
-    __shared__ float2 ml_s[kDecWarps][kHeads];
+    __shared__ float2 ml_s[kDecWarps][kHeads], joined_s[kHeads];
     __shared__ int bad_s[kDecWarps][G::kStages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = ptx::smem_u32(smem) + warp * (G::kStages * G::kStageBytes);
@@ -163,36 +166,45 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     pdl_wait();
     pdl_launch();
     const Line line = make_line(p);
-    if ((int)blockIdx.x >= line.ctas) return;
+    if ((int)blockIdx.x >= line.ctas) {
+        if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
     const long long u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
     long long row_first;
     Cursor cur = seek(p, u0, &row_first), ahead = cur;
-    int to_load = (int)(u1 - u0);
+    int to_find = (int)(u1 - u0), to_load = to_find;
     const long long key_stride = (long long)p.Hkv * G::kRow;
 
-    // loads this warp's 16 keys of the tile at `ahead` into a stage (rows past the length, and rows
-    // of a page that does not exist, become zeros) and moves on
-    auto load = [&](int stage) {
+    // Where the loads are: find() looks up the rows of this warp's 16 keys of the tile at `ahead` (-1: past the
+    // length or on a page that does not exist) and moves on; load() copies the tile found before into a
+    // stage, absent rows as zeros.  A tile is found one load ahead, so that the table's latency is hidden.
+    struct Found { int row; bool bad; int kv_head; };
+    auto find = [&]() {
+        Found f{-1, false, ahead.row / p.head_blocks};
+        if (to_find <= 0) return f;
+        const int j = ahead.tile * kDecTile + warp * kDecKeys + lane;
+        if (lane < kDecKeys && j < ahead.len) {
+            f.row = page_row(p.pages, p.pages.table + (long long)ahead.b * p.pages.max_pages, j);
+            f.bad = f.row < 0;
+        }
+        if (--to_find > 0) advance(p, ahead);
+        return f;
+    };
+    auto load = [&](int stage, const Found& f) {
         if (to_load > 0) {
-            const int j0 = ahead.tile * kDecTile + warp * kDecKeys;
-            int row = -1;
-            bool bad = false;
-            if (lane < kDecKeys && j0 + lane < ahead.len) {
-                row = page_row(p.pages, p.pages.table + (long long)ahead.b * p.pages.max_pages, j0 + lane);
-                bad = row < 0;
-            }
-            const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
+            const bool any_bad = __any_sync(0xFFFFFFFFu, f.bad);
             if (lane == 0) {
                 bad_s[warp][stage] = any_bad;
                 if (any_bad) report_invalid(ATTN_CACHE_SITE_DECODE);
             }
             const int chunk = lane % kChunks;
-            const long long col = (long long)(ahead.row / p.head_blocks) * G::kRow + chunk * 16;
+            const long long col = (long long)f.kv_head * G::kRow + chunk * 16;
             const uint32_t dst = ring + stage * G::kStageBytes;
 #pragma unroll
             for (int i = 0; i < kDecKeys / kRowsPerCopy; ++i) {
                 const int r = i * kRowsPerCopy + lane / kChunks;
-                const int src_row = __shfl_sync(0xFFFFFFFFu, row, r);
+                const int src_row = __shfl_sync(0xFFFFFFFFu, f.row, r);
                 const long long off = (long long)max(src_row, 0) * key_stride + col;
                 const uint32_t at = dst + r * G::kRow + ((chunk ^ (r & 7)) * 16);
                 const uint32_t bytes = src_row < 0 ? 0u : 16u;
@@ -200,12 +212,21 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 cp_async16(at + kDecKeys * G::kRow, p.v + off, bytes);
             }
             --to_load;
-            if (to_load > 0) advance(p, ahead);
         }
         cp_async_commit();
     };
+    Found found[G::kStages - 1];
 #pragma unroll
-    for (int s = 0; s < G::kStages - 1; ++s) load(s);
+    for (int s = 0; s < G::kStages - 1; ++s) found[s] = find();
+#pragma unroll
+    for (int s = 0; s < G::kStages - 1; ++s) load(s, found[s]);
+    Found next_tile = find();
+    if (threadIdx.x == 0) {
+        int4 d = make_int4(-1, 0, 0, 0);
+        if (row_first < u0 && line.cta_of(row_first) + 1 == (int)blockIdx.x)
+            d = make_int4(cur.b, cur.row, blockIdx.x - 1, line.cta_of(row_first + cur.tiles - 1));
+        p.split[blockIdx.x] = d;
+    }
 
     // ldmatrix addresses inside a stage: lane i gives row i % 8 of 8x8 matrix i / 8
     const int mat = lane >> 3, mrow = lane & 7;
@@ -269,15 +290,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int e = 0; e < 4; ++e) grow |= s[t][e] > m[t][e & 1] + tau;
             }
             if constexpr (kWeights) {
-                float* to = p.scores +
-                            ((long long)(b * p.Hkv + kv_head) * ((long long)p.pages.max_pages * p.pages.page_size) + j0) *
-                                p.group + head0 + (lane & 3) * 2;
+                const long long room = (long long)p.pages.max_pages * p.pages.page_size;
+                float* to = p.scores + ((long long)b * p.H + kv_head * p.group + head0 + (lane & 3) * 2) * room + j0;
 #pragma unroll
                 for (int t = 0; t < NH; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (j0 + (e >> 1) * 8 < len && head0 + t * 8 + (lane & 3) * 2 + (e & 1) < p.group)
-                            to[(e >> 1) * 8 * p.group + t * 8 + (e & 1)] = s[t][e];
+                            to[(t * 8 + (e & 1)) * room + (e >> 1) * 8] = s[t][e];
             }
             if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
@@ -298,7 +318,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                         }
                     }
             }
-            uint32_t pb[NH][2];
+            // The weights go to the second product as two bf16 parts, the upper 8 bits and the next 8 (an error of 2^-16;
+            // one part alone would add 2^-9 to every weight, as much as rounding the output).  Both parts of a
+            // positive weight are positive, so that an infinite value stays infinite.
+            uint32_t hi[NH][2], lo[NH][2];
 #pragma unroll
             for (int t = 0; t < NH; ++t) {
                 float w[4];
@@ -306,22 +329,30 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int e = 0; e < 4; ++e) w[e] = weight_of(s[t][e], m[t][e & 1], p.scale_log2);
                 l[t][0] += w[0] + w[2];
                 l[t][1] += w[1] + w[3];
-                // the weights go to the second product as bf16 (nearest even): an error of at most 2^-8
-                // relative in each, independent from key to key
-                pb[t][0] = movmatrix_trans(ptx::pack_bf16x2(w[0], w[1]));
-                pb[t][1] = movmatrix_trans(ptx::pack_bf16x2(w[2], w[3]));
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t h = ptx::pack_bf16x2_rz(w[2 * c], w[2 * c + 1]);
+                    const float r0 = w[2 * c] - __uint_as_float(h << 16), r1 = w[2 * c + 1] - __uint_as_float(h & 0xFFFF0000u);
+                    hi[t][c] = movmatrix_trans(h);
+                    lo[t][c] = movmatrix_trans(ptx::pack_bf16x2(w[2 * c] > 0.0f ? fmaxf(r0, 0x1p-126f) : r0,
+                                                                w[2 * c + 1] > 0.0f ? fmaxf(r1, 0x1p-126f) : r1));
+                }
             }
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
                 uint32_t a[4];
                 ldmatrix_x4_trans(vs_base + vrow * G::kRow + (((mt * 2 + vchunk) ^ (vrow & 7)) * 16), a);
 #pragma unroll
-                for (int t = 0; t < NH; ++t) mma_16816(acc[t][mt], a, pb[t][0], pb[t][1]);
+                for (int t = 0; t < NH; ++t) {
+                    mma_16816(acc[t][mt], a, hi[t][0], hi[t][1]);
+                    mma_16816(acc[t][mt], a, lo[t][0], lo[t][1]);
+                }
             }
             __syncwarp();                               // every lane has read the stage that is filled next
             int next = stage + G::kStages - 1;
             if (next >= G::kStages) next -= G::kStages;
-            load(next);
+            load(next, next_tile);
+            next_tile = find();
             stage = stage + 1 == G::kStages ? 0 : stage + 1;
         }
 
@@ -336,52 +367,61 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
             }
         bad = __syncthreads_or(bad);
         const bool whole = row_first >= u0 && row_end <= u1;
-        const int slot = 2 * blockIdx.x + (row_first >= u0 ? 1 : 0);
-        const long long row_id = ((long long)b * p.Hkv + kv_head) * p.head_blocks + (head0 / kHeads);
+        const long long slot = (2 * blockIdx.x + (row_first >= u0 ? 1 : 0)) * kHeads;
+        const long long out0 = (long long)b * p.H + kv_head * p.group + head0;
+        if (threadIdx.x < kHeads) {
+            const int h = threadIdx.x;
+            float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, ml_s[w][h].x);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) sum += ml_s[w][h].y * rescale(ml_s[w][h].x, mx, p.scale_log2);
+            // no weight at all (every logit -inf), or a NaN one: the row is NaN
+            joined_s[h] = make_float2(mx, whole ? (sum > 0.0f ? 1.0f / sum : NAN) : 1.0f);
+            const float2 ml = make_float2(mx, bad ? kBadPart : sum);
+            if (!whole) p.part_ml[slot + h] = ml;
+            else if (h < p.group - head0) {
+                if (p.lse && !bad) p.lse[out0 + h] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
+                if (kWeights) p.row_ml[(((long long)b * p.Hkv + kv_head) * p.head_blocks + head0 / kHeads) * kHeads + h] = ml;
+            }
+        }
+        // o in halves of d, 8 heads at a time: red[warp][head][d / 2]
 #pragma unroll
         for (int t = 0; t < NH; ++t) {
             float f[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float mx = -INFINITY;
+#pragma unroll
                 for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, ml_s[w][t * 8 + (lane & 3) * 2 + c].x);
                 f[c] = rescale(m[t][c], mx, p.scale_log2);
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                // red[warp][d / 2][8 heads]
+                float* to = red + (warp * 8 + (lane & 3) * 2) * G::kRedRow + (lane >> 2);
 #pragma unroll
                 for (int mt = 0; mt < D / 32; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float* a = acc[t][half * (D / 32) + mt];
-                        *reinterpret_cast<float2*>(
-                            red + (warp * (D / 2) + mt * 16 + e * 8 + (lane >> 2)) * 8 + (lane & 3) * 2) =
-                            make_float2(a[2 * e] * f[0], a[2 * e + 1] * f[1]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        to[(e & 1) * G::kRedRow + mt * 16 + (e >> 1) * 8] = acc[t][half * (D / 32) + mt][e] * f[e & 1];
                 __syncthreads();
-                for (int i = threadIdx.x; i < 8 * (D / 2); i += kDecThreads) {
-                    const int hh = i / (D / 2), x = i % (D / 2), h = head0 + t * 8 + hh;
-                    float mx = -INFINITY, sum = 0.0f, o = 0.0f;
-                    for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, ml_s[w][t * 8 + hh].x);
+                // two neighbouring elements of a head a thread
+                for (int i = threadIdx.x; i < 8 * (D / 4); i += kDecThreads) {
+                    const int hh = i / (D / 4), x = i % (D / 4) * 2;
+                    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
                     for (int w = 0; w < kDecWarps; ++w) {
-                        const float2 ml = ml_s[w][t * 8 + hh];
-                        sum += ml.y * rescale(ml.x, mx, p.scale_log2);
-                        o += red[(w * (D / 2) + x) * 8 + hh];
+                        const float2 part = *reinterpret_cast<const float2*>(red + (w * 8 + hh) * G::kRedRow + x);
+                        o.x += part.x;
+                        o.y += part.y;
                     }
-                    const int xd = half * (D / 2) + x;
-                    if (whole) {
-                        if (h < p.group && !bad) {
-                            const long long at = (long long)b * p.H + kv_head * p.group + h;
-                            // no weight at all (every logit -inf), or a NaN one: the row is NaN
-                            p.o[at * D + xd] = __ushort_as_bfloat16(
-                                (unsigned short)round_bf16(sum > 0.0f ? o / sum : NAN, p.round_mode));
-                            if (p.lse && xd == 0) p.lse[at] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
-                        }
-                        if (kWeights && xd == 0) p.row_ml[row_id * kHeads + t * 8 + hh] = make_float2(mx, bad ? kBadPart : sum);
-                    } else {
-                        p.part_o[((long long)slot * kHeads + t * 8 + hh) * D + xd] = o;
-                        if (xd == 0) p.part_ml[(long long)slot * kHeads + t * 8 + hh] = make_float2(mx, bad ? kBadPart : sum);
+                    const int xd = half * (D / 2) + x, h = t * 8 + hh;
+                    if (!whole) {
+                        *reinterpret_cast<float2*>(p.part_o + (slot + h) * D + xd) = o;
+                    } else if (head0 + h < p.group && !bad) {
+                        const float inv = joined_s[h].y;
+                        *reinterpret_cast<uint32_t*>(p.o + (out0 + h) * D + xd) =
+                            round_bf16(o.x * inv, p.round_mode) | round_bf16(o.y * inv, p.round_mode) << 16;
                     }
                 }
                 __syncthreads();
@@ -396,111 +436,140 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     }
 }
 
-// One block per CTA boundary of the line: the block of the first boundary inside a row merges the row's
-// parts.  It also writes the rows of sequences without keys and reports bad lengths.
+// The join.  Blocks 0 .. grid - 1: the block of the CTA that has a split row's second part merges the row's parts;
+// they also write the rows of sequences without keys and report bad lengths.  With kWeights the blocks
+// behind them add every key's softmax weights to its running weight, from the logits that the attention kernel
+// kept and the rows' (m, l); they divide the tiles evenly over (sequence, K/V head) rows.
 template <int D, int NH, bool kWeights>
 __global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int kHeads = 8 * NH, kC = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch();
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const int n = __ldg(p.seqlens_k + b);
-        if (n < 0 || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
-            if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
-        } else if (n == 0) {
-            for (long long i = threadIdx.x; i < (long long)p.H * D; i += 256)
-                p.o[(long long)b * p.H * D + i] = __ushort_as_bfloat16((unsigned short)0x7FC0u);
-            if (p.lse)
-                for (int h = threadIdx.x; h < p.H; h += 256) p.lse[(long long)b * p.H + h] = -INFINITY;
-        }
-    }
-    const Line line = make_line(p);
-    const int c = blockIdx.x;
-    if (c < 1 || c >= line.ctas) return;
-    const long long u = line.start(c);
-    long long first;
-    const Cursor cur = seek(p, u, &first);
-    if (first == u) return;                            // a row begins here: nothing is split
-    const int c0 = line.cta_of(first), c1 = line.cta_of(first + cur.tiles - 1);
-    if (c != c0 + 1) return;
-    const int kv_head = cur.row / p.head_blocks, block = cur.row - kv_head * p.head_blocks, head0 = block * kHeads;
-    for (int hh = warp; hh < kHeads; hh += 8) {
-        const int h = head0 + hh;
-        if (h >= p.group) break;
-        float mx = -INFINITY;
-        bool bad = false;
-        for (int i = c0 + lane; i <= c1; i += 32) {
-            const float2 ml = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
-            mx = fmaxf(mx, ml.x);
-            bad |= ml.y == kBadPart;
-        }
+    if ((int)blockIdx.x < p.grid) {
+        const int4 row = p.split[blockIdx.x];
+        const int b = row.x, c0 = row.z, c1 = row.w;
+        const int kv_head = row.y / p.head_blocks, head0 = (row.y - kv_head * p.head_blocks) * kHeads;
+        for (int hh = warp; b >= 0 && hh < kHeads && head0 + hh < p.group; hh += 8) {
+            // a row's first part is in slot 1 of its CTA, the others in slot 0 of theirs
+            float mx = -INFINITY;
+            bool bad = false;
+            for (int i = c0 + lane; i <= c1; i += 32) {
+                const float2 ml = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
+                mx = fmaxf(mx, ml.x);
+                bad |= ml.y == kBadPart;
+            }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        bad = __any_sync(0xFFFFFFFFu, bad);
-        float sum = 0.0f, o[kC];
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+            bad = __any_sync(0xFFFFFFFFu, bad);
+            float sum = 0.0f, o[kC];
 #pragma unroll
-        for (int x = 0; x < kC; ++x) o[x] = 0.0f;
-        for (int i = c0; i <= c1; ++i) {
-            const long long at = (long long)(2 * i + (i == c0)) * kHeads + hh;
-            const float2 ml = p.part_ml[at];
-            const float f = rescale(ml.x, mx, p.scale_log2);
-            sum += ml.y * f;
+            for (int x = 0; x < kC; ++x) o[x] = 0.0f;
+#pragma unroll 4
+            for (int i = c0; i <= c1; ++i) {
+                const long long at = (long long)(2 * i + (i == c0)) * kHeads + hh;
+                const float2 ml = p.part_ml[at];
+                const float f = rescale(ml.x, mx, p.scale_log2);
+                sum += ml.y * f;
 #pragma unroll
-            for (int x = 0; x < kC; ++x) o[x] += p.part_o[at * D + x * 32 + lane] * f;
-        }
-        if (!bad) {
-            const long long at = (long long)cur.b * p.H + kv_head * p.group + h;
+                for (int x = 0; x < kC; ++x) o[x] += p.part_o[at * D + x * 32 + lane] * f;
+            }
+            if (bad) continue;
+            const long long at = (long long)b * p.H + kv_head * p.group + head0 + hh;
+            const float inv = sum > 0.0f ? 1.0f / sum : NAN;
 #pragma unroll
             for (int x = 0; x < kC; ++x)
-                p.o[at * D + x * 32 + lane] = __ushort_as_bfloat16(
-                    (unsigned short)round_bf16(sum > 0.0f ? o[x] / sum : NAN, p.round_mode));
+                p.o[at * D + x * 32 + lane] = __ushort_as_bfloat16((unsigned short)round_bf16(o[x] * inv, p.round_mode));
             if (p.lse && lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
         }
-        if (kWeights && lane == 0)
-            p.row_ml[(((long long)cur.b * p.Hkv + kv_head) * p.head_blocks + block) * kHeads + hh] =
-                make_float2(mx, bad ? kBadPart : sum);
-    }
-}
-
-// Adds every key's softmax weights to its running weight: reads the logits that the attention kernel wrote
-// and the rows' final (m, l).  The tiles are divided as there, over (sequence, K/V head) rows.
-template <int NH>
-__global__ void __launch_bounds__(256) attn_decode_weights_kernel(DecodeParams p) {
-    constexpr int kHeads = 8 * NH;
-    pdl_wait();
-    pdl_launch();
-    const int blocks = p.head_blocks;
-    p.head_blocks = 1;                                 // a row is a K/V head here
-    p.grid = gridDim.x;
-    const Line line = make_line(p);
-    if ((int)blockIdx.x >= line.ctas) return;
-    const long long u1 = line.start(blockIdx.x + 1);
-    long long u = line.start(blockIdx.x), first;
-    Cursor cur = seek(p, u, &first);
-    const long long room = (long long)p.pages.max_pages * p.pages.page_size;
-    while (u < u1) {
-        const long long left = u1 - u;
-        const int n = left < cur.tiles - cur.tile ? (int)left : cur.tiles - cur.tile;
-        const int end = min(cur.len, (cur.tile + n) * kDecTile);
-        const long long row = (long long)cur.b * p.Hkv + cur.row;
-        const float2* ml = p.row_ml + row * blocks * kHeads;     // head g of the group is at g: blocks are full but the last
-        for (int j = cur.tile * kDecTile + threadIdx.x; j < end; j += 256) {
-            const float* s = p.scores + (row * room + j) * p.group;
-            float w = 0.0f;
-            bool bad = false;
-            for (int g = 0; g < p.group; ++g) {
-                const float2 x = ml[g];
-                bad |= x.y == kBadPart;
-                const float e = s[g] == -INFINITY ? 0.0f : exp2f((s[g] - x.x) * p.scale_log2);
-                w += e / x.y;
+        for (int s = blockIdx.x; s < p.B; s += p.grid) {
+            const int n = __ldg(p.seqlens_k + s);
+            if (n < 0 || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
+                if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
+            } else if (n == 0) {
+                for (long long i = threadIdx.x; i < (long long)p.H * D; i += 256)
+                    p.o[(long long)s * p.H * D + i] = __ushort_as_bfloat16((unsigned short)0x7FC0u);
+                if (p.lse)
+                    for (int h = threadIdx.x; h < p.H; h += 256) p.lse[(long long)s * p.H + h] = -INFINITY;
             }
-            if (!bad) p.weights[row * room + j] += w;
         }
-        u += n;
-        if (u < u1) {
-            cur.tile += n - 1;
-            advance(p, cur);
+        return;
+    }
+    if constexpr (kWeights) {
+        constexpr int kG = 8;                          // query heads at a time
+        __shared__ float2 ml_s[kG];                    // (m, 1 / l)
+        __shared__ int bad_s;
+        const Line line = make_line(p);
+        if (line.units == 0) return;
+        // this block's tiles of the line of K/V heads, which has a tile for head_blocks of the attention kernel's
+        const long long tiles = line.units / p.head_blocks;
+        const int block = blockIdx.x - p.grid, blocks = gridDim.x - p.grid;
+        const long long t1 = tiles * (block + 1) / blocks;
+        const long long room = (long long)p.pages.max_pages * p.pages.page_size;
+        for (long long t = tiles * block / blocks; t < t1;) {
+            // rows of a sequence are head_blocks times as many on the attention kernel's line
+            DecodeParams one = p;
+            one.head_blocks = 1;
+            long long first;
+            const Cursor cur = seek(one, t, &first);
+            const int n = (int)(t1 - t < cur.tiles - cur.tile ? t1 - t : cur.tiles - cur.tile);
+            const int j1 = min(cur.len, (cur.tile + n) * kDecTile);
+            const long long kv = (long long)cur.b * p.Hkv + cur.row;
+            // the place of the row's first block on the attention kernel's line: `first` counts the tiles of the
+            // heads before it once, that line head_blocks times
+            const long long main0 = first * p.head_blocks;
+            float* out = p.weights + kv * room;
+            for (int g0 = 0; g0 < p.group; g0 += kG) {
+                __syncthreads();
+                if (threadIdx.x == 0) bad_s = 0;
+                __syncthreads();
+                if (warp < kG && g0 + warp < p.group) {
+                    const int g = g0 + warp, blk = g / kHeads, hh = g - blk * kHeads;
+                    const long long r0 = main0 + (long long)blk * cur.tiles;
+                    const int c0 = line.cta_of(r0), c1 = line.cta_of(r0 + cur.tiles - 1);
+                    float2 ml;
+                    if (c0 == c1) {
+                        ml = p.row_ml[(kv * p.head_blocks + blk) * kHeads + hh];
+                    } else {
+                        float mx = -INFINITY, sum = 0.0f;
+                        bool bad = false;
+                        for (int i = c0 + lane; i <= c1; i += 32) {
+                            const float2 x = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
+                            mx = fmaxf(mx, x.x);
+                            bad |= x.y == kBadPart;
+                        }
+#pragma unroll
+                        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+                        for (int i = c0; i <= c1; ++i) {
+                            const float2 x = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
+                            sum += x.y * rescale(x.x, mx, p.scale_log2);
+                        }
+                        ml = make_float2(mx, __any_sync(0xFFFFFFFFu, bad) ? kBadPart : sum);
+                    }
+                    if (lane == 0) {
+                        ml_s[warp] = make_float2(ml.x, 1.0f / ml.y);
+                        if (ml.y == kBadPart) bad_s = 1;
+                    }
+                }
+                __syncthreads();
+                if (bad_s) break;
+                for (int j = cur.tile * kDecTile + threadIdx.x; j < j1; j += 256) {
+                    const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * room + j;
+                    float x[kG], w = 0.0f;
+                    const float old = out[j];
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) x[g] = g0 + g < p.group ? s[g * room] : -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        if (g0 + g >= p.group) break;
+                        // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
+                        const float e = x[g] == -INFINITY ? 0.0f : exp2f((x[g] - ml_s[g].x) * p.scale_log2);
+                        w += e * ml_s[g].y;
+                    }
+                    out[j] = old + w;
+                }
+            }
+            t += n;
         }
     }
 }

@@ -366,16 +366,19 @@ int check_decode_shape(const attn_decode_args_t& a) {
     if (a.H % a.Hkv != 0 || a.round_mode < ATTN_ROUND_RTNE || a.round_mode > ATTN_ROUND_RTZ || a.reserved != 0)
         return ATTN_ERR_INVALID_ARG;
     if (a.H > kLim || a.B * a.H > kLim) return ATTN_ERR_UNSUPPORTED;
+    // places on the attention kernel's line are int32
+    const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
+    if (cdiv(a.max_pages * a.page_size, kDecTile) + 1 > (2 * kLim - 1) / rows) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
 template <int D, int NH>
 int launch_decode(const DecodeParams& p, cudaStream_t stream) {
     int st;
-    // the weights' blocks: four an SM
+    // the weights' blocks: three an SM, beside one that joins
     if (p.weights) {
         if ((st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
-        return launch(attn_decode_join_kernel<D, NH, true>, 5 * p.grid, 1, 256, 0, stream, p);
+        return launch(attn_decode_join_kernel<D, NH, true>, 4 * p.grid, 1, 256, 0, stream, p);
     }
     if ((st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
     return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);

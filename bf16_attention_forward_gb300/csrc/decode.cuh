@@ -15,7 +15,8 @@
 // Work.  A CTA of 8 warps per SM.  The tiles (128 keys) of all (sequence, K/V head) rows form
 // one line, which the CTAs divide evenly: a CTA takes a contiguous range, so every CTA
 // reads the same bytes whatever the lengths are, and a row is split only where a range
-// ends inside it.  Each warp streams 16 keys of a tile through a ring of its own (cp.async, no
+// ends inside it.  Behind each row's tiles the line has one more place, which stands for the row's
+// end (loading its queries and joining the warps take about as long as a tile).  Each warp streams 16 keys of a tile through a ring of its own (cp.async, no
 // barrier between warps) and keeps its own m, l and o; the warps are joined at the end of a row.
 // A range holds at most one part that begins before it and one that ends behind it, so two part
 // slots per CTA suffice; attn_decode_join_kernel merges a split row's parts, and beside that adds the
@@ -66,77 +67,84 @@ struct DecGeo {
 };
 
 // tiles of a sequence; 0 for a length that the table has no room for (the join kernel reports it)
-__device__ __forceinline__ int seq_tiles(const DecodeParams& p, int b) {
-    const int n = __ldg(p.seqlens_k + b);
+__device__ __forceinline__ int seq_tiles(const DecodeParams& p, int n) {
     return n > 0 && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - 1) / kDecTile + 1 : 0;
 }
 
-// The line of tiles: sequence by sequence, row by row, tile by tile.
+// The line: sequence by sequence, row by row, a row's tiles and its end.  (The host refuses sizes whose
+// line could have 2^31 places.)
 struct Line {
-    long long units;               // tiles of all rows
+    int units;                     // places
     int ctas;                      // CTAs that get any: min(grid, units)
-    __device__ __forceinline__ long long start(int c) const { return units * c / ctas; }
-    __device__ __forceinline__ int cta_of(long long u) const { return (int)(((u + 1) * ctas - 1) / units); }
+    int per, more;                 // units / ctas, and how many CTAs have one more
+    __device__ __forceinline__ int start(int c) const { return per * c + min(c, more); }
+    __device__ __forceinline__ int cta_of(int u) const {
+        return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
+    }
 };
 
-__device__ __forceinline__ Line make_line(const DecodeParams& p) {   // every lane of a warp calls it
-    long long n = 0;
-    for (int b = threadIdx.x & 31; b < p.B; b += 32) n += seq_tiles(p, b);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+// rows: of a sequence
+__device__ __forceinline__ Line make_line(const DecodeParams& p, int rows) {   // every lane of a warp calls it
+    int n = 0;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        const int t = seq_tiles(p, __ldg(p.seqlens_k + b));
+        n += t > 0 ? t + 1 : 0;
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
     Line l;
-    l.units = n * p.Hkv * p.head_blocks;
-    l.ctas = (int)(l.units < p.grid ? l.units : p.grid);
+    l.units = n * rows;
+    l.ctas = min(l.units, p.grid);
+    l.per = l.ctas ? l.units / l.ctas : 1;
+    l.more = l.units - l.per * l.ctas;
     return l;
 }
 
 struct Cursor {
-    int b, row, tile, tiles, len;  // row: K/V head * head_blocks + block of query heads
+    int u, b, row, tile, tiles, len;   // place; row: K/V head * head_blocks + block of query heads; tile == tiles: its end
 };
 
-// the tile at place u of the line (u < units); *first: the place of its row's first tile
-__device__ __forceinline__ Cursor seek(const DecodeParams& p, long long u, long long* first) {
+// what is at place u of the line (u < units)
+__device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
     const int lane = threadIdx.x & 31;
-    const int rows = p.Hkv * p.head_blocks;
-    long long done = 0;
-    Cursor c{0, 0, 0, 1, 0};
+    int done = 0;                      // places of a row, of the sequences before
+    Cursor c{u, 0, 0, 0, 1, 0};
     for (int base = 0; base < p.B; base += 32) {
-        const int mine = base + lane < p.B ? seq_tiles(p, base + lane) : 0;
-        long long incl = mine;
+        const int len = base + lane < p.B ? __ldg(p.seqlens_k + base + lane) : 0, tiles = seq_tiles(p, len);
+        const int mine = tiles > 0 ? tiles + 1 : 0;
+        int incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+            const int x = __shfl_up_sync(0xFFFFFFFFu, incl, off);
             if (lane >= off) incl += x;
         }
         const unsigned past = __ballot_sync(0xFFFFFFFFu, (done + incl) * rows > u);
         if (past) {
             const int w = __ffs(past) - 1;
-            c.tiles = __shfl_sync(0xFFFFFFFFu, mine, w);
-            const long long before = (done + __shfl_sync(0xFFFFFFFFu, incl, w) - c.tiles) * rows;
             c.b = base + w;
-            c.row = (int)((u - before) / c.tiles);
-            c.tile = (int)((u - before) - (long long)c.row * c.tiles);
-            *first = u - c.tile;
+            c.len = __shfl_sync(0xFFFFFFFFu, len, w);
+            c.tiles = __shfl_sync(0xFFFFFFFFu, tiles, w);
+            const int in = u - (done + __shfl_sync(0xFFFFFFFFu, incl, w) - (c.tiles + 1)) * rows;
+            c.row = in / (c.tiles + 1);
+            c.tile = in - c.row * (c.tiles + 1);
             break;
         }
         done += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    c.len = __ldg(p.seqlens_k + c.b);
     return c;
 }
 
-// to the next tile of the line (there is one)
-__device__ __forceinline__ void advance(const DecodeParams& p, Cursor& c) {
-    if (++c.tile < c.tiles) return;
+// to the first tile of the next row (past the last sequence's last row: any place behind the line)
+__device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor& c) {
+    c.u += c.tiles + 1 - c.tile;
     c.tile = 0;
-    if (++c.row < p.Hkv * p.head_blocks) return;
+    if (++c.row < rows) return;
     c.row = 0;
     while (c.b + 1 < p.B) {
         ++c.b;
-        c.tiles = seq_tiles(p, c.b);
+        c.len = __ldg(p.seqlens_k + c.b);
+        c.tiles = seq_tiles(p, c.len);
         if (c.tiles > 0) break;
     }
-    c.len = __ldg(p.seqlens_k + c.b);
 }
 
 // softmax weight of logit s against the reference m, in base 2: exactly 1 for the logit that set m, a
@@ -165,34 +173,38 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
 
     pdl_wait();
     pdl_launch();
-    const Line line = make_line(p);
+    const int rows = p.Hkv * p.head_blocks;
+    const Line line = make_line(p, rows);
     if ((int)blockIdx.x >= line.ctas) {
         if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const long long u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
-    long long row_first;
-    Cursor cur = seek(p, u0, &row_first), ahead = cur;
-    int to_find = (int)(u1 - u0), to_load = to_find;
+    const int u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
+    Cursor cur = seek(p, rows, u0);
+    if (cur.tile == cur.tiles) next_row(p, rows, cur);
+    Cursor ahead = cur;
+    const Cursor at0 = cur;
     const long long key_stride = (long long)p.Hkv * G::kRow;
 
     // Where the loads are: find() looks up the rows of this warp's 16 keys of the tile at `ahead` (-1: past the
     // length or on a page that does not exist) and moves on; load() copies the tile found before into a
     // stage, absent rows as zeros.  A tile is found one load ahead, so that the table's latency is hidden.
-    struct Found { int row; bool bad; int kv_head; };
+    struct Found { int row, kv_head; bool bad; };      // kv_head: -1 behind the range
     auto find = [&]() {
-        Found f{-1, false, ahead.row / p.head_blocks};
-        if (to_find <= 0) return f;
+        Found f{-1, -1, false};
+        if (ahead.u >= u1) return f;
+        f.kv_head = ahead.row / p.head_blocks;
         const int j = ahead.tile * kDecTile + warp * kDecKeys + lane;
         if (lane < kDecKeys && j < ahead.len) {
             f.row = page_row(p.pages, p.pages.table + (long long)ahead.b * p.pages.max_pages, j);
             f.bad = f.row < 0;
         }
-        if (--to_find > 0) advance(p, ahead);
+        ++ahead.u;
+        if (++ahead.tile == ahead.tiles && ahead.u < u1) next_row(p, rows, ahead);
         return f;
     };
     auto load = [&](int stage, const Found& f) {
-        if (to_load > 0) {
+        if (f.kv_head >= 0) {
             const bool any_bad = __any_sync(0xFFFFFFFFu, f.bad);
             if (lane == 0) {
                 bad_s[warp][stage] = any_bad;
@@ -211,7 +223,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 cp_async16(at, p.k + off, bytes);
                 cp_async16(at + kDecKeys * G::kRow, p.v + off, bytes);
             }
-            --to_load;
         }
         cp_async_commit();
     };
@@ -221,12 +232,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
 #pragma unroll
     for (int s = 0; s < G::kStages - 1; ++s) load(s, found[s]);
     Found next_tile = find();
-    if (threadIdx.x == 0) {
-        int4 d = make_int4(-1, 0, 0, 0);
-        if (row_first < u0 && line.cta_of(row_first) + 1 == (int)blockIdx.x)
-            d = make_int4(cur.b, cur.row, blockIdx.x - 1, line.cta_of(row_first + cur.tiles - 1));
-        p.split[blockIdx.x] = d;
-    }
 
     // ldmatrix addresses inside a stage: lane i gives row i % 8 of 8x8 matrix i / 8
     const int mat = lane >> 3, mrow = lane & 7;
@@ -235,10 +240,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     const float tau = 8.0f / p.scale_log2;                             // a reference may lag by 2^8
     int stage = 0;
 
-    for (long long u = u0; u < u1;) {
+    while (cur.u < u1) {
         const int kv_head = cur.row / p.head_blocks, head0 = (cur.row - kv_head * p.head_blocks) * kHeads;
-        const long long row_end = row_first + cur.tiles;
-        const int n = (int)((row_end < u1 ? row_end : u1) - u);        // tiles of this row in the range
+        const int n = min(cur.tiles - cur.tile, u1 - cur.u);           // tiles of this row in the range
         const int b = cur.b, len = cur.len;
         // Q as the B operand: head lane / 4, elements 2 * (lane % 4) and + 8 of each 16
         uint32_t qf[NH][D / 16][2];
@@ -366,8 +370,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 if (lane < 4) ml_s[warp][t * 8 + lane * 2 + c] = make_float2(m[t][c], l[t][c]);
             }
         bad = __syncthreads_or(bad);
-        const bool whole = row_first >= u0 && row_end <= u1;
-        const long long slot = (2 * blockIdx.x + (row_first >= u0 ? 1 : 0)) * kHeads;
+        const bool whole = n == cur.tiles;
+        const long long slot = (2 * blockIdx.x + (cur.tile == 0 ? 1 : 0)) * kHeads;
         const long long out0 = (long long)b * p.H + kv_head * p.group + head0;
         if (threadIdx.x < kHeads) {
             const int h = threadIdx.x;
@@ -427,12 +431,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 __syncthreads();
             }
         }
-        u += n;
-        if (u < u1) {
-            cur.tile += n - 1;
-            advance(p, cur);
-            row_first = u;
-        }
+        next_row(p, rows, cur);
+    }
+    if (threadIdx.x == 0) {
+        // a row whose second part was this CTA's: for the join
+        int4 d = make_int4(-1, 0, 0, 0);
+        const int first = at0.u - at0.tile;
+        if (at0.tile > 0 && line.cta_of(first) + 1 == (int)blockIdx.x)
+            d = make_int4(at0.b, at0.row, blockIdx.x - 1, line.cta_of(first + at0.tiles - 1));
+        p.split[blockIdx.x] = d;
     }
 }
 
@@ -441,7 +448,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
 // behind them add every key's softmax weights to its running weight, from the logits that the attention kernel
 // kept and the rows' (m, l); they divide the tiles evenly over (sequence, K/V head) rows.
 template <int D, int NH, bool kWeights>
-__global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int kHeads = 8 * NH, kC = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
@@ -452,29 +459,45 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_cons
         const int kv_head = row.y / p.head_blocks, head0 = (row.y - kv_head * p.head_blocks) * kHeads;
         for (int hh = warp; b >= 0 && hh < kHeads && head0 + hh < p.group; hh += 8) {
             // a row's first part is in slot 1 of its CTA, the others in slot 0 of theirs
-            float mx = -INFINITY;
-            bool bad = false;
-            for (int i = c0 + lane; i <= c1; i += 32) {
-                const float2 ml = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
-                mx = fmaxf(mx, ml.x);
-                bad |= ml.y == kBadPart;
-            }
+            auto part = [&](int i) { return (long long)(2 * i + (i == c0)) * kHeads + hh; };
+            constexpr int kU = 8;                      // parts in flight
+            float v[kU][kC];
+            auto load = [&](int i0) {
+#pragma unroll
+                for (int j = 0; j < kU; ++j)
+                    if (i0 + j <= c1)
+#pragma unroll
+                        for (int x = 0; x < kC; ++x) v[j][x] = p.part_o[part(i0 + j) * D + x * 32 + lane];
+            };
+            float2 ml = c0 + lane <= c1 ? p.part_ml[part(c0 + lane)] : make_float2(-INFINITY, 0.0f);
+            load(c0);
+            float mx = ml.x;
+            for (int i = c0 + 32 + lane; i <= c1; i += 32) mx = fmaxf(mx, p.part_ml[part(i)].x);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-            bad = __any_sync(0xFFFFFFFFu, bad);
+            bool bad = false;
             float sum = 0.0f, o[kC];
 #pragma unroll
             for (int x = 0; x < kC; ++x) o[x] = 0.0f;
-#pragma unroll 4
-            for (int i = c0; i <= c1; ++i) {
-                const long long at = (long long)(2 * i + (i == c0)) * kHeads + hh;
-                const float2 ml = p.part_ml[at];
-                const float f = rescale(ml.x, mx, p.scale_log2);
-                sum += ml.y * f;
+            for (int base = c0; base <= c1; base += 32) {
+                // lane j: part base + j
+                if (base > c0) ml = base + lane <= c1 ? p.part_ml[part(base + lane)] : make_float2(-INFINITY, 0.0f);
+                bad |= ml.y == kBadPart;
+                const float f = rescale(ml.x, mx, p.scale_log2), s = ml.y * f;
+                const int n = min(32, c1 - base + 1);
+                for (int j0 = 0; j0 < n; j0 += kU) {
+                    if (base + j0 > c0) load(base + j0);
 #pragma unroll
-                for (int x = 0; x < kC; ++x) o[x] += p.part_o[at * D + x * 32 + lane] * f;
+                    for (int j = 0; j < kU; ++j)
+                        if (j0 + j < n) {
+                            const float fj = __shfl_sync(0xFFFFFFFFu, f, j0 + j);
+                            sum += __shfl_sync(0xFFFFFFFFu, s, j0 + j);
+#pragma unroll
+                            for (int x = 0; x < kC; ++x) o[x] += v[j][x] * fj;
+                        }
+                }
             }
-            if (bad) continue;
+            if (__any_sync(0xFFFFFFFFu, bad)) continue;
             const long long at = (long long)b * p.H + kv_head * p.group + head0 + hh;
             const float inv = sum > 0.0f ? 1.0f / sum : NAN;
 #pragma unroll
@@ -499,25 +522,21 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_cons
         constexpr int kG = 8;                          // query heads at a time
         __shared__ float2 ml_s[kG];                    // (m, 1 / l)
         __shared__ int bad_s;
-        const Line line = make_line(p);
-        if (line.units == 0) return;
-        // this block's tiles of the line of K/V heads, which has a tile for head_blocks of the attention kernel's
-        const long long tiles = line.units / p.head_blocks;
-        const int block = blockIdx.x - p.grid, blocks = gridDim.x - p.grid;
-        const long long t1 = tiles * (block + 1) / blocks;
+        const Line line = make_line(p, p.Hkv * p.head_blocks);
+        // this block's places on the line of K/V heads, which has one for head_blocks of the attention kernel's
+        const int units = line.units / p.head_blocks, block = blockIdx.x - p.grid, blocks = gridDim.x - p.grid;
+        const int t1 = (int)((long long)units * (block + 1) / blocks), t0 = (int)((long long)units * block / blocks);
+        if (t0 >= t1) return;
         const long long room = (long long)p.pages.max_pages * p.pages.page_size;
-        for (long long t = tiles * block / blocks; t < t1;) {
-            // rows of a sequence are head_blocks times as many on the attention kernel's line
-            DecodeParams one = p;
-            one.head_blocks = 1;
-            long long first;
-            const Cursor cur = seek(one, t, &first);
-            const int n = (int)(t1 - t < cur.tiles - cur.tile ? t1 - t : cur.tiles - cur.tile);
+        Cursor cur = seek(p, p.Hkv, t0);
+        for (; cur.u < t1; next_row(p, p.Hkv, cur)) {
+            const int n = min(cur.tiles - cur.tile, t1 - cur.u);
+            if (n == 0) continue;
             const int j1 = min(cur.len, (cur.tile + n) * kDecTile);
             const long long kv = (long long)cur.b * p.Hkv + cur.row;
-            // the place of the row's first block on the attention kernel's line: `first` counts the tiles of the
-            // heads before it once, that line head_blocks times
-            const long long main0 = first * p.head_blocks;
+            // the place of the head's first row on the attention kernel's line: the places of the heads before it
+            // count there head_blocks times
+            const int main0 = (cur.u - cur.tile) * p.head_blocks;
             float* out = p.weights + kv * room;
             for (int g0 = 0; g0 < p.group; g0 += kG) {
                 __syncthreads();
@@ -525,7 +544,7 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_cons
                 __syncthreads();
                 if (warp < kG && g0 + warp < p.group) {
                     const int g = g0 + warp, blk = g / kHeads, hh = g - blk * kHeads;
-                    const long long r0 = main0 + (long long)blk * cur.tiles;
+                    const int r0 = main0 + blk * (cur.tiles + 1);
                     const int c0 = line.cta_of(r0), c1 = line.cta_of(r0 + cur.tiles - 1);
                     float2 ml;
                     if (c0 == c1) {
@@ -553,23 +572,33 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_cons
                 }
                 __syncthreads();
                 if (bad_s) break;
-                for (int j = cur.tile * kDecTile + threadIdx.x; j < j1; j += 256) {
-                    const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * room + j;
-                    float x[kG], w = 0.0f;
-                    const float old = out[j];
+                constexpr int kJ = 2;                  // keys of a thread in flight
+                for (int j0 = cur.tile * kDecTile + threadIdx.x; j0 < j1; j0 += 256 * kJ) {
+                    const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * room + j0;
+                    float x[kJ][kG], w[kJ];
 #pragma unroll
-                    for (int g = 0; g < kG; ++g) x[g] = g0 + g < p.group ? s[g * room] : -INFINITY;
+                    for (int i = 0; i < kJ; ++i) {
+                        if (j0 + 256 * i >= j1) continue;
+                        w[i] = out[j0 + 256 * i];
 #pragma unroll
-                    for (int g = 0; g < kG; ++g) {
-                        if (g0 + g >= p.group) break;
-                        // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
-                        const float e = x[g] == -INFINITY ? 0.0f : exp2f((x[g] - ml_s[g].x) * p.scale_log2);
-                        w += e * ml_s[g].y;
+                        for (int g = 0; g < kG; ++g)
+                            if (g0 + g < p.group) x[i][g] = s[g * room + 256 * i];
                     }
-                    out[j] = old + w;
+#pragma unroll
+                    for (int i = 0; i < kJ; ++i) {
+                        if (j0 + 256 * i >= j1) continue;
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int g = 0; g < kG; ++g) {
+                            if (g0 + g >= p.group) continue;
+                            // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
+                            const float e = x[i][g] == -INFINITY ? 0.0f : exp2f((x[i][g] - ml_s[g].x) * p.scale_log2);
+                            sum += e * ml_s[g].y;
+                        }
+                        out[j0 + 256 * i] = w[i] + sum;
+                    }
                 }
             }
-            t += n;
         }
     }
 }

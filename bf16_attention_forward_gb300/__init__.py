@@ -7,8 +7,8 @@ is missing, importing the binding's entry points raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -670,24 +670,34 @@ def _wrong(t, name, dtype, dim, index):
     raise ValueError("%s must be contiguous" % name)
 
 
-def _tensor(t, name, dtype, dim, index=None):
-    """A contiguous CUDA tensor; returns its device's index."""
+def _device_of(t, name, dtype, dim):
+    """Index of a CUDA tensor's device."""
     import torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim or not t.is_contiguous()
-            or not t.is_cuda or (index is not None and t.get_device() != index)):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _wrong(t, name, dtype, dim, None)
+    return t.get_device()
+
+
+def _check(index, *wanted):
+    """(tensor, name, dtype, dimensions) each: contiguous tensors on one device."""
+    for t, name, dtype, dim in wanted:
+        try:
+            if t.dtype is dtype and t.get_device() == index and t.dim() == dim and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
         _wrong(t, name, dtype, dim, index)
-    return t.get_device()
 
 
-def _heads(t, name, dim, index=None):
-    """A bf16 tensor whose heads are contiguous, with any strides else; returns its device's index."""
+def _check_heads(index, dim, *wanted):
+    """(tensor, name) each: bf16 tensors on one device whose heads are contiguous, with any strides else."""
     import torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dim or not t.is_cuda
-            or (index is not None and t.get_device() != index)):
-        _wrong(t, name, torch.bfloat16, dim, index)
-    if t.stride()[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError("the head dimension of %s must be contiguous" % name)
-    return t.get_device()
+    for t, name in wanted:
+        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != dim
+                or t.get_device() != index):
+            _wrong(t, name, torch.bfloat16, dim, index)
+        if t.stride()[-1] != 1 and t.shape[-1] > 1:
+            raise ValueError("the head dimension of %s must be contiguous" % name)
 
 
 def rope_freqs(axis_dims, base: float = 10000.0, spectrum: str = "axis", scale=None, device="cuda"):
@@ -720,8 +730,7 @@ def _rope_tables(positions, freqs, axes, pairing, index, pos_dim):
     import torch
     if pairing not in PAIRINGS:
         raise ValueError("pairing must be adjacent or halves")
-    _tensor(freqs, "freqs", torch.float64, 1, index)
-    _tensor(axes, "axes", torch.int32, 1, index)
+    _check(index, (freqs, "freqs", torch.float64, 1), (axes, "axes", torch.int32, 1))
     pairs = freqs.numel()
     if pairs != axes.numel():
         raise ValueError("freqs and axes must have one entry per pair")
@@ -749,7 +758,8 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     if layout not in LAYOUTS:
         raise ValueError("layout must be bshd or bhsd")
     dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
-    dev = _heads(q, "q", dim)
+    dev = _device_of(q, "q", torch.bfloat16, dim)
+    _check_heads(dev, dim, (q, "q")) if k is None else _check_heads(dev, dim, (q, "q"), (k, "k"))
     per_batch = dim == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 3
     pairs = _rope_tables(positions, freqs, axes, pairing, dev, 3 if per_batch else 2)
     swap = dim == 4 and layout == "bhsd"
@@ -766,7 +776,6 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     (B, S, H, d), qs = geometry(q)
     Hkv, ks = 0, (0, 0, 0)
     if k is not None:
-        _heads(k, "k", dim, dev)
         (Bk, Sk, Hkv, dk), ks = geometry(k)
         if Bk != B or Sk != S or dk != d:
             raise ValueError("q and k must agree in all but their heads")
@@ -774,22 +783,24 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     if pn[-1] != S or (per_batch and pn[1] != B):
         raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
     for o, t, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if o is not None and (t is None or _heads(o, name, dim, dev) != dev or o.shape != t.shape):
-            raise ValueError("%s must have its input's shape" % name)
+        if o is not None:
+            _check_heads(dev, dim, (o, name))
+            if t is None or o.shape != t.shape:
+                raise ValueError("%s must have its input's shape" % name)
     on = _on(dev, stream)
     if on is not None:
         on.__enter__()
     try:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = q.new_empty(q.shape)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+            k_out = k.new_empty(k.shape)
         if S > 0:
             kp, ko, kos = (0, 0, ks) if k is None else (k.data_ptr(), k_out.data_ptr(), geometry(k_out)[1])
             a = _pack_rope(q.data_ptr(), q_out.data_ptr(), kp, ko, positions.data_ptr(), freqs.data_ptr(),
                            axes.data_ptr(), B, S, H, Hkv, d, *qs, *geometry(q_out)[1], *ks, *kos, pst[0],
                            pst[1] if per_batch else 0, pairs, pn[0], PAIRINGS[pairing], 1 if inverse else 0)
-            st = load().attn_rope(a, torch._C._cuda_getCurrentRawStream(dev))
+            st = (_lib or load()).attn_rope(a, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_rope")
     finally:
@@ -808,10 +819,9 @@ def attn_rope_bwd(dq, dk, positions, freqs, axes, layout: str = "bshd", pairing:
 def _check_cache(k_cache, v_cache, block_table, seqlens_k):
     """Checks the cache's tensors; returns (device index, pages, page size, Hkv, d, B, max pages)."""
     import torch
-    dev = _tensor(k_cache, "k_cache", torch.bfloat16, 4)
-    _tensor(v_cache, "v_cache", torch.bfloat16, 4, dev)
-    _tensor(seqlens_k, "seqlens_k", torch.int32, 1, dev)
-    _tensor(block_table, "block_table", torch.int32, 2, dev)
+    dev = _device_of(k_cache, "k_cache", torch.bfloat16, 4)
+    _check(dev, (k_cache, "k_cache", torch.bfloat16, 4), (v_cache, "v_cache", torch.bfloat16, 4),
+           (seqlens_k, "seqlens_k", torch.int32, 1), (block_table, "block_table", torch.int32, 2))
     shape, (B, most) = k_cache.shape, block_table.shape
     if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
@@ -835,9 +845,8 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
     it is allocated here), or None without ``q``."""
     import torch
     dev, pages, ps, Hkv, d, B, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
-    _heads(k, "k", 3, dev)
-    _heads(v, "v", 3, dev)
-    _tensor(cu_seqlens_new, "cu_seqlens_new", torch.int32, 1, dev)
+    _check_heads(dev, 3, (k, "k"), (v, "v")) if q is None else _check_heads(dev, 3, (k, "k"), (v, "v"), (q, "q"))
+    _check(dev, (cu_seqlens_new, "cu_seqlens_new", torch.int32, 1))
     shape = k.shape
     total = shape[0]
     if v.shape != shape or shape[1] != Hkv or shape[2] != d:
@@ -857,13 +866,14 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
         raise ValueError("pairing must be adjacent or halves")
     H, qs = 0, (0, 0)
     if q is not None:
-        _heads(q, "q", 3, dev)
         qt, H, qd = q.shape
         qs = q.stride()[:2]
         if qt != total or qd != d:
             raise ValueError("q must be [total, H, d]")
-        if q_out is not None and (_tensor(q_out, "q_out", torch.bfloat16, 3, dev) != dev or q_out.shape != q.shape):
-            raise ValueError("q_out must have q's shape")
+        if q_out is not None:
+            _check(dev, (q_out, "q_out", torch.bfloat16, 3))
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out needs q")
     on = _on(dev, stream)
@@ -878,7 +888,7 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
                              cu_seqlens_new.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(), pos, fp, ap, B, H,
                              Hkv, total, pages, ps, most, d, *qs, *k.stride()[:2], *v.stride()[:2], pos_stride, pairs,
                              num_axes, PAIRINGS[pairing], 0)
-            st = load().attn_paged_append(a, torch._C._cuda_getCurrentRawStream(dev))
+            st = (_lib or load()).attn_paged_append(a, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_paged_append")
     finally:
@@ -887,18 +897,20 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
     return q_out
 
 
-def _with_workspace(name, a, workspace, tensor, index):
-    """Calls an entry point that wants a workspace: the caller's, or one allocated on the current stream."""
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, index, *shape):
+    """A call's workspace size, by the shapes that it depends on (and the device, which has to be current)."""
+    a = (DecodeArgs if name == "attn_paged_decode" else EvictArgs)()
+    for n, x in shape:
+        setattr(a, n, x)
+    return max(int(getattr(load(), name + "_workspace_size")(ctypes.byref(a))), 16)
+
+
+def _check_workspace(workspace, index):
     import torch
-    lib = load()
-    if workspace is None:
-        workspace = torch.empty(max(getattr(lib, name + "_workspace_size")(a), 16), dtype=torch.uint8, device=tensor.device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != tensor.device or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
-    st = getattr(lib, name)(a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                            torch._C._cuda_getCurrentRawStream(index))
-    if st != 0:
-        raise AttnError(st, name)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None, o=None, lse=None,
@@ -917,20 +929,27 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
     if round not in MODES:
         raise ValueError("round must be rtne/rtna/rtz")
     dev, pages, ps, Hkv, dc, Bc, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
-    _tensor(q, "q", torch.bfloat16, 3, dev)
+    _check(dev, (q, "q", torch.bfloat16, 3))
     B, H, d = q.shape
     if B != Bc or d != dc:
         raise ValueError("q must be [B, H, d] with seqlens_k's B and the cache's d")
     if Hkv < 1 or H % Hkv != 0:
         raise ValueError("k/v heads (%d) must divide the query heads (%d)" % (Hkv, H))
     if weights is not None:
-        _tensor(weights, "weights", torch.float32, 3, dev)
+        _check(dev, (weights, "weights", torch.float32, 3))
         if weights.shape != (B, Hkv, most * ps):
             raise ValueError("weights must be [B, Hkv, max_pages * page_size]")
-    if o is not None and (_tensor(o, "o", torch.bfloat16, 3, dev) != dev or o.shape != q.shape):
-        raise ValueError("o must be shaped like q")
-    if lse is not None and (_tensor(lse, "lse", torch.float32, 2, dev) != dev or lse.shape != (B, H)):
-        raise ValueError("lse must be [B, H]")
+    if o is not None:
+        _check(dev, (o, "o", torch.bfloat16, 3))
+        if o.shape != q.shape:
+            raise ValueError("o must be shaped like q")
+    if lse is not None:
+        _check(dev, (lse, "lse", torch.float32, 2))
+        if lse.shape != (B, H):
+            raise ValueError("lse must be [B, H]")
+    ws_bytes = 0
+    if workspace is not None:
+        workspace, ws_bytes = _check_workspace(workspace, dev)
     on = _on(dev, stream)
     if on is not None:
         on.__enter__()
@@ -942,7 +961,14 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
         a = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
                          0 if lse is None else lse.data_ptr(), 0 if weights is None else weights.data_ptr(),
                          seqlens_k.data_ptr(), block_table.data_ptr(), B, H, Hkv, pages, ps, most, d, MODES[round], 0)
-        _with_workspace("attn_paged_decode", a, workspace, q, dev)
+        if workspace is None:
+            ws_bytes = _workspace_bytes("attn_paged_decode", dev, ("B", B), ("H", H), ("Hkv", Hkv), ("num_pages", pages),
+                                        ("page_size", ps), ("max_pages", most), ("d", d),
+                                        ("weights", 0 if weights is None else 16))
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        st = (_lib or load()).attn_paged_decode(a, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+        if st != 0:
+            raise AttnError(st, "attn_paged_decode")
     finally:
         if on is not None:
             on.__exit__(None, None, None)
@@ -965,21 +991,30 @@ def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: 
     dev, pages, ps, Hkv, d, B, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
     weights_out = weights if weights_out is None else weights_out
     seqlens_out = seqlens_k if seqlens_out is None else seqlens_out
-    for t, name in ((weights, "weights"), (weights_out, "weights_out")):
-        _tensor(t, name, torch.float32, 3, dev)
-        if t.shape != (B, Hkv, most * ps):
-            raise ValueError("%s must be [B, Hkv, max_pages * page_size]" % name)
-    _tensor(seqlens_out, "seqlens_out", torch.int32, 1, dev)
+    _check(dev, (weights, "weights", torch.float32, 3), (weights_out, "weights_out", torch.float32, 3),
+           (seqlens_out, "seqlens_out", torch.int32, 1))
+    if weights.shape != (B, Hkv, most * ps) or weights_out.shape != (B, Hkv, most * ps):
+        raise ValueError("weights and weights_out must be [B, Hkv, max_pages * page_size]")
     if seqlens_out.numel() != B:
         raise ValueError("seqlens_out must hold B lengths")
+    budget, sinks, recent, ws_bytes = int(budget), int(sinks), int(recent), 0
+    if workspace is not None:
+        workspace, ws_bytes = _check_workspace(workspace, dev)
     on = _on(dev, stream)
     if on is not None:
         on.__enter__()
     try:
         a = _pack_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
                         seqlens_k.data_ptr(), seqlens_out.data_ptr(), block_table.data_ptr(), B, Hkv, pages, ps, most, d,
-                        int(budget), int(sinks), int(recent))
-        _with_workspace("attn_paged_evict", a, workspace, k_cache, dev)
+                        budget, sinks, recent)
+        if workspace is None:
+            ws_bytes = _workspace_bytes("attn_paged_evict", dev, ("B", B), ("Hkv", Hkv), ("num_pages", pages),
+                                        ("page_size", ps), ("max_pages", most), ("d", d), ("budget", budget),
+                                        ("sinks", sinks), ("recent", recent))
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=k_cache.device)
+        st = (_lib or load()).attn_paged_evict(a, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+        if st != 0:
+            raise AttnError(st, "attn_paged_evict")
     finally:
         if on is not None:
             on.__exit__(None, None, None)

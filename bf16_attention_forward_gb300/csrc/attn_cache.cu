@@ -222,7 +222,7 @@ int launch_rope(RopeParams& p, int64_t d, bool halves, bool append, int sms, cud
     // short of threads (2048 each); then the heads are dealt out evenly.
     const int64_t lanes = p.tokens * (d / 16), full = (int64_t)sms * 2048;
     int64_t splits = lanes < full ? cdiv(full, lanes) : 1;
-    if (splits > cdiv(p.heads, kRopeUnroll)) splits = cdiv(p.heads, kRopeUnroll);
+    if (splits > cdiv(p.heads, kRopeHeads)) splits = cdiv(p.heads, kRopeHeads);
     p.heads_per_thread = (int)cdiv(p.heads, splits);
     const int64_t grid = cdiv(lanes, kRopeThreads);
     const int gy = (int)cdiv(p.heads, p.heads_per_thread);
@@ -532,7 +532,8 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     p.cluster = 1;
     while (p.cluster < kMostCluster && (room > (int64_t)p.cluster * kMostStaged || (2 * rows * p.cluster <= sms && room > p.cluster * 2048)))
         p.cluster *= 2;
-    p.staged = (int)(cdiv(room, p.cluster) < kMostStaged ? cdiv(room, p.cluster) : kMostStaged);
+    p.staged = (int)cdiv(cdiv(room, p.cluster), 1024) * 1024;
+    if (p.staged > kMostStaged) p.staged = kMostStaged;
     // column pieces of 32 bytes at least (a DRAM sector), until there are three CTAs for every SM
     p.pieces = 1;
     while (2 * rows * p.pieces < 3 * sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) attn_evict_prep_kernel(const 
 
 // It starts while the prepare kernel runs, and waits for that before it touches what it writes.
 template <int T>
-__global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kWarps = T / 32, kU = 16;            // kU: loads in flight
     constexpr int kEach = kMostGathered / T;
     extern __shared__ uint32_t key_s[];
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
     static_assert(kWarps * kListRows * 32 * 2 <= 2 * sizeof pool[0], "the warps' lists take the place of the first two");
     uint16_t* const slot_s = reinterpret_cast<uint16_t*>(pool[0]) + (threadIdx.x >> 5) * (kListRows * 32);
     __shared__ int near_n, warp_n[2][kWarps];
-    __shared__ int total_s[2];             // ties and listed slots of this CTA, read by the cluster
+    __shared__ int count_s[2][kWarps];     // ties and listed slots of each warp, read by the cluster
     __shared__ int start_s;                // rank 0: the row's place on the fill list
     __shared__ uint32_t prefix_s;
     __shared__ int want_s, tied_s;
@@ -164,31 +164,32 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
     const long long room = (long long)p.pages.max_pages * p.pages.page_size;
     const float* w = p.weights + bh * room;
     float* out = p.weights_out + bh * room;
-    // slots [j0, j1) of the weights as they are, where the new ones have a buffer of their own
-    auto copy_weights = [&](int j0, int j1) {
-        for (int j = j0 + tid; j < j1; j += kU * T) {
+    // slots j0 .. j1 - 1 of the weights as they are, where the new ones have a buffer of their own
+    auto copy_weights = [&](int j0, int j1, int thread, int threads) {
+        for (int j = j0 + thread; j < j1; j += kU * threads) {
             float x[kU];
 #pragma unroll
             for (int u = 0; u < kU; ++u)
-                if (j + u * T < j1) x[u] = w[j + u * T];
+                if (j + u * threads < j1) x[u] = w[j + u * threads];
 #pragma unroll
             for (int u = 0; u < kU; ++u)
-                if (j + u * T < j1) out[j + u * T] = x[u];
+                if (j + u * threads < j1) out[j + u * threads] = x[u];
         }
     };
     if (!valid_len(p, n) || n <= p.budget) {           // (the whole cluster)
         pdl_wait();                                    // the kernels behind this one rely on the one before it too
-        if (out != w && rank == 0 && valid_len(p, n)) copy_weights(0, n);
+        if (out != w && rank == 0 && valid_len(p, n)) copy_weights(0, n, tid, T);
         return;
     }
     const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
     const int keep = p.budget - p.sinks - p.recent, end = p.budget - p.recent;
-    // this CTA's slots, and each warp's
-    const int per = (n - p.recent - p.sinks - 1) / C + 1;
-    const int lo = p.sinks + min(rank * per, n - p.recent - p.sinks), hi = min(lo + per, n - p.recent);
-    const bool staged = per <= p.staged;               // (the same for the whole cluster)
-    const int per_warp = ((hi - lo - 1) / T + 1) * 32;
-    const int wlo = min(lo + warp * per_warp, hi), whi = min(wlo + per_warp, hi);
+    // The slots between the sinks and the recent ones go to the warps of the cluster in runs of `run`, CTA by CTA within
+    // a warp number: freed slots lie at the front and would otherwise all be one CTA's.
+    const int all_slots = n - p.recent - p.sinks, run = ((all_slots - 1) / (C * T) + 1) * 32;
+    const int place = warp * C + rank;                 // of this warp among the cluster's
+    const int wlo = p.sinks + min(place * run, all_slots), whi = min(wlo + run, n - p.recent);
+    const bool staged = run * kWarps <= p.staged;      // (the same for the whole cluster)
+    uint32_t* const key_w = key_s + warp * run;        // this warp's keys
     for (int i = tid; i < 4 * kBins; i += T) pool[0][i] = 0;
     if (tid == 0) near_n = 0;
     if (C > 1) cluster_sync(); else __syncthreads();   // no CTA adds to another's counts before they are zero
@@ -208,22 +209,22 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
                     atomicAdd(&hist[(near[e] >> shift) & ((1u << bits) - 1)], 1);
         } else if (pass > 0 && staged) {
 #pragma unroll 4
-            for (int j = tid; j < hi - lo; j += T) {
-                const uint32_t key = key_s[j];
+            for (int j = lane; j < whi - wlo; j += 32) {
+                const uint32_t key = key_w[j];
                 if ((key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
             }
         } else {
-            for (int j0 = lo + tid; j0 < hi; j0 += kU * T) {
+            for (int j0 = wlo + lane; j0 < whi; j0 += kU * 32) {
                 float x[kU];
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    if (j0 + u * T < hi) x[u] = w[j0 + u * T];
+                    if (j0 + u * 32 < whi) x[u] = w[j0 + u * 32];
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    const int j = j0 + u * T;
-                    if (j < hi) {
+                    const int j = j0 + u * 32;
+                    if (j < whi) {
                         const uint32_t key = weight_key(x[u]);
-                        if (staged) key_s[j - lo] = key;
+                        if (staged) key_w[j - wlo] = key;
                         if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
                     }
                 }
@@ -281,8 +282,8 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
 
         // gather the bin's keys, of every CTA
 #pragma unroll 4
-        for (int j = tid; j < hi - lo; j += T) {
-            const uint32_t key = key_s[j];
+        for (int j = lane; j < whi - wlo; j += 32) {
+            const uint32_t key = key_w[j];
             if ((key >> 21) == prefix) near_s[atomicAdd(&near_n, 1)] = key;
         }
         if (C > 1) cluster_sync(); else __syncthreads();
@@ -309,41 +310,48 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
         }
         gathered = true;
         first_tied = tied;
-        int before = 0;
-        for (int r = 0; r < C; ++r) {
-            const int m = cluster_ld(cluster_map(ptx::smem_u32(&near_n), r));
+        const int near_r = lane < C ? cluster_ld(cluster_map(ptx::smem_u32(&near_n), lane)) : 0;
+        int before[kEach], from[kEach];                // keys of the CTAs before the one that holds key tid + e * T
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int i = tid + e * T - before;
-                if (i >= 0 && i < m) near[e] = (uint32_t)cluster_ld(cluster_map(ptx::smem_u32(near_s) + 4 * i, r));
-            }
-            before += m;
+        for (int e = 0; e < kEach; ++e) before[e] = from[e] = 0;
+        int sum = 0;
+        for (int r = 0; r + 1 < C; ++r) {
+            sum += __shfl_sync(0xFFFFFFFFu, near_r, r);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                if (tid + e * T >= sum) { before[e] = sum; from[e] = r + 1; }
         }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (tid + e * T < tied)
+                near[e] = (uint32_t)cluster_ld(cluster_map(ptx::smem_u32(near_s) + 4 * (tid + e * T - before[e]), from[e]));
     }
 
-    auto key_at = [&](int j) { return staged ? key_s[j - lo] : weight_key(w[j]); };
+    auto key_at = [&](int j) { return staged ? key_w[j - wlo] : weight_key(w[j]); };
+    // Of a count of this warp's: the sum over the warps before it in the cluster, and over all.  Every warp of the
+    // cluster leaves its count in its CTA, and each reads them all.
+    auto sums_before = [&](int count, int which, int& all) {
+        if (lane == 0) count_s[which][warp] = count;
+        if (C > 1) cluster_sync(); else __syncthreads();
+        int before = 0, total = 0;
+        for (int r = 0; r < C; ++r) {
+            const uint32_t from = ptx::smem_u32(&count_s[which][lane]);
+            const int x = lane < kWarps ? (C > 1 ? cluster_ld(cluster_map(from, r)) : count_s[which][lane]) : 0;
+            total += x;
+            before += lane * C + r < place ? x : 0;
+        }
+        all = __reduce_add_sync(0xFFFFFFFFu, total);
+        return __reduce_add_sync(0xFFFFFFFFu, before);
+    };
     // of the keys equal to the threshold the first `want` are kept: where not all are, their ranks count
-    int ties = 0;                          // ties before this warp's slots
+    int ties = 0, all = 0;                 // ties before this warp's slots
     const bool some = tied > want;
     if (some) {
         int count = 0;
 #pragma unroll 4
         for (int j0 = wlo; j0 < whi; j0 += 32)
-            count += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < whi && key_at(min(j0 + lane, hi - 1)) == prefix));
-        __syncthreads();
-        if (lane == 0) warp_n[0][warp] = count;
-        __syncthreads();
-        int all = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            const int x = warp_n[0][i];
-            ties += i < warp ? x : 0;
-            all += x;
-        }
-        if (C > 1) {
-            if (tid == 0) total_s[0] = all;
-            cluster_sync();
-            for (int r = 0; r < rank; ++r) ties += cluster_ld(cluster_map(ptx::smem_u32(&total_s[0]), r));
-        }
+            count += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < whi && key_at(min(j0 + lane, whi - 1)) == prefix));
+        ties = sums_before(count, 0, all);
     }
     // listed are freed slots below `end` and survivors at or past it: counted here, and listed below
     const uint32_t least = keep > 0 ? prefix : 0xFFFFFFFFu;      // (above every key)
@@ -360,25 +368,14 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
     int count = 0, seen = ties;
 #pragma unroll 4
     for (int j0 = wlo; j0 < whi; j0 += 32) count += __popc(listed(j0 + lane, j0 + lane < whi ? key_at(j0 + lane) : 0u, seen));
-    __syncthreads();
-    if (lane == 0) warp_n[1][warp] = count;
-    __syncthreads();
-    const int warps_n = lane < kWarps ? warp_n[1][lane] : 0;
-    int at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warps_n : 0), all = __reduce_add_sync(0xFFFFFFFFu, warps_n);
+    int at = sums_before(count, 1, all);
     pdl_wait();                            // the prepare kernel's verdict, and its zero in p.total
     const bool stays = p.cut[b] == 0;
-    if (C > 1) {
-        if (tid == 0) total_s[1] = all;
-        cluster_sync();
-        const int x = lane < C ? cluster_ld(cluster_map(ptx::smem_u32(&total_s[1]), lane)) : 0;
-        at += __reduce_add_sync(0xFFFFFFFFu, lane < rank ? x : 0);
-        all = __reduce_add_sync(0xFFFFFFFFu, x);
-    }
     const int moves = stays ? 0 : all >> 1;
     if (rank == 0 && tid == 0) start_s = atomicAdd(p.total, moves);
     if (out != w && !stays) {
-        if (rank == 0) copy_weights(0, p.sinks);
-        copy_weights(lo, min(hi, end));
+        if (rank == 0) copy_weights(0, p.sinks, tid, T);
+        copy_weights(wlo, min(whi, end), lane, 32);
         for (int j = p.budget + rank * T + tid; j < n; j += C * T) out[j] = 0.0f;
     }
     if (C > 1) cluster_sync(); else __syncthreads();
@@ -394,6 +391,7 @@ __global__ void __launch_bounds__(T) attn_evict_select_kernel(const __grid_const
 #pragma unroll 4
             for (int r = 0; r < kListRows; ++r) {
                 const int j = j0 + 32 * r + lane;
+                if (j0 + 32 * r >= whi) break;
                 const unsigned bits = listed(j, j < whi ? key_at(j) : 0u, seen);
                 if ((bits >> lane) & 1) slot_s[m + __popc(bits & below)] = (uint16_t)(32 * r + lane);
                 m += __popc(bits);

@@ -42,8 +42,8 @@ struct RopeParams {
     int B;
 };
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;
+constexpr int kRopeThreads = 128;
+constexpr int kRopeHeads = 2;       // heads that a thread turns at a time, while the next ones are on their way
 constexpr int kCuStage = 1024;     // sequence offsets that a block searches in shared memory
 
 // bf16 pair (x0 in the low half) turned by (c, s)
@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t rotate_word(uint32_t w, float c, float s) {
 }
 
 template <int D, bool kHalves, bool kAppend>
-__global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kL = D / 16;     // threads of a token: 16 elements (two 16-byte chunks) of a head each
     __shared__ unsigned long long turn[D / 2];
     __shared__ int axis[D / 2];
@@ -81,24 +81,8 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_co
     if (token >= p.tokens) return;
     const long long b = kAppend ? 0 : token / p.S, s = kAppend ? token : token - b * p.S;
 
-    long long row = -1;            // the token's row of the cache
-    if constexpr (kAppend) {
-        const int* cu = staged ? cu_s : p.cu_new;
-        // the last sequence that starts at or before the token (a later one, empty, may start there too)
-        int lo = 0, hi = p.B;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= token) lo = mid; else hi = mid - 1;
-        }
-        if (lo >= p.B || cu[lo] > token) return;           // in front of the first sequence or behind the last
-        const int end = cu[lo + 1];
-        const long long len = __ldg(p.seqlens_k + lo), first = len - ((long long)end - cu[lo]);
-        const long long at = len - end + token;            // its slot in the sequence
-        if (first >= 0 && at >= 0 && at < (long long)p.pages.max_pages * p.pages.page_size)
-            row = page_row(p.pages, p.pages.table + (long long)lo * p.pages.max_pages, (int)at);
-        if (row < 0 && l == 0) report_invalid(ATTN_CACHE_SITE_APPEND);
-    }
-
+    const int h_begin = blockIdx.y * p.heads_per_thread;
+    const int h_end = min(h_begin + p.heads_per_thread, p.heads);
     // the two chunks of this thread, and the first pair of each
     int ca, cb, pa, pb;
     if constexpr (kHalves) {
@@ -113,6 +97,48 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_co
         pa = 4 * ca;
         pb = 4 * cb;
     }
+    // which tensor head h of the token belongs to, and its number there
+    auto tensor_of = [&](int& h) {
+        int t = 0;
+        if (h >= p.x[0].heads) { h -= p.x[0].heads; t = 1; }
+        if (kAppend && t == 1 && h >= p.x[1].heads) { h -= p.x[1].heads; t = 2; }
+        return t;
+    };
+    struct Heads { uint4 a[kRopeHeads], b[kRopeHeads]; };
+    auto load = [&](int h0, Heads& x) {
+#pragma unroll
+        for (int u = 0; u < kRopeHeads; ++u) {
+            int h = h0 + u;
+            if (h >= h_end) continue;
+            const RopeTensor& t = p.x[tensor_of(h)];
+            const char* src = t.src + b * t.src_b + s * t.src_t + h * t.src_h;
+            x.a[u] = *reinterpret_cast<const uint4*>(src + ca * 16);
+            x.b[u] = *reinterpret_cast<const uint4*>(src + cb * 16);
+        }
+    };
+
+    Heads x, next;
+    long long row = -1;            // the token's row of the cache
+    if constexpr (kAppend) {
+        const int* cu = staged ? cu_s : p.cu_new;
+        // the last sequence that starts at or before the token (a later one, empty, may start there too)
+        int lo = 0, hi = p.B;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (cu[mid] <= token) lo = mid; else hi = mid - 1;
+        }
+        if (lo >= p.B || cu[lo] > token) return;           // in front of the first sequence or behind the last
+        load(h_begin, x);
+        const int end = cu[lo + 1];
+        const long long len = __ldg(p.seqlens_k + lo), first = len - ((long long)end - cu[lo]);
+        const long long at = len - end + token;            // its slot in the sequence
+        if (first >= 0 && at >= 0 && at < (long long)p.pages.max_pages * p.pages.page_size)
+            row = page_row(p.pages, p.pages.table + (long long)lo * p.pages.max_pages, (int)at);
+        if (row < 0 && l == 0) report_invalid(ATTN_CACHE_SITE_APPEND);
+    } else {
+        load(h_begin, x);
+    }
+
     float c[8], sn[8];
     bool turned[8];
 #pragma unroll
@@ -128,33 +154,16 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_co
             if (p.inverse) sn[e] = -sn[e];
         }
     }
-    const int h_begin = blockIdx.y * p.heads_per_thread;
-    const int h_end = min(h_begin + p.heads_per_thread, p.heads);
-    for (int h0 = h_begin; h0 < h_end; h0 += kRopeUnroll) {
-        uint4 xa[kRopeUnroll], xb[kRopeUnroll];
-        char* dst[kRopeUnroll];
-        bool copy[kRopeUnroll];
+    for (int h0 = h_begin; h0 < h_end; h0 += kRopeHeads) {
+        load(h0 + kRopeHeads, next);
 #pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            int h = h0 + u, t = 0;
-            dst[u] = nullptr;
-            copy[u] = false;
+        for (int u = 0; u < kRopeHeads; ++u) {
+            int h = h0 + u;
             if (h >= h_end) continue;
-            if (h >= p.x[0].heads) { h -= p.x[0].heads; t = 1; }
-            if (kAppend && t == 1 && h >= p.x[1].heads) { h -= p.x[1].heads; t = 2; }
-            const RopeTensor& x = p.x[t];
+            const int t = tensor_of(h);
             if (kAppend && t > 0 && row < 0) continue;
-            const char* src = x.src + b * x.src_b + s * x.src_t + h * x.src_h;
-            dst[u] = x.dst + b * x.dst_b + (kAppend && t > 0 ? row : s) * x.dst_t + h * x.dst_h;
-            copy[u] = t == 2;
-            xa[u] = *reinterpret_cast<const uint4*>(src + ca * 16);
-            xb[u] = *reinterpret_cast<const uint4*>(src + cb * 16);
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            if (!dst[u]) continue;
-            if (!kAppend || !copy[u]) {
-                uint32_t wa[4] = {xa[u].x, xa[u].y, xa[u].z, xa[u].w}, wb[4] = {xb[u].x, xb[u].y, xb[u].z, xb[u].w};
+            if (!kAppend || t < 2) {
+                uint32_t wa[4] = {x.a[u].x, x.a[u].y, x.a[u].z, x.a[u].w}, wb[4] = {x.b[u].x, x.b[u].y, x.b[u].z, x.b[u].w};
                 if constexpr (kHalves) {
                     if (turned[0]) {
 #pragma unroll
@@ -175,12 +184,15 @@ __global__ void __launch_bounds__(kRopeThreads) attn_rope_kernel(const __grid_co
                         if (turned[4 + i]) wb[i] = rotate_word(wb[i], c[4 + i], sn[4 + i]);
                     }
                 }
-                xa[u] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-                xb[u] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                x.a[u] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                x.b[u] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
             }
-            *reinterpret_cast<uint4*>(dst[u] + ca * 16) = xa[u];
-            *reinterpret_cast<uint4*>(dst[u] + cb * 16) = xb[u];
+            const RopeTensor& to = p.x[t];
+            char* dst = to.dst + b * to.dst_b + (kAppend && t > 0 ? row : s) * to.dst_t + h * to.dst_h;
+            *reinterpret_cast<uint4*>(dst + ca * 16) = x.a[u];
+            *reinterpret_cast<uint4*>(dst + cb * 16) = x.b[u];
         }
+        x = next;
     }
 }
 

@@ -656,6 +656,8 @@ def _on(index, stream):
     import torch
     if stream is not None:
         s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=index)
+        if s.device_index != index:
+            raise ValueError("the stream must be on the tensors' device")
         return torch.cuda.stream(s)
     return None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
@@ -792,9 +794,9 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
         on.__enter__()
     try:
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if k is not None and k_out is None:
-            k_out = k.new_empty(k.shape)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         if S > 0:
             kp, ko, kos = (0, 0, ks) if k is None else (k.data_ptr(), k_out.data_ptr(), geometry(k_out)[1])
             a = _pack_rope(q.data_ptr(), q_out.data_ptr(), kp, ko, positions.data_ptr(), freqs.data_ptr(),
@@ -841,8 +843,8 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
     ``seqlens_k``: int32 [B] lengths WITH the new tokens, as :func:`attn_fwd_paged` and
     :func:`attn_paged_decode` then take them; ``block_table``: int32 [B, max_pages].  Tokens whose slot or
     page the cache does not have are not written and are reported by :func:`cache_device_status`.
-    Returns ``q_out`` (dense [total, H, d]; rows outside every sequence are left as they were, zero where
-    it is allocated here), or None without ``q``."""
+    Returns ``q_out`` (dense [total, H, d]; rows outside every sequence are not written), or None without
+    ``q``."""
     import torch
     dev, pages, ps, Hkv, d, B, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
     _check_heads(dev, 3, (k, "k"), (v, "v")) if q is None else _check_heads(dev, 3, (k, "k"), (v, "v"), (q, "q"))
@@ -881,7 +883,7 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
         on.__enter__()
     try:
         if q is not None and q_out is None:
-            q_out = torch.zeros((total, H, d), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         if total > 0:
             a = _pack_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                              0 if q is None else q.data_ptr(), 0 if q is None else q_out.data_ptr(),

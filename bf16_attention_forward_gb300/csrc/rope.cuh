@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
         const int end = cu[lo + 1];
         const long long len = __ldg(p.seqlens_k + lo), first = len - ((long long)end - cu[lo]);
         const long long at = len - end + token;            // its slot in the sequence
-        if (first >= 0 && at >= 0 && at < (long long)p.pages.max_pages * p.pages.page_size)
+        if (first >= 0 && at >= 0 && at < len && len <= (long long)p.pages.max_pages * p.pages.page_size)
             row = page_row(p.pages, p.pages.table + (long long)lo * p.pages.max_pages, (int)at);
         if (row < 0 && l == 0) report_invalid(ATTN_CACHE_SITE_APPEND);
     } else {

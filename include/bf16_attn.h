@@ -452,7 +452,8 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
  * sequence b is slot j % page_size of page block_table[b * max_pages + j / page_size], as in
  * attn_fwd_paged (which itself wants a page_size that is a multiple of 128).  All calls run on
  * `stream`, allocate nothing and keep nothing between calls; a workspace is the caller's, and calls
- * that may run at the same time need workspaces of their own.  Argument errors are returned as by
+ * that may run at the same time need workspaces of their own.  Calls may be captured into CUDA graphs
+ * (lengths, offsets and tables are read when the graph runs).  Argument errors are returned as by
  * attn_fwd; what only the device can see (lengths, page indices, axes) is reported through
  * attn_cache_get_device_status() as ATTN_ERR_INVALID_ARG at the site given below.
  */
@@ -574,8 +575,9 @@ int attn_paged_decode(const attn_decode_args_t* args, void* workspace, size_t wo
  * they are, the i-th survivor past it moves into the i-th freed slot, and the recent keys follow in order
  * up to slot budget - 1: attention does not depend on the order of keys, and the recent window stays
  * last for the tokens to come.  Shorter sequences stay as they are.
- *   k_cache, v_cache   rewritten in place.  A page that a rewritten sequence uses must be used once in
- *                      the whole table (checked: such a sequence is left as it was and reported)
+ *   k_cache, v_cache   rewritten in place.  A page that a rewritten sequence uses must be used once among all
+ *                      sequences' used table entries (checked: else the sequence is left as it was, its
+ *                      weights_out too, and reported)
  *   weights            fp32 [B][Hkv][max_pages * page_size], as attn_paged_decode accumulates them
  *   weights_out        the weights of the slots after the call, freed slots up to the old length zero; may be
  *                      `weights` itself, else overlaps nothing.  Entries past the old length are not written

@@ -102,6 +102,7 @@ CASES = [  # lens, H, Hkv, d, page size, mode
     ([90, 260], 80, 2, 128, 256, "rtz"),
     ([3000], 8, 8, 128, 256, "rtne"),
     ([37] * 80, 6, 3, 64, 16, "rtne"),
+    ([3, 0, 130, 1] * 500, 2, 2, 64, 8, "rtne"),     # more sequences than a block's threads
 ]
 
 

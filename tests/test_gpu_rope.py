@@ -247,6 +247,22 @@ def test_append_slots_that_are_not_in_the_cache(attn):
     status_ok(attn)
 
 
+def test_offsets_that_decrease_write_inside_the_lengths_only(attn):
+    P, Hkv, d = 4, 1, 64
+    kc, vc = filled(4, P, Hkv, d), filled(4, P, Hkv, d)
+    k, v = draw(6, Hkv, d, seed=1), draw(6, Hkv, d, seed=2)
+    cu = torch.tensor([0, 3, 1, 6], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([3, 2, 5], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, 3], [1, 3], [2, 3]], dtype=torch.int32, device="cuda")
+    attn.attn_paged_append(k, v, kc, vc, cu, lens, table)
+    attn.cache_device_status()
+    untouched = filled(1, Hkv, d)[0].view(torch.int16)
+    for b, n in enumerate(lens.tolist()):
+        for j in range(n, P):
+            assert torch.equal(kc[b, j].view(torch.int16), untouched), (b, j)
+    status_ok(attn)
+
+
 def test_captured_and_replayed_on_another_stream(attn):
     freqs, axes = attn.rope_freqs((128,))
     q, k = draw(1, 50, 4, 128, seed=1), draw(1, 50, 2, 128, seed=2)

@@ -764,24 +764,18 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     _check_heads(dev, dim, (q, "q")) if k is None else _check_heads(dev, dim, (q, "q"), (k, "k"))
     per_batch = dim == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 3
     pairs = _rope_tables(positions, freqs, axes, pairing, dev, 3 if per_batch else 2)
-    swap = dim == 4 and layout == "bhsd"
-
-    def geometry(t):
-        """(B, S, heads, d) and the (batch, token, head) strides."""
-        n, st = t.shape, t.stride()
-        if dim == 3:
-            return (1, n[0], n[1], n[2]), (0, st[0], st[1])
-        if swap:
-            return (n[0], n[2], n[1], n[3]), (st[0], st[2], st[1])
-        return tuple(n), st[:3]
-
-    (B, S, H, d), qs = geometry(q)
-    Hkv, ks = 0, (0, 0, 0)
+    bhsd = dim == 4 and layout == "bhsd"
+    # (batch,) token and head dimensions
+    t_dim, h_dim = (0, 1) if dim == 3 else (2, 1) if bhsd else (1, 2)
+    qn, qs = q.shape, q.stride()
+    B, S, H, d = 1 if dim == 3 else qn[0], qn[t_dim], qn[h_dim], qn[-1]
+    Hkv, ks = 0, qs
     if k is not None:
-        (Bk, Sk, Hkv, dk), ks = geometry(k)
-        if Bk != B or Sk != S or dk != d:
+        kn, ks = k.shape, k.stride()
+        Hkv = kn[h_dim]
+        if kn[t_dim] != S or kn[-1] != d or (dim == 4 and kn[0] != B):
             raise ValueError("q and k must agree in all but their heads")
-    pn, pst = positions.shape, positions.stride()
+    pn, ps = positions.shape, positions.stride()
     if pn[-1] != S or (per_batch and pn[1] != B):
         raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
     for o, t, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
@@ -793,15 +787,27 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     if on is not None:
         on.__enter__()
     try:
+        # strides (batch, token, head); an output allocated here is contiguous
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if k is not None and k_out is None:
+            qos = (S * H * d, d, S * d) if bhsd else (S * H * d, H * d, d)
+        else:
+            os = q_out.stride()
+            qos = (0 if dim == 3 else os[0], os[t_dim], os[h_dim])
+        if k is None:
+            kos = qos
+        elif k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            kos = (S * Hkv * d, d, S * d) if bhsd else (S * Hkv * d, Hkv * d, d)
+        else:
+            os = k_out.stride()
+            kos = (0 if dim == 3 else os[0], os[t_dim], os[h_dim])
         if S > 0:
-            kp, ko, kos = (0, 0, ks) if k is None else (k.data_ptr(), k_out.data_ptr(), geometry(k_out)[1])
-            a = _pack_rope(q.data_ptr(), q_out.data_ptr(), kp, ko, positions.data_ptr(), freqs.data_ptr(),
-                           axes.data_ptr(), B, S, H, Hkv, d, *qs, *geometry(q_out)[1], *ks, *kos, pst[0],
-                           pst[1] if per_batch else 0, pairs, pn[0], PAIRINGS[pairing], 1 if inverse else 0)
+            qb, kb = (0, 0) if dim == 3 else (qs[0], ks[0])
+            a = _pack_rope(q.data_ptr(), q_out.data_ptr(), 0 if k is None else k.data_ptr(),
+                           0 if k is None else k_out.data_ptr(), positions.data_ptr(), freqs.data_ptr(), axes.data_ptr(),
+                           B, S, H, Hkv, d, qb, qs[t_dim], qs[h_dim], *qos, kb, ks[t_dim], ks[h_dim], *kos, ps[0],
+                           ps[1] if per_batch else 0, pairs, pn[0], PAIRINGS[pairing], 1 if inverse else 0)
             st = (_lib or load()).attn_rope(a, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_rope")

@@ -2768,6 +2768,6 @@ const char* attn_status_string(int status) {
     }
 }
 
-int attn_version(void) { return 400; }
+int attn_version(void) { return 300; }
 
 }  // extern "C"

@@ -347,6 +347,7 @@ int head_tiles(int64_t group) { return group <= 8 ? 1 : group <= 16 ? 2 : 4; }
 struct DecodeLayout {
     size_t part_o, part_ml, split, row_ml, scores, bytes;
 };
+int64_t score_room(const attn_decode_args_t& a) { return cdiv(a.max_pages * a.page_size, 4) * 4; }
 DecodeLayout decode_layout(const attn_decode_args_t& a, int sms) {
     const int64_t heads = 8 * head_tiles(a.H / a.Hkv), blocks = cdiv(a.H / a.Hkv, heads);
     DecodeLayout l;
@@ -355,7 +356,7 @@ DecodeLayout decode_layout(const attn_decode_args_t& a, int sms) {
     l.split = l.part_ml + align256((size_t)(2 * sms * heads) * 8);
     l.row_ml = l.split + align256((size_t)sms * 16);
     l.scores = l.row_ml + (a.weights ? align256((size_t)(a.B * a.Hkv * blocks * heads) * 8) : 0);
-    l.bytes = l.scores + (a.weights ? (size_t)a.B * a.H * (size_t)(a.max_pages * a.page_size) * 4 : 0);
+    l.bytes = l.scores + (a.weights ? (size_t)(a.B * a.H) * (size_t)score_room(a) * 4 : 0);
     return l;
 }
 
@@ -442,6 +443,7 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     p.split = reinterpret_cast<int4*>(ws + l.split);
     p.row_ml = reinterpret_cast<float2*>(ws + l.row_ml);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
+    p.score_room = score_room(a);
     if (a.d == 128) return nh == 1 ? launch_decode<128, 1>(p, stream) : nh == 2 ? launch_decode<128, 2>(p, stream) : launch_decode<128, 4>(p, stream);
     return nh == 1 ? launch_decode<64, 1>(p, stream) : nh == 2 ? launch_decode<64, 2>(p, stream) : launch_decode<64, 4>(p, stream);
 }

@@ -46,7 +46,8 @@ struct DecodeParams {
     float2* part_ml;               // [2 * grid][heads of a block]: (m in logits, l); l = -1: a bad page
     int4* split;                   // [grid]: (b, row, first and last CTA) of a row whose second part is the CTA's, else b = -1
     float2* row_ml;                // [B][Hkv][head_blocks][heads of a block] of unsplit rows (weights only)
-    float* scores;                 // [B][H][max_pages * page_size] logits (weights only)
+    float* scores;                 // [B][H][score_room] logits (weights only)
+    long long score_room;          // max_pages * page_size rounded up to 16 bytes
 };
 
 constexpr int kDecWarps = 8;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int e = 0; e < 4; ++e) grow |= s[t][e] > m[t][e & 1] + tau;
             }
             if constexpr (kWeights) {
-                const long long room = (long long)p.pages.max_pages * p.pages.page_size;
+                const long long room = p.score_room;
                 float* to = p.scores + ((long long)b * p.H + kv_head * p.group + head0 + (lane & 3) * 2) * room + j0;
 #pragma unroll
                 for (int t = 0; t < NH; ++t)
@@ -528,6 +529,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
         const int t1 = (int)((long long)units * (block + 1) / blocks), t0 = (int)((long long)units * block / blocks);
         if (t0 >= t1) return;
         const long long room = (long long)p.pages.max_pages * p.pages.page_size;
+        const bool vector = room % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
         Cursor cur = seek(p, p.Hkv, t0);
         for (; cur.u < t1; next_row(p, p.Hkv, cur)) {
             const int n = min(cur.tiles - cur.tile, t1 - cur.u);
@@ -572,30 +574,41 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                 }
                 __syncthreads();
                 if (bad_s) break;
-                constexpr int kJ = 2;                  // keys of a thread in flight
-                for (int j0 = cur.tile * kDecTile + threadIdx.x; j0 < j1; j0 += 256 * kJ) {
-                    const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * room + j0;
-                    float x[kJ][kG], w[kJ];
+                // four neighbouring keys a thread: 16-byte loads (4-byte ones left the loop at 2.5 TB/s)
+                for (int j0 = cur.tile * kDecTile + threadIdx.x * 4; j0 < j1; j0 += 1024) {
+                    const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * p.score_room + j0;
+                    float4 x[kG], w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < kJ; ++i) {
-                        if (j0 + 256 * i >= j1) continue;
-                        w[i] = out[j0 + 256 * i];
-#pragma unroll
-                        for (int g = 0; g < kG; ++g)
-                            if (g0 + g < p.group) x[i][g] = s[g * room + 256 * i];
+                    for (int g = 0; g < kG; ++g)
+                        if (g0 + g < p.group) x[g] = *reinterpret_cast<const float4*>(s + g * p.score_room);
+                    if (vector) {
+                        w = *reinterpret_cast<const float4*>(out + j0);
+                    } else {
+                        w.x = out[j0];
+                        if (j0 + 1 < j1) w.y = out[j0 + 1];
+                        if (j0 + 2 < j1) w.z = out[j0 + 2];
+                        if (j0 + 3 < j1) w.w = out[j0 + 3];
                     }
+                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < kJ; ++i) {
-                        if (j0 + 256 * i >= j1) continue;
-                        float sum = 0.0f;
-#pragma unroll
-                        for (int g = 0; g < kG; ++g) {
-                            if (g0 + g >= p.group) continue;
-                            // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
-                            const float e = x[i][g] == -INFINITY ? 0.0f : exp2f((x[i][g] - ml_s[g].x) * p.scale_log2);
-                            sum += e * ml_s[g].y;
-                        }
-                        out[j0 + 256 * i] = w[i] + sum;
+                    for (int g = 0; g < kG; ++g) {
+                        if (g0 + g >= p.group) continue;
+                        const float2 ml = ml_s[g];
+                        // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
+                        auto weight = [&](float v) { return (v == -INFINITY ? 0.0f : exp2f((v - ml.x) * p.scale_log2)) * ml.y; };
+                        sum.x += weight(x[g].x);
+                        sum.y += weight(x[g].y);
+                        sum.z += weight(x[g].z);
+                        sum.w += weight(x[g].w);
+                    }
+                    w.x += sum.x; w.y += sum.y; w.z += sum.z; w.w += sum.w;
+                    if (vector && j0 + 3 < j1) {
+                        *reinterpret_cast<float4*>(out + j0) = w;
+                    } else {
+                        out[j0] = w.x;
+                        if (j0 + 1 < j1) out[j0 + 1] = w.y;
+                        if (j0 + 2 < j1) out[j0 + 2] = w.z;
+                        if (j0 + 3 < j1) out[j0 + 3] = w.w;
                     }
                 }
             }

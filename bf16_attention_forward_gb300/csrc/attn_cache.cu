@@ -37,6 +37,10 @@ cudaError_t set_decode_attr() {
     return e;
 }
 
+cudaError_t set_select_attr(void (*kernel)(EvictParams)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStaged * 4);
+}
+
 int device(int* sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return ATTN_ERR_NO_DEVICE; }
@@ -54,10 +58,10 @@ int device(int* sms) {
             (set_decode_attr<128, 1>() != cudaSuccess || set_decode_attr<128, 2>() != cudaSuccess ||
              set_decode_attr<128, 4>() != cudaSuccess || set_decode_attr<64, 1>() != cudaSuccess ||
              set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess ||
-             cudaFuncSetAttribute(attn_evict_select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  kMostStaged * 4) != cudaSuccess ||
-             cudaFuncSetAttribute(attn_evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  kMostStaged * 4) != cudaSuccess)) {
+             set_select_attr(attn_evict_select_kernel<512, false>) != cudaSuccess ||
+             set_select_attr(attn_evict_select_kernel<512, true>) != cudaSuccess ||
+             set_select_attr(attn_evict_select_kernel<1024, false>) != cudaSuccess ||
+             set_select_attr(attn_evict_select_kernel<1024, true>) != cudaSuccess)) {
             cudaGetLastError();
             return ATTN_ERR_CUDA;
         }
@@ -541,8 +545,16 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     while (2 * rows * p.pieces < 3 * sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
     if ((st = launch_clusters(attn_evict_prep_kernel, kPrepCtas, kPrepCtas, kPrepThreads, 0, stream, p)) != ATTN_OK) return st;
     // threads: two keys each at least, 512 or 1024
-    st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024>, rows * p.cluster, p.cluster, 1024, (size_t)p.staged * 4, stream, p)
-                         : launch_clusters(attn_evict_select_kernel<512>, rows * p.cluster, p.cluster, 512, (size_t)p.staged * 4, stream, p);
+    const size_t smem = (size_t)p.staged * 4;
+    const int64_t ctas = rows * p.cluster;
+    if (p.cluster == 1 && l.most_moves <= kMostWhole && a.recent <= kMostWhole) {
+        st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024, true>, ctas, 1, 1024, smem, stream, p)
+                             : launch_clusters(attn_evict_select_kernel<512, true>, ctas, 1, 512, smem, stream, p);
+        if (st != ATTN_OK || p.seqlens_out != p.seqlens_k) return st;
+        return launch(attn_evict_lens_kernel, 1, 1, 256, 0, stream, p);
+    }
+    st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024, false>, ctas, p.cluster, 1024, smem, stream, p)
+                         : launch_clusters(attn_evict_select_kernel<512, false>, ctas, p.cluster, 512, smem, stream, p);
     if (st != ATTN_OK) return st;
     if (l.most_moves > 0) {
         st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, stream, p)

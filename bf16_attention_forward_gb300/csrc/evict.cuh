@@ -18,6 +18,8 @@
 // late survivors.
 // Fill kernel: the rows that move into freed slots.  Their sources and targets are disjoint, so all
 // sequences' moves lie on one list (in no fixed order) that the warps share evenly.
+// Where few rows can move (kMostWhole), each select CTA moves its own, and the two kernels below are not launched
+// (32 caches a few keys over 1024: 19.5 -> 14.9 us).
 // Shift kernel: the recent block, and the weights.  Its rows may overlap their targets, so one CTA
 // moves a (tensor, sequence, head) in ascending order, each step's reads before its writes; columns are
 // independent, and a few long caches split their rows into column pieces for more CTAs.
@@ -56,6 +58,7 @@ constexpr int kPrepCtas = 8;
 constexpr int kMostCluster = 8;        // (16 took 25 us longer to start, for 1 us less in the select kernel)
 constexpr int kBins = 2048;
 constexpr int kMostGathered = 2 * kBins;   // keys of the threshold's bin that are searched in registers
+constexpr int kMostWhole = 256;        // most moves, and most recent keys, that the select kernel does itself
 constexpr int kMostRanked = 128;       // ... and up to which each key's rank says it (0.6 us less than the two passes)
 constexpr int kListRows = 8;           // rows of 32 slots that a warp lists at a time
 constexpr int kMostStaged = 16384;     // 64 KB: three CTAs an SM
@@ -137,8 +140,53 @@ __global__ void __launch_bounds__(kPrepThreads, 1) attn_evict_prep_kernel(const 
     }
 }
 
+// The recent block of a head's rows, 16 bytes a thread: `base` is the thread's place in a row, r its row of `rows` that
+// a step moves. Each step's reads come before its writes, and its targets lie below every later step's sources.
+__device__ __forceinline__ void shift_rows(const EvictParams& p, const int32_t* table, char* base, int n, int r, int rows) {
+    constexpr int kU = 8;                              // rows in flight
+    const long long stride = (long long)p.Hkv * p.row_bytes;
+    const int end = p.budget - p.recent;
+    for (int i0 = 0; i0 < p.recent; i0 += rows * kU) {
+        uint4 x[kU];
+        int to[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = i0 + u * rows + r;
+            to[u] = -1;
+            if (i < p.recent) {
+                x[u] = *reinterpret_cast<const uint4*>(base + page_row(p.pages, table, n - p.recent + i) * stride);
+                to[u] = page_row(p.pages, table, end + i);
+            }
+        }
+        if (n - p.budget < p.recent) __syncthreads();  // (else sources and targets do not overlap)
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u] * stride) = x[u];
+    }
+}
+
+// The recent block of a head's weights, and zeros behind the budget (if the new weights take the place of the old).
+__device__ __forceinline__ void shift_weights(const EvictParams& p, const float* w, float* out, int n, int tid, int threads) {
+    constexpr int kU = 8;
+    const int end = p.budget - p.recent;
+    for (int i0 = 0; i0 < p.recent; i0 += kU * threads) {
+        float x[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (i0 + u * threads + tid < p.recent) x[u] = w[n - p.recent + i0 + u * threads + tid];
+        __syncthreads();                               // (as above)
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (i0 + u * threads + tid < p.recent) out[end + i0 + u * threads + tid] = x[u];
+    }
+    __syncthreads();
+    if (out == w)
+        for (int j = p.budget + tid; j < n; j += threads) out[j] = 0.0f;
+}
+
 // It starts while the prepare kernel runs, and waits for that before it touches what it writes.
-template <int T>
+// kWhole: the CTA (a cluster of one) moves its own rows too, in place of the fill and shift kernels.
+template <int T, bool kWhole>
 __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kWarps = T / 32, kU = 16;            // kU: loads in flight
     constexpr int kEach = kMostGathered / T;
@@ -179,6 +227,7 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
     if (!valid_len(p, n) || n <= p.budget) {           // (the whole cluster)
         pdl_wait();                                    // the kernels behind this one rely on the one before it too
         if (out != w && rank == 0 && valid_len(p, n)) copy_weights(0, n, tid, T);
+        if (kWhole && h == 0 && tid == 0 && p.seqlens_out != p.seqlens_k) p.seqlens_out[b] = p.lens[b];
         return;
     }
     const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
@@ -372,16 +421,17 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
     pdl_wait();                            // the prepare kernel's verdict, and its zero in p.total
     const bool stays = p.cut[b] == 0;
     const int moves = stays ? 0 : all >> 1;
-    if (rank == 0 && tid == 0) start_s = atomicAdd(p.total, moves);
+    if (!kWhole && rank == 0 && tid == 0) start_s = atomicAdd(p.total, moves);
     if (out != w && !stays) {
         if (rank == 0) copy_weights(0, p.sinks, tid, T);
         copy_weights(wlo, min(whi, end), lane, 32);
         for (int j = p.budget + rank * T + tid; j < n; j += C * T) out[j] = 0.0f;
     }
     if (C > 1) cluster_sync(); else __syncthreads();
-    const int start = C > 1 ? cluster_ld(cluster_map(ptx::smem_u32(&start_s), 0)) : start_s;
+    const int start = kWhole ? 0 : C > 1 ? cluster_ld(cluster_map(ptx::smem_u32(&start_s), 0)) : start_s;
     int2* fill = p.fill + start;
     uint2* fill_w = p.fill_w + start;
+    int* const list = pool[2];                         // kWhole: freed slots, then the survivors that fill them
     const uint32_t w0 = (uint32_t)(bh * room);
     seen = ties;
     if (moves > 0)
@@ -397,6 +447,12 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
                 m += __popc(bits);
             }
             __syncwarp();
+            if constexpr (kWhole) {
+                for (int e = lane; e < m; e += 32) list[at + e] = j0 + slot_s[e];
+                at += m;
+                __syncwarp();
+                continue;
+            }
             constexpr int kE = 4;              // page lookups in flight
             for (int e0 = lane; e0 < m; e0 += 32 * kE) {
                 int j[kE], row[kE];
@@ -424,6 +480,30 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
             __syncwarp();
         }
     if (C > 1) cluster_sync();             // no CTA leaves while its shared memory may be read
+    if constexpr (kWhole) {
+        // (lengths in place are the next kernel's: another head's CTA may not have read them yet)
+        if (h == 0 && tid == 0 && p.seqlens_out != p.seqlens_k) p.seqlens_out[b] = p.lens[b];
+        if (stays) return;
+        __syncthreads();                   // the list is complete
+        const int lanes = p.row_bytes / 16, rows = T / (2 * lanes), r = tid / (2 * lanes), c = tid % (2 * lanes);
+        char* base = (c < lanes ? p.k : p.v) + (long long)h * p.row_bytes + (c % lanes) * 16;
+        const long long stride = (long long)p.Hkv * p.row_bytes;
+        for (int i = tid; i < moves; i += T) out[list[i]] = w[list[moves + i]];
+        for (int i0 = r; i0 < moves; i0 += 4 * rows) {
+            uint4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * rows < moves)
+                    x[u] = *reinterpret_cast<const uint4*>(base + page_row(p.pages, table, list[moves + i0 + u * rows]) * stride);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * rows < moves)
+                    *reinterpret_cast<uint4*>(base + page_row(p.pages, table, list[i0 + u * rows]) * stride) = x[u];
+        }
+        __syncthreads();                   // the late survivors are out before the recent block covers their slots
+        shift_rows(p, table, base, n, r, rows);
+        shift_weights(p, w, out, n, tid, T);
+    }
 }
 
 // K and V rows and weights into freed slots: 16 bytes a lane, a warp takes 512 bytes of rows at a time, 8 of them in flight.
@@ -460,10 +540,15 @@ __global__ void __launch_bounds__(kFillThreads, 4) attn_evict_fill_kernel(const 
     }
 }
 
+__global__ void __launch_bounds__(256) attn_evict_lens_kernel(const __grid_constant__ EvictParams p) {
+    pdl_wait();
+    pdl_launch();
+    for (int b = threadIdx.x; b < p.B; b += 256) p.seqlens_out[b] = p.lens[b];
+}
+
 // The recent block and the weights.  One CTA per (sequence, K/V head) and task: a column piece of K or V, or the
 // weights.
 __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const __grid_constant__ EvictParams p) {
-    constexpr int kU = 8;                              // loads in flight
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_launch();
@@ -476,25 +561,11 @@ __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const _
     if (task == tasks - 1 && h == 0 && tid == 0) p.seqlens_out[b] = p.lens[b];
     if (cut == 0) return;
     const bool over = cut > 0;
-    const int n = over ? cut : -1 - cut, end = p.budget - p.recent, shift = n - p.budget;
+    const int n = cut;
 
     if (task == tasks - 1) {
         if (!over) return;
-        const float* w = p.weights + bh * room;
-        float* out = p.weights_out + bh * room;
-        for (int i0 = 0; i0 < p.recent; i0 += kU * kShiftThreads) {
-            float x[kU];
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (i0 + u * kShiftThreads + tid < p.recent) x[u] = w[n - p.recent + i0 + u * kShiftThreads + tid];
-            __syncthreads();           // (a slot is read before it is written: targets lie below the sources left)
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (i0 + u * kShiftThreads + tid < p.recent) out[end + i0 + u * kShiftThreads + tid] = x[u];
-        }
-        __syncthreads();
-        if (out == w)
-            for (int j = p.budget + tid; j < n; j += kShiftThreads) out[j] = 0.0f;
+        shift_weights(p, p.weights + bh * room, p.weights_out + bh * room, n, tid, kShiftThreads);
         return;
     }
     if (!over) return;
@@ -503,26 +574,7 @@ __global__ void __launch_bounds__(kShiftThreads) attn_evict_shift_kernel(const _
     const int lanes = bytes / 16, rows = kShiftThreads / lanes;
     const int32_t* table = p.pages.table + (long long)b * p.pages.max_pages;
     char* base = (task < p.pieces ? p.k : p.v) + (long long)h * p.row_bytes + piece * bytes + (tid % lanes) * 16;
-    const long long stride = (long long)p.Hkv * p.row_bytes;
-    const int r = tid / lanes;
-    for (int i0 = 0; i0 < p.recent; i0 += rows * kU) {
-        uint4 x[kU];
-        int to[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = i0 + u * rows + r;
-            to[u] = -1;
-            if (i < p.recent) {
-                x[u] = *reinterpret_cast<const uint4*>(base + page_row(p.pages, table, n - p.recent + i) * stride);
-                to[u] = page_row(p.pages, table, end + i);
-            }
-        }
-        // this step's reads before its writes; its targets lie below every later step's sources
-        if (shift < p.recent) __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (to[u] >= 0) *reinterpret_cast<uint4*>(base + to[u] * stride) = x[u];
-    }
+    shift_rows(p, table, base, n, tid / lanes, rows);
 }
 
 }  // namespace cache

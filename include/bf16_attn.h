@@ -4,7 +4,9 @@
  * Operation.  O = softmax(Q K^T / sqrt(d)) V, non-causal, head dimension d = 128 (64 is
  * accepted too), bf16 in and out, fp32 accumulation.  Extensions below: the causal mask,
  * grouped K/V heads and the row log-sum-exp (attn_fwd_ex), variable-length batches
- * (attn_fwd_varlen), a paged K/V cache (attn_fwd_paged) and the backward (attn_bwd).  Source: "MoonMath AI open-sources a HIP attention kernel for
+ * (attn_fwd_varlen), a paged K/V cache (attn_fwd_paged), the backward (attn_bwd), and what surrounds a
+ * paged cache: rotary positions (attn_rope), appending (attn_paged_append), one-token decoding
+ * (attn_paged_decode) and eviction (attn_paged_evict).  Source: "MoonMath AI open-sources a HIP attention kernel for
  * AMD MI300X that beats AITER" (news.chathome.org), opening section: attention is the fused
  * softmax(QK^T/sqrt(d))V; the kernel takes BSHD or BHSD tensors without transposes, head
  * dimension fixed at 128, any query and key length including cross-attention; its

@@ -911,7 +911,7 @@ def _workspace_bytes(name, index, *shape):
     a = (DecodeArgs if name == "attn_paged_decode" else EvictArgs)()
     for n, x in shape:
         setattr(a, n, x)
-    return max(int(getattr(load(), name + "_workspace_size")(ctypes.byref(a))), 16)
+    return int(getattr(load(), name + "_workspace_size")(ctypes.byref(a)))
 
 
 def _check_workspace(workspace, index):
@@ -973,8 +973,9 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
             ws_bytes = _workspace_bytes("attn_paged_decode", dev, ("B", B), ("H", H), ("Hkv", Hkv), ("num_pages", pages),
                                         ("page_size", ps), ("max_pages", most), ("d", d),
                                         ("weights", 0 if weights is None else 16))
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        st = (_lib or load()).attn_paged_decode(a, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+            if ws_bytes:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        st = (_lib or load()).attn_paged_decode(a, workspace.data_ptr() if ws_bytes else None, ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise AttnError(st, "attn_paged_decode")
     finally:

@@ -348,6 +348,17 @@ int run_append(const attn_append_args_t& a, cudaStream_t stream) {
 // powers of two (the instances); larger groups read the keys once per 32 heads
 int head_tiles(int64_t group) { return group <= 8 ? 1 : group <= 16 ? 2 : 4; }
 
+// Few short rows go to a CTA each: one launch, no parts to join.  A tile costs such a CTA 0.5 to 0.9 us, and
+// the split path 3 us more to begin with, so rows of up to 5 tiles are not split; where the rows nearly fill
+// the SMs a split gains little, and up to 10 tiles are not.  By the table's room (lengths are on the device).
+// us a call in a graph, d = 128, split / whole:  8 rows of 2 tiles 7.0 / 4.8, 5 tiles 7.0 / 7.1, 8 tiles 7.2 / 9.4;
+// 16 x 8 rows of 2 tiles 7.8 / 5.2, 5 tiles 11.8 / 8.0, 8 tiles 14.5 / 10.8.
+bool decode_whole(const attn_decode_args_t& a, int sms) {
+    const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
+    const int64_t tiles = cdiv(a.max_pages * a.page_size, kDecTile);
+    return !a.weights && rows <= sms && (tiles <= 5 || (tiles <= 10 && tiles * (sms - rows) <= 5 * sms));
+}
+
 struct DecodeLayout {
     size_t part_o, part_ml, split, row_ml, scores, bytes;
 };
@@ -360,7 +371,7 @@ DecodeLayout decode_layout(const attn_decode_args_t& a, int sms) {
     l.split = l.part_ml + align256((size_t)(2 * sms * heads) * 8);
     l.row_ml = l.split + align256((size_t)sms * 16);
     l.scores = l.row_ml + (a.weights ? align256((size_t)(a.B * a.Hkv * blocks * heads) * 8) : 0);
-    l.bytes = l.scores + (a.weights ? (size_t)(a.B * a.H) * (size_t)score_room(a) * 4 : 0);
+    l.bytes = decode_whole(a, sms) ? 0 : l.scores + (a.weights ? (size_t)(a.B * a.H) * (size_t)score_room(a) * 4 : 0);
     return l;
 }
 
@@ -385,7 +396,8 @@ int launch_decode(const DecodeParams& p, cudaStream_t stream) {
         if ((st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
         return launch(attn_decode_join_kernel<D, NH, true>, 4 * p.grid, 1, 256, 0, stream, p);
     }
-    if ((st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
+    st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
+    if (st != ATTN_OK || p.whole) return st;
     return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);
 }
 
@@ -407,8 +419,8 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
         if (pass == 1) {       // the workspace, once its size is known
             if ((st = device(&sms)) != ATTN_OK) return st;
             const DecodeLayout l = decode_layout(a, sms);
-            if (!workspace || workspace_bytes < l.bytes) return ATTN_ERR_WORKSPACE;
-            if ((uintptr_t)workspace & 15u) return ATTN_ERR_MISALIGNED;
+            if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return ATTN_ERR_WORKSPACE;
+            if (l.bytes && (uintptr_t)workspace & 15u) return ATTN_ERR_MISALIGNED;
             out[3].at = (uintptr_t)workspace;
             out[3].bytes = l.bytes;
         }
@@ -439,7 +451,8 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     const int nh = head_tiles(p.group);
     p.head_blocks = (int)cdiv(p.group, 8 * nh);
     p.round_mode = a.round_mode;
-    p.grid = sms;
+    p.whole = decode_whole(a, sms);
+    p.grid = p.whole ? p.B * p.Hkv * p.head_blocks : sms;
     p.scale = (float)(1.0 / std::sqrt((double)a.d));
     p.scale_log2 = (float)((1.0 / std::sqrt((double)a.d)) * 1.4426950408889634);
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);

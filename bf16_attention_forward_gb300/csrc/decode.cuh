@@ -22,7 +22,8 @@
 // the join has read them (24 caches of 250,000 keys: 178 -> 171 us), and of caches near the L2's size a part stays for
 // the next step (4 caches, 181 MB: 35.5 -> 33.8 us).
 // A range holds at most one part that begins before it and one that ends behind it, so two part
-// slots per CTA suffice; attn_decode_join_kernel merges a split row's parts, and beside that adds the
+// slots per CTA suffice.  A few short rows go to a CTA each instead: one launch, no parts.
+// attn_decode_join_kernel merges a split row's parts, and beside that adds the
 // weights from the logits that the attention kernel kept.
 #pragma once
 #include "cache_common.cuh"
@@ -42,6 +43,7 @@ struct DecodeParams {
     int head_blocks;               // blocks of 8 * NH query heads that a K/V head's group takes
     int round_mode;
     int grid;                      // CTAs of the attention kernel (the join kernel derives the parts)
+    int whole;                     // 1: a CTA per row, nothing is split, no workspace, no join
     float scale_log2;              // log2(e) / sqrt(d)
     float scale;
     // workspace
@@ -151,6 +153,18 @@ __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor
     }
 }
 
+// The rows of a sequence without keys, and the report of a bad length; by the threads of a block.
+__device__ __forceinline__ void keyless(const DecodeParams& p, int b, int n, int d) {
+    if (n < 0 || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
+        if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
+    } else if (n == 0) {
+        for (long long i = threadIdx.x; i < (long long)p.H * d; i += blockDim.x)
+            p.o[(long long)b * p.H * d + i] = __ushort_as_bfloat16((unsigned short)0x7FC0u);
+        if (p.lse)
+            for (int h = threadIdx.x; h < p.H; h += blockDim.x) p.lse[(long long)b * p.H + h] = -INFINITY;
+    }
+}
+
 // softmax weight of logit s against the reference m, in base 2: exactly 1 for the logit that set m, a
 // positive normal number for every other finite one, 0 for -inf, NaN for NaN
 __device__ __forceinline__ float weight_of(float s, float m, float c) {
@@ -178,14 +192,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     pdl_wait();
     pdl_launch();
     const int rows = p.Hkv * p.head_blocks;
-    const Line line = make_line(p, rows);
-    if ((int)blockIdx.x >= line.ctas) {
-        if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        return;
+    Line line;
+    Cursor cur;
+    int u0 = 0, u1;
+    if (p.whole) {
+        cur = Cursor{0, (int)blockIdx.x / rows, (int)blockIdx.x % rows, 0, 0, 0};
+        cur.len = __ldg(p.seqlens_k + cur.b);
+        u1 = cur.tiles = seq_tiles(p, cur.len);
+        if (cur.row == 0) keyless(p, cur.b, cur.len, D);
+        if (u1 == 0) return;
+    } else {
+        line = make_line(p, rows);
+        if ((int)blockIdx.x >= line.ctas) {
+            if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            return;
+        }
+        u0 = line.start(blockIdx.x);
+        u1 = line.start(blockIdx.x + 1);
+        cur = seek(p, rows, u0);
+        if (cur.tile == cur.tiles) next_row(p, rows, cur);
     }
-    const int u0 = line.start(blockIdx.x), u1 = line.start(blockIdx.x + 1);
-    Cursor cur = seek(p, rows, u0);
-    if (cur.tile == cur.tiles) next_row(p, rows, cur);
     Cursor ahead = cur;
     const Cursor at0 = cur;
     const long long key_stride = (long long)p.Hkv * G::kRow;
@@ -438,7 +464,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         }
         next_row(p, rows, cur);
     }
-    if (threadIdx.x == 0) {
+    if (!p.whole && threadIdx.x == 0) {
         // a row whose second part was this CTA's: for the join
         int4 d = make_int4(-1, 0, 0, 0);
         const int first = at0.u - at0.tile;
@@ -510,17 +536,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                 p.o[at * D + x * 32 + lane] = __ushort_as_bfloat16((unsigned short)round_bf16(o[x] * inv, p.round_mode));
             if (p.lse && lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
         }
-        for (int s = blockIdx.x; s < p.B; s += p.grid) {
-            const int n = __ldg(p.seqlens_k + s);
-            if (n < 0 || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
-                if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
-            } else if (n == 0) {
-                for (long long i = threadIdx.x; i < (long long)p.H * D; i += 256)
-                    p.o[(long long)s * p.H * D + i] = __ushort_as_bfloat16((unsigned short)0x7FC0u);
-                if (p.lse)
-                    for (int h = threadIdx.x; h < p.H; h += 256) p.lse[(long long)s * p.H + h] = -INFINITY;
-            }
-        }
+        for (int s = blockIdx.x; s < p.B; s += p.grid) keyless(p, s, __ldg(p.seqlens_k + s), D);
         return;
     }
     if constexpr (kWeights) {

@@ -4,10 +4,10 @@
  * Operation.  O = softmax(Q K^T / sqrt(d)) V, non-causal, head dimension d = 128 (64 is
  * accepted too), bf16 in and out, fp32 accumulation.  Extensions below: the causal mask,
  * grouped K/V heads and the row log-sum-exp (attn_fwd_ex), variable-length batches
- * (attn_fwd_varlen), a paged K/V cache (attn_fwd_paged), the backward (attn_bwd), and what surrounds a
- * paged cache: rotary positions (attn_rope), appending (attn_paged_append), one-token decoding
- * (attn_paged_decode) and eviction (attn_paged_evict).  Source: "MoonMath AI open-sources a HIP attention kernel for
- * AMD MI300X that beats AITER" (news.chathome.org), opening section: attention is the fused
+ * (attn_fwd_varlen), a paged K/V cache (attn_fwd_paged), the backward (attn_bwd), and what
+ * surrounds a paged cache: rotary positions (attn_rope), appending (attn_paged_append), one-token
+ * decoding (attn_paged_decode) and eviction (attn_paged_evict).  Source: "MoonMath AI open-sources
+ * a HIP attention kernel for AMD MI300X that beats AITER" (news.chathome.org), opening section: attention is the fused
  * softmax(QK^T/sqrt(d))V; the kernel takes BSHD or BHSD tensors without transposes, head
  * dimension fixed at 128, any query and key length including cross-attention; its
  * limitations paragraph: three output rounding modes (RTNE, RTNA, RTZ), NaN/Inf handled
@@ -549,8 +549,8 @@ int attn_paged_append(const attn_append_args_t* args, attn_stream_t stream);
  *   round_mode    as in attn_fwd.  Non-finite values are treated as there
  * Results are bitwise reproducible for the same lengths on the same GPU model.  workspace: caller device
  * memory of at least attn_paged_decode_workspace_size() bytes, 16-byte aligned: the parts of split rows,
- * and with weights the logits (4 bytes per query head and table slot).  The size query returns
- * 0 for invalid arguments or without a usable device.
+ * and with weights the logits (4 bytes per query head and table slot).  A few short sequences need none:
+ * the size query returns 0 for them, as it does for invalid arguments or without a usable device.
  */
 typedef struct {
     const void* q;

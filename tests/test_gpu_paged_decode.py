@@ -114,6 +114,28 @@ def test_decode_matches_oracle(attn, case, weights):
     check(attn, lens, H, Hkv, d, P, mode, seed=100 + P, weights=weights)
 
 
+def test_few_short_rows_and_their_neighbours_split(attn):
+    # the same sequences with a table that has room for more keys: split rows against whole ones
+    lens, P, d = [600, 1, 0, 129], 16, 128
+    q, k, v = packed(4, sum(lens), 8, 2, d, seed=15)
+    kc, vc, table = build_cache(k, v, lens, P, seed=16)
+    wide = np.concatenate([table, np.full((4, 200), -5, dtype=table.dtype)], axis=1)
+    a, b = run(attn, q, kc, vc, lens, table), run(attn, q, kc, vc, lens, wide)
+    status_ok(attn)
+    assert torch.isnan(a[0][2]).all() and torch.isnan(b[0][2]).all()
+    assert torch.isneginf(a[1][2]).all() and torch.isneginf(b[1][2]).all()
+    used = [0, 1, 3]
+    # nearly equal values, each rounded by half a step (2^-8) at most
+    assert ((a[0][used].float() - b[0][used].float()).abs() <= 2.0 ** -7 * b[0][used].float().abs() + 1e-5).all()
+    assert torch.allclose(a[1][used], b[1][used], rtol=0, atol=1e-5)
+    o = torch.full((4, 8, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    bad = table.copy()
+    bad[0, 3] = kc.shape[0]
+    attn.attn_paged_decode(q.cuda(), kc.cuda(), vc.cuda(), cuda([600, -1, 0, table.shape[1] * P + 1]), cuda(bad), o=o)
+    assert attn.cache_device_status() == (1, 22)
+    assert (o[[0, 1, 3]] == 7.0).all() and torch.isnan(o[2]).all()
+
+
 def test_peaked_rows(attn):
     # logits of deviation 16: the running maximum moves far, most weights underflow
     check(attn, [2000, 999], 8, 2, 128, 16, seed=7, weights=True, sigma=4.0)

@@ -37,10 +37,6 @@ cudaError_t set_decode_attr() {
     return e;
 }
 
-cudaError_t set_select_attr(void (*kernel)(EvictParams)) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStaged * 4);
-}
-
 int device(int* sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return ATTN_ERR_NO_DEVICE; }
@@ -57,11 +53,7 @@ int device(int* sms) {
         if (d.major == 10 && d.minor == 3 &&
             (set_decode_attr<128, 1>() != cudaSuccess || set_decode_attr<128, 2>() != cudaSuccess ||
              set_decode_attr<128, 4>() != cudaSuccess || set_decode_attr<64, 1>() != cudaSuccess ||
-             set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess ||
-             set_select_attr(attn_evict_select_kernel<512, false>) != cudaSuccess ||
-             set_select_attr(attn_evict_select_kernel<512, true>) != cudaSuccess ||
-             set_select_attr(attn_evict_select_kernel<1024, false>) != cudaSuccess ||
-             set_select_attr(attn_evict_select_kernel<1024, true>) != cudaSuccess)) {
+             set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess)) {
             cudaGetLastError();
             return ATTN_ERR_CUDA;
         }
@@ -546,28 +538,26 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     p.fill = reinterpret_cast<int2*>(ws + l.fill);
     p.fill_w = reinterpret_cast<uint2*>(ws + l.fill_w);
     const int64_t rows = a.B * a.Hkv, room = a.max_pages * a.page_size;
-    // select: the CTAs of a row hold its keys in shared memory where 8 of them can (else the keys are read again for
+    // select: the CTAs of a row hold its keys in registers where 8 of 1024 threads can (else the keys are read again for
     // each pass), and more of them share a row while every CTA has an SM and 2048 keys
     p.cluster = 1;
-    while (p.cluster < kMostCluster && (room > (int64_t)p.cluster * kMostStaged || (2 * rows * p.cluster <= sms && room > p.cluster * 2048)))
+    while (p.cluster < kMostCluster &&
+           (room > (int64_t)p.cluster * 1024 * kHeldMost || (2 * rows * p.cluster <= sms && room > p.cluster * 2048)))
         p.cluster *= 2;
-    p.staged = (int)cdiv(cdiv(room, p.cluster), 1024) * 1024;
-    if (p.staged > kMostStaged) p.staged = kMostStaged;
+    const bool wide = room > (int64_t)p.cluster * 2048;      // 1024 threads, else 512: four keys a thread
     // column pieces of 32 bytes at least (a DRAM sector), until there are three CTAs for every SM
     p.pieces = 1;
     while (2 * rows * p.pieces < 3 * sms && p.row_bytes / p.pieces > 32) p.pieces *= 2;
     if ((st = launch_clusters(attn_evict_prep_kernel, kPrepCtas, kPrepCtas, kPrepThreads, 0, stream, p)) != ATTN_OK) return st;
-    // threads: two keys each at least, 512 or 1024
-    const size_t smem = (size_t)p.staged * 4;
     const int64_t ctas = rows * p.cluster;
     if (p.cluster == 1 && l.most_moves <= kMostWhole && a.recent <= kMostWhole) {
-        st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024, true>, ctas, 1, 1024, smem, stream, p)
-                             : launch_clusters(attn_evict_select_kernel<512, true>, ctas, 1, 512, smem, stream, p);
+        st = wide ? launch(attn_evict_select_kernel<1024, true>, ctas, 1, 1024, 0, stream, p)
+                  : launch(attn_evict_select_kernel<512, true>, ctas, 1, 512, 0, stream, p);
         if (st != ATTN_OK || p.seqlens_out != p.seqlens_k) return st;
         return launch(attn_evict_lens_kernel, 1, 1, 256, 0, stream, p);
     }
-    st = p.staged > 2048 ? launch_clusters(attn_evict_select_kernel<1024, false>, ctas, p.cluster, 1024, smem, stream, p)
-                         : launch_clusters(attn_evict_select_kernel<512, false>, ctas, p.cluster, 512, smem, stream, p);
+    st = wide ? launch_clusters(attn_evict_select_kernel<1024, false>, ctas, p.cluster, 1024, 0, stream, p)
+              : launch_clusters(attn_evict_select_kernel<512, false>, ctas, p.cluster, 512, 0, stream, p);
     if (st != ATTN_OK) return st;
     if (l.most_moves > 0) {
         st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, stream, p)

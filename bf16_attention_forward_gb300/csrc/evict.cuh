@@ -11,7 +11,8 @@
 // Prepare kernel (one cluster of 8 CTAs): counts each page's uses in the table and decides which sequences are
 // cut: over the budget, a valid length, every page in the cache and used once.
 // Select kernel (a cluster of 1 to 8 CTAs per (sequence, K/V head)): the weights are read once, as
-// order-preserving 32-bit keys that stay in shared memory.  A histogram of the upper 11 bits, summed over
+// order-preserving 32-bit keys that stay in registers (up to 16 a thread; longer rows are read again for
+// each pass).  A histogram of the upper 11 bits, summed over
 // the cluster, gives the bin of the threshold, and two more histograms (of 11 and 10 bits) of that bin's keys the
 // threshold itself; a bin of up to 4096 keys is gathered into every CTA's registers for that, which spares
 // those two the cluster's exchange and the walk over all keys.  An ordered pass then lists freed slots and
@@ -43,7 +44,6 @@ struct EvictParams {
     int budget, sinks, recent;
     int cluster;               // CTAs of a (sequence, K/V head) in the select kernel
     int pieces;                // column pieces of a row in the shift kernel
-    int staged;                // keys that a select CTA has room for in shared memory
     // workspace
     int32_t* uses;             // [num_pages]: table entries of used pages that name the page
     int32_t* cut;              // [B]: the length n of a sequence that is cut, -1 - n of one that fits, 0: refused
@@ -61,7 +61,7 @@ constexpr int kMostGathered = 2 * kBins;   // keys of the threshold's bin that a
 constexpr int kMostWhole = 256;        // most moves, and most recent keys, that the select kernel does itself
 constexpr int kMostRanked = 128;       // ... and up to which each key's rank says it (0.6 us less than the two passes)
 constexpr int kListRows = 8;           // rows of 32 slots that a warp lists at a time
-constexpr int kMostStaged = 16384;     // 64 KB: three CTAs an SM
+constexpr int kHeldMost = 16;          // rows of 32 slots whose keys a warp of 1024 threads' CTA holds in registers
 constexpr int kFillThreads = 256;
 constexpr int kShiftThreads = 256;
 
@@ -190,7 +190,7 @@ template <int T, bool kWhole>
 __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kWarps = T / 32, kU = 16;            // kU: loads in flight
     constexpr int kEach = kMostGathered / T;
-    extern __shared__ uint32_t key_s[];
+    constexpr int kHeldRows = T == 1024 ? kHeldMost : 4, kList = kHeldRows < kListRows ? kHeldRows : kListRows;
     __shared__ __align__(16) int pool[4][kBins];
     int* const hist = pool[0];                         // this CTA's counts,
     int(* const sum_s)[kBins] = &pool[1];              // and the cluster's of each pass;
@@ -237,8 +237,23 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
     const int all_slots = n - p.recent - p.sinks, run = ((all_slots - 1) / (C * T) + 1) * 32;
     const int place = warp * C + rank;                 // of this warp among the cluster's
     const int wlo = p.sinks + min(place * run, all_slots), whi = min(wlo + run, n - p.recent);
-    const bool staged = run * kWarps <= p.staged;      // (the same for the whole cluster)
-    uint32_t* const key_w = key_s + warp * run;        // this warp's keys
+    // Their keys, kHeldRows rows of 32 slots at a time: row r of chunk c holds slots wlo + 32 (kHeldRows c + r) + lane.
+    const int chunks = (run / 32 - 1) / kHeldRows + 1; // (the same for the whole cluster)
+    const bool held = chunks == 1;                     // loaded once, for the histogram's first pass
+    uint32_t key[kHeldRows];
+    int rows = 0, mine_n = 0;                          // of the chunk: the warp's rows, and this lane's keys
+    auto load = [&](int c) {
+        const int left = whi - wlo - c * (32 * kHeldRows);
+        const float* from = w + wlo + c * (32 * kHeldRows) + lane;
+        rows = min(max((left + 31) / 32, 0), kHeldRows);
+        mine_n = min(max((left - lane + 31) / 32, 0), kHeldRows);
+        float x[kHeldRows];
+#pragma unroll
+        for (int r = 0; r < kHeldRows; ++r)
+            if (r < mine_n) x[r] = from[32 * r];
+#pragma unroll
+        for (int r = 0; r < kHeldRows; ++r) key[r] = r < mine_n ? weight_key(x[r]) : 0u;
+    };
     for (int i = tid; i < 4 * kBins; i += T) pool[0][i] = 0;
     if (tid == 0) near_n = 0;
     if (C > 1) cluster_sync(); else __syncthreads();   // no CTA adds to another's counts before they are zero
@@ -256,26 +271,14 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
             for (int e = 0; e < kEach; ++e)
                 if (tid + e * T < first_tied && (near[e] >> (shift + bits)) == prefix)
                     atomicAdd(&hist[(near[e] >> shift) & ((1u << bits) - 1)], 1);
-        } else if (pass > 0 && staged) {
-#pragma unroll 4
-            for (int j = lane; j < whi - wlo; j += 32) {
-                const uint32_t key = key_w[j];
-                if ((key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
-            }
         } else {
-            for (int j0 = wlo + lane; j0 < whi; j0 += kU * 32) {
-                float x[kU];
+            for (int c = 0; c < chunks; ++c) {
+                if (pass == 0 || !held) load(c);
 #pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    if (j0 + u * 32 < whi) x[u] = w[j0 + u * 32];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int j = j0 + u * 32;
-                    if (j < whi) {
-                        const uint32_t key = weight_key(x[u]);
-                        if (staged) key_w[j - wlo] = key;
-                        if (pass == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
-                    }
+                for (int r = 0; r < kHeldRows; ++r) {
+                    if (r >= rows) break;
+                    if (r < mine_n && (pass == 0 || (key[r] >> (shift + bits)) == prefix))
+                        atomicAdd(&hist[(key[r] >> shift) & ((1u << bits) - 1)], 1);
                 }
             }
         }
@@ -327,13 +330,13 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
         prefix = prefix_s;
         want = want_s;
         tied = tied_s;
-        if (pass > 0 || !staged || tied > kMostGathered) continue;
+        if (pass > 0 || !held || tied > kMostGathered) continue;
 
         // gather the bin's keys, of every CTA
-#pragma unroll 4
-        for (int j = lane; j < whi - wlo; j += 32) {
-            const uint32_t key = key_w[j];
-            if ((key >> 21) == prefix) near_s[atomicAdd(&near_n, 1)] = key;
+#pragma unroll
+        for (int r = 0; r < kHeldRows; ++r) {
+            if (r >= rows) break;
+            if (r < mine_n && (key[r] >> 21) == prefix) near_s[atomicAdd(&near_n, 1)] = key[r];
         }
         if (C > 1) cluster_sync(); else __syncthreads();
         if (C == 1 && tied <= kMostRanked) {           // each key's rank among them
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
                 near[e] = (uint32_t)cluster_ld(cluster_map(ptx::smem_u32(near_s) + 4 * (tid + e * T - before[e]), from[e]));
     }
 
-    auto key_at = [&](int j) { return staged ? key_w[j - wlo] : weight_key(w[j]); };
+    if (keep == 0 && held) load(0);                    // (no pass has; only the slots matter then)
     // Of a count of this warp's: the sum over the warps before it in the cluster, and over all.  Every warp of the
     // cluster leaves its count in its CTA, and each reads them all.
     auto sums_before = [&](int count, int which, int& all) {
@@ -397,26 +400,38 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
     const bool some = tied > want;
     if (some) {
         int count = 0;
-#pragma unroll 4
-        for (int j0 = wlo; j0 < whi; j0 += 32)
-            count += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < whi && key_at(min(j0 + lane, whi - 1)) == prefix));
+        for (int c = 0; c < chunks; ++c) {
+            if (!held) load(c);
+#pragma unroll
+            for (int r = 0; r < kHeldRows; ++r) {
+                if (r >= rows) break;
+                count += __popc(__ballot_sync(0xFFFFFFFFu, r < mine_n && key[r] == prefix));
+            }
+        }
         ties = sums_before(count, 0, all);
     }
     // listed are freed slots below `end` and survivors at or past it: counted here, and listed below
     const uint32_t least = keep > 0 ? prefix : 0xFFFFFFFFu;      // (above every key)
-    auto listed = [&](int j, uint32_t key, int& seen) {
-        bool kept = key >= least;
+    auto listed = [&](int c, int r, int& seen) {
+        bool kept = key[r] >= least;
         if (some) {
-            const bool tie = j < whi && key == prefix;
+            const bool tie = r < mine_n && key[r] == prefix;
             const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
             if (tie) kept = seen + __popc(tb & below) < want;
             seen += __popc(tb);
         }
-        return __ballot_sync(0xFFFFFFFFu, j < whi && kept == (j >= end));
+        const bool late = wlo + 32 * (kHeldRows * c + r) + lane >= end;
+        return __ballot_sync(0xFFFFFFFFu, r < mine_n && kept == late);
     };
     int count = 0, seen = ties;
-#pragma unroll 4
-    for (int j0 = wlo; j0 < whi; j0 += 32) count += __popc(listed(j0 + lane, j0 + lane < whi ? key_at(j0 + lane) : 0u, seen));
+    for (int c = 0; c < chunks; ++c) {
+        if (!held) load(c);
+#pragma unroll
+        for (int r = 0; r < kHeldRows; ++r) {
+            if (r >= rows) break;
+            count += __popc(listed(c, r, seen));
+        }
+    }
     int at = sums_before(count, 1, all);
     pdl_wait();                            // the prepare kernel's verdict, and its zero in p.total
     const bool stays = p.cut[b] == 0;
@@ -434,15 +449,18 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
     int* const list = pool[2];                         // kWhole: freed slots, then the survivors that fill them
     const uint32_t w0 = (uint32_t)(bh * room);
     seen = ties;
-    if (moves > 0)
-        for (int j0 = wlo; j0 < whi; j0 += 32 * kListRows) {
+    for (int c = 0; moves > 0 && c < chunks; ++c) {
+        if (!held) load(c);
+#pragma unroll
+        for (int r0 = 0; r0 < kHeldRows; r0 += kList) {
+            if (r0 >= rows) break;
             // slots (from j0 on) that are listed, close together: about one in four is, and each costs a page lookup
+            const int j0 = wlo + 32 * (kHeldRows * c + r0);
             int m = 0;
-#pragma unroll 4
-            for (int r = 0; r < kListRows; ++r) {
-                const int j = j0 + 32 * r + lane;
-                if (j0 + 32 * r >= whi) break;
-                const unsigned bits = listed(j, j < whi ? key_at(j) : 0u, seen);
+#pragma unroll
+            for (int r = 0; r < kList; ++r) {
+                if (r0 + r >= rows) break;
+                const unsigned bits = listed(c, r0 + r, seen);
                 if ((bits >> lane) & 1) slot_s[m + __popc(bits & below)] = (uint16_t)(32 * r + lane);
                 m += __popc(bits);
             }
@@ -479,6 +497,7 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
             at += m;
             __syncwarp();
         }
+    }
     if (C > 1) cluster_sync();             // no CTA leaves while its shared memory may be read
     if constexpr (kWhole) {
         // (lengths in place are the next kernel's: another head's CTA may not have read them yet)

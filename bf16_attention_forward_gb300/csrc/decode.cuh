@@ -92,6 +92,7 @@ struct Line {
 // rows: of a sequence
 __device__ __forceinline__ Line make_line(const DecodeParams& p, int rows) {   // every lane of a warp calls it
     int n = 0;
+#pragma unroll 2
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
         const int t = seq_tiles(p, __ldg(p.seqlens_k + b));
         n += t > 0 ? t + 1 : 0;
@@ -114,6 +115,7 @@ __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
     const int lane = threadIdx.x & 31;
     int done = 0;                      // places of a row, of the sequences before
     Cursor c{u, 0, 0, 0, 1, 0};
+#pragma unroll 1
     for (int base = 0; base < p.B; base += 32) {
         const int len = base + lane < p.B ? __ldg(p.seqlens_k + base + lane) : 0, tiles = seq_tiles(p, len);
         const int mine = tiles > 0 ? tiles + 1 : 0;
@@ -145,6 +147,7 @@ __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor
     c.tile = 0;
     if (++c.row < rows) return;
     c.row = 0;
+#pragma unroll 1
     while (c.b + 1 < p.B) {
         ++c.b;
         c.len = __ldg(p.seqlens_k + c.b);
@@ -158,9 +161,11 @@ __device__ __forceinline__ void keyless(const DecodeParams& p, int b, int n, int
     if (n < 0 || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
     } else if (n == 0) {
+#pragma unroll 1
         for (long long i = threadIdx.x; i < (long long)p.H * d; i += blockDim.x)
             p.o[(long long)b * p.H * d + i] = __ushort_as_bfloat16((unsigned short)0x7FC0u);
         if (p.lse)
+#pragma unroll 1
             for (int h = threadIdx.x; h < p.H; h += blockDim.x) p.lse[(long long)b * p.H + h] = -INFINITY;
     }
 }
@@ -257,12 +262,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         }
         cp_async_commit();
     };
-    Found found[G::kStages - 1];
-#pragma unroll
-    for (int s = 0; s < G::kStages - 1; ++s) found[s] = find();
-#pragma unroll
-    for (int s = 0; s < G::kStages - 1; ++s) load(s, found[s]);
+    // (code that runs once is kept short: every launch fetches it anew)
     Found next_tile = find();
+#pragma unroll 1
+    for (int s = 0; s < G::kStages - 1; ++s) {
+        const Found f = next_tile;
+        next_tile = find();
+        load(s, f);
+    }
 
     // ldmatrix addresses inside a stage: lane i gives row i % 8 of 8x8 matrix i / 8
     const int mat = lane >> 3, mrow = lane & 7;
@@ -299,6 +306,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int e = 0; e < 4; ++e) acc[t][mt][e] = 0.0f;
         }
         bool bad = false;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
             cp_async_wait<G::kStages - 2>();
             __syncwarp();
@@ -488,44 +496,46 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
         const int4 row = p.split[blockIdx.x];
         const int b = row.x, c0 = row.z, c1 = row.w;
         const int kv_head = row.y / p.head_blocks, head0 = (row.y - kv_head * p.head_blocks) * kHeads;
+#pragma unroll 1
         for (int hh = warp; b >= 0 && hh < kHeads && head0 + hh < p.group; hh += 8) {
             // a row's first part is in slot 1 of its CTA, the others in slot 0 of theirs
             auto part = [&](int i) { return (long long)(2 * i + (i == c0)) * kHeads + hh; };
-            constexpr int kU = 8;                      // parts in flight
-            float v[kU][kC];
+            // the weight of part c0 + lane of the row, and of parts past the 31st later
+            float2 ml = c0 + lane <= c1 ? p.part_ml[part(c0 + lane)] : make_float2(-INFINITY, 0.0f);
+            constexpr int kU = 4;                      // parts in flight
+            float v[kU][kC], sum = 0.0f, o[kC];
             auto load = [&](int i0) {
+                const float* from = p.part_o + part(i0) * D + lane;
 #pragma unroll
-                for (int j = 0; j < kU; ++j)
+                for (int j = 0; j < kU; ++j) {
                     if (i0 + j <= c1)
 #pragma unroll
-                        for (int x = 0; x < kC; ++x) v[j][x] = p.part_o[part(i0 + j) * D + x * 32 + lane];
+                        for (int x = 0; x < kC; ++x) v[j][x] = from[x * 32];
+                    from = p.part_o + part(i0 + j + 1) * D + lane;
+                }
             };
-            float2 ml = c0 + lane <= c1 ? p.part_ml[part(c0 + lane)] : make_float2(-INFINITY, 0.0f);
-            load(c0);
             float mx = ml.x;
+#pragma unroll 1
             for (int i = c0 + 32 + lane; i <= c1; i += 32) mx = fmaxf(mx, p.part_ml[part(i)].x);
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
             bool bad = false;
-            float sum = 0.0f, o[kC];
 #pragma unroll
             for (int x = 0; x < kC; ++x) o[x] = 0.0f;
-            for (int base = c0; base <= c1; base += 32) {
-                // lane j: part base + j
-                if (base > c0) ml = base + lane <= c1 ? p.part_ml[part(base + lane)] : make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+            for (int i0 = c0; i0 <= c1; i0 += kU) {
+                load(i0);
+                const int j0 = (i0 - c0) & 31;
+                if (j0 == 0 && i0 > c0) ml = i0 + lane <= c1 ? p.part_ml[part(i0 + lane)] : make_float2(-INFINITY, 0.0f);
                 bad |= ml.y == kBadPart;
                 const float f = rescale(ml.x, mx, p.scale_log2), s = ml.y * f;
-                const int n = min(32, c1 - base + 1);
-                for (int j0 = 0; j0 < n; j0 += kU) {
-                    if (base + j0 > c0) load(base + j0);
 #pragma unroll
-                    for (int j = 0; j < kU; ++j)
-                        if (j0 + j < n) {
-                            const float fj = __shfl_sync(0xFFFFFFFFu, f, j0 + j);
-                            sum += __shfl_sync(0xFFFFFFFFu, s, j0 + j);
+                for (int j = 0; j < kU; ++j) {
+                    const float fj = __shfl_sync(0xFFFFFFFFu, f, j0 + j), sj = __shfl_sync(0xFFFFFFFFu, s, j0 + j);
+                    if (i0 + j > c1) continue;
+                    sum += sj;
 #pragma unroll
-                            for (int x = 0; x < kC; ++x) o[x] += v[j][x] * fj;
-                        }
+                    for (int x = 0; x < kC; ++x) o[x] += v[j][x] * fj;
                 }
             }
             if (__any_sync(0xFFFFFFFFu, bad)) continue;
@@ -536,6 +546,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                 p.o[at * D + x * 32 + lane] = __ushort_as_bfloat16((unsigned short)round_bf16(o[x] * inv, p.round_mode));
             if (p.lse && lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
         }
+#pragma unroll 1
         for (int s = blockIdx.x; s < p.B; s += p.grid) keyless(p, s, __ldg(p.seqlens_k + s), D);
         return;
     }
@@ -546,12 +557,14 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
         const Line line = make_line(p, p.Hkv * p.head_blocks);
         // this block's places on the line of K/V heads, which has one for head_blocks of the attention kernel's
         const int units = line.units / p.head_blocks, block = blockIdx.x - p.grid, blocks = gridDim.x - p.grid;
-        const int t1 = (int)((long long)units * (block + 1) / blocks), t0 = (int)((long long)units * block / blocks);
+        const int per = units / blocks, more = units - per * blocks;
+        const int t0 = per * block + min(block, more), t1 = t0 + per + (block < more);
         if (t0 >= t1) return;
         const long long room = (long long)p.pages.max_pages * p.pages.page_size;
         const bool vector = room % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
         const uint64_t done_policy = ptx::policy_evict_first();
         Cursor cur = seek(p, p.Hkv, t0);
+#pragma unroll 1
         for (; cur.u < t1; next_row(p, p.Hkv, cur)) {
             const int n = min(cur.tiles - cur.tile, t1 - cur.u);
             if (n == 0) continue;
@@ -561,6 +574,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
             // count there head_blocks times
             const int main0 = (cur.u - cur.tile) * p.head_blocks;
             float* out = p.weights + kv * room;
+#pragma unroll 1
             for (int g0 = 0; g0 < p.group; g0 += kG) {
                 __syncthreads();
                 if (threadIdx.x == 0) bad_s = 0;
@@ -575,6 +589,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                     } else {
                         float mx = -INFINITY, sum = 0.0f;
                         bool bad = false;
+#pragma unroll 1
                         for (int i = c0 + lane; i <= c1; i += 32) {
                             const float2 x = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
                             mx = fmaxf(mx, x.x);
@@ -582,6 +597,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                         }
 #pragma unroll
                         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+#pragma unroll 1
                         for (int i = c0; i <= c1; ++i) {
                             const float2 x = p.part_ml[(long long)(2 * i + (i == c0)) * kHeads + hh];
                             sum += x.y * rescale(x.x, mx, p.scale_log2);
@@ -596,6 +612,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                 __syncthreads();
                 if (bad_s) break;
                 // four neighbouring keys a thread: 16-byte loads (4-byte ones left the loop at 2.5 TB/s)
+#pragma unroll 1
                 for (int j0 = cur.tile * kDecTile + threadIdx.x * 4; j0 < j1; j0 += 1024) {
                     const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * p.score_room + j0;
                     float4 x[kG], w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -616,7 +633,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                         if (g0 + g >= p.group) continue;
                         const float2 ml = ml_s[g];
                         // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
-                        auto weight = [&](float v) { return (v == -INFINITY ? 0.0f : exp2f((v - ml.x) * p.scale_log2)) * ml.y; };
+                        auto weight = [&](float v) { return (v == -INFINITY ? 0.0f : ptx::ex2_approx((v - ml.x) * p.scale_log2)) * ml.y; };
                         sum.x += weight(x[g].x);
                         sum.y += weight(x[g].y);
                         sum.z += weight(x[g].z);

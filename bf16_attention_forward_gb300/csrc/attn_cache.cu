@@ -560,8 +560,8 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
               : launch_clusters(attn_evict_select_kernel<512, false>, ctas, p.cluster, 512, 0, stream, p);
     if (st != ATTN_OK) return st;
     if (l.most_moves > 0) {
-        st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 4 * sms, 1, kFillThreads, 0, stream, p)
-                        : launch(attn_evict_fill_kernel<64>, 4 * sms, 1, kFillThreads, 0, stream, p);
+        st = a.d == 128 ? launch(attn_evict_fill_kernel<128>, 16 * sms, 1, kFillThreads, 0, stream, p)
+                        : launch(attn_evict_fill_kernel<64>, 16 * sms, 1, kFillThreads, 0, stream, p);
         if (st != ATTN_OK) return st;
     }
     return launch(attn_evict_shift_kernel, rows * (2 * p.pieces + 1), 1, kShiftThreads, 0, stream, p);

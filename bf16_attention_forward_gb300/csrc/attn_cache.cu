@@ -214,14 +214,14 @@ RopeTensor rope_tensor(const void* src, void* dst, const int64_t* ss, const int6
 }
 
 int launch_rope(RopeParams& p, int64_t d, bool halves, bool append, int sms, cudaStream_t stream) {
-    // Heads per thread: all of a token's, which computes each angle once, unless that leaves the SMs
-    // short of threads (2048 each); then the heads are dealt out evenly.
-    const int64_t lanes = p.tokens * (d / 16), full = (int64_t)sms * 2048;
+    // Heads of a block: all of its tokens', which computes each angle once, unless that leaves the SMs short
+    // of threads (2048 each); then the heads are dealt out evenly, in the pieces that a warp turns at a time.
+    const int64_t lanes = p.tokens * 32, full = (int64_t)sms * 2048, piece = kRopeHeads * (32 / (d / 16));
     int64_t splits = lanes < full ? cdiv(full, lanes) : 1;
-    if (splits > cdiv(p.heads, kRopeHeads)) splits = cdiv(p.heads, kRopeHeads);
-    p.heads_per_thread = (int)cdiv(p.heads, splits);
-    const int64_t grid = cdiv(lanes, kRopeThreads);
-    const int gy = (int)cdiv(p.heads, p.heads_per_thread);
+    if (splits > cdiv(p.heads, piece)) splits = cdiv(p.heads, piece);
+    p.heads_per_block = (int)(cdiv(cdiv(p.heads, splits), piece) * piece);
+    const int64_t grid = cdiv(p.tokens, kRopeThreads / 32);
+    const int gy = (int)cdiv(p.heads, p.heads_per_block);
     if (gy > 65535) return ATTN_ERR_UNSUPPORTED;
     if (d == 128)
         return append ? (halves ? launch(attn_rope_kernel<128, true, true>, grid, gy, kRopeThreads, 0, stream, p)

@@ -12,9 +12,9 @@
 // frequency from its fp64 value.  The top 32 bits of the product, read as a signed number of
 // half turns in [-1, 1), go to sincospi.
 //
-// Bound: HBM bytes (each element read and written once).  One thread holds the cosines and
-// sines of the 8 pairs of 16 elements and applies them to those elements of several heads, so that
-// the sincospi work is shared by the heads of a token.
+// Bound: HBM bytes (each element read and written once).  A warp takes a token: it computes each angle
+// once, into shared memory; a thread then holds the cosines and sines of 16 elements and applies
+// them to those elements of every 4th (d = 64: 8th) head, so that a warp reads 1 KB of a token at a time.
 #pragma once
 #include "cache_common.cuh"
 
@@ -34,7 +34,7 @@ struct RopeParams {
     const int32_t* axes;
     long long pos_axis, pos_b;     // element strides of positions
     long long S, tokens;           // tokens per batch entry, and in all
-    int pairs, num_axes, inverse, heads_per_thread, heads;
+    int pairs, num_axes, inverse, heads_per_block, heads;
     // appending
     Pages pages;
     const int32_t* cu_new;
@@ -54,9 +54,12 @@ __device__ __forceinline__ uint32_t rotate_word(uint32_t w, float c, float s) {
 
 template <int D, bool kHalves, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kL = D / 16;     // threads of a token: 16 elements (two 16-byte chunks) of a head each
+    constexpr int kL = D / 16;     // lanes of a head: 16 elements (two 16-byte chunks) each
+    constexpr int kSub = 32 / kL;  // heads that a warp takes side by side
+    constexpr int kWarps = kRopeThreads / 32;
     __shared__ unsigned long long turn[D / 2];
     __shared__ int axis[D / 2];
+    __shared__ float2 cs[kWarps][D / 2];               // cosine and sine of a warp's token
     __shared__ int cu_s[kAppend ? kCuStage : 1];
     pdl_wait();
     pdl_launch();
@@ -76,13 +79,9 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_AXES);
         return;
     }
-    const int l = threadIdx.x % kL;
-    const long long token = (long long)blockIdx.x * (kRopeThreads / kL) + threadIdx.x / kL;
-    if (token >= p.tokens) return;
-    const long long b = kAppend ? 0 : token / p.S, s = kAppend ? token : token - b * p.S;
-
-    const int h_begin = blockIdx.y * p.heads_per_thread;
-    const int h_end = min(h_begin + p.heads_per_thread, p.heads);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kL;
+    const int h_begin = blockIdx.y * p.heads_per_block + lane / kL;
+    const int h_end = min((int)(blockIdx.y + 1) * p.heads_per_block, p.heads);
     // the two chunks of this thread, and the first pair of each
     int ca, cb, pa, pb;
     if constexpr (kHalves) {
@@ -104,95 +103,105 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
         if (kAppend && t == 1 && h >= p.x[1].heads) { h -= p.x[1].heads; t = 2; }
         return t;
     };
-    struct Heads { uint4 a[kRopeHeads], b[kRopeHeads]; };
-    auto load = [&](int h0, Heads& x) {
+    // a token a warp
+#pragma unroll 1
+    for (long long token = (long long)blockIdx.x * kWarps + warp; token < p.tokens; token += (long long)gridDim.x * kWarps) {
+        const long long b = kAppend ? 0 : token / p.S, s = kAppend ? token : token - b * p.S;
+        struct Heads { uint4 a[kRopeHeads], b[kRopeHeads]; };
+        auto load = [&](int h0, Heads& x) {
 #pragma unroll
-        for (int u = 0; u < kRopeHeads; ++u) {
-            int h = h0 + u;
-            if (h >= h_end) continue;
-            const RopeTensor& t = p.x[tensor_of(h)];
-            const char* src = t.src + b * t.src_b + s * t.src_t + h * t.src_h;
-            x.a[u] = *reinterpret_cast<const uint4*>(src + ca * 16);
-            x.b[u] = *reinterpret_cast<const uint4*>(src + cb * 16);
+            for (int u = 0; u < kRopeHeads; ++u) {
+                int h = h0 + u * kSub;
+                if (h >= h_end) continue;
+                const RopeTensor& t = p.x[tensor_of(h)];
+                const char* src = t.src + b * t.src_b + s * t.src_t + h * t.src_h;
+                x.a[u] = *reinterpret_cast<const uint4*>(src + ca * 16);
+                x.b[u] = *reinterpret_cast<const uint4*>(src + cb * 16);
+            }
+        };
+        Heads x, next;
+        long long row = -1;        // the token's row of the cache
+        if constexpr (kAppend) {
+            const int* cu = staged ? cu_s : p.cu_new;
+            // the last sequence that starts at or before the token (a later one, empty, may start there too)
+            int lo = 0, hi = p.B;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (cu[mid] <= token) lo = mid; else hi = mid - 1;
+            }
+            if (lo >= p.B || cu[lo] > token) continue;     // in front of the first sequence or behind the last
+            load(h_begin, x);
+            const int end = cu[lo + 1];
+            const long long len = __ldg(p.seqlens_k + lo), first = len - ((long long)end - cu[lo]);
+            const long long at = len - end + token;        // its slot in the sequence
+            if (first >= 0 && at >= 0 && at < len && len <= (long long)p.pages.max_pages * p.pages.page_size)
+                row = page_row(p.pages, p.pages.table + (long long)lo * p.pages.max_pages, (int)at);
+            if (row < 0 && lane == 0) report_invalid(ATTN_CACHE_SITE_APPEND);
+        } else {
+            load(h_begin, x);
         }
-    };
 
-    Heads x, next;
-    long long row = -1;            // the token's row of the cache
-    if constexpr (kAppend) {
-        const int* cu = staged ? cu_s : p.cu_new;
-        // the last sequence that starts at or before the token (a later one, empty, may start there too)
-        int lo = 0, hi = p.B;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= token) lo = mid; else hi = mid - 1;
-        }
-        if (lo >= p.B || cu[lo] > token) return;           // in front of the first sequence or behind the last
-        load(h_begin, x);
-        const int end = cu[lo + 1];
-        const long long len = __ldg(p.seqlens_k + lo), first = len - ((long long)end - cu[lo]);
-        const long long at = len - end + token;            // its slot in the sequence
-        if (first >= 0 && at >= 0 && at < len && len <= (long long)p.pages.max_pages * p.pages.page_size)
-            row = page_row(p.pages, p.pages.table + (long long)lo * p.pages.max_pages, (int)at);
-        if (row < 0 && l == 0) report_invalid(ATTN_CACHE_SITE_APPEND);
-    } else {
-        load(h_begin, x);
-    }
-
-    float c[8], sn[8];
-    bool turned[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int pr = e < 4 ? pa + e : pb + e - 4;
-        turned[e] = pr < p.pairs;
-        c[e] = 1.0f;
-        sn[e] = 0.0f;
-        if (turned[e]) {
+        __syncwarp();              // (the token before is done with cs)
+#pragma unroll 2
+        for (int pr = lane; pr < p.pairs; pr += 32) {
             const long long pos = __ldg(p.positions + axis[pr] * p.pos_axis + b * p.pos_b + s);
             const unsigned long long at = turn[pr] * (unsigned long long)pos;
-            sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn[e], &c[e]);
-            if (p.inverse) sn[e] = -sn[e];
+            float sn, c;
+            sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn, &c);
+            cs[warp][pr] = make_float2(c, p.inverse ? -sn : sn);
         }
-    }
-    for (int h0 = h_begin; h0 < h_end; h0 += kRopeHeads) {
-        load(h0 + kRopeHeads, next);
+        __syncwarp();
+        float c[8], sn[8];
+        bool turned[8];
 #pragma unroll
-        for (int u = 0; u < kRopeHeads; ++u) {
-            int h = h0 + u;
-            if (h >= h_end) continue;
-            const int t = tensor_of(h);
-            if (kAppend && t > 0 && row < 0) continue;
-            if (!kAppend || t < 2) {
-                uint32_t wa[4] = {x.a[u].x, x.a[u].y, x.a[u].z, x.a[u].w}, wb[4] = {x.b[u].x, x.b[u].y, x.b[u].z, x.b[u].w};
-                if constexpr (kHalves) {
-                    if (turned[0]) {
+        for (int e = 0; e < 8; ++e) {
+            const int pr = e < 4 ? pa + e : pb + e - 4;
+            turned[e] = pr < p.pairs;
+            const float2 v = turned[e] ? cs[warp][pr] : make_float2(1.0f, 0.0f);
+            c[e] = v.x;
+            sn[e] = v.y;
+        }
+#pragma unroll 1
+        for (int h0 = h_begin; h0 < h_end; h0 += kRopeHeads * kSub) {
+            load(h0 + kRopeHeads * kSub, next);
+#pragma unroll
+            for (int u = 0; u < kRopeHeads; ++u) {
+                int h = h0 + u * kSub;
+                if (h >= h_end) continue;
+                const int t = tensor_of(h);
+                if (kAppend && t > 0 && row < 0) continue;
+                if (!kAppend || t < 2) {
+                    uint32_t wa[4] = {x.a[u].x, x.a[u].y, x.a[u].z, x.a[u].w}, wb[4] = {x.b[u].x, x.b[u].y, x.b[u].z, x.b[u].w};
+                    if constexpr (kHalves) {
+                        if (turned[0]) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                // elements 2i and 2i + 1 of both chunks
+                                const float a0 = __uint_as_float(wa[i] << 16), a1 = __uint_as_float(wa[i] & 0xFFFF0000u);
+                                const float b0 = __uint_as_float(wb[i] << 16), b1 = __uint_as_float(wb[i] & 0xFFFF0000u);
+                                wa[i] = ptx::pack_bf16x2(a0 * c[2 * i] - b0 * sn[2 * i],
+                                                         a1 * c[2 * i + 1] - b1 * sn[2 * i + 1]);
+                                wb[i] = ptx::pack_bf16x2(b0 * c[2 * i] + a0 * sn[2 * i],
+                                                         b1 * c[2 * i + 1] + a1 * sn[2 * i + 1]);
+                            }
+                        }
+                    } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            // elements 2i and 2i + 1 of both chunks
-                            const float a0 = __uint_as_float(wa[i] << 16), a1 = __uint_as_float(wa[i] & 0xFFFF0000u);
-                            const float b0 = __uint_as_float(wb[i] << 16), b1 = __uint_as_float(wb[i] & 0xFFFF0000u);
-                            wa[i] = ptx::pack_bf16x2(a0 * c[2 * i] - b0 * sn[2 * i],
-                                                     a1 * c[2 * i + 1] - b1 * sn[2 * i + 1]);
-                            wb[i] = ptx::pack_bf16x2(b0 * c[2 * i] + a0 * sn[2 * i],
-                                                     b1 * c[2 * i + 1] + a1 * sn[2 * i + 1]);
+                            if (turned[i]) wa[i] = rotate_word(wa[i], c[i], sn[i]);
+                            if (turned[4 + i]) wb[i] = rotate_word(wb[i], c[4 + i], sn[4 + i]);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (turned[i]) wa[i] = rotate_word(wa[i], c[i], sn[i]);
-                        if (turned[4 + i]) wb[i] = rotate_word(wb[i], c[4 + i], sn[4 + i]);
-                    }
+                    x.a[u] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+                    x.b[u] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
                 }
-                x.a[u] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-                x.b[u] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+                const RopeTensor& to = p.x[t];
+                char* dst = to.dst + b * to.dst_b + (kAppend && t > 0 ? row : s) * to.dst_t + h * to.dst_h;
+                *reinterpret_cast<uint4*>(dst + ca * 16) = x.a[u];
+                *reinterpret_cast<uint4*>(dst + cb * 16) = x.b[u];
             }
-            const RopeTensor& to = p.x[t];
-            char* dst = to.dst + b * to.dst_b + (kAppend && t > 0 ? row : s) * to.dst_t + h * to.dst_h;
-            *reinterpret_cast<uint4*>(dst + ca * 16) = x.a[u];
-            *reinterpret_cast<uint4*>(dst + cb * 16) = x.b[u];
+            x = next;
         }
-        x = next;
     }
 }
 

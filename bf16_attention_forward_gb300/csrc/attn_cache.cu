@@ -220,7 +220,9 @@ int launch_rope(RopeParams& p, int64_t d, bool halves, bool append, int sms, cud
     int64_t splits = lanes < full ? cdiv(full, lanes) : 1;
     if (splits > cdiv(p.heads, piece)) splits = cdiv(p.heads, piece);
     p.heads_per_block = (int)(cdiv(cdiv(p.heads, splits), piece) * piece);
-    const int64_t grid = cdiv(p.tokens, kRopeThreads / 32);
+    // 28 blocks an SM at most, 4 waves of the 7 that fit; longer lines give a warp several tokens (32,760 tokens of
+    // 24 heads: 63.1 us with a block per 4 tokens, 61.7 so; 16,384 of 40: 51.8 either way)
+    const int64_t most = cdiv(p.tokens, kRopeThreads / 32), grid = most < 28 * sms ? most : 28 * sms;
     const int gy = (int)cdiv(p.heads, p.heads_per_block);
     if (gy > 65535) return ATTN_ERR_UNSUPPORTED;
     if (d == 128)

@@ -15,6 +15,8 @@
 // Bound: HBM bytes (each element read and written once).  A warp takes a token: it computes each angle
 // once, into shared memory; a thread then holds the cosines and sines of 16 elements and applies
 // them to those elements of every 4th (d = 64: 8th) head, so that a warp reads 1 KB of a token at a time.
+// (A thread per 16 elements of a token, which reads 256 bytes of four tokens at a time and computes its 8
+// angles itself, took 55.7 us where this takes 51.7: 16,384 tokens of 40 heads, 336 MB at 6.5 TB/s.)
 #pragma once
 #include "cache_common.cuh"
 
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
         }
 
         __syncwarp();              // (the token before is done with cs)
-#pragma unroll 2
+#pragma unroll 1
         for (int pr = lane; pr < p.pairs; pr += 32) {
             const long long pos = __ldg(p.positions + axis[pr] * p.pos_axis + b * p.pos_b + s);
             const unsigned long long at = turn[pr] * (unsigned long long)pos;

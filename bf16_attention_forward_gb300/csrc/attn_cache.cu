@@ -164,9 +164,9 @@ bool strides_ok(const int64_t* st, const int64_t* n, int dims) {
         if (st[i] < 0 || (n[i] > 1 && st[i] > ((int64_t)1 << 40) / (n[i] - 1))) return false;
     return true;
 }
-bool strides_aligned(const int64_t* st, int n) {
-    for (int i = 0; i < n; ++i)
-        if (st[i] % 8 != 0) return false;
+bool strides_aligned(const int64_t* st, const int64_t* n, int dims) {
+    for (int i = 0; i < dims; ++i)
+        if (n[i] > 1 && st[i] % 8 != 0) return false;
     return true;
 }
 
@@ -250,8 +250,8 @@ int run_rope(const attn_rope_args_t& a, cudaStream_t stream) {
     if (a.k && (!strides_ok(a.k_stride, nk, 3) || !strides_ok(a.k_out_stride, nk, 3))) return ATTN_ERR_INVALID_ARG;
     if (((uintptr_t)a.q | (uintptr_t)a.q_out | (uintptr_t)a.k | (a.k ? (uintptr_t)a.k_out : 0)) & 15u) return ATTN_ERR_MISALIGNED;
     if (((uintptr_t)a.positions | (uintptr_t)a.axes) & 3u || (uintptr_t)a.freqs & 7u) return ATTN_ERR_MISALIGNED;
-    if (!strides_aligned(a.q_stride, 3) || !strides_aligned(a.q_out_stride, 3)) return ATTN_ERR_MISALIGNED;
-    if (a.k && (!strides_aligned(a.k_stride, 3) || !strides_aligned(a.k_out_stride, 3))) return ATTN_ERR_MISALIGNED;
+    if (!strides_aligned(a.q_stride, nq, 3) || !strides_aligned(a.q_out_stride, nq, 3)) return ATTN_ERR_MISALIGNED;
+    if (a.k && (!strides_aligned(a.k_stride, nk, 3) || !strides_aligned(a.k_out_stride, nk, 3))) return ATTN_ERR_MISALIGNED;
     auto v = [&](const void* p, int64_t H, const int64_t* s) { return view(p, a.B, a.S, H, a.d, s[0], s[1], s[2]); };
     const View q = v(a.q, a.H, a.q_stride), qo = v(a.q_out, a.H, a.q_out_stride);
     if (!nested(qo) || (!same(q, qo) && meet(q, qo))) return ATTN_ERR_ALIAS;
@@ -297,7 +297,7 @@ int run_append(const attn_append_args_t& a, cudaStream_t stream) {
         return ATTN_ERR_MISALIGNED;
     if (((uintptr_t)a.cu_seqlens_new | (uintptr_t)a.seqlens_k | (uintptr_t)a.block_table) & 3u) return ATTN_ERR_MISALIGNED;
     if (a.pairs && (((uintptr_t)a.positions | (uintptr_t)a.axes) & 3u || (uintptr_t)a.freqs & 7u)) return ATTN_ERR_MISALIGNED;
-    if (!strides_aligned(a.k_stride, 2) || !strides_aligned(a.v_stride, 2) || (a.q && !strides_aligned(a.q_stride, 2)))
+    if (!strides_aligned(a.k_stride, nk, 2) || !strides_aligned(a.v_stride, nk, 2) || (a.q && !strides_aligned(a.q_stride, nq, 2)))
         return ATTN_ERR_MISALIGNED;
     auto v = [&](const void* p, int64_t heads, const int64_t* s) { return view(p, 1, a.total, heads, a.d, 0, s[0], s[1]); };
     const int64_t dense[2] = {H * a.d, a.d}, cs[2] = {a.Hkv * a.d, a.d};

@@ -474,8 +474,8 @@ typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_
  * 2 * pairs pass through unchanged.  Angles are exact to fp32 for every int32 position; the
  * rotation is computed in fp32 and rounded once (nearest even).  A NaN stays some NaN.
  *   q, k          [B][S][H or Hkv][d] as strides say: element (b, s, h, x) at b * stride[0] +
- *                 s * stride[1] + h * stride[2] + x (elements; multiples of 8), so BSHD, BHSD and
- *                 views of a fused projection are all taken.  k may be NULL (Hkv is then ignored)
+ *                 s * stride[1] + h * stride[2] + x (elements; multiples of 8 where the dimension has
+ *                 more than one entry), so BSHD, BHSD and views of a fused projection are all taken.  k may be NULL (Hkv is then ignored)
  *   q_out, k_out  likewise with strides of their own (no two elements on one address); each may be
  *                 its input itself (same pointer and strides), and otherwise overlaps no input or output
  *   positions     int32: axis a of token (b, s) at a * pos_axis_stride + b * pos_batch_stride + s
@@ -584,7 +584,8 @@ int attn_paged_decode(const attn_decode_args_t* args, void* workspace, size_t wo
  *   weights_out        the weights of the slots after the call, freed slots up to the old length zero; may be
  *                      `weights` itself, else overlaps nothing.  Entries past the old length are not written
  *   seqlens_k, seqlens_out   device int32 [B]: lengths before and after; may be the same
- *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget
+ *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget; the weights, and the cache's rows times
+ *                      Hkv, are at most 2^31 (else ATTN_ERR_UNSUPPORTED)
  * workspace: caller device memory of at least attn_paged_evict_workspace_size() bytes, 16-byte aligned.
  */
 typedef struct {

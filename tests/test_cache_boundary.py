@@ -64,7 +64,7 @@ ROPE = [
     (ALIAS, [dict(q_out=M + 256), dict(k_out=2 * M), dict(k_out=M), dict(q_out=M, q_out_stride=(5120, 128, 1280)),
              dict(q_out_stride=(5120, 512, 64)), dict(q_out_stride=(512, 512, 128)), dict(q_out=3 * M)]),
     # columns of one projection's rows, in place or not, do not meet
-    (NO_DEVICE, [dict(), dict(k=0), dict(q_out=M, k_out=3 * M), dict(S=1, q_stride=(512, 0, 128)),
+    (NO_DEVICE, [dict(), dict(k=0), dict(q_out=M, k_out=3 * M), dict(S=1, q_stride=(512, 0, 128)), dict(S=1, q_stride=(512, 3, 128)), dict(B=1, q_stride=(7, 512, 128)),
                  dict(q=M, k=M + 1024, q_out=M, k_out=M + 1024, q_stride=(10240, 1024, 128), k_stride=(10240, 1024, 128),
                       q_out_stride=(10240, 1024, 128), k_out_stride=(10240, 1024, 128)),
                  dict(q_stride=(0, 512, 128)), dict(pairs=1), dict(pairing=1, pairs=8)]),
@@ -99,7 +99,8 @@ EVICT = [
     (INVALID, [dict(k_cache=0), dict(v_cache=0), dict(weights=0), dict(weights_out=0), dict(seqlens_k=0),
                dict(seqlens_out=0), dict(block_table=0), dict(B=0), dict(Hkv=0), dict(budget=0), dict(sinks=-1),
                dict(recent=-1), dict(sinks=30, recent=3), dict(page_size=0)]),
-    (UNSUPPORTED, [dict(d=80), dict(budget=(1 << 30) + 1), dict(num_pages=1 << 29, page_size=16)]),
+    (UNSUPPORTED, [dict(d=80), dict(budget=(1 << 30) + 1), dict(num_pages=1 << 29, page_size=16),
+                   dict(num_pages=1 << 26, Hkv=16), dict(max_pages=1 << 25, Hkv=8)]),
     (MISALIGNED, [dict(k_cache=M + 8), dict(weights=3 * M + 2), dict(seqlens_out=6 * M + 1)]),
     (ALIAS, [dict(v_cache=M), dict(weights_out=3 * M + 64), dict(weights=M), dict(seqlens_out=5 * M + 4),
              dict(weights_out=2 * M)]),

@@ -129,3 +129,43 @@ def test_the_loop_as_a_graph(attn):
     for a, b in zip(eager.state(), graphed.state()):
         assert torch.equal(a, b)
     assert attn.cache_device_status() == (0, 0)
+
+
+def test_caches_past_four_gigabytes(attn):
+    """Pages whose byte offsets pass 2^32: append, attend and evict there as in a small cache of the same pages."""
+    B, H, Hkv, d, ps, n = 2, 8, 8, 128, 128, 300
+    pages = 2 ** 32 // (ps * Hkv * d * 2) + 8                       # 4 GiB of keys and eight pages
+    g = torch.Generator("cuda").manual_seed(3)
+    far = torch.tensor([[pages - 1, 1, pages - 4], [pages - 2, pages - 3, 0]], dtype=torch.int32, device="cuda")
+    near = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32, device="cuda")
+    x = torch.randn((B * n, H + 2 * Hkv, d), generator=g, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    w = torch.rand((B, Hkv, 3 * ps), generator=g, device="cuda")
+    out = []
+    for table, count in ((near, 6), (far, pages)):
+        kc, vc = (torch.empty((count, ps, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lens, weights = torch.full((B,), n, dtype=torch.int32, device="cuda"), w.clone()
+        attn.attn_paged_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, cu, lens, table)
+        q = x[:B, :H].contiguous()
+        o = attn.attn_paged_decode(q, kc, vc, lens, table, weights=weights)
+        attn.attn_paged_evict(kc, vc, weights, lens, table, 200, sinks=3, recent=50)
+        o2 = attn.attn_paged_decode(q, kc, vc, lens, table)
+        out.append((o, o2, weights, lens, kc[table.long()].flatten(1, 2)[:, :200], vc[table.long()].flatten(1, 2)[:, :200]))
+        del kc, vc
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    assert attn.cache_device_status() == (0, 0)
+
+
+def test_rotary_positions_of_a_tensor_past_two_to_the_31_elements(attn):
+    S, H, d = 131080, 128, 128
+    freqs, axes = attn.rope_freqs((128,))
+    q = torch.empty((1, S, H, d), dtype=torch.bfloat16, device="cuda")
+    assert q.numel() > 2 ** 31
+    q[:, -4:].normal_()
+    positions = torch.arange(S, dtype=torch.int32, device="cuda")[None]
+    tail = q[:, -4:].clone()
+    attn.attn_rope(q, None, positions, freqs, axes, q_out=q)
+    want = attn.attn_rope(tail, None, positions[:, -4:], freqs, axes)
+    assert torch.equal(q[:, -4:], want)
+    assert attn.cache_device_status() == (0, 0)

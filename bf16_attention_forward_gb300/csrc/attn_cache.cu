@@ -474,7 +474,7 @@ int check_evict_shape(const attn_evict_args_t& a) {
 }
 
 struct EvictLayout {
-    size_t uses, cut, lens, total, fill, fill_w, bytes;
+    size_t uses, cut, lens, total, list, each, bytes;
     int64_t most_moves;
 };
 EvictLayout evict_layout(const attn_evict_args_t& a) {
@@ -486,9 +486,9 @@ EvictLayout evict_layout(const attn_evict_args_t& a) {
     l.cut = align256((size_t)a.num_pages * 4);
     l.lens = l.cut + align256((size_t)a.B * 4);
     l.total = l.lens + align256((size_t)a.B * 4);
-    l.fill = l.total + 256;
-    l.fill_w = l.fill + align256(all * 8);
-    l.bytes = l.fill_w + all * 8;
+    l.list = l.total + 256;
+    l.each = align256(all * 4);
+    l.bytes = l.list + 4 * l.each;
     return l;
 }
 
@@ -537,8 +537,10 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     p.cut = reinterpret_cast<int32_t*>(ws + l.cut);
     p.lens = reinterpret_cast<int32_t*>(ws + l.lens);
     p.total = reinterpret_cast<int32_t*>(ws + l.total);
-    p.fill = reinterpret_cast<int2*>(ws + l.fill);
-    p.fill_w = reinterpret_cast<uint2*>(ws + l.fill_w);
+    p.to = reinterpret_cast<int32_t*>(ws + l.list);
+    p.from = reinterpret_cast<int32_t*>(ws + l.list + l.each);
+    p.w_to = reinterpret_cast<uint32_t*>(ws + l.list + 2 * l.each);
+    p.w_from = reinterpret_cast<uint32_t*>(ws + l.list + 3 * l.each);
     const int64_t rows = a.B * a.Hkv, room = a.max_pages * a.page_size;
     // select: the CTAs of a row hold its keys in registers where 8 of 1024 threads can (else the keys are read again for
     // each pass), and more of them share a row while every CTA has an SM and 2048 keys

@@ -49,8 +49,8 @@ struct EvictParams {
     int32_t* cut;              // [B]: the length n of a sequence that is cut, -1 - n of one that fits, 0: refused
     int32_t* lens;             // [B]: lengths after the call (seqlens_out may be seqlens_k, which the select kernel reads)
     int32_t* total;            // moves on the fill list
-    int2* fill;                // [B * Hkv * most_moves]: (to, from) as rows of [cache rows * Hkv]
-    uint2* fill_w;             // the same as elements of weights
+    int32_t *to, *from;        // [B * Hkv * most_moves]: rows of [cache rows * Hkv]
+    uint32_t *w_to, *w_from;   // the same as elements of weights
 };
 
 constexpr int kPrepThreads = 1024;
@@ -444,8 +444,6 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
     }
     if (C > 1) cluster_sync(); else __syncthreads();
     const int start = kWhole ? 0 : C > 1 ? cluster_ld(cluster_map(ptx::smem_u32(&start_s), 0)) : start_s;
-    int2* fill = p.fill + start;
-    uint2* fill_w = p.fill_w + start;
     int* const list = pool[2];                         // kWhole: freed slots, then the survivors that fill them
     const uint32_t w0 = (uint32_t)(bh * room);
     seen = ties;
@@ -485,13 +483,8 @@ __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __
                     const int i = at + e0 + 32 * u;
                     if (e0 + 32 * u >= m) continue;
                     const uint32_t we = w0 + (uint32_t)j[u];
-                    if (i < moves) {
-                        fill[i].x = row[u];
-                        fill_w[i].x = we;
-                    } else {
-                        fill[i - moves].y = row[u];
-                        fill_w[i - moves].y = we;
-                    }
+                    (i < moves ? p.to + start : p.from + start - moves)[i] = row[u];
+                    (i < moves ? p.w_to + start : p.w_from + start - moves)[i] = we;
                 }
             }
             at += m;
@@ -539,21 +532,21 @@ __global__ void __launch_bounds__(kFillThreads, 4) attn_evict_fill_kernel(const 
     const int sub = (lane % 16) / kLanes;
     for (long long m = (long long)(blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5)) * kU * kPer; m < total;
          m += (long long)warps * kU * kPer) {
-        int2 mv = make_int2(0, 0);
+        int to = 0, from = 0;
         if (lane < kU * kPer && m + lane < total) {
-            mv = p.fill[m + lane];
-            const uint2 we = p.fill_w[m + lane];
-            p.weights_out[we.x] = p.weights[we.y];
+            to = p.to[m + lane];
+            from = p.from[m + lane];
+            p.weights_out[p.w_to[m + lane]] = p.weights[p.w_from[m + lane]];
         }
         uint4 x[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int src = __shfl_sync(0xFFFFFFFFu, mv.y, u * kPer + sub);
+            const int src = __shfl_sync(0xFFFFFFFFu, from, u * kPer + sub);
             if (m + u * kPer + sub < total) x[u] = *reinterpret_cast<const uint4*>(base + (long long)src * (2 * D));
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int dst = __shfl_sync(0xFFFFFFFFu, mv.x, u * kPer + sub);
+            const int dst = __shfl_sync(0xFFFFFFFFu, to, u * kPer + sub);
             if (m + u * kPer + sub < total) *reinterpret_cast<uint4*>(base + (long long)dst * (2 * D)) = x[u];
         }
     }

@@ -975,7 +975,8 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
                                         ("weights", 0 if weights is None else 16))
             if ws_bytes:
                 workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        st = (_lib or load()).attn_paged_decode(a, workspace.data_ptr() if ws_bytes else None, ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+        st = (_lib or load()).attn_paged_decode(a, workspace.data_ptr() if ws_bytes else None, ws_bytes,
+                                                torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise AttnError(st, "attn_paged_decode")
     finally:
@@ -1021,7 +1022,8 @@ def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: 
                                         ("page_size", ps), ("max_pages", most), ("d", d), ("budget", budget),
                                         ("sinks", sinks), ("recent", recent))
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=k_cache.device)
-        st = (_lib or load()).attn_paged_evict(a, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+        st = (_lib or load()).attn_paged_evict(a, workspace.data_ptr(), ws_bytes,
+                                               torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise AttnError(st, "attn_paged_evict")
     finally:

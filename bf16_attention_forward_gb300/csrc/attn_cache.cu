@@ -244,11 +244,14 @@ int run_rope(const attn_rope_args_t& a, cudaStream_t stream) {
     int st = check_pairs(a.pairs, a.num_axes, a.pairing, head_dim(a.d) ? a.d : 128);
     if (st != ATTN_OK) return st;
     if (!head_dim(a.d)) return ATTN_ERR_UNSUPPORTED;
-    if (a.B > kLim || a.S > kLim || a.H > kLim || Hkv > kLim || a.B * a.S > kLim || a.H + Hkv > kLim) return ATTN_ERR_UNSUPPORTED;
-    const int64_t nq[3] = {a.B, a.S, a.H}, nk[3] = {a.B, a.S, Hkv}, np[2] = {a.num_axes, a.B}, ps[2] = {a.pos_axis_stride, a.pos_batch_stride};
+    if (a.B > kLim || a.S > kLim || a.H > kLim || Hkv > kLim || a.B * a.S > kLim || a.H + Hkv > kLim)
+        return ATTN_ERR_UNSUPPORTED;
+    const int64_t nq[3] = {a.B, a.S, a.H}, nk[3] = {a.B, a.S, Hkv};
+    const int64_t np[2] = {a.num_axes, a.B}, ps[2] = {a.pos_axis_stride, a.pos_batch_stride};
     if (!strides_ok(a.q_stride, nq, 3) || !strides_ok(a.q_out_stride, nq, 3) || !strides_ok(ps, np, 2)) return ATTN_ERR_INVALID_ARG;
     if (a.k && (!strides_ok(a.k_stride, nk, 3) || !strides_ok(a.k_out_stride, nk, 3))) return ATTN_ERR_INVALID_ARG;
-    if (((uintptr_t)a.q | (uintptr_t)a.q_out | (uintptr_t)a.k | (a.k ? (uintptr_t)a.k_out : 0)) & 15u) return ATTN_ERR_MISALIGNED;
+    if (((uintptr_t)a.q | (uintptr_t)a.q_out | (uintptr_t)a.k | (a.k ? (uintptr_t)a.k_out : 0)) & 15u)
+        return ATTN_ERR_MISALIGNED;
     if (((uintptr_t)a.positions | (uintptr_t)a.axes) & 3u || (uintptr_t)a.freqs & 7u) return ATTN_ERR_MISALIGNED;
     if (!strides_aligned(a.q_stride, nq, 3) || !strides_aligned(a.q_out_stride, nq, 3)) return ATTN_ERR_MISALIGNED;
     if (a.k && (!strides_aligned(a.k_stride, nk, 3) || !strides_aligned(a.k_out_stride, nk, 3))) return ATTN_ERR_MISALIGNED;
@@ -287,17 +290,21 @@ int run_append(const attn_append_args_t& a, cudaStream_t stream) {
     if (a.pairs != 0 && (!a.positions || !a.freqs || !a.axes)) return ATTN_ERR_INVALID_ARG;
     int st = check_cache(a.B, a.Hkv, a.num_pages, a.page_size, a.max_pages, a.d);
     if (st != ATTN_OK) return st;
-    if (a.total < 0 || (a.q && H < 1) || a.reserved != 0 || a.pos_axis_stride < 0 || a.pos_axis_stride > ((int64_t)1 << 40)) return ATTN_ERR_INVALID_ARG;
+    if (a.total < 0 || (a.q && H < 1) || a.reserved != 0 || a.pos_axis_stride < 0 ||
+        a.pos_axis_stride > ((int64_t)1 << 40))
+        return ATTN_ERR_INVALID_ARG;
     if (a.pairs != 0 && (st = check_pairs(a.pairs, a.num_axes, a.pairing, a.d)) != ATTN_OK) return st;
     if (a.total > kLim || H > kLim || H + 2 * a.Hkv > kLim) return ATTN_ERR_UNSUPPORTED;
     const int64_t nk[2] = {a.total, a.Hkv}, nq[2] = {a.total, H};
-    if (!strides_ok(a.k_stride, nk, 2) || !strides_ok(a.v_stride, nk, 2) || (a.q && !strides_ok(a.q_stride, nq, 2))) return ATTN_ERR_INVALID_ARG;
+    if (!strides_ok(a.k_stride, nk, 2) || !strides_ok(a.v_stride, nk, 2) || (a.q && !strides_ok(a.q_stride, nq, 2)))
+        return ATTN_ERR_INVALID_ARG;
     if (((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache | (uintptr_t)a.q |
          (a.q ? (uintptr_t)a.q_out : 0)) & 15u)
         return ATTN_ERR_MISALIGNED;
     if (((uintptr_t)a.cu_seqlens_new | (uintptr_t)a.seqlens_k | (uintptr_t)a.block_table) & 3u) return ATTN_ERR_MISALIGNED;
     if (a.pairs && (((uintptr_t)a.positions | (uintptr_t)a.axes) & 3u || (uintptr_t)a.freqs & 7u)) return ATTN_ERR_MISALIGNED;
-    if (!strides_aligned(a.k_stride, nk, 2) || !strides_aligned(a.v_stride, nk, 2) || (a.q && !strides_aligned(a.q_stride, nq, 2)))
+    if (!strides_aligned(a.k_stride, nk, 2) || !strides_aligned(a.v_stride, nk, 2) ||
+        (a.q && !strides_aligned(a.q_stride, nq, 2)))
         return ATTN_ERR_MISALIGNED;
     auto v = [&](const void* p, int64_t heads, const int64_t* s) { return view(p, 1, a.total, heads, a.d, 0, s[0], s[1]); };
     const int64_t dense[2] = {H * a.d, a.d}, cs[2] = {a.Hkv * a.d, a.d};
@@ -387,7 +394,8 @@ int launch_decode(const DecodeParams& p, cudaStream_t stream) {
     int st;
     // the weights' blocks: three an SM, beside one that joins
     if (p.weights) {
-        if ((st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p)) != ATTN_OK) return st;
+        st = launch(attn_decode_kernel<D, NH, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
+        if (st != ATTN_OK) return st;
         return launch(attn_decode_join_kernel<D, NH, true>, 4 * p.grid, 1, 256, 0, stream, p);
     }
     st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
@@ -400,7 +408,8 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     if (st != ATTN_OK) return st;
     if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.seqlens_k || !a.block_table) return ATTN_ERR_INVALID_ARG;
     if (((uintptr_t)a.q | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache | (uintptr_t)a.o) & 15u) return ATTN_ERR_MISALIGNED;
-    if (((uintptr_t)a.lse | (uintptr_t)a.weights | (uintptr_t)a.seqlens_k | (uintptr_t)a.block_table) & 3u) return ATTN_ERR_MISALIGNED;
+    if (((uintptr_t)a.lse | (uintptr_t)a.weights | (uintptr_t)a.seqlens_k | (uintptr_t)a.block_table) & 3u)
+        return ATTN_ERR_MISALIGNED;
     const uintptr_t cb = (uintptr_t)(a.num_pages * a.page_size * a.Hkv * a.d * 2), qb = (uintptr_t)(a.B * a.H * a.d * 2);
     const uintptr_t wb = (uintptr_t)(a.B * a.Hkv) * (uintptr_t)(a.max_pages * a.page_size) * 4;
     struct { uintptr_t at, bytes; } in[] = {{(uintptr_t)a.q, qb}, {(uintptr_t)a.k_cache, cb}, {(uintptr_t)a.v_cache, cb},
@@ -423,7 +432,8 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
             for (const auto& x : in)
                 if (overlap(out[i].at, out[i].at + out[i].bytes, x.at, x.at + x.bytes)) return ATTN_ERR_ALIAS;
             for (int j = 0; j < i; ++j)
-                if (out[j].bytes && overlap(out[i].at, out[i].at + out[i].bytes, out[j].at, out[j].at + out[j].bytes)) return ATTN_ERR_ALIAS;
+                if (out[j].bytes && overlap(out[i].at, out[i].at + out[i].bytes, out[j].at, out[j].at + out[j].bytes))
+                    return ATTN_ERR_ALIAS;
         }
     }
     const DecodeLayout l = decode_layout(a, sms);
@@ -455,8 +465,13 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     p.row_ml = reinterpret_cast<float2*>(ws + l.row_ml);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     p.score_room = score_room(a);
-    if (a.d == 128) return nh == 1 ? launch_decode<128, 1>(p, stream) : nh == 2 ? launch_decode<128, 2>(p, stream) : launch_decode<128, 4>(p, stream);
-    return nh == 1 ? launch_decode<64, 1>(p, stream) : nh == 2 ? launch_decode<64, 2>(p, stream) : launch_decode<64, 4>(p, stream);
+    if (a.d == 128)
+        return nh == 1   ? launch_decode<128, 1>(p, stream)
+               : nh == 2 ? launch_decode<128, 2>(p, stream)
+                         : launch_decode<128, 4>(p, stream);
+    return nh == 1   ? launch_decode<64, 1>(p, stream)
+           : nh == 2 ? launch_decode<64, 2>(p, stream)
+                     : launch_decode<64, 4>(p, stream);
 }
 
 // ------------------------------------------------------------------------------ evict
@@ -512,7 +527,8 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
                          {(uintptr_t)workspace, workspace ? l.bytes : 0}};
     for (const Range& x : all)
         for (const Range& y : all)
-            if (&x != &y && x.bytes && y.bytes && overlap(x.at, x.at + x.bytes, y.at, y.at + y.bytes)) return ATTN_ERR_ALIAS;
+            if (&x != &y && x.bytes && y.bytes && overlap(x.at, x.at + x.bytes, y.at, y.at + y.bytes))
+                return ATTN_ERR_ALIAS;
     if (!workspace || workspace_bytes < l.bytes) return ATTN_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 15u) return ATTN_ERR_MISALIGNED;
     int sms = 0;

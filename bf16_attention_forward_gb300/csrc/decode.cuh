@@ -16,8 +16,9 @@
 // one line, which the CTAs divide evenly: a CTA takes a contiguous range, so every CTA
 // reads the same bytes whatever the lengths are, and a row is split only where a range
 // ends inside it.  Behind each row's tiles the line has one more place, which stands for the row's
-// end (loading its queries and joining the warps take about as long as a tile).  Each warp streams 16 keys of a tile through a ring of its own (cp.async, no
-// barrier between warps) and keeps its own m, l and o; the warps are joined at the end of a row.
+// end (loading its queries and joining the warps take about as long as a tile).  Each warp streams 16 keys
+// of a tile through a ring of its own (cp.async, no barrier between warps) and keeps its own m, l and o; the
+// warps are joined at the end of a row.
 // Keys and values are read once and leave the L2 first: the logits kept for the weights stay there until
 // the join has read them (24 caches of 250,000 keys: 178 -> 171 us), and of caches near the L2's size a part stays for
 // the next step (4 caches, 181 MB: 35.5 -> 33.8 us).
@@ -614,11 +615,13 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                 // four neighbouring keys a thread: 16-byte loads (4-byte ones left the loop at 2.5 TB/s)
 #pragma unroll 1
                 for (int j0 = cur.tile * kDecTile + threadIdx.x * 4; j0 < j1; j0 += 1024) {
-                    const float* s = p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * p.score_room + j0;
+                    const float* s =
+                        p.scores + ((long long)cur.b * p.H + (long long)cur.row * p.group + g0) * p.score_room + j0;
                     float4 x[kG], w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int g = 0; g < kG; ++g)
-                        if (g0 + g < p.group) x[g] = ld_policy(reinterpret_cast<const float4*>(s + g * p.score_room), done_policy);
+                        if (g0 + g < p.group)
+                            x[g] = ld_policy(reinterpret_cast<const float4*>(s + g * p.score_room), done_policy);
                     if (vector) {
                         w = *reinterpret_cast<const float4*>(out + j0);
                     } else {
@@ -633,7 +636,9 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
                         if (g0 + g >= p.group) continue;
                         const float2 ml = ml_s[g];
                         // (-inf logits weigh nothing, but in a row of nothing else, which is NaN: 0 / 0)
-                        auto weight = [&](float v) { return (v == -INFINITY ? 0.0f : ptx::ex2_approx((v - ml.x) * p.scale_log2)) * ml.y; };
+                        auto weight = [&](float v) {
+                            return (v == -INFINITY ? 0.0f : ptx::ex2_approx((v - ml.x) * p.scale_log2)) * ml.y;
+                        };
                         sum.x += weight(x[g].x);
                         sum.y += weight(x[g].y);
                         sum.z += weight(x[g].z);

@@ -316,3 +316,28 @@ def test_two_streams_with_workspaces_of_their_own_and_a_graph(attn):
     for o, lse in kept:
         assert torch.equal(o.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, wl)
     status_ok(attn)
+
+
+def test_what_the_binding_refuses(attn):
+    q, k, v = packed(2, 20, 4, 2, 64, seed=91)
+    kc, vc, table = build_cache(k, v, [10, 10], 16, seed=92)
+    q, kc, vc, n, t = q.cuda(), kc.cuda(), vc.cuda(), cuda([10, 10]), cuda(table)
+    room = table.shape[1] * 16
+    w = torch.zeros((2, 2, room), device="cuda")
+    call = attn.attn_paged_decode
+    for f, error in (
+            (lambda: call(q.float(), kc, vc, n, t), TypeError),
+            (lambda: call(q[:1].contiguous(), kc, vc, n, t), ValueError),
+            (lambda: call(q[:, :3].contiguous(), kc, vc, n, t), ValueError),
+            (lambda: call(q[:, :, :32].contiguous(), kc, vc, n, t), ValueError),
+            (lambda: call(q.transpose(0, 1), kc, vc, n, t), ValueError),
+            (lambda: call(q, kc, vc[:1], n, t), ValueError),
+            (lambda: call(q, kc, vc, n.long(), t), TypeError),
+            (lambda: call(q, kc, vc, n, t, round="up"), ValueError),
+            (lambda: call(q, kc, vc, n, t, weights=w[:, :1].contiguous()), ValueError),
+            (lambda: call(q, kc, vc, n, t, lse=torch.zeros((4, 2), device="cuda")), ValueError),
+            (lambda: call(q, kc, vc, n, t, o=q), attn.AttnError),
+            (lambda: call(q, kc, vc, n, t, weights=w, workspace=torch.empty(64, device="cuda")), attn.AttnError)):
+        with pytest.raises(error):
+            f()
+    status_ok(attn)

@@ -202,6 +202,48 @@ def test_bad_and_shared_sequences_stay(attn):
     status_ok(attn)
 
 
+def test_refused_sequences_leave_the_outputs_of_their_own_alone(attn):
+    kc, vc, table = cache([100, 110, 30], 8, 16, 2, 64, 15)
+    table = table.copy()
+    table[1, 2] = kc.shape[0] + 5
+    w = torch.rand((3, 2, 128), generator=torch.Generator().manual_seed(1)).cuda()
+    wo, lo = torch.full_like(w, -5.0), torch.full((3,), -5, dtype=torch.int32, device="cuda")
+    k, v, lens = kc.cuda(), vc.cuda(), torch.tensor([100, 110, 30], dtype=torch.int32, device="cuda")
+    keep = [t.clone() for t in (k, v, w, lens)]
+    for recent in (8, 0):              # (the second time the kept rows have moved already; the refused ones never)
+        attn.attn_paged_evict(k, v, w, lens, torch.as_tensor(table).cuda(), 64, sinks=4, recent=recent, weights_out=wo,
+                              seqlens_out=lo)
+        assert attn.cache_device_status() == (1, 23)
+        assert lo.tolist() == [64, 110, 30] and torch.equal(w, keep[2]) and torch.equal(lens, keep[3])
+        assert (wo[1] == -5.0).all() and torch.equal(wo[2, :, :30], w[2, :, :30]) and (wo[2, :, 30:] == -5.0).all()
+        own = [p for p in table[1] if p < kc.shape[0]]
+        for t, old in ((k, keep[0]), (v, keep[1])):
+            assert torch.equal(t[own].view(torch.int16), old[own].view(torch.int16))
+
+
+def test_what_the_binding_refuses(attn):
+    kc, vc, table = cache([20], 2, 16, 2, 64, 3)
+    k, v, t = kc.cuda(), vc.cuda(), torch.as_tensor(table).cuda()
+    w, n = torch.zeros((1, 2, 32), device="cuda"), torch.tensor([20], dtype=torch.int32, device="cuda")
+    evict = attn.attn_paged_evict
+    for call, error in (
+            (lambda: evict(k, v[:2], w, n, t, 8), ValueError),
+            (lambda: evict(k, v, w[:, :, :31].contiguous(), n, t, 8), ValueError),
+            (lambda: evict(k, v, w.half(), n, t, 8), TypeError),
+            (lambda: evict(k, v, w, n.long(), t, 8), TypeError),
+            (lambda: evict(k, v, w, torch.cat([n, n]), t, 8), ValueError),
+            (lambda: evict(k, v, w, n, t, 8, seqlens_out=torch.cat([n, n])), ValueError),
+            (lambda: evict(k.transpose(1, 2), v.transpose(1, 2), w, n, t, 8), ValueError),
+            (lambda: evict(k, k, w, n, t, 8), attn.AttnError),
+            (lambda: evict(k, v, w, n, t, 0), attn.AttnError),
+            (lambda: evict(k, v, w, n, t, 8, sinks=5, recent=4), attn.AttnError),
+            (lambda: evict(k, v, w, n, t, 8, workspace=torch.empty(16, device="cuda")), attn.AttnError)):
+        with pytest.raises(error):
+            call()
+    assert n.item() == 20
+    status_ok(attn)
+
+
 def test_guards(attn):
     lens, most, P, Hkv, d, budget = [300, 77], 20, 16, 3, 64, 100
     kc, vc, table = cache(lens, most, P, Hkv, d, 7)

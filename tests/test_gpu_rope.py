@@ -146,6 +146,53 @@ def test_views_of_a_projection_and_in_place(attn, layout):
     status_ok(attn)
 
 
+def test_one_token_a_sequence_in_place_and_a_shared_input(attn):
+    B, H, Hkv, d = 3, 4, 2, 64
+    freqs, axes = attn.rope_freqs((64,))
+    positions = torch.tensor([[[5], [900], [77]]], dtype=torch.int32, device="cuda")       # [axes, B, 1]
+    x = draw(B, 1, H + 2 * Hkv, d, seed=8)
+    keep = x.clone()
+    q, k = x[:, :, :H], x[:, :, H:H + Hkv]
+    want = attn.attn_rope(q, k, positions, freqs, axes)
+    check(want[0], keep[:, :, :H], positions, freqs, axes, "adjacent")
+    attn.attn_rope(q, k, positions, freqs, axes, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(x[:, :, H + Hkv:], keep[:, :, H + Hkv:])
+    # one row of queries for every sequence (a stride of zero)
+    one = draw(1, 1, H, d, seed=9)
+    got = attn.attn_rope(one.expand(B, 1, H, d), None, positions, freqs, axes)
+    assert torch.equal(got, attn.attn_rope(one.expand(B, 1, H, d).contiguous(), None, positions, freqs, axes))
+    status_ok(attn)
+
+
+def test_what_the_binding_refuses(attn):
+    freqs, axes = attn.rope_freqs((64,))
+    q, k, pos = draw(1, 6, 4, 64), draw(1, 6, 2, 64), torch.zeros((1, 6), dtype=torch.int32, device="cuda")
+    rope = attn.attn_rope
+    for call, error in (
+            (lambda: rope(q.float(), k, pos, freqs, axes), TypeError),
+            (lambda: rope(q.cpu(), k, pos, freqs, axes), TypeError),
+            (lambda: rope(q, k.cpu(), pos, freqs, axes), TypeError),
+            (lambda: rope(q, k, pos.long(), freqs, axes), TypeError),
+            (lambda: rope(q, k, pos, freqs.float(), axes), TypeError),
+            (lambda: rope(q, k, pos, freqs, axes[:5]), ValueError),
+            (lambda: rope(q, k, pos[:, :5], freqs, axes), ValueError),
+            (lambda: rope(q, k[:, :5], pos, freqs, axes), ValueError),
+            (lambda: rope(q, k, pos, freqs, axes, layout="sbhd"), ValueError),
+            (lambda: rope(q, k, pos, freqs, axes, pairing="both"), ValueError),
+            (lambda: rope(q, k, pos, freqs, axes, q_out=q[:, :5]), ValueError),
+            (lambda: rope(q, None, pos, freqs, axes, k_out=k), ValueError),
+            (lambda: rope(q.transpose(2, 3), k, pos, freqs, axes), ValueError),
+            (lambda: rope(q, k, pos, freqs, axes, q_out=k.expand_as(k), k_out=q), ValueError),
+            (lambda: rope(draw(1, 6, 4, 96), None, pos, freqs, axes), attn.AttnError),
+            (lambda: rope(q, k, pos, torch.ones(40, dtype=torch.float64, device="cuda"),
+                          torch.zeros(40, dtype=torch.int32, device="cuda")), attn.AttnError),
+            (lambda: rope(q, k, pos, freqs[:12], axes[:12], pairing="halves"), attn.AttnError),
+            (lambda: rope(q[:, :4], None, pos[:, :4], freqs, axes, q_out=q[:, 1:5]), attn.AttnError)):
+        with pytest.raises(error):
+            call()
+    status_ok(attn)
+
+
 def test_non_finite_elements_stay_in_their_pair_and_the_rest_keeps_its_bits(attn):
     freqs, axes = attn.rope_freqs((32,))
     q = torch.zeros((1, 3, 1, 64), dtype=torch.bfloat16, device="cuda")

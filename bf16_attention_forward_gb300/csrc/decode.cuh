@@ -7,21 +7,22 @@
 // of each key, summed over the query heads of its K/V head, is added to a running fp32 weight.
 //
 // Bound: HBM bytes; every key and value is read once (2 * d * 2 bytes for 4 * d * G flops, G =
-// H / Hkv query heads).  64 caches, 2.7 GB of keys and values: 383 us, 6.9 TB/s, the tensor pipe 10 % busy.  The products run on mma.sync with the KEYS as the M rows and the
-// query heads as the N columns (S^T = K Q^T, O^T = V^T P^T): N is 8, so a K/V head's 4 to 8 query
-// heads waste at most half of it.  tcgen05 would need 128 rows of one operand and a trip through
-// TMEM for a product that takes a few percent of the time.
+// H / Hkv query heads).  64 caches, 2.7 GB of keys and values: 383 us, 6.9 TB/s, the tensor pipe
+// 10 % busy.  The products run on mma.sync with the KEYS as the M rows and the query heads as the
+// N columns (S^T = K Q^T, O^T = V^T P^T): N is 8, so a K/V head's 4 to 8 query heads waste at most
+// half of it.  tcgen05 would need 128 rows of one operand and a trip through TMEM for a product
+// that takes a few percent of the time.
 //
 // Work.  A CTA of 8 warps per SM.  The tiles (128 keys) of all (sequence, K/V head) rows form
-// one line, which the CTAs divide evenly: a CTA takes a contiguous range, so every CTA
-// reads the same bytes whatever the lengths are, and a row is split only where a range
-// ends inside it.  Behind each row's tiles the line has one more place, which stands for the row's
-// end (loading its queries and joining the warps take about as long as a tile).  Each warp streams 16 keys
-// of a tile through a ring of its own (cp.async, no barrier between warps) and keeps its own m, l and o; the
+// one line, which the CTAs divide evenly: a CTA takes a contiguous range, so every CTA reads the
+// same bytes whatever the lengths are, and a row is split only where a range ends inside it.
+// Behind each row's tiles the line has one more place, which stands for the row's end (loading its
+// queries and joining the warps take about as long as a tile).  Each warp streams 16 keys of a tile
+// through a ring of its own (cp.async, no barrier between warps) and keeps its own m, l and o; the
 // warps are joined at the end of a row.
-// Keys and values are read once and leave the L2 first: the logits kept for the weights stay there until
-// the join has read them (24 caches of 250,000 keys: 178 -> 171 us), and of caches near the L2's size a part stays for
-// the next step (4 caches, 181 MB: 35.5 -> 33.8 us).
+// Keys and values are read once and leave the L2 first: the logits kept for the weights stay there
+// until the join has read them (24 caches, 240,000 keys: 178 -> 171 us), and of caches near the
+// L2's size a part stays for the next step (4 caches, 181 MB: 35.5 -> 33.8 us).
 // A range holds at most one part that begins before it and one that ends behind it, so two part
 // slots per CTA suffice.  A few short rows go to a CTA each instead: one launch, no parts.
 // attn_decode_join_kernel merges a split row's parts, and beside that adds the

@@ -9,8 +9,9 @@
 // kernel keeps freq / 2pi as a 64-bit binary fraction of a turn; an integer position times it,
 // modulo 2^64, is the fraction of a turn (whole turns drop out of the high end), exact
 // but for the fraction's own last bit: pos * 2^-64 turns, and pos * 2^-53 relative to the
-// frequency from its fp64 value.  The top 32 bits of the product, read as a signed number of
-// half turns in [-1, 1), go to sincospi.
+// frequency from its fp64 value.  The product, read as a signed number of half turns in [-1, 1)
+// and rounded to fp32 as a whole (its upper 32 bits alone would leave an angle of 10^-7 rad 1 % off),
+// goes to sincospi.
 //
 // Bound: HBM bytes (each element read and written once).  A warp takes a token: it computes each angle
 // once, into shared memory; a thread then holds the cosines and sines of 16 elements and applies
@@ -147,9 +148,9 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
 #pragma unroll 1
         for (int pr = lane; pr < p.pairs; pr += 32) {
             const long long pos = __ldg(p.positions + axis[pr] * p.pos_axis + b * p.pos_b + s);
-            const unsigned long long at = turn[pr] * (unsigned long long)pos;
+            const long long at = (long long)(turn[pr] * (unsigned long long)pos);
             float sn, c;
-            sincospif((float)(int)(at >> 32) * 0x1p-31f, &sn, &c);
+            sincospif((float)at * 0x1p-63f, &sn, &c);
             cs[warp][pr] = make_float2(c, p.inverse ? -sn : sn);
         }
         __syncwarp();

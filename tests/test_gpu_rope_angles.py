@@ -1,0 +1,67 @@
+"""Angles of attn_rope and attn_paged_append where they show: small ones beside a partner of zero (needs a GB300).
+
+Tolerances.  An element x0 cos - x1 sin is rounded once to bf16, half a step, 2^-8 of itself.  Before that, in
+fp32: the angle in half turns is rounded once (2^-24 of itself; at most pi 2^-25 rad), cosine and sine are off by
+2^-23 of themselves at most, two products and their difference by 2^-24 each.  With one product zero all of
+these are relative to the result, below 2^-21 together; in general they are below 2^-21 (|x0| + |x1|).  The
+frequency's fraction of a turn is off by two units of 2^-64 at most, which a position p multiplies: below
+2^-32 turns, 2^-29 rad, of an angle of any size, and 2^-30 of the smallest angles below.
+"""
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+# 1 / 2 pi to 60 digits
+TURN = Fraction(159154943091895335768883763372514362034459645740456448747667, 10 ** 60)
+
+
+@pytest.fixture(scope="module")
+def attn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import bf16_attention_forward_gb300 as a
+    a.load()
+    return a
+
+
+def angle(position, freq):
+    """position * freq in radians, whole turns taken off exactly, -pi .. pi."""
+    turns = position * Fraction(freq) * TURN
+    return float((turns - round(turns)) / TURN)
+
+
+def rotated(positions, freqs):
+    """Cosines and sines [tokens, pairs] in 64 bits."""
+    a = np.array([[angle(p, f) for f in freqs] for p in positions])
+    return np.cos(a), np.sin(a)
+
+
+@pytest.mark.parametrize("base", [1e4, 5e5, 1e7, 1e9])
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+def test_small_angles_beside_a_partner_of_zero(attn, base, pairing):
+    d, positions = 128, [0, 1, -1, 2, 3, -5, 7, 10, 33, 64, 100, 1000, -4095, 100000]
+    freqs, axes = attn.rope_freqs((d,), base=base)
+    pos = torch.tensor([positions], dtype=torch.int32, device="cuda")
+    q = torch.zeros((1, len(positions), 2, d), dtype=torch.bfloat16, device="cuda")
+    first, second = (slice(0, None, 2), slice(1, None, 2)) if pairing == "adjacent" else (slice(0, 64), slice(64, None))
+    q[:, :, 0, first] = 1.0            # head 0: (1, 0), head 1: (0, 1.5)
+    q[:, :, 1, second] = 1.5
+    c, s = rotated(positions, freqs.tolist())
+    want = np.zeros((len(positions), 2, d))
+    want[:, 0, first], want[:, 0, second] = c, s
+    want[:, 1, first], want[:, 1, second] = -1.5 * s, 1.5 * c
+    back = want.copy()
+    back[:, 0, second], back[:, 1, first] = -s, 1.5 * s
+    kc, vc = (torch.empty((1, len(positions), 2, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n = torch.tensor([0, len(positions)], dtype=torch.int32, device="cuda")
+    attn.attn_paged_append(q[0], q[0], kc, vc, n, n[1:], torch.zeros((1, 1), dtype=torch.int32, device="cuda"),
+                           positions=pos, freqs=freqs, axes=axes, pairing=pairing)
+    for got, ref in ((attn.attn_rope(q, None, pos, freqs, axes, pairing=pairing), want), (kc, want),
+                     (attn.attn_rope(q, None, pos, freqs, axes, pairing=pairing, inverse=True), back)):
+        off = np.abs(got[0].float().cpu().numpy().astype(np.float64) - ref) - (2.0 ** -8 + 2.0 ** -21) * np.abs(ref)
+        assert np.all(off <= 0), (float(off.max()), np.argwhere(off > 0)[:4])
+    assert attn.cache_device_status() == (0, 0)

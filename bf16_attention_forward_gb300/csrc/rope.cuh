@@ -8,10 +8,9 @@
 // Angles.  Positions reach 2^31, where pos * freq in fp32 has no correct digit left.  The
 // kernel keeps freq / 2pi as a 64-bit binary fraction of a turn; an integer position times it,
 // modulo 2^64, is the fraction of a turn (whole turns drop out of the high end), exact
-// but for the fraction's own last bit: pos * 2^-64 turns, and pos * 2^-53 relative to the
-// frequency from its fp64 value.  The product, read as a signed number of half turns in [-1, 1)
-// and rounded to fp32 as a whole (its upper 32 bits alone would leave an angle of 10^-7 rad 1 % off),
-// goes to sincospi.
+// but for the fraction's own last bit: pos * 2^-64 turns.  The product, read as a signed number of
+// half turns in [-1, 1) and rounded to fp32 as a whole (its upper 32 bits alone would leave an angle of
+// 10^-7 rad 1 % off), goes to sincospi.
 //
 // Bound: HBM bytes (each element read and written once).  A warp takes a token: it computes each angle
 // once, into shared memory; a thread then holds the cosines and sines of 16 elements and applies
@@ -55,6 +54,22 @@ __device__ __forceinline__ uint32_t rotate_word(uint32_t w, float c, float s) {
     return ptx::pack_bf16x2(x0 * c - x1 * s, x1 * c + x0 * s);
 }
 
+// freq / 2pi without its whole turns, in units of 2^-64 turns (rounded towards zero): the 53-bit mantissa times
+// 1 / 2pi in 128 bits, shifted by the exponent.  (In fp64 the product alone is off by 2^-53 of the frequency, 2^-22
+// radians per radian of it at position 2^31, and a second part for its error took this kernel 0.6 us more.)
+__device__ __forceinline__ unsigned long long turn_of(double freq) {
+    constexpr unsigned long long kTurn1 = 0x28be60db9391054aull, kTurn0 = 0x7f09d5f47d4d3770ull;       // 2^128 / 2pi
+    const unsigned long long u = (unsigned long long)__double_as_longlong(freq);
+    const int e = (int)(u >> 52) & 2047;
+    const unsigned long long m = (u & 0xFFFFFFFFFFFFFull) | (e ? 1ull << 52 : 0ull);       // freq = +-m * 2^(max(e, 1) - 1075)
+    const unsigned __int128 x = (unsigned __int128)m * kTurn1 + __umul64hi(m, kTurn0);    // m / 2pi in units of 2^-64
+    const int s = 1075 - max(e, 1);
+    unsigned long long t = 0;
+    if (s >= 0 && s < 128) t = (unsigned long long)(x >> s);
+    else if (s < 0 && s > -64) t = (unsigned long long)x << -s;
+    return u >> 63 ? 0ull - t : t;
+}
+
 template <int D, bool kHalves, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kL = D / 16;     // lanes of a head: 16 elements (two 16-byte chunks) each
@@ -68,9 +83,7 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
     pdl_launch();
     int bad = 0;
     for (int i = threadIdx.x; i < p.pairs; i += kRopeThreads) {
-        double t = p.freqs[i] * 0.15915494309189533577;    // 1 / 2pi
-        t -= floor(t);
-        turn[i] = (unsigned long long)(t * 18446744073709551616.0);
+        turn[i] = turn_of(p.freqs[i]);
         axis[i] = p.axes[i];
         bad |= (unsigned)axis[i] >= (unsigned)p.num_axes;
     }

@@ -471,8 +471,9 @@ typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_
  * attn_rope -- rotary positions with several axes on queries and keys, before the attention; with
  * `inverse` the rotation by the negative angles, which is the gradient (dq, dk from the gradients of
  * the rotated q, k).  Pair p turns by positions[axes[p]] * freqs[p] radians; elements past
- * 2 * pairs pass through unchanged.  Angles are exact to fp32 for every int32 position; the
- * rotation is computed in fp32 and rounded once (nearest even).  A NaN stays some NaN.
+ * 2 * pairs pass through unchanged.  Angles, reduced to a half turn, are exact to fp32 for every int32
+ * position and frequencies up to 2^32 radians, but for |position| * 2^-64 turns; the rotation is computed in
+ * fp32 and rounded once (nearest even).  A NaN stays some NaN.
  *   q, k          [B][S][H or Hkv][d] as strides say: element (b, s, h, x) at b * stride[0] +
  *                 s * stride[1] + h * stride[2] + x (elements; multiples of 8 where the dimension has
  *                 more than one entry), so BSHD, BHSD and views of a fused projection are all taken.  k may be NULL (Hkv is then ignored)

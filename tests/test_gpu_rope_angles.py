@@ -1,10 +1,11 @@
-"""Angles of attn_rope and attn_paged_append where they show: small ones beside a partner of zero (needs a GB300).
+"""Angles of attn_rope and attn_paged_append where they show: small ones beside a partner of zero, and those of
+fast pairs at far positions (needs a GB300).
 
 Tolerances.  An element x0 cos - x1 sin is rounded once to bf16, half a step, 2^-8 of itself.  Before that, in
 fp32: the angle in half turns is rounded once (2^-24 of itself; at most pi 2^-25 rad), cosine and sine are off by
 2^-23 of themselves at most, two products and their difference by 2^-24 each.  With one product zero all of
 these are relative to the result, below 2^-21 together; in general they are below 2^-21 (|x0| + |x1|).  The
-frequency's fraction of a turn is off by two units of 2^-64 at most, which a position p multiplies: below
+frequency's fraction of a turn is off by a unit of 2^-64 at most, which a position p multiplies: below
 2^-32 turns, 2^-29 rad, of an angle of any size, and 2^-30 of the smallest angles below.
 """
 from fractions import Fraction
@@ -64,4 +65,22 @@ def test_small_angles_beside_a_partner_of_zero(attn, base, pairing):
                      (attn.attn_rope(q, None, pos, freqs, axes, pairing=pairing, inverse=True), back)):
         off = np.abs(got[0].float().cpu().numpy().astype(np.float64) - ref) - (2.0 ** -8 + 2.0 ** -21) * np.abs(ref)
         assert np.all(off <= 0), (float(off.max()), np.argwhere(off > 0)[:4])
+    assert attn.cache_device_status() == (0, 0)
+
+
+def test_far_positions_of_fast_pairs(attn):
+    # a frequency's own error counts 2^31 times here; where the two products cancel the angle shows
+    d, freqs = 64, [1.0, 0.7, 2.5, 17.0, 100.0, 3.3e4, -1e6, 1e-4]
+    positions = [s * (2 ** 31 - 1 - 37 * i) for i in range(300) for s in (1, -1)] + [-2 ** 31, 2 ** 30, 10 ** 9 + 7]
+    x = np.random.default_rng(5).integers(-60, 61, (len(positions), 8, len(freqs), 2)) / 64.0       # exact in bf16
+    q = torch.zeros((1, len(positions), 8, d), dtype=torch.bfloat16, device="cuda")
+    q[0, :, :, :2 * len(freqs)] = torch.as_tensor(x).flatten(2).to(torch.bfloat16)
+    got = attn.attn_rope(q, None, torch.tensor([positions], dtype=torch.int32, device="cuda"),
+                         torch.tensor(freqs, dtype=torch.float64, device="cuda"),
+                         torch.zeros(len(freqs), dtype=torch.int32, device="cuda"))
+    c, s = (t[:, None] for t in rotated(positions, freqs))
+    ref = np.stack([x[..., 0] * c - x[..., 1] * s, x[..., 1] * c + x[..., 0] * s], -1)
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -21 * np.abs(x).sum(-1, keepdims=True)
+    off = np.abs(got[0, :, :, :2 * len(freqs)].float().cpu().numpy().reshape(x.shape) - ref) - tol
+    assert np.all(off <= 0), [float(off[:, :, p].max()) for p in range(len(freqs))]
     assert attn.cache_device_status() == (0, 0)

@@ -83,9 +83,11 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
     pdl_launch();
     int bad = 0;
     for (int i = threadIdx.x; i < p.pairs; i += kRopeThreads) {
-        turn[i] = turn_of(p.freqs[i]);
-        axis[i] = p.axes[i];
-        bad |= (unsigned)axis[i] >= (unsigned)p.num_axes;
+        const double freq = p.freqs[i];
+        const int a = p.axes[i];
+        turn[i] = turn_of(freq);
+        axis[i] = isfinite(freq) ? a : ~a;                 // (an infinite frequency or NaN: the pair becomes NaN)
+        bad |= (unsigned)a >= (unsigned)p.num_axes;
     }
     const bool staged = kAppend && p.B < kCuStage;
     if constexpr (kAppend)
@@ -160,10 +162,11 @@ __global__ void __launch_bounds__(kRopeThreads, 7) attn_rope_kernel(const __grid
         __syncwarp();              // (the token before is done with cs)
 #pragma unroll 1
         for (int pr = lane; pr < p.pairs; pr += 32) {
-            const long long pos = __ldg(p.positions + axis[pr] * p.pos_axis + b * p.pos_b + s);
+            const int a = axis[pr];
+            const long long pos = __ldg(p.positions + (a < 0 ? ~a : a) * p.pos_axis + b * p.pos_b + s);
             const long long at = (long long)(turn[pr] * (unsigned long long)pos);
             float sn, c;
-            sincospif((float)at * 0x1p-63f, &sn, &c);
+            sincospif(a < 0 ? NAN : (float)at * 0x1p-63f, &sn, &c);
             cs[warp][pr] = make_float2(c, p.inverse ? -sn : sn);
         }
         __syncwarp();

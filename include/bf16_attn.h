@@ -473,7 +473,8 @@ typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_
  * the rotated q, k).  Pair p turns by positions[axes[p]] * freqs[p] radians; elements past
  * 2 * pairs pass through unchanged.  Angles, reduced to a half turn, are exact to fp32 for every int32
  * position and frequencies up to 2^32 radians, but for |position| * 2^-64 turns; the rotation is computed in
- * fp32 and rounded once (nearest even).  A NaN stays some NaN.
+ * fp32 and rounded once (nearest even).  A NaN stays some NaN; both elements of a pair whose frequency is
+ * infinite or NaN become NaN.
  *   q, k          [B][S][H or Hkv][d] as strides say: element (b, s, h, x) at b * stride[0] +
  *                 s * stride[1] + h * stride[2] + x (elements; multiples of 8 where the dimension has
  *                 more than one entry), so BSHD, BHSD and views of a fused projection are all taken.  k may be NULL (Hkv is then ignored)

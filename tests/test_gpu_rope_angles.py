@@ -1,5 +1,5 @@
-"""Angles of attn_rope and attn_paged_append where they show: small ones beside a partner of zero, and those of
-fast pairs at far positions (needs a GB300).
+"""Angles of attn_rope and attn_paged_append where they show: small ones beside a partner of zero, those of
+fast pairs at far positions, and frequencies that are not finite (needs a GB300).
 
 Tolerances.  An element x0 cos - x1 sin is rounded once to bf16, half a step, 2^-8 of itself.  Before that, in
 fp32: the angle in half turns is rounded once (2^-24 of itself; at most pi 2^-25 rad), cosine and sine are off by
@@ -83,4 +83,26 @@ def test_far_positions_of_fast_pairs(attn):
     tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -21 * np.abs(x).sum(-1, keepdims=True)
     off = np.abs(got[0, :, :, :2 * len(freqs)].float().cpu().numpy().reshape(x.shape) - ref) - tol
     assert np.all(off <= 0), [float(off[:, :, p].max()) for p in range(len(freqs))]
+    assert attn.cache_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+def test_a_frequency_that_is_not_finite_makes_its_pair_nan(attn, pairing):
+    # at position 0 too: 0 * inf has no value; the pair's zeros are NaN as well, the other pairs and the rest keep theirs
+    d, odd = 64, {0: float("nan"), 3: float("inf"), 6: float("-inf")}
+    freqs, axes = attn.rope_freqs((16, 16))
+    positions = torch.tensor([[0, 1, -7, 2 ** 31 - 1], [0, 5, 6, 7]], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, 4, 3, d), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    q[0, 1, 1] = 0.0
+    want = attn.attn_rope(q, None, positions, freqs, axes, pairing=pairing)
+    hit = torch.zeros(d, dtype=torch.bool)
+    for p, f in odd.items():
+        freqs[p] = f
+        for i in (2 * p, 2 * p + 1) if pairing == "adjacent" else (p, p + 16):
+            hit[i] = True
+    for inverse in (False, True):
+        got = attn.attn_rope(q, None, positions, freqs, axes, pairing=pairing, inverse=inverse)
+        assert torch.isnan(got[..., hit]).all() and not torch.isnan(got[..., ~hit]).any()
+        if not inverse:
+            assert torch.equal(got[..., ~hit], want[..., ~hit])
     assert attn.cache_device_status() == (0, 0)

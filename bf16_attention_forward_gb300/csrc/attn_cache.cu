@@ -128,18 +128,59 @@ bool same(const View& a, const View& b) {
 
 bool overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
 
-// whether two views can share an element: their ranges meet, and they are not columns side by side of
-// the same tokens (views of one projection's rows)
+// Two views as sums of multiples of common strides, largest first: 0 .. n - 1 times each, and an extent behind the
+// last (an extent of one entry, or of stride zero, adds nothing; two of one stride add up).
+struct Lattice {
+    int levels = 0;
+    int64_t st[6], n[2][6], d[2];
+    void add(int64_t stride) {
+        int i = 0;
+        while (i < levels && st[i] > stride) ++i;
+        if (i < levels && st[i] == stride) return;
+        for (int j = levels++; j > i; --j) st[j] = st[j - 1];
+        st[i] = stride;
+    }
+    int64_t width(int v, int level) const {        // of what the levels from `level` on span
+        int64_t w = d[v];
+        for (int i = level; i < levels; ++i) w += (n[v][i] - 1) * st[i];
+        return w;
+    }
+    // whether the two share an element from `level` on, the second `diff` elements behind the first: the multiples
+    // i of the first and j of the second leave diff - (i - j) * st for the levels behind, so only i - j for which
+    // those still reach each other count: three at most where extents nest (more: taken to meet)
+    bool meet(int level, int64_t diff) const {
+        const int64_t wa = width(0, level), wb = width(1, level);
+        if (diff >= wa || -diff >= wb) return false;
+        if (level == levels) return true;
+        const int64_t t = st[level], ra = width(0, level + 1), rb = width(1, level + 1);
+        auto floor_div = [&](int64_t x) { return x / t - (x % t < 0); };
+        int64_t k0 = floor_div(diff - ra) + 1, k1 = -floor_div(-(diff + rb)) - 1;
+        if (k0 < 1 - n[1][level]) k0 = 1 - n[1][level];
+        if (k1 > n[0][level] - 1) k1 = n[0][level] - 1;
+        if (k1 - k0 > 3) return true;
+        for (int64_t k = k0; k <= k1; ++k)
+            if (meet(level + 1, diff - k * t)) return true;
+        return false;
+    }
+};
+
+// whether two views share an element: slices of one buffer, side by side in any of their extents, do not
 bool meet(const View& a, const View& b) {
     if (!a.span() || !b.span() || !overlap(a.at, a.end(), b.at, b.end())) return false;
-    const int64_t ts = a.st[1];
-    const bool batch = (a.n[0] == 1 && b.n[0] == 1) || (a.st[0] == b.st[0] && a.st[0] == ts * a.n[1]);
-    if (batch && ts > 0 && ts == b.st[1] && a.n[1] == b.n[1]) {
-        const int64_t wa = (a.n[2] - 1) * a.st[2] + a.d, wb = (b.n[2] - 1) * b.st[2] + b.d;
-        const int64_t diff = ((int64_t)(b.at - a.at) / 2 % ts + ts) % ts;
-        if (diff >= wa && diff + wb <= ts) return false;
+    const View* v[2] = {&a, &b};
+    Lattice l;
+    for (int x = 0; x < 2; ++x)
+        for (int i = 0; i < 3; ++i)
+            if (v[x]->n[i] > 1 && v[x]->st[i] > 0) l.add(v[x]->st[i]);
+    for (int x = 0; x < 2; ++x) {
+        l.d[x] = v[x]->d;
+        for (int j = 0; j < l.levels; ++j) {
+            l.n[x][j] = 1;
+            for (int i = 0; i < 3; ++i)
+                if (v[x]->n[i] > 1 && v[x]->st[i] == l.st[j]) l.n[x][j] += v[x]->n[i] - 1;
+        }
     }
-    return true;
+    return l.meet(0, (int64_t)(b.at - a.at) / 2);
 }
 
 // no two elements of a view on one address: its extents nest

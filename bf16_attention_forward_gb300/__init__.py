@@ -1033,9 +1033,18 @@ def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: 
 
 
 def cache_device_status(stream=None) -> tuple:
-    """Synchronize and read/clear the status word of the rope, append, decode and evict kernels: (status, check)."""
+    """Synchronize ``stream`` and read/clear the status word of the rope, append, decode and evict kernels on its
+    device (of a stream by its handle: on the current device): (status, check)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
+    s = torch.cuda.current_stream() if stream is None else stream
+    handle, index = (s.cuda_stream, s.device_index) if hasattr(s, "cuda_stream") else (int(s), None)
+    on = None if index is None or index == torch._C._cuda_getDevice() else torch.cuda.device(index)
     site = ctypes.c_int32(0)
-    st = load().attn_cache_get_device_status(ctypes.c_void_p(s.cuda_stream), ctypes.byref(site))
+    if on is not None:
+        on.__enter__()
+    try:
+        st = load().attn_cache_get_device_status(ctypes.c_void_p(handle), ctypes.byref(site))
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
     return int(st), int(site.value)

@@ -605,7 +605,7 @@ size_t attn_paged_evict_workspace_size(const attn_evict_args_t* args);
 int attn_paged_evict(const attn_evict_args_t* args, void* workspace, size_t workspace_bytes,
                      attn_stream_t stream);
 
-/* Synchronize `stream`, then read and clear the status word of these four calls' kernels. */
+/* Synchronize `stream`, then read and clear the current device's status word of these four calls' kernels. */
 int attn_cache_get_device_status(attn_stream_t stream, int32_t* site);
 
 #ifdef __cplusplus

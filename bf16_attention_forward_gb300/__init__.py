@@ -474,7 +474,8 @@ def attn_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table, ma
     page are not read).  Key j of sequence b is slot j % page_size of page
     block_table[b, j // page_size].  Causal: aligned at each sequence's last query and key.
     Bad offsets, lengths or page indices write nothing and are reported by
-    :func:`device_status`.  Returns ``o`` or ``(o, lse)`` (lse: fp32 [H, total_q]).
+    :func:`device_status`.  For one query per sequence :func:`attn_paged_decode` is faster and takes any
+    page size and number of heads.  Returns ``o`` or ``(o, lse)`` (lse: fp32 [H, total_q]).
     """
     import torch
     if round not in MODES:
@@ -752,8 +753,8 @@ def attn_rope(q, k, positions, freqs, axes, layout: str = "bshd", pairing: str =
     ``q``/``k``: CUDA bf16, 4-D in ``layout`` or packed [total, heads, d]; any strides that keep a head
     contiguous and rows 16-byte aligned (views of a fused projection).  ``positions``: CUDA int32
     [axes, S] (one grid for every batch entry), [axes, B, S], or [axes, total] for packed tensors.
-    ``freqs``/``axes``: float64 and int32 [pairs], as :func:`rope_freqs` makes them; elements past
-    2 * pairs pass through.  ``pairing``: "adjacent" elements (2p, 2p + 1) or "halves" (p, p + pairs).
+    ``freqs``/``axes``: float64 and int32 [pairs], as :func:`rope_freqs` makes them (a pair whose
+    frequency is infinite or NaN becomes NaN); elements past 2 * pairs pass through.  ``pairing``: "adjacent" elements (2p, 2p + 1) or "halves" (p, p + pairs).
     ``q_out``/``k_out``: optional outputs (q and k themselves: in place).  ``inverse`` turns by the negative
     angles.  Returns ``(q_out, k_out)``, or ``q_out`` when k is None."""
     import torch
@@ -995,8 +996,9 @@ def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: 
     order, and the recent keys follow up to the budget's end.  ``k_cache``/``v_cache`` (as in
     :func:`attn_paged_decode`) are rewritten in place; ``weights`` [B, Hkv, max_pages * page_size] and
     ``seqlens_k`` too, unless ``weights_out`` / ``seqlens_out`` take the new ones.  A sequence with a bad
-    length or page, or with a page that the table holds more than once, stays as it is and is reported
-    by :func:`cache_device_status`.  Returns ``seqlens_out``."""
+    length, and one to be cut with a bad page or a page that the table holds more than once, stays as it is
+    and is reported by :func:`cache_device_status`.  Which kernels run goes by the table's width, not by the
+    lengths: a table much wider than the sequences are long costs time.  Returns ``seqlens_out``."""
     import torch
     dev, pages, ps, Hkv, d, B, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
     weights_out = weights if weights_out is None else weights_out

@@ -64,8 +64,11 @@ int device(int* sms) {
     return ATTN_OK;
 }
 
-// Every kernel waits for the one before it before it touches global memory, so each is launched as its programmatic
-// dependent.  cluster: CTAs of a cluster.
+// Each kernel is launched as the programmatic dependent of the one before it in the stream, waits for that one before
+// it touches global memory and before it ends, and only then lets the next one start.  One reads earlier: eviction's
+// select kernel reads lengths and weights while the prepare kernel runs, which only reads them too; what ran before that
+// is complete by then, because the prepare kernel's CTAs let select start behind their own wait.
+// cluster: CTAs of a cluster.
 template <class P>
 int launch_clusters(void (*kernel)(P), int64_t grid, int cluster, int threads, size_t smem, cudaStream_t stream,
                     const std::remove_const_t<P>& args, int grid_y = 1) {
@@ -395,6 +398,7 @@ int head_tiles(int64_t group) { return group <= 8 ? 1 : group <= 16 ? 2 : 4; }
 // the SMs a split gains little, and up to 10 tiles are not.  By the table's room (lengths are on the device).
 // us a call in a graph, d = 128, split / whole:  8 rows of 2 tiles 7.0 / 4.8, 5 tiles 7.0 / 7.1, 8 tiles 7.2 / 9.4;
 // 16 x 8 rows of 2 tiles 7.8 / 5.2, 5 tiles 11.8 / 8.0, 8 tiles 14.5 / 10.8.
+// (Short rows in a wide table are split: 2 rows of 513 keys, d = 64, 5.9 in a table of 528 slots, 6.2 in one of 32,768.)
 bool decode_whole(const attn_decode_args_t& a, int sms) {
     const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
     const int64_t tiles = cdiv(a.max_pages * a.page_size, kDecTile);

@@ -10,9 +10,6 @@
 
 namespace cache {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.693147180559945309f;
-
 __device__ uint32_t g_status[2];   // [0] status code, [1] the check that failed
 
 // first failure wins until the host reads and clears the word

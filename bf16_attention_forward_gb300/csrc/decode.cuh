@@ -7,8 +7,8 @@
 // of each key, summed over the query heads of its K/V head, is added to a running fp32 weight.
 //
 // Bound: HBM bytes; every key and value is read once (2 * d * 2 bytes for 4 * d * G flops, G =
-// H / Hkv query heads).  64 caches, 2.7 GB of keys and values: 383 us, 6.9 TB/s, the tensor pipe
-// 10 % busy.  The products run on mma.sync with the KEYS as the M rows and the query heads as the
+// H / Hkv query heads).  64 caches, 2.7 GB of keys and values: 383 to 397 us over boxes, 6.8 to 7.0 TB/s, the
+// tensor pipe 10 % busy.  The products run on mma.sync with the KEYS as the M rows and the query heads as the
 // N columns (S^T = K Q^T, O^T = V^T P^T): N is 8, so a K/V head's 4 to 8 query heads waste at most
 // half of it.  tcgen05 would need 128 rows of one operand and a trip through TMEM for a product
 // that takes a few percent of the time.

@@ -22,7 +22,9 @@
 // moves a (tensor, sequence, head) in ascending order, each step's reads before its writes; columns are
 // independent, and a few long caches split their rows into column pieces for more CTAs.
 // Where few rows can move (kMostWhole), each select CTA moves its own, and fill and shift are not launched
-// (32 caches a few keys over 1024, 8 heads: 19.5 -> 14.2 us).
+// (32 caches a few keys over 1024, 8 heads: 19.5 -> 14.2 us).  The host decides that, and the clusters, by the slots
+// that the table has room for, since lengths are on the device: the same caches in tables of 1280 slots take 14.3 us, of
+// 1536 (four kernels) 17.3, of 4096 24.7 and of 32,768 (clusters; the weights' rows lie far apart) 38.5.
 //
 // Bound: the moved rows' bytes (K and V, read and written) and 4 bytes per key; below a few MB the
 // launches' latency.  16 caches of 2048 to 16,384 keys, 8 heads, to 4096: 69 us, of them 18 for select (one
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) attn_evict_prep_kernel(const 
     const int tid = blockIdx.x * kPrepThreads + threadIdx.x, lane = threadIdx.x & 31, warp = tid >> 5;
     constexpr int kThreads = kPrepThreads * kPrepCtas;
     pdl_wait();
-    pdl_launch();
+    pdl_launch();                                      // (not sooner: select reads lengths and weights at once)
     for (int i = tid; i < p.pages.num_pages; i += kThreads) p.uses[i] = 0;
     if (tid == 0) *p.total = 0;
     cluster_sync();
@@ -179,7 +181,9 @@ __device__ __forceinline__ void shift_weights(const EvictParams& p, const float*
         for (int j = p.budget + tid; j < n; j += threads) out[j] = 0.0f;
 }
 
-// It starts while the prepare kernel runs, and waits for that before it touches what it writes.
+// It starts while the prepare kernel runs, and waits for that before it touches what that one writes, and before it
+// writes anything.  What it reads sooner, lengths and weights, the prepare kernel does not write, and all that ran before
+// the prepare kernel is complete once that lets this one start.
 // kWhole: the CTA (a cluster of one) moves its own rows too, in place of the fill and shift kernels.
 template <int T, bool kWhole>
 __global__ void __launch_bounds__(T, 1024 / T) attn_evict_select_kernel(const __grid_constant__ EvictParams p) {

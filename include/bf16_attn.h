@@ -307,8 +307,10 @@ int attn_fwd_varlen(const attn_varlen_args_t* args, const attn_options_t* opts, 
  *   block_table   device int32 [B][max_pages]; entries past a sequence's last used page are
  *                 not read.  Pages may be shared between sequences.
  *   page_size     a multiple of 128 (a key tile never straddles pages)
- *   pack_heads    as in attn_fwd_varlen (the natural setting for decoding over a paged cache)
- *   max_splits    as in attn_fwd_varlen (decoding a few long sequences)
+ *   pack_heads    as in attn_fwd_varlen (the natural setting for a few queries per sequence)
+ *   max_splits    as in attn_fwd_varlen (a few queries over a few long sequences)
+ * For ONE query per sequence attn_paged_decode is the call to take: any page size, any H / Hkv, and faster (64 caches
+ * of 4096 to 16,384 keys, H32 Hkv8 d128: 397 us against 482 here with both options; 4 caches: 35 against 56).
  * Checked on the device: bad query offsets, lengths or page indices (outside 0 ..
  * num_pages - 1) write no output and report ATTN_ERR_INVALID_ARG at ATTN_SITE_SEQLENS.  Slots
  * of a sequence's last page past its length are never read as keys (they read as zeros), so
@@ -342,7 +344,8 @@ int attn_get_device_status(attn_stream_t stream, int32_t* site);
 /* Static string for a status code. */
 const char* attn_status_string(int status);
 
-/* Library version, as major*10000 + minor*100 + patch. */
+/* Library version, as major*10000 + minor*100 + patch, of the attention calls.  (The calls around the paged cache
+ * came to 0.3.0 without raising it: a program that also runs with older builds looks for their symbols.) */
 int attn_version(void);
 
 /*
@@ -462,7 +465,7 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
 #define ATTN_CACHE_SITE_AXES 20     /* an axis outside 0 .. num_axes - 1: nothing is written           */
 #define ATTN_CACHE_SITE_APPEND 21   /* a new token's slot or page is not in the cache: k, v not written  */
 #define ATTN_CACHE_SITE_DECODE 22   /* a bad length or page: that sequence's outputs are not written    */
-#define ATTN_CACHE_SITE_EVICT 23    /* a bad length or page, or a page used twice: the sequence stays    */
+#define ATTN_CACHE_SITE_EVICT 23    /* a bad length, or of a sequence to be cut a bad page or one used twice: it stays */
 
 /* Which elements of a head form pair p of `pairs`: 2p and 2p + 1, or p and p + pairs. */
 typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_t;
@@ -509,7 +512,8 @@ int attn_rope(const attn_rope_args_t* args, attn_stream_t stream);
  *   q, q_out         optional queries [total][H][d] (strided) and their rotated copy (dense; may be q
  *                    itself if q is dense).  NULL: none
  *   cu_seqlens_new   device int32 [B + 1]: sequence b's new tokens are rows cu[b] .. cu[b+1] - 1 (a
- *                    sequence may have none); rows outside every sequence are not read or written
+ *                    sequence may have none); rows outside every sequence are not read or written.  0 <= start, never
+ *                    decreasing, end <= total: else some tokens are not written, but nothing outside the lengths is
  *   seqlens_k        device int32 [B]: lengths WITH the new tokens (as the attention takes them), so row
  *                    cu[b] + i goes to slot seqlens_k[b] - (cu[b+1] - cu[b]) + i
  *   positions, freqs, axes, pairs, num_axes, pairing   as in attn_rope, positions [num_axes] x [total]
@@ -549,7 +553,8 @@ int attn_paged_append(const attn_append_args_t* args, attn_stream_t stream);
  *                 over the query heads of its K/V head, is added (the accumulated weight that
  *                 attn_paged_evict goes by).  A NaN row adds NaN to its keys
  *   round_mode    as in attn_fwd.  Non-finite values are treated as there
- * Results are bitwise reproducible for the same lengths on the same GPU model.  workspace: caller device
+ * Results are bitwise reproducible for the same lengths and the same shapes (max_pages and the presence of weights
+ * among them: they decide whether a short row is split) on the same GPU model.  workspace: caller device
  * memory of at least attn_paged_decode_workspace_size() bytes, 16-byte aligned: the parts of split rows,
  * and with weights the logits (4 bytes per query head and table slot).  A few short sequences need none:
  * the size query returns 0 for them, as it does for invalid arguments or without a usable device.
@@ -578,16 +583,18 @@ int attn_paged_decode(const attn_decode_args_t* args, void* workspace, size_t wo
  * slots; -0 equals 0; a NaN ranks below every number).  Survivors below slot budget - recent stay where
  * they are, the i-th survivor past it moves into the i-th freed slot, and the recent keys follow in order
  * up to slot budget - 1: attention does not depend on the order of keys, and the recent window stays
- * last for the tokens to come.  Shorter sequences stay as they are.
- *   k_cache, v_cache   rewritten in place.  A page that a rewritten sequence uses must be used once among all
+ * last for the tokens to come.  Sequences of `budget` keys or fewer stay as they are; their pages are not checked.
+ *   k_cache, v_cache   rewritten in place.  A page that a sequence to be cut uses must be used once among all
  *                      sequences' used table entries (checked: else the sequence is left as it was, its
- *                      weights_out too, and reported)
+ *                      weights_out too, seqlens_out takes its length, and it is reported; likewise a bad length)
  *   weights            fp32 [B][Hkv][max_pages * page_size], as attn_paged_decode accumulates them
  *   weights_out        the weights of the slots after the call, freed slots up to the old length zero; may be
  *                      `weights` itself, else overlaps nothing.  Entries past the old length are not written
  *   seqlens_k, seqlens_out   device int32 [B]: lengths before and after; may be the same
  *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget; the weights, and the cache's rows times
  *                      Hkv, are at most 2^31 (else ATTN_ERR_UNSUPPORTED)
+ * Which kernels run goes by max_pages * page_size, not by the lengths: a table much wider than the sequences are long
+ * costs time (32 caches of 1040 keys cut to 1024: 14 us in a table of 1040 slots, 25 in one of 4096, 38 in one of 32,768).
  * workspace: caller device memory of at least attn_paged_evict_workspace_size() bytes, 16-byte aligned.
  */
 typedef struct {

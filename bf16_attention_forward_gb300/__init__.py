@@ -28,7 +28,9 @@ EXPORTS = ("attn_fwd", "attn_fwd_ws", "attn_fwd_noalloc", "attn_fwd_ex", "attn_f
            "attn_fwd_varlen", "attn_fwd_varlen_workspace_size", "attn_fwd_paged",
            "attn_fwd_paged_workspace_size", "attn_bwd_varlen", "attn_bwd_varlen_workspace_size",
            "attn_rope", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size",
-           "attn_paged_evict", "attn_paged_evict_workspace_size", "attn_cache_get_device_status")
+           "attn_paged_evict", "attn_paged_evict_workspace_size", "attn_norm_rope", "attn_norm_rope_bwd",
+           "attn_norm_rope_bwd_workspace_size", "attn_norm_rope_append", "attn_paged_reserve",
+           "attn_cache_get_device_status")
 
 
 class AttnError(RuntimeError):
@@ -122,6 +124,43 @@ class EvictArgs(ctypes.Structure):
                                               "sinks", "recent")]
 
 
+class NormRopeArgs(ctypes.Structure):
+    """attn_norm_rope_args_t: the argument set of attn_norm_rope."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_out", "k", "k_out", "q_weight", "k_weight", "positions", "freqs",
+                                               "axes")] + \
+               [(n, ctypes.c_int64) for n in ("B", "S", "H", "Hkv", "d")] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_stride", "q_out_stride", "k_stride", "k_out_stride")] + \
+               [(n, ctypes.c_int64) for n in ("pos_axis_stride", "pos_batch_stride")] + \
+               [(n, ctypes.c_int32) for n in ("pairs", "num_axes", "pairing", "weight_bf16")] + \
+               [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class NormRopeBwdArgs(ctypes.Structure):
+    """attn_norm_rope_bwd_args_t: the argument set of attn_norm_rope_bwd, the forward's (`fwd`) first."""
+    _fields_ = NormRopeArgs._fields_ + \
+               [(n, ctypes.c_void_p) for n in ("dq", "dk", "dq_weight", "dk_weight")] + \
+               [(n, ctypes.c_int64 * 3) for n in ("dq_stride", "dk_stride")]
+
+
+class NormAppendArgs(ctypes.Structure):
+    """attn_norm_append_args_t: the argument set of attn_norm_rope_append."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_cache", "v_cache", "q", "q_out", "q_weight", "k_weight",
+                                               "slots", "positions", "freqs", "axes")] + \
+               [(n, ctypes.c_int64) for n in ("H", "Hkv", "total", "num_pages", "page_size", "d")] + \
+               [(n, ctypes.c_int64 * 2) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [("pos_axis_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("pairs", "num_axes", "pairing", "weight_bf16")] + \
+               [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ReserveArgs(ctypes.Structure):
+    """attn_reserve_args_t: the argument set of attn_paged_reserve."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("seqlens_k", "cu_seqlens_new", "block_table", "pages_held", "held_out",
+                                               "shared_pages", "free_pages", "free_count", "count_out", "slots",
+                                               "positions")] + \
+               [(n, ctypes.c_int64) for n in ("B", "max_pages", "page_size", "capacity", "total")]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("units", "kv_tiles", "full_items", "split_units",
                                               "splits", "items", "grid", "workspace_bytes")]
@@ -190,10 +229,10 @@ def load(path: str | None = None):
         lib.attn_bwd_varlen_workspace_size.restype = ctypes.c_size_t
         lib.attn_bwd_varlen_workspace_size.argtypes = [ctypes.POINTER(BwdVarlenArgs)]
         # the argument sets of these calls travel as packed bytes or as structures
-        for name in ("attn_rope", "attn_paged_append"):
+        for name in ("attn_rope", "attn_paged_append", "attn_norm_rope", "attn_norm_rope_append", "attn_paged_reserve"):
             getattr(lib, name).restype = i32
             getattr(lib, name).argtypes = [vp, vp]
-        for name in ("attn_paged_decode", "attn_paged_evict"):
+        for name in ("attn_paged_decode", "attn_paged_evict", "attn_norm_rope_bwd"):
             getattr(lib, name).restype = i32
             getattr(lib, name).argtypes = [vp, vp, ctypes.c_size_t, vp]
             getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
@@ -641,7 +680,7 @@ def bwd_device_status(stream=None) -> tuple:
 # attribute reads, packed in one go, and shapes and strides are read once.
 def _packer(cls):
     """struct.pack for the fields of an argument structure, arrays flattened."""
-    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i"}
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
     fmt = "@" + "".join(codes[t] if t in codes else "%d%s" % (t._length_, codes[t._type_]) for _, t in cls._fields_)
     packed = struct.Struct(fmt)
     assert packed.size <= ctypes.sizeof(cls) <= packed.size + 4      # the structure may end in padding
@@ -649,6 +688,8 @@ def _packer(cls):
 
 
 _pack_rope, _pack_append, _pack_decode, _pack_evict = map(_packer, (RopeArgs, AppendArgs, DecodeArgs, EvictArgs))
+_pack_norm, _pack_norm_bwd, _pack_norm_append, _pack_reserve = map(_packer, (NormRopeArgs, NormRopeBwdArgs, NormAppendArgs,
+                                                                             ReserveArgs))
 
 
 def _on(index, stream):
@@ -909,7 +950,7 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name, index, *shape):
     """A call's workspace size, by the shapes that it depends on (and the device, which has to be current)."""
-    a = (DecodeArgs if name == "attn_paged_decode" else EvictArgs)()
+    a = {"attn_paged_decode": DecodeArgs, "attn_paged_evict": EvictArgs, "attn_norm_rope_bwd": NormRopeBwdArgs}[name]()
     for n, x in shape:
         setattr(a, n, x)
     return int(getattr(load(), name + "_workspace_size")(ctypes.byref(a)))
@@ -1034,9 +1075,317 @@ def attn_paged_evict(k_cache, v_cache, weights, seqlens_k, block_table, budget: 
     return seqlens_out
 
 
+# ------------------------------------------------------------- norms with positions, pages and slots
+def _norm_weights(index, d, q_weight, k_weight):
+    """Checks the norms' weights; returns their addresses and whether they are bf16."""
+    import torch
+    dtype = None
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("%s must be a CUDA float32 or bfloat16 tensor" % name)
+        _check(index, (w, name, w.dtype, 1))
+        if w.shape[0] != d:
+            raise ValueError("%s must hold one weight per element of a head" % name)
+        if dtype is not None and w.dtype is not dtype:
+            raise TypeError("q_weight and k_weight must have one type")
+        dtype = w.dtype
+    return (0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+            1 if dtype is torch.bfloat16 else 0)
+
+
+class _NormOperands:
+    """The operands that attn_norm_rope and its gradient take alike, checked: sizes, strides and tables."""
+
+    def __init__(self, q, k, q_weight, k_weight, positions, freqs, axes, eps, layout, pairing):
+        import torch
+        if layout not in LAYOUTS:
+            raise ValueError("layout must be bshd or bhsd")
+        if pairing not in PAIRINGS:
+            raise ValueError("pairing must be adjacent or halves")
+        self.dim = dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+        self.dev = dev = _device_of(q, "q", torch.bfloat16, dim)
+        _check_heads(dev, dim, (q, "q")) if k is None else _check_heads(dev, dim, (q, "q"), (k, "k"))
+        self.bhsd = dim == 4 and layout == "bhsd"
+        # token and head dimensions
+        self.t, self.h = (0, 1) if dim == 3 else (2, 1) if self.bhsd else (1, 2)
+        qn = q.shape
+        self.B, self.S, self.H, self.d = 1 if dim == 3 else qn[0], qn[self.t], qn[self.h], qn[-1]
+        self.Hkv = 0
+        if k is not None:
+            kn = k.shape
+            self.Hkv = kn[self.h]
+            if kn[self.t] != self.S or kn[-1] != self.d or (dim == 4 and kn[0] != self.B):
+                raise ValueError("q and k must agree in all but their heads")
+        elif k_weight is not None:
+            raise ValueError("k_weight needs k")
+        self.weights = _norm_weights(dev, self.d, q_weight, k_weight)
+        # (positions, freqs, axes; strides of positions; pairs, axes)
+        self.tables, self.pos, self.pairs, self.axes = (0, 0, 0), (0, 0), 0, 1
+        if positions is not None and freqs is not None and axes is not None:
+            per_batch = dim == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 3
+            self.pairs = _rope_tables(positions, freqs, axes, pairing, dev, 3 if per_batch else 2)
+            pn, ps = positions.shape, positions.stride()
+            if pn[-1] != self.S or (per_batch and pn[1] != self.B):
+                raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
+            self.tables = positions.data_ptr(), freqs.data_ptr(), axes.data_ptr()
+            self.pos, self.axes = (ps[0], ps[1] if per_batch else 0), pn[0]
+        elif positions is not None or freqs is not None or axes is not None:
+            raise ValueError("positions, freqs and axes go together")
+        self.eps, self.pairing = float(eps), PAIRINGS[pairing]
+
+    def like(self, t, of, name):
+        """Checks a tensor that has to have another's shape."""
+        _check_heads(self.dev, self.dim, (t, name))
+        if of is None or t.shape != of.shape:
+            raise ValueError("%s must have its input's shape" % name)
+
+    def strides(self, t):
+        """(batch, token, head) strides; of none: zeros."""
+        if t is None:
+            return 0, 0, 0
+        s = t.stride()
+        return 0 if self.dim == 3 else s[0], s[self.t], s[self.h]
+
+    def fields(self, q, k, q_out, k_out):
+        return (q.data_ptr(), q_out.data_ptr(), 0 if k is None else k.data_ptr(), 0 if k is None else k_out.data_ptr(),
+                self.weights[0], self.weights[1], *self.tables, self.B, self.S, self.H, self.Hkv, self.d, *self.strides(q),
+                *self.strides(q_out), *self.strides(k), *self.strides(k_out), *self.pos, self.pairs, self.axes, self.pairing,
+                self.weights[2], self.eps, 0)
+
+
+def attn_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, freqs=None, axes=None, eps: float = 1e-6,
+                   layout: str = "bshd", pairing: str = "adjacent", q_out=None, k_out=None, stream=None):
+    """Norms of q's (and k's, unless it is None) heads with their rotary positions in the same pass: every head x
+    becomes x * weight / sqrt(mean(x ** 2) + eps), then is rotated as :func:`attn_rope` does; fp32, rounded once.
+
+    ``q``/``k``, ``positions``, ``freqs``, ``axes``, ``layout``, ``pairing``, ``q_out``/``k_out``: as in
+    :func:`attn_rope`; without the three tables nothing is rotated.  ``q_weight``/``k_weight``: CUDA [d], both float32 or
+    both bfloat16; None: ones.  Returns ``(q_out, k_out)``, or ``q_out`` when k is None."""
+    import torch
+    a = _NormOperands(q, k, q_weight, k_weight, positions, freqs, axes, eps, layout, pairing)
+    for o, t, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if o is not None:
+            a.like(o, t, name)
+    on = _on(a.dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        if a.S > 0:
+            st = (_lib or load()).attn_norm_rope(_pack_norm(*a.fields(q, k, q_out, k_out)),
+                                                 torch._C._cuda_getCurrentRawStream(a.dev))
+            if st != 0:
+                raise AttnError(st, "attn_norm_rope")
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return q_out if k is None else (q_out, k_out)
+
+
+def attn_norm_rope_bwd(dq, dk, q, k, q_weight=None, k_weight=None, positions=None, freqs=None, axes=None,
+                       eps: float = 1e-6, layout: str = "bshd", pairing: str = "adjacent", dq_out=None, dk_out=None,
+                       dq_weight=None, dk_weight=None, stream=None, workspace=None):
+    """Gradients of :func:`attn_norm_rope`: from ``dq``/``dk``, those of its outputs, and its arguments (dk is None exactly
+    when k is) the gradients of q, k (bf16) and of the weights (float32 [d], whatever the weights' type: sums over every
+    token and head; None for a weight that is None).  ``dq_out``/``dk_out``: optional outputs of any strides (dq and dk
+    themselves: in place); ``dq_weight``/``dk_weight``: likewise.  All are bitwise reproducible.  ``workspace``: optional
+    caller tensor (calls that may run at the same time need one each).  Returns
+    ``(dq_out, dk_out, dq_weight, dk_weight)``, or ``(dq_out, dq_weight)`` when k is None."""
+    import torch
+    a = _NormOperands(q, k, q_weight, k_weight, positions, freqs, axes, eps, layout, pairing)
+    if (dk is None) != (k is None):
+        raise ValueError("dk and k go together")
+    a.like(dq, q, "dq")
+    if dk is not None:
+        a.like(dk, k, "dk")
+    for o, t, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
+        if o is not None:
+            a.like(o, t, name)
+    for o, w, name in ((dq_weight, q_weight, "dq_weight"), (dk_weight, k_weight, "dk_weight")):
+        if o is not None:
+            if w is None:
+                raise ValueError("%s needs its weight" % name)
+            _check(a.dev, (o, name, torch.float32, 1))
+            if o.shape[0] != a.d:
+                raise ValueError("%s must hold d elements" % name)
+    ws_bytes = 0
+    if workspace is not None:
+        workspace, ws_bytes = _check_workspace(workspace, a.dev)
+    on = _on(a.dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        if dq_out is None:
+            dq_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if k is not None and dk_out is None:
+            dk_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        if q_weight is not None and dq_weight is None:
+            dq_weight = torch.empty(a.d, dtype=torch.float32, device=q.device)
+        if k_weight is not None and dk_weight is None:
+            dk_weight = torch.empty(a.d, dtype=torch.float32, device=q.device)
+        if a.S > 0:
+            if workspace is None:
+                ws_bytes = _workspace_bytes("attn_norm_rope_bwd", a.dev, ("B", a.B), ("S", a.S), ("H", a.H), ("Hkv", a.Hkv),
+                                            ("d", a.d), ("k", 0 if k is None else 16), ("num_axes", 1))
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            args = _pack_norm_bwd(*a.fields(q, k, dq_out, dk_out), dq.data_ptr(), 0 if dk is None else dk.data_ptr(),
+                                  0 if dq_weight is None else dq_weight.data_ptr(),
+                                  0 if dk_weight is None else dk_weight.data_ptr(), *a.strides(dq), *a.strides(dk))
+            st = (_lib or load()).attn_norm_rope_bwd(args, workspace.data_ptr(), ws_bytes,
+                                                     torch._C._cuda_getCurrentRawStream(a.dev))
+            if st != 0:
+                raise AttnError(st, "attn_norm_rope_bwd")
+        else:
+            for w in (dq_weight, dk_weight):
+                if w is not None:
+                    w.zero_()
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return (dq_out, dq_weight) if k is None else (dq_out, dk_out, dq_weight, dk_weight)
+
+
+def attn_norm_rope_append(k, v, k_cache, v_cache, slots, q=None, q_out=None, q_weight=None, k_weight=None,
+                          positions=None, freqs=None, axes=None, eps: float = 1e-6, pairing: str = "adjacent", stream=None):
+    """Write new tokens' keys, normed and rotated as :func:`attn_norm_rope` does, and their values to the ``slots`` of a
+    paged cache that :func:`attn_paged_reserve` gave them; the queries ``q`` if given are normed and rotated beside them.
+
+    ``k``/``v``: [total, Hkv, d], ``q``: [total, H, d] (CUDA bf16, heads contiguous, token strides free); ``slots``: CUDA
+    int64 [total] rows of the cache, -1 for a token that is not read or written.  Weights, tables (positions
+    [axes, total]) and eps as in :func:`attn_norm_rope`.  Keys and values of other slots outside the cache are not
+    written and are reported by :func:`cache_device_status`.  Returns ``q_out`` (dense [total, H, d]), or None without ``q``."""
+    import torch
+    if pairing not in PAIRINGS:
+        raise ValueError("pairing must be adjacent or halves")
+    dev = _device_of(k_cache, "k_cache", torch.bfloat16, 4)
+    _check(dev, (k_cache, "k_cache", torch.bfloat16, 4), (v_cache, "v_cache", torch.bfloat16, 4),
+           (slots, "slots", torch.int64, 1))
+    pages, ps, Hkv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    _check_heads(dev, 3, (k, "k"), (v, "v")) if q is None else _check_heads(dev, 3, (k, "k"), (v, "v"), (q, "q"))
+    shape = k.shape
+    total = shape[0]
+    if v.shape != shape or shape[1] != Hkv or shape[2] != d:
+        raise ValueError("k and v must be [total, Hkv, d] with the cache's Hkv and d")
+    if slots.shape[0] != total:
+        raise ValueError("slots must hold one slot per token")
+    pairs, num_axes, pos, pos_stride, fp, ap = 0, 1, 0, 0, 0, 0
+    if positions is not None and freqs is not None and axes is not None:
+        pairs = _rope_tables(positions, freqs, axes, pairing, dev, 2)
+        num_axes = positions.shape[0]
+        if positions.shape[1] != total:
+            raise ValueError("positions must be [axes, total]")
+        pos, pos_stride, fp, ap = positions.data_ptr(), positions.stride()[0], freqs.data_ptr(), axes.data_ptr()
+    elif positions is not None or freqs is not None or axes is not None:
+        raise ValueError("positions, freqs and axes go together")
+    H, qs = 0, (0, 0)
+    if q is not None:
+        qt, H, qd = q.shape
+        qs = q.stride()[:2]
+        if qt != total or qd != d:
+            raise ValueError("q must be [total, H, d]")
+        if q_out is not None:
+            _check(dev, (q_out, "q_out", torch.bfloat16, 3))
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    qw, kw, bf16 = _norm_weights(dev, d, q_weight, k_weight)
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        if q is not None and q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if total > 0:
+            a = _pack_norm_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                  0 if q is None else q.data_ptr(), 0 if q is None else q_out.data_ptr(), qw, kw,
+                                  slots.data_ptr(), pos, fp, ap, H, Hkv, total, pages, ps, d, *qs, *k.stride()[:2],
+                                  *v.stride()[:2], pos_stride, pairs, num_axes, PAIRINGS[pairing], bf16, float(eps), 0)
+            st = (_lib or load()).attn_norm_rope_append(a, torch._C._cuda_getCurrentRawStream(dev))
+            if st != 0:
+                raise AttnError(st, "attn_norm_rope_append")
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return q_out
+
+
+def attn_paged_reserve(seqlens_k, cu_seqlens_new, block_table, pages_held, free_pages, free_count, page_size: int,
+                       total: int = 0, shared_pages=None, held_out=None, count_out=None, slots=None, positions=None,
+                       stream=None):
+    """The pages and slots of a step's new tokens, from the requests' lengths, on the GPU: sequences take the pages that they
+    lack from a stack of free ones and give back those they no longer need, and every new token gets its slot.
+
+    All int32 CUDA tensors but ``slots``.  ``seqlens_k``: [B] lengths WITH the new tokens (0: the sequence has ended);
+    ``cu_seqlens_new``: [B + 1] offsets of each sequence's new tokens among the step's ``total``; ``block_table``:
+    [B, max_pages], of which ``pages_held`` [B] says how many entries each sequence has; ``free_pages``: [capacity], of
+    which the first ``free_count`` [1] are free (the end is the stack's top); ``shared_pages``: optional [B], leading entries
+    that belong to a shared prefix and are never given back (at most pages_held).  The table, the stack, and
+    ``pages_held`` and ``free_count`` (unless ``held_out`` / ``count_out`` take the new ones) are rewritten in place.
+    ``slots``: optional int64 [total] output (without it ``total`` says how many tokens the step has), the row of the cache
+    of each token, -1 for rows outside every sequence; ``positions``: optional int32 [total] output, each
+    token's place in its sequence.  Bad lengths, offsets or counts, or too few free pages, change nothing, make
+    every slot -1 and are reported by :func:`cache_device_status`.  Returns ``(slots, positions)``."""
+    import torch
+    dev = _device_of(block_table, "block_table", torch.int32, 2)
+    held_out = pages_held if held_out is None else held_out
+    count_out = free_count if count_out is None else count_out
+    i32 = torch.int32
+    _check(dev, (block_table, "block_table", i32, 2), (seqlens_k, "seqlens_k", i32, 1),
+           (cu_seqlens_new, "cu_seqlens_new", i32, 1), (pages_held, "pages_held", i32, 1), (held_out, "held_out", i32, 1),
+           (free_pages, "free_pages", i32, 1), (free_count, "free_count", i32, 1), (count_out, "count_out", i32, 1))
+    B, most = block_table.shape
+    if seqlens_k.shape[0] != B or pages_held.shape[0] != B or held_out.shape[0] != B:
+        raise ValueError("seqlens_k, pages_held and held_out must hold one number per row of block_table")
+    if cu_seqlens_new.shape[0] != B + 1:
+        raise ValueError("cu_seqlens_new must hold B + 1 offsets")
+    if free_count.shape[0] != 1 or count_out.shape[0] != 1:
+        raise ValueError("free_count and count_out must hold one number")
+    if shared_pages is not None:
+        _check(dev, (shared_pages, "shared_pages", i32, 1))
+        if shared_pages.shape[0] != B:
+            raise ValueError("shared_pages must hold one number per row of block_table")
+    total = int(total)
+    if slots is not None:
+        _check(dev, (slots, "slots", torch.int64, 1))
+        if total not in (0, slots.shape[0]):
+            raise ValueError("slots must hold one slot per token")
+        total = slots.shape[0]
+    if positions is not None:
+        _check(dev, (positions, "positions", i32, 1))
+        if positions.shape[0] != total:
+            raise ValueError("positions must hold one number per token")
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        if slots is None:
+            slots = torch.empty(total, dtype=torch.int64, device=block_table.device)
+        if positions is None:
+            positions = torch.empty(total, dtype=i32, device=block_table.device)
+        a = _pack_reserve(seqlens_k.data_ptr(), cu_seqlens_new.data_ptr(), block_table.data_ptr(), pages_held.data_ptr(),
+                          held_out.data_ptr(), 0 if shared_pages is None else shared_pages.data_ptr(), free_pages.data_ptr(),
+                          free_count.data_ptr(), count_out.data_ptr(), slots.data_ptr(), positions.data_ptr(), B, most,
+                          int(page_size), free_pages.shape[0], total)
+        st = (_lib or load()).attn_paged_reserve(a, torch._C._cuda_getCurrentRawStream(dev))
+        if st != 0:
+            raise AttnError(st, "attn_paged_reserve")
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return slots, positions
+
+
 def cache_device_status(stream=None) -> tuple:
-    """Synchronize ``stream`` and read/clear the status word of the rope, append, decode and evict kernels on its
-    device (of a stream by its handle: on the current device): (status, check)."""
+    """Synchronize ``stream`` and read/clear the status word of the kernels around the cache (from
+    :func:`attn_rope` on) on its device (of a stream by its handle: on the current device): (status, check)."""
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     handle, index = (s.cuda_stream, s.device_index) if hasattr(s, "cuda_stream") else (int(s), None)

@@ -1,5 +1,6 @@
 // attn_cache.cu -- host side of the calls around the paged K/V cache: rotary positions (rope.cuh),
-// appending (rope.cuh), attention of one new token (decode.cuh) and eviction (evict.cuh).
+// appending (rope.cuh), attention of one new token (decode.cuh) and eviction (evict.cuh); norms with positions
+// (norm_rope.cuh), pages and slots (reserve.cuh).
 #include <cuda_runtime.h>
 #include <string.h>
 
@@ -10,6 +11,8 @@
 #include "cache_common.cuh"
 #include "decode.cuh"
 #include "evict.cuh"
+#include "norm_rope.cuh"
+#include "reserve.cuh"
 #include "rope.cuh"
 
 namespace {
@@ -632,6 +635,302 @@ int run_evict(const attn_evict_args_t& a, void* workspace, size_t workspace_byte
     return launch(attn_evict_shift_kernel, rows * (2 * p.pieces + 1), 1, kShiftThreads, 0, stream, p);
 }
 
+// ------------------------------------------------------------------------------ norms with positions
+View rows_view(const void* p, const attn_norm_rope_args_t& a, int64_t heads, const int64_t* s) {
+    return view(p, a.B, a.S, heads, a.d, s[0], s[1], s[2]);
+}
+bool weight_ok(const void* w, int32_t bf16) { return ((uintptr_t)w & (bf16 ? 1u : 3u)) == 0; }
+bool weights_meet(const View& out, const void* w, int64_t d, int32_t bf16) {
+    return w && out.span() && overlap(out.at, out.end(), (uintptr_t)w, (uintptr_t)w + (uintptr_t)d * (bf16 ? 2 : 4));
+}
+
+// what attn_norm_rope and its gradient check alike: sizes, then pointers and strides
+int check_norm_rope_shape(const attn_norm_rope_args_t& a) {
+    const int64_t Hkv = a.k ? a.Hkv : 0;
+    if (a.B < 1 || a.S < 0 || a.H < 1 || (a.k && Hkv < 1)) return ATTN_ERR_INVALID_ARG;
+    if (!(a.eps >= 0.0f) || std::isinf(a.eps) || (a.weight_bf16 != 0 && a.weight_bf16 != 1) || a.reserved != 0)
+        return ATTN_ERR_INVALID_ARG;
+    const int st = check_pairs(a.pairs, a.num_axes, a.pairing, head_dim(a.d) ? a.d : 128);
+    if (st != ATTN_OK) return st;
+    if (!head_dim(a.d)) return ATTN_ERR_UNSUPPORTED;
+    if (a.B > kLim || a.S > kLim || a.H > kLim || Hkv > kLim || a.B * a.S > kLim || a.H + Hkv > kLim)
+        return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+int check_norm_rope(const attn_norm_rope_args_t& a) {
+    const int64_t Hkv = a.k ? a.Hkv : 0;
+    if (!a.q || !a.q_out || (a.k && !a.k_out)) return ATTN_ERR_INVALID_ARG;
+    if (a.pairs != 0 && (!a.positions || !a.freqs || !a.axes)) return ATTN_ERR_INVALID_ARG;
+    const int st = check_norm_rope_shape(a);
+    if (st != ATTN_OK) return st;
+    const int64_t nq[3] = {a.B, a.S, a.H}, nk[3] = {a.B, a.S, Hkv};
+    const int64_t np[2] = {a.num_axes, a.B}, ps[2] = {a.pos_axis_stride, a.pos_batch_stride};
+    if (!strides_ok(a.q_stride, nq, 3) || !strides_ok(a.q_out_stride, nq, 3)) return ATTN_ERR_INVALID_ARG;
+    if (a.pairs != 0 && !strides_ok(ps, np, 2)) return ATTN_ERR_INVALID_ARG;
+    if (a.k && (!strides_ok(a.k_stride, nk, 3) || !strides_ok(a.k_out_stride, nk, 3))) return ATTN_ERR_INVALID_ARG;
+    if (((uintptr_t)a.q | (uintptr_t)a.q_out | (uintptr_t)a.k | (a.k ? (uintptr_t)a.k_out : 0)) & 15u)
+        return ATTN_ERR_MISALIGNED;
+    if (a.pairs != 0 && (((uintptr_t)a.positions | (uintptr_t)a.axes) & 3u || (uintptr_t)a.freqs & 7u))
+        return ATTN_ERR_MISALIGNED;
+    if (!weight_ok(a.q_weight, a.weight_bf16) || !weight_ok(a.k_weight, a.weight_bf16)) return ATTN_ERR_MISALIGNED;
+    if (!strides_aligned(a.q_stride, nq, 3) || !strides_aligned(a.q_out_stride, nq, 3)) return ATTN_ERR_MISALIGNED;
+    if (a.k && (!strides_aligned(a.k_stride, nk, 3) || !strides_aligned(a.k_out_stride, nk, 3))) return ATTN_ERR_MISALIGNED;
+    const View qo = rows_view(a.q_out, a, a.H, a.q_out_stride);
+    const View ko = rows_view(a.k ? a.k_out : nullptr, a, Hkv, a.k_out_stride);
+    if (!nested(qo) || (a.k && (!nested(ko) || meet(qo, ko)))) return ATTN_ERR_ALIAS;
+    for (const void* w : {a.q_weight, a.k_weight})
+        if (weights_meet(qo, w, a.d, a.weight_bf16) || (a.k && weights_meet(ko, w, a.d, a.weight_bf16))) return ATTN_ERR_ALIAS;
+    return ATTN_OK;
+}
+
+void fill_norm_rope(NormRopeParams& p, const attn_norm_rope_args_t& a) {
+    memset(&p, 0, sizeof p);
+    p.x[0] = rope_tensor(a.q, a.q_out, a.q_stride, a.q_out_stride, a.H);
+    if (a.k) p.x[1] = rope_tensor(a.k, a.k_out, a.k_stride, a.k_out_stride, a.Hkv);
+    p.weight[0] = a.q_weight;
+    p.weight[1] = a.k_weight;
+    p.weight_bf16 = a.weight_bf16;
+    p.eps = a.eps;
+    p.positions = a.positions;
+    p.freqs = a.freqs;
+    p.axes = a.axes;
+    p.pos_axis = a.pos_axis_stride;
+    p.pos_b = a.pos_batch_stride;
+    p.S = a.S;
+    p.tokens = a.B * a.S;
+    p.pairs = a.pairs;
+    p.num_axes = a.num_axes;
+    p.heads = (int)(a.H + (a.k ? a.Hkv : 0));
+}
+
+template <bool kAppend>
+int launch_norm_rope(NormRopeParams& p, int64_t d, bool halves, int sms, cudaStream_t stream) {
+    // heads of a block as in launch_rope
+    const int64_t lanes = p.tokens * 32, full = (int64_t)sms * 2048, piece = kRopeHeads * (32 / (d / 16));
+    int64_t splits = lanes < full ? cdiv(full, lanes) : 1;
+    if (splits > cdiv(p.heads, piece)) splits = cdiv(p.heads, piece);
+    p.heads_per_block = (int)(cdiv(cdiv(p.heads, splits), piece) * piece);
+    const int64_t most = cdiv(p.tokens, kNormWarps), grid = most < 20 * sms ? most : 20 * sms;
+    const int gy = (int)cdiv(p.heads, p.heads_per_block);
+    if (gy > 65535) return ATTN_ERR_UNSUPPORTED;
+    auto* kernel = d == 128 ? (halves ? attn_norm_rope_kernel<128, true, kAppend> : attn_norm_rope_kernel<128, false, kAppend>)
+                            : (halves ? attn_norm_rope_kernel<64, true, kAppend> : attn_norm_rope_kernel<64, false, kAppend>);
+    return launch(kernel, grid, gy, kNormThreads, 0, stream, p);
+}
+
+int run_norm_rope(const attn_norm_rope_args_t& a, cudaStream_t stream) {
+    int st = check_norm_rope(a);
+    if (st != ATTN_OK) return st;
+    const View q = rows_view(a.q, a, a.H, a.q_stride), qo = rows_view(a.q_out, a, a.H, a.q_out_stride);
+    if (!same(q, qo) && meet(q, qo)) return ATTN_ERR_ALIAS;
+    if (a.k) {
+        const View k = rows_view(a.k, a, a.Hkv, a.k_stride), ko = rows_view(a.k_out, a, a.Hkv, a.k_out_stride);
+        if ((!same(k, ko) && meet(k, ko)) || meet(qo, k) || meet(ko, q)) return ATTN_ERR_ALIAS;
+    }
+    if (a.S == 0) return ATTN_OK;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    NormRopeParams p;
+    fill_norm_rope(p, a);
+    return launch_norm_rope<false>(p, a.d, a.pairs && a.pairing == ATTN_ROPE_HALVES, sms, stream);
+}
+
+// Blocks of the gradient's kernel: as many as fit at once, q's and k's in proportion to their heads (each block leaves
+// d sums to be added up).
+constexpr int kNormBwdBlocks = 4;      // an SM
+void norm_bwd_blocks(const attn_norm_rope_args_t& a, int sms, int (&blocks)[2]) {
+    const int64_t Hkv = a.k ? a.Hkv : 0, most = cdiv(a.B * a.S, kNormWarps), all = (int64_t)kNormBwdBlocks * sms;
+    int64_t k = a.k ? (all * Hkv + (a.H + Hkv) / 2) / (a.H + Hkv) : 0;
+    if (a.k && k < 1) k = 1;
+    if (k > all - 1) k = all - 1;
+    const int64_t q = all - k;
+    blocks[0] = (int)(most < 1 ? 1 : q < most ? q : most);
+    blocks[1] = (int)(a.k ? (most < 1 ? 1 : k < most ? k : most) : 0);
+}
+size_t norm_bwd_bytes(const attn_norm_rope_args_t& a, int sms) {
+    int blocks[2];
+    norm_bwd_blocks(a, sms, blocks);
+    return (size_t)(blocks[0] + blocks[1]) * (size_t)a.d * 4;
+}
+
+int run_norm_rope_bwd(const attn_norm_rope_bwd_args_t& g, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const attn_norm_rope_args_t& a = g.fwd;
+    int st = check_norm_rope(a);
+    if (st != ATTN_OK) return st;
+    if (!g.dq || (g.dk != nullptr) != (a.k != nullptr) || (g.dk_weight && !a.k)) return ATTN_ERR_INVALID_ARG;
+    const int64_t Hkv = a.k ? a.Hkv : 0, nq[3] = {a.B, a.S, a.H}, nk[3] = {a.B, a.S, Hkv};
+    if (!strides_ok(g.dq_stride, nq, 3) || (a.k && !strides_ok(g.dk_stride, nk, 3))) return ATTN_ERR_INVALID_ARG;
+    if (((uintptr_t)g.dq | (uintptr_t)g.dk) & 15u || ((uintptr_t)g.dq_weight | (uintptr_t)g.dk_weight) & 3u)
+        return ATTN_ERR_MISALIGNED;
+    if (!strides_aligned(g.dq_stride, nq, 3) || (a.k && !strides_aligned(g.dk_stride, nk, 3))) return ATTN_ERR_MISALIGNED;
+    // tensors read, and written; what is flat in memory
+    const View in[4] = {rows_view(a.q, a, a.H, a.q_stride), rows_view(g.dq, a, a.H, g.dq_stride),
+                        rows_view(a.k, a, Hkv, a.k_stride), rows_view(g.dk, a, Hkv, g.dk_stride)};
+    const View out[2] = {rows_view(a.q_out, a, a.H, a.q_out_stride), rows_view(a.k ? a.k_out : nullptr, a, Hkv, a.k_out_stride)};
+    struct { uintptr_t at, bytes; } flat[3] = {{(uintptr_t)g.dq_weight, g.dq_weight ? (uintptr_t)a.d * 4 : 0},
+                                               {(uintptr_t)g.dk_weight, g.dk_weight ? (uintptr_t)a.d * 4 : 0},
+                                               {0, 0}};
+    for (int o = 0; o < 2; ++o)
+        for (int i = 0; i < 4; ++i)
+            if (!(i == 2 * o + 1 && same(in[i], out[o])) && meet(in[i], out[o])) return ATTN_ERR_ALIAS;
+    auto clash = [&](int f) {
+        const uintptr_t b = flat[f].at, e = b + flat[f].bytes;
+        if (b == e) return false;
+        for (const View& v : in)
+            if (v.span() && overlap(b, e, v.at, v.end())) return true;
+        for (const View& v : out)
+            if (v.span() && overlap(b, e, v.at, v.end())) return true;
+        for (const void* w : {a.q_weight, a.k_weight})
+            if (w && overlap(b, e, (uintptr_t)w, (uintptr_t)w + (uintptr_t)a.d * (a.weight_bf16 ? 2 : 4))) return true;
+        for (int o = 0; o < f; ++o)
+            if (flat[o].bytes && overlap(b, e, flat[o].at, flat[o].at + flat[o].bytes)) return true;
+        return false;
+    };
+    if (clash(0) || clash(1)) return ATTN_ERR_ALIAS;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    const size_t need = norm_bwd_bytes(a, sms);            // (the workspace, once its size is known)
+    if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 15u) return ATTN_ERR_MISALIGNED;
+    flat[2].at = (uintptr_t)workspace;
+    flat[2].bytes = need;
+    if (clash(2)) return ATTN_ERR_ALIAS;
+    NormRopeParams p;
+    fill_norm_rope(p, a);
+    p.dy[0] = rope_tensor(g.dq, nullptr, g.dq_stride, g.dq_stride, a.H);
+    if (a.k) p.dy[1] = rope_tensor(g.dk, nullptr, g.dk_stride, g.dk_stride, Hkv);
+    p.part = reinterpret_cast<float*>(workspace);
+    p.dw[0] = g.dq_weight;
+    p.dw[1] = g.dk_weight;
+    norm_bwd_blocks(a, sms, p.blocks);
+    const bool halves = a.pairs && a.pairing == ATTN_ROPE_HALVES;
+    auto* kernel = a.d == 128 ? (halves ? attn_norm_rope_bwd_kernel<128, true> : attn_norm_rope_bwd_kernel<128, false>)
+                              : (halves ? attn_norm_rope_bwd_kernel<64, true> : attn_norm_rope_bwd_kernel<64, false>);
+    if ((st = launch(kernel, p.blocks[0] + p.blocks[1], 1, kNormThreads, 0, stream, p)) != ATTN_OK) return st;
+    if (!p.dw[0] && !p.dw[1]) return ATTN_OK;
+    const int64_t grid = (a.k ? 2 : 1) * (a.d / 32);
+    return a.d == 128 ? launch(attn_norm_rope_dw_kernel<128>, grid, 1, 32 * kDwRows, 0, stream, p)
+                      : launch(attn_norm_rope_dw_kernel<64>, grid, 1, 32 * kDwRows, 0, stream, p);
+}
+
+int run_norm_append(const attn_norm_append_args_t& a, cudaStream_t stream) {
+    const int64_t H = a.q ? a.H : 0;
+    if (!a.k || !a.v || !a.k_cache || !a.v_cache || (a.q && !a.q_out) || !a.slots) return ATTN_ERR_INVALID_ARG;
+    if (a.pairs != 0 && (!a.positions || !a.freqs || !a.axes)) return ATTN_ERR_INVALID_ARG;
+    int st = check_cache(1, a.Hkv, a.num_pages, a.page_size, 1, a.d);
+    if (st != ATTN_OK) return st;
+    if (a.total < 0 || (a.q && H < 1) || a.reserved != 0 || a.pos_axis_stride < 0 ||
+        a.pos_axis_stride > ((int64_t)1 << 40))
+        return ATTN_ERR_INVALID_ARG;
+    if (!(a.eps >= 0.0f) || std::isinf(a.eps) || (a.weight_bf16 != 0 && a.weight_bf16 != 1)) return ATTN_ERR_INVALID_ARG;
+    if ((st = check_pairs(a.pairs, a.num_axes, a.pairing, a.d)) != ATTN_OK) return st;
+    if (a.total > kLim || H > kLim || H + 2 * a.Hkv > kLim) return ATTN_ERR_UNSUPPORTED;
+    const int64_t nk[2] = {a.total, a.Hkv}, nq[2] = {a.total, H};
+    if (!strides_ok(a.k_stride, nk, 2) || !strides_ok(a.v_stride, nk, 2) || (a.q && !strides_ok(a.q_stride, nq, 2)))
+        return ATTN_ERR_INVALID_ARG;
+    if (((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache | (uintptr_t)a.q |
+         (a.q ? (uintptr_t)a.q_out : 0)) & 15u)
+        return ATTN_ERR_MISALIGNED;
+    if ((uintptr_t)a.slots & 7u) return ATTN_ERR_MISALIGNED;
+    if (a.pairs && (((uintptr_t)a.positions | (uintptr_t)a.axes) & 3u || (uintptr_t)a.freqs & 7u)) return ATTN_ERR_MISALIGNED;
+    if (!weight_ok(a.q_weight, a.weight_bf16) || !weight_ok(a.k_weight, a.weight_bf16)) return ATTN_ERR_MISALIGNED;
+    if (!strides_aligned(a.k_stride, nk, 2) || !strides_aligned(a.v_stride, nk, 2) ||
+        (a.q && !strides_aligned(a.q_stride, nq, 2)))
+        return ATTN_ERR_MISALIGNED;
+    const int64_t qs[3] = {0, a.q_stride[0], a.q_stride[1]}, qo[3] = {0, H * a.d, a.d};
+    const int64_t ks[3] = {0, a.k_stride[0], a.k_stride[1]}, vs[3] = {0, a.v_stride[0], a.v_stride[1]};
+    const int64_t co[3] = {0, a.Hkv * a.d, a.d};
+    auto v = [&](const void* p, int64_t rows, int64_t heads, const int64_t* s) {
+        return view(p, 1, rows, heads, a.d, 0, s[1], s[2]);
+    };
+    auto hits = [](const View& x, const View& y) { return x.span() && y.span() && overlap(x.at, x.end(), y.at, y.end()); };
+    const int64_t rows = a.num_pages * a.page_size;
+    const View in[3] = {v(a.k, a.total, a.Hkv, ks), v(a.v, a.total, a.Hkv, vs), v(a.q, a.total, H, qs)};
+    const View kc = v(a.k_cache, rows, a.Hkv, co), vc = v(a.v_cache, rows, a.Hkv, co), out = v(a.q ? a.q_out : nullptr, a.total, H, qo);
+    if (hits(kc, vc) || hits(out, kc) || hits(out, vc)) return ATTN_ERR_ALIAS;
+    for (const View& x : in)
+        if (hits(x, kc) || hits(x, vc) || (!(&x == &in[2] && same(x, out)) && meet(x, out))) return ATTN_ERR_ALIAS;
+    for (const void* w : {a.q_weight, a.k_weight})
+        for (const View* o : {&kc, &vc, &out})
+            if (weights_meet(*o, w, a.d, a.weight_bf16)) return ATTN_ERR_ALIAS;
+    if (a.total == 0) return ATTN_OK;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    NormRopeParams p;
+    memset(&p, 0, sizeof p);
+    if (a.q) p.x[0] = rope_tensor(a.q, a.q_out, qs, qo, H);
+    p.x[1] = rope_tensor(a.k, a.k_cache, ks, co, a.Hkv);
+    p.x[2] = rope_tensor(a.v, a.v_cache, vs, co, a.Hkv);
+    p.weight[0] = a.q_weight;
+    p.weight[1] = a.k_weight;
+    p.weight_bf16 = a.weight_bf16;
+    p.eps = a.eps;
+    p.positions = a.positions;
+    p.freqs = a.freqs;
+    p.axes = a.axes;
+    p.pos_axis = a.pos_axis_stride;
+    p.S = p.tokens = a.total;
+    p.pairs = a.pairs;
+    p.num_axes = a.num_axes;
+    p.heads = (int)(H + 2 * a.Hkv);
+    p.slots = a.slots;
+    p.rows = rows;
+    return launch_norm_rope<true>(p, a.d, a.pairs && a.pairing == ATTN_ROPE_HALVES, sms, stream);
+}
+
+// ------------------------------------------------------------------------------ pages and slots
+int run_reserve(const attn_reserve_args_t& a, cudaStream_t stream) {
+    if (!a.seqlens_k || !a.cu_seqlens_new || !a.block_table || !a.pages_held || !a.held_out || !a.free_pages ||
+        !a.free_count || !a.count_out || (a.total > 0 && !a.slots))
+        return ATTN_ERR_INVALID_ARG;
+    int st = check_cache(a.B, 1, 1, a.page_size, a.max_pages, 128);
+    if (st != ATTN_OK) return st;
+    if (a.capacity < 1 || a.total < 0) return ATTN_ERR_INVALID_ARG;
+    if (a.capacity > kLim || a.total > kLim) return ATTN_ERR_UNSUPPORTED;
+    const uintptr_t B = (uintptr_t)a.B;
+    const struct { uintptr_t at, bytes; bool written; } all[] = {
+        {(uintptr_t)a.seqlens_k, B * 4, false},
+        {(uintptr_t)a.cu_seqlens_new, (B + 1) * 4, false},
+        {(uintptr_t)a.shared_pages, a.shared_pages ? B * 4 : 0, false},
+        {(uintptr_t)a.pages_held, a.pages_held != a.held_out ? B * 4 : 0, false},
+        {(uintptr_t)a.free_count, a.free_count != a.count_out ? 4u : 0u, false},
+        {(uintptr_t)a.block_table, B * (uintptr_t)a.max_pages * 4, true},
+        {(uintptr_t)a.free_pages, (uintptr_t)a.capacity * 4, true},
+        {(uintptr_t)a.held_out, B * 4, true},
+        {(uintptr_t)a.count_out, 4, true},
+        {(uintptr_t)a.positions, a.positions ? (uintptr_t)a.total * 4 : 0, true},
+        {(uintptr_t)a.slots, (uintptr_t)a.total * 8, true}};
+    for (const auto& x : all) {
+        if (x.at & 3u) return ATTN_ERR_MISALIGNED;
+        for (const auto& y : all)
+            if (&x != &y && (x.written || y.written) && x.bytes && y.bytes && overlap(x.at, x.at + x.bytes, y.at, y.at + y.bytes))
+                return ATTN_ERR_ALIAS;
+    }
+    if ((uintptr_t)a.slots & 7u) return ATTN_ERR_MISALIGNED;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    ReserveParams p;
+    memset(&p, 0, sizeof p);
+    p.seqlens = a.seqlens_k;
+    p.cu_new = a.cu_seqlens_new;
+    p.table = a.block_table;
+    p.held = a.pages_held;
+    p.held_out = a.held_out;
+    p.shared = a.shared_pages;
+    p.free_pages = a.free_pages;
+    p.count = a.free_count;
+    p.count_out = a.count_out;
+    p.slots = a.slots;
+    p.positions = a.positions;
+    p.pages = make_pages(a.block_table, 1, a.page_size, a.max_pages);
+    p.B = (int)a.B;
+    p.capacity = (int)a.capacity;
+    p.total = a.total;
+    // a CTA while every thread has at most one token, else a cluster of them
+    const int ctas = a.total > kReserveThreads ? 8 : 1;
+    return launch_clusters(attn_reserve_kernel, ctas, ctas, kReserveThreads, 0, stream, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -660,6 +959,28 @@ size_t attn_paged_evict_workspace_size(const attn_evict_args_t* args) {
 
 int attn_paged_evict(const attn_evict_args_t* args, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
     return args ? run_evict(*args, workspace, workspace_bytes, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
+}
+
+int attn_norm_rope(const attn_norm_rope_args_t* args, attn_stream_t stream) {
+    return args ? run_norm_rope(*args, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
+}
+
+size_t attn_norm_rope_bwd_workspace_size(const attn_norm_rope_bwd_args_t* args) {
+    int sms = 0;
+    if (!args || check_norm_rope_shape(args->fwd) != ATTN_OK || device(&sms) != ATTN_OK) return 0;
+    return norm_bwd_bytes(args->fwd, sms);
+}
+
+int attn_norm_rope_bwd(const attn_norm_rope_bwd_args_t* args, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+    return args ? run_norm_rope_bwd(*args, workspace, workspace_bytes, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
+}
+
+int attn_norm_rope_append(const attn_norm_append_args_t* args, attn_stream_t stream) {
+    return args ? run_norm_append(*args, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
+}
+
+int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream) {
+    return args ? run_reserve(*args, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
 }
 
 int attn_cache_get_device_status(attn_stream_t stream, int32_t* site) {

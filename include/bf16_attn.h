@@ -6,7 +6,8 @@
  * grouped K/V heads and the row log-sum-exp (attn_fwd_ex), variable-length batches
  * (attn_fwd_varlen), a paged K/V cache (attn_fwd_paged), the backward (attn_bwd), and what
  * surrounds a paged cache: rotary positions (attn_rope), appending (attn_paged_append), one-token
- * decoding (attn_paged_decode) and eviction (attn_paged_evict).  Source: "MoonMath AI open-sources
+ * decoding (attn_paged_decode) and eviction (attn_paged_evict); norms of queries and keys with their positions
+ * (attn_norm_rope, attn_norm_rope_append) and pages and slots (attn_paged_reserve).  Source: "MoonMath AI open-sources
  * a HIP attention kernel for AMD MI300X that beats AITER" (news.chathome.org), opening section: attention is the fused
  * softmax(QK^T/sqrt(d))V; the kernel takes BSHD or BHSD tensors without transposes, head
  * dimension fixed at 128, any query and key length including cross-attention; its
@@ -449,9 +450,10 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
                     attn_stream_t stream);
 
 /*
- * Around the paged K/V cache: rotary positions, appending, attention of one new token, eviction.
+ * Around the paged K/V cache: rotary positions, appending, attention of one new token, eviction; norms with positions,
+ * pages and slots.
  *
- * Common to the four calls.  Tensors are bf16 with head dimension d = 128 or 64 unless said
+ * Common to these calls.  Tensors are bf16 with head dimension d = 128 or 64 unless said
  * otherwise, device pointers 16-byte aligned (int32 and fp32 tensors 4-byte, fp64 8-byte).  The
  * cache is k_cache, v_cache bf16 [num_pages][page_size][Hkv][d] with any page_size >= 1; key j of
  * sequence b is slot j % page_size of page block_table[b * max_pages + j / page_size], as in
@@ -466,6 +468,8 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
 #define ATTN_CACHE_SITE_APPEND 21   /* a new token's slot or page is not in the cache: k, v not written  */
 #define ATTN_CACHE_SITE_DECODE 22   /* a bad length or page: that sequence's outputs are not written    */
 #define ATTN_CACHE_SITE_EVICT 23    /* a bad length, or of a sequence to be cut a bad page or one used twice: it stays */
+#define ATTN_CACHE_SITE_SLOTS 24    /* a slot outside the cache (other than -1): k, v not written               */
+#define ATTN_CACHE_SITE_RESERVE 25  /* bad lengths, offsets, counts, or too few free pages: nothing is reserved */
 
 /* Which elements of a head form pair p of `pairs`: 2p and 2p + 1, or p and p + pairs. */
 typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_t;
@@ -612,7 +616,133 @@ size_t attn_paged_evict_workspace_size(const attn_evict_args_t* args);
 int attn_paged_evict(const attn_evict_args_t* args, void* workspace, size_t workspace_bytes,
                      attn_stream_t stream);
 
-/* Synchronize `stream`, then read and clear the current device's status word of these four calls' kernels. */
+/*
+ * attn_norm_rope -- norms of queries and keys, head by head, with their rotary positions in the same pass:
+ *   y = R(x * w / sqrt(mean(x^2) + eps)), R the rotation of attn_rope, computed in fp32 and rounded once (nearest even).
+ *   q, k, q_out, k_out, positions, freqs, axes, pairing, strides   as in attn_rope
+ *   q_weight, k_weight   [d], fp32 or bf16 (weight_bf16 = 1); NULL: ones
+ *   eps           >= 0, finite
+ *   pairs         0 .. d / 2; 0: no rotation, positions, freqs and axes are ignored (num_axes >= 1 all the same)
+ * The squares are summed in fp32: heads with elements past about 10^19 come out zero (NaN where they are infinite).
+ */
+typedef struct {
+    const void* q;
+    void* q_out;
+    const void* k;
+    void* k_out;
+    const void* q_weight;
+    const void* k_weight;
+    const int32_t* positions;
+    const double* freqs;
+    const int32_t* axes;
+    int64_t B, S, H, Hkv, d;
+    int64_t q_stride[3], q_out_stride[3], k_stride[3], k_out_stride[3];
+    int64_t pos_axis_stride, pos_batch_stride;
+    int32_t pairs, num_axes, pairing, weight_bf16;
+    float eps;
+    int32_t reserved;
+} attn_norm_rope_args_t;
+
+int attn_norm_rope(const attn_norm_rope_args_t* args, attn_stream_t stream);
+
+/*
+ * attn_norm_rope_bwd -- the gradient of attn_norm_rope: from the gradients of its outputs those of q, k and the weights.
+ *   fwd           the forward's arguments: q, k, weights, tables, sizes, q_stride and k_stride; its q_out and k_out, with
+ *                 q_out_stride and k_out_stride, take the gradients of q and k
+ *   dq, dk        the gradients of the forward's outputs, with strides of their own; dk NULL exactly when fwd.k is.  The
+ *                 outputs may be dq and dk themselves (same pointer and strides), and otherwise overlap no input or output
+ *   dq_weight, dk_weight   fp32 [d], the sums over tokens and heads; NULL: not wanted
+ * dq, dk and the weights' gradients are bitwise reproducible for the same sizes on the same GPU model.  Two kernels run,
+ * the second (the weights' last sums) where a weight's gradient is wanted.  With a bad axis nothing is written.
+ * workspace: caller device memory of at least attn_norm_rope_bwd_workspace_size() bytes, 16-byte aligned; calls that may
+ * run at the same time need one each.
+ */
+typedef struct {
+    attn_norm_rope_args_t fwd;
+    const void* dq;
+    const void* dk;
+    float* dq_weight;
+    float* dk_weight;
+    int64_t dq_stride[3], dk_stride[3];
+} attn_norm_rope_bwd_args_t;
+
+size_t attn_norm_rope_bwd_workspace_size(const attn_norm_rope_bwd_args_t* args);
+int attn_norm_rope_bwd(const attn_norm_rope_bwd_args_t* args, void* workspace, size_t workspace_bytes,
+                       attn_stream_t stream);
+
+/*
+ * attn_norm_rope_append -- attn_norm_rope on the way into a paged cache: new tokens' keys (normed and rotated) and
+ * values are written to the slots that attn_paged_reserve gave them, the queries beside them.
+ *   k, v, q, q_out   as in attn_paged_append
+ *   slots            device int64 [total]: a token's row of the cache, page * page_size + its place in the page; -1: the
+ *                    token is not read or written, its row of q_out neither.  Another slot outside the cache is reported at
+ *                    ATTN_CACHE_SITE_SLOTS: that token's k and v are not written.  Two tokens of one slot leave either's data
+ *   weights, eps, positions, freqs, axes, pairs   as in attn_norm_rope, positions [num_axes] x [total]
+ */
+typedef struct {
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    const void* q;
+    void* q_out;
+    const void* q_weight;
+    const void* k_weight;
+    const int64_t* slots;
+    const int32_t* positions;
+    const double* freqs;
+    const int32_t* axes;
+    int64_t H, Hkv, total, num_pages, page_size, d;
+    int64_t q_stride[2], k_stride[2], v_stride[2];
+    int64_t pos_axis_stride;
+    int32_t pairs, num_axes, pairing, weight_bf16;
+    float eps;
+    int32_t reserved;
+} attn_norm_append_args_t;
+
+int attn_norm_rope_append(const attn_norm_append_args_t* args, attn_stream_t stream);
+
+/*
+ * attn_paged_reserve -- the pages and slots of a step, on the GPU, from the requests' lengths: what stands before
+ * attn_paged_append or attn_norm_rope_append.
+ *   seqlens_k        device int32 [B]: lengths WITH the new tokens, 0 .. max_pages * page_size
+ *   cu_seqlens_new   device int32 [B + 1]: sequence b's new tokens are rows cu[b] .. cu[b+1] - 1 of the step's `total`
+ *                    (no more than its length); rows outside every sequence are padding
+ *   block_table      device int32 [B][max_pages], of which sequence b's first pages_held[b] entries are its pages
+ *   pages_held       device int32 [B];  held_out: the same after the call, max(ceil(length / page_size), shared_pages);
+ *                    may be pages_held itself
+ *   shared_pages     device int32 [B], or NULL (none): leading entries that belong to a shared prefix and are never given
+ *                    back; at most pages_held
+ *   free_pages       device int32 [capacity]: a stack of free pages, the first free_count[0] of them
+ *   free_count       device int32 [1];  count_out: the same after the call, may be free_count itself
+ *   slots            device int64 [total]: each new token's row of the cache, -1 for padding
+ *   positions        device int32 [total] or NULL: each new token's place in its sequence, 0 for padding
+ * Pages that a sequence holds past what its length wants (after eviction; all of them for one that has ended, length 0)
+ * go on top of the stack, in the order (sequence, page); after that the missing pages come off its top in the same order,
+ * and their entries are written to the table.  Entries past held_out stay as they are.
+ * All or nothing: bad lengths, offsets or counts, a stack without room for what comes back, or fewer free pages than are
+ * missing leave table, stack and counts as they were, give every token the slot -1 and position 0, and are reported
+ * at ATTN_CACHE_SITE_RESERVE.  Page numbers are not looked at (the calls that use them check them).
+ */
+typedef struct {
+    const int32_t* seqlens_k;
+    const int32_t* cu_seqlens_new;
+    int32_t* block_table;
+    const int32_t* pages_held;
+    int32_t* held_out;
+    const int32_t* shared_pages;
+    int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* count_out;
+    int64_t* slots;
+    int32_t* positions;
+    int64_t B, max_pages, page_size, capacity, total;
+} attn_reserve_args_t;
+
+int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
+
+/* Synchronize `stream`, then read and clear the current device's status word of these calls' kernels (all from attn_rope
+ * on). */
 int attn_cache_get_device_status(attn_stream_t stream, int32_t* site);
 
 #ifdef __cplusplus

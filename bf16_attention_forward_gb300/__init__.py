@@ -30,7 +30,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_ws", "attn_fwd_noalloc", "attn_fwd_ex", "attn_f
            "attn_rope", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size",
            "attn_paged_evict", "attn_paged_evict_workspace_size", "attn_norm_rope", "attn_norm_rope_bwd",
            "attn_norm_rope_bwd_workspace_size", "attn_norm_rope_append", "attn_paged_reserve",
-           "attn_cache_get_device_status")
+           "attn_paged_prefix_decode", "attn_paged_prefix_decode_workspace_size", "attn_cache_get_device_status")
 
 
 class AttnError(RuntimeError):
@@ -237,6 +237,10 @@ def load(path: str | None = None):
             getattr(lib, name).argtypes = [vp, vp, ctypes.c_size_t, vp]
             getattr(lib, name + "_workspace_size").restype = ctypes.c_size_t
             getattr(lib, name + "_workspace_size").argtypes = [vp]
+        lib.attn_paged_prefix_decode.restype = i32
+        lib.attn_paged_prefix_decode.argtypes = [vp, i64, vp, ctypes.c_size_t, vp]
+        lib.attn_paged_prefix_decode_workspace_size.restype = ctypes.c_size_t
+        lib.attn_paged_prefix_decode_workspace_size.argtypes = [vp, i64]
         lib.attn_cache_get_device_status.restype = i32
         lib.attn_cache_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         lib.attn_plan.restype = i32
@@ -963,6 +967,29 @@ def _check_workspace(workspace, index):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _check_decode(q, k_cache, v_cache, seqlens_k, block_table, o, lse, round):
+    """Checks the tensors of a decoding call; returns (device index, pages, page size, Hkv, d, B, max pages, H)."""
+    import torch
+    if round not in MODES:
+        raise ValueError("round must be rtne/rtna/rtz")
+    dev, pages, ps, Hkv, dc, Bc, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
+    _check(dev, (q, "q", torch.bfloat16, 3))
+    B, H, d = q.shape
+    if B != Bc or d != dc:
+        raise ValueError("q must be [B, H, d] with seqlens_k's B and the cache's d")
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError("k/v heads (%d) must divide the query heads (%d)" % (Hkv, H))
+    if o is not None:
+        _check(dev, (o, "o", torch.bfloat16, 3))
+        if o.shape != q.shape:
+            raise ValueError("o must be shaped like q")
+    if lse is not None:
+        _check(dev, (lse, "lse", torch.float32, 2))
+        if lse.shape != (B, H):
+            raise ValueError("lse must be [B, H]")
+    return dev, pages, ps, Hkv, d, B, most, H
+
+
 def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None, o=None, lse=None,
                       round: str = "rtne", return_lse: bool = False, stream=None, workspace=None):
     """Attention of one new token per sequence over a paged K/V cache.
@@ -976,27 +1003,11 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
     :func:`cache_device_status`.  ``workspace``: optional caller tensor (calls that may run at the same
     time need one each); without it one is allocated here.  Returns ``o`` or ``(o, lse)`` (lse fp32 [B, H])."""
     import torch
-    if round not in MODES:
-        raise ValueError("round must be rtne/rtna/rtz")
-    dev, pages, ps, Hkv, dc, Bc, most = _check_cache(k_cache, v_cache, block_table, seqlens_k)
-    _check(dev, (q, "q", torch.bfloat16, 3))
-    B, H, d = q.shape
-    if B != Bc or d != dc:
-        raise ValueError("q must be [B, H, d] with seqlens_k's B and the cache's d")
-    if Hkv < 1 or H % Hkv != 0:
-        raise ValueError("k/v heads (%d) must divide the query heads (%d)" % (Hkv, H))
+    dev, pages, ps, Hkv, d, B, most, H = _check_decode(q, k_cache, v_cache, seqlens_k, block_table, o, lse, round)
     if weights is not None:
         _check(dev, (weights, "weights", torch.float32, 3))
         if weights.shape != (B, Hkv, most * ps):
             raise ValueError("weights must be [B, Hkv, max_pages * page_size]")
-    if o is not None:
-        _check(dev, (o, "o", torch.bfloat16, 3))
-        if o.shape != q.shape:
-            raise ValueError("o must be shaped like q")
-    if lse is not None:
-        _check(dev, (lse, "lse", torch.float32, 2))
-        if lse.shape != (B, H):
-            raise ValueError("lse must be [B, H]")
     ws_bytes = 0
     if workspace is not None:
         workspace, ws_bytes = _check_workspace(workspace, dev)
@@ -1021,6 +1032,57 @@ def attn_paged_decode(q, k_cache, v_cache, seqlens_k, block_table, weights=None,
                                                 torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise AttnError(st, "attn_paged_decode")
+    finally:
+        if on is not None:
+            on.__exit__(None, None, None)
+    return o if lse is None else (o, lse)
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace_bytes(index, prefix_len, *shape):
+    """attn_paged_prefix_decode's workspace size, by shapes and device (which has to be current)."""
+    a = DecodeArgs()
+    for n, x in shape:
+        setattr(a, n, x)
+    return int(load().attn_paged_prefix_decode_workspace_size(ctypes.byref(a), prefix_len))
+
+
+def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix_len: int, o=None, lse=None,
+                             round: str = "rtne", return_lse: bool = False, stream=None, workspace=None):
+    """:func:`attn_paged_decode` for a batch whose sequences all begin with the same ``prefix_len`` keys (one instruction,
+    one document): those are read once for the whole batch, through ``block_table``'s first row.
+
+    Arguments as there; ``seqlens_k`` holds whole lengths (prefix_len or more), and a row's entries from the page that the
+    prefix ends in on are its own (its entries of pages that end inside the prefix are not read, but in the first row).
+    A sequence with another length or a bad page of its own is not written and is reported by
+    :func:`cache_device_status`; a bad page of the prefix leaves every sequence unwritten.  ``workspace``: optional caller tensor
+    (calls that may run at the same time need one each).  Returns ``o`` or ``(o, lse)`` (lse fp32 [B, H])."""
+    import torch
+    dev, pages, ps, Hkv, d, B, most, H = _check_decode(q, k_cache, v_cache, seqlens_k, block_table, o, lse, round)
+    prefix_len, ws_bytes = int(prefix_len), 0
+    if not 1 <= prefix_len <= most * ps:
+        raise ValueError("prefix_len must be 1 .. max_pages * page_size")
+    if workspace is not None:
+        workspace, ws_bytes = _check_workspace(workspace, dev)
+    on = _on(dev, stream)
+    if on is not None:
+        on.__enter__()
+    try:
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None and return_lse:
+            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        a = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                         0 if lse is None else lse.data_ptr(), 0, seqlens_k.data_ptr(), block_table.data_ptr(), B, H, Hkv,
+                         pages, ps, most, d, MODES[round], 0)
+        if workspace is None:
+            ws_bytes = _prefix_workspace_bytes(dev, prefix_len, ("B", B), ("H", H), ("Hkv", Hkv), ("num_pages", pages),
+                                               ("page_size", ps), ("max_pages", most), ("d", d))
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        st = (_lib or load()).attn_paged_prefix_decode(a, prefix_len, workspace.data_ptr(), ws_bytes,
+                                                       torch._C._cuda_getCurrentRawStream(dev))
+        if st != 0:
+            raise AttnError(st, "attn_paged_prefix_decode")
     finally:
         if on is not None:
             on.__exit__(None, None, None)

@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, n) for n in ("attn_fwd.cu", "attn_bwd.cu", "attn_cache.cu")]
 HEADERS = [os.path.join(CSRC, n) for n in ("ptx.cuh", "cache_common.cuh", "rope.cuh", "decode.cuh", "evict.cuh",
-                                         "norm_rope.cuh", "reserve.cuh")] + \
+                                         "norm_rope.cuh", "prefix.cuh", "reserve.cuh")] + \
           [os.path.join(os.path.dirname(HERE), "include", "bf16_attn.h")]
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libbf16attn.so")

@@ -1,6 +1,6 @@
 // attn_cache.cu -- host side of the calls around the paged K/V cache: rotary positions (rope.cuh),
 // appending (rope.cuh), attention of one new token (decode.cuh) and eviction (evict.cuh); norms with positions
-// (norm_rope.cuh), pages and slots (reserve.cuh).
+// (norm_rope.cuh), pages and slots (reserve.cuh), and one new token behind a shared prefix (prefix.cuh).
 #include <cuda_runtime.h>
 #include <string.h>
 
@@ -12,6 +12,7 @@
 #include "decode.cuh"
 #include "evict.cuh"
 #include "norm_rope.cuh"
+#include "prefix.cuh"
 #include "reserve.cuh"
 #include "rope.cuh"
 
@@ -30,9 +31,17 @@ Device g_dev[kMaxDevices];
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+template <int D, bool kSingle>
+cudaError_t set_prefix_attr() {
+    return cudaFuncSetAttribute(attn_prefix_kernel<D, kSingle>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PfGeo<D, kSingle>::kSmem);
+}
 template <int D, int NH>
 cudaError_t set_decode_attr() {
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         DecGeo<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          DecGeo<D>::kSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -56,7 +65,9 @@ int device(int* sms) {
         if (d.major == 10 && d.minor == 3 &&
             (set_decode_attr<128, 1>() != cudaSuccess || set_decode_attr<128, 2>() != cudaSuccess ||
              set_decode_attr<128, 4>() != cudaSuccess || set_decode_attr<64, 1>() != cudaSuccess ||
-             set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess)) {
+             set_decode_attr<64, 2>() != cudaSuccess || set_decode_attr<64, 4>() != cudaSuccess ||
+             set_prefix_attr<128, false>() != cudaSuccess || set_prefix_attr<128, true>() != cudaSuccess ||
+             set_prefix_attr<64, false>() != cudaSuccess || set_prefix_attr<64, true>() != cudaSuccess)) {
             cudaGetLastError();
             return ATTN_ERR_CUDA;
         }
@@ -402,9 +413,9 @@ int head_tiles(int64_t group) { return group <= 8 ? 1 : group <= 16 ? 2 : 4; }
 // us a call in a graph, d = 128, split / whole:  8 rows of 2 tiles 7.0 / 4.8, 5 tiles 7.0 / 7.1, 8 tiles 7.2 / 9.4;
 // 16 x 8 rows of 2 tiles 7.8 / 5.2, 5 tiles 11.8 / 8.0, 8 tiles 14.5 / 10.8.
 // (Short rows in a wide table are split: 2 rows of 513 keys, d = 64, 5.9 in a table of 528 slots, 6.2 in one of 32,768.)
-bool decode_whole(const attn_decode_args_t& a, int sms) {
+bool decode_whole(const attn_decode_args_t& a, int sms, int64_t first = 0) {
     const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
-    const int64_t tiles = cdiv(a.max_pages * a.page_size, kDecTile);
+    const int64_t tiles = cdiv(a.max_pages * a.page_size - first, kDecTile);
     return !a.weights && rows <= sms && (tiles <= 5 || (tiles <= 10 && tiles * (sms - rows) <= 5 * sms));
 }
 
@@ -451,42 +462,8 @@ int launch_decode(const DecodeParams& p, cudaStream_t stream) {
     return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);
 }
 
-int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    int st = check_decode_shape(a);
-    if (st != ATTN_OK) return st;
-    if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.seqlens_k || !a.block_table) return ATTN_ERR_INVALID_ARG;
-    if (((uintptr_t)a.q | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache | (uintptr_t)a.o) & 15u) return ATTN_ERR_MISALIGNED;
-    if (((uintptr_t)a.lse | (uintptr_t)a.weights | (uintptr_t)a.seqlens_k | (uintptr_t)a.block_table) & 3u)
-        return ATTN_ERR_MISALIGNED;
-    const uintptr_t cb = (uintptr_t)(a.num_pages * a.page_size * a.Hkv * a.d * 2), qb = (uintptr_t)(a.B * a.H * a.d * 2);
-    const uintptr_t wb = (uintptr_t)(a.B * a.Hkv) * (uintptr_t)(a.max_pages * a.page_size) * 4;
-    struct { uintptr_t at, bytes; } in[] = {{(uintptr_t)a.q, qb}, {(uintptr_t)a.k_cache, cb}, {(uintptr_t)a.v_cache, cb},
-                                            {(uintptr_t)a.seqlens_k, (uintptr_t)a.B * 4},
-                                            {(uintptr_t)a.block_table, (uintptr_t)(a.B * a.max_pages) * 4}},
-      out[4] = {{(uintptr_t)a.o, qb}, {(uintptr_t)a.lse, a.lse ? (uintptr_t)(a.B * a.H) * 4 : 0},
-                {(uintptr_t)a.weights, a.weights ? wb : 0}, {0, 0}};
-    int sms = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        if (pass == 1) {       // the workspace, once its size is known
-            if ((st = device(&sms)) != ATTN_OK) return st;
-            const DecodeLayout l = decode_layout(a, sms);
-            if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return ATTN_ERR_WORKSPACE;
-            if (l.bytes && (uintptr_t)workspace & 15u) return ATTN_ERR_MISALIGNED;
-            out[3].at = (uintptr_t)workspace;
-            out[3].bytes = l.bytes;
-        }
-        for (int i = 0; i < 4; ++i) {
-            if (!out[i].bytes) continue;
-            for (const auto& x : in)
-                if (overlap(out[i].at, out[i].at + out[i].bytes, x.at, x.at + x.bytes)) return ATTN_ERR_ALIAS;
-            for (int j = 0; j < i; ++j)
-                if (out[j].bytes && overlap(out[i].at, out[i].at + out[i].bytes, out[j].at, out[j].at + out[j].bytes))
-                    return ATTN_ERR_ALIAS;
-        }
-    }
-    const DecodeLayout l = decode_layout(a, sms);
-    char* ws = reinterpret_cast<char*>(workspace);
-    DecodeParams p;
+// all but the workspace; first: the first key that is looked at
+void fill_decode(DecodeParams& p, const attn_decode_args_t& a, int sms, int64_t first) {
     memset(&p, 0, sizeof p);
     p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
     p.k = reinterpret_cast<const char*>(a.k_cache);
@@ -500,19 +477,78 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     p.H = (int)a.H;
     p.Hkv = (int)a.Hkv;
     p.group = (int)(a.H / a.Hkv);
-    const int nh = head_tiles(p.group);
-    p.head_blocks = (int)cdiv(p.group, 8 * nh);
+    p.block_heads = 8 * head_tiles(p.group);
+    p.head_blocks = (int)cdiv(p.group, p.block_heads);
     p.round_mode = a.round_mode;
-    p.whole = decode_whole(a, sms);
+    p.whole = decode_whole(a, sms, first);
     p.grid = p.whole ? p.B * p.Hkv * p.head_blocks : sms;
     p.scale = (float)(1.0 / std::sqrt((double)a.d));
     p.scale_log2 = (float)((1.0 / std::sqrt((double)a.d)) * 1.4426950408889634);
+    p.first = (int)first;
+}
+
+// what a decoding call reads and writes: pointers, alignment, overlaps; then its workspace, once the size is known
+struct DecodeRanges {
+    struct Range { uintptr_t at, bytes; } in[5], out[3];
+    explicit DecodeRanges(const attn_decode_args_t& a) {
+        const uintptr_t cb = (uintptr_t)(a.num_pages * a.page_size * a.Hkv * a.d * 2), qb = (uintptr_t)(a.B * a.H * a.d * 2);
+        const uintptr_t wb = (uintptr_t)(a.B * a.Hkv) * (uintptr_t)(a.max_pages * a.page_size) * 4;
+        in[0] = {(uintptr_t)a.q, qb};
+        in[1] = {(uintptr_t)a.k_cache, cb};
+        in[2] = {(uintptr_t)a.v_cache, cb};
+        in[3] = {(uintptr_t)a.seqlens_k, (uintptr_t)a.B * 4};
+        in[4] = {(uintptr_t)a.block_table, (uintptr_t)(a.B * a.max_pages) * 4};
+        out[0] = {(uintptr_t)a.o, qb};
+        out[1] = {(uintptr_t)a.lse, a.lse ? (uintptr_t)(a.B * a.H) * 4 : 0};
+        out[2] = {(uintptr_t)a.weights, a.weights ? wb : 0};
+    }
+    // whether a written range meets an input, or one of the first n outputs
+    bool clash(const Range& r, int n) const {
+        if (!r.bytes) return false;
+        for (const Range& x : in)
+            if (overlap(r.at, r.at + r.bytes, x.at, x.at + x.bytes)) return true;
+        for (int i = 0; i < n; ++i)
+            if (out[i].bytes && overlap(r.at, r.at + r.bytes, out[i].at, out[i].at + out[i].bytes)) return true;
+        return false;
+    }
+};
+
+int check_decode_tensors(const attn_decode_args_t& a) {
+    if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.seqlens_k || !a.block_table) return ATTN_ERR_INVALID_ARG;
+    if (((uintptr_t)a.q | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache | (uintptr_t)a.o) & 15u) return ATTN_ERR_MISALIGNED;
+    if (((uintptr_t)a.lse | (uintptr_t)a.weights | (uintptr_t)a.seqlens_k | (uintptr_t)a.block_table) & 3u)
+        return ATTN_ERR_MISALIGNED;
+    const DecodeRanges r(a);
+    for (int i = 0; i < 3; ++i)
+        if (r.clash(r.out[i], i)) return ATTN_ERR_ALIAS;
+    return ATTN_OK;
+}
+
+int check_decode_workspace(const attn_decode_args_t& a, const void* workspace, size_t bytes, size_t need) {
+    if (!need) return ATTN_OK;
+    if (!workspace || bytes < need) return ATTN_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 15u) return ATTN_ERR_MISALIGNED;
+    return DecodeRanges(a).clash({(uintptr_t)workspace, need}, 3) ? ATTN_ERR_ALIAS : ATTN_OK;
+}
+
+int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    int st = check_decode_shape(a);
+    if (st != ATTN_OK) return st;
+    if ((st = check_decode_tensors(a)) != ATTN_OK) return st;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    if ((st = check_decode_workspace(a, workspace, workspace_bytes, decode_layout(a, sms).bytes)) != ATTN_OK) return st;
+    const DecodeLayout l = decode_layout(a, sms);
+    char* ws = reinterpret_cast<char*>(workspace);
+    DecodeParams p;
+    fill_decode(p, a, sms, 0);
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
     p.split = reinterpret_cast<int4*>(ws + l.split);
     p.row_ml = reinterpret_cast<float2*>(ws + l.row_ml);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     p.score_room = score_room(a);
+    const int nh = head_tiles(p.group);
     if (a.d == 128)
         return nh == 1   ? launch_decode<128, 1>(p, stream)
                : nh == 2 ? launch_decode<128, 2>(p, stream)
@@ -520,6 +556,120 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     return nh == 1   ? launch_decode<64, 1>(p, stream)
            : nh == 2 ? launch_decode<64, 2>(p, stream)
                      : launch_decode<64, 4>(p, stream);
+}
+
+// ------------------------------------------------------------------------------ shared prefix
+// How the prefix's kernel divides: row blocks, and ranges of key tiles so that the waves of CTAs are short.  A CTA's start
+// and end (its first loads, its row parts) take about as long as three steps.
+struct PrefixPlan {
+    bool single;
+    int64_t row_blocks, splits, ctas;
+};
+PrefixPlan prefix_plan(const attn_decode_args_t& a, int64_t prefix_len, int sms) {
+    PrefixPlan p;
+    const int64_t rows = a.B * (a.H / a.Hkv), tiles = cdiv(prefix_len, kPfTile);
+    p.single = rows <= kPfTile;
+    p.row_blocks = cdiv(rows, p.single ? kPfTile : 2 * kPfTile);
+    const int64_t units = a.Hkv * p.row_blocks, most = tiles < sms ? tiles : sms;
+    p.splits = 1;
+    int64_t best = 0;
+    for (int64_t n = 1; n <= most; ++n) {
+        const int64_t share = cdiv(tiles, n), cost = cdiv(units * n, sms) * ((p.single ? cdiv(share, 2) : share) + 3);
+        if (n == 1 || cost < best) {
+            best = cost;
+            p.splits = n;
+        }
+    }
+    p.ctas = units * p.splits;
+    return p;
+}
+
+struct PrefixLayout {
+    size_t x_o, x_ml, part_o, part_ml, span, own_o, own_ml, bytes;
+};
+PrefixLayout prefix_layout(const attn_decode_args_t& a, const PrefixPlan& plan, int sms) {
+    const int64_t heads = 8 * head_tiles(a.H / a.Hkv), blocks = cdiv(a.H / a.Hkv, heads);
+    PrefixLayout l;
+    l.x_o = 0;
+    l.x_ml = align256((size_t)plan.ctas * 2 * kPfTile * (size_t)a.d * 4);
+    l.part_o = l.x_ml + align256((size_t)plan.ctas * 2 * kPfTile * 8);
+    l.part_ml = l.part_o + align256((size_t)(2 * sms * heads * a.d) * 4);
+    l.span = l.part_ml + align256((size_t)(2 * sms * heads) * 8);
+    l.own_o = l.span + align256((size_t)(a.B * a.Hkv * blocks) * 8);
+    l.own_ml = l.own_o + align256((size_t)(a.B * a.H) * (size_t)a.d * 4);
+    l.bytes = l.own_ml + align256((size_t)(a.B * a.H) * 8);
+    return l;
+}
+
+int check_prefix_shape(const attn_decode_args_t& a, int64_t prefix_len) {
+    const int st = check_decode_shape(a);
+    if (st != ATTN_OK) return st;
+    if (a.weights || prefix_len < 1 || prefix_len > a.max_pages * a.page_size) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+template <int D, int NH>
+int launch_own(const DecodeParams& p, cudaStream_t stream) {
+    return launch(attn_decode_kernel<D, NH, false, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
+}
+template <int D, bool kSingle>
+int launch_prefix(const PrefixParams& p, int64_t ctas, cudaStream_t stream) {
+    return launch(attn_prefix_kernel<D, kSingle>, ctas, 1, kPfThreads, PfGeo<D, kSingle>::kSmem, stream, p);
+}
+
+int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+    int st = check_prefix_shape(a, prefix_len);
+    if (st != ATTN_OK) return st;
+    if ((st = check_decode_tensors(a)) != ATTN_OK) return st;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    const PrefixPlan plan = prefix_plan(a, prefix_len, sms);
+    const PrefixLayout l = prefix_layout(a, plan, sms);
+    if ((st = check_decode_workspace(a, workspace, workspace_bytes, l.bytes)) != ATTN_OK) return st;
+    char* ws = reinterpret_cast<char*>(workspace);
+    PrefixJoin j;
+    memset(&j, 0, sizeof j);
+    fill_decode(j.s, a, sms, prefix_len);
+    j.s.part_o = reinterpret_cast<float*>(ws + l.part_o);
+    j.s.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
+    j.s.span = reinterpret_cast<int2*>(ws + l.span);
+    j.s.own_o = reinterpret_cast<float*>(ws + l.own_o);
+    j.s.own_ml = reinterpret_cast<float2*>(ws + l.own_ml);
+    PrefixParams& x = j.x;
+    x.q = j.s.q;
+    x.k = j.s.k;
+    x.v = j.s.v;
+    x.pages = j.s.pages;
+    x.H = j.s.H;
+    x.Hkv = j.s.Hkv;
+    x.group = j.s.group;
+    x.rows = j.s.B * j.s.group;
+    x.prefix_len = (int)prefix_len;
+    x.tiles = (int)cdiv(prefix_len, kPfTile);
+    x.row_blocks = (int)plan.row_blocks;
+    x.splits = (int)plan.splits;
+    x.scale_log2 = j.s.scale_log2;
+    x.part_o = reinterpret_cast<float*>(ws + l.x_o);
+    x.part_ml = reinterpret_cast<float2*>(ws + l.x_ml);
+    x.wait_limit_ns = 2000000000ull;
+    j.single = plan.single;
+    // a warp has at most 8 parts of a row, while a block has the warps
+    const int64_t parts = plan.splits * (plan.single ? 2 : 1);
+    j.warps = 1;
+    while (j.warps < kPfJoinWarps && parts > 8 * j.warps) j.warps *= 2;
+    st = a.d == 128 ? (plan.single ? launch_prefix<128, true>(x, plan.ctas, stream) : launch_prefix<128, false>(x, plan.ctas, stream))
+                    : (plan.single ? launch_prefix<64, true>(x, plan.ctas, stream) : launch_prefix<64, false>(x, plan.ctas, stream));
+    if (st != ATTN_OK) return st;
+    const int nh = head_tiles(j.s.group);
+    if (a.d == 128)
+        st = nh == 1 ? launch_own<128, 1>(j.s, stream) : nh == 2 ? launch_own<128, 2>(j.s, stream) : launch_own<128, 4>(j.s, stream);
+    else
+        st = nh == 1 ? launch_own<64, 1>(j.s, stream) : nh == 2 ? launch_own<64, 2>(j.s, stream) : launch_own<64, 4>(j.s, stream);
+    if (st != ATTN_OK) return st;
+    const int64_t grid = cdiv(a.B * a.H * j.warps, kPfJoinWarps);
+    return a.d == 128 ? launch(attn_prefix_join_kernel<128>, grid, 1, 32 * kPfJoinWarps, 0, stream, j)
+                      : launch(attn_prefix_join_kernel<64>, grid, 1, 32 * kPfJoinWarps, 0, stream, j);
 }
 
 // ------------------------------------------------------------------------------ evict
@@ -981,6 +1131,17 @@ int attn_norm_rope_append(const attn_norm_append_args_t* args, attn_stream_t str
 
 int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream) {
     return args ? run_reserve(*args, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
+}
+
+size_t attn_paged_prefix_decode_workspace_size(const attn_decode_args_t* args, int64_t prefix_len) {
+    int sms = 0;
+    if (!args || check_prefix_shape(*args, prefix_len) != ATTN_OK || device(&sms) != ATTN_OK) return 0;
+    return prefix_layout(*args, prefix_plan(*args, prefix_len, sms), sms).bytes;
+}
+
+int attn_paged_prefix_decode(const attn_decode_args_t* args, int64_t prefix_len, void* workspace, size_t workspace_bytes,
+                             attn_stream_t stream) {
+    return args ? run_prefix_decode(*args, prefix_len, workspace, workspace_bytes, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
 }
 
 int attn_cache_get_device_status(attn_stream_t stream, int32_t* site) {

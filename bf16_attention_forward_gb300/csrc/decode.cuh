@@ -55,6 +55,12 @@ struct DecodeParams {
     float2* row_ml;                // [B][Hkv][head_blocks][heads of a block] of unsplit rows (weights only)
     float* scores;                 // [B][H][score_room] logits (weights only)
     long long score_room;          // max_pages * page_size rounded up to 16 bytes
+    // behind a shared prefix (prefix.cuh, whose join merges every row): the keys from `first` on (else 0)
+    int first;
+    int block_heads;               // heads of a block: 8 * NH
+    int2* span;                    // [B][rows of a sequence]: first and last CTA of a split row, -1 of a whole one
+    float* own_o;                  // [B][H][d] and (m, l) of whole rows, not divided by l
+    float2* own_ml;
 };
 
 constexpr int kDecWarps = 8;
@@ -76,7 +82,7 @@ struct DecGeo {
 
 // tiles of a sequence; 0 for a length that the table has no room for (the join kernel reports it)
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, int n) {
-    return n > 0 && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - 1) / kDecTile + 1 : 0;
+    return n > p.first && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - p.first - 1) / kDecTile + 1 : 0;
 }
 
 // The line: sequence by sequence, row by row, a row's tiles and its end.  (The host refuses sizes whose
@@ -183,7 +189,8 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
     return m == -INFINITY ? 0.0f : ptx::ex2_approx(ptx::fmax_nan((m - to) * c, -125.0f));
 }
 
-template <int D, int NH, bool kWeights>
+// kShared: the own keys behind a shared prefix; whole rows leave (m, l, o) like split ones, for the prefix's join.
+template <int D, int NH, bool kWeights, bool kShared = false>
 __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using G = DecGeo<D>;
     constexpr int kHeads = 8 * NH;
@@ -206,12 +213,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         cur = Cursor{0, (int)blockIdx.x / rows, (int)blockIdx.x % rows, 0, 0, 0};
         cur.len = __ldg(p.seqlens_k + cur.b);
         u1 = cur.tiles = seq_tiles(p, cur.len);
-        if (cur.row == 0) keyless(p, cur.b, cur.len, D);
+        if (!kShared && cur.row == 0) keyless(p, cur.b, cur.len, D);
         if (u1 == 0) return;
     } else {
         line = make_line(p, rows);
         if ((int)blockIdx.x >= line.ctas) {
-            if (threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            if (!kShared && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
             return;
         }
         u0 = line.start(blockIdx.x);
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         Found f{-1, -1, false};
         if (ahead.u >= u1) return f;
         f.kv_head = ahead.row / p.head_blocks;
-        const int j = ahead.tile * kDecTile + warp * kDecKeys + lane;
+        const int j = p.first + ahead.tile * kDecTile + warp * kDecKeys + lane;
         if (lane < kDecKeys && j < ahead.len) {
             f.row = page_row(p.pages, p.pages.table + (long long)ahead.b * p.pages.max_pages, j);
             f.bad = f.row < 0;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int t = 0; t < NH; ++t) mma_16816(s[t], a, qf[t][ks][0], qf[t][ks][1]);
             }
             // s[t][0..1]: key j0, heads 2 * (lane % 4) and + 1; s[t][2..3]: key j0 + 8
-            const int j0 = (cur.tile + i) * kDecTile + warp * kDecKeys + (lane >> 2);
+            const int j0 = p.first + (cur.tile + i) * kDecTile + warp * kDecKeys + (lane >> 2);
             bool grow = false;
 #pragma unroll
             for (int t = 0; t < NH; ++t) {
@@ -414,6 +421,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         const bool whole = n == cur.tiles;
         const long long slot = (2 * blockIdx.x + (cur.tile == 0 ? 1 : 0)) * kHeads;
         const long long out0 = (long long)b * p.H + kv_head * p.group + head0;
+        if (kShared && threadIdx.x == 0 && cur.tile == 0)
+            p.span[(long long)b * rows + cur.row] =
+                whole ? make_int2(-1, -1) : make_int2(blockIdx.x, line.cta_of(cur.u + cur.tiles - 1));
         if (threadIdx.x < kHeads) {
             const int h = threadIdx.x;
             float mx = -INFINITY, sum = 0.0f;
@@ -425,7 +435,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
             joined_s[h] = make_float2(mx, whole ? (sum > 0.0f ? 1.0f / sum : NAN) : 1.0f);
             const float2 ml = make_float2(mx, bad ? kBadPart : sum);
             if (!whole) p.part_ml[slot + h] = ml;
-            else if (h < p.group - head0) {
+            else if (kShared) {
+                if (h < p.group - head0) p.own_ml[out0 + h] = ml;
+            } else if (h < p.group - head0) {
                 if (p.lse && !bad) p.lse[out0 + h] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
                 if (kWeights) p.row_ml[(((long long)b * p.Hkv + kv_head) * p.head_blocks + head0 / kHeads) * kHeads + h] = ml;
             }
@@ -463,6 +475,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                     const int xd = half * (D / 2) + x, h = t * 8 + hh;
                     if (!whole) {
                         *reinterpret_cast<float2*>(p.part_o + (slot + h) * D + xd) = o;
+                    } else if (kShared) {
+                        if (head0 + h < p.group) *reinterpret_cast<float2*>(p.own_o + (out0 + h) * D + xd) = o;
                     } else if (head0 + h < p.group && !bad) {
                         const float inv = joined_s[h].y;
                         *reinterpret_cast<uint32_t*>(p.o + (out0 + h) * D + xd) =
@@ -474,7 +488,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         }
         next_row(p, rows, cur);
     }
-    if (!p.whole && threadIdx.x == 0) {
+    if (!kShared && !p.whole && threadIdx.x == 0) {
         // a row whose second part was this CTA's: for the join
         int4 d = make_int4(-1, 0, 0, 0);
         const int first = at0.u - at0.tile;

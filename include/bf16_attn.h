@@ -7,7 +7,8 @@
  * (attn_fwd_varlen), a paged K/V cache (attn_fwd_paged), the backward (attn_bwd), and what
  * surrounds a paged cache: rotary positions (attn_rope), appending (attn_paged_append), one-token
  * decoding (attn_paged_decode) and eviction (attn_paged_evict); norms of queries and keys with their positions
- * (attn_norm_rope, attn_norm_rope_append) and pages and slots (attn_paged_reserve).  Source: "MoonMath AI open-sources
+ * (attn_norm_rope, attn_norm_rope_append), pages and slots (attn_paged_reserve) and decoding behind a prefix that
+ * the batch shares (attn_paged_prefix_decode).  Source: "MoonMath AI open-sources
  * a HIP attention kernel for AMD MI300X that beats AITER" (news.chathome.org), opening section: attention is the fused
  * softmax(QK^T/sqrt(d))V; the kernel takes BSHD or BHSD tensors without transposes, head
  * dimension fixed at 128, any query and key length including cross-attention; its
@@ -451,7 +452,7 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
 
 /*
  * Around the paged K/V cache: rotary positions, appending, attention of one new token, eviction; norms with positions,
- * pages and slots.
+ * pages and slots, a shared prefix.
  *
  * Common to these calls.  Tensors are bf16 with head dimension d = 128 or 64 unless said
  * otherwise, device pointers 16-byte aligned (int32 and fp32 tensors 4-byte, fp64 8-byte).  The
@@ -470,6 +471,7 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
 #define ATTN_CACHE_SITE_EVICT 23    /* a bad length, or of a sequence to be cut a bad page or one used twice: it stays */
 #define ATTN_CACHE_SITE_SLOTS 24    /* a slot outside the cache (other than -1): k, v not written               */
 #define ATTN_CACHE_SITE_RESERVE 25  /* bad lengths, offsets, counts, or too few free pages: nothing is reserved */
+#define ATTN_CACHE_SITE_PREFIX 26   /* a bad page of the shared prefix (or a wait that expired): no outputs     */
 
 /* Which elements of a head form pair p of `pairs`: 2p and 2p + 1, or p and p + pairs. */
 typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_t;
@@ -740,6 +742,25 @@ typedef struct {
 } attn_reserve_args_t;
 
 int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
+
+/*
+ * attn_paged_prefix_decode -- attn_paged_decode for a batch whose sequences all begin with the same prefix_len keys: those
+ * are read once for the whole batch, and the products with them run on tiles of all sequences' queries.
+ *   q, caches, o, lse, seqlens_k, block_table, round_mode   as in attn_paged_decode (weights: NULL)
+ *   prefix_len       1 .. max_pages * page_size: keys 0 .. prefix_len - 1 of every sequence are those of sequence 0, and are
+ *                    read through block_table's first row; the other rows' entries of pages that end inside the prefix
+ *                    are not read.  A page that the prefix ends in may be sequence 0's, a copy of it in each sequence, or (without own
+ *                    keys behind it) anything
+ *   seqlens_k        lengths WITH the prefix, prefix_len .. max_pages * page_size; another length leaves that sequence's
+ *                    outputs unwritten and is reported at ATTN_CACHE_SITE_DECODE, like a bad page of its own; a bad page of the
+ *                    prefix leaves all outputs unwritten (ATTN_CACHE_SITE_PREFIX)
+ * Softmax weights of the prefix's keys are rounded to bf16 before the product with the values, as in attn_fwd.  Results are
+ * bitwise reproducible for the same lengths and shapes on the same GPU model.  workspace: caller device memory of at least
+ * attn_paged_prefix_decode_workspace_size() bytes, 16-byte aligned.
+ */
+size_t attn_paged_prefix_decode_workspace_size(const attn_decode_args_t* args, int64_t prefix_len);
+int attn_paged_prefix_decode(const attn_decode_args_t* args, int64_t prefix_len, void* workspace, size_t workspace_bytes,
+                             attn_stream_t stream);
 
 /* Synchronize `stream`, then read and clear the current device's status word of these calls' kernels (all from attn_rope
  * on). */

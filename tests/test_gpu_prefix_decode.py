@@ -1,0 +1,277 @@
+"""Attention of one new token per sequence behind a prefix that the batch shares (attn_paged_prefix_decode) against plain
+fp64 attention over each sequence's keys (needs a GB300).
+
+Tolerance, derived before the first run.  With A = sum_j w_j |v_j| / l (the softmax weights' sum of magnitudes): each weight of the
+prefix is rounded to bf16, 2^-8 relative, the own keys' to 2^-15; fp32 logits off by d * 2^-24 of their magnitudes (below
+2^-13 here), exponentials, sums and joins below 2^-13 together; the output's rounding is 2^-8 relative (RTNE, RTNA), 2^-7
+(RTZ).  So |o - ref| <= 2^-8 |ref| + (2^-8 + 2^-12) A.  The log-sum-exp takes the unrounded weights: 2^-14 (1 + |lse|) + 2^-12.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+NAN_BITS = 0x7FC0
+
+
+@pytest.fixture(scope="module")
+def attn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import bf16_attention_forward_gb300 as a
+    a.load()
+    return a
+
+
+def draw(*shape, seed=0, scale=1.0):
+    return (scale * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).to(torch.bfloat16).cuda()
+
+
+class Batch:
+    """Sequences of `own` keys behind a prefix; the table's other rows name no page that only the prefix uses."""
+
+    def __init__(self, own, H, Hkv, d, page, prefix, seed=0, scale=1.0, spare=1, hidden=-7):
+        B = len(own)
+        self.H, self.Hkv, self.d, self.page, self.prefix = H, Hkv, d, page, prefix
+        lens = [prefix + n for n in own]
+        cut, most = prefix // page, -(-max(lens) // page) + spare
+        g = torch.Generator().manual_seed(seed)
+        order = torch.randperm(cut + B * (most - cut) + 3, generator=g).to(torch.int32)
+        table = torch.full((B, most), hidden, dtype=torch.int32)
+        table[0, :cut] = order[:cut]
+        table[:, cut:] = order[cut:cut + B * (most - cut)].view(B, most - cut)
+        for b, n in enumerate(lens):
+            table[b, max(-(-n // page), -(-prefix // page) if b == 0 else 0):] = hidden     # nothing behind the last page
+        self.table, self.lens = table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.k, self.v = draw(len(order), page, Hkv, d, seed=seed + 1), draw(len(order), page, Hkv, d, seed=seed + 2)
+        self.q = draw(B, H, d, seed=seed + 3, scale=scale)
+
+    def keys(self, b):
+        """Keys and values of sequence b, in order, fp64 [keys, Hkv, d]."""
+        n, page = int(self.lens[b]), self.page
+        j = torch.arange(n)
+        t = self.table.cpu()
+        row = torch.where(j < self.prefix, t[0, j // page], t[b, j // page]).long() * page + j % page
+        return [c.cpu().flatten(0, 1)[row].double().numpy() for c in (self.k, self.v)]
+
+    def reference(self, b):
+        k, v = self.keys(b)
+        G, q = self.H // self.Hkv, self.q[b].cpu().double().numpy()
+        o, lse, A = np.empty((self.H, self.d)), np.empty(self.H), np.empty((self.H, self.d))
+        for h in range(self.H):
+            x = k[:, h // G] @ q[h] / np.sqrt(self.d)
+            m = x.max()
+            w = np.exp(x - m)
+            o[h], A[h] = w @ v[:, h // G] / w.sum(), w @ np.abs(v[:, h // G]) / w.sum()
+            lse[h] = m + np.log(w.sum())
+        return o, lse, A
+
+    def call(self, attn, **kw):
+        return attn.attn_paged_prefix_decode(self.q, self.k, self.v, self.lens, self.table, self.prefix, return_lse=True, **kw)
+
+    def check(self, got, rows=None, out=2.0 ** -8):
+        o, lse = (x.cpu().double().numpy() for x in got)
+        for b in range(len(self.lens)) if rows is None else rows:
+            ref, ref_lse, A = self.reference(b)
+            err = np.abs(o[b] - ref) - (out * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * A)
+            assert np.all(err <= 0), (b, float(err.max()))
+            assert np.all(np.abs(lse[b] - ref_lse) <= 2.0 ** -14 * (1 + np.abs(ref_lse)) + 2.0 ** -12), b
+
+
+CASES = [  # own keys, H, Hkv, d, page, prefix
+    ([1], 8, 8, 128, 16, 1),
+    ([0], 4, 2, 64, 16, 40),
+    ([0, 0, 0], 6, 2, 128, 32, 64),                  # no sequence has a key of its own
+    ([5, 0, 300, 1, 129], 8, 2, 128, 16, 127),
+    ([3, 77, 128], 5, 1, 128, 24, 128),
+    ([3, 77, 128], 24, 3, 64, 7, 129),
+    ([1] * 32, 32, 8, 128, 128, 513),                # 128 rows
+    ([2, 300] * 16 + [9], 32, 8, 128, 256, 1000),    # 132: two tiles
+    ([1, 40, 0, 17] * 13, 40, 8, 128, 24, 2500),     # 260: a second block of rows
+    ([7] * 9, 71, 1, 64, 100, 777),                  # 639 rows of one K/V head
+    ([64, 1] * 20, 12, 12, 128, 1, 300),             # 40 rows, a page a key
+    ([11, 500], 142, 2, 128, 64, 6000),
+    ([1, 2], 2, 1, 128, 512, 40000),                 # many parts of a row
+    ([2000, 1, 4000], 8, 8, 64, 16, 90),             # more own keys than shared ones
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "B%d_H%d_%d_d%d_p%d_%d" % (len(c[0]), *c[1:]))
+def test_against_plain_attention(attn, case):
+    x = Batch(*case, seed=len(case[0]) + case[5], scale=2.0)
+    got = x.call(attn)
+    assert attn.cache_device_status() == (0, 0)
+    x.check(got)
+    again = x.call(attn)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(attn, seed):
+    g = np.random.default_rng(seed)
+    Hkv, G, d = int(g.integers(1, 9)), int(g.integers(1, 12)), int(g.choice([64, 128]))
+    B, page = int(g.integers(1, 80)), int(g.choice([1, 3, 8, 16, 48, 128, 300]))
+    own = g.integers(0, int(g.choice([2, 40, 400])), B).tolist()
+    x = Batch(own, Hkv * G, Hkv, d, page, int(g.integers(1, 1500)), seed=100 + seed, scale=float(g.choice([0.1, 1, 4])))
+    x.check(x.call(attn), rows=sorted(set(g.integers(0, B, 6).tolist())))
+    assert attn.cache_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("mode", ["rtna", "rtz"])
+def test_rounding_modes(attn, mode):
+    x = Batch([10, 90, 3], 16, 4, 128, 16, 300, seed=4)
+    near, other = x.call(attn), x.call(attn, round=mode)
+    x.check(other, out=2.0 ** -8 if mode == "rtna" else 2.0 ** -7)
+    step = (other[0].view(torch.int16).int() - near[0].view(torch.int16).int()).abs()
+    assert step.max() <= 1 and torch.equal(near[1], other[1])
+
+
+def test_equals_the_plain_decoding_call_where_pages_are_shared(attn):
+    """The same caches through attn_paged_decode, whose rows name the prefix's pages too."""
+    x = Batch([40, 0, 200, 7], 32, 8, 128, 16, 320, seed=9, scale=2.0)
+    got = x.call(attn)
+    table = x.table.clone()
+    table[:, :20] = table[0, :20]
+    want = attn.attn_paged_decode(x.q, x.k, x.v, x.lens, table, return_lse=True)
+    assert (got[0].float() - want[0].float()).norm() <= 2.0 ** -7 * want[0].float().norm()
+    assert (got[1] - want[1]).abs().max() <= 1e-4
+    # rows that name the shared pages change nothing, nor do other sequences
+    assert torch.equal(attn.attn_paged_prefix_decode(x.q, x.k, x.v, x.lens, table, 320), got[0])
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_non_finite_keys_and_values(attn, rows):
+    """Of the prefix and of own keys, as in attn_paged_decode: the same classes of outputs."""
+    x = Batch([50, 3, 0, 20] * (rows // 4) + [8] * (rows % 4), 8, 1, 128, 16, 160, seed=rows)
+    k, v = x.k.flatten(0, 1), x.v.flatten(0, 1)
+    page = x.table[0].cpu()
+
+    def slot(b, j):
+        t = page if j < x.prefix else x.table[b].cpu()
+        return int(t[j // 16]) * 16 + j % 16
+    table = x.table.clone()
+    table[:, :10] = table[0, :10]
+    cases = [(k, 0, 5, float("nan")), (k, 0, 130, float("inf")), (k, 0, 131, float("-inf")), (v, 0, 7, float("inf")),
+             (v, 0, 9, float("nan")), (k, 1, 161, float("nan")), (v, 1, 162, float("-inf")), (k, 0, 170, float("inf"))]
+    for c, b, j, value in cases:
+        at = slot(b, j)
+        kept = c[at].clone()
+        c[at, :, 3] = value
+        got, want = x.call(attn), attn.attn_paged_decode(x.q, x.k, x.v, x.lens, table, return_lse=True)
+        for a, w in zip(got, want):
+            assert torch.equal(a.isnan(), w.isnan()) and torch.equal(a.isinf(), w.isinf())
+            assert torch.equal(a[a.isinf()], w[w.isinf()])
+        assert set(got[0][got[0].isnan()].view(torch.int16).tolist()) <= {NAN_BITS}
+        c[at] = kept
+
+
+def test_infinite_values_under_vanishing_weights(attn):
+    """A finite logit weighs something, however small: an infinite value stays infinite."""
+    x = Batch([3, 20], 4, 1, 64, 16, 200, seed=5)
+    x.q.fill_(4.0)
+    k, v = x.k.flatten(0, 1), x.v.flatten(0, 1)
+    k[int(x.table[0, 2]) * 16 + 1] = 64.0            # stands far out: every other weight underflows
+    k[int(x.table[0, 3]) * 16 + 2] = -64.0
+    v[int(x.table[0, 3]) * 16 + 2, 0, 5] = float("inf")
+    got = x.call(attn)[0]
+    assert torch.isposinf(got[:, :, 5]).all() and got[:, :, :5].isfinite().all()
+
+
+def test_all_logits_minus_infinity(attn):
+    x = Batch([3, 0, 20], 4, 2, 128, 16, 150, seed=5)
+    x.q.fill_(1.0)
+    x.k.fill_(float("-inf"))
+    o, lse = x.call(attn)
+    assert o.isnan().all() and torch.isneginf(lse).all()
+
+
+def test_bad_lengths_and_pages_leave_their_rows(attn):
+    def run(x, **kw):
+        o, lse = torch.full_like(x.q, 7.0), torch.full((len(x.lens), x.H), 7.0, device="cuda")
+        x.call(attn, o=o, lse=lse)
+        return o, lse
+    x = Batch([30, 4, 200, 9, 0], 8, 2, 128, 16, 96, seed=2)
+    room = x.table.shape[1] * 16
+    for length in (95, -1, 0, room + 1, 2 ** 31 - 1):
+        kept = int(x.lens[2])
+        x.lens[2] = length
+        o, lse = run(x)
+        assert attn.cache_device_status() == (1, 22) and (o[2] == 7).all() and (lse[2] == 7).all()
+        x.lens[2] = kept
+        x.check((o, lse), rows=[0, 1, 3, 4])
+    for page in (-1, len(x.k), 2 ** 31 - 1):
+        kept = int(x.table[2, 8])
+        x.table[2, 8] = page
+        o, lse = run(x)
+        assert attn.cache_device_status() == (1, 22) and (o[2] == 7).all() and (lse[2] == 7).all()
+        x.table[2, 8] = kept
+        x.check((o, lse), rows=[0, 1, 3, 4])
+    x.table[0, 2] = len(x.k)                         # of the prefix: nobody's outputs are written
+    o, lse = run(x)
+    assert attn.cache_device_status() == (1, 26) and (o == 7).all() and (lse == 7).all()
+
+
+def test_stays_in_bounds_with_the_caller_s_workspace(attn):
+    x = Batch([30, 4, 700], 10, 2, 128, 24, 1111, seed=2)
+    want = x.call(attn)
+    a = attn.DecodeArgs()
+    a.B, a.H, a.Hkv, a.num_pages, a.page_size, a.max_pages, a.d = 3, 10, 2, len(x.k), 24, x.table.shape[1], 128
+    need = int(attn.load().attn_paged_prefix_decode_workspace_size(ctypes.byref(a), 1111))
+    assert need > 0
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    room, lses = torch.full((64 + x.q.numel() + 64,), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((30 + 64,), 3.0, device="cuda")
+    got = x.call(attn, o=room[64:-64].view_as(x.q), lse=lses[32:-32].view(3, 10), workspace=ws[:need])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (room[:64] == 3).all() and (room[-64:] == 3).all() and (lses[:32] == 3).all() and (lses[-32:] == 3).all()
+    assert (ws[need:] == 0xFF).all()
+    with pytest.raises(attn.AttnError):
+        x.call(attn, workspace=ws[:need - 256])
+    with pytest.raises(ValueError):
+        attn.attn_paged_prefix_decode(x.q, x.k, x.v, x.lens, x.table, x.table.shape[1] * 24 + 1)
+
+
+def test_rows_past_2_to_the_32_bytes(attn):
+    """A cache of 5 GB, its pages at the far end."""
+    x = Batch([30, 4, 200], 8, 8, 128, 128, 500, seed=3)
+    far = 2_400_000 // 128
+    k, v = (torch.zeros((far + len(x.k), 128, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[far:], v[far:] = x.k, x.v
+    table = torch.where(x.table >= 0, x.table + far, x.table)
+    got = attn.attn_paged_prefix_decode(x.q, k, v, x.lens, table, 500, return_lse=True)
+    want = x.call(attn)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_captured_while_lengths_grow(attn):
+    x = Batch([1, 30, 4], 8, 2, 128, 16, 200, seed=7, spare=3)
+    t = torch.arange(len(x.k), dtype=torch.int32)
+    cut = 200 // 16
+    x.table[:, cut:] = t[cut:cut + 3 * (x.table.shape[1] - cut)].view(3, -1).cuda()
+    x.table[0, :cut] = t[:cut].cuda()
+    x.call(attn)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = x.call(attn)
+    for _ in range(4):
+        x.lens.add_(1)
+        x.q.copy_(draw(3, 8, 128, seed=int(x.lens[0])))
+        graph.replay()
+        x.check(got)
+        assert all(torch.equal(a, b) for a, b in zip(got, x.call(attn)))
+
+
+def test_two_streams_with_workspaces_of_their_own(attn):
+    batches = [Batch([30, 4, 700], 8, 2, 128, 16, 1500, seed=s) for s in (1, 2)]
+    want = [x.call(attn) for x in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        got = [x.call(attn, stream=s) for x, s in zip(batches, streams)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])

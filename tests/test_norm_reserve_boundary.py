@@ -1,4 +1,4 @@
-"""Refusals of the norms with positions and of attn_paged_reserve, on the host: argument errors come back before anything is
+"""Refusals of the norms with positions, of attn_paged_reserve and of attn_paged_prefix_decode, on the host: argument errors come back before anything is
 launched (CPU only; the C entries get fake addresses that nothing reads)."""
 import ctypes
 
@@ -55,6 +55,12 @@ def reserve(**kw):
     return fill(a, **kw)
 
 
+def prefix(**kw):
+    a = fill(attn.DecodeArgs(), q=M, k_cache=2 * M, v_cache=3 * M, o=4 * M, lse=5 * M, seqlens_k=7 * M, block_table=8 * M,
+             B=2, H=8, Hkv=2, num_pages=8, page_size=16, max_pages=4, d=128)
+    return fill(a, **kw)
+
+
 NORM = [
     (INVALID, [dict(q=0), dict(q_out=0), dict(k_out=0), dict(positions=0), dict(freqs=0), dict(axes=0), dict(B=0),
                dict(S=-1), dict(H=0), dict(Hkv=0), dict(pairs=-1), dict(pairs=65), dict(num_axes=0), dict(pairing=2),
@@ -108,6 +114,17 @@ RESERVE = [
 ]
 
 
+PREFIX = [
+    (INVALID, [dict(q=0), dict(k_cache=0), dict(v_cache=0), dict(o=0), dict(seqlens_k=0), dict(block_table=0), dict(B=0),
+               dict(H=0), dict(Hkv=0), dict(H=7), dict(num_pages=0), dict(page_size=0), dict(max_pages=0), dict(round_mode=3),
+               dict(reserved=1), dict(weights=6 * M), dict(n=0), dict(n=-1), dict(n=65)]),
+    (UNSUPPORTED, [dict(d=256), dict(num_pages=1 << 29, page_size=16), dict(B=1 << 29)]),
+    (MISALIGNED, [dict(q=M + 2), dict(o=4 * M + 8), dict(lse=5 * M + 2), dict(seqlens_k=7 * M + 2)]),
+    (ALIAS, [dict(o=M), dict(o=2 * M + 512), dict(lse=4 * M), dict(lse=7 * M), dict(lse=8 * M)]),
+    (NO_DEVICE, [dict(), dict(n=1), dict(n=64), dict(lse=0), dict(page_size=1, n=4), dict(H=142)]),
+]
+
+
 def cases(table):
     return [(want, kw) for want, kws in table for kw in kws]
 
@@ -141,7 +158,16 @@ def test_paged_reserve(lib, want, kw):
 
 
 @fake_pointers
+@pytest.mark.parametrize("want,kw", cases(PREFIX), ids=name)
+def test_paged_prefix_decode(lib, want, kw):
+    kw = dict(kw)
+    n = kw.pop("n", 20)
+    assert lib.attn_paged_prefix_decode(ctypes.byref(prefix(**kw)), n, 16 * M, 1 << 20, None) == want
+
+
+@fake_pointers
 def test_sizes_without_a_device(lib):
+    assert lib.attn_paged_prefix_decode_workspace_size(ctypes.byref(prefix()), 20) == 0
     assert lib.attn_norm_rope_bwd_workspace_size(ctypes.byref(back())) == 0
 
 
@@ -149,6 +175,8 @@ def test_null_arguments(lib):
     assert lib.attn_norm_rope(None, None) == INVALID and lib.attn_norm_rope_append(None, None) == INVALID
     assert lib.attn_norm_rope_bwd(None, None, 0, None) == INVALID and lib.attn_paged_reserve(None, None) == INVALID
     assert lib.attn_norm_rope_bwd_workspace_size(None) == 0
+    assert lib.attn_paged_prefix_decode(None, 1, None, 0, None) == INVALID
+    assert lib.attn_paged_prefix_decode_workspace_size(None, 1) == 0
 
 
 def test_argument_structures_have_the_abi_s_sizes():
@@ -165,7 +193,8 @@ def test_binding_wants_cuda_tensors():
     i, j = torch.zeros(1, dtype=torch.int32), torch.zeros((1, 1), dtype=torch.int32)
     for call in (lambda: attn.attn_norm_rope(t, t), lambda: attn.attn_norm_rope(None, None),
                  lambda: attn.attn_norm_rope_bwd(t, t, t, t), lambda: attn.attn_norm_rope_append(t, t, c, c, i.long()),
-                 lambda: attn.attn_paged_reserve(i, i, j, i, i, i, 16)):
+                 lambda: attn.attn_paged_reserve(i, i, j, i, i, i, 16),
+                 lambda: attn.attn_paged_prefix_decode(t, c, c, i, j, 1)):
         with pytest.raises(TypeError):
             call()
     for call in (lambda: attn.attn_norm_rope(t, t, layout="x"), lambda: attn.attn_norm_rope(t, t, pairing="x")):

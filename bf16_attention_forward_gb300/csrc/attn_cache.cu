@@ -413,9 +413,9 @@ int head_tiles(int64_t group) { return group <= 8 ? 1 : group <= 16 ? 2 : 4; }
 // us a call in a graph, d = 128, split / whole:  8 rows of 2 tiles 7.0 / 4.8, 5 tiles 7.0 / 7.1, 8 tiles 7.2 / 9.4;
 // 16 x 8 rows of 2 tiles 7.8 / 5.2, 5 tiles 11.8 / 8.0, 8 tiles 14.5 / 10.8.
 // (Short rows in a wide table are split: 2 rows of 513 keys, d = 64, 5.9 in a table of 528 slots, 6.2 in one of 32,768.)
-bool decode_whole(const attn_decode_args_t& a, int sms, int64_t first = 0) {
+bool decode_whole(const attn_decode_args_t& a, int sms) {
     const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
-    const int64_t tiles = cdiv(a.max_pages * a.page_size - first, kDecTile);
+    const int64_t tiles = cdiv(a.max_pages * a.page_size, kDecTile);
     return !a.weights && rows <= sms && (tiles <= 5 || (tiles <= 10 && tiles * (sms - rows) <= 5 * sms));
 }
 
@@ -462,8 +462,8 @@ int launch_decode(const DecodeParams& p, cudaStream_t stream) {
     return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);
 }
 
-// all but the workspace; first: the first key that is looked at
-void fill_decode(DecodeParams& p, const attn_decode_args_t& a, int sms, int64_t first) {
+// all but the workspace
+void fill_decode(DecodeParams& p, const attn_decode_args_t& a, int sms) {
     memset(&p, 0, sizeof p);
     p.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
     p.k = reinterpret_cast<const char*>(a.k_cache);
@@ -480,11 +480,10 @@ void fill_decode(DecodeParams& p, const attn_decode_args_t& a, int sms, int64_t 
     p.block_heads = 8 * head_tiles(p.group);
     p.head_blocks = (int)cdiv(p.group, p.block_heads);
     p.round_mode = a.round_mode;
-    p.whole = decode_whole(a, sms, first);
+    p.whole = decode_whole(a, sms);
     p.grid = p.whole ? p.B * p.Hkv * p.head_blocks : sms;
     p.scale = (float)(1.0 / std::sqrt((double)a.d));
     p.scale_log2 = (float)((1.0 / std::sqrt((double)a.d)) * 1.4426950408889634);
-    p.first = (int)first;
 }
 
 // what a decoding call reads and writes: pointers, alignment, overlaps; then its workspace, once the size is known
@@ -541,7 +540,7 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
     const DecodeLayout l = decode_layout(a, sms);
     char* ws = reinterpret_cast<char*>(workspace);
     DecodeParams p;
-    fill_decode(p, a, sms, 0);
+    fill_decode(p, a, sms);
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
     p.split = reinterpret_cast<int4*>(ws + l.split);
@@ -559,28 +558,20 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
 }
 
 // ------------------------------------------------------------------------------ shared prefix
-// How the prefix's kernel divides: row blocks, and ranges of key tiles so that the waves of CTAs are short.  A CTA's start
-// and end (its first loads, its row parts) take about as long as three steps.
+// How the prefix's kernel divides: row blocks, and a line of steps over the CTAs.
 struct PrefixPlan {
     bool single;
-    int64_t row_blocks, splits, ctas;
+    int64_t row_blocks, steps, line, ctas, slots;
 };
 PrefixPlan prefix_plan(const attn_decode_args_t& a, int64_t prefix_len, int sms) {
     PrefixPlan p;
     const int64_t rows = a.B * (a.H / a.Hkv), tiles = cdiv(prefix_len, kPfTile);
     p.single = rows <= kPfTile;
     p.row_blocks = cdiv(rows, p.single ? kPfTile : 2 * kPfTile);
-    const int64_t units = a.Hkv * p.row_blocks, most = tiles < sms ? tiles : sms;
-    p.splits = 1;
-    int64_t best = 0;
-    for (int64_t n = 1; n <= most; ++n) {
-        const int64_t share = cdiv(tiles, n), cost = cdiv(units * n, sms) * ((p.single ? cdiv(share, 2) : share) + 3);
-        if (n == 1 || cost < best) {
-            best = cost;
-            p.splits = n;
-        }
-    }
-    p.ctas = units * p.splits;
+    p.steps = p.single ? cdiv(tiles, 2) : tiles;
+    p.line = a.Hkv * p.row_blocks * p.steps;
+    p.ctas = p.line < sms ? p.line : sms;
+    p.slots = (cdiv(p.line, p.ctas) - 1 + p.steps - 1) / p.steps + 1;      // shares of a range that begins anywhere
     return p;
 }
 
@@ -589,12 +580,13 @@ struct PrefixLayout {
 };
 PrefixLayout prefix_layout(const attn_decode_args_t& a, const PrefixPlan& plan, int sms) {
     const int64_t heads = 8 * head_tiles(a.H / a.Hkv), blocks = cdiv(a.H / a.Hkv, heads);
+    const size_t rows = (size_t)(plan.ctas * plan.slots) * 2 * kPfTile, own = (size_t)(2 * sms * kDecWarps * heads);
     PrefixLayout l;
     l.x_o = 0;
-    l.x_ml = align256((size_t)plan.ctas * 2 * kPfTile * (size_t)a.d * 4);
-    l.part_o = l.x_ml + align256((size_t)plan.ctas * 2 * kPfTile * 8);
-    l.part_ml = l.part_o + align256((size_t)(2 * sms * heads * a.d) * 4);
-    l.span = l.part_ml + align256((size_t)(2 * sms * heads) * 8);
+    l.x_ml = align256(rows * (size_t)a.d * 4);
+    l.part_o = l.x_ml + align256(rows * 8);
+    l.part_ml = l.part_o + align256(own * (size_t)a.d * 4);
+    l.span = l.part_ml + align256(own * 8);
     l.own_o = l.span + align256((size_t)(a.B * a.Hkv * blocks) * 8);
     l.own_ml = l.own_o + align256((size_t)(a.B * a.H) * (size_t)a.d * 4);
     l.bytes = l.own_ml + align256((size_t)(a.B * a.H) * 8);
@@ -605,6 +597,11 @@ int check_prefix_shape(const attn_decode_args_t& a, int64_t prefix_len) {
     const int st = check_decode_shape(a);
     if (st != ATTN_OK) return st;
     if (a.weights || prefix_len < 1 || prefix_len > a.max_pages * a.page_size) return ATTN_ERR_INVALID_ARG;
+    // strides of a key are 32 bits, places on the lines of both kernels int32
+    if (a.Hkv * a.d > kLim) return ATTN_ERR_UNSUPPORTED;
+    const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
+    if (cdiv(a.max_pages * a.page_size - prefix_len, kDecKeys) + 1 > (2 * kLim - 1) / rows) return ATTN_ERR_UNSUPPORTED;
+    if (cdiv(prefix_len, kPfTile) > (2 * kLim - 1) / (a.Hkv * cdiv(a.B * group, kPfTile))) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -630,7 +627,10 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     char* ws = reinterpret_cast<char*>(workspace);
     PrefixJoin j;
     memset(&j, 0, sizeof j);
-    fill_decode(j.s, a, sms, prefix_len);
+    fill_decode(j.s, a, sms);
+    j.s.first = (int)prefix_len;
+    j.s.whole = 0;
+    j.s.grid = sms;
     j.s.part_o = reinterpret_cast<float*>(ws + l.part_o);
     j.s.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
     j.s.span = reinterpret_cast<int2*>(ws + l.span);
@@ -645,17 +645,23 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     x.Hkv = j.s.Hkv;
     x.group = j.s.group;
     x.rows = j.s.B * j.s.group;
+    const Pages by_group = make_pages(nullptr, 1, x.group, 1);     // its divisor's constants
+    x.group_mul = by_group.mul;
+    x.group_shift = by_group.shift;
     x.prefix_len = (int)prefix_len;
-    x.tiles = (int)cdiv(prefix_len, kPfTile);
     x.row_blocks = (int)plan.row_blocks;
-    x.splits = (int)plan.splits;
+    x.steps = (int)plan.steps;
+    x.ctas = (int)plan.ctas;
+    x.per = (int)(plan.line / plan.ctas);
+    x.more = (int)(plan.line % plan.ctas);
+    x.slots = (int)plan.slots;
     x.scale_log2 = j.s.scale_log2;
     x.part_o = reinterpret_cast<float*>(ws + l.x_o);
     x.part_ml = reinterpret_cast<float2*>(ws + l.x_ml);
     x.wait_limit_ns = 2000000000ull;
     j.single = plan.single;
     // a warp has at most 8 parts of a row, while a block has the warps
-    const int64_t parts = plan.splits * (plan.single ? 2 : 1);
+    const int64_t parts = (plan.steps / x.per + 1) * (plan.single ? 2 : 1);
     j.warps = 1;
     while (j.warps < kPfJoinWarps && parts > 8 * j.warps) j.warps *= 2;
     st = a.d == 128 ? (plan.single ? launch_prefix<128, true>(x, plan.ctas, stream) : launch_prefix<128, false>(x, plan.ctas, stream))

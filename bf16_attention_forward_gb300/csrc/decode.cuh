@@ -58,7 +58,7 @@ struct DecodeParams {
     // behind a shared prefix (prefix.cuh, whose join merges every row): the keys from `first` on (else 0)
     int first;
     int block_heads;               // heads of a block: 8 * NH
-    int2* span;                    // [B][rows of a sequence]: first and last CTA of a split row, -1 of a whole one
+    int2* span;                    // [B][rows of a sequence]: first and last warp of a split row, -1 of a whole one
     float* own_o;                  // [B][H][d] and (m, l) of whole rows, not divided by l
     float2* own_ml;
 };
@@ -81,8 +81,9 @@ struct DecGeo {
 };
 
 // tiles of a sequence; 0 for a length that the table has no room for (the join kernel reports it)
+template <int kTile = kDecTile>
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, int n) {
-    return n > p.first && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - p.first - 1) / kDecTile + 1 : 0;
+    return n > p.first && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - p.first - 1) / kTile + 1 : 0;
 }
 
 // The line: sequence by sequence, row by row, a row's tiles and its end.  (The host refuses sizes whose
@@ -97,18 +98,19 @@ struct Line {
     }
 };
 
-// rows: of a sequence
-__device__ __forceinline__ Line make_line(const DecodeParams& p, int rows) {   // every lane of a warp calls it
+// rows: of a sequence; workers: how many share the line, with `least` places at least (but for one worker)
+template <int kTile = kDecTile>
+__device__ __forceinline__ Line make_line(const DecodeParams& p, int rows, int workers, int least = 1) {   // by a whole warp
     int n = 0;
 #pragma unroll 2
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-        const int t = seq_tiles(p, __ldg(p.seqlens_k + b));
+        const int t = seq_tiles<kTile>(p, __ldg(p.seqlens_k + b));
         n += t > 0 ? t + 1 : 0;
     }
     n = __reduce_add_sync(0xFFFFFFFFu, n);
     Line l;
     l.units = n * rows;
-    l.ctas = min(l.units, p.grid);
+    l.ctas = min((l.units + least - 1) / least, workers);
     l.per = l.ctas ? l.units / l.ctas : 1;
     l.more = l.units - l.per * l.ctas;
     return l;
@@ -119,13 +121,14 @@ struct Cursor {
 };
 
 // what is at place u of the line (u < units)
+template <int kTile = kDecTile>
 __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
     const int lane = threadIdx.x & 31;
     int done = 0;                      // places of a row, of the sequences before
     Cursor c{u, 0, 0, 0, 1, 0};
 #pragma unroll 1
     for (int base = 0; base < p.B; base += 32) {
-        const int len = base + lane < p.B ? __ldg(p.seqlens_k + base + lane) : 0, tiles = seq_tiles(p, len);
+        const int len = base + lane < p.B ? __ldg(p.seqlens_k + base + lane) : 0, tiles = seq_tiles<kTile>(p, len);
         const int mine = tiles > 0 ? tiles + 1 : 0;
         int incl = mine;
 #pragma unroll
@@ -150,6 +153,7 @@ __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
 }
 
 // to the first tile of the next row (past the last sequence's last row: any place behind the line)
+template <int kTile = kDecTile>
 __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor& c) {
     c.u += c.tiles + 1 - c.tile;
     c.tile = 0;
@@ -159,7 +163,7 @@ __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor
     while (c.b + 1 < p.B) {
         ++c.b;
         c.len = __ldg(p.seqlens_k + c.b);
-        c.tiles = seq_tiles(p, c.len);
+        c.tiles = seq_tiles<kTile>(p, c.len);
         if (c.tiles > 0) break;
     }
 }
@@ -189,13 +193,16 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
     return m == -INFINITY ? 0.0f : ptx::ex2_approx(ptx::fmax_nan((m - to) * c, -125.0f));
 }
 
-// kShared: the own keys behind a shared prefix; whole rows leave (m, l, o) like split ones, for the prefix's join.
+// kShared: the own keys behind a shared prefix, as a line of 16-key tiles that the WARPS divide: own keys are often few, and
+// a row's end then costs a warp a few stores instead of a block its barriers (512 sequences of 1 to 200 own keys, 8 K/V
+// heads: 98 us a CTA's rows at a time).  Every row leaves (m, l, o) for the prefix's join.
 template <int D, int NH, bool kWeights, bool kShared = false>
 __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using G = DecGeo<D>;
     constexpr int kHeads = 8 * NH;
     constexpr int kChunks = G::kRow / 16;              // 16-byte chunks of a key
     constexpr int kRowsPerCopy = 32 / kChunks;         // keys that one cp.async of the warp takes
+    constexpr int kTile = kShared ? kDecKeys : kDecTile;
     extern __shared__ __align__(128) char smem[];
     __shared__ float2 ml_s[kDecWarps][kHeads], joined_s[kHeads];
     __shared__ int bad_s[kDecWarps][G::kStages];
@@ -203,9 +210,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     const uint32_t ring = ptx::smem_u32(smem) + warp * (G::kStages * G::kStageBytes);
     float* red = reinterpret_cast<float*>(smem + G::kRing);
 
-    pdl_wait();
+    // (kShared: what it reads was complete before the prefix's kernel, all of whose CTAs let this one start behind their
+    // own wait, and what it writes only the join reads)
+    if (!kShared) pdl_wait();
     pdl_launch();
     const int rows = p.Hkv * p.head_blocks;
+    // which of the line's workers this is, and the warp's first key in a tile
+    const int worker = kShared ? warp * gridDim.x + blockIdx.x : blockIdx.x, key0 = kShared ? 0 : warp * kDecKeys;
     Line line;
     Cursor cur;
     int u0 = 0, u1;
@@ -213,18 +224,20 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         cur = Cursor{0, (int)blockIdx.x / rows, (int)blockIdx.x % rows, 0, 0, 0};
         cur.len = __ldg(p.seqlens_k + cur.b);
         u1 = cur.tiles = seq_tiles(p, cur.len);
-        if (!kShared && cur.row == 0) keyless(p, cur.b, cur.len, D);
+        if (cur.row == 0) keyless(p, cur.b, cur.len, D);
         if (u1 == 0) return;
     } else {
-        line = make_line(p, rows);
-        if ((int)blockIdx.x >= line.ctas) {
+        // (a warp has up to three tiles in flight at once: fewer would only make more parts)
+        line = make_line<kTile>(p, rows, kShared ? p.grid * kDecWarps : p.grid, kShared ? 3 : 1);
+        if (worker >= line.ctas) {
             if (!kShared && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            if (kShared) pdl_wait();
             return;
         }
-        u0 = line.start(blockIdx.x);
-        u1 = line.start(blockIdx.x + 1);
-        cur = seek(p, rows, u0);
-        if (cur.tile == cur.tiles) next_row(p, rows, cur);
+        u0 = line.start(worker);
+        u1 = line.start(worker + 1);
+        cur = seek<kTile>(p, rows, u0);
+        if (cur.tile == cur.tiles) next_row<kTile>(p, rows, cur);
     }
     Cursor ahead = cur;
     const Cursor at0 = cur;
@@ -239,13 +252,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         Found f{-1, -1, false};
         if (ahead.u >= u1) return f;
         f.kv_head = ahead.row / p.head_blocks;
-        const int j = p.first + ahead.tile * kDecTile + warp * kDecKeys + lane;
+        const int j = p.first + ahead.tile * kTile + key0 + lane;
         if (lane < kDecKeys && j < ahead.len) {
             f.row = page_row(p.pages, p.pages.table + (long long)ahead.b * p.pages.max_pages, j);
             f.bad = f.row < 0;
         }
         ++ahead.u;
-        if (++ahead.tile == ahead.tiles && ahead.u < u1) next_row(p, rows, ahead);
+        if (++ahead.tile == ahead.tiles && ahead.u < u1) next_row<kTile>(p, rows, ahead);
         return f;
     };
     auto load = [&](int stage, const Found& f) {
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int t = 0; t < NH; ++t) mma_16816(s[t], a, qf[t][ks][0], qf[t][ks][1]);
             }
             // s[t][0..1]: key j0, heads 2 * (lane % 4) and + 1; s[t][2..3]: key j0 + 8
-            const int j0 = p.first + (cur.tile + i) * kDecTile + warp * kDecKeys + (lane >> 2);
+            const int j0 = p.first + (cur.tile + i) * kTile + key0 + (lane >> 2);
             bool grow = false;
 #pragma unroll
             for (int t = 0; t < NH; ++t) {
@@ -415,15 +428,35 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[t][c] += __shfl_xor_sync(0xFFFFFFFFu, l[t][c], off);
-                if (lane < 4) ml_s[warp][t * 8 + lane * 2 + c] = make_float2(m[t][c], l[t][c]);
+                if (!kShared && lane < 4) ml_s[warp][t * 8 + lane * 2 + c] = make_float2(m[t][c], l[t][c]);
             }
-        bad = __syncthreads_or(bad);
         const bool whole = n == cur.tiles;
-        const long long slot = (2 * blockIdx.x + (cur.tile == 0 ? 1 : 0)) * kHeads;
+        const long long slot = (2ll * worker + (cur.tile == 0 ? 1 : 0)) * kHeads;
         const long long out0 = (long long)b * p.H + kv_head * p.group + head0;
-        if (kShared && threadIdx.x == 0 && cur.tile == 0)
-            p.span[(long long)b * rows + cur.row] =
-                whole ? make_int2(-1, -1) : make_int2(blockIdx.x, line.cta_of(cur.u + cur.tiles - 1));
+        if constexpr (kShared) {
+            bad = __any_sync(0xFFFFFFFFu, bad);
+            if (lane == 0 && cur.tile == 0)
+                p.span[(long long)b * rows + cur.row] =
+                    whole ? make_int2(-1, -1) : make_int2(worker, line.cta_of(cur.u + cur.tiles - 1));
+            float* to = whole ? p.own_o + out0 * D : p.part_o + slot * D;
+            float2* ml = whole ? p.own_ml + out0 : p.part_ml + slot;
+#pragma unroll
+            for (int t = 0; t < NH; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = t * 8 + (lane & 3) * 2 + c;
+                    if (head0 + h >= p.group) continue;
+                    if (lane < 4) ml[h] = make_float2(m[t][c], bad ? kBadPart : l[t][c]);
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt) {
+                        to[h * D + mt * 16 + (lane >> 2)] = acc[t][mt][c];
+                        to[h * D + mt * 16 + 8 + (lane >> 2)] = acc[t][mt][c + 2];
+                    }
+                }
+            next_row<kTile>(p, rows, cur);
+            continue;
+        }
+        bad = __syncthreads_or(bad);
         if (threadIdx.x < kHeads) {
             const int h = threadIdx.x;
             float mx = -INFINITY, sum = 0.0f;
@@ -435,9 +468,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
             joined_s[h] = make_float2(mx, whole ? (sum > 0.0f ? 1.0f / sum : NAN) : 1.0f);
             const float2 ml = make_float2(mx, bad ? kBadPart : sum);
             if (!whole) p.part_ml[slot + h] = ml;
-            else if (kShared) {
-                if (h < p.group - head0) p.own_ml[out0 + h] = ml;
-            } else if (h < p.group - head0) {
+            else if (h < p.group - head0) {
                 if (p.lse && !bad) p.lse[out0 + h] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
                 if (kWeights) p.row_ml[(((long long)b * p.Hkv + kv_head) * p.head_blocks + head0 / kHeads) * kHeads + h] = ml;
             }
@@ -475,8 +506,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                     const int xd = half * (D / 2) + x, h = t * 8 + hh;
                     if (!whole) {
                         *reinterpret_cast<float2*>(p.part_o + (slot + h) * D + xd) = o;
-                    } else if (kShared) {
-                        if (head0 + h < p.group) *reinterpret_cast<float2*>(p.own_o + (out0 + h) * D + xd) = o;
                     } else if (head0 + h < p.group && !bad) {
                         const float inv = joined_s[h].y;
                         *reinterpret_cast<uint32_t*>(p.o + (out0 + h) * D + xd) =
@@ -486,8 +515,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 __syncthreads();
             }
         }
-        next_row(p, rows, cur);
+        next_row<kTile>(p, rows, cur);
     }
+    if (kShared) pdl_wait();       // the join waits for this kernel only
     if (!kShared && !p.whole && threadIdx.x == 0) {
         // a row whose second part was this CTA's: for the join
         int4 d = make_int4(-1, 0, 0, 0);
@@ -570,7 +600,7 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
         constexpr int kG = 8;                          // query heads at a time
         __shared__ float2 ml_s[kG];                    // (m, 1 / l)
         __shared__ int bad_s;
-        const Line line = make_line(p, p.Hkv * p.head_blocks);
+        const Line line = make_line(p, p.Hkv * p.head_blocks, p.grid);
         // this block's places on the line of K/V heads, which has one for head_blocks of the attention kernel's
         const int units = line.units / p.head_blocks, block = blockIdx.x - p.grid, blocks = gridDim.x - p.grid;
         const int per = units / blocks, more = units - per * blocks;

@@ -4,8 +4,12 @@
 // Mathematics.  The prefix's keys are the same for all sequences, so the queries of a K/V head's group in all sequences,
 // B * G rows (G = H / Hkv), form one matrix against them:
 //   S = Q K^T,  m_i = max_j S_ij,  P_ij = exp((S_ij - m_i) / sqrt(d)),  l_i = sum_j P_ij,  O_i = sum_j P_ij v_j,
-// with a running m and l over tiles of 128 keys.  The keys are dealt to CTAs in contiguous ranges; a row's parts
-// (m, l, O in fp32) of all ranges and of its own keys are joined as in decode.cuh.
+// with a running m and l over tiles of 128 keys; a row's parts (m, l, O in fp32) and those of its own keys are joined as
+// in decode.cuh.
+//
+// Work.  A unit is a block of rows of a K/V head, with all tiles of keys as its steps.  The steps of all units form one line,
+// which one CTA per SM divide evenly (the host knows every length, so the places are arithmetic): a CTA takes a
+// contiguous range, and leaves one part for each unit that it meets.
 //
 // Bound.  Every key of the prefix is read once for the batch (2 * d * 2 bytes) and costs 4 * d * B * G flops: with some
 // 285 rows and more the tensor pipe bounds it, with fewer HBM.  So the products run on tcgen05, with queries as the 128
@@ -17,9 +21,10 @@
 // P is rounded to bf16 for the second product (tcgen05 takes it in that type from TMEM; a second product
 // with its lower bits, as in decode.cuh, would double the work that bounds the kernel), l sums the unrounded weights.
 //
-// Loads.  Two warps copy keys and values with cp.async, row by row, into the 128-byte-swizzled tiles that the
-// tensor pipe reads: any page size, any number of heads, no tensor maps to make on the host.  Each load is signalled kLag
-// loads later, when it has landed (cp.async.wait_group, a proxy fence, an mbarrier), so kLag + 1 are in flight.
+// Loads.  Three warps copy keys and values with cp.async, row by row, into the 128-byte-swizzled tiles that the tensor pipe
+// reads: any page size, any number of heads, no tensor maps to make on the host (TMA boxes of a page's rows reach the
+// same rate from 64 rows on, and half of HBM's with 8).  A slot's barrier counts the copies as they land, and the
+// products' thread sets a proxy fence between that and its first product.  The softmax warps load the queries.
 #pragma once
 #include "cache_common.cuh"
 #include "decode.cuh"
@@ -32,18 +37,27 @@ struct PrefixParams {
     const char* v;
     Pages pages;                   // table: the first sequence's row
     int H, Hkv, group, rows;       // rows = B * group
-    int prefix_len, tiles;         // keys, and tiles of 128 of them
-    int row_blocks, splits;        // blocks of 256 rows (kSingle: 128), ranges of tiles
+    uint32_t group_mul, group_shift;       // row / group = row * group_mul >> group_shift (as in Pages)
+    int prefix_len;
+    int row_blocks;                // blocks of 256 rows (kSingle: 128)
+    int steps;                     // of a unit: tiles of 128 keys (kSingle: pairs of them)
+    int per, more, ctas;           // places of a CTA on the line: `per`, the first `more` CTAs one more
+    int slots;                     // parts that a CTA may leave
     float scale_log2;              // log2(e) / sqrt(d)
-    float* part_o;                 // [CTAs][2][128][d]
-    float2* part_ml;               // [CTAs][2][128]: (m in logits, l); l = -1: a bad page
+    float* part_o;                 // [ctas][slots][2][128][d]
+    float2* part_ml;               // [ctas][slots][2][128]: (m in logits, l); l = -1: a bad page
     unsigned long long wait_limit_ns;
+    // the line has fewer than 2^31 places (the host checks)
+    __device__ __forceinline__ int start(int c) const { return per * c + min(c, more); }
+    __device__ __forceinline__ int cta_of(int u) const {
+        return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
+    }
 };
 
-constexpr int kPfThreads = 384;    // warpgroups 0, 1: softmax; warps 8 and 10 load, warp 9 issues the products
+constexpr int kPfThreads = 384;    // warpgroups 0, 1: queries, softmax; warps 8, 10 and 11 load, warp 9 issues the products
 constexpr int kPfTile = 128;
 constexpr int kPfBox = kPfTile * 64 * 2;       // 64 columns of a tile: rows of 128 bytes
-constexpr uint32_t kPfRegsSoftmax = 200, kPfRegsOther = 104;       // 256 * 200 + 128 * 104 = 384 * 168
+constexpr uint32_t kPfRegsSoftmax = 208, kPfRegsOther = 88;       // 256 * 208 + 128 * 88 = 384 * 168
 constexpr uint32_t kPfTmemCols = 512;          // S0 | S1 | O0 | O1
 
 template <int D, bool kSingle>
@@ -51,12 +65,13 @@ struct PfGeo {
     static constexpr int kTileBytes = kPfTile * D * 2;
     static constexpr int kQTiles = kSingle ? 1 : 2;
     static constexpr int kStages = 7 * 128 / D - kQTiles;          // all the shared memory that Q leaves
-    static constexpr int kLag = D == 128 ? 2 : 5;                  // 96 KB in flight
     static constexpr int kRing = kQTiles * kTileBytes;
+    static constexpr int kRoom = kQTiles * kTileBytes / 8;         // of Q, a softmax warp's, on a part's way out
+    static constexpr int kCols = kRoom / 128 < 32 ? kRoom / 128 : 32;      // columns of its 32 rows at a time: 16 or 32
     static constexpr int kBars = kRing + kStages * kTileBytes;
     // barriers
-    static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kSFull = kQFull + 1, kPFull = kSFull + 2,
-                         kOFull = kPFull + 2, kDrain = kOFull + 2, kNumBars = kDrain + 1;
+    static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 1, kSFull = kQFree + 1,
+                         kPFull = kSFull + 2, kOFull = kPFull + 2, kDrain = kOFull + 2, kNumBars = kDrain + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;             // TMEM address, abort flag, bad page
     static constexpr int kSmem = kMisc + 16 + 1024;                // from a 1024-byte boundary
     static_assert(kSmem <= 232448, "shared memory over the 227 KB limit");
@@ -88,25 +103,37 @@ __device__ __forceinline__ uint64_t pf_desc(uint32_t addr, uint32_t leading, uin
 __host__ __device__ constexpr uint32_t pf_idesc(int N, bool b_mn) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u : 0u) << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
+// 16 bytes global -> shared under an L2 policy
+__device__ __forceinline__ void pf_copy16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
+// the barrier counts this thread's arrival once all its copies so far have landed
+__device__ __forceinline__ void pf_arrive_landed(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // where chunk c (16 bytes) of row r is in a tile
 __device__ __forceinline__ uint32_t pf_chunk(int r, int c) {
     return (uint32_t)((c >> 3) * kPfBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// The range of a CTA, and its row block: CTAs that read the same keys are neighbours.
-struct PfWork {
-    int rb, kv, t0, t1;
+// A CTA's share of a unit: steps j0 .. j1 - 1.  Units of one K/V head are neighbours, row block by row block.
+struct PfShare {
+    int unit, j0, j1, rb, kv;
 };
-__device__ __forceinline__ PfWork pf_work(const PrefixParams& p, int cta) {
-    PfWork w;
-    w.rb = cta % p.row_blocks;
-    const int rest = cta / p.row_blocks;
-    w.kv = rest % p.Hkv;
-    const int s = rest / p.Hkv, base = p.tiles / p.splits, more = p.tiles - base * p.splits;
-    w.t0 = s * base + min(s, more);
-    w.t1 = w.t0 + base + (s < more);
-    return w;
-}
+struct PfWalk {                    // over the shares of a range u .. end - 1 of the line
+    int u, end;
+    __device__ __forceinline__ PfWalk(const PrefixParams& p) : u(p.start(blockIdx.x)), end(p.start(blockIdx.x + 1)) {}
+    __device__ __forceinline__ bool next(const PrefixParams& p, PfShare& w) {
+        if (u >= end) return false;
+        w.unit = u / p.steps;
+        w.j0 = u - w.unit * p.steps;
+        w.j1 = min(p.steps, w.j0 + end - u);
+        w.kv = w.unit / p.row_blocks;
+        w.rb = w.unit - w.kv * p.row_blocks;
+        u += w.j1 - w.j0;
+        return true;
+    }
+};
 
 template <int D, bool kSingle>
 __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
@@ -121,10 +148,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
-            ptx::mbar_init(bar(G::kFull + s), 64);
+            ptx::mbar_init(bar(G::kFull + s), 96);
             ptx::mbar_init(bar(G::kEmpty + s), 1);
         }
         ptx::mbar_init(bar(G::kQFull), 256);
+        ptx::mbar_init(bar(G::kQFree), 256);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(G::kSFull + i), 1);
             ptx::mbar_init(bar(G::kPFull + i), kPfTile);
@@ -146,89 +174,120 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
     pdl_wait();
     pdl_launch();
 
-    const PfWork w = pf_work(p, blockIdx.x);
-    const int steps = kSingle ? (w.t1 - w.t0 + 1) / 2 : w.t1 - w.t0;
-    const int key_end = min(p.prefix_len, w.t1 * kPfTile);         // behind the range's last key
-    // tile of step jj that warpgroup t's rows meet
-    auto tile_of = [&](int jj, int t) { return kSingle ? w.t0 + 2 * jj + t : w.t0 + jj; };
+    PfWalk walk(p);
+    PfShare w = {};
+    // tile of a unit's step j that warpgroup t's rows meet
+    auto tile_of = [&](int j, int t) { return kSingle ? 2 * j + t : j; };
 
     if (warp >= 8) {
         ptx::reg_dealloc<kPfRegsOther>();
-        if (warp == 8 || warp == 10) {
+        if (warp != 9) {
             // ------------------------------------------------------------------ loads
             // In the order in which the products take them: K0 V0 K1 V1 ..., or with two key tiles a step (a, b)
-            // Ka0 Kb0, then Va0 Ka1 Vb0 Kb1, ..., and at the end Va Vb.
-            const int half = warp == 8 ? 0 : 64, total = (kSingle ? 4 : 2) * steps;
-            constexpr int kChunks = D / 8, kRowsPerCopy = 32 / kChunks;
-            const long long key_stride = (long long)p.Hkv * D * 2;
+            // Ka0 Kb0, then Va0 Ka1 Vb0 Kb1, ..., and at the end Va Vb of every share.  A tile's 16 groups of 8 rows are dealt to
+            // the three warps; the pages of a tile of keys are looked up once, for its values too, and before the wait for a slot.
+            const int who = warp == 8 ? 0 : warp - 9;
+            constexpr int kChunks = D / 8, kRowsPerCopy = 32 / kChunks, kCopies = 8 / kRowsPerCopy;
+            const uint32_t key_stride = (uint32_t)p.Hkv * D * 2;   // (the host refuses more)
             const uint64_t policy = p.row_blocks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
-            struct Found { int tile_v, row[2]; };                  // value tile? ; rows of keys half + lane and + 32 (-1: none)
-            auto find = [&](int pos) {
-                int jj, t = 0, v;
-                if (!kSingle) {
-                    jj = pos >> 1;
-                    v = pos & 1;
-                } else if (pos < 2) {
-                    jj = 0; t = pos; v = 0;
-                } else {
-                    const int g = (pos - 2) >> 2, r = (pos - 2) & 3;
-                    if (g < steps - 1) {
-                        t = r >> 1;
-                        v = !(r & 1);
-                        jj = v ? g : g + 1;
-                    } else {
-                        t = r; v = 1; jj = g;
-                    }
-                }
-                Found f;
-                f.tile_v = v;
-                const int j0 = tile_of(jj, t) * kPfTile + half + lane;
-                bool bad = false;
+            // keys `lane` and + 32 of this warp's 48 (40) of a tile: in group who + 3 * (i / 8), as page and its slot (-1:
+            // behind the prefix)
+            struct Rows { int page[2], in[2]; };
+            auto lookup = [&](int tile) {
+                Rows r;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int j = j0 + 32 * u;
-                    f.row[u] = j < key_end ? page_row(p.pages, p.pages.table, j) : -1;
-                    bad |= j < key_end && f.row[u] < 0;
+                    const int i = lane + 32 * u, in_tile = (who + 3 * (i >> 3)) * 8 + (i & 7), key = tile * kPfTile + in_tile;
+                    const bool there = in_tile < kPfTile && key < p.prefix_len;
+                    const int pg = page_of(p.pages, there ? key : 0);
+                    r.in[u] = there ? key - pg * p.pages.page_size : -1;
+                    r.page[u] = there ? __ldg(p.pages.table + pg) : -1;
                 }
-                if (bad) {
-                    *bad_flag = 1u;
-                    report_invalid(ATTN_CACHE_SITE_PREFIX);
-                }
-                return f;
+                return r;
             };
-            Found next = find(0);
-            bool ok = true;
-            int pos = 0;
-#pragma unroll 1
-            for (; pos < total; ++pos) {
-                const Found f = next;
-                if (pos + 1 < total) next = find(pos + 1);
-                const int slot = pos % G::kStages;
-                if (pos >= G::kStages) {
-                    ok = pf_wait(bar(G::kEmpty + slot), (uint32_t)(pos / G::kStages - 1) & 1u, abort_flag, lim);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) break;
-                }
-                const char* src = (f.tile_v ? p.v : p.k) + (long long)w.kv * D * 2 + (lane % kChunks) * 16;
-                const uint32_t dst = sbase + (uint32_t)(G::kRing + slot * G::kTileBytes);
+            // where this lane's 16 bytes of each copy of a group go in a slot (the next group of this warp lies 24 rows on)
+            uint32_t to[kCopies];
 #pragma unroll
-                for (int i = 0; i < 64 / kRowsPerCopy; ++i) {
-                    const int r = i * kRowsPerCopy + lane / kChunks;           // of this warp's 64
-                    const int row = __shfl_sync(0xFFFFFFFFu, i * kRowsPerCopy < 32 ? f.row[0] : f.row[1], r & 31);
-                    cp_async16(dst + pf_chunk(half + r, lane % kChunks), src + (long long)max(row, 0) * key_stride,
-                               row < 0 ? 0u : 16u, policy);
+            for (int i = 0; i < kCopies; ++i) to[i] = pf_chunk(who * 8 + i * kRowsPerCopy + lane / kChunks, lane % kChunks);
+            const int groups = who == 0 ? 6 : 5;
+            uint32_t pos = 0;                                      // loads
+            bool ok = true;
+            auto load = [&](const char* base, const Rows& f) {
+                const uint32_t slot = pos % G::kStages;
+                if (pos >= G::kStages) {
+                    ok = pf_wait(bar(G::kEmpty + slot), (pos / G::kStages - 1) & 1u, abort_flag, lim);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) return;
                 }
-                cp_async_commit();
-                if (pos >= G::kLag) {
-                    cp_async_wait<G::kLag>();
-                    ptx::fence_proxy_async_smem();
-                    ptx::mbar_arrive(bar(G::kFull + (pos - G::kLag) % G::kStages));
+                const uint32_t dst = sbase + (uint32_t)G::kRing + slot * G::kTileBytes;
+                const char* src = base + (long long)w.kv * D * 2 + (lane % kChunks) * 16;
+                bool there = true;
+                int row[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const bool good = (unsigned)f.page[u] < (unsigned)p.pages.num_pages;
+                    there &= good || lane + 32 * u >= groups * 8;
+                    row[u] = good ? f.page[u] * p.pages.page_size + f.in[u] : -1;
+                    if (!good && f.in[u] >= 0) {
+                        *bad_flag = 1u;
+                        report_invalid(ATTN_CACHE_SITE_PREFIX);
+                    }
+                }
+                if (__all_sync(0xFFFFFFFFu, there)) {
+                    // (a group's rows are handed over before its copies: one after another, each copy would wait for its own)
+#pragma unroll
+                    for (int n = 0; n < 6; ++n) {
+                        if (n == 5 && groups == 5) break;
+                        const char* from[kCopies];
+#pragma unroll
+                        for (int i = 0; i < kCopies; ++i)
+                            from[i] = src + (unsigned long long)key_stride *
+                                      (uint32_t)__shfl_sync(0xFFFFFFFFu, row[n >> 2], (n * 8 + i * kRowsPerCopy + lane / kChunks) & 31);
+#pragma unroll
+                        for (int i = 0; i < kCopies; ++i) pf_copy16(dst + to[i] + n * (24 * 128), from[i], policy);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int n = 0; n < groups; ++n)
+#pragma unroll
+                        for (int i = 0; i < kCopies; ++i) {
+                            const int x = __shfl_sync(0xFFFFFFFFu, n < 4 ? row[0] : row[1], (n * 8 + i * kRowsPerCopy + lane / kChunks) & 31);
+                            cp_async16(dst + to[i] + n * (24 * 128), src + (unsigned long long)key_stride * (uint32_t)max(x, 0),
+                                       x < 0 ? 0u : 16u, policy);
+                        }
+                }
+                pf_arrive_landed(bar(G::kFull + slot));
+                ++pos;
+            };
+#pragma unroll 1
+            while (ok && walk.next(p, w)) {
+                if constexpr (!kSingle) {
+                    Rows next = lookup(w.j0);
+#pragma unroll 1
+                    for (int j = w.j0; j < w.j1 && ok; ++j) {
+                        const Rows f = next;
+                        if (j + 1 < w.j1) next = lookup(j + 1);
+                        load(p.k, f);
+                        if (ok) load(p.v, f);
+                    }
+                } else {
+                    Rows f[2] = {lookup(2 * w.j0), lookup(2 * w.j0 + 1)};
+                    load(p.k, f[0]);
+                    if (ok) load(p.k, f[1]);
+#pragma unroll 1
+                    for (int j = w.j0; j < w.j1 && ok; ++j)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const Rows now = f[t];
+                            if (j + 1 < w.j1) f[t] = lookup(2 * j + 2 + t);
+                            if (ok) load(p.v, now);
+                            if (ok && j + 1 < w.j1) load(p.k, f[t]);
+                        }
                 }
             }
-            cp_async_wait<0>();
-            ptx::fence_proxy_async_smem();
-            if (pos == total)
-                for (int q = max(total - G::kLag, 0); q < total; ++q) ptx::mbar_arrive(bar(G::kFull + q % G::kStages));
-        } else if (warp == 9 && lane == 0) {
+            cp_async_commit();
+            cp_async_wait<0>();                                    // (a block that gives up leaves no copy behind)
+        } else if (lane == 0) {
             // ------------------------------------------------------------------ products
             constexpr uint32_t idesc_s = pf_idesc(kPfTile, false), idesc_o = pf_idesc(D, true);
             // Q, K: rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart, 16 elements 32 bytes on, the second 64
@@ -252,54 +311,58 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                 for (int kk = 0; kk < kPfTile / 16; ++kk)
                     ptx::mma_ts(d, a + (uint32_t)kk * 8u, b0 + (uint64_t)((kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : acc0);
             };
-            uint32_t pos = 0;
-            bool ok = pf_wait(bar(G::kQFull), 0, abort_flag, lim);
-            // the slot of the next load in order, once it has landed
+            uint32_t pos = 0, count = 0;                           // loads, and steps, before this share
+            bool ok = true;
+            // the slot of load `at`, once it has landed
             auto landed = [&](uint32_t at) {
                 ok = ok && pf_wait(bar(G::kFull + at % G::kStages), (at / G::kStages) & 1u, abort_flag, lim);
+                ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 return at % G::kStages;
             };
             auto release = [&](uint32_t at) { ptx::mma_commit(bar(G::kEmpty + at % G::kStages)); };
-            {
-                const uint32_t s0 = landed(0);
-                if (ok) {
+#pragma unroll 1
+            for (uint32_t n = 0; ok && walk.next(p, w); ++n) {
+                const int steps = w.j1 - w.j0;
+                ok = pf_wait(bar(G::kQFull), n & 1u, abort_flag, lim);
+                {
+                    const uint32_t s0 = landed(pos);
+                    if (!ok) break;
                     issue_s(0, s0);
                     ptx::mma_commit(bar(G::kSFull));
-                    if (kSingle) release(0);
-                }
-                const uint32_t s1 = kSingle ? landed(1) : s0;
-                if (ok) {
+                    if (kSingle) release(pos++);
+                    const uint32_t s1 = kSingle ? landed(pos) : s0;
+                    if (!ok) break;
                     issue_s(1, s1);
                     ptx::mma_commit(bar(G::kSFull + 1));
-                    release(kSingle ? 1 : 0);
+                    release(pos++);
                 }
-                pos = kSingle ? 2 : 1;
-            }
 #pragma unroll 1
-            for (int jj = 0; jj < steps && ok; ++jj) {
-                const bool more = jj + 1 < steps;
-                // loads of this step: value tile(s) vt, key tile(s) of the next step kt
-                const uint32_t v0 = pos, k0 = pos + 1, v1 = kSingle ? pos + (more ? 2 : 1) : pos, k1 = kSingle ? pos + 3 : pos + 1;
+                for (int jj = 0; jj < steps && ok; ++jj) {
+                    const bool more = jj + 1 < steps;
+                    // loads of this step: value tile(s), key tile(s) of the next step
+                    const uint32_t v0 = pos, k0 = pos + 1, v1 = kSingle ? pos + (more ? 2 : 1) : pos, k1 = kSingle ? pos + 3 : pos + 1;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t vt = t ? v1 : v0, kt = t ? k1 : k0;
-                    const uint32_t vs = landed(vt);
-                    ok = ok && pf_wait(bar(G::kPFull + t), (uint32_t)jj & 1u, abort_flag, lim);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    issue_o(t, vs, jj == 0);
-                    if (!more) ptx::mma_commit(bar(G::kOFull + t));
-                    if (kSingle || t == 1) release(vt);
-                    if (more) {
-                        const uint32_t ks = landed(kt);
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t vt = t ? v1 : v0, kt = t ? k1 : k0;
+                        const uint32_t vs = kSingle || t == 0 ? landed(vt) : vt % G::kStages;
+                        ok = ok && pf_wait(bar(G::kPFull + t), (count + jj) & 1u, abort_flag, lim);
                         if (!ok) break;
-                        issue_s(t, ks);
-                        ptx::mma_commit(bar(G::kSFull + t));
-                        if (kSingle || t == 1) release(kt);
+                        ptx::tc_fence_after();
+                        issue_o(t, vs, jj == 0);
+                        if (!more) ptx::mma_commit(bar(G::kOFull + t));
+                        if (kSingle || t == 1) release(vt);
+                        if (more) {
+                            const uint32_t ks = kSingle || t == 0 ? landed(kt) : kt % G::kStages;
+                            if (!ok) break;
+                            issue_s(t, ks);
+                            ptx::mma_commit(bar(G::kSFull + t));
+                            if (kSingle || t == 1) release(kt);
+                        }
                     }
+                    pos += (kSingle ? 2 : 1) * (more ? 2 : 1);
                 }
-                pos += (kSingle ? 2 : 1) * (more ? 2 : 1);
+                count += steps;
             }
             // every product has finished before TMEM goes back
             ptx::mma_commit(bar(G::kDrain));
@@ -309,36 +372,46 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
         }
     } else {
         ptx::reg_alloc<kPfRegsSoftmax>();
-        // ---------------------------------------------------------------------- queries, softmax
+        // ---------------------------------------------------------------------- softmax
         const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-        const int block0 = w.rb * (kSingle ? kPfTile : 2 * kPfTile);           // first row of the CTA
-        {
-            constexpr int kChunks = D / 8, kRowsQ = kSingle ? kPfTile : 2 * kPfTile;
-#pragma unroll 4
-            for (int i = threadIdx.x; i < kRowsQ * kChunks; i += 256) {
-                const int r = i / kChunks, c = i % kChunks, at = block0 + r;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (at < p.rows) {
-                    const int b = at / p.group, g = at - b * p.group;
-                    x = *reinterpret_cast<const uint4*>(p.q + ((long long)b * p.H + w.kv * p.group + g) * D + c * 8);
-                }
-                ptx::st_shared_v4(sbase + (uint32_t)((r / kPfTile) * G::kTileBytes) + pf_chunk(r % kPfTile, c), x.x, x.y, x.z, x.w);
-            }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(bar(G::kQFull));
-        }
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_off + 128u * t, tO = tmem + lane_off + 256u + (uint32_t)(D * t);
         const float c = p.scale_log2, tau = 8.0f;                  // a reference may lag by 2^8
-        const int at = block0 + (kSingle ? row : t * kPfTile + row);
+        // queries of a share, 16 bytes of a row at a time
+        constexpr int kChunks = D / 8, kRowsQ = G::kQTiles * kPfTile, kQ = kRowsQ * kChunks / 256;
+        auto put_queries = [&](const PfShare& s) {
+            uint4 q[kQ];
+            const int c8 = threadIdx.x % kChunks;
+            const __nv_bfloat16* from = p.q + (long long)s.kv * p.group * D + c8 * 8;
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) {
+                const int at = s.rb * kRowsQ + (i * 256 + threadIdx.x) / kChunks;
+                const int b = (int)(((unsigned long long)(uint32_t)at * p.group_mul) >> p.group_shift);
+                q[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (at < p.rows) q[i] = *reinterpret_cast<const uint4*>(from + ((long long)b * p.H + at - b * p.group) * D);
+            }
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) {
+                const int r = (i * 256 + threadIdx.x) / kChunks;
+                ptx::st_shared_v4(sbase + (uint32_t)((r / kPfTile) * G::kTileBytes) + pf_chunk(r % kPfTile, c8), q[i].x, q[i].y,
+                                  q[i].z, q[i].w);
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(bar(G::kQFull));
+        };
+        uint32_t count = 0;                                        // steps before this share
+        bool ok = true, have = walk.next(p, w);
+        put_queries(w);
+#pragma unroll 1
+        for (uint32_t n = 0; have; ++n) {
+        const int at = w.rb * (kSingle ? kPfTile : 2 * kPfTile) + (kSingle ? row : t * kPfTile + row);
         // warps without a row keep every wait and arrival, and skip the rest: a row is its own lane of TMEM
         const bool live = at - lane < p.rows;
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
         if (!live) {
 #pragma unroll 1
-            for (int jj = 0; jj < steps; ++jj) {
-                ok = pf_wait(bar(G::kSFull + t), (uint32_t)jj & 1u, abort_flag, lim);
+            for (int j = w.j0; j < w.j1; ++j, ++count) {
+                ok = pf_wait(bar(G::kSFull + t), count & 1u, abort_flag, lim);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
                 ptx::tc_fence_before();
@@ -346,13 +419,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
             }
         } else {
 #pragma unroll 1
-            for (int jj = 0; jj < steps; ++jj) {
-                ok = pf_wait(bar(G::kSFull + t), (uint32_t)jj & 1u, abort_flag, lim);
+            for (int j = w.j0; j < w.j1; ++j, ++count) {
+                ok = pf_wait(bar(G::kSFull + t), count & 1u, abort_flag, lim);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
                 uint32_t s[128];
                 ptx::tmem_ld128(tS, s);
-                const int valid = key_end - tile_of(jj, t) * kPfTile;          // keys of the tile (the same for every row)
+                const int valid = p.prefix_len - tile_of(j, t) * kPfTile;      // keys of the tile (the same for every row)
                 if (valid < kPfTile) {
 #pragma unroll
                     for (int e = 0; e < 128; ++e)
@@ -380,7 +453,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                 float alpha = 1.0f;
                 if (mx > m && (mx - m) * c > tau) {
                     alpha = rescale(m, mx, c);
-                    rescale_o = m != -INFINITY && jj > 0;
+                    rescale_o = m != -INFINITY && j > w.j0;
                     l *= alpha;
                     m = mx;
                 }
@@ -433,21 +506,45 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                 ptx::mbar_arrive(bar(G::kPFull + t));
             }
         }
-        if (ok) ok = pf_wait(bar(G::kOFull + t), 0, abort_flag, lim);
-        if (__all_sync(0xFFFFFFFFu, ok) && live) {
-            ptx::tc_fence_after();
-            uint32_t o[D];
-            if constexpr (D == 128) ptx::tmem_ld128(tO, o);
-            else ptx::tmem_ld64(tO, o);
-            if (at < p.rows) {
-                const long long part = ((long long)blockIdx.x * 2 + t) * kPfTile + row;
-                float4* to = reinterpret_cast<float4*>(p.part_o + part * D);
+        if (!ok) break;
+        have = walk.next(p, w);
+        ok = pf_wait(bar(G::kOFull + t), n & 1u, abort_flag, lim);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        ptx::tc_fence_after();
+        // The warp's 32 rows, some columns at a time, through its share of Q (its products ended before the last ones of
+        // values): each store then takes whole 128-byte lines (64-byte pieces where the room is less).
+        if (live) {
+            constexpr int kCols = G::kCols, kPieces = kCols / 4, kSide = 32 / kPieces;       // 16-byte pieces of a row, rows at a time
+            const long long part0 = (((long long)blockIdx.x * p.slots + n) * 2 + t) * kPfTile + quarter * 32;
+            const uint32_t room = sbase + (uint32_t)(warp * G::kRoom);
+            const int rows = min(32, p.rows - (at - lane));
+#pragma unroll 1
+            for (int ch = 0; ch < D / kCols; ++ch) {
+                uint32_t o[kCols];
+                if constexpr (kCols == 32) ptx::tmem_ld32(tO + ch * 32, o);
+                else ptx::tmem_ld16(tO + ch * 16, o);
 #pragma unroll
-                for (int i = 0; i < D / 4; ++i)
-                    to[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                                        __uint_as_float(o[4 * i + 3]));
-                p.part_ml[part] = make_float2(m, *bad_flag ? kBadPart : l);
+                for (int i = 0; i < kPieces; ++i)
+                    ptx::st_shared_v4(room + lane * (kCols * 4) + ((i ^ (lane & (kPieces - 1))) << 4), o[4 * i], o[4 * i + 1],
+                                      o[4 * i + 2], o[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int r = i * kSide + lane / kPieces, x = lane % kPieces;
+                    const float4 y = *reinterpret_cast<const float4*>(smem + warp * G::kRoom + r * (kCols * 4) +
+                                                                      ((x ^ (r & (kPieces - 1))) << 4));
+                    if (r < rows) *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + ch * kCols + x * 4) = y;
+                }
+                __syncwarp();
             }
+            if (lane < rows) p.part_ml[part0 + lane] = make_float2(m, *bad_flag ? kBadPart : l);
+        }
+        if (have) {
+            ptx::mbar_arrive(bar(G::kQFree));                      // every softmax warp's part has to be out of Q
+            ok = pf_wait(bar(G::kQFree), n & 1u, abort_flag, lim);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            put_queries(w);
+        }
         }
     }
     ptx::tc_fence_before();
@@ -461,7 +558,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
 struct PrefixJoin {
     PrefixParams x;                // of the prefix's kernel
     DecodeParams s;                // of the kernel of the own keys
-    int single, warps;             // one tile of rows a CTA; warps a row
+    int single, warps;             // one tile of rows a unit; warps a row
 };
 
 // The join: a row's parts of the prefix and of its own keys.  `warps` warps take a row, a contiguous share of its parts
@@ -483,10 +580,11 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps) attn_prefix_join_kernel(con
     const int len = __ldg(p.s.seqlens_k + b);
     const bool good = there && len >= p.x.prefix_len && (long long)len <= (long long)p.s.pages.max_pages * p.s.pages.page_size;
     if (there && !good && h == 0 && share == 0 && lane == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
-    // parts: the prefix's, then those of the own keys
+    // parts: the prefix's (of each CTA that has steps of the row's unit), then those of the own keys
     const int block_rows = p.single ? kPfTile : 2 * kPfTile, rb = r / block_rows, in = r - rb * block_rows;
-    const int shared_parts = p.x.splits * (p.single ? 2 : 1);
-    int c0 = -1, own = 0;                              // first CTA (-1: the row is whole) and number of the own parts
+    const int unit = kv * p.x.row_blocks + rb, first = p.x.cta_of(unit * p.x.steps);
+    const int shared_parts = (p.x.cta_of(unit * p.x.steps + p.x.steps - 1) - first + 1) * (p.single ? 2 : 1);
+    int c0 = -1, own = 0;                              // first warp (-1: the row is whole) and number of the own parts
     const int heads = p.s.block_heads, blk = g / heads, hh = g - blk * heads;
     if (good && len > p.x.prefix_len) {
         const int2 span = p.s.span[((long long)b * p.s.Hkv + kv) * p.s.head_blocks + blk];
@@ -496,17 +594,17 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps) attn_prefix_join_kernel(con
     const int parts = good ? shared_parts + own : 0;
     auto where = [&](int i, const float2*& ml, const float*& o) {
         if (i < shared_parts) {
-            const int s = p.single ? i >> 1 : i, t = p.single ? i & 1 : in / kPfTile;
-            const long long cta = ((long long)s * p.x.Hkv + kv) * p.x.row_blocks + rb;
-            const long long part = (cta * 2 + t) * kPfTile + in % kPfTile;
+            const int c = first + (p.single ? i >> 1 : i), t = p.single ? i & 1 : in / kPfTile;
+            const long long slot = (long long)c * p.x.slots + (unit - p.x.start(c) / p.x.steps);
+            const long long part = (slot * 2 + t) * kPfTile + in % kPfTile;
             ml = p.x.part_ml + part;
             o = p.x.part_o + part * D;
         } else if (c0 < 0) {
             ml = p.s.own_ml + out;
             o = p.s.own_o + out * D;
         } else {
-            const int c = c0 + i - shared_parts;       // a row's first part is in slot 1 of its CTA, the others in slot 0
-            const long long part = (long long)(2 * c + (c == c0)) * heads + hh;
+            const int c = c0 + i - shared_parts;       // a row's first part is in slot 1 of its warp, the others in slot 0
+            const long long part = (2ll * c + (c == c0)) * heads + hh;
             ml = p.s.part_ml + part;
             o = p.s.part_o + part * D;
         }

@@ -209,9 +209,10 @@ def test_bad_lengths_and_pages_leave_their_rows(attn):
         assert attn.cache_device_status() == (1, 22) and (o[2] == 7).all() and (lse[2] == 7).all()
         x.table[2, 8] = kept
         x.check((o, lse), rows=[0, 1, 3, 4])
-    x.table[0, 2] = len(x.k)                         # of the prefix: nobody's outputs are written
-    o, lse = run(x)
-    assert attn.cache_device_status() == (1, 26) and (o == 7).all() and (lse == 7).all()
+    for page in (len(x.k), -1, -2 ** 31):            # of the prefix: nobody's outputs are written
+        x.table[0, 2] = page
+        o, lse = run(x)
+        assert attn.cache_device_status() == (1, 26) and (o == 7).all() and (lse == 7).all()
 
 
 def test_stays_in_bounds_with_the_caller_s_workspace(attn):

@@ -1078,8 +1078,9 @@ def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix
         if workspace is None:
             ws_bytes = _prefix_workspace_bytes(dev, prefix_len, ("B", B), ("H", H), ("Hkv", Hkv), ("num_pages", pages),
                                                ("page_size", ps), ("max_pages", most), ("d", d))
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        st = (_lib or load()).attn_paged_prefix_decode(a, prefix_len, workspace.data_ptr(), ws_bytes,
+            if ws_bytes:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        st = (_lib or load()).attn_paged_prefix_decode(a, prefix_len, workspace.data_ptr() if ws_bytes else None, ws_bytes,
                                                        torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise AttnError(st, "attn_paged_prefix_decode")

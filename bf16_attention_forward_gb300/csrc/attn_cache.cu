@@ -530,17 +530,13 @@ int check_decode_workspace(const attn_decode_args_t& a, const void* workspace, s
     return DecodeRanges(a).clash({(uintptr_t)workspace, need}, 3) ? ATTN_ERR_ALIAS : ATTN_OK;
 }
 
-int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    int st = check_decode_shape(a);
-    if (st != ATTN_OK) return st;
-    if ((st = check_decode_tensors(a)) != ATTN_OK) return st;
-    int sms = 0;
-    if ((st = device(&sms)) != ATTN_OK) return st;
-    if ((st = check_decode_workspace(a, workspace, workspace_bytes, decode_layout(a, sms).bytes)) != ATTN_OK) return st;
+// common: leading keys that every sequence has of the first one's pages
+int launch_decode_call(const attn_decode_args_t& a, int64_t common, int sms, void* workspace, cudaStream_t stream) {
     const DecodeLayout l = decode_layout(a, sms);
     char* ws = reinterpret_cast<char*>(workspace);
     DecodeParams p;
     fill_decode(p, a, sms);
+    p.common = (int)common;
     p.part_o = reinterpret_cast<float*>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
     p.split = reinterpret_cast<int4*>(ws + l.split);
@@ -557,7 +553,26 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
                      : launch_decode<64, 4>(p, stream);
 }
 
+int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    int st = check_decode_shape(a);
+    if (st != ATTN_OK) return st;
+    if ((st = check_decode_tensors(a)) != ATTN_OK) return st;
+    int sms = 0;
+    if ((st = device(&sms)) != ATTN_OK) return st;
+    if ((st = check_decode_workspace(a, workspace, workspace_bytes, decode_layout(a, sms).bytes)) != ATTN_OK) return st;
+    return launch_decode_call(a, 0, sms, workspace, stream);
+}
+
 // ------------------------------------------------------------------------------ shared prefix
+// Where a batch's tiles of the prefix, and two a row for its own keys and its end, are few, the decoding kernel itself reads the
+// prefix's pages for each sequence: one or two kernels instead of three.  us a call in a graph, d = 128, 8 K/V heads, again / shared:
+// 2 sequences of 16,384 shared keys (2,080 tiles) 24.0 / 28.0;  16 of 2,000 (2,256) 21.9 / 21.7;  64 of 200 (1,824) 21.8 / 24.1;
+// 4 of 16,384 (4,160) 36.3 / 30.3;  64 of 600 (3,430) 31.0 / 23.9;  256 of 32 (4,608) 45 / 36.
+bool prefix_again(const attn_decode_args_t& a, int64_t prefix_len, int sms) {
+    const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
+    return a.B == 1 || rows * (cdiv(prefix_len, kDecTile) + 2) <= 14 * sms;
+}
+
 // How the prefix's kernel divides: row blocks, and a line of steps over the CTAs.
 struct PrefixPlan {
     bool single;
@@ -569,9 +584,9 @@ PrefixPlan prefix_plan(const attn_decode_args_t& a, int64_t prefix_len, int sms)
     p.single = rows <= kPfTile;
     p.row_blocks = cdiv(rows, p.single ? kPfTile : 2 * kPfTile);
     p.steps = p.single ? cdiv(tiles, 2) : tiles;
-    p.line = a.Hkv * p.row_blocks * p.steps;
-    p.ctas = p.line < sms ? p.line : sms;
-    p.slots = (cdiv(p.line, p.ctas) - 1 + p.steps - 1) / p.steps + 1;      // shares of a range that begins anywhere
+    p.line = a.Hkv * p.row_blocks * (p.steps + kPfEnd);
+    p.ctas = a.Hkv * p.row_blocks * p.steps < sms ? a.Hkv * p.row_blocks * p.steps : sms;
+    p.slots = (cdiv(p.line, p.ctas) - 1 + p.steps + kPfEnd - 1) / (p.steps + kPfEnd) + 1;      // of a range that begins anywhere
     return p;
 }
 
@@ -597,11 +612,11 @@ int check_prefix_shape(const attn_decode_args_t& a, int64_t prefix_len) {
     const int st = check_decode_shape(a);
     if (st != ATTN_OK) return st;
     if (a.weights || prefix_len < 1 || prefix_len > a.max_pages * a.page_size) return ATTN_ERR_INVALID_ARG;
-    // strides of a key are 32 bits, places on the lines of both kernels int32
+    // strides of a key are 32 bits, places on the lines of both kernels int32; the join has heads in y, a warp each or more
     if (a.Hkv * a.d > kLim) return ATTN_ERR_UNSUPPORTED;
     const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
     if (cdiv(a.max_pages * a.page_size - prefix_len, kDecKeys) + 1 > (2 * kLim - 1) / rows) return ATTN_ERR_UNSUPPORTED;
-    if (cdiv(prefix_len, kPfTile) > (2 * kLim - 1) / (a.Hkv * cdiv(a.B * group, kPfTile))) return ATTN_ERR_UNSUPPORTED;
+    if (cdiv(prefix_len, kPfTile) + kPfEnd > (kLim - 1) / (a.Hkv * cdiv(a.B * group, kPfTile)) || a.H > 65535) return ATTN_ERR_UNSUPPORTED;
     return ATTN_OK;
 }
 
@@ -621,6 +636,10 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     if ((st = check_decode_tensors(a)) != ATTN_OK) return st;
     int sms = 0;
     if ((st = device(&sms)) != ATTN_OK) return st;
+    if (prefix_again(a, prefix_len, sms)) {
+        if ((st = check_decode_workspace(a, workspace, workspace_bytes, decode_layout(a, sms).bytes)) != ATTN_OK) return st;
+        return launch_decode_call(a, prefix_len, sms, workspace, stream);
+    }
     const PrefixPlan plan = prefix_plan(a, prefix_len, sms);
     const PrefixLayout l = prefix_layout(a, plan, sms);
     if ((st = check_decode_workspace(a, workspace, workspace_bytes, l.bytes)) != ATTN_OK) return st;
@@ -645,9 +664,11 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     x.Hkv = j.s.Hkv;
     x.group = j.s.group;
     x.rows = j.s.B * j.s.group;
-    const Pages by_group = make_pages(nullptr, 1, x.group, 1);     // its divisor's constants
-    x.group_mul = by_group.mul;
-    x.group_shift = by_group.shift;
+    auto divisor = [](int64_t n) {
+        const Pages c = make_pages(nullptr, 1, n, 1);
+        return Divisor{c.mul, c.shift};
+    };
+    x.by_group = divisor(x.group);
     x.prefix_len = (int)prefix_len;
     x.row_blocks = (int)plan.row_blocks;
     x.steps = (int)plan.steps;
@@ -655,15 +676,19 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     x.per = (int)(plan.line / plan.ctas);
     x.more = (int)(plan.line % plan.ctas);
     x.slots = (int)plan.slots;
+    x.by_places = divisor(plan.steps + kPfEnd);
+    x.by_per = divisor(x.per);
+    x.by_more = divisor(x.per + 1);
     x.scale_log2 = j.s.scale_log2;
     x.part_o = reinterpret_cast<float*>(ws + l.x_o);
     x.part_ml = reinterpret_cast<float2*>(ws + l.x_ml);
     x.wait_limit_ns = 2000000000ull;
     j.single = plan.single;
-    // a warp has at most 8 parts of a row, while a block has the warps
-    const int64_t parts = (plan.steps / x.per + 1) * (plan.single ? 2 : 1);
+    // several warps a row where a row has more parts than a warp has in flight, while the SMs have room (16 warps each):
+    // every warp has the same arithmetic to begin with
+    const int64_t parts = (cdiv(plan.steps - 1, x.per) + 1) * (plan.single ? 2 : 1);
     j.warps = 1;
-    while (j.warps < kPfJoinWarps && parts > 8 * j.warps) j.warps *= 2;
+    while (j.warps < kPfJoinWarps && parts > 8 * j.warps && a.B * a.H * j.warps * 2 <= 16 * sms) j.warps *= 2;
     st = a.d == 128 ? (plan.single ? launch_prefix<128, true>(x, plan.ctas, stream) : launch_prefix<128, false>(x, plan.ctas, stream))
                     : (plan.single ? launch_prefix<64, true>(x, plan.ctas, stream) : launch_prefix<64, false>(x, plan.ctas, stream));
     if (st != ATTN_OK) return st;
@@ -673,9 +698,10 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     else
         st = nh == 1 ? launch_own<64, 1>(j.s, stream) : nh == 2 ? launch_own<64, 2>(j.s, stream) : launch_own<64, 4>(j.s, stream);
     if (st != ATTN_OK) return st;
-    const int64_t grid = cdiv(a.B * a.H * j.warps, kPfJoinWarps);
-    return a.d == 128 ? launch(attn_prefix_join_kernel<128>, grid, 1, 32 * kPfJoinWarps, 0, stream, j)
-                      : launch(attn_prefix_join_kernel<64>, grid, 1, 32 * kPfJoinWarps, 0, stream, j);
+    const int heads = (int)cdiv(a.H * j.warps, kPfJoinWarps);
+    auto* join = a.d == 128 ? (parts <= 4 ? attn_prefix_join_kernel<128, 4> : attn_prefix_join_kernel<128, 8>)
+                            : (parts <= 4 ? attn_prefix_join_kernel<64, 4> : attn_prefix_join_kernel<64, 8>);
+    return launch(join, a.B, heads, 32 * kPfJoinWarps, 0, stream, j);
 }
 
 // ------------------------------------------------------------------------------ evict
@@ -1142,7 +1168,8 @@ int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream) {
 size_t attn_paged_prefix_decode_workspace_size(const attn_decode_args_t* args, int64_t prefix_len) {
     int sms = 0;
     if (!args || check_prefix_shape(*args, prefix_len) != ATTN_OK || device(&sms) != ATTN_OK) return 0;
-    return prefix_layout(*args, prefix_plan(*args, prefix_len, sms), sms).bytes;
+    return prefix_again(*args, prefix_len, sms) ? decode_layout(*args, sms).bytes
+                                           : prefix_layout(*args, prefix_plan(*args, prefix_len, sms), sms).bytes;
 }
 
 int attn_paged_prefix_decode(const attn_decode_args_t* args, int64_t prefix_len, void* workspace, size_t workspace_bytes,

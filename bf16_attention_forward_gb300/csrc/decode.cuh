@@ -55,6 +55,7 @@ struct DecodeParams {
     float2* row_ml;                // [B][Hkv][head_blocks][heads of a block] of unsplit rows (weights only)
     float* scores;                 // [B][H][score_room] logits (weights only)
     long long score_room;          // max_pages * page_size rounded up to 16 bytes
+    int common;                    // keys in front that every sequence has of the first one's pages (else 0)
     // behind a shared prefix (prefix.cuh, whose join merges every row): the keys from `first` on (else 0)
     int first;
     int block_heads;               // heads of a block: 8 * NH
@@ -83,7 +84,7 @@ struct DecGeo {
 // tiles of a sequence; 0 for a length that the table has no room for (the join kernel reports it)
 template <int kTile = kDecTile>
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, int n) {
-    return n > p.first && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - p.first - 1) / kTile + 1 : 0;
+    return n > p.first && n >= p.common && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - p.first - 1) / kTile + 1 : 0;
 }
 
 // The line: sequence by sequence, row by row, a row's tiles and its end.  (The host refuses sizes whose
@@ -170,7 +171,7 @@ __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor
 
 // The rows of a sequence without keys, and the report of a bad length; by the threads of a block.
 __device__ __forceinline__ void keyless(const DecodeParams& p, int b, int n, int d) {
-    if (n < 0 || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
+    if (n < p.common || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
     } else if (n == 0) {
 #pragma unroll 1
@@ -247,15 +248,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     // Where the loads are: find() looks up the rows of this warp's 16 keys of the tile at `ahead` (-1: past the
     // length or on a page that does not exist) and moves on; load() copies the tile found before into a
     // stage, absent rows as zeros.  A tile is found one load ahead, so that the table's latency is hidden.
-    struct Found { int row, kv_head; bool bad; };      // kv_head: -1 behind the range
+    struct Found { int row, kv_head, bad; };           // kv_head: -1 behind the range; bad: the site of a page that is not there
     auto find = [&]() {
-        Found f{-1, -1, false};
+        Found f{-1, -1, 0};
         if (ahead.u >= u1) return f;
         f.kv_head = ahead.row / p.head_blocks;
         const int j = p.first + ahead.tile * kTile + key0 + lane;
         if (lane < kDecKeys && j < ahead.len) {
-            f.row = page_row(p.pages, p.pages.table + (long long)ahead.b * p.pages.max_pages, j);
-            f.bad = f.row < 0;
+            f.row = page_row(p.pages, p.pages.table + (j < p.common ? 0 : (long long)ahead.b * p.pages.max_pages), j);
+            if (f.row < 0) f.bad = j < p.common ? ATTN_CACHE_SITE_PREFIX : ATTN_CACHE_SITE_DECODE;
         }
         ++ahead.u;
         if (++ahead.tile == ahead.tiles && ahead.u < u1) next_row<kTile>(p, rows, ahead);
@@ -263,11 +264,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     };
     auto load = [&](int stage, const Found& f) {
         if (f.kv_head >= 0) {
-            const bool any_bad = __any_sync(0xFFFFFFFFu, f.bad);
-            if (lane == 0) {
-                bad_s[warp][stage] = any_bad;
-                if (any_bad) report_invalid(ATTN_CACHE_SITE_DECODE);
-            }
+            const bool any_bad = __any_sync(0xFFFFFFFFu, f.bad != 0);
+            if (lane == 0) bad_s[warp][stage] = any_bad;
+            if (f.bad) report_invalid((uint32_t)f.bad);
             const int chunk = lane % kChunks;
             const long long col = (long long)f.kv_head * G::kRow + chunk * 16;
             const uint32_t dst = ring + stage * G::kStageBytes;

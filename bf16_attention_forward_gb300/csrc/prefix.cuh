@@ -9,7 +9,8 @@
 //
 // Work.  A unit is a block of rows of a K/V head, with all tiles of keys as its steps.  The steps of all units form one line,
 // which one CTA per SM divide evenly (the host knows every length, so the places are arithmetic): a CTA takes a
-// contiguous range, and leaves one part for each unit that it meets.
+// contiguous range, and leaves one part for each unit that it meets.  Behind each unit's steps the line has kPfEnd more places,
+// for the change of units, which takes as long (without them the CTAs that met one ended 6 to 10 us after the others).
 //
 // Bound.  Every key of the prefix is read once for the batch (2 * d * 2 bytes) and costs 4 * d * B * G flops: with some
 // 285 rows and more the tensor pipe bounds it, with fewer HBM.  So the products run on tcgen05, with queries as the 128
@@ -24,12 +25,21 @@
 // Loads.  Three warps copy keys and values with cp.async, row by row, into the 128-byte-swizzled tiles that the tensor pipe
 // reads: any page size, any number of heads, no tensor maps to make on the host (TMA boxes of a page's rows reach the
 // same rate from 64 rows on, and half of HBM's with 8).  A slot's barrier counts the copies as they land, and the
-// products' thread sets a proxy fence between that and its first product.  The softmax warps load the queries.
+// products' thread sets a proxy fence between that and its first product.  A unit's queries come first, as soon as the unit before
+// it has had its last product with its own.
 #pragma once
 #include "cache_common.cuh"
 #include "decode.cuh"
 
 namespace cache {
+
+constexpr int kPfEnd = 2;          // places behind a unit's steps
+
+// x / n = x * mul >> shift for 0 <= x < 2^30 (as in Pages)
+struct Divisor {
+    uint32_t mul, shift;
+    __device__ __forceinline__ int of(int x) const { return (int)(((unsigned long long)(uint32_t)x * mul) >> shift); }
+};
 
 struct PrefixParams {
     const __nv_bfloat16* q;        // [B][H][d]
@@ -37,24 +47,26 @@ struct PrefixParams {
     const char* v;
     Pages pages;                   // table: the first sequence's row
     int H, Hkv, group, rows;       // rows = B * group
-    uint32_t group_mul, group_shift;       // row / group = row * group_mul >> group_shift (as in Pages)
+    Divisor by_group;
     int prefix_len;
     int row_blocks;                // blocks of 256 rows (kSingle: 128)
-    int steps;                     // of a unit: tiles of 128 keys (kSingle: pairs of them)
+    int steps;                     // of a unit: tiles of 128 keys (kSingle: pairs of them); it has steps + kPfEnd places
     int per, more, ctas;           // places of a CTA on the line: `per`, the first `more` CTAs one more
+    Divisor by_places, by_per, by_more;    // by a unit's places, per, per + 1
     int slots;                     // parts that a CTA may leave
     float scale_log2;              // log2(e) / sqrt(d)
     float* part_o;                 // [ctas][slots][2][128][d]
     float2* part_ml;               // [ctas][slots][2][128]: (m in logits, l); l = -1: a bad page
     unsigned long long wait_limit_ns;
-    // the line has fewer than 2^31 places (the host checks)
+    // the line has fewer than 2^30 places (the host checks)
     __device__ __forceinline__ int start(int c) const { return per * c + min(c, more); }
     __device__ __forceinline__ int cta_of(int u) const {
-        return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
+        const int v = u - more * (per + 1);
+        return v < 0 ? by_more.of(u) : more + by_per.of(v);
     }
 };
 
-constexpr int kPfThreads = 384;    // warpgroups 0, 1: queries, softmax; warps 8, 10 and 11 load, warp 9 issues the products
+constexpr int kPfThreads = 384;    // warpgroups 0, 1: softmax; warps 8, 10 and 11 load, warp 9 issues the products
 constexpr int kPfTile = 128;
 constexpr int kPfBox = kPfTile * 64 * 2;       // 64 columns of a tile: rows of 128 bytes
 constexpr uint32_t kPfRegsSoftmax = 208, kPfRegsOther = 88;       // 256 * 208 + 128 * 88 = 384 * 168
@@ -64,13 +76,12 @@ template <int D, bool kSingle>
 struct PfGeo {
     static constexpr int kTileBytes = kPfTile * D * 2;
     static constexpr int kQTiles = kSingle ? 1 : 2;
-    static constexpr int kStages = 7 * 128 / D - kQTiles;          // all the shared memory that Q leaves
+    static constexpr int kStages = 6 * 128 / D - kQTiles;          // all the shared memory that Q and the parts' room leave
     static constexpr int kRing = kQTiles * kTileBytes;
-    static constexpr int kRoom = kQTiles * kTileBytes / 8;         // of Q, a softmax warp's, on a part's way out
-    static constexpr int kCols = kRoom / 128 < 32 ? kRoom / 128 : 32;      // columns of its 32 rows at a time: 16 or 32
-    static constexpr int kBars = kRing + kStages * kTileBytes;
+    static constexpr int kRoom = kRing + kStages * kTileBytes;     // 4 KB a softmax warp, on a part's way out
+    static constexpr int kBars = kRoom + 8 * 4096;
     // barriers
-    static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 1, kSFull = kQFree + 1,
+    static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 1, kSFull = kQEmpty + 1,
                          kPFull = kSFull + 2, kOFull = kPFull + 2, kDrain = kOFull + 2, kNumBars = kDrain + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;             // TMEM address, abort flag, bad page
     static constexpr int kSmem = kMisc + 16 + 1024;                // from a 1024-byte boundary
@@ -118,19 +129,24 @@ __device__ __forceinline__ uint32_t pf_chunk(int r, int c) {
 
 // A CTA's share of a unit: steps j0 .. j1 - 1.  Units of one K/V head are neighbours, row block by row block.
 struct PfShare {
-    int unit, j0, j1, rb, kv;
+    int j0, j1, rb, kv;
 };
 struct PfWalk {                    // over the shares of a range u .. end - 1 of the line
     int u, end;
     __device__ __forceinline__ PfWalk(const PrefixParams& p) : u(p.start(blockIdx.x)), end(p.start(blockIdx.x + 1)) {}
     __device__ __forceinline__ bool next(const PrefixParams& p, PfShare& w) {
+        const int places = p.steps + kPfEnd;
+        int unit = p.by_places.of(u);
+        w.j0 = u - unit * places;
+        if (w.j0 >= p.steps) {         // (in the places behind a unit)
+            w.j0 = 0;
+            u = ++unit * places;
+        }
         if (u >= end) return false;
-        w.unit = u / p.steps;
-        w.j0 = u - w.unit * p.steps;
         w.j1 = min(p.steps, w.j0 + end - u);
-        w.kv = w.unit / p.row_blocks;
-        w.rb = w.unit - w.kv * p.row_blocks;
-        u += w.j1 - w.j0;
+        w.kv = unit / p.row_blocks;
+        w.rb = unit - w.kv * p.row_blocks;
+        u = w.j1 == p.steps ? (unit + 1) * places : end;
         return true;
     }
 };
@@ -151,8 +167,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
             ptx::mbar_init(bar(G::kFull + s), 96);
             ptx::mbar_init(bar(G::kEmpty + s), 1);
         }
-        ptx::mbar_init(bar(G::kQFull), 256);
-        ptx::mbar_init(bar(G::kQFree), 256);
+        ptx::mbar_init(bar(G::kQFull), 96);
+        ptx::mbar_init(bar(G::kQEmpty), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(G::kSFull + i), 1);
             ptx::mbar_init(bar(G::kPFull + i), kPfTile);
@@ -260,7 +276,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                 ++pos;
             };
 #pragma unroll 1
-            while (ok && walk.next(p, w)) {
+            for (uint32_t n = 0; ok && walk.next(p, w); ++n) {
+                {
+                    constexpr int kRowsQ = G::kQTiles * kPfTile;
+                    if (n > 0) {
+                        ok = pf_wait(bar(G::kQEmpty), (n - 1) & 1u, abort_flag, lim);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                    }
+                    const __nv_bfloat16* from = p.q + (long long)w.kv * p.group * D + lane % kChunks * 8;
+#pragma unroll 4
+                    for (int i = who; i < kRowsQ / kRowsPerCopy; i += 3) {
+                        const int r = i * kRowsPerCopy + lane / kChunks, x = w.rb * kRowsQ + r, b = p.by_group.of(x);
+                        const bool there = x < p.rows;
+                        cp_async16(sbase + (uint32_t)((r / kPfTile) * G::kTileBytes) + pf_chunk(r % kPfTile, lane % kChunks),
+                                   from + (there ? ((long long)b * p.H + x - b * p.group) * D : 0), there ? 16u : 0u, policy);
+                    }
+                    pf_arrive_landed(bar(G::kQFull));
+                }
                 if constexpr (!kSingle) {
                     Rows next = lookup(w.j0);
 #pragma unroll 1
@@ -324,7 +357,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
 #pragma unroll 1
             for (uint32_t n = 0; ok && walk.next(p, w); ++n) {
                 const int steps = w.j1 - w.j0;
-                ok = pf_wait(bar(G::kQFull), n & 1u, abort_flag, lim);
+                ok = pf_wait(bar(G::kQFull), n & 1u, abort_flag, lim);     // (its proxy fence: the next slot's)
                 {
                     const uint32_t s0 = landed(pos);
                     if (!ok) break;
@@ -336,6 +369,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                     issue_s(1, s1);
                     ptx::mma_commit(bar(G::kSFull + 1));
                     release(pos++);
+                    if (steps == 1) ptx::mma_commit(bar(G::kQEmpty));
                 }
 #pragma unroll 1
                 for (int jj = 0; jj < steps && ok; ++jj) {
@@ -358,6 +392,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                             issue_s(t, ks);
                             ptx::mma_commit(bar(G::kSFull + t));
                             if (kSingle || t == 1) release(kt);
+                            if (t == 1 && jj + 2 == steps) ptx::mma_commit(bar(G::kQEmpty));
                         }
                     }
                     pos += (kSingle ? 2 : 1) * (more ? 2 : 1);
@@ -377,33 +412,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_off + 128u * t, tO = tmem + lane_off + 256u + (uint32_t)(D * t);
         const float c = p.scale_log2, tau = 8.0f;                  // a reference may lag by 2^8
-        // queries of a share, 16 bytes of a row at a time
-        constexpr int kChunks = D / 8, kRowsQ = G::kQTiles * kPfTile, kQ = kRowsQ * kChunks / 256;
-        auto put_queries = [&](const PfShare& s) {
-            uint4 q[kQ];
-            const int c8 = threadIdx.x % kChunks;
-            const __nv_bfloat16* from = p.q + (long long)s.kv * p.group * D + c8 * 8;
-#pragma unroll
-            for (int i = 0; i < kQ; ++i) {
-                const int at = s.rb * kRowsQ + (i * 256 + threadIdx.x) / kChunks;
-                const int b = (int)(((unsigned long long)(uint32_t)at * p.group_mul) >> p.group_shift);
-                q[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (at < p.rows) q[i] = *reinterpret_cast<const uint4*>(from + ((long long)b * p.H + at - b * p.group) * D);
-            }
-#pragma unroll
-            for (int i = 0; i < kQ; ++i) {
-                const int r = (i * 256 + threadIdx.x) / kChunks;
-                ptx::st_shared_v4(sbase + (uint32_t)((r / kPfTile) * G::kTileBytes) + pf_chunk(r % kPfTile, c8), q[i].x, q[i].y,
-                                  q[i].z, q[i].w);
-            }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(bar(G::kQFull));
-        };
         uint32_t count = 0;                                        // steps before this share
-        bool ok = true, have = walk.next(p, w);
-        put_queries(w);
+        bool ok = true;
 #pragma unroll 1
-        for (uint32_t n = 0; have; ++n) {
+        for (uint32_t n = 0; ok && walk.next(p, w); ++n) {
         const int at = w.rb * (kSingle ? kPfTile : 2 * kPfTile) + (kSingle ? row : t * kPfTile + row);
         // warps without a row keep every wait and arrival, and skip the rest: a row is its own lane of TMEM
         const bool live = at - lane < p.rows;
@@ -507,44 +519,32 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
             }
         }
         if (!ok) break;
-        have = walk.next(p, w);
         ok = pf_wait(bar(G::kOFull + t), n & 1u, abort_flag, lim);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         ptx::tc_fence_after();
-        // The warp's 32 rows, some columns at a time, through its share of Q (its products ended before the last ones of
-        // values): each store then takes whole 128-byte lines (64-byte pieces where the room is less).
-        if (live) {
-            constexpr int kCols = G::kCols, kPieces = kCols / 4, kSide = 32 / kPieces;       // 16-byte pieces of a row, rows at a time
-            const long long part0 = (((long long)blockIdx.x * p.slots + n) * 2 + t) * kPfTile + quarter * 32;
-            const uint32_t room = sbase + (uint32_t)(warp * G::kRoom);
-            const int rows = min(32, p.rows - (at - lane));
+        if (!live) continue;
+        // the warp's 32 rows, 32 columns at a time, through its room: each store then takes four whole 128-byte lines
+        // (a thread's own row in 16-byte pieces took 4 us more)
+        const long long part0 = (((long long)blockIdx.x * p.slots + n) * 2 + t) * kPfTile + quarter * 32;
+        const uint32_t room = sbase + (uint32_t)(G::kRoom + warp * 4096);
+        const int rows = min(32, p.rows - (at - lane));
 #pragma unroll 1
-            for (int ch = 0; ch < D / kCols; ++ch) {
-                uint32_t o[kCols];
-                if constexpr (kCols == 32) ptx::tmem_ld32(tO + ch * 32, o);
-                else ptx::tmem_ld16(tO + ch * 16, o);
+        for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + ch * 32, o);
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-                    ptx::st_shared_v4(room + lane * (kCols * 4) + ((i ^ (lane & (kPieces - 1))) << 4), o[4 * i], o[4 * i + 1],
-                                      o[4 * i + 2], o[4 * i + 3]);
-                __syncwarp();
+            for (int i = 0; i < 8; ++i)
+                ptx::st_shared_v4(room + lane * 128 + ((i ^ (lane & 7)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int r = i * kSide + lane / kPieces, x = lane % kPieces;
-                    const float4 y = *reinterpret_cast<const float4*>(smem + warp * G::kRoom + r * (kCols * 4) +
-                                                                      ((x ^ (r & (kPieces - 1))) << 4));
-                    if (r < rows) *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + ch * kCols + x * 4) = y;
-                }
-                __syncwarp();
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3), x = lane & 7;
+                const float4 y = *reinterpret_cast<const float4*>(smem + G::kRoom + warp * 4096 + r * 128 + ((x ^ (r & 7)) << 4));
+                if (r < rows) *reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + ch * 32 + x * 4) = y;
             }
-            if (lane < rows) p.part_ml[part0 + lane] = make_float2(m, *bad_flag ? kBadPart : l);
+            __syncwarp();
         }
-        if (have) {
-            ptx::mbar_arrive(bar(G::kQFree));                      // every softmax warp's part has to be out of Q
-            ok = pf_wait(bar(G::kQFree), n & 1u, abort_flag, lim);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            put_queries(w);
-        }
+        if (lane < rows) p.part_ml[part0 + lane] = make_float2(m, *bad_flag ? kBadPart : l);
         }
     }
     ptx::tc_fence_before();
@@ -561,113 +561,102 @@ struct PrefixJoin {
     int single, warps;             // one tile of rows a unit; warps a row
 };
 
-// The join: a row's parts of the prefix and of its own keys.  `warps` warps take a row, a contiguous share of its parts
-// each, and are joined through shared memory.
+// The join: a row's parts of the prefix and of its own keys.  `warps` warps take a row, each a share of the prefix's parts and
+// the first of them its own keys', and are joined through shared memory.  The prefix's parts lie where arithmetic says, so
+// they are on their way while the row's length and span are read.
 constexpr int kPfJoinWarps = 8;
-template <int D>
-__global__ void __launch_bounds__(32 * kPfJoinWarps) attn_prefix_join_kernel(const __grid_constant__ PrefixJoin p) {
+// kU: parts in flight; 4 where a row has no more, for more rows on an SM (20,480 rows of 1 or 2 parts: 25 us with 8, 15 with 4;
+// 2,048 rows of 20: 8 and 12).
+template <int D, int kU>
+__global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 4) attn_prefix_join_kernel(const __grid_constant__ PrefixJoin p) {
     constexpr int kC = D / 32;
-    __shared__ float o_s[kPfJoinWarps][D];
+    struct __align__(4 * kC) V { float x[kC]; };       // a lane's neighbouring elements
+    __shared__ V o_s[kPfJoinWarps][32];
     __shared__ float2 ml_s[kPfJoinWarps];
     __shared__ int bad_s[kPfJoinWarps];
     pdl_wait();
     pdl_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = p.warps, share = warp % W;
-    const long long out = (long long)blockIdx.x * (kPfJoinWarps / W) + warp / W;       // (b, h)
-    const bool there = out < (long long)p.s.B * p.s.H;
-    const int b = there ? (int)(out / p.s.H) : 0, h = there ? (int)(out - (long long)b * p.s.H) : 0;
-    const int kv = h / p.s.group, g = h - kv * p.s.group, r = b * p.s.group + g;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = p.warps, share = warp & (W - 1);
+    // (W is a power of two; heads in y)
+    const int b = blockIdx.x, h = blockIdx.y * (kPfJoinWarps / W) + warp / W;
+    const bool there = h < p.s.H;
+    const long long out = (long long)b * p.s.H + h;
+    const int kv = there ? p.x.by_group.of(h) : 0, g = there ? h - kv * p.s.group : 0, r = b * p.s.group + g;
+    const int heads = p.s.block_heads, blk = g / heads, hh = g - blk * heads;      // (8, 16 or 32 heads)
     const int len = __ldg(p.s.seqlens_k + b);
-    const bool good = there && len >= p.x.prefix_len && (long long)len <= (long long)p.s.pages.max_pages * p.s.pages.page_size;
-    if (there && !good && h == 0 && share == 0 && lane == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
-    // parts: the prefix's (of each CTA that has steps of the row's unit), then those of the own keys
-    const int block_rows = p.single ? kPfTile : 2 * kPfTile, rb = r / block_rows, in = r - rb * block_rows;
-    const int unit = kv * p.x.row_blocks + rb, first = p.x.cta_of(unit * p.x.steps);
-    const int shared_parts = (p.x.cta_of(unit * p.x.steps + p.x.steps - 1) - first + 1) * (p.single ? 2 : 1);
-    int c0 = -1, own = 0;                              // first warp (-1: the row is whole) and number of the own parts
-    const int heads = p.s.block_heads, blk = g / heads, hh = g - blk * heads;
-    if (good && len > p.x.prefix_len) {
-        const int2 span = p.s.span[((long long)b * p.s.Hkv + kv) * p.s.head_blocks + blk];
-        c0 = span.x;
-        own = c0 < 0 ? 1 : span.y - c0 + 1;
-    }
-    const int parts = good ? shared_parts + own : 0;
-    auto where = [&](int i, const float2*& ml, const float*& o) {
-        if (i < shared_parts) {
-            const int c = first + (p.single ? i >> 1 : i), t = p.single ? i & 1 : in / kPfTile;
-            const long long slot = (long long)c * p.x.slots + (unit - p.x.start(c) / p.x.steps);
-            const long long part = (slot * 2 + t) * kPfTile + in % kPfTile;
-            ml = p.x.part_ml + part;
-            o = p.x.part_o + part * D;
-        } else if (c0 < 0) {
-            ml = p.s.own_ml + out;
-            o = p.s.own_o + out * D;
-        } else {
-            const int c = c0 + i - shared_parts;       // a row's first part is in slot 1 of its warp, the others in slot 0
-            const long long part = (2ll * c + (c == c0)) * heads + hh;
-            ml = p.s.part_ml + part;
-            o = p.s.part_o + part * D;
-        }
+    const int2 span = p.s.span[((long long)b * p.s.Hkv + kv) * p.s.head_blocks + blk];     // (of a row with own keys)
+    // the prefix's parts: of each CTA that has steps of the row's unit, its first share but in the first of them
+    const int in_shift = p.single ? 7 : 8, rb = r >> in_shift, in = r - (rb << in_shift), places = p.x.steps + kPfEnd;
+    const int place0 = (kv * p.x.row_blocks + rb) * places, first = p.x.cta_of(place0);
+    const int parts = (p.x.cta_of(place0 + p.x.steps - 1) - first + 1) << p.single;
+    const int before = p.x.by_places.of(p.x.start(first));     // the unit in which that CTA's range begins
+    const int skip = kv * p.x.row_blocks + rb - before - (p.x.start(first) - before * places >= p.x.steps);
+    const long long first_part = (((long long)first * p.x.slots + skip) * 2) * kPfTile + (p.single ? in : (in >> 7) * kPfTile + (in & 127));
+    const long long rest_part = first_part - (long long)skip * (2 * kPfTile);      // (as if every CTA had it as its first)
+    const int step_part = p.x.slots * (2 * kPfTile);
+    auto prefix_part = [&](int i) {
+        const int c = i >> p.single;
+        return (c == 0 ? first_part : rest_part + (long long)c * step_part) + (p.single ? (i & 1) * kPfTile : 0);
     };
-    const int i0 = parts * share / W, i1 = parts * (share + 1) / W;
     float mx = -INFINITY, sum = 0.0f, acc[kC];
     bool bad = false;
 #pragma unroll
     for (int x = 0; x < kC; ++x) acc[x] = 0.0f;
-    // 32 parts at a time: a lane has one's m and l, then the warp adds up their rows, eight in flight
-#pragma unroll 1
-    for (int base = i0; base < i1; base += 32) {
-        const int n = min(32, i1 - base);
-        const float2* mlp = nullptr;
-        const float* op = nullptr;
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < n) {
-            where(base + lane, mlp, op);
-            ml = *mlp;
-        }
+    // (every lane has a part's m and l, and its own elements: nothing to hand over)
+    auto merge = [&](float2 ml, const V& v) {
         bad |= ml.y == kBadPart;
-        float top = ml.x;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-        top = fmaxf(top, mx);
-        const float down = rescale(mx, top, p.s.scale_log2);
+        const float top = fmaxf(mx, ml.x), down = rescale(mx, top, p.s.scale_log2), f = rescale(ml.x, top, p.s.scale_log2);
         mx = top;
-        sum *= down;
+        sum = sum * down + ml.y * f;
 #pragma unroll
-        for (int x = 0; x < kC; ++x) acc[x] *= down;
-        const float f = rescale(ml.x, top, p.s.scale_log2);
-        float add = ml.y * f;
+        for (int x = 0; x < kC; ++x) acc[x] = acc[x] * down + v.x[x] * f;
+    };
+    const int i0 = parts * share / W, i1 = parts * (share + 1) / W;
+    V v[kU], own_v;
+    float2 ml[kU], own_m;
+    auto fetch = [&](int i) {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, off);
-        sum += add;
-        constexpr int kU = 8;
+        for (int j = 0; j < kU; ++j)
+            if (i + j < i1) {
+                const long long part = prefix_part(i + j);
+                ml[j] = p.x.part_ml[part];
+                v[j] = reinterpret_cast<const V*>(p.x.part_o + part * D)[lane];
+            }
+    };
+    fetch(i0);
+    const bool good = there && len >= p.x.prefix_len && (long long)len <= (long long)p.s.pages.max_pages * p.s.pages.page_size;
+    if (there && !good && h == 0 && share == 0 && lane == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
+    // the own keys' parts: one of a whole row, or one of each warp of the span (its first in slot 1 of its warp, the others in 0)
+    const bool whole = span.x < 0;
+    const int own = good && share == 0 && len > p.x.prefix_len ? (whole ? 1 : span.y - span.x + 1) : 0;
+    auto own_fetch = [&](int i) {
+        const long long part = (2ll * (span.x + i) + (i == 0)) * heads + hh;
+        own_m = whole ? p.s.own_ml[out] : p.s.part_ml[part];
+        own_v = reinterpret_cast<const V*>(whole ? p.s.own_o + out * D : p.s.part_o + part * D)[lane];
+    };
+    if (own > 0) own_fetch(0);
 #pragma unroll 1
-        for (int j0 = 0; j0 < n; j0 += kU) {
-            float v[kU][kC];
+    for (int i = i0; i < i1; i += kU) {
+        if (i > i0) fetch(i);
 #pragma unroll
-            for (int j = 0; j < kU; ++j) {
-                const float* from = reinterpret_cast<const float*>(
-                    __shfl_sync(0xFFFFFFFFu, (unsigned long long)reinterpret_cast<uintptr_t>(op), (j0 + j) & 31));
-#pragma unroll
-                for (int x = 0; x < kC; ++x) v[j][x] = j0 + j < n ? from[x * 32 + lane] : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < kU; ++j) {
-                const float fj = __shfl_sync(0xFFFFFFFFu, f, (j0 + j) & 31);
-#pragma unroll
-                for (int x = 0; x < kC; ++x)
-                    if (j0 + j < n) acc[x] += v[j][x] * fj;
-            }
-        }
+        for (int j = 0; j < kU; ++j)
+            if (i + j < i1) merge(ml[j], v[j]);
     }
-    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (own > 0) merge(own_m, own_v);
+#pragma unroll 2
+    for (int i = 1; i < own; ++i) {
+        own_fetch(i);
+        merge(own_m, own_v);
+    }
     if (W > 1) {
         if (lane == 0) {
             ml_s[warp] = make_float2(mx, sum);
             bad_s[warp] = bad;
         }
+        V mine;
 #pragma unroll
-        for (int x = 0; x < kC; ++x) o_s[warp][x * 32 + lane] = acc[x];
+        for (int x = 0; x < kC; ++x) mine.x[x] = acc[x];
+        o_s[warp][lane] = mine;
         __syncthreads();
         if (share != 0) return;
         float top = mx;
@@ -680,16 +669,18 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps) attn_prefix_join_kernel(con
             const float f = rescale(ml_s[warp + w].x, top, p.s.scale_log2);
             sum += ml_s[warp + w].y * f;
             bad |= bad_s[warp + w] != 0;
+            const V other = o_s[warp + w][lane];
 #pragma unroll
-            for (int x = 0; x < kC; ++x) acc[x] += o_s[warp + w][x * 32 + lane] * f;
+            for (int x = 0; x < kC; ++x) acc[x] += other.x[x] * f;
         }
         mx = top;
     }
     if (!good || bad) return;
     const float inv = sum > 0.0f ? 1.0f / sum : NAN;   // no weight at all, or a NaN one: the row is NaN
+    uint32_t* to = reinterpret_cast<uint32_t*>(p.s.o + out * D) + lane * (kC / 2);
 #pragma unroll
-    for (int x = 0; x < kC; ++x)
-        p.s.o[out * D + x * 32 + lane] = __ushort_as_bfloat16((unsigned short)round_bf16(acc[x] * inv, p.s.round_mode));
+    for (int x = 0; x < kC; x += 2)
+        to[x / 2] = round_bf16(acc[x] * inv, p.s.round_mode) | round_bf16(acc[x + 1] * inv, p.s.round_mode) << 16;
     if (p.s.lse && lane == 0) p.s.lse[out] = sum == 0.0f ? -INFINITY : mx * p.s.scale + logf(sum);
 }
 

@@ -1,6 +1,6 @@
 """Executable model of attn_prefix_kernel's synchronisation (csrc/prefix.cuh; host only, no GPU): three warps that copy keys and
-values, whose barriers count them as they land, the thread that issues the products and two softmax warpgroups that also bring the queries
-and take their parts out through the queries' room, which meet only through mbarriers, under random schedules and shares of a range.  Checked: no deadlock, no wait two phases behind, every product
+values and the queries, whose barriers count them as they land, the thread that issues the products and two softmax warpgroups,
+which meet only through mbarriers, under random schedules and shares of a range.  Checked: no deadlock, no wait two phases behind, every product
 reads the tiles (and the queries and the P) of its own step, and nothing is overwritten before its products have read it.  Planted mistakes are caught.  A change to the kernel's barriers or to the order of
 its loads must be made here too.
 """
@@ -18,10 +18,10 @@ class Prefix:
         self.shares, self.single, self.stages, self.rng, self.mistake = shares, single, stages, rng, mistake
         self.full = [Barrier("full%d" % i, 3) for i in range(stages)]
         self.empty = [Barrier("empty%d" % i, 1) for i in range(stages)]
-        self.q, self.q_free = Barrier("q", 2), Barrier("q_free", 2)
+        self.q, self.q_empty = Barrier("q", 3), Barrier("q_empty", 1)
         self.s, self.p, self.o = ([Barrier("%s%d" % (n, i), 1) for i in range(2)] for n in "spo")
         self.slot = [[None] * 3 for _ in range(stages)]        # what each warp has put into a slot
-        self.queries = [None, None]                             # whose queries each warpgroup has brought
+        self.queries = [None] * 3                               # whose queries each warp has brought
         self.buf = [None, None]                                 # ("S" or "P", share, step) in TMEM
         self.acc = [(None, []), (None, [])]                     # share and steps accumulated in O
         self.pending, self.now, self.seq, self.mma_free = [], 0, 0, 0
@@ -57,7 +57,19 @@ class Prefix:
                         yield ("V", n, g, r)
 
     def loader(self, who):
+        share = -1
         for pos, what in enumerate(self.loads()):
+            if what[1] != share:
+                share = what[1]
+                if share and self.mistake != "no query wait":
+                    yield from self.wait(self.q_empty, share - 1)
+                self.queries[who] = None
+
+                def bring(share=share):
+                    self.queries[who] = share
+                    self.q.arrive()
+                self.later(bring)
+                yield
             slot = pos % self.stages
             if pos >= self.stages and self.mistake != "no empty wait":
                 yield from self.wait(self.empty[slot], pos // self.stages - 1)
@@ -84,7 +96,7 @@ class Prefix:
 
             def run():
                 read(at % self.stages, what)
-                if self.queries != [n, n]:
+                if self.queries != [n] * 3:
                     raise Violation("S of share %d read queries of %s" % (n, self.queries))
                 if step and self.acc[t] != (n, list(range(step))):
                     raise Violation("S over a P that was not used")
@@ -120,6 +132,8 @@ class Prefix:
             issue_s(1, pos, n, 0)
             release(pos)
             pos += 1
+            if steps == 1:
+                self.later(self.q_empty.arrive, True)
             for jj in range(steps):
                 more = jj + 1 < steps
                 v = [pos, pos + (2 if more else 1) if single else pos]
@@ -140,13 +154,13 @@ class Prefix:
                         issue_s(t, k[t], n, jj + 1)
                         if single or t == 1:
                             release(k[t])
+                        if t == 1 and jj + 2 == steps:
+                            self.later(self.q_empty.arrive, True)
                 pos += (2 if single else 1) * (2 if more else 1)
             count += steps
 
     def softmax(self, t):
         count = 0
-        self.queries[t] = 0
-        self.q.arrive()
         for n, steps in enumerate(self.shares):
             for jj in range(steps):
                 yield from self.wait(self.s[t], count)
@@ -158,17 +172,6 @@ class Prefix:
                 count += 1
             if self.mistake != "no O wait":
                 yield from self.wait(self.o[t], n)
-            self.queries[t] = "part"
-            yield
-            if n + 1 < len(self.shares):
-                self.q_free.arrive()
-                if self.mistake != "no free wait":
-                    yield from self.wait(self.q_free, n)
-                if self.queries[1 - t] == "part" and self.mistake == "no free wait":
-                    raise Violation("queries over a part")
-                self.queries[t] = n + 1
-                self.q.arrive()
-                yield
             if self.acc[t] != (n, list(range(steps))):
                 raise Violation("O read early")
             yield
@@ -176,7 +179,7 @@ class Prefix:
 
     def state(self):
         return self.seq, sum(b.done * 3 + b.pending for b in
-                             self.full + self.empty + self.s + self.p + self.o + [self.q, self.q_free])
+                             self.full + self.empty + self.s + self.p + self.o + [self.q, self.q_empty])
 
     def run(self):
         roles = [self.loader(0), self.loader(1), self.loader(2), self.mma(), self.softmax(0), self.softmax(1)]
@@ -198,7 +201,7 @@ class Prefix:
                 raise Deadlock()
 
 
-GEOMETRIES = [(False, 5), (True, 6), (False, 12), (True, 13)]     # single, stages: d = 128, then 64
+GEOMETRIES = [(False, 4), (True, 5), (False, 10), (True, 11)]     # single, stages: d = 128, then 64
 
 
 @pytest.mark.parametrize("single,stages", GEOMETRIES)
@@ -209,12 +212,12 @@ def test_runs_to_the_end(single, stages):
             Prefix(shares, single, stages, rng).run()
 
 
-@pytest.mark.parametrize("mistake", ["no empty wait", "signalled at once", "no P wait", "early release", "no O wait", "no free wait"])
+@pytest.mark.parametrize("mistake", ["no empty wait", "signalled at once", "no P wait", "early release", "no O wait", "no query wait"])
 def test_mistakes_are_caught(mistake):
     rng, caught = random.Random(1), 0
     for _ in range(20):
         try:
-            Prefix([20, 3, 10], False, 5, rng, mistake).run()
+            Prefix([20, 3, 10], False, 4, rng, mistake).run()
         except (Violation, Deadlock):
             caught += 1
     assert caught

@@ -888,11 +888,11 @@ void fill_norm_rope(NormRopeParams& p, const attn_norm_rope_args_t& a) {
 template <bool kAppend>
 int launch_norm_rope(NormRopeParams& p, int64_t d, bool halves, int sms, cudaStream_t stream) {
     // heads of a block as in launch_rope
-    const int64_t lanes = p.tokens * 32, full = (int64_t)sms * 2048, piece = kRopeHeads * (32 / (d / 16));
+    const int64_t lanes = p.tokens * 32, full = (int64_t)sms * 2048, piece = 32 / (d / 16);
     int64_t splits = lanes < full ? cdiv(full, lanes) : 1;
     if (splits > cdiv(p.heads, piece)) splits = cdiv(p.heads, piece);
     p.heads_per_block = (int)(cdiv(cdiv(p.heads, splits), piece) * piece);
-    const int64_t most = cdiv(p.tokens, kNormWarps), grid = most < 20 * sms ? most : 20 * sms;
+    const int64_t most = cdiv(p.tokens, kNormWarps), grid = most < kNormBlocks * sms ? most : kNormBlocks * sms;
     const int gy = (int)cdiv(p.heads, p.heads_per_block);
     if (gy > 65535) return ATTN_ERR_UNSUPPORTED;
     auto* kernel = d == 128 ? (halves ? attn_norm_rope_kernel<128, true, kAppend> : attn_norm_rope_kernel<128, false, kAppend>)
@@ -917,22 +917,13 @@ int run_norm_rope(const attn_norm_rope_args_t& a, cudaStream_t stream) {
     return launch_norm_rope<false>(p, a.d, a.pairs && a.pairing == ATTN_ROPE_HALVES, sms, stream);
 }
 
-// Blocks of the gradient's kernel: as many as fit at once, q's and k's in proportion to their heads (each block leaves
-// d sums to be added up).
-constexpr int kNormBwdBlocks = 4;      // an SM
-void norm_bwd_blocks(const attn_norm_rope_args_t& a, int sms, int (&blocks)[2]) {
-    const int64_t Hkv = a.k ? a.Hkv : 0, most = cdiv(a.B * a.S, kNormWarps), all = (int64_t)kNormBwdBlocks * sms;
-    int64_t k = a.k ? (all * Hkv + (a.H + Hkv) / 2) / (a.H + Hkv) : 0;
-    if (a.k && k < 1) k = 1;
-    if (k > all - 1) k = all - 1;
-    const int64_t q = all - k;
-    blocks[0] = (int)(most < 1 ? 1 : q < most ? q : most);
-    blocks[1] = (int)(a.k ? (most < 1 ? 1 : k < most ? k : most) : 0);
+// blocks of the gradient's kernel: as many as fit at once (each leaves 2 * d sums to be added up)
+int norm_bwd_blocks(const attn_norm_rope_args_t& a, int sms) {
+    const int64_t most = cdiv(a.B * a.S, kNormWarps), all = (int64_t)kNormBwdBlocks * sms;
+    return (int)(most < 1 ? 1 : all < most ? all : most);
 }
 size_t norm_bwd_bytes(const attn_norm_rope_args_t& a, int sms) {
-    int blocks[2];
-    norm_bwd_blocks(a, sms, blocks);
-    return (size_t)(blocks[0] + blocks[1]) * (size_t)a.d * 4;
+    return 2 * (size_t)norm_bwd_blocks(a, sms) * (size_t)a.d * 4;
 }
 
 int run_norm_rope_bwd(const attn_norm_rope_bwd_args_t& g, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -984,11 +975,11 @@ int run_norm_rope_bwd(const attn_norm_rope_bwd_args_t& g, void* workspace, size_
     p.part = reinterpret_cast<float*>(workspace);
     p.dw[0] = g.dq_weight;
     p.dw[1] = g.dk_weight;
-    norm_bwd_blocks(a, sms, p.blocks);
+    p.blocks = norm_bwd_blocks(a, sms);
     const bool halves = a.pairs && a.pairing == ATTN_ROPE_HALVES;
     auto* kernel = a.d == 128 ? (halves ? attn_norm_rope_bwd_kernel<128, true> : attn_norm_rope_bwd_kernel<128, false>)
                               : (halves ? attn_norm_rope_bwd_kernel<64, true> : attn_norm_rope_bwd_kernel<64, false>);
-    if ((st = launch(kernel, p.blocks[0] + p.blocks[1], 1, kNormThreads, 0, stream, p)) != ATTN_OK) return st;
+    if ((st = launch(kernel, p.blocks, 1, kNormThreads, 0, stream, p)) != ATTN_OK) return st;
     if (!p.dw[0] && !p.dw[1]) return ATTN_OK;
     const int64_t grid = (a.k ? 2 : 1) * (a.d / 32);
     return a.d == 128 ? launch(attn_norm_rope_dw_kernel<128>, grid, 1, 32 * kDwRows, 0, stream, p)

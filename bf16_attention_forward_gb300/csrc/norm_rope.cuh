@@ -11,6 +11,8 @@
 // a warp takes a token, whose angles it computes once; D / 16 lanes take a head, 16 elements each, so the sums over a
 // head are 2 or 3 shuffles.  Weights are fp32 in shared memory: 64 bytes of it a thread and head beside 32 from HBM.
 #pragma once
+#include <type_traits>
+
 #include "rope.cuh"
 
 namespace cache {
@@ -31,13 +33,14 @@ struct NormRopeParams {
     const int64_t* slots;          // [tokens] rows of the cache, -1: none
     long long rows;                // of the cache
     // backward
-    float* part;                   // [blocks][D] sums of dw
+    float* part;                   // [2][blocks][D] sums of q's and k's dw
     float* dw[2];                  // [d] or null
-    int blocks[2];                 // of q and of k
+    int blocks;
 };
 
 constexpr int kNormThreads = 128;
 constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kNormBwdBlocks = 4;  // of the gradient's kernel an SM: one wave, since each block leaves sums to be added up
 
 // The rotation's tables in shared memory, by the threads of a block; true (for all) when an axis is not there.
 template <int D>
@@ -55,16 +58,31 @@ struct TurnTable {
         }
         return __syncthreads_or(bad);
     }
-    // cosines and sines of a token's pairs, by the lanes of a warp
-    __device__ __forceinline__ void angles(const NormRopeParams& p, long long b, long long s, float2* cs) const {
+    // A warp's lanes take a token's pairs: the positions (read one token ahead: each waits for memory), then cosines and sines.
+    static constexpr int kPairs = (D / 2 + 31) / 32;       // of a lane
+    struct Positions { int at[kPairs]; };
+    __device__ __forceinline__ Positions positions(const NormRopeParams& p, long long b, long long s) const {
+        Positions pos;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const int pr = (threadIdx.x & 31) + 32 * i;
+            pos.at[i] = 0;
+            if (pr < p.pairs) {
+                const int a = axis[pr];
+                pos.at[i] = __ldg(p.positions + (a < 0 ? ~a : a) * p.pos_axis + b * p.pos_b + s);
+            }
+        }
+        return pos;
+    }
+    __device__ __forceinline__ void angles(const NormRopeParams& p, const Positions& pos, float2* cs) const {
         __syncwarp();                                      // (the token before is done with cs)
-#pragma unroll 1
-        for (int pr = threadIdx.x & 31; pr < p.pairs; pr += 32) {
-            const int a = axis[pr];
-            const long long pos = __ldg(p.positions + (a < 0 ? ~a : a) * p.pos_axis + b * p.pos_b + s);
-            const long long at = (long long)(turn[pr] * (unsigned long long)pos);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const int pr = (threadIdx.x & 31) + 32 * i;
+            if (pr >= p.pairs) break;
+            const long long at = (long long)(turn[pr] * (unsigned long long)(long long)pos.at[i]);
             float sn, c;
-            sincospif(a < 0 ? NAN : (float)at * 0x1p-63f, &sn, &c);
+            sincospif(axis[pr] < 0 ? NAN : (float)at * 0x1p-63f, &sn, &c);
             cs[pr] = make_float2(c, sn);
         }
         __syncwarp();
@@ -104,64 +122,135 @@ struct Place {
         }
         return turns;
     }
-    // the thread's elements (chunk a in x[0..7], chunk b in x[8..15]) turned by the angles, or by their negatives (a pair
-    // that does not turn is left alone: a NaN in one of its elements stays there)
-    template <bool kBack>
-    static __device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&sn)[8], uint32_t turns) {
-        if (turns == 0) return;
+    // Of weights, cosines and sines the factors of a word: y = x * A + (its partners) * B.  Adjacent: a word is a pair and its
+    // partners its own elements, swapped; halves: the word of the other chunk.
+    static __device__ __forceinline__ void factors(const float2 (&w)[8], const float (&c)[8], const float (&sn)[8], float2 (&A)[8],
+                                                   float2 (&B)[8]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = kHalves ? e : 2 * e, j = kHalves ? e + 8 : 2 * e + 1;
-            const float s = kBack ? -sn[e] : sn[e], x0 = x[i], x1 = x[j];
-            if (!kHalves && !(turns >> e & 1u)) continue;      // (halves: all 8 or none)
-            x[i] = x0 * c[e] - x1 * s;
-            x[j] = x1 * c[e] + x0 * s;
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (kHalves) {
+                const int e = 2 * (i & 3);
+                const float2 cc = make_float2(c[e], c[e + 1]), ss = make_float2(sn[e], sn[e + 1]);
+                A[i] = __fmul2_rn(w[i], cc);
+                B[i] = __fmul2_rn(w[i ^ 4], i < 4 ? make_float2(-ss.x, -ss.y) : ss);
+            } else {
+                A[i] = make_float2(w[i].x * c[i], w[i].y * c[i]);
+                B[i] = make_float2(-w[i].y * sn[i], w[i].x * sn[i]);
+            }
+        }
+    }
+    static __device__ __forceinline__ float2 partners(const float2 (&x)[8], int i) {
+        return kHalves ? x[i ^ 4] : make_float2(x[i].y, x[i].x);
+    }
+    // whether word i turns (a pair that does not is left alone: a NaN in one of its elements stays there)
+    static __device__ __forceinline__ bool turned(uint32_t turns, int i) { return kHalves ? turns != 0 : turns >> i & 1u; }
+    // the thread's elements, two by two (chunk a in x[0..3], chunk b in x[4..7]), turned by the angles, or by their negatives (a
+    // pair that does not turn is left alone: a NaN in one of its elements stays there)
+    template <bool kBack>
+    static __device__ __forceinline__ void turn(float2 (&x)[8], const float (&c)[8], const float (&sn)[8], uint32_t turns) {
+        if (turns == 0) return;
+        if constexpr (kHalves) {           // (all 8 or none)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 cc = make_float2(c[2 * e], c[2 * e + 1]), v = make_float2(sn[2 * e], sn[2 * e + 1]);
+                const float2 s = kBack ? make_float2(-v.x, -v.y) : v, m = make_float2(-s.x, -s.y), x0 = x[e], x1 = x[e + 4];
+                x[e] = __ffma2_rn(x0, cc, __fmul2_rn(x1, m));
+                x[e + 4] = __ffma2_rn(x1, cc, __fmul2_rn(x0, s));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!(turns >> e & 1u)) continue;
+                const float s = kBack ? -sn[e] : sn[e];
+                const float2 v = x[e];
+                x[e] = make_float2(v.x * c[e] - v.y * s, v.y * c[e] + v.x * s);
+            }
         }
     }
 };
 
-__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float2 (&x)[8]) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void pack16(const float (&x)[16], uint4& a, uint4& b) {
+__device__ __forceinline__ void pack16(const float2 (&x)[8], uint4& a, uint4& b) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16x2(x[i].x, x[i].y);
     a = make_uint4(w[0], w[1], w[2], w[3]);
     b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 // a head's weights of the thread's two chunks
-__device__ __forceinline__ void weights16(const float* w, int ca, int cb, float (&x)[16]) {
-    *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(w + ca * 8);
-    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(w + ca * 8 + 4);
-    *reinterpret_cast<float4*>(x + 8) = *reinterpret_cast<const float4*>(w + cb * 8);
-    *reinterpret_cast<float4*>(x + 12) = *reinterpret_cast<const float4*>(w + cb * 8 + 4);
+__device__ __forceinline__ void weights16(const float* w, int ca, int cb, float2 (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(w + (i < 2 ? ca : cb) * 8 + (i & 1) * 4);
+        x[2 * i] = make_float2(v.x, v.y);
+        x[2 * i + 1] = make_float2(v.z, v.w);
+    }
 }
 __device__ __forceinline__ float weight_at(const NormRopeParams& p, int t, int i) {
     if (!p.weight[t]) return 1.0f;
     return p.weight_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.weight[t])[i])
                          : reinterpret_cast<const float*>(p.weight[t])[i];
 }
-// the sum over the lanes of a head
+// sum of a thread's products over the lanes of a head
 template <int kL>
-__device__ __forceinline__ float head_sum(float v) {
+__device__ __forceinline__ float head_dot(const float2 (&x)[8], const float2 (&y)[8]) {
+    float2 s = __fmul2_rn(x[0], y[0]), t = __fmul2_rn(x[1], y[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        s = __ffma2_rn(x[i], y[i], s);
+        t = __ffma2_rn(x[i + 1], y[i + 1], t);
+    }
+    s = __fadd2_rn(s, t);
+    float v = s.x + s.y;
 #pragma unroll
     for (int off = 1; off < kL; off <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     return v;
 }
+// 16 bytes global -> shared
+__device__ __forceinline__ void cp_async16_plain(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// A token, and where it is in its batch entry; the next one of a warp lies `tokens` on.  (The host refuses 2^30 of them.)
+struct NormToken {
+    int token, b, s;
+};
+struct NormStride {
+    int tokens, b, s, S;
+    __device__ __forceinline__ explicit NormStride(const NormRopeParams& p)
+        : tokens(gridDim.x * kNormWarps), b((int)(tokens / p.S)), s((int)(tokens - b * p.S)), S((int)p.S) {}
+    __device__ __forceinline__ NormToken first() const {
+        const int t = blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+        return {t, t / S, t % S};
+    }
+    __device__ __forceinline__ void next(NormToken& t) const {
+        t.token += tokens;
+        t.b += b;
+        t.s += s;
+        if (t.s >= S) { t.s -= S; ++t.b; }
+    }
+};
+
+// Each thread copies its own 16-byte chunks into shared memory some heads ahead and reads only those back: nothing but its own
+// wait_group stands between.  At HBM's rate the SMs have 350 instructions for a warp's kSub heads, so the loop is kept
+// short: weights, cosines and sines multiplied once a token, two products an instruction, addresses by addition.
+constexpr int kNormStages = 3;
+constexpr int kNormHeads = 2;      // of a thread at a time
+constexpr int kNormBlocks = 5;     // an SM, one wave: a block's tables and weights take as long as some tokens
 template <int D, bool kHalves, bool kAppend>
-__global__ void __launch_bounds__(kNormThreads, 5) attn_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int kL = D / 16;     // lanes of a head
     constexpr int kSub = 32 / kL;  // heads that a warp takes side by side
+    constexpr int kTensors = kAppend ? 3 : 2;
     __shared__ TurnTable<D> table;
     __shared__ __align__(16) float w_s[2][D];
     __shared__ float2 cs[kNormWarps][D / 2];
+    __shared__ uint4 ring[kNormStages][2 * kNormHeads][kNormThreads];
     pdl_wait();
     pdl_launch();
     for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) w_s[i / D][i % D] = weight_at(p, i / D, i % D);
@@ -169,175 +258,271 @@ __global__ void __launch_bounds__(kNormThreads, 5) attn_norm_rope_kernel(const _
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_AXES);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kL;
     const Place<D, kHalves> place(lane % kL, p.pairs);
-    const int h_first = blockIdx.y * p.heads_per_block, h_begin = h_first + lane / kL;
-    const int h_end = min(h_first + p.heads_per_block, p.heads);
-    // which tensor head h of the token belongs to, and its number there
-    auto tensor_of = [&](int& h) {
-        int t = 0;
-        if (h >= p.x[0].heads) { h -= p.x[0].heads; t = 1; }
-        if (kAppend && t == 1 && h >= p.x[1].heads) { h -= p.x[1].heads; t = 2; }
-        return t;
+    const uint32_t ring_at = ptx::smem_u32(&ring[0][0][threadIdx.x]);
+    // this block's heads of tensor t
+    const int block_h = blockIdx.y * p.heads_per_block;
+    auto first_head = [&](int t) { return max(block_h - (t > 0 ? p.x[0].heads : 0) - (t > 1 ? p.x[1].heads : 0), 0); };
+    auto last_head = [&](int t) {
+        return min(block_h + p.heads_per_block - (t > 0 ? p.x[0].heads : 0) - (t > 1 ? p.x[1].heads : 0), p.x[t].heads);
+    };
+    // the loads ahead: tensor, heads left of it, where the next ones are
+    const NormStride stride(p);
+    NormToken at = stride.first(), ahead = at;
+    const int tokens = (int)p.tokens;
+    int ta = -1, left = 0;
+    const char* from = nullptr;
+    auto slot_of = [&](int token) {
+        return token < tokens ? __ldg(reinterpret_cast<const long long*>(p.slots) + token) : 0;
+    };
+    // appending: the slots of the token ahead and of the next one (a token without a slot is passed over)
+    long long slot = kAppend ? slot_of(ahead.token) : 0, next_slot = kAppend ? slot_of(ahead.token + stride.tokens) : 0;
+    auto pass = [&]() {
+        stride.next(ahead);
+        slot = next_slot;
+        if (kAppend) next_slot = slot_of(ahead.token + stride.tokens);
+    };
+    auto load = [&](int stage) {
+        while (left <= 0 && ahead.token < tokens) {
+            if (kAppend && slot == -1) {
+                pass();
+                continue;
+            }
+            if (++ta == kTensors) {
+                ta = -1;
+                pass();
+                continue;
+            }
+            const int h = first_head(ta);
+            left = last_head(ta) - h;
+            from = p.x[ta].src + (long long)ahead.b * p.x[ta].src_b + (long long)ahead.s * p.x[ta].src_t + (h + sub) * p.x[ta].src_h;
+        }
+#pragma unroll
+        for (int u = 0; u < kNormHeads; ++u) {
+            if (left > sub) {
+                cp_async16_plain(ring_at + ((stage * kNormHeads + u) * 2) * (kNormThreads * 16), from + place.ca * 16);
+                cp_async16_plain(ring_at + ((stage * kNormHeads + u) * 2 + 1) * (kNormThreads * 16), from + place.cb * 16);
+            }
+            if (left > 0) from += kSub * p.x[ta].src_h;
+            left -= kSub;
+        }
+        cp_async_commit();
     };
 #pragma unroll 1
-    for (long long token = (long long)blockIdx.x * kNormWarps + warp; token < p.tokens;
-         token += (long long)gridDim.x * kNormWarps) {
-        const long long b = kAppend ? 0 : token / p.S, s = kAppend ? token : token - b * p.S;
-        struct Heads { uint4 a[kRopeHeads], b[kRopeHeads]; };
-        auto load = [&](int h0, Heads& x) {
-#pragma unroll
-            for (int u = 0; u < kRopeHeads; ++u) {
-                int h = h0 + u * kSub;
-                x.a[u] = x.b[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (h >= h_end) continue;
-                const RopeTensor& t = p.x[tensor_of(h)];
-                const char* src = t.src + b * t.src_b + s * t.src_t + h * t.src_h;
-                x.a[u] = *reinterpret_cast<const uint4*>(src + place.ca * 16);
-                x.b[u] = *reinterpret_cast<const uint4*>(src + place.cb * 16);
-            }
-        };
-        Heads x, next;
+    for (int i = 0; i < kNormStages - 1; ++i) load(i);
+    int stage = 0;
+    typename TurnTable<D>::Positions pos, next_pos = at.token < tokens ? table.positions(p, at.b, at.s) : typename TurnTable<D>::Positions();
+#pragma unroll 1
+    for (NormToken then = at; at.token < tokens; at = then) {
+        pos = next_pos;
+        stride.next(then);
+        if (then.token < tokens) next_pos = table.positions(p, then.b, then.s);
         long long row = -1;        // the token's row of the cache
         if constexpr (kAppend) {
-            row = __ldg(reinterpret_cast<const long long*>(p.slots) + token);
-            load(h_begin, x);      // (beside the slot's read: a token without a slot is rare)
+            row = slot_of(at.token);
             if (row == -1) continue;
             if (row < 0 || row >= p.rows) {
                 row = -1;
                 if (lane == 0) report_invalid(ATTN_CACHE_SITE_SLOTS);
             }
-        } else {
-            load(h_begin, x);
         }
-        table.angles(p, b, s, cs[warp]);
-        float c[8], sn[8];
-        const uint32_t turns = place.take(cs[warp], p.pairs, c, sn);
+        table.angles(p, pos, cs[warp]);
 #pragma unroll 1
-        for (int h0 = h_first; h0 < h_end; h0 += kRopeHeads * kSub) {      // (every lane of the warp)
-            load(h0 + lane / kL + kRopeHeads * kSub, next);
-#pragma unroll
-            for (int u = 0; u < kRopeHeads; ++u) {
-                int h = h0 + lane / kL + u * kSub;
-                const bool there = h < h_end;
-                float v[16];
-                unpack16(x.a[u], x.b[u], v);
-                float ss = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) ss += v[e] * v[e];
-                const float r = rsqrtf(head_sum<kL>(ss) * (1.0f / D) + p.eps);
-                if (!there) continue;
-                const int t = tensor_of(h);
-                if (kAppend && t > 0 && row < 0) continue;
-                if (!kAppend || t < 2) {
-                    float w[16];
-                    weights16(w_s[t], place.ca, place.cb, w);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] *= r * w[e];
-                    place.template turn<false>(v, c, sn, turns);
-                    pack16(v, x.a[u], x.b[u]);
-                }
-                const RopeTensor& to = p.x[t];
-                char* dst = to.dst + b * to.dst_b + (kAppend && t > 0 ? row : s) * to.dst_t + h * to.dst_h;
-                *reinterpret_cast<uint4*>(dst + place.ca * 16) = x.a[u];
-                *reinterpret_cast<uint4*>(dst + place.cb * 16) = x.b[u];
+        for (int t = 0; t < kTensors; ++t) {
+            const int h0 = first_head(t), h1 = last_head(t);
+            if (h0 >= h1) continue;
+            const bool out = !(kAppend && t > 0 && row < 0);
+            char* dst = p.x[t].dst + (long long)at.b * p.x[t].dst_b + (kAppend && t > 0 ? row : (long long)at.s) * p.x[t].dst_t + (h0 + sub) * p.x[t].dst_h;
+            const long long step = kSub * p.x[t].dst_h;
+            float2 A[8], B[8];
+            uint32_t turns = 0;
+            if (!kAppend || t < 2) {
+                float2 w[8];
+                float c[8], sn[8];
+                weights16(w_s[t & 1], place.ca, place.cb, w);
+                turns = place.take(cs[warp], p.pairs, c, sn);
+                place.factors(w, c, sn, A, B);
             }
-            x = next;
+            auto heads = [&](auto all) {       // all: every word of the warp turns
+#pragma unroll 1
+                for (int h = h0 + sub; h - sub < h1; h += kNormHeads * kSub) {
+                    cp_async_wait<kNormStages - 2>();
+                    uint4 xa[kNormHeads], xb[kNormHeads];
+#pragma unroll
+                    for (int u = 0; u < kNormHeads; ++u) {
+                        xa[u] = ring[stage][2 * u][threadIdx.x];
+                        xb[u] = ring[stage][2 * u + 1][threadIdx.x];
+                    }
+                    load(stage == 0 ? kNormStages - 1 : stage - 1);        // (the stage read in the step before)
+                    stage = stage + 1 == kNormStages ? 0 : stage + 1;
+#pragma unroll
+                    for (int u = 0; u < kNormHeads; ++u) {
+                        if (!kAppend || t < 2) {
+                            float2 x[8], y[8];
+                            unpack16(xa[u], xb[u], x);
+                            const float r = rsqrtf(head_dot<kL>(x, x) * (1.0f / D) + p.eps);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                y[i] = __fmul2_rn(x[i], A[i]);
+                                if (all.value || place.turned(turns, i)) y[i] = __ffma2_rn(place.partners(x, i), B[i], y[i]);
+                                y[i] = __fmul2_rn(y[i], both(r));
+                            }
+                            pack16(y, xa[u], xb[u]);
+                        }
+                        if (out && h + u * kSub < h1) {
+                            *reinterpret_cast<uint4*>(dst + place.ca * 16) = xa[u];
+                            *reinterpret_cast<uint4*>(dst + place.cb * 16) = xb[u];
+                        }
+                        dst += step;
+                    }
+                }
+            };
+            if (__all_sync(0xFFFFFFFFu, turns == 0xFFu)) heads(std::true_type());
+            else heads(std::false_type());
         }
     }
+    cp_async_wait<0>();
 }
 
-// The gradient.  Blocks 0 .. blocks[0] - 1 take q, the others k, each tokens in turn; a thread sums its 16 elements of dw
-// over all of its heads, a block adds up its threads' in a fixed order, and attn_norm_rope_dw_kernel the blocks'.
+// The gradient.  A warp takes a token's q heads, then its k heads; a thread sums its 16 elements of q's dw over all of its heads
+// in registers, of k's in shared memory, a block adds up its threads' in a fixed order, and attn_norm_rope_dw_kernel the blocks'.
+// (q and k in blocks of their own: each token's angles twice, and they take as long as four heads' steps.)
+constexpr int kNormBwdStages = 3;
 template <int D, bool kHalves>
-__global__ void __launch_bounds__(kNormThreads, 4) attn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int kL = D / 16, kSub = 32 / kL;
     __shared__ TurnTable<D> table;
-    __shared__ __align__(16) float w_s[D];
+    __shared__ __align__(16) float w_s[2][D];
     __shared__ float2 cs[kNormWarps][D / 2];
-    __shared__ float sum_s[kNormWarps][D];
+    __shared__ uint4 ring[kNormBwdStages][4][kNormThreads];
+    __shared__ float4 dk_s[4][kNormThreads];           // a thread's sums of k's dw
+    float(*sum_s)[D] = reinterpret_cast<float(*)[D]>(ring);        // (at the end)
     pdl_wait();
     pdl_launch();
-    const int t = (int)blockIdx.x >= p.blocks[0], block = blockIdx.x - t * p.blocks[0];
-    for (int i = threadIdx.x; i < D; i += kNormThreads) w_s[i] = weight_at(p, t, i);
+    for (int i = threadIdx.x; i < 2 * D; i += kNormThreads) w_s[i / D][i % D] = weight_at(p, i / D, i % D);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dk_s[i][threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (table.fill(p)) {
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_AXES);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / kL;
     const Place<D, kHalves> place(lane % kL, p.pairs);
-    const RopeTensor &tx = p.x[t], &tg = p.dy[t];
-    float dw[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) dw[e] = 0.0f;
-#pragma unroll 1
-    for (long long token = (long long)block * kNormWarps + warp; token < p.tokens;
-         token += (long long)p.blocks[t] * kNormWarps) {
-        const long long b = token / p.S, s = token - b * p.S;
-        struct Head { uint4 xa, xb, ga, gb; };
-        auto load = [&](int h) {
-            Head y;
-            y.xa = y.xb = y.ga = y.gb = make_uint4(0u, 0u, 0u, 0u);
-            if (h < tx.heads) {
-                const char* x = tx.src + b * tx.src_b + s * tx.src_t + h * tx.src_h;
-                const char* g = tg.src + b * tg.src_b + s * tg.src_t + h * tg.src_h;
-                y.xa = *reinterpret_cast<const uint4*>(x + place.ca * 16);
-                y.xb = *reinterpret_cast<const uint4*>(x + place.cb * 16);
-                y.ga = *reinterpret_cast<const uint4*>(g + place.ca * 16);
-                y.gb = *reinterpret_cast<const uint4*>(g + place.cb * 16);
+    const NormStride stride(p);
+    NormToken at = stride.first(), ahead = at;
+    const int tokens = (int)p.tokens;
+    const uint32_t ring_at = ptx::smem_u32(&ring[0][0][threadIdx.x]);
+    // the loads ahead: tensor, heads left of it, where the next ones are
+    int ta = -1, left = 0;
+    const char *from_x = nullptr, *from_g = nullptr;
+    auto load = [&](int stage) {
+        while (left <= 0 && ahead.token < tokens) {
+            if (++ta == 2) {
+                ta = -1;
+                stride.next(ahead);
+                continue;
             }
-            return y;
-        };
-        Head y = load(lane / kL);
-        table.angles(p, b, s, cs[warp]);
+            left = p.x[ta].heads;
+            from_x = p.x[ta].src + (long long)ahead.b * p.x[ta].src_b + (long long)ahead.s * p.x[ta].src_t + sub * p.x[ta].src_h;
+            from_g = p.dy[ta].src + (long long)ahead.b * p.dy[ta].src_b + (long long)ahead.s * p.dy[ta].src_t + sub * p.dy[ta].src_h;
+        }
+        if (left > sub) {
+            const uint32_t to = ring_at + stage * (4 * kNormThreads * 16);
+            cp_async16_plain(to, from_x + place.ca * 16);
+            cp_async16_plain(to + kNormThreads * 16, from_x + place.cb * 16);
+            cp_async16_plain(to + 2 * kNormThreads * 16, from_g + place.ca * 16);
+            cp_async16_plain(to + 3 * kNormThreads * 16, from_g + place.cb * 16);
+        }
+        if (left > 0) {
+            from_x += kSub * p.x[ta].src_h;
+            from_g += kSub * p.dy[ta].src_h;
+        }
+        left -= kSub;
+        cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kNormBwdStages - 1; ++i) load(i);
+    float2 dq[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dq[e] = make_float2(0.0f, 0.0f);
+    int stage = 0;
+    typename TurnTable<D>::Positions pos, next_pos = at.token < tokens ? table.positions(p, at.b, at.s) : typename TurnTable<D>::Positions();
+#pragma unroll 1
+    for (NormToken then = at; at.token < tokens; at = then) {
+        pos = next_pos;
+        stride.next(then);
+        if (then.token < tokens) next_pos = table.positions(p, then.b, then.s);
+        table.angles(p, pos, cs[warp]);
         float c[8], sn[8];
         const uint32_t turns = place.take(cs[warp], p.pairs, c, sn);
+        auto tensor = [&](int t, float2 (&dw)[8]) {
+            char* dst = p.x[t].dst + (long long)at.b * p.x[t].dst_b + (long long)at.s * p.x[t].dst_t + sub * p.x[t].dst_h;
+            const long long step = kSub * p.x[t].dst_h;
+            const int heads = p.x[t].heads;
 #pragma unroll 1
-        for (int h0 = 0; h0 < tx.heads; h0 += kSub) {
-            const int h = h0 + lane / kL;
-            const Head next = load(h + kSub);
-            float x[16], g[16], w[16];
-            unpack16(y.xa, y.xb, x);
-            unpack16(y.ga, y.gb, g);
-            place.template turn<true>(g, c, sn, turns);
-            float ss = 0.0f;
+            for (int h = sub; h - sub < heads; h += kSub) {
+                cp_async_wait<kNormBwdStages - 2>();
+                float2 x[8], g[8], w[8];
+                unpack16(ring[stage][0][threadIdx.x], ring[stage][1][threadIdx.x], x);
+                unpack16(ring[stage][2][threadIdx.x], ring[stage][3][threadIdx.x], g);
+                load(stage == 0 ? kNormBwdStages - 1 : stage - 1);     // (the stage read in the step before)
+                place.template turn<true>(g, c, sn, turns);
+                const float r = rsqrtf(head_dot<kL>(x, x) * (1.0f / D) + p.eps);
+                const bool there = h < heads;                          // (what an absent head's place holds is another's)
+                weights16(w_s[t], place.ca, place.cb, w);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ss += x[e] * x[e];
-            const float r = rsqrtf(head_sum<kL>(ss) * (1.0f / D) + p.eps);
-            weights16(w_s, place.ca, place.cb, w);
-            float dot = 0.0f;
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = __fmul2_rn(x[e], both(r));
+                    if (there) dw[e] = __ffma2_rn(g[e], x[e], dw[e]);
+                    g[e] = __fmul2_rn(g[e], w[e]);
+                }
+                const float dot = head_dot<kL>(g, x) * (1.0f / D);
+                if (there) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                x[e] *= r;
-                if (h < tx.heads) dw[e] += g[e] * x[e];    // (an absent head's r may be infinite)
-                g[e] *= w[e];
-                dot += g[e] * x[e];
+                    for (int e = 0; e < 8; ++e) g[e] = __fmul2_rn(__ffma2_rn(x[e], both(-dot), g[e]), both(r));
+                    uint4 oa, ob;
+                    pack16(g, oa, ob);
+                    *reinterpret_cast<uint4*>(dst + place.ca * 16) = oa;
+                    *reinterpret_cast<uint4*>(dst + place.cb * 16) = ob;
+                }
+                dst += step;
+                stage = stage + 1 == kNormBwdStages ? 0 : stage + 1;
             }
-            dot = head_sum<kL>(dot) * (1.0f / D);
-            if (h < tx.heads) {
+        };
+        tensor(0, dq);
+        if (p.x[1].heads > 0) {
+            float2 dk[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) g[e] = r * (g[e] - x[e] * dot);
-                char* dst = tx.dst + b * tx.dst_b + s * tx.dst_t + h * tx.dst_h;
-                uint4 oa, ob;
-                pack16(g, oa, ob);
-                *reinterpret_cast<uint4*>(dst + place.ca * 16) = oa;
-                *reinterpret_cast<uint4*>(dst + place.cb * 16) = ob;
+            for (int e = 0; e < 8; ++e) dk[e] = make_float2(0.0f, 0.0f);
+            tensor(1, dk);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4 v = dk_s[i][threadIdx.x];
+                v.x += dk[2 * i].x; v.y += dk[2 * i].y; v.z += dk[2 * i + 1].x; v.w += dk[2 * i + 1].y;
+                dk_s[i][threadIdx.x] = v;
             }
-            y = next;
         }
     }
+    cp_async_wait<0>();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int t = 0; t < 2; ++t) {
+        __syncthreads();
 #pragma unroll
-        for (int off = kL; off < 32; off <<= 1) dw[e] += __shfl_xor_sync(0xFFFFFFFFu, dw[e], off);
-        if (lane < kL) sum_s[warp][(e < 8 ? place.ca : place.cb) * 8 + (e & 7)] = dw[e];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < D; i += kNormThreads) {
-        float v = 0.0f;
+        for (int e = 0; e < 16; ++e) {
+            const float4 k = dk_s[e >> 2][threadIdx.x];
+            float v = t ? ((e & 3) == 0 ? k.x : (e & 3) == 1 ? k.y : (e & 3) == 2 ? k.z : k.w) : e & 1 ? dq[e / 2].y : dq[e / 2].x;
 #pragma unroll
-        for (int w = 0; w < kNormWarps; ++w) v += sum_s[w][i];
-        p.part[(long long)blockIdx.x * D + i] = v;
+            for (int off = kL; off < 32; off <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+            if (lane < kL) sum_s[warp][(e < 8 ? place.ca : place.cb) * 8 + (e & 7)] = v;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < D; i += kNormThreads) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kNormWarps; ++w) v += sum_s[w][i];
+            p.part[((long long)t * gridDim.x + blockIdx.x) * D + i] = v;
+        }
     }
 }
 
@@ -354,10 +539,10 @@ __global__ void __launch_bounds__(32 * kDwRows) attn_norm_rope_dw_kernel(const _
     int bad = 0;
     for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) bad |= (unsigned)p.axes[i] >= (unsigned)p.num_axes;
     if (__syncthreads_or(bad)) return;
-    const float* part = p.part + (t ? (long long)p.blocks[0] * D : 0) + col;
+    const float* part = p.part + (long long)t * p.blocks * D + col;
     float v = 0.0f;
 #pragma unroll 8
-    for (int i = y; i < p.blocks[t]; i += kDwRows) v += part[(long long)i * D];
+    for (int i = y; i < p.blocks; i += kDwRows) v += part[(long long)i * D];
     sum_s[y][threadIdx.x & 31] = v;
     __syncthreads();
     if (y == 0) {

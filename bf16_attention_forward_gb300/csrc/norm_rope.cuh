@@ -58,29 +58,25 @@ struct TurnTable {
         }
         return __syncthreads_or(bad);
     }
-    // A warp's lanes take a token's pairs: the positions (read one token ahead: each waits for memory), then cosines and sines.
-    static constexpr int kPairs = (D / 2 + 31) / 32;       // of a lane
-    struct Positions { int at[kPairs]; };
-    __device__ __forceinline__ Positions positions(const NormRopeParams& p, long long b, long long s) const {
-        Positions pos;
+    // cosines and sines of a token's pairs, by the lanes of a warp: positions first (they wait for memory)
+    __device__ __forceinline__ void angles(const NormRopeParams& p, int b, int s, float2* cs) const {
+        constexpr int kPairs = (D / 2 + 31) / 32;          // of a lane
+        int pos[kPairs];
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
             const int pr = (threadIdx.x & 31) + 32 * i;
-            pos.at[i] = 0;
+            pos[i] = 0;
             if (pr < p.pairs) {
                 const int a = axis[pr];
-                pos.at[i] = __ldg(p.positions + (a < 0 ? ~a : a) * p.pos_axis + b * p.pos_b + s);
+                pos[i] = __ldg(p.positions + (a < 0 ? ~a : a) * p.pos_axis + b * p.pos_b + s);
             }
         }
-        return pos;
-    }
-    __device__ __forceinline__ void angles(const NormRopeParams& p, const Positions& pos, float2* cs) const {
         __syncwarp();                                      // (the token before is done with cs)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
             const int pr = (threadIdx.x & 31) + 32 * i;
             if (pr >= p.pairs) break;
-            const long long at = (long long)(turn[pr] * (unsigned long long)(long long)pos.at[i]);
+            const long long at = (long long)(turn[pr] * (unsigned long long)(long long)pos[i]);
             float sn, c;
             sincospif(axis[pr] < 0 ? NAN : (float)at * 0x1p-63f, &sn, &c);
             cs[pr] = make_float2(c, sn);
@@ -108,19 +104,27 @@ struct Place {
             pb = 4 * cb;
         }
     }
-    // cosines and sines of the thread's 8 pairs; returns which of them turn, a bit each
-    __device__ __forceinline__ uint32_t take(const float2* cs, int pairs, float (&c)[8], float (&sn)[8]) const {
+    // which of the thread's 8 pairs turn, a bit each
+    __device__ __forceinline__ uint32_t turning(int pairs) const {
         uint32_t turns = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int pr = e < 4 ? pa + e : pb + e - 4;
-            const bool t = pr < pairs;
-            const float2 v = t ? cs[pr] : make_float2(1.0f, 0.0f);
-            turns |= (uint32_t)t << e;
-            c[e] = v.x;
-            sn[e] = v.y;
-        }
+        for (int e = 0; e < 8; ++e) turns |= (uint32_t)((e < 4 ? pa + e : pb + e - 4) < pairs) << e;
         return turns;
+    }
+    // their cosines and sines (1 and 0 where they do not turn: see still())
+    __device__ __forceinline__ void take(const float2* cs, float (&c)[8], float (&sn)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const float4 v = *reinterpret_cast<const float4*>(cs + (e < 4 ? pa + e : pb + e - 4));
+            c[e] = v.x; sn[e] = v.y;
+            c[e + 1] = v.z; sn[e + 1] = v.w;
+        }
+    }
+    // a warp's cosines and sines of pairs that do not turn; behind the last pair halves read 8 more
+    static constexpr int kAngles = D / 2 + 8;
+    static __device__ __forceinline__ void still(float2* cs, int pairs) {
+        for (int i = pairs + (threadIdx.x & 31); i < kAngles; i += 32) cs[i] = make_float2(1.0f, 0.0f);
+        __syncwarp();
     }
     // Of weights, cosines and sines the factors of a word: y = x * A + (its partners) * B.  Adjacent: a word is a pair and its
     // partners its own elements, swapped; halves: the word of the other chunk.
@@ -134,8 +138,8 @@ struct Place {
                 A[i] = __fmul2_rn(w[i], cc);
                 B[i] = __fmul2_rn(w[i ^ 4], i < 4 ? make_float2(-ss.x, -ss.y) : ss);
             } else {
-                A[i] = make_float2(w[i].x * c[i], w[i].y * c[i]);
-                B[i] = make_float2(-w[i].y * sn[i], w[i].x * sn[i]);
+                A[i] = __fmul2_rn(w[i], make_float2(c[i], c[i]));
+                B[i] = __fmul2_rn(make_float2(w[i].y, w[i].x), make_float2(-sn[i], sn[i]));
             }
         }
     }
@@ -236,12 +240,14 @@ struct NormStride {
     }
 };
 
-// Each thread copies its own 16-byte chunks into shared memory some heads ahead and reads only those back: nothing but its own
+// Each thread copies its own 16-byte chunks into shared memory two steps ahead and reads only those back: nothing but its own
 // wait_group stands between.  At HBM's rate the SMs have 350 instructions for a warp's kSub heads, so the loop is kept
 // short: weights, cosines and sines multiplied once a token, two products an instruction, addresses by addition.
+// 32,760 tokens of 24 heads (403 MB): 63 us, 95 % of a copy; with the next heads in registers 72, with more steps ahead or more
+// blocks 64 to 75 (more rows of the memory are open then).
 constexpr int kNormStages = 3;
 constexpr int kNormHeads = 2;      // of a thread at a time
-constexpr int kNormBlocks = 5;     // an SM, one wave: a block's tables and weights take as long as some tokens
+constexpr int kNormBlocks = 4;     // an SM, one wave: a block's tables and weights take as long as some tokens
 template <int D, bool kHalves, bool kAppend>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int kL = D / 16;     // lanes of a head
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
     constexpr int kTensors = kAppend ? 3 : 2;
     __shared__ TurnTable<D> table;
     __shared__ __align__(16) float w_s[2][D];
-    __shared__ float2 cs[kNormWarps][D / 2];
+    __shared__ __align__(16) float2 cs[kNormWarps][Place<D, kHalves>::kAngles];
     __shared__ uint4 ring[kNormStages][2 * kNormHeads][kNormThreads];
     pdl_wait();
     pdl_launch();
@@ -267,6 +273,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
     auto last_head = [&](int t) {
         return min(block_h + p.heads_per_block - (t > 0 ? p.x[0].heads : 0) - (t > 1 ? p.x[1].heads : 0), p.x[t].heads);
     };
+    place.still(cs[warp], p.pairs);
+    const uint32_t turns = place.turning(p.pairs);
+    const bool all_turn = __all_sync(0xFFFFFFFFu, turns == 0xFFu);
     // the loads ahead: tensor, heads left of it, where the next ones are
     const NormStride stride(p);
     NormToken at = stride.first(), ahead = at;
@@ -312,12 +321,8 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
 #pragma unroll 1
     for (int i = 0; i < kNormStages - 1; ++i) load(i);
     int stage = 0;
-    typename TurnTable<D>::Positions pos, next_pos = at.token < tokens ? table.positions(p, at.b, at.s) : typename TurnTable<D>::Positions();
 #pragma unroll 1
-    for (NormToken then = at; at.token < tokens; at = then) {
-        pos = next_pos;
-        stride.next(then);
-        if (then.token < tokens) next_pos = table.positions(p, then.b, then.s);
+    for (; at.token < tokens; stride.next(at)) {
         long long row = -1;        // the token's row of the cache
         if constexpr (kAppend) {
             row = slot_of(at.token);
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
                 if (lane == 0) report_invalid(ATTN_CACHE_SITE_SLOTS);
             }
         }
-        table.angles(p, pos, cs[warp]);
+        table.angles(p, at.b, at.s, cs[warp]);
 #pragma unroll 1
         for (int t = 0; t < kTensors; ++t) {
             const int h0 = first_head(t), h1 = last_head(t);
@@ -336,12 +341,11 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
             char* dst = p.x[t].dst + (long long)at.b * p.x[t].dst_b + (kAppend && t > 0 ? row : (long long)at.s) * p.x[t].dst_t + (h0 + sub) * p.x[t].dst_h;
             const long long step = kSub * p.x[t].dst_h;
             float2 A[8], B[8];
-            uint32_t turns = 0;
             if (!kAppend || t < 2) {
                 float2 w[8];
                 float c[8], sn[8];
                 weights16(w_s[t & 1], place.ca, place.cb, w);
-                turns = place.take(cs[warp], p.pairs, c, sn);
+                place.take(cs[warp], c, sn);
                 place.factors(w, c, sn, A, B);
             }
             auto heads = [&](auto all) {       // all: every word of the warp turns
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
                     }
                 }
             };
-            if (__all_sync(0xFFFFFFFFu, turns == 0xFFu)) heads(std::true_type());
+            if (all_turn) heads(std::true_type());
             else heads(std::false_type());
         }
     }
@@ -387,14 +391,15 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
 
 // The gradient.  A warp takes a token's q heads, then its k heads; a thread sums its 16 elements of q's dw over all of its heads
 // in registers, of k's in shared memory, a block adds up its threads' in a fixed order, and attn_norm_rope_dw_kernel the blocks'.
-// (q and k in blocks of their own: each token's angles twice, and they take as long as four heads' steps.)
+// 16,384 tokens of 40 heads (503 MB): 82 us both kernels, 91 % of a copy's rate; q and k in blocks of their own took 93 (a token's
+// angles, which wait for its position, take as long as some heads' steps), the next head in registers 105.
 constexpr int kNormBwdStages = 3;
 template <int D, bool kHalves>
 __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p) {
     constexpr int kL = D / 16, kSub = 32 / kL;
     __shared__ TurnTable<D> table;
     __shared__ __align__(16) float w_s[2][D];
-    __shared__ float2 cs[kNormWarps][D / 2];
+    __shared__ __align__(16) float2 cs[kNormWarps][Place<D, kHalves>::kAngles];
     __shared__ uint4 ring[kNormBwdStages][4][kNormThreads];
     __shared__ float4 dk_s[4][kNormThreads];           // a thread's sums of k's dw
     float(*sum_s)[D] = reinterpret_cast<float(*)[D]>(ring);        // (at the end)
@@ -413,6 +418,8 @@ __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_b
     NormToken at = stride.first(), ahead = at;
     const int tokens = (int)p.tokens;
     const uint32_t ring_at = ptx::smem_u32(&ring[0][0][threadIdx.x]);
+    place.still(cs[warp], p.pairs);
+    const uint32_t turns = place.turning(p.pairs);
     // the loads ahead: tensor, heads left of it, where the next ones are
     int ta = -1, left = 0;
     const char *from_x = nullptr, *from_g = nullptr;
@@ -447,15 +454,11 @@ __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_b
 #pragma unroll
     for (int e = 0; e < 8; ++e) dq[e] = make_float2(0.0f, 0.0f);
     int stage = 0;
-    typename TurnTable<D>::Positions pos, next_pos = at.token < tokens ? table.positions(p, at.b, at.s) : typename TurnTable<D>::Positions();
 #pragma unroll 1
-    for (NormToken then = at; at.token < tokens; at = then) {
-        pos = next_pos;
-        stride.next(then);
-        if (then.token < tokens) next_pos = table.positions(p, then.b, then.s);
-        table.angles(p, pos, cs[warp]);
+    for (; at.token < tokens; stride.next(at)) {
+        table.angles(p, at.b, at.s, cs[warp]);
         float c[8], sn[8];
-        const uint32_t turns = place.take(cs[warp], p.pairs, c, sn);
+        place.take(cs[warp], c, sn);
         auto tensor = [&](int t, float2 (&dw)[8]) {
             char* dst = p.x[t].dst + (long long)at.b * p.x[t].dst_b + (long long)at.s * p.x[t].dst_t + sub * p.x[t].dst_h;
             const long long step = kSub * p.x[t].dst_h;

@@ -1052,8 +1052,9 @@ def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix
     """:func:`attn_paged_decode` for a batch whose sequences all begin with the same ``prefix_len`` keys (one instruction,
     one document): those are read once for the whole batch, through ``block_table``'s first row.
 
-    Arguments as there; ``seqlens_k`` holds whole lengths (prefix_len or more), and a row's entries from the page that the
-    prefix ends in on are its own (its entries of pages that end inside the prefix are not read, but in the first row).
+    Arguments as there; ``seqlens_k`` holds whole lengths (prefix_len or more, or 0: a sequence that has ended gets NaN and -inf),
+    and a row's entries from the page that the prefix ends in on are its own (its entries of pages that end inside the
+    prefix are not read, but in the first row, which names them whatever its own length is).
     A sequence with another length or a bad page of its own is not written and is reported by
     :func:`cache_device_status`; a bad page of the prefix leaves every sequence unwritten.  ``workspace``: optional caller tensor
     (calls that may run at the same time need one each).  Returns ``o`` or ``(o, lse)`` (lse fp32 [B, H])."""

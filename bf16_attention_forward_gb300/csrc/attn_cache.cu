@@ -688,7 +688,7 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     // every warp has the same arithmetic to begin with
     const int64_t parts = (cdiv(plan.steps - 1, x.per) + 1) * (plan.single ? 2 : 1);
     j.warps = 1;
-    while (j.warps < kPfJoinWarps && parts > 8 * j.warps && a.B * a.H * j.warps * 2 <= 16 * sms) j.warps *= 2;
+    while (j.warps < kPfJoinWarps && parts > 8 * j.warps && a.B * a.H * j.warps <= 16 * sms) j.warps *= 2;
     st = a.d == 128 ? (plan.single ? launch_prefix<128, true>(x, plan.ctas, stream) : launch_prefix<128, false>(x, plan.ctas, stream))
                     : (plan.single ? launch_prefix<64, true>(x, plan.ctas, stream) : launch_prefix<64, false>(x, plan.ctas, stream));
     if (st != ATTN_OK) return st;
@@ -698,7 +698,7 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     else
         st = nh == 1 ? launch_own<64, 1>(j.s, stream) : nh == 2 ? launch_own<64, 2>(j.s, stream) : launch_own<64, 4>(j.s, stream);
     if (st != ATTN_OK) return st;
-    const int heads = (int)cdiv(a.H * j.warps, kPfJoinWarps);
+    const int heads = (int)cdiv(a.H * j.warps, 2 * kPfJoinWarps);
     auto* join = a.d == 128 ? (parts <= 4 ? attn_prefix_join_kernel<128, 4> : attn_prefix_join_kernel<128, 8>)
                             : (parts <= 4 ? attn_prefix_join_kernel<64, 4> : attn_prefix_join_kernel<64, 8>);
     return launch(join, a.B, heads, 32 * kPfJoinWarps, 0, stream, j);

@@ -171,7 +171,7 @@ __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor
 
 // The rows of a sequence without keys, and the report of a bad length; by the threads of a block.
 __device__ __forceinline__ void keyless(const DecodeParams& p, int b, int n, int d) {
-    if (n < p.common || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
+    if (n < 0 || (n > 0 && n < p.common) || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
     } else if (n == 0) {
 #pragma unroll 1

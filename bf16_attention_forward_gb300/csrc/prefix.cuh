@@ -561,24 +561,24 @@ struct PrefixJoin {
     int single, warps;             // one tile of rows a unit; warps a row
 };
 
-// The join: a row's parts of the prefix and of its own keys.  `warps` warps take a row, each a share of the prefix's parts and
-// the first of them its own keys', and are joined through shared memory.  The prefix's parts lie where arithmetic says, so
+// The join: a row's parts of the prefix and of its own keys.  `warps` warps take two rows (16 lanes each), each a share of the
+// prefix's parts and the first of them the own keys', and are joined through shared memory.  The prefix's parts lie where arithmetic says, so
 // they are on their way while the row's length and span are read.
 constexpr int kPfJoinWarps = 8;
-// kU: parts in flight; 4 where a row has no more, for more rows on an SM (20,480 rows of 1 or 2 parts: 25 us with 8, 15 with 4;
-// 2,048 rows of 20: 8 and 12).
+// kU: parts in flight; 4 where a row has no more, for more rows on an SM.  20,480 rows of 1 or 2 parts of the prefix: 13 us; 2,048
+// rows of 20: 7.
 template <int D, int kU>
-__global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 4) attn_prefix_join_kernel(const __grid_constant__ PrefixJoin p) {
-    constexpr int kC = D / 32;
-    struct __align__(4 * kC) V { float x[kC]; };       // a lane's neighbouring elements
+__global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 3) attn_prefix_join_kernel(const __grid_constant__ PrefixJoin p) {
+    constexpr int kQ = D / 64, kC = 4 * kQ;            // a lane's elements: 4 of each 64
+    struct V { float4 q[kQ]; };
     __shared__ V o_s[kPfJoinWarps][32];
-    __shared__ float2 ml_s[kPfJoinWarps];
-    __shared__ int bad_s[kPfJoinWarps];
+    __shared__ float2 ml_s[kPfJoinWarps][2];
+    __shared__ int bad_s[kPfJoinWarps][2];
     pdl_wait();
     pdl_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, W = p.warps, share = warp & (W - 1);
     // (W is a power of two; heads in y)
-    const int b = blockIdx.x, h = blockIdx.y * (kPfJoinWarps / W) + warp / W;
+    const int b = blockIdx.x, half = lane >> 4, at = lane & 15, h = (blockIdx.y * (kPfJoinWarps / W) + warp / W) * 2 + half;
     const bool there = h < p.s.H;
     const long long out = (long long)b * p.s.H + h;
     const int kv = there ? p.x.by_group.of(h) : 0, g = there ? h - kv * p.s.group : 0, r = b * p.s.group + g;
@@ -603,13 +603,27 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 4) attn_prefix
 #pragma unroll
     for (int x = 0; x < kC; ++x) acc[x] = 0.0f;
     // (every lane has a part's m and l, and its own elements: nothing to hand over)
+    auto row_of = [&](const float* row) {
+        V v;
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) v.q[q] = reinterpret_cast<const float4*>(row)[q * 16 + at];
+        return v;
+    };
+    auto add = [&](const V& v, float down, float f) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+            acc[4 * q] = acc[4 * q] * down + v.q[q].x * f;
+            acc[4 * q + 1] = acc[4 * q + 1] * down + v.q[q].y * f;
+            acc[4 * q + 2] = acc[4 * q + 2] * down + v.q[q].z * f;
+            acc[4 * q + 3] = acc[4 * q + 3] * down + v.q[q].w * f;
+        }
+    };
     auto merge = [&](float2 ml, const V& v) {
         bad |= ml.y == kBadPart;
         const float top = fmaxf(mx, ml.x), down = rescale(mx, top, p.s.scale_log2), f = rescale(ml.x, top, p.s.scale_log2);
         mx = top;
         sum = sum * down + ml.y * f;
-#pragma unroll
-        for (int x = 0; x < kC; ++x) acc[x] = acc[x] * down + v.x[x] * f;
+        add(v, down, f);
     };
     const int i0 = parts * share / W, i1 = parts * (share + 1) / W;
     V v[kU], own_v;
@@ -620,19 +634,19 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 4) attn_prefix
             if (i + j < i1) {
                 const long long part = prefix_part(i + j);
                 ml[j] = p.x.part_ml[part];
-                v[j] = reinterpret_cast<const V*>(p.x.part_o + part * D)[lane];
+                v[j] = row_of(p.x.part_o + part * D);
             }
     };
     fetch(i0);
     const bool good = there && len >= p.x.prefix_len && (long long)len <= (long long)p.s.pages.max_pages * p.s.pages.page_size;
-    if (there && !good && h == 0 && share == 0 && lane == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
+    if (there && !good && len != 0 && h == 0 && share == 0 && at == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
     // the own keys' parts: one of a whole row, or one of each warp of the span (its first in slot 1 of its warp, the others in 0)
     const bool whole = span.x < 0;
     const int own = good && share == 0 && len > p.x.prefix_len ? (whole ? 1 : span.y - span.x + 1) : 0;
     auto own_fetch = [&](int i) {
         const long long part = (2ll * (span.x + i) + (i == 0)) * heads + hh;
         own_m = whole ? p.s.own_ml[out] : p.s.part_ml[part];
-        own_v = reinterpret_cast<const V*>(whole ? p.s.own_o + out * D : p.s.part_o + part * D)[lane];
+        own_v = row_of(whole ? p.s.own_o + out * D : p.s.part_o + part * D);
     };
     if (own > 0) own_fetch(0);
 #pragma unroll 1
@@ -649,39 +663,39 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 4) attn_prefix
         merge(own_m, own_v);
     }
     if (W > 1) {
-        if (lane == 0) {
-            ml_s[warp] = make_float2(mx, sum);
-            bad_s[warp] = bad;
+        if (at == 0) {
+            ml_s[warp][half] = make_float2(mx, sum);
+            bad_s[warp][half] = bad;
         }
         V mine;
 #pragma unroll
-        for (int x = 0; x < kC; ++x) mine.x[x] = acc[x];
+        for (int q = 0; q < kQ; ++q) mine.q[q] = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
         o_s[warp][lane] = mine;
         __syncthreads();
         if (share != 0) return;
         float top = mx;
-        for (int w = 1; w < W; ++w) top = fmaxf(top, ml_s[warp + w].x);
+        for (int w = 1; w < W; ++w) top = fmaxf(top, ml_s[warp + w][half].x);
         const float f0 = rescale(mx, top, p.s.scale_log2);
         sum *= f0;
 #pragma unroll
         for (int x = 0; x < kC; ++x) acc[x] *= f0;
         for (int w = 1; w < W; ++w) {
-            const float f = rescale(ml_s[warp + w].x, top, p.s.scale_log2);
-            sum += ml_s[warp + w].y * f;
-            bad |= bad_s[warp + w] != 0;
-            const V other = o_s[warp + w][lane];
-#pragma unroll
-            for (int x = 0; x < kC; ++x) acc[x] += other.x[x] * f;
+            const float2 ml = ml_s[warp + w][half];
+            const float f = rescale(ml.x, top, p.s.scale_log2);
+            sum += ml.y * f;
+            bad |= bad_s[warp + w][half] != 0;
+            add(o_s[warp + w][lane], 1.0f, f);
         }
         mx = top;
     }
-    if (!good || bad) return;
-    const float inv = sum > 0.0f ? 1.0f / sum : NAN;   // no weight at all, or a NaN one: the row is NaN
-    uint32_t* to = reinterpret_cast<uint32_t*>(p.s.o + out * D) + lane * (kC / 2);
+    const bool ended = there && len == 0;              // without keys: NaN and -inf
+    if (!(good || ended) || bad) return;
+    const float inv = good && sum > 0.0f ? 1.0f / sum : NAN;       // no weight at all, or a NaN one: the row is NaN
+    auto pair = [&](float x, float y) { return round_bf16(x * inv, p.s.round_mode) | round_bf16(y * inv, p.s.round_mode) << 16; };
 #pragma unroll
-    for (int x = 0; x < kC; x += 2)
-        to[x / 2] = round_bf16(acc[x] * inv, p.s.round_mode) | round_bf16(acc[x + 1] * inv, p.s.round_mode) << 16;
-    if (p.s.lse && lane == 0) p.s.lse[out] = sum == 0.0f ? -INFINITY : mx * p.s.scale + logf(sum);
+    for (int q = 0; q < kQ; ++q)
+        reinterpret_cast<uint2*>(p.s.o + out * D)[q * 16 + at] = make_uint2(pair(acc[4 * q], acc[4 * q + 1]), pair(acc[4 * q + 2], acc[4 * q + 3]));
+    if (p.s.lse && at == 0) p.s.lse[out] = ended || sum == 0.0f ? -INFINITY : mx * p.s.scale + logf(sum);
 }
 
 }  // namespace cache

@@ -749,12 +749,14 @@ int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
  *   q, caches, o, lse, seqlens_k, block_table, round_mode   as in attn_paged_decode (weights: NULL)
  *   prefix_len       1 .. max_pages * page_size: keys 0 .. prefix_len - 1 of every sequence are those of sequence 0, and are
  *                    read through block_table's first row; the other rows' entries of pages that end inside the prefix
- *                    are not read.  A page that the prefix ends in may be sequence 0's, a copy of it in each sequence, or (without own
- *                    keys behind it) anything
- *   seqlens_k        lengths WITH the prefix, prefix_len .. max_pages * page_size; another length leaves that sequence's
- *                    outputs unwritten and is reported at ATTN_CACHE_SITE_DECODE, like a bad page of its own; a bad page of the
- *                    prefix leaves all outputs unwritten (ATTN_CACHE_SITE_PREFIX)
- * Softmax weights of the prefix's keys are rounded to bf16 before the product with the values, as in attn_fwd.  Results are
+ *                    are not read.  The page that the prefix ends in is each sequence's own from its end on: sequence 0's page,
+ *                    or a copy of it, or a page whose first slots hold anything
+ *   seqlens_k        lengths WITH the prefix, prefix_len .. max_pages * page_size, or 0: a sequence that has ended gets NaN and
+ *                    -inf.  Another length leaves that sequence's outputs unwritten and is reported at ATTN_CACHE_SITE_DECODE,
+ *                    like a bad page of its own; a bad page of the prefix leaves the outputs of all sequences with keys unwritten
+ *                    (ATTN_CACHE_SITE_PREFIX).  Sequence 0's row names the prefix's pages even when its length is 0
+ * Where the prefix is shared by kernels of its own, its keys' softmax weights are rounded to bf16 before the product with the values,
+ * as in attn_fwd; a short prefix, or one sequence, goes to attn_paged_decode's kernel (by the sizes alone).  H at most 65535.  Results are
  * bitwise reproducible for the same lengths and shapes on the same GPU model.  workspace: caller device memory of at least
  * attn_paged_prefix_decode_workspace_size() bytes, 16-byte aligned.
  */

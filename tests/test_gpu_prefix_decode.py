@@ -81,22 +81,35 @@ class Batch:
             assert np.all(np.abs(lse[b] - ref_lse) <= 2.0 ** -14 * (1 + np.abs(ref_lse)) + 2.0 ** -12), b
 
 
-CASES = [  # own keys, H, Hkv, d, page, prefix
+# The rule that sends a call to the decoding kernel alone goes by sequences * K/V heads * (tiles of the prefix + 2) against 14
+# an SM (2,128 on 152): "few" cases are below it, the others above.
+FEW = [  # own keys, H, Hkv, d, page, prefix
     ([1], 8, 8, 128, 16, 1),
     ([0], 4, 2, 64, 16, 40),
+    ([9], 4, 2, 64, 16, 40000),                      # one sequence shares with nobody
     ([0, 0, 0], 6, 2, 128, 32, 64),                  # no sequence has a key of its own
     ([5, 0, 300, 1, 129], 8, 2, 128, 16, 127),
-    ([3, 77, 128], 5, 1, 128, 24, 128),
     ([3, 77, 128], 24, 3, 64, 7, 129),
-    ([1] * 32, 32, 8, 128, 128, 513),                # 128 rows
-    ([2, 300] * 16 + [9], 32, 8, 128, 256, 1000),    # 132: two tiles
-    ([1, 40, 0, 17] * 13, 40, 8, 128, 24, 2500),     # 260: a second block of rows
-    ([7] * 9, 71, 1, 64, 100, 777),                  # 639 rows of one K/V head
-    ([64, 1] * 20, 12, 12, 128, 1, 300),             # 40 rows, a page a key
-    ([11, 500], 142, 2, 128, 64, 6000),
-    ([1, 2], 2, 1, 128, 512, 40000),                 # many parts of a row
-    ([2000, 1, 4000], 8, 8, 64, 16, 90),             # more own keys than shared ones
+    ([7] * 9, 71, 1, 64, 100, 777),
+    ([2000, 1, 4000], 8, 8, 64, 16, 90),
 ]
+MANY = [
+    ([2, 0, 40, 1] * 32, 8, 8, 128, 16, 1),          # 128 rows against one key
+    ([1] * 128, 8, 8, 64, 7, 129),
+    ([0] * 128, 8, 8, 128, 24, 257),                 # no own keys; an odd number of tiles
+    ([3, 300] * 8, 64, 8, 128, 100, 2100),
+    ([5] * 15, 64, 8, 128, 1, 2500),                 # a page a key
+    ([1, 2, 0], 8, 8, 128, 512, 14000),              # three rows of many parts
+    ([64, 1] * 20, 12, 12, 128, 3, 300),
+    ([2, 300] * 16 + [9], 32, 8, 128, 256, 1000),    # 132 rows: two tiles of them
+    ([1, 40, 0, 17] * 13, 40, 8, 128, 24, 2500),     # 260: a second block of rows
+    ([7] * 60, 71, 1, 64, 100, 3000),
+    ([11, 500] * 7, 142, 2, 128, 64, 6000),
+    ([300, 1] * 150, 4, 1, 64, 16, 900),
+    ([1, 0, 130] * 250, 3, 1, 128, 48, 1),
+    ([0, 3] * 200, 8, 2, 128, 128, 128),             # whole tiles only
+]
+CASES = FEW + MANY
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B%d_H%d_%d_d%d_p%d_%d" % (len(c[0]), *c[1:]))
@@ -104,7 +117,9 @@ def test_against_plain_attention(attn, case):
     x = Batch(*case, seed=len(case[0]) + case[5], scale=2.0)
     got = x.call(attn)
     assert attn.cache_device_status() == (0, 0)
-    x.check(got)
+    B = len(case[0])
+    x.check(got, rows=sorted({0, 1, 2, B // 2, B - 2, B - 1, *range(0, B, max(1, B // 12))} & set(range(B))))
+    assert got[0].isfinite().all() and got[1].isfinite().all()
     again = x.call(attn)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
@@ -113,36 +128,38 @@ def test_against_plain_attention(attn, case):
 def test_random_shapes(attn, seed):
     g = np.random.default_rng(seed)
     Hkv, G, d = int(g.integers(1, 9)), int(g.integers(1, 12)), int(g.choice([64, 128]))
-    B, page = int(g.integers(1, 80)), int(g.choice([1, 3, 8, 16, 48, 128, 300]))
+    B, page = int(g.integers(1, 80)) if seed % 2 else int(g.integers(150, 400)), int(g.choice([1, 3, 8, 16, 48, 128, 300]))
     own = g.integers(0, int(g.choice([2, 40, 400])), B).tolist()
     x = Batch(own, Hkv * G, Hkv, d, page, int(g.integers(1, 1500)), seed=100 + seed, scale=float(g.choice([0.1, 1, 4])))
     x.check(x.call(attn), rows=sorted(set(g.integers(0, B, 6).tolist())))
     assert attn.cache_device_status() == (0, 0)
 
 
+@pytest.mark.parametrize("times", [1, 40])
 @pytest.mark.parametrize("mode", ["rtna", "rtz"])
-def test_rounding_modes(attn, mode):
-    x = Batch([10, 90, 3], 16, 4, 128, 16, 300, seed=4)
+def test_rounding_modes(attn, mode, times):
+    x = Batch([10, 90, 3] * times, 16, 4, 128, 16, 2000, seed=4)
     near, other = x.call(attn), x.call(attn, round=mode)
-    x.check(other, out=2.0 ** -8 if mode == "rtna" else 2.0 ** -7)
+    x.check(other, rows=[0, 1, 2], out=2.0 ** -8 if mode == "rtna" else 2.0 ** -7)
     step = (other[0].view(torch.int16).int() - near[0].view(torch.int16).int()).abs()
     assert step.max() <= 1 and torch.equal(near[1], other[1])
 
 
-def test_equals_the_plain_decoding_call_where_pages_are_shared(attn):
+@pytest.mark.parametrize("times", [1, 10])
+def test_equals_the_plain_decoding_call_where_pages_are_shared(attn, times):
     """The same caches through attn_paged_decode, whose rows name the prefix's pages too."""
-    x = Batch([40, 0, 200, 7], 32, 8, 128, 16, 320, seed=9, scale=2.0)
+    x = Batch([40, 0, 200, 7] * times, 32, 8, 128, 16, 960, seed=9, scale=2.0)
     got = x.call(attn)
     table = x.table.clone()
-    table[:, :20] = table[0, :20]
+    table[:, :60] = table[0, :60]
     want = attn.attn_paged_decode(x.q, x.k, x.v, x.lens, table, return_lse=True)
     assert (got[0].float() - want[0].float()).norm() <= 2.0 ** -7 * want[0].float().norm()
     assert (got[1] - want[1]).abs().max() <= 1e-4
     # rows that name the shared pages change nothing, nor do other sequences
-    assert torch.equal(attn.attn_paged_prefix_decode(x.q, x.k, x.v, x.lens, table, 320), got[0])
+    assert torch.equal(attn.attn_paged_prefix_decode(x.q, x.k, x.v, x.lens, table, 960), got[0])
 
 
-@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("rows", [4, 600])
 def test_non_finite_keys_and_values(attn, rows):
     """Of the prefix and of own keys, as in attn_paged_decode: the same classes of outputs."""
     x = Batch([50, 3, 0, 20] * (rows // 4) + [8] * (rows % 4), 8, 1, 128, 16, 160, seed=rows)
@@ -168,9 +185,10 @@ def test_non_finite_keys_and_values(attn, rows):
         c[at] = kept
 
 
-def test_infinite_values_under_vanishing_weights(attn):
+@pytest.mark.parametrize("times", [1, 350])
+def test_infinite_values_under_vanishing_weights(attn, times):
     """A finite logit weighs something, however small: an infinite value stays infinite."""
-    x = Batch([3, 20], 4, 1, 64, 16, 200, seed=5)
+    x = Batch([3, 20] * times, 4, 1, 64, 16, 200, seed=5)
     x.q.fill_(4.0)
     k, v = x.k.flatten(0, 1), x.v.flatten(0, 1)
     k[int(x.table[0, 2]) * 16 + 1] = 64.0            # stands far out: every other weight underflows
@@ -180,22 +198,39 @@ def test_infinite_values_under_vanishing_weights(attn):
     assert torch.isposinf(got[:, :, 5]).all() and got[:, :, :5].isfinite().all()
 
 
-def test_all_logits_minus_infinity(attn):
-    x = Batch([3, 0, 20], 4, 2, 128, 16, 150, seed=5)
+@pytest.mark.parametrize("times", [1, 100])
+def test_all_logits_minus_infinity(attn, times):
+    x = Batch([3, 0, 20] * times, 4, 2, 128, 16, 150, seed=5)
     x.q.fill_(1.0)
     x.k.fill_(float("-inf"))
     o, lse = x.call(attn)
     assert o.isnan().all() and torch.isneginf(lse).all()
 
 
-def test_bad_lengths_and_pages_leave_their_rows(attn):
+@pytest.mark.parametrize("B,prefix", [(5, 96), (40, 2000)])
+def test_sequences_that_have_ended(attn, B, prefix):
+    x = Batch([30, 4, 200, 9, 1] + [3] * (B - 5), 8, 2, 128, 16, prefix, seed=2)
+    x.lens[[0, 3]] = 0
+    o, lse = x.call(attn)
+    assert attn.cache_device_status() == (0, 0)
+    assert (o[[0, 3]].view(torch.int16) == NAN_BITS).all() and torch.isneginf(lse[[0, 3]]).all()
+    x.check((o, lse), rows=[1, 2, 4])
+
+
+def many(own, H, Hkv, d, page, prefix, seed=0):
+    """A batch that is too large for the decoding kernel alone."""
+    return Batch(own + [2] * 36, H, Hkv, d, page, prefix, seed=seed)
+
+
+@pytest.mark.parametrize("make", [Batch, many])
+def test_bad_lengths_and_pages_leave_their_rows(attn, make):
     def run(x, **kw):
         o, lse = torch.full_like(x.q, 7.0), torch.full((len(x.lens), x.H), 7.0, device="cuda")
         x.call(attn, o=o, lse=lse)
         return o, lse
-    x = Batch([30, 4, 200, 9, 0], 8, 2, 128, 16, 96, seed=2)
+    x = make([30, 4, 200, 9, 0], 8, 2, 128, 16, 5 * 16 if make is Batch else 2000, seed=2)
     room = x.table.shape[1] * 16
-    for length in (95, -1, 0, room + 1, 2 ** 31 - 1):
+    for length in (x.prefix - 1, -1, 1, room + 1, 2 ** 31 - 1):
         kept = int(x.lens[2])
         x.lens[2] = length
         o, lse = run(x)
@@ -203,11 +238,12 @@ def test_bad_lengths_and_pages_leave_their_rows(attn):
         x.lens[2] = kept
         x.check((o, lse), rows=[0, 1, 3, 4])
     for page in (-1, len(x.k), 2 ** 31 - 1):
-        kept = int(x.table[2, 8])
-        x.table[2, 8] = page
+        at = x.prefix // 16 + 2
+        kept = int(x.table[2, at])
+        x.table[2, at] = page
         o, lse = run(x)
         assert attn.cache_device_status() == (1, 22) and (o[2] == 7).all() and (lse[2] == 7).all()
-        x.table[2, 8] = kept
+        x.table[2, at] = kept
         x.check((o, lse), rows=[0, 1, 3, 4])
     for page in (len(x.k), -1, -2 ** 31):            # of the prefix: nobody's outputs are written
         x.table[0, 2] = page
@@ -216,15 +252,15 @@ def test_bad_lengths_and_pages_leave_their_rows(attn):
 
 
 def test_stays_in_bounds_with_the_caller_s_workspace(attn):
-    x = Batch([30, 4, 700], 10, 2, 128, 24, 1111, seed=2)
+    x = Batch([30, 4, 700] * 40, 10, 2, 128, 24, 1111, seed=2)
     want = x.call(attn)
     a = attn.DecodeArgs()
-    a.B, a.H, a.Hkv, a.num_pages, a.page_size, a.max_pages, a.d = 3, 10, 2, len(x.k), 24, x.table.shape[1], 128
+    a.B, a.H, a.Hkv, a.num_pages, a.page_size, a.max_pages, a.d = 120, 10, 2, len(x.k), 24, x.table.shape[1], 128
     need = int(attn.load().attn_paged_prefix_decode_workspace_size(ctypes.byref(a), 1111))
     assert need > 0
     ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
-    room, lses = torch.full((64 + x.q.numel() + 64,), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((30 + 64,), 3.0, device="cuda")
-    got = x.call(attn, o=room[64:-64].view_as(x.q), lse=lses[32:-32].view(3, 10), workspace=ws[:need])
+    room, lses = torch.full((64 + x.q.numel() + 64,), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((1200 + 64,), 3.0, device="cuda")
+    got = x.call(attn, o=room[64:-64].view_as(x.q), lse=lses[32:-32].view(120, 10), workspace=ws[:need])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert (room[:64] == 3).all() and (room[-64:] == 3).all() and (lses[:32] == 3).all() and (lses[-32:] == 3).all()
     assert (ws[need:] == 0xFF).all()
@@ -234,23 +270,25 @@ def test_stays_in_bounds_with_the_caller_s_workspace(attn):
         attn.attn_paged_prefix_decode(x.q, x.k, x.v, x.lens, x.table, x.table.shape[1] * 24 + 1)
 
 
-def test_rows_past_2_to_the_32_bytes(attn):
+@pytest.mark.parametrize("times", [1, 20])
+def test_rows_past_2_to_the_32_bytes(attn, times):
     """A cache of 5 GB, its pages at the far end."""
-    x = Batch([30, 4, 200], 8, 8, 128, 128, 500, seed=3)
+    x = Batch([30, 4, 200] * times, 8, 8, 128, 128, 700, seed=3)
     far = 2_400_000 // 128
     k, v = (torch.zeros((far + len(x.k), 128, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     k[far:], v[far:] = x.k, x.v
     table = torch.where(x.table >= 0, x.table + far, x.table)
-    got = attn.attn_paged_prefix_decode(x.q, k, v, x.lens, table, 500, return_lse=True)
+    got = attn.attn_paged_prefix_decode(x.q, k, v, x.lens, table, 700, return_lse=True)
     want = x.call(attn)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-def test_captured_while_lengths_grow(attn):
-    x = Batch([1, 30, 4], 8, 2, 128, 16, 200, seed=7, spare=3)
+@pytest.mark.parametrize("times,prefix", [(1, 200), (40, 1500)])
+def test_captured_while_lengths_grow(attn, times, prefix):
+    B, cut = 3 * times, prefix // 16
+    x = Batch([1, 30, 4] * times, 8, 2, 128, 16, prefix, seed=7, spare=3)
     t = torch.arange(len(x.k), dtype=torch.int32)
-    cut = 200 // 16
-    x.table[:, cut:] = t[cut:cut + 3 * (x.table.shape[1] - cut)].view(3, -1).cuda()
+    x.table[:, cut:] = t[cut:cut + B * (x.table.shape[1] - cut)].view(B, -1).cuda()
     x.table[0, :cut] = t[:cut].cuda()
     x.call(attn)
     torch.cuda.synchronize()
@@ -259,14 +297,14 @@ def test_captured_while_lengths_grow(attn):
         got = x.call(attn)
     for _ in range(4):
         x.lens.add_(1)
-        x.q.copy_(draw(3, 8, 128, seed=int(x.lens[0])))
+        x.q.copy_(draw(B, 8, 128, seed=int(x.lens[0])))
         graph.replay()
-        x.check(got)
+        x.check(got, rows=[0, 1, 2, B - 1])
         assert all(torch.equal(a, b) for a, b in zip(got, x.call(attn)))
 
 
 def test_two_streams_with_workspaces_of_their_own(attn):
-    batches = [Batch([30, 4, 700], 8, 2, 128, 16, 1500, seed=s) for s in (1, 2)]
+    batches = [Batch([30, 4, 700] * 40, 8, 2, 128, 16, 1500, seed=s) for s in (1, 2)]
     want = [x.call(attn) for x in batches]
     streams = [torch.cuda.Stream() for _ in batches]
     for s in streams:

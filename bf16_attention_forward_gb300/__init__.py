@@ -954,7 +954,7 @@ def attn_paged_append(k, v, k_cache, v_cache, cu_seqlens_new, seqlens_k, block_t
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name, index, *shape):
     """A call's workspace size, by the shapes that it depends on (and the device, which has to be current)."""
-    a = {"attn_paged_decode": DecodeArgs, "attn_paged_evict": EvictArgs, "attn_norm_rope_bwd": NormRopeBwdArgs}[name]()
+    a = (DecodeArgs if name == "attn_paged_decode" else EvictArgs)()
     for n, x in shape:
         setattr(a, n, x)
     return int(getattr(load(), name + "_workspace_size")(ctypes.byref(a)))
@@ -1149,74 +1149,68 @@ def _norm_weights(index, d, q_weight, k_weight):
             continue
         if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("%s must be a CUDA float32 or bfloat16 tensor" % name)
-        _check(index, (w, name, w.dtype, 1))
-        if w.shape[0] != d:
-            raise ValueError("%s must hold one weight per element of a head" % name)
         if dtype is not None and w.dtype is not dtype:
             raise TypeError("q_weight and k_weight must have one type")
         dtype = w.dtype
+        _check(index, (w, name, dtype, 1))
+        if w.shape[0] != d:
+            raise ValueError("%s must hold one weight per element of a head" % name)
     return (0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
             1 if dtype is torch.bfloat16 else 0)
 
 
-class _NormOperands:
-    """The operands that attn_norm_rope and its gradient take alike, checked: sizes, strides and tables."""
+def _norm_operands(q, k, q_weight, k_weight, positions, freqs, axes, layout, pairing):
+    """Checks the operands that attn_norm_rope and its gradient take alike.  Returns the device, how a tensor's strides are
+    read and what a contiguous one's are, and the argument structure's fields from the weights to d, the strides of
+    q and k, and the fields from the positions' strides to weight_bf16."""
+    import torch
+    if layout not in LAYOUTS:
+        raise ValueError("layout must be bshd or bhsd")
+    if pairing not in PAIRINGS:
+        raise ValueError("pairing must be adjacent or halves")
+    dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
+    dev = _device_of(q, "q", torch.bfloat16, dim)
+    _check_heads(dev, dim, (q, "q")) if k is None else _check_heads(dev, dim, (q, "q"), (k, "k"))
+    bhsd = dim == 4 and layout == "bhsd"
+    # token and head dimensions
+    t, h = (0, 1) if dim == 3 else (2, 1) if bhsd else (1, 2)
+    qn = q.shape
+    B, S, H, d = 1 if dim == 3 else qn[0], qn[t], qn[h], qn[-1]
+    Hkv = 0
+    if k is not None:
+        kn = k.shape
+        Hkv = kn[h]
+        if kn[t] != S or kn[-1] != d or (dim == 4 and kn[0] != B):
+            raise ValueError("q and k must agree in all but their heads")
+    elif k_weight is not None:
+        raise ValueError("k_weight needs k")
+    qw, kw, bf16 = _norm_weights(dev, d, q_weight, k_weight)
+    pairs, num_axes, pos, fp, ap, pos_a, pos_b = 0, 1, 0, 0, 0, 0, 0
+    if positions is not None and freqs is not None and axes is not None:
+        per_batch = dim == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 3
+        pairs = _rope_tables(positions, freqs, axes, pairing, dev, 3 if per_batch else 2)
+        pn, ps = positions.shape, positions.stride()
+        if pn[-1] != S or (per_batch and pn[1] != B):
+            raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
+        pos, fp, ap = positions.data_ptr(), freqs.data_ptr(), axes.data_ptr()
+        num_axes, pos_a, pos_b = pn[0], ps[0], ps[1] if per_batch else 0
+    elif positions is not None or freqs is not None or axes is not None:
+        raise ValueError("positions, freqs and axes go together")
 
-    def __init__(self, q, k, q_weight, k_weight, positions, freqs, axes, eps, layout, pairing):
-        import torch
-        if layout not in LAYOUTS:
-            raise ValueError("layout must be bshd or bhsd")
-        if pairing not in PAIRINGS:
-            raise ValueError("pairing must be adjacent or halves")
-        self.dim = dim = 3 if isinstance(q, torch.Tensor) and q.dim() == 3 else 4
-        self.dev = dev = _device_of(q, "q", torch.bfloat16, dim)
-        _check_heads(dev, dim, (q, "q")) if k is None else _check_heads(dev, dim, (q, "q"), (k, "k"))
-        self.bhsd = dim == 4 and layout == "bhsd"
-        # token and head dimensions
-        self.t, self.h = (0, 1) if dim == 3 else (2, 1) if self.bhsd else (1, 2)
-        qn = q.shape
-        self.B, self.S, self.H, self.d = 1 if dim == 3 else qn[0], qn[self.t], qn[self.h], qn[-1]
-        self.Hkv = 0
-        if k is not None:
-            kn = k.shape
-            self.Hkv = kn[self.h]
-            if kn[self.t] != self.S or kn[-1] != self.d or (dim == 4 and kn[0] != self.B):
-                raise ValueError("q and k must agree in all but their heads")
-        elif k_weight is not None:
-            raise ValueError("k_weight needs k")
-        self.weights = _norm_weights(dev, self.d, q_weight, k_weight)
-        # (positions, freqs, axes; strides of positions; pairs, axes)
-        self.tables, self.pos, self.pairs, self.axes = (0, 0, 0), (0, 0), 0, 1
-        if positions is not None and freqs is not None and axes is not None:
-            per_batch = dim == 4 and isinstance(positions, torch.Tensor) and positions.dim() == 3
-            self.pairs = _rope_tables(positions, freqs, axes, pairing, dev, 3 if per_batch else 2)
-            pn, ps = positions.shape, positions.stride()
-            if pn[-1] != self.S or (per_batch and pn[1] != self.B):
-                raise ValueError("positions must be [axes, S], [axes, B, S] or, for packed tensors, [axes, total]")
-            self.tables = positions.data_ptr(), freqs.data_ptr(), axes.data_ptr()
-            self.pos, self.axes = (ps[0], ps[1] if per_batch else 0), pn[0]
-        elif positions is not None or freqs is not None or axes is not None:
-            raise ValueError("positions, freqs and axes go together")
-        self.eps, self.pairing = float(eps), PAIRINGS[pairing]
+    def strides(x):
+        s = x.stride()
+        return 0 if dim == 3 else s[0], s[t], s[h]
 
-    def like(self, t, of, name):
-        """Checks a tensor that has to have another's shape."""
-        _check_heads(self.dev, self.dim, (t, name))
-        if of is None or t.shape != of.shape:
-            raise ValueError("%s must have its input's shape" % name)
+    def dense(heads):
+        return (S * heads * d, d, S * d) if bhsd else (S * heads * d, heads * d, d)
+    return (dev, dim, strides, dense, (qw, kw, pos, fp, ap, B, S, H, Hkv, d), (pos_a, pos_b, pairs, num_axes, PAIRINGS[pairing], bf16))
 
-    def strides(self, t):
-        """(batch, token, head) strides; of none: zeros."""
-        if t is None:
-            return 0, 0, 0
-        s = t.stride()
-        return 0 if self.dim == 3 else s[0], s[self.t], s[self.h]
 
-    def fields(self, q, k, q_out, k_out):
-        return (q.data_ptr(), q_out.data_ptr(), 0 if k is None else k.data_ptr(), 0 if k is None else k_out.data_ptr(),
-                self.weights[0], self.weights[1], *self.tables, self.B, self.S, self.H, self.Hkv, self.d, *self.strides(q),
-                *self.strides(q_out), *self.strides(k), *self.strides(k_out), *self.pos, self.pairs, self.axes, self.pairing,
-                self.weights[2], self.eps, 0)
+def _check_like(dev, dim, t, of, name):
+    """Checks a tensor that has to have another's shape."""
+    _check_heads(dev, dim, (t, name))
+    if of is None or t.shape != of.shape:
+        raise ValueError("%s must have its input's shape" % name)
 
 
 def attn_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, freqs=None, axes=None, eps: float = 1e-6,
@@ -1228,27 +1222,46 @@ def attn_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, freqs=Non
     :func:`attn_rope`; without the three tables nothing is rotated.  ``q_weight``/``k_weight``: CUDA [d], both float32 or
     both bfloat16; None: ones.  Returns ``(q_out, k_out)``, or ``q_out`` when k is None."""
     import torch
-    a = _NormOperands(q, k, q_weight, k_weight, positions, freqs, axes, eps, layout, pairing)
-    for o, t, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if o is not None:
-            a.like(o, t, name)
-    on = _on(a.dev, stream)
+    dev, dim, strides, dense, sizes, rest = _norm_operands(q, k, q_weight, k_weight, positions, freqs, axes, layout, pairing)
+    S, H, Hkv = sizes[6:9]
+    if q_out is not None:
+        _check_like(dev, dim, q_out, q, "q_out")
+    if k_out is not None:
+        _check_like(dev, dim, k_out, k, "k_out")
+    on = _on(dev, stream)
     if on is not None:
         on.__enter__()
     try:
+        # (an output allocated here is contiguous)
+        qs = qos = strides(q)
+        ks = kos = (0, 0, 0) if k is None else strides(k)
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        if a.S > 0:
-            st = (_lib or load()).attn_norm_rope(_pack_norm(*a.fields(q, k, q_out, k_out)),
-                                                 torch._C._cuda_getCurrentRawStream(a.dev))
+            q_out, qos = torch.empty_like(q, memory_format=torch.contiguous_format), dense(H)
+        elif q_out is not q:
+            qos = strides(q_out)
+        if k is not None:
+            if k_out is None:
+                k_out, kos = torch.empty_like(k, memory_format=torch.contiguous_format), dense(Hkv)
+            elif k_out is not k:
+                kos = strides(k_out)
+        if S > 0:
+            a = _pack_norm(q.data_ptr(), q_out.data_ptr(), 0 if k is None else k.data_ptr(), 0 if k is None else k_out.data_ptr(),
+                           *sizes, *qs, *qos, *ks, *kos, *rest, eps, 0)
+            st = (_lib or load()).attn_norm_rope(a, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_norm_rope")
     finally:
         if on is not None:
             on.__exit__(None, None, None)
     return q_out if k is None else (q_out, k_out)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_bytes(index, B, S, H, Hkv, d):
+    """attn_norm_rope_bwd's workspace size, by sizes and device (which has to be current)."""
+    a = NormRopeBwdArgs()
+    a.B, a.S, a.H, a.Hkv, a.d, a.k, a.num_axes = B, S, H, Hkv, d, 16 if Hkv else 0, 1
+    return int(load().attn_norm_rope_bwd_workspace_size(ctypes.byref(a)))
 
 
 def attn_norm_rope_bwd(dq, dk, q, k, q_weight=None, k_weight=None, positions=None, freqs=None, axes=None,
@@ -1261,47 +1274,57 @@ def attn_norm_rope_bwd(dq, dk, q, k, q_weight=None, k_weight=None, positions=Non
     caller tensor (calls that may run at the same time need one each).  Returns
     ``(dq_out, dk_out, dq_weight, dk_weight)``, or ``(dq_out, dq_weight)`` when k is None."""
     import torch
-    a = _NormOperands(q, k, q_weight, k_weight, positions, freqs, axes, eps, layout, pairing)
+    dev, dim, strides, dense, sizes, rest = _norm_operands(q, k, q_weight, k_weight, positions, freqs, axes, layout, pairing)
+    B, S, H, Hkv, d = sizes[5:]
     if (dk is None) != (k is None):
         raise ValueError("dk and k go together")
-    a.like(dq, q, "dq")
+    _check_like(dev, dim, dq, q, "dq")
     if dk is not None:
-        a.like(dk, k, "dk")
-    for o, t, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        if o is not None:
-            a.like(o, t, name)
+        _check_like(dev, dim, dk, k, "dk")
+    if dq_out is not None:
+        _check_like(dev, dim, dq_out, q, "dq_out")
+    if dk_out is not None:
+        _check_like(dev, dim, dk_out, k, "dk_out")
     for o, w, name in ((dq_weight, q_weight, "dq_weight"), (dk_weight, k_weight, "dk_weight")):
         if o is not None:
             if w is None:
                 raise ValueError("%s needs its weight" % name)
-            _check(a.dev, (o, name, torch.float32, 1))
-            if o.shape[0] != a.d:
+            _check(dev, (o, name, torch.float32, 1))
+            if o.shape[0] != d:
                 raise ValueError("%s must hold d elements" % name)
     ws_bytes = 0
     if workspace is not None:
-        workspace, ws_bytes = _check_workspace(workspace, a.dev)
-    on = _on(a.dev, stream)
+        workspace, ws_bytes = _check_workspace(workspace, dev)
+    on = _on(dev, stream)
     if on is not None:
         on.__enter__()
     try:
+        device = q.device
+        dqs = qos = strides(dq)
+        dks = kos = (0, 0, 0) if k is None else strides(dk)
         if dq_out is None:
-            dq_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        if k is not None and dk_out is None:
-            dk_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            dq_out, qos = torch.empty_like(q, memory_format=torch.contiguous_format), dense(H)
+        elif dq_out is not dq:
+            qos = strides(dq_out)
+        if k is not None:
+            if dk_out is None:
+                dk_out, kos = torch.empty_like(k, memory_format=torch.contiguous_format), dense(Hkv)
+            elif dk_out is not dk:
+                kos = strides(dk_out)
         if q_weight is not None and dq_weight is None:
-            dq_weight = torch.empty(a.d, dtype=torch.float32, device=q.device)
+            dq_weight = torch.empty(d, dtype=torch.float32, device=device)
         if k_weight is not None and dk_weight is None:
-            dk_weight = torch.empty(a.d, dtype=torch.float32, device=q.device)
-        if a.S > 0:
+            dk_weight = torch.empty(d, dtype=torch.float32, device=device)
+        if S > 0:
             if workspace is None:
-                ws_bytes = _workspace_bytes("attn_norm_rope_bwd", a.dev, ("B", a.B), ("S", a.S), ("H", a.H), ("Hkv", a.Hkv),
-                                            ("d", a.d), ("k", 0 if k is None else 16), ("num_axes", 1))
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            args = _pack_norm_bwd(*a.fields(q, k, dq_out, dk_out), dq.data_ptr(), 0 if dk is None else dk.data_ptr(),
-                                  0 if dq_weight is None else dq_weight.data_ptr(),
-                                  0 if dk_weight is None else dk_weight.data_ptr(), *a.strides(dq), *a.strides(dk))
-            st = (_lib or load()).attn_norm_rope_bwd(args, workspace.data_ptr(), ws_bytes,
-                                                     torch._C._cuda_getCurrentRawStream(a.dev))
+                ws_bytes = _norm_bwd_bytes(dev, B, S, H, Hkv, d)
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+            a = _pack_norm_bwd(q.data_ptr(), dq_out.data_ptr(), 0 if k is None else k.data_ptr(),
+                               0 if k is None else dk_out.data_ptr(), *sizes, *strides(q), *qos,
+                               *((0, 0, 0) if k is None else strides(k)), *kos, *rest, eps, 0, dq.data_ptr(),
+                               0 if dk is None else dk.data_ptr(), 0 if dq_weight is None else dq_weight.data_ptr(),
+                               0 if dk_weight is None else dk_weight.data_ptr(), *dqs, *dks)
+            st = (_lib or load()).attn_norm_rope_bwd(a, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
             if st != 0:
                 raise AttnError(st, "attn_norm_rope_bwd")
         else:

@@ -38,14 +38,10 @@ cudaError_t set_prefix_attr() {
 }
 template <int D, int NH>
 cudaError_t set_decode_attr() {
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DecGeo<D>::kSmem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DecGeo<D>::kSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attn_decode_kernel<D, NH, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 DecGeo<D>::kSmem);
+    cudaError_t e = cudaSuccess;
+    for (auto kernel : {attn_decode_kernel<D, NH, false>, attn_decode_kernel<D, NH, true>, attn_decode_kernel<D, NH, false, kCommonKeys>,
+                        attn_decode_kernel<D, NH, false, kOwnKeys>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DecGeo<D>::kSmem);
     return e;
 }
 
@@ -457,6 +453,11 @@ int launch_decode(const DecodeParams& p, cudaStream_t stream) {
         if (st != ATTN_OK) return st;
         return launch(attn_decode_join_kernel<D, NH, true>, 4 * p.grid, 1, 256, 0, stream, p);
     }
+    if (p.common) {
+        st = launch(attn_decode_kernel<D, NH, false, kCommonKeys>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
+        if (st != ATTN_OK || p.whole) return st;
+        return launch(attn_decode_join_kernel<D, NH, false, kCommonKeys>, p.grid, 1, 256, 0, stream, p);
+    }
     st = launch(attn_decode_kernel<D, NH, false>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
     if (st != ATTN_OK || p.whole) return st;
     return launch(attn_decode_join_kernel<D, NH, false>, p.grid, 1, 256, 0, stream, p);
@@ -622,7 +623,7 @@ int check_prefix_shape(const attn_decode_args_t& a, int64_t prefix_len) {
 
 template <int D, int NH>
 int launch_own(const DecodeParams& p, cudaStream_t stream) {
-    return launch(attn_decode_kernel<D, NH, false, true>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
+    return launch(attn_decode_kernel<D, NH, false, kOwnKeys>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
 }
 template <int D, bool kSingle>
 int launch_prefix(const PrefixParams& p, int64_t ctas, cudaStream_t stream) {

@@ -81,10 +81,20 @@ struct DecGeo {
     static constexpr int kSmem = kRing + kRed;
 };
 
+// Which keys a call takes: all of a sequence's pages; the same with the leading `common` ones of the first sequence's
+// pages; or those from `first` on, which leave parts for another kernel's join.  (A template's choice: with `common` and
+// `first` looked up by every call, 513 keys took 6.55 us instead of 6.05.)
+enum DecodeKeys { kAllKeys, kCommonKeys, kOwnKeys };
+template <int kKeys>
+constexpr int kTileKeys = kKeys == kOwnKeys ? kDecKeys : kDecTile;
+
 // tiles of a sequence; 0 for a length that the table has no room for (the join kernel reports it)
-template <int kTile = kDecTile>
+template <int kKeys>
 __device__ __forceinline__ int seq_tiles(const DecodeParams& p, int n) {
-    return n > p.first && n >= p.common && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - p.first - 1) / kTile + 1 : 0;
+    const int first = kKeys == kOwnKeys ? p.first : 0;
+    if (kKeys == kCommonKeys && n < p.common) return 0;
+    return n > first && (long long)n <= (long long)p.pages.max_pages * p.pages.page_size ? (n - first - 1) / kTileKeys<kKeys> + 1
+                                                                                       : 0;
 }
 
 // The line: sequence by sequence, row by row, a row's tiles and its end.  (The host refuses sizes whose
@@ -99,19 +109,20 @@ struct Line {
     }
 };
 
-// rows: of a sequence; workers: how many share the line, with `least` places at least (but for one worker)
-template <int kTile = kDecTile>
-__device__ __forceinline__ Line make_line(const DecodeParams& p, int rows, int workers, int least = 1) {   // by a whole warp
+// rows: of a sequence; workers: how many share the line.  (A warp of own keys has up to three tiles in flight at once: fewer
+// places of it would only make more parts.)
+template <int kKeys>
+__device__ __forceinline__ Line make_line(const DecodeParams& p, int rows, int workers) {   // by a whole warp
     int n = 0;
 #pragma unroll 2
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-        const int t = seq_tiles<kTile>(p, __ldg(p.seqlens_k + b));
+        const int t = seq_tiles<kKeys>(p, __ldg(p.seqlens_k + b));
         n += t > 0 ? t + 1 : 0;
     }
     n = __reduce_add_sync(0xFFFFFFFFu, n);
     Line l;
     l.units = n * rows;
-    l.ctas = min((l.units + least - 1) / least, workers);
+    l.ctas = min(kKeys == kOwnKeys ? (l.units + 2) / 3 : l.units, workers);
     l.per = l.ctas ? l.units / l.ctas : 1;
     l.more = l.units - l.per * l.ctas;
     return l;
@@ -122,14 +133,14 @@ struct Cursor {
 };
 
 // what is at place u of the line (u < units)
-template <int kTile = kDecTile>
+template <int kKeys>
 __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
     const int lane = threadIdx.x & 31;
     int done = 0;                      // places of a row, of the sequences before
     Cursor c{u, 0, 0, 0, 1, 0};
 #pragma unroll 1
     for (int base = 0; base < p.B; base += 32) {
-        const int len = base + lane < p.B ? __ldg(p.seqlens_k + base + lane) : 0, tiles = seq_tiles<kTile>(p, len);
+        const int len = base + lane < p.B ? __ldg(p.seqlens_k + base + lane) : 0, tiles = seq_tiles<kKeys>(p, len);
         const int mine = tiles > 0 ? tiles + 1 : 0;
         int incl = mine;
 #pragma unroll
@@ -154,7 +165,7 @@ __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
 }
 
 // to the first tile of the next row (past the last sequence's last row: any place behind the line)
-template <int kTile = kDecTile>
+template <int kKeys>
 __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor& c) {
     c.u += c.tiles + 1 - c.tile;
     c.tile = 0;
@@ -164,14 +175,15 @@ __device__ __forceinline__ void next_row(const DecodeParams& p, int rows, Cursor
     while (c.b + 1 < p.B) {
         ++c.b;
         c.len = __ldg(p.seqlens_k + c.b);
-        c.tiles = seq_tiles<kTile>(p, c.len);
+        c.tiles = seq_tiles<kKeys>(p, c.len);
         if (c.tiles > 0) break;
     }
 }
 
 // The rows of a sequence without keys, and the report of a bad length; by the threads of a block.
+template <int kKeys>
 __device__ __forceinline__ void keyless(const DecodeParams& p, int b, int n, int d) {
-    if (n < 0 || (n > 0 && n < p.common) || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
+    if (n < 0 || (kKeys == kCommonKeys && n > 0 && n < p.common) || (long long)n > (long long)p.pages.max_pages * p.pages.page_size) {
         if (threadIdx.x == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
     } else if (n == 0) {
 #pragma unroll 1
@@ -194,16 +206,17 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
     return m == -INFINITY ? 0.0f : ptx::ex2_approx(ptx::fmax_nan((m - to) * c, -125.0f));
 }
 
-// kShared: the own keys behind a shared prefix, as a line of 16-key tiles that the WARPS divide: own keys are often few, and
+// kOwnKeys: the own keys behind a shared prefix, as a line of 16-key tiles that the WARPS divide: own keys are often few, and
 // a row's end then costs a warp a few stores instead of a block its barriers (512 sequences of 1 to 200 own keys, 8 K/V
 // heads: 98 us a CTA's rows at a time).  Every row leaves (m, l, o) for the prefix's join.
-template <int D, int NH, bool kWeights, bool kShared = false>
+template <int D, int NH, bool kWeights, int kKeys = kAllKeys>
 __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using G = DecGeo<D>;
     constexpr int kHeads = 8 * NH;
     constexpr int kChunks = G::kRow / 16;              // 16-byte chunks of a key
     constexpr int kRowsPerCopy = 32 / kChunks;         // keys that one cp.async of the warp takes
-    constexpr int kTile = kShared ? kDecKeys : kDecTile;
+    constexpr int kTile = kTileKeys<kKeys>;
+    constexpr bool kShared = kKeys == kOwnKeys;
     extern __shared__ __align__(128) char smem[];
     __shared__ float2 ml_s[kDecWarps][kHeads], joined_s[kHeads];
     __shared__ int bad_s[kDecWarps][G::kStages];
@@ -218,18 +231,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     const int rows = p.Hkv * p.head_blocks;
     // which of the line's workers this is, and the warp's first key in a tile
     const int worker = kShared ? warp * gridDim.x + blockIdx.x : blockIdx.x, key0 = kShared ? 0 : warp * kDecKeys;
+    const int first_key = kShared ? p.first : 0;
     Line line;
     Cursor cur;
     int u0 = 0, u1;
     if (p.whole) {
         cur = Cursor{0, (int)blockIdx.x / rows, (int)blockIdx.x % rows, 0, 0, 0};
         cur.len = __ldg(p.seqlens_k + cur.b);
-        u1 = cur.tiles = seq_tiles(p, cur.len);
-        if (cur.row == 0) keyless(p, cur.b, cur.len, D);
+        u1 = cur.tiles = seq_tiles<kKeys>(p, cur.len);
+        if (cur.row == 0) keyless<kKeys>(p, cur.b, cur.len, D);
         if (u1 == 0) return;
     } else {
-        // (a warp has up to three tiles in flight at once: fewer would only make more parts)
-        line = make_line<kTile>(p, rows, kShared ? p.grid * kDecWarps : p.grid, kShared ? 3 : 1);
+        line = make_line<kKeys>(p, rows, kShared ? p.grid * kDecWarps : p.grid);
         if (worker >= line.ctas) {
             if (!kShared && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
             if (kShared) pdl_wait();
@@ -237,8 +250,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         }
         u0 = line.start(worker);
         u1 = line.start(worker + 1);
-        cur = seek<kTile>(p, rows, u0);
-        if (cur.tile == cur.tiles) next_row<kTile>(p, rows, cur);
+        cur = seek<kKeys>(p, rows, u0);
+        if (cur.tile == cur.tiles) next_row<kKeys>(p, rows, cur);
     }
     Cursor ahead = cur;
     const Cursor at0 = cur;
@@ -248,25 +261,29 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     // Where the loads are: find() looks up the rows of this warp's 16 keys of the tile at `ahead` (-1: past the
     // length or on a page that does not exist) and moves on; load() copies the tile found before into a
     // stage, absent rows as zeros.  A tile is found one load ahead, so that the table's latency is hidden.
-    struct Found { int row, kv_head, bad; };           // kv_head: -1 behind the range; bad: the site of a page that is not there
+    struct Found { int row, kv_head, bad; };           // kv_head: -1 behind the range; bad: 1, of a common key 2
     auto find = [&]() {
         Found f{-1, -1, 0};
         if (ahead.u >= u1) return f;
         f.kv_head = ahead.row / p.head_blocks;
-        const int j = p.first + ahead.tile * kTile + key0 + lane;
+        const int j = first_key + ahead.tile * kTile + key0 + lane;
         if (lane < kDecKeys && j < ahead.len) {
-            f.row = page_row(p.pages, p.pages.table + (j < p.common ? 0 : (long long)ahead.b * p.pages.max_pages), j);
-            if (f.row < 0) f.bad = j < p.common ? ATTN_CACHE_SITE_PREFIX : ATTN_CACHE_SITE_DECODE;
+            const bool common = kKeys == kCommonKeys && j < p.common;
+            f.row = page_row(p.pages, p.pages.table + (common ? 0 : (long long)ahead.b * p.pages.max_pages), j);
+            f.bad = f.row < 0 ? common ? 2 : 1 : 0;
         }
         ++ahead.u;
-        if (++ahead.tile == ahead.tiles && ahead.u < u1) next_row<kTile>(p, rows, ahead);
+        if (++ahead.tile == ahead.tiles && ahead.u < u1) next_row<kKeys>(p, rows, ahead);
         return f;
     };
     auto load = [&](int stage, const Found& f) {
         if (f.kv_head >= 0) {
-            const bool any_bad = __any_sync(0xFFFFFFFFu, f.bad != 0);
-            if (lane == 0) bad_s[warp][stage] = any_bad;
-            if (f.bad) report_invalid((uint32_t)f.bad);
+            const unsigned bad_keys = __ballot_sync(0xFFFFFFFFu, f.bad != 0);
+            const bool common_bad = kKeys == kCommonKeys && __any_sync(0xFFFFFFFFu, f.bad == 2);
+            if (lane == 0) {
+                bad_s[warp][stage] = bad_keys != 0;
+                if (bad_keys) report_invalid(common_bad ? ATTN_CACHE_SITE_PREFIX : ATTN_CACHE_SITE_DECODE);
+            }
             const int chunk = lane % kChunks;
             const long long col = (long long)f.kv_head * G::kRow + chunk * 16;
             const uint32_t dst = ring + stage * G::kStageBytes;
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 for (int t = 0; t < NH; ++t) mma_16816(s[t], a, qf[t][ks][0], qf[t][ks][1]);
             }
             // s[t][0..1]: key j0, heads 2 * (lane % 4) and + 1; s[t][2..3]: key j0 + 8
-            const int j0 = p.first + (cur.tile + i) * kTile + key0 + (lane >> 2);
+            const int j0 = first_key + (cur.tile + i) * kTile + key0 + (lane >> 2);
             bool grow = false;
 #pragma unroll
             for (int t = 0; t < NH; ++t) {
@@ -452,7 +469,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                         to[h * D + mt * 16 + 8 + (lane >> 2)] = acc[t][mt][c + 2];
                     }
                 }
-            next_row<kTile>(p, rows, cur);
+            next_row<kKeys>(p, rows, cur);
             continue;
         }
         bad = __syncthreads_or(bad);
@@ -514,7 +531,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 __syncthreads();
             }
         }
-        next_row<kTile>(p, rows, cur);
+        next_row<kKeys>(p, rows, cur);
     }
     if (kShared) pdl_wait();       // the join waits for this kernel only
     if (!kShared && !p.whole && threadIdx.x == 0) {
@@ -531,7 +548,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
 // they also write the rows of sequences without keys and report bad lengths.  With kWeights the blocks
 // behind them add every key's softmax weights to its running weight, from the logits that the attention kernel
 // kept and the rows' (m, l); they divide the tiles evenly over (sequence, K/V head) rows.
-template <int D, int NH, bool kWeights>
+template <int D, int NH, bool kWeights, int kKeys = kAllKeys>
 __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int kHeads = 8 * NH, kC = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -592,14 +609,14 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
             if (p.lse && lane == 0) p.lse[at] = sum == 0.0f ? -INFINITY : mx * p.scale + logf(sum);
         }
 #pragma unroll 1
-        for (int s = blockIdx.x; s < p.B; s += p.grid) keyless(p, s, __ldg(p.seqlens_k + s), D);
+        for (int s = blockIdx.x; s < p.B; s += p.grid) keyless<kKeys>(p, s, __ldg(p.seqlens_k + s), D);
         return;
     }
     if constexpr (kWeights) {
         constexpr int kG = 8;                          // query heads at a time
         __shared__ float2 ml_s[kG];                    // (m, 1 / l)
         __shared__ int bad_s;
-        const Line line = make_line(p, p.Hkv * p.head_blocks, p.grid);
+        const Line line = make_line<kKeys>(p, p.Hkv * p.head_blocks, p.grid);
         // this block's places on the line of K/V heads, which has one for head_blocks of the attention kernel's
         const int units = line.units / p.head_blocks, block = blockIdx.x - p.grid, blocks = gridDim.x - p.grid;
         const int per = units / blocks, more = units - per * blocks;
@@ -608,9 +625,9 @@ __global__ void __launch_bounds__(256, 4) attn_decode_join_kernel(const __grid_c
         const long long room = (long long)p.pages.max_pages * p.pages.page_size;
         const bool vector = room % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
         const uint64_t done_policy = ptx::policy_evict_first();
-        Cursor cur = seek(p, p.Hkv, t0);
+        Cursor cur = seek<kKeys>(p, p.Hkv, t0);
 #pragma unroll 1
-        for (; cur.u < t1; next_row(p, p.Hkv, cur)) {
+        for (; cur.u < t1; next_row<kKeys>(p, p.Hkv, cur)) {
             const int n = min(cur.tiles - cur.tile, t1 - cur.u);
             if (n == 0) continue;
             const int j1 = min(cur.len, (cur.tile + n) * kDecTile);

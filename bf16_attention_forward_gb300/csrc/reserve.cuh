@@ -27,7 +27,7 @@ struct ReserveParams {
     int32_t* count_out;
     int64_t* slots;                // [total]
     int32_t* positions;            // [total] or null
-    Pages pages;                   // (num_pages is not looked at: entries are taken as they are)
+    Pages pages;                   // (num_pages is not looked at)
     int B, capacity;
     long long total;
 };
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kReserveThreads, 1) attn_reserve_kernel(const 
     pdl_launch();
     const int t = threadIdx.x, per = (p.B - 1) / kReserveThreads + 1;          // sequences a thread
     const bool staged = p.B < kReserveCu;
-    const int count = __ldg(p.count);
+    const int count = p.count[0];
     int bad = count < 0 || count > p.capacity;
     // sequence b: pages it holds and wants
     auto pages_of = [&](int b) {
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kReserveThreads, 1) attn_reserve_kernel(const 
     for (int i = 0; i < per; ++i) {
         const int b = t * per + i;
         if (b >= p.B) break;
-        const int len = p.seqlens[b], c0 = __ldg(p.cu_new + b), c1 = __ldg(p.cu_new + b + 1);
+        const int len = p.seqlens[b], c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
         const int shared = p.shared ? p.shared[b] : 0;
         const int held = p.held[b];
         bad |= len < 0 || (long long)len > (long long)p.pages.max_pages * p.pages.page_size;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kReserveThreads, 1) attn_reserve_kernel(const 
         }
         if (staged) cu_s[b] = c0;
     }
-    if (staged && t == 0) cu_s[p.B] = __ldg(p.cu_new + p.B);
+    if (staged && t == 0) cu_s[p.B] = p.cu_new[p.B];
     // (B * max_pages is below 2^31, and so are the sums)
     const int2 incl = block_scan(make_int2(back, take), warp_s);
     back_s[t + 1] = incl.x;
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kReserveThreads, 1) attn_reserve_kernel(const 
             j = p.seqlens[lo] - (cu[lo + 1] - (int)i);
             const int pg = page_of(p.pages, j);
             const int phys = p.table[(long long)lo * p.pages.max_pages + pg];
-            slot = (long long)phys * p.pages.page_size + (j - pg * p.pages.page_size);
+            // (of a negative page never -1, which would pass for padding)
+            slot = phys < 0 ? -2 : (long long)phys * p.pages.page_size + (j - pg * p.pages.page_size);
         }
         p.slots[i] = slot;
         if (p.positions) p.positions[i] = j;

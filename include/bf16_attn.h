@@ -724,7 +724,8 @@ int attn_norm_rope_append(const attn_norm_append_args_t* args, attn_stream_t str
  * and their entries are written to the table.  Entries past held_out stay as they are.
  * All or nothing: bad lengths, offsets or counts, a stack without room for what comes back, or fewer free pages than are
  * missing leave table, stack and counts as they were, give every token the slot -1 and position 0, and are reported
- * at ATTN_CACHE_SITE_RESERVE.  Page numbers are not looked at (the calls that use them check them).
+ * at ATTN_CACHE_SITE_RESERVE.  Page numbers are not looked at (the calls that use them check them), but that a token on a
+ * negative one gets the slot -2, which attn_norm_rope_append reports.
  */
 typedef struct {
     const int32_t* seqlens_k;
@@ -754,7 +755,8 @@ int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
  *   seqlens_k        lengths WITH the prefix, prefix_len .. max_pages * page_size, or 0: a sequence that has ended gets NaN and
  *                    -inf.  Another length leaves that sequence's outputs unwritten and is reported at ATTN_CACHE_SITE_DECODE,
  *                    like a bad page of its own; a bad page of the prefix leaves the outputs of all sequences with keys unwritten
- *                    (ATTN_CACHE_SITE_PREFIX).  Sequence 0's row names the prefix's pages even when its length is 0
+ *                    (ATTN_CACHE_SITE_PREFIX).  Sequence 0's row names the prefix's pages even when its length is 0, the page
+ *                    that the prefix ends in among them: with attn_paged_reserve, shared_pages[0] counts that page too
  * Where the prefix is shared by kernels of its own, its keys' softmax weights are rounded to bf16 before the product with the values,
  * as in attn_fwd; a short prefix, or one sequence, goes to attn_paged_decode's kernel (by the sizes alone).  H at most 65535.  Results are
  * bitwise reproducible for the same lengths and shapes on the same GPU model.  workspace: caller device memory of at least

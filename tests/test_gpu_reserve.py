@@ -231,3 +231,18 @@ def test_a_captured_loop(attn):
         seen |= set(now)
     assert len(seen) == B * steps and int(count) == B * most - B * (steps // page)
     assert attn.cache_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("page", [1, 4])
+def test_a_negative_page_is_no_padding(attn, page):
+    """Tokens on a held page that is not there: no slot of theirs is -1, and the call that writes them reports it."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, cu, held = torch.tensor([page], **i32), torch.tensor([0, page], **i32), torch.tensor([1], **i32)
+    table, free, count = torch.full((1, 2), -1, **i32), torch.zeros(3, **i32), torch.tensor([0], **i32)
+    slots, positions = attn.attn_paged_reserve(lens, cu, table, held, free, count, page, total=page)
+    assert attn.cache_device_status() == (0, 0)
+    assert slots.tolist() == [-2] * page and positions.tolist() == list(range(page))
+    k = torch.ones(page, 1, 64, dtype=torch.bfloat16, device="cuda")
+    cache = torch.zeros(3, page, 1, 64, dtype=torch.bfloat16, device="cuda")
+    attn.attn_norm_rope_append(k, k, cache, cache.clone(), slots)
+    assert attn.cache_device_status()[1] == 24 and not cache.any()

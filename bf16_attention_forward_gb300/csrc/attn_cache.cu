@@ -627,7 +627,7 @@ int launch_own(const DecodeParams& p, cudaStream_t stream) {
 }
 template <int D, bool kSingle>
 int launch_prefix(const PrefixParams& p, int64_t ctas, cudaStream_t stream) {
-    return launch(attn_prefix_kernel<D, kSingle>, ctas, 1, kPfThreads, PfGeo<D, kSingle>::kSmem, stream, p);
+    return launch(attn_prefix_kernel<D, kSingle>, ctas, 1, PfGeo<D, kSingle>::kThreads, PfGeo<D, kSingle>::kSmem, stream, p);
 }
 
 int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* workspace, size_t workspace_bytes,

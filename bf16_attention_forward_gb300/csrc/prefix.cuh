@@ -22,7 +22,7 @@
 // P is rounded to bf16 for the second product (tcgen05 takes it in that type from TMEM; a second product
 // with its lower bits, as in decode.cuh, would double the work that bounds the kernel), l sums the unrounded weights.
 //
-// Loads.  Three warps copy keys and values with cp.async, row by row, into the 128-byte-swizzled tiles that the tensor pipe
+// Loads.  Three or six warps copy keys and values with cp.async, row by row, into the 128-byte-swizzled tiles that the tensor pipe
 // reads: any page size, any number of heads, no tensor maps to make on the host (TMA boxes of a page's rows reach the
 // same rate from 64 rows on, and half of HBM's with 8).  A slot's barrier counts the copies as they land, and the
 // products' thread sets a proxy fence between that and its first product.  A unit's queries come first, as soon as the unit before
@@ -66,14 +66,18 @@ struct PrefixParams {
     }
 };
 
-constexpr int kPfThreads = 384;    // warpgroups 0, 1: softmax; warps 8, 10 and 11 load, warp 9 issues the products
 constexpr int kPfTile = 128;
 constexpr int kPfBox = kPfTile * 64 * 2;       // 64 columns of a tile: rows of 128 bytes
-constexpr uint32_t kPfRegsSoftmax = 208, kPfRegsOther = 88;       // 256 * 208 + 128 * 88 = 384 * 168
 constexpr uint32_t kPfTmemCols = 512;          // S0 | S1 | O0 | O1
 
 template <int D, bool kSingle>
 struct PfGeo {
+    // Warpgroups 0, 1: softmax; warp 9 issues the products, and of the other warps those of other schedulers than its own load: three,
+    // or with one tile of rows, where HBM bounds, six in a block of 512 threads (24 sequences of 32 heads, 65,500 keys: 69.3 us,
+    // with three 76.5; but 64 sequences, 16,384 keys, two tiles of rows: 60.6, with three 58.4).
+    static constexpr int kLoaders = kSingle ? 6 : 3, kThreads = kSingle ? 512 : 384;
+    static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = kSingle ? 48 : 88;
+    static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= 65536 / kThreads / 8 * 8 * kThreads, "more registers than at launch");
     static constexpr int kTileBytes = kPfTile * D * 2;
     static constexpr int kQTiles = kSingle ? 1 : 2;
     static constexpr int kStages = 6 * 128 / D - kQTiles;          // all the shared memory that Q and the parts' room leave
@@ -152,7 +156,7 @@ struct PfWalk {                    // over the shares of a range u .. end - 1 of
 };
 
 template <int D, bool kSingle>
-__global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
+__global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_kernel(const __grid_constant__ PrefixParams p) {
     using G = PfGeo<D, kSingle>;
     extern __shared__ __align__(1024) uint8_t pf_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)pf_raw + 1023) & ~(uintptr_t)1023);
@@ -164,10 +168,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
-            ptx::mbar_init(bar(G::kFull + s), 96);
+            ptx::mbar_init(bar(G::kFull + s), 32 * G::kLoaders);
             ptx::mbar_init(bar(G::kEmpty + s), 1);
         }
-        ptx::mbar_init(bar(G::kQFull), 96);
+        ptx::mbar_init(bar(G::kQFull), 32 * G::kLoaders);
         ptx::mbar_init(bar(G::kQEmpty), 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(G::kSFull + i), 1);
@@ -196,24 +200,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
     auto tile_of = [&](int j, int t) { return kSingle ? 2 * j + t : j; };
 
     if (warp >= 8) {
-        ptx::reg_dealloc<kPfRegsOther>();
-        if (warp != 9) {
+        ptx::reg_dealloc<G::kRegsOther>();
+        if ((warp & 3) != 1) {
             // ------------------------------------------------------------------ loads
             // In the order in which the products take them: K0 V0 K1 V1 ..., or with two key tiles a step (a, b)
             // Ka0 Kb0, then Va0 Ka1 Vb0 Kb1, ..., and at the end Va Vb of every share.  A tile's 16 groups of 8 rows are dealt to
-            // the three warps; the pages of a tile of keys are looked up once, for its values too, and before the wait for a slot.
-            const int who = warp == 8 ? 0 : warp - 9;
+            // the loading warps; the pages of a tile of keys are looked up once, for its values too, and before the wait for a slot.
+            const int who = (warp >= 12 ? 3 : 0) + ((warp & 3) == 0 ? 0 : (warp & 3) - 1);
             constexpr int kChunks = D / 8, kRowsPerCopy = 32 / kChunks, kCopies = 8 / kRowsPerCopy;
             const uint32_t key_stride = (uint32_t)p.Hkv * D * 2;   // (the host refuses more)
             const uint64_t policy = p.row_blocks > 1 ? ptx::policy_evict_last() : ptx::policy_evict_first();
-            // keys `lane` and + 32 of this warp's 48 (40) of a tile: in group who + 3 * (i / 8), as page and its slot (-1:
-            // behind the prefix)
-            struct Rows { int page[2], in[2]; };
+            // Key i = lane + 32 * u of this warp's: row i % 8 of group who + loaders * (i / 8), as page and its slot (-1: behind
+            // the prefix).
+            constexpr int kGroups = (16 + G::kLoaders - 1) / G::kLoaders, kU = (8 * kGroups + 31) / 32;
+            struct Rows { int page[kU], in[kU]; };
             auto lookup = [&](int tile) {
                 Rows r;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int i = lane + 32 * u, in_tile = (who + 3 * (i >> 3)) * 8 + (i & 7), key = tile * kPfTile + in_tile;
+                for (int u = 0; u < kU; ++u) {
+                    const int i = lane + 32 * u, in_tile = (who + G::kLoaders * (i >> 3)) * 8 + (i & 7), key = tile * kPfTile + in_tile;
                     const bool there = in_tile < kPfTile && key < p.prefix_len;
                     const int pg = page_of(p.pages, there ? key : 0);
                     r.in[u] = there ? key - pg * p.pages.page_size : -1;
@@ -221,11 +226,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                 }
                 return r;
             };
-            // where this lane's 16 bytes of each copy of a group go in a slot (the next group of this warp lies 24 rows on)
+            // where this lane's 16 bytes of each copy of a group go in a slot (its next group lies 8 * loaders rows on)
             uint32_t to[kCopies];
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) to[i] = pf_chunk(who * 8 + i * kRowsPerCopy + lane / kChunks, lane % kChunks);
-            const int groups = who == 0 ? 6 : 5;
+            const int groups = (16 - who + G::kLoaders - 1) / G::kLoaders;
             uint32_t pos = 0;                                      // loads
             bool ok = true;
             auto load = [&](const char* base, const Rows& f) {
@@ -238,9 +243,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                 const uint32_t dst = sbase + (uint32_t)G::kRing + slot * G::kTileBytes;
                 const char* src = base + (long long)w.kv * D * 2 + (lane % kChunks) * 16;
                 bool there = true;
-                int row[2];
+                int row[kU];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < kU; ++u) {
                     const bool good = (unsigned)f.page[u] < (unsigned)p.pages.num_pages;
                     there &= good || lane + 32 * u >= groups * 8;
                     row[u] = good ? f.page[u] * p.pages.page_size + f.in[u] : -1;
@@ -249,26 +254,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                         report_invalid(ATTN_CACHE_SITE_PREFIX);
                     }
                 }
+                auto row_of = [&](int n, int i) {
+                    return __shfl_sync(0xFFFFFFFFu, n < 4 ? row[0] : row[kU - 1], (n * 8 + i * kRowsPerCopy + lane / kChunks) & 31);
+                };
                 if (__all_sync(0xFFFFFFFFu, there)) {
                     // (a group's rows are handed over before its copies: one after another, each copy would wait for its own)
 #pragma unroll
-                    for (int n = 0; n < 6; ++n) {
-                        if (n == 5 && groups == 5) break;
+                    for (int n = 0; n < kGroups; ++n) {
+                        if (n == kGroups - 1 && groups < kGroups) break;
                         const char* from[kCopies];
 #pragma unroll
-                        for (int i = 0; i < kCopies; ++i)
-                            from[i] = src + (unsigned long long)key_stride *
-                                      (uint32_t)__shfl_sync(0xFFFFFFFFu, row[n >> 2], (n * 8 + i * kRowsPerCopy + lane / kChunks) & 31);
+                        for (int i = 0; i < kCopies; ++i) from[i] = src + (unsigned long long)key_stride * (uint32_t)row_of(n, i);
 #pragma unroll
-                        for (int i = 0; i < kCopies; ++i) pf_copy16(dst + to[i] + n * (24 * 128), from[i], policy);
+                        for (int i = 0; i < kCopies; ++i) pf_copy16(dst + to[i] + n * (G::kLoaders * 8 * 128), from[i], policy);
                     }
                 } else {
 #pragma unroll 1
                     for (int n = 0; n < groups; ++n)
 #pragma unroll
                         for (int i = 0; i < kCopies; ++i) {
-                            const int x = __shfl_sync(0xFFFFFFFFu, n < 4 ? row[0] : row[1], (n * 8 + i * kRowsPerCopy + lane / kChunks) & 31);
-                            cp_async16(dst + to[i] + n * (24 * 128), src + (unsigned long long)key_stride * (uint32_t)max(x, 0),
+                            const int x = row_of(n, i);
+                            cp_async16(dst + to[i] + n * (G::kLoaders * 8 * 128), src + (unsigned long long)key_stride * (uint32_t)max(x, 0),
                                        x < 0 ? 0u : 16u, policy);
                         }
                 }
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
                     }
                     const __nv_bfloat16* from = p.q + (long long)w.kv * p.group * D + lane % kChunks * 8;
 #pragma unroll 4
-                    for (int i = who; i < kRowsQ / kRowsPerCopy; i += 3) {
+                    for (int i = who; i < kRowsQ / kRowsPerCopy; i += G::kLoaders) {
                         const int r = i * kRowsPerCopy + lane / kChunks, x = w.rb * kRowsQ + r, b = p.by_group.of(x);
                         const bool there = x < p.rows;
                         cp_async16(sbase + (uint32_t)((r / kPfTile) * G::kTileBytes) + pf_chunk(r % kPfTile, lane % kChunks),
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
             }
             cp_async_commit();
             cp_async_wait<0>();                                    // (a block that gives up leaves no copy behind)
-        } else if (lane == 0) {
+        } else if (warp == 9 && lane == 0) {
             // ------------------------------------------------------------------ products
             constexpr uint32_t idesc_s = pf_idesc(kPfTile, false), idesc_o = pf_idesc(D, true);
             // Q, K: rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart, 16 elements 32 bytes on, the second 64
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefix_kernel(const __grid
             }
         }
     } else {
-        ptx::reg_alloc<kPfRegsSoftmax>();
+        ptx::reg_alloc<G::kRegsSoftmax>();
         // ---------------------------------------------------------------------- softmax
         const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;

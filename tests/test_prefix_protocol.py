@@ -1,4 +1,4 @@
-"""Executable model of attn_prefix_kernel's synchronisation (csrc/prefix.cuh; host only, no GPU): three warps that copy keys and
+"""Executable model of attn_prefix_kernel's synchronisation (csrc/prefix.cuh; host only, no GPU): three or six warps that copy keys and
 values and the queries, whose barriers count them as they land, the thread that issues the products and two softmax warpgroups,
 which meet only through mbarriers, under random schedules and shares of a range.  Checked: no deadlock, no wait two phases behind, every product
 reads the tiles (and the queries and the P) of its own step, and nothing is overwritten before its products have read it.  Planted mistakes are caught.  A change to the kernel's barriers or to the order of
@@ -16,12 +16,13 @@ class Prefix:
 
     def __init__(self, shares, single, stages, rng, mistake=None):
         self.shares, self.single, self.stages, self.rng, self.mistake = shares, single, stages, rng, mistake
-        self.full = [Barrier("full%d" % i, 3) for i in range(stages)]
+        self.loaders = loaders = 6 if single else 3
+        self.full = [Barrier("full%d" % i, loaders) for i in range(stages)]
         self.empty = [Barrier("empty%d" % i, 1) for i in range(stages)]
-        self.q, self.q_empty = Barrier("q", 3), Barrier("q_empty", 1)
+        self.q, self.q_empty = Barrier("q", loaders), Barrier("q_empty", 1)
         self.s, self.p, self.o = ([Barrier("%s%d" % (n, i), 1) for i in range(2)] for n in "spo")
-        self.slot = [[None] * 3 for _ in range(stages)]        # what each warp has put into a slot
-        self.queries = [None] * 3                               # whose queries each warp has brought
+        self.slot = [[None] * loaders for _ in range(stages)]        # what each warp has put into a slot
+        self.queries = [None] * loaders                               # whose queries each warp has brought
         self.buf = [None, None]                                 # ("S" or "P", share, step) in TMEM
         self.acc = [(None, []), (None, [])]                     # share and steps accumulated in O
         self.pending, self.now, self.seq, self.mma_free = [], 0, 0, 0
@@ -88,7 +89,7 @@ class Prefix:
             yield from self.wait(self.full[at % self.stages], at // self.stages)
 
         def read(slot, what):
-            if self.slot[slot] != [what] * 3:
+            if self.slot[slot] != [what] * self.loaders:
                 raise Violation("product of %s read %s" % (what, self.slot[slot]))
 
         def issue_s(t, at, n, step):
@@ -96,7 +97,7 @@ class Prefix:
 
             def run():
                 read(at % self.stages, what)
-                if self.queries != [n] * 3:
+                if self.queries != [n] * self.loaders:
                     raise Violation("S of share %d read queries of %s" % (n, self.queries))
                 if step and self.acc[t] != (n, list(range(step))):
                     raise Violation("S over a P that was not used")
@@ -178,11 +179,11 @@ class Prefix:
             self.acc[t] = (None, [])
 
     def state(self):
-        return self.seq, sum(b.done * 3 + b.pending for b in
+        return self.seq, sum(b.done * 8 + b.pending for b in
                              self.full + self.empty + self.s + self.p + self.o + [self.q, self.q_empty])
 
     def run(self):
-        roles = [self.loader(0), self.loader(1), self.loader(2), self.mma(), self.softmax(0), self.softmax(1)]
+        roles = [self.loader(i) for i in range(self.loaders)] + [self.mma(), self.softmax(0), self.softmax(1)]
         idle = 0
         while roles or self.pending:
             self.now += 1

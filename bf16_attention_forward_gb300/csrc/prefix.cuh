@@ -568,7 +568,7 @@ struct PrefixJoin {
 };
 
 // The join: a row's parts of the prefix and of its own keys.  `warps` warps take two rows (16 lanes each), each a share of the
-// prefix's parts and the first of them the own keys', and are joined through shared memory.  The prefix's parts lie where arithmetic says, so
+// prefix's parts and of the own keys', and are joined through shared memory.  The prefix's parts lie where arithmetic says, so
 // they are on their way while the row's length and span are read.
 constexpr int kPfJoinWarps = 8;
 // kU: parts in flight; 4 where a row has no more, for more rows on an SM.  20,480 rows of 1 or 2 parts of the prefix: 13 us; 2,048
@@ -648,13 +648,13 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 3) attn_prefix
     if (there && !good && len != 0 && h == 0 && share == 0 && at == 0) report_invalid(ATTN_CACHE_SITE_DECODE);
     // the own keys' parts: one of a whole row, or one of each warp of the span (its first in slot 1 of its warp, the others in 0)
     const bool whole = span.x < 0;
-    const int own = good && share == 0 && len > p.x.prefix_len ? (whole ? 1 : span.y - span.x + 1) : 0;
+    const int own = good && len > p.x.prefix_len ? (whole ? 1 : span.y - span.x + 1) : 0;
     auto own_fetch = [&](int i) {
         const long long part = (2ll * (span.x + i) + (i == 0)) * heads + hh;
         own_m = whole ? p.s.own_ml[out] : p.s.part_ml[part];
         own_v = row_of(whole ? p.s.own_o + out * D : p.s.part_o + part * D);
     };
-    if (own > 0) own_fetch(0);
+    if (share < own) own_fetch(share);
 #pragma unroll 1
     for (int i = i0; i < i1; i += kU) {
         if (i > i0) fetch(i);
@@ -662,10 +662,9 @@ __global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 3) attn_prefix
         for (int j = 0; j < kU; ++j)
             if (i + j < i1) merge(ml[j], v[j]);
     }
-    if (own > 0) merge(own_m, own_v);
-#pragma unroll 2
-    for (int i = 1; i < own; ++i) {
-        own_fetch(i);
+#pragma unroll 1
+    for (int i = share; i < own; i += W) {
+        if (i > share) own_fetch(i);
         merge(own_m, own_v);
     }
     if (W > 1) {

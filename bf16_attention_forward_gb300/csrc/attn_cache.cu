@@ -596,7 +596,7 @@ struct PrefixLayout {
 };
 PrefixLayout prefix_layout(const attn_decode_args_t& a, const PrefixPlan& plan, int sms) {
     const int64_t heads = 8 * head_tiles(a.H / a.Hkv), blocks = cdiv(a.H / a.Hkv, heads);
-    const size_t rows = (size_t)(plan.ctas * plan.slots) * 2 * kPfTile, own = (size_t)(2 * sms * kDecWarps * heads);
+    const size_t rows = (size_t)(plan.ctas * plan.slots) * 2 * kPfTile, own = (size_t)(2 * sms * (heads == 8 ? kOwnWarps<1> : kOwnWarps<2>) * heads);
     PrefixLayout l;
     l.x_o = 0;
     l.x_ml = align256(rows * (size_t)a.d * 4);
@@ -623,7 +623,7 @@ int check_prefix_shape(const attn_decode_args_t& a, int64_t prefix_len) {
 
 template <int D, int NH>
 int launch_own(const DecodeParams& p, cudaStream_t stream) {
-    return launch(attn_decode_kernel<D, NH, false, kOwnKeys>, p.grid, 1, kDecThreads, DecGeo<D>::kSmem, stream, p);
+    return launch(attn_decode_kernel<D, NH, false, kOwnKeys>, p.grid, 1, 32 * kOwnWarps<NH>, DecGeo<D>::kSmem, stream, p);
 }
 template <int D, bool kSingle>
 int launch_prefix(const PrefixParams& p, int64_t ctas, cudaStream_t stream) {

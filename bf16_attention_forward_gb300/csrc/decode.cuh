@@ -80,6 +80,9 @@ struct DecGeo {
     static constexpr int kRed = kDecWarps * 8 * kRedRow * 4;      // 8 heads, half of d, per warp
     static constexpr int kSmem = kRing + kRed;
 };
+// Of own keys behind a prefix, whose rows are many and short: as many warps as the registers of 8 heads let run, two tiles each.
+template <int NH>
+constexpr int kOwnWarps = NH == 1 ? 12 : 8;
 
 // Which keys a call takes: all of a sequence's pages; the same with the leading `common` ones of the first sequence's
 // pages; or those from `first` on, which leave parts for another kernel's join.  (A template's choice: with `common` and
@@ -210,18 +213,21 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
 // a row's end then costs a warp a few stores instead of a block its barriers (512 sequences of 1 to 200 own keys, 8 K/V
 // heads: 98 us a CTA's rows at a time).  Every row leaves (m, l, o) for the prefix's join.
 template <int D, int NH, bool kWeights, int kKeys = kAllKeys>
-__global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(32 * (kKeys == kOwnKeys ? kOwnWarps<NH> : kDecWarps), 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using G = DecGeo<D>;
     constexpr int kHeads = 8 * NH;
     constexpr int kChunks = G::kRow / 16;              // 16-byte chunks of a key
     constexpr int kRowsPerCopy = 32 / kChunks;         // keys that one cp.async of the warp takes
     constexpr int kTile = kTileKeys<kKeys>;
     constexpr bool kShared = kKeys == kOwnKeys;
+    constexpr int kWarps = kShared ? kOwnWarps<NH> : kDecWarps;
+    constexpr int kStages = kWarps > kDecWarps ? G::kStages * 2 / 3 : G::kStages;
+    static_assert(kWarps * kStages <= kDecWarps * G::kStages, "ring larger than its room");
     extern __shared__ __align__(128) char smem[];
     __shared__ float2 ml_s[kDecWarps][kHeads], joined_s[kHeads];
-    __shared__ int bad_s[kDecWarps][G::kStages];
+    __shared__ int bad_s[kWarps][kStages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t ring = ptx::smem_u32(smem) + warp * (G::kStages * G::kStageBytes);
+    const uint32_t ring = ptx::smem_u32(smem) + warp * (kStages * G::kStageBytes);
     float* red = reinterpret_cast<float*>(smem + G::kRing);
 
     // (kShared: what it reads was complete before the prefix's kernel, all of whose CTAs let this one start behind their
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         if (cur.row == 0) keyless<kKeys>(p, cur.b, cur.len, D);
         if (u1 == 0) return;
     } else {
-        line = make_line<kKeys>(p, rows, kShared ? p.grid * kDecWarps : p.grid);
+        line = make_line<kKeys>(p, rows, kShared ? p.grid * kWarps : p.grid);
         if (worker >= line.ctas) {
             if (!kShared && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
             if (kShared) pdl_wait();
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
     // (code that runs once is kept short: every launch fetches it anew)
     Found next_tile = find();
 #pragma unroll 1
-    for (int s = 0; s < G::kStages - 1; ++s) {
+    for (int s = 0; s < kStages - 1; ++s) {
         const Found f = next_tile;
         next_tile = find();
         load(s, f);
@@ -346,9 +352,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
         bool bad = false;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            cp_async_wait<G::kStages - 2>();
+            cp_async_wait<kStages - 2>();
             __syncwarp();
             bad |= bad_s[warp][stage] != 0;
+            auto load_next = [&]() {                    // into the stage read last
+                load(stage == 0 ? kStages - 1 : stage - 1, next_tile);
+                next_tile = find();
+            };
+            if (kShared) load_next();
             const uint32_t ks_base = ring + stage * G::kStageBytes, vs_base = ks_base + kDecKeys * G::kRow;
             float s[NH][4];
 #pragma unroll
@@ -430,11 +441,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) attn_decode_kernel(const __gri
                 }
             }
             __syncwarp();                               // every lane has read the stage that is filled next
-            int next = stage + G::kStages - 1;
-            if (next >= G::kStages) next -= G::kStages;
-            load(next, next_tile);
-            next_tile = find();
-            stage = stage + 1 == G::kStages ? 0 : stage + 1;
+            if (!kShared) load_next();
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
 
         // join the warps: m and l through ml_s, o in halves of d through red

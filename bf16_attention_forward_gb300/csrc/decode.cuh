@@ -28,6 +28,8 @@
 // attn_decode_join_kernel merges a split row's parts, and beside that adds the
 // weights from the logits that the attention kernel kept.
 #pragma once
+#include <type_traits>
+
 #include "cache_common.cuh"
 
 namespace cache {
@@ -115,6 +117,15 @@ struct Line {
 // rows: of a sequence; workers: how many share the line.  (A warp of own keys has up to three tiles in flight at once: fewer
 // places of it would only make more parts.)
 template <int kKeys>
+__device__ __forceinline__ Line line_of(int places, int rows, int workers) {
+    Line l;
+    l.units = places * rows;
+    l.ctas = min(kKeys == kOwnKeys ? (l.units + 2) / 3 : l.units, workers);
+    l.per = l.ctas ? l.units / l.ctas : 1;
+    l.more = l.units - l.per * l.ctas;
+    return l;
+}
+template <int kKeys>
 __device__ __forceinline__ Line make_line(const DecodeParams& p, int rows, int workers) {   // by a whole warp
     int n = 0;
 #pragma unroll 2
@@ -122,13 +133,7 @@ __device__ __forceinline__ Line make_line(const DecodeParams& p, int rows, int w
         const int t = seq_tiles<kKeys>(p, __ldg(p.seqlens_k + b));
         n += t > 0 ? t + 1 : 0;
     }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    Line l;
-    l.units = n * rows;
-    l.ctas = min(kKeys == kOwnKeys ? (l.units + 2) / 3 : l.units, workers);
-    l.per = l.ctas ? l.units / l.ctas : 1;
-    l.more = l.units - l.per * l.ctas;
-    return l;
+    return line_of<kKeys>(__reduce_add_sync(0xFFFFFFFFu, n), rows, workers);
 }
 
 struct Cursor {
@@ -166,6 +171,59 @@ __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
     }
     return c;
 }
+
+// The same two by a block, which reads the lengths once for all its warps: thread t takes sequences t * per and on, and
+// places[t] counts those of the threads before it.
+template <int kKeys, int kWarps>
+struct BlockLine {
+    int places[32 * kWarps + 1], warps[kWarps];
+    __device__ __forceinline__ int fill(const DecodeParams& p) {
+        const int t = threadIdx.x, per = (p.B - 1) / (32 * kWarps) + 1;
+        int n = 0;
+#pragma unroll 4
+        for (int b = t * per; b < min(t * per + per, p.B); ++b) {
+            const int tiles = seq_tiles<kKeys>(p, __ldg(p.seqlens_k + b));
+            n += tiles > 0 ? tiles + 1 : 0;
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, n, off);
+            if ((t & 31) >= off) n += x;
+        }
+        if ((t & 31) == 31) warps[t >> 5] = n;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) n += w < (t >> 5) ? warps[w] : 0;
+        places[t + 1] = n;
+        if (t == 0) places[0] = 0;
+        __syncthreads();
+        return places[32 * kWarps];
+    }
+    __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) const {
+        const int per = (p.B - 1) / (32 * kWarps) + 1;
+        int lo = 0, hi = 32 * kWarps - 1;          // the last thread with no more places before it
+#pragma unroll 1
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (places[mid] * rows <= u) lo = mid; else hi = mid - 1;
+        }
+        Cursor c{u, lo * per, 0, 0, 1, 0};
+        int done = places[lo];
+#pragma unroll 1
+        while (true) {
+            c.len = __ldg(p.seqlens_k + c.b);
+            c.tiles = seq_tiles<kKeys>(p, c.len);
+            const int n = c.tiles > 0 ? c.tiles + 1 : 0;
+            if ((done + n) * rows > u) break;
+            done += n;
+            ++c.b;
+        }
+        const int in = u - done * rows;
+        c.row = in / (c.tiles + 1);
+        c.tile = in - c.row * (c.tiles + 1);
+        return c;
+    }
+};
 
 // to the first tile of the next row (past the last sequence's last row: any place behind the line)
 template <int kKeys>
@@ -248,7 +306,9 @@ __global__ void __launch_bounds__(32 * (kKeys == kOwnKeys ? kOwnWarps<NH> : kDec
         if (cur.row == 0) keyless<kKeys>(p, cur.b, cur.len, D);
         if (u1 == 0) return;
     } else {
-        line = make_line<kKeys>(p, rows, kShared ? p.grid * kWarps : p.grid);
+        __shared__ std::conditional_t<kShared, BlockLine<kKeys, kWarps>, int> block_line;
+        if constexpr (kShared) line = line_of<kKeys>(block_line.fill(p), rows, p.grid * kWarps);
+        else line = make_line<kKeys>(p, rows, p.grid);
         if (worker >= line.ctas) {
             if (!kShared && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
             if (kShared) pdl_wait();
@@ -256,7 +316,8 @@ __global__ void __launch_bounds__(32 * (kKeys == kOwnKeys ? kOwnWarps<NH> : kDec
         }
         u0 = line.start(worker);
         u1 = line.start(worker + 1);
-        cur = seek<kKeys>(p, rows, u0);
+        if constexpr (kShared) cur = block_line.seek(p, rows, u0);
+        else cur = seek<kKeys>(p, rows, u0);
         if (cur.tile == cur.tiles) next_row<kKeys>(p, rows, cur);
     }
     Cursor ahead = cur;

@@ -888,9 +888,11 @@ void fill_norm_rope(NormRopeParams& p, const attn_norm_rope_args_t& a) {
 
 template <bool kAppend>
 int launch_norm_rope(NormRopeParams& p, int64_t d, bool halves, int sms, cudaStream_t stream) {
-    // heads of a block as in launch_rope
-    const int64_t lanes = p.tokens * 32, full = (int64_t)sms * 2048, piece = 32 / (d / 16);
-    int64_t splits = lanes < full ? cdiv(full, lanes) : 1;
+    // Few tokens have their heads split over blocks, as long as all blocks still run at once: a second wave takes as long as the
+    // first.  24 heads of d = 128, us: 600 tokens 5.4 (in more parts and two waves 7.6); 1,200 5.4 (11.1);
+    // 2,400 7.1 (12.0); 6,144 tokens of 48 heads, appending, 29.6 in one part and 31.3 in two.
+    const int64_t lanes = p.tokens * 32, full = (int64_t)kNormBlocks * kNormThreads * sms, piece = 32 / (d / 16);
+    int64_t splits = lanes < full ? full / lanes : 1;
     if (splits > cdiv(p.heads, piece)) splits = cdiv(p.heads, piece);
     p.heads_per_block = (int)(cdiv(cdiv(p.heads, splits), piece) * piece);
     const int64_t most = cdiv(p.tokens, kNormWarps), grid = most < kNormBlocks * sms ? most : kNormBlocks * sms;

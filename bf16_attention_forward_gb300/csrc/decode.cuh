@@ -82,7 +82,8 @@ struct DecGeo {
     static constexpr int kRed = kDecWarps * 8 * kRedRow * 4;      // 8 heads, half of d, per warp
     static constexpr int kSmem = kRing + kRed;
 };
-// Of own keys behind a prefix, whose rows are many and short: as many warps as the registers of 8 heads let run, two tiles each.
+// Of own keys behind a prefix, whose rows are many and short: as many warps as the registers of 8 heads let run, two tiles each
+// (eight of three: 2 us more of 512 sequences of 1 to 200 own keys, 8 K/V heads).
 template <int NH>
 constexpr int kOwnWarps = NH == 1 ? 12 : 8;
 
@@ -173,7 +174,7 @@ __device__ __forceinline__ Cursor seek(const DecodeParams& p, int rows, int u) {
 }
 
 // The same two by a block, which reads the lengths once for all its warps: thread t takes sequences t * per and on, and
-// places[t] counts those of the threads before it.
+// places[t] counts those of the threads before it.  (512 sequences: 3 us less than each warp with make_line and seek.)
 template <int kKeys, int kWarps>
 struct BlockLine {
     int places[32 * kWarps + 1], warps[kWarps];
@@ -269,7 +270,7 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
 
 // kOwnKeys: the own keys behind a shared prefix, as a line of 16-key tiles that the WARPS divide: own keys are often few, and
 // a row's end then costs a warp a few stores instead of a block its barriers (512 sequences of 1 to 200 own keys, 8 K/V
-// heads: 98 us a CTA's rows at a time).  Every row leaves (m, l, o) for the prefix's join.
+// heads, 210 MB: 41 us, and 98 with a CTA's rows one after another).  Every row leaves (m, l, o) for the prefix's join.
 template <int D, int NH, bool kWeights, int kKeys = kAllKeys>
 __global__ void __launch_bounds__(32 * (kKeys == kOwnKeys ? kOwnWarps<NH> : kDecWarps), 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using G = DecGeo<D>;

@@ -7,9 +7,10 @@
 //   dw = sum over heads and tokens of g * n,  dx = r (g * w - n (sum (g * w)_i n_i) / d).
 // All of it in fp32, y and dx rounded once.  (The squares' sum is fp32 too: elements past 10^19 overflow it, r is 0.)
 //
-// Bound: HBM bytes; x read and y written once (backward: x and dy read, dx written).  The threads stand as in rope.cuh:
-// a warp takes a token, whose angles it computes once; D / 16 lanes take a head, 16 elements each, so the sums over a
-// head are 2 or 3 shuffles.  Weights are fp32 in shared memory: 64 bytes of it a thread and head beside 32 from HBM.
+// Bound: HBM bytes; x read and y written once (backward: x and dy read, dx written).  A warp takes a token, whose angles it
+// computes once; D / 16 lanes take a head, 16 elements each (two 16-byte chunks, so that a pair's elements meet in one thread),
+// and the sums over a head are 2 or 3 shuffles.  Weights stand in shared memory as fp32; the forward multiplies them into
+// the cosines and sines once a token.
 #pragma once
 #include <type_traits>
 

@@ -77,6 +77,9 @@ CASES = [  # B, S, H, Hkv, d, layout, axis dims, pairing, first position, weight
     (1, 700, 1, 1, 64, "bshd", (2,), "adjacent", -2 ** 31, "fp32", 1.0),
     (2, 9, 71, 1, 128, "bhsd", (16, 16, 16, 16), "halves", 7, "fp32", EPS),
     (1, 1021, 17, 3, 64, "bshd", (64,), "halves", 0, "bf16", EPS),
+    (1, 900, 13, 5, 128, "bshd", (64,), "adjacent", 0, "fp32", EPS),       # heads in two parts
+    (3, 1201, 7, 2, 128, "bhsd", (64, 32), "adjacent", 3, "fp32", EPS),    # several tokens a warp, across batch entries
+    (1, 5003, 3, 1, 64, "bshd", (48,), "halves", -9, "bf16", EPS),
 ]
 ids = lambda c: "B%d_S%d_H%d_%d_d%d_%s_%s_%s_%s" % (*c[:6], "x".join(map(str, c[6])), c[7], c[9])      # noqa: E731
 

@@ -108,6 +108,8 @@ MANY = [
     ([300, 1] * 150, 4, 1, 64, 16, 900),
     ([1, 0, 130] * 250, 3, 1, 128, 48, 1),
     ([0, 3] * 200, 8, 2, 128, 128, 128),             # whole tiles only
+    ([0, 1, 0, 0, 90] * 340, 2, 1, 64, 16, 200),     # more sequences than a block has threads
+    ([0] * 1500 + [33] * 3, 5, 1, 128, 8, 77),       # only the last ones have keys of their own
 ]
 CASES = FEW + MANY
 

@@ -566,12 +566,13 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
 
 // ------------------------------------------------------------------------------ shared prefix
 // Where a batch's tiles of the prefix, and two a row for its own keys and its end, are few, the decoding kernel itself reads the
-// prefix's pages for each sequence: one or two kernels instead of three.  us a call in a graph, d = 128, 8 K/V heads, again / shared:
-// 2 sequences of 16,384 shared keys (2,080 tiles) 24.0 / 28.0;  16 of 2,000 (2,256) 21.9 / 21.7;  64 of 200 (1,824) 21.8 / 24.1;
-// 4 of 16,384 (4,160) 36.3 / 30.3;  64 of 600 (3,430) 31.0 / 23.9;  256 of 32 (4,608) 45 / 36.
+// prefix's pages for each sequence: one or two kernels instead of three.  us a call in a graph, d = 128, again / shared:
+// 16 sequences of 600 shared keys, 8 K/V heads (896 tiles) 10.1 / 23.0;  64 of 200 (2,048) 21.6 / 27.3;  16 of 2,000 (2,304)
+// 22.4 / 24.6;  2 of 20,000 (2,544) 26.3 / 29.5;  4 of 10,000 (2,592) 25.3 / 24.9;  64 of 5,000, one K/V head (2,688)
+// 25.6 / 23.0;  64 of 600 (3,584) 30.6 / 27.3;  4 of 16,384 (4,160) 35.6 / 28.9;  256 of 32 (6,144) 44.3 / 29.6.
 bool prefix_again(const attn_decode_args_t& a, int64_t prefix_len, int sms) {
     const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
-    return a.B == 1 || rows * (cdiv(prefix_len, kDecTile) + 2) <= 14 * sms;
+    return a.B == 1 || rows * (cdiv(prefix_len, kDecTile) + 2) <= 17 * sms;
 }
 
 // How the prefix's kernel divides: row blocks, and a line of steps over the CTAs.

@@ -81,8 +81,15 @@ class Batch:
             assert np.all(np.abs(lse[b] - ref_lse) <= 2.0 ** -14 * (1 + np.abs(ref_lse)) + 2.0 ** -12), b
 
 
-# The rule that sends a call to the decoding kernel alone goes by sequences * K/V heads * (tiles of the prefix + 2) against 14
-# an SM (2,128 on 152): "few" cases are below it, the others above.
+def alone(x):
+    """Whether the rule sends a call to the decoding kernel alone: by sequences * K/V heads * (tiles of the prefix + 2) against 17 an SM
+    (2,584 on 152)."""
+    group, B = x.H // x.Hkv, len(x.lens)
+    rows = B * x.Hkv * -(-group // (8 if group <= 8 else 16 if group <= 16 else 32))
+    return B == 1 or rows * (-(-x.prefix // 128) + 2) <= 17 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+# "few" cases go to the decoding kernel alone, "many" to the shared prefix's kernels
 FEW = [  # own keys, H, Hkv, d, page, prefix
     ([1], 8, 8, 128, 16, 1),
     ([0], 4, 2, 64, 16, 40),
@@ -97,17 +104,17 @@ MANY = [
     ([2, 0, 40, 1] * 32, 8, 8, 128, 16, 1),          # 128 rows against one key
     ([1] * 128, 8, 8, 64, 7, 129),
     ([0] * 128, 8, 8, 128, 24, 257),                 # no own keys; an odd number of tiles
-    ([3, 300] * 8, 64, 8, 128, 100, 2100),
+    ([3, 300] * 9, 64, 8, 128, 100, 2100),
     ([5] * 15, 64, 8, 128, 1, 2500),                 # a page a key
     ([1, 2, 0], 8, 8, 128, 512, 14000),              # three rows of many parts
-    ([64, 1] * 20, 12, 12, 128, 3, 300),
+    ([64, 1] * 22, 12, 12, 128, 3, 300),
     ([2, 300] * 16 + [9], 32, 8, 128, 256, 1000),    # 132 rows: two tiles of them
     ([1, 40, 0, 17] * 13, 40, 8, 128, 24, 2500),     # 260: a second block of rows
     ([7] * 60, 71, 1, 64, 100, 3000),
     ([11, 500] * 7, 142, 2, 128, 64, 6000),
     ([300, 1] * 150, 4, 1, 64, 16, 900),
-    ([1, 0, 130] * 250, 3, 1, 128, 48, 1),
-    ([0, 3] * 200, 8, 2, 128, 128, 128),             # whole tiles only
+    ([1, 0, 130] * 300, 3, 1, 128, 48, 1),
+    ([0, 3] * 220, 8, 2, 128, 128, 128),             # whole tiles only
     ([0, 1, 0, 0, 90] * 340, 2, 1, 64, 16, 200),     # more sequences than a block has threads
     ([0] * 1500 + [33] * 3, 5, 1, 128, 8, 77),       # only the last ones have keys of their own
 ]
@@ -117,6 +124,7 @@ CASES = FEW + MANY
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "B%d_H%d_%d_d%d_p%d_%d" % (len(c[0]), *c[1:]))
 def test_against_plain_attention(attn, case):
     x = Batch(*case, seed=len(case[0]) + case[5], scale=2.0)
+    assert alone(x) == (case in FEW)
     got = x.call(attn)
     assert attn.cache_device_status() == (0, 0)
     B = len(case[0])
@@ -141,6 +149,7 @@ def test_random_shapes(attn, seed):
 @pytest.mark.parametrize("mode", ["rtna", "rtz"])
 def test_rounding_modes(attn, mode, times):
     x = Batch([10, 90, 3] * times, 16, 4, 128, 16, 2000, seed=4)
+    assert alone(x) == (times == 1)
     near, other = x.call(attn), x.call(attn, round=mode)
     x.check(other, rows=[0, 1, 2], out=2.0 ** -8 if mode == "rtna" else 2.0 ** -7)
     step = (other[0].view(torch.int16).int() - near[0].view(torch.int16).int()).abs()
@@ -151,6 +160,7 @@ def test_rounding_modes(attn, mode, times):
 def test_equals_the_plain_decoding_call_where_pages_are_shared(attn, times):
     """The same caches through attn_paged_decode, whose rows name the prefix's pages too."""
     x = Batch([40, 0, 200, 7] * times, 32, 8, 128, 16, 960, seed=9, scale=2.0)
+    assert alone(x) == (times == 1)
     got = x.call(attn)
     table = x.table.clone()
     table[:, :60] = table[0, :60]
@@ -161,10 +171,11 @@ def test_equals_the_plain_decoding_call_where_pages_are_shared(attn, times):
     assert torch.equal(attn.attn_paged_prefix_decode(x.q, x.k, x.v, x.lens, table, 960), got[0])
 
 
-@pytest.mark.parametrize("rows", [4, 600])
+@pytest.mark.parametrize("rows", [4, 700])
 def test_non_finite_keys_and_values(attn, rows):
     """Of the prefix and of own keys, as in attn_paged_decode: the same classes of outputs."""
     x = Batch([50, 3, 0, 20] * (rows // 4) + [8] * (rows % 4), 8, 1, 128, 16, 160, seed=rows)
+    assert alone(x) == (rows == 4)
     k, v = x.k.flatten(0, 1), x.v.flatten(0, 1)
     page = x.table[0].cpu()
 
@@ -191,6 +202,7 @@ def test_non_finite_keys_and_values(attn, rows):
 def test_infinite_values_under_vanishing_weights(attn, times):
     """A finite logit weighs something, however small: an infinite value stays infinite."""
     x = Batch([3, 20] * times, 4, 1, 64, 16, 200, seed=5)
+    assert alone(x) == (times == 1)
     x.q.fill_(4.0)
     k, v = x.k.flatten(0, 1), x.v.flatten(0, 1)
     k[int(x.table[0, 2]) * 16 + 1] = 64.0            # stands far out: every other weight underflows
@@ -200,18 +212,20 @@ def test_infinite_values_under_vanishing_weights(attn, times):
     assert torch.isposinf(got[:, :, 5]).all() and got[:, :, :5].isfinite().all()
 
 
-@pytest.mark.parametrize("times", [1, 100])
+@pytest.mark.parametrize("times", [1, 120])
 def test_all_logits_minus_infinity(attn, times):
     x = Batch([3, 0, 20] * times, 4, 2, 128, 16, 150, seed=5)
+    assert alone(x) == (times == 1)
     x.q.fill_(1.0)
     x.k.fill_(float("-inf"))
     o, lse = x.call(attn)
     assert o.isnan().all() and torch.isneginf(lse).all()
 
 
-@pytest.mark.parametrize("B,prefix", [(5, 96), (40, 2000)])
+@pytest.mark.parametrize("B,prefix", [(5, 96), (100, 2000)])
 def test_sequences_that_have_ended(attn, B, prefix):
     x = Batch([30, 4, 200, 9, 1] + [3] * (B - 5), 8, 2, 128, 16, prefix, seed=2)
+    assert alone(x) == (B == 5)
     x.lens[[0, 3]] = 0
     o, lse = x.call(attn)
     assert attn.cache_device_status() == (0, 0)
@@ -221,7 +235,7 @@ def test_sequences_that_have_ended(attn, B, prefix):
 
 def many(own, H, Hkv, d, page, prefix, seed=0):
     """A batch that is too large for the decoding kernel alone."""
-    return Batch(own + [2] * 36, H, Hkv, d, page, prefix, seed=seed)
+    return Batch(own + [2] * 95, H, Hkv, d, page, prefix, seed=seed)
 
 
 @pytest.mark.parametrize("make", [Batch, many])
@@ -231,6 +245,7 @@ def test_bad_lengths_and_pages_leave_their_rows(attn, make):
         x.call(attn, o=o, lse=lse)
         return o, lse
     x = make([30, 4, 200, 9, 0], 8, 2, 128, 16, 5 * 16 if make is Batch else 2000, seed=2)
+    assert alone(x) == (make is Batch)
     room = x.table.shape[1] * 16
     for length in (x.prefix - 1, -1, 1, room + 1, 2 ** 31 - 1):
         kept = int(x.lens[2])
@@ -255,6 +270,7 @@ def test_bad_lengths_and_pages_leave_their_rows(attn, make):
 
 def test_stays_in_bounds_with_the_caller_s_workspace(attn):
     x = Batch([30, 4, 700] * 40, 10, 2, 128, 24, 1111, seed=2)
+    assert not alone(x)
     want = x.call(attn)
     a = attn.DecodeArgs()
     a.B, a.H, a.Hkv, a.num_pages, a.page_size, a.max_pages, a.d = 120, 10, 2, len(x.k), 24, x.table.shape[1], 128
@@ -276,6 +292,7 @@ def test_stays_in_bounds_with_the_caller_s_workspace(attn):
 def test_rows_past_2_to_the_32_bytes(attn, times):
     """A cache of 5 GB, its pages at the far end."""
     x = Batch([30, 4, 200] * times, 8, 8, 128, 128, 700, seed=3)
+    assert alone(x) == (times == 1)
     far = 2_400_000 // 128
     k, v = (torch.zeros((far + len(x.k), 128, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     k[far:], v[far:] = x.k, x.v
@@ -289,6 +306,7 @@ def test_rows_past_2_to_the_32_bytes(attn, times):
 def test_captured_while_lengths_grow(attn, times, prefix):
     B, cut = 3 * times, prefix // 16
     x = Batch([1, 30, 4] * times, 8, 2, 128, 16, prefix, seed=7, spare=3)
+    assert alone(x) == (times == 1)
     t = torch.arange(len(x.k), dtype=torch.int32)
     x.table[:, cut:] = t[cut:cut + B * (x.table.shape[1] - cut)].view(B, -1).cuda()
     x.table[0, :cut] = t[:cut].cuda()

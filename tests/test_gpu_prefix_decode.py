@@ -238,7 +238,12 @@ def many(own, H, Hkv, d, page, prefix, seed=0):
     return Batch(own + [2] * 95, H, Hkv, d, page, prefix, seed=seed)
 
 
-@pytest.mark.parametrize("make", [Batch, many])
+def far(own, H, Hkv, d, page, prefix, seed=0):
+    """One tile of rows behind a long prefix."""
+    return Batch(own + [2] * 25, H, Hkv, d, page, 6 * prefix, seed=seed)
+
+
+@pytest.mark.parametrize("make", [Batch, many, far])
 def test_bad_lengths_and_pages_leave_their_rows(attn, make):
     def run(x, **kw):
         o, lse = torch.full_like(x.q, 7.0), torch.full((len(x.lens), x.H), 7.0, device="cuda")
@@ -262,10 +267,15 @@ def test_bad_lengths_and_pages_leave_their_rows(attn, make):
         assert attn.cache_device_status() == (1, 22) and (o[2] == 7).all() and (lse[2] == 7).all()
         x.table[2, at] = kept
         x.check((o, lse), rows=[0, 1, 3, 4])
-    for page in (len(x.k), -1, -2 ** 31):            # of the prefix: nobody's outputs are written
-        x.table[0, 2] = page
+    last = x.prefix // 16 - 1
+    for at, page in ((2, len(x.k)), (last, -1), (2, -2 ** 31), (last, 2 ** 31 - 1)):      # of the prefix: nobody's outputs are written
+        kept = int(x.table[0, at])
+        x.table[0, at] = page
         o, lse = run(x)
         assert attn.cache_device_status() == (1, 26) and (o == 7).all() and (lse == 7).all()
+        x.table[0, at] = kept
+    x.check(run(x), rows=[0, 1, 2, 3, 4])
+    assert attn.cache_device_status() == (0, 0)
 
 
 def test_stays_in_bounds_with_the_caller_s_workspace(attn):

@@ -19,8 +19,9 @@
 //   more than 128 rows: two tiles of rows against one tile of keys;
 //   128 rows and fewer (kSingle): one tile of rows against two tiles of keys, even and odd ones, which keep
 //   an m, l and O each.
-// P is rounded to bf16 for the second product (tcgen05 takes it in that type from TMEM; a second product
-// with its lower bits, as in decode.cuh, would double the work that bounds the kernel), l sums the unrounded weights.
+// P goes to the second product as two bf16 parts, as in decode.cuh (an error of 2^-16, so that a sequence's outputs are as exact
+// whichever kernels its batch's size chooses): both fit where S was, and the products are half as many again.  l sums
+// the unrounded weights.
 //
 // Loads.  Three or six warps copy keys and values with cp.async, row by row, into the 128-byte-swizzled tiles that the tensor pipe
 // reads: any page size, any number of heads, no tensor maps to make on the host (TMA boxes of a page's rows reach the
@@ -76,7 +77,7 @@ struct PfGeo {
     // or with one tile of rows, where HBM bounds, six in a block of 512 threads (24 sequences of 32 heads, 65,500 keys: 69.3 us,
     // with three 76.5; but 64 sequences, 16,384 keys, two tiles of rows: 60.6, with three 58.4).
     static constexpr int kLoaders = kSingle ? 6 : 3, kThreads = kSingle ? 512 : 384;
-    static constexpr uint32_t kRegsSoftmax = 208, kRegsOther = kSingle ? 48 : 88;
+    static constexpr uint32_t kRegsSoftmax = kSingle ? 160 : 176, kRegsOther = kSingle ? 96 : 128;
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= 65536 / kThreads / 8 * 8 * kThreads, "more registers than at launch");
     static constexpr int kTileBytes = kPfTile * D * 2;
     static constexpr int kQTiles = kSingle ? 1 : 2;
@@ -129,6 +130,22 @@ __device__ __forceinline__ void pf_arrive_landed(uint32_t bar) {
 // where chunk c (16 bytes) of row r is in a tile
 __device__ __forceinline__ uint32_t pf_chunk(int r, int c) {
     return (uint32_t)((c >> 3) * kPfBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Two weights y (0, 2^-100 or more, or NaN) as bf16 parts: hi the upper 8 bits of y (1 - 2^-16), cut off, lo what is left of y, rounded.
+// So the lower part of a positive weight is positive too, and an infinite value stays infinite under it.
+__device__ __forceinline__ void pf_parts(float2 y, uint32_t& hi, uint32_t& lo) {
+    const float2 z = __fmul2_rn(y, make_float2(1.0f - 0x1p-16f, 1.0f - 0x1p-16f));
+    hi = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
+    float x0, x1;                  // y - hi, exact
+    asm("{\n\t.reg .b16 a, b, m;\n\t"
+        "mov.b32 {a, b}, %4;\n\t"
+        "mov.b16 m, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, a, m, %2;\n\t"
+        "fma.rn.f32.bf16 %1, b, m, %3;\n\t}"
+        : "=f"(x0), "=f"(x1)
+        : "f"(y.x), "f"(y.y), "r"(hi));
+    lo = ptx::pack_bf16x2(x0, x1);
 }
 
 // A CTA's share of a unit: steps j0 .. j1 - 1.  Units of one K/V head are neighbours, row block by row block.
@@ -347,8 +364,11 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
                 const uint64_t b0 = dv + (uint64_t)((slot * G::kTileBytes) >> 4);
                 const uint32_t d = tmem + 256u + (uint32_t)(D * t), a = tmem + 128u * t, acc0 = first ? 0u : 1u;
 #pragma unroll
-                for (int kk = 0; kk < kPfTile / 16; ++kk)
-                    ptx::mma_ts(d, a + (uint32_t)kk * 8u, b0 + (uint64_t)((kk * 2048) >> 4), idesc_o, kk > 0 ? 1u : acc0);
+                for (int kk = 0; kk < 2 * (kPfTile / 16); ++kk) {  // upper parts, then lower ones: of 32 keys 16 columns each, side by side
+                    const int k = kk & 7;
+                    ptx::mma_ts(d, a + (uint32_t)((k >> 1) * 32 + (kk >> 3) * 16 + (k & 1) * 8), b0 + (uint64_t)((k * 2048) >> 4), idesc_o,
+                                kk > 0 ? 1u : acc0);
+                }
             };
             uint32_t pos = 0, count = 0;                           // loads, and steps, before this share
             bool ok = true;
@@ -418,6 +438,10 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_off + 128u * t, tO = tmem + lane_off + 256u + (uint32_t)(D * t);
         const float c = p.scale_log2, tau = 8.0f;                  // a reference may lag by 2^8
+        // A tile's logits are read from TMEM twice, a piece at a time in short loops: for their maximum, then for the weights, which
+        // go where they were.  (Unrolled over all 128 the step was longer than the schedulers' instruction caches and waited for its
+        // code: 24 sequences of 32 heads, 65,500 keys: 64 us, unrolled 79; 512 of 40, 4,133: 111 and 113.)
+        constexpr int kLook = kSingle ? 32 : 64;                   // columns of a piece for the maximum
         uint32_t count = 0;                                        // steps before this share
         bool ok = true;
 #pragma unroll 1
@@ -441,29 +465,31 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
                 ok = pf_wait(bar(G::kSFull + t), count & 1u, abort_flag, lim);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 ptx::tc_fence_after();
-                uint32_t s[128];
-                ptx::tmem_ld128(tS, s);
                 const int valid = p.prefix_len - tile_of(j, t) * kPfTile;      // keys of the tile (the same for every row)
-                if (valid < kPfTile) {
-#pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e >= valid) s[e] = __float_as_uint(-INFINITY);
-                }
                 float mxa[4], mna[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mxa[i] = mna[i] = __uint_as_float(s[i]);
+                for (int i = 0; i < 4; ++i) {
+                    mxa[i] = -INFINITY;
+                    mna[i] = INFINITY;
+                }
+#pragma unroll 1
+                for (int ch = 0; ch < kPfTile / kLook; ++ch) {
+                    uint32_t s[kLook];
+                    if constexpr (kLook == 32) ptx::tmem_ld32(tS + kLook * ch, s);
+                    else ptx::tmem_ld64(tS + kLook * ch, s);
+                    if (valid < kPfTile) {
 #pragma unroll
-                for (int e = 4; e < 124; e += 8)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = __uint_as_float(s[e + i]), b = __uint_as_float(s[e + 4 + i]);
-                        mxa[i] = ptx::fmax3(mxa[i], a, b);
-                        mna[i] = ptx::fmin3(mna[i], a, b);
+                        for (int e = 0; e < kLook; ++e)
+                            if (kLook * ch + e >= valid) s[e] = __float_as_uint(-INFINITY);
                     }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mxa[i] = fmaxf(mxa[i], __uint_as_float(s[124 + i]));
-                    mna[i] = fminf(mna[i], __uint_as_float(s[124 + i]));
+                    for (int e = 0; e < kLook; e += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float a = __uint_as_float(s[e + i]), b = __uint_as_float(s[e + 4 + i]);
+                            mxa[i] = ptx::fmax3(mxa[i], a, b);
+                            mna[i] = ptx::fmin3(mna[i], a, b);
+                        }
                 }
                 const float mx = ptx::fmax3(mxa[0], mxa[1], fmaxf(mxa[2], mxa[3]));
                 const float mn = ptx::fmin3(mna[0], mna[1], fminf(mna[2], mna[3]));
@@ -476,31 +502,34 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
                     m = mx;
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                // no exponent so low that its weight would need weight_of's lower bound, none of -inf
-                const bool plain = mn > -INFINITY && (mn - ref) * c >= -125.0f;
-                const float2 c2 = make_float2(c, c), nm2 = make_float2(-ref, -ref);
+                // Plain: no logit of -inf, which weighs 0, none so low that its weight would need the lower bound of 2^-100 (a finite logit
+                // weighs something, and both parts of its weight are normal numbers), and a reference of 2^10 at most: then
+                // (s - ref) c is one fma with ref * c rounded, which takes every weight by the same 2^-15 of an exponent or less.
+                const bool plain = __all_sync(0xFFFFFFFFu, mn > -INFINITY && (mn - ref) * c >= -100.0f && fabsf(ref) * c <= 1024.0f);
+                const float least = ref - 100.0f / c, minus = plain ? -ref * c : 0.0f;
+                const float2 c2 = make_float2(c, c), minus2 = make_float2(minus, minus);
                 float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t pk[64];
-                if (__all_sync(0xFFFFFFFFu, plain)) {
+#pragma unroll 1
+                for (int ch = 0; ch < kPfTile / 32; ++ch) {
+                    uint32_t s[32], hi[16], lo[16];
+                    ptx::tmem_ld32(tS + 32 * ch, s);
+                    if (!plain) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        const float2 x = __fmul2_rn(
-                            __fadd2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), nm2), c2);
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = 32 * ch + e < valid ? __uint_as_float(s[e]) : -INFINITY;
+                            s[e] = __float_as_uint(x == -INFINITY ? x : ptx::fmax_nan(x, least) - ref);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, minus2);
                         const float2 y = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));
                         sum[e & 3] = __fadd2_rn(sum[e & 3], y);
-                        pk[e] = ptx::pack_bf16x2(y.x, y.y);
+                        pf_parts(y, hi[e], lo[e]);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        const float y0 = weight_of(__uint_as_float(s[2 * e]), ref, c);
-                        const float y1 = weight_of(__uint_as_float(s[2 * e + 1]), ref, c);
-                        sum[e & 3] = __fadd2_rn(sum[e & 3], make_float2(y0, y1));
-                        pk[e] = ptx::pack_bf16x2(y0, y1);
-                    }
+                    ptx::tmem_st16(tS + 32 * ch, hi);
+                    ptx::tmem_st16(tS + 32 * ch + 16, lo);
                 }
-                ptx::tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-                ptx::tmem_st32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
                 const float2 ls = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l += ls.x + ls.y;
                 if (__any_sync(0xFFFFFFFFu, rescale_o)) {

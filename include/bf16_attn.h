@@ -757,9 +757,8 @@ int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
  *                    like a bad page of its own; a bad page of the prefix leaves the outputs of all sequences with keys unwritten
  *                    (ATTN_CACHE_SITE_PREFIX).  Sequence 0's row names the prefix's pages even when its length is 0, the page
  *                    that the prefix ends in among them: with attn_paged_reserve, shared_pages[0] counts that page too
- * Where the prefix is shared by kernels of its own, its keys' softmax weights are rounded to bf16 before the product with the values,
- * as in attn_fwd; a short prefix, or one sequence, goes to attn_paged_decode's kernel (by the sizes alone).  H at most 65535.  Results are
- * bitwise reproducible for the same lengths and shapes on the same GPU model.  workspace: caller device memory of at least
+ * A short prefix, or one sequence, goes to attn_paged_decode's kernel, others to kernels of their own (by the sizes alone); the softmax
+ * weights go to the product with the values to 2^-16 in both.  H at most 65535.  Results are bitwise reproducible for the same lengths and shapes on the same GPU model.  workspace: caller device memory of at least
  * attn_paged_prefix_decode_workspace_size() bytes, 16-byte aligned.
  */
 size_t attn_paged_prefix_decode_workspace_size(const attn_decode_args_t* args, int64_t prefix_len);

@@ -30,7 +30,8 @@ EXPORTS = ("attn_fwd", "attn_fwd_ws", "attn_fwd_noalloc", "attn_fwd_ex", "attn_f
            "attn_rope", "attn_paged_append", "attn_paged_decode", "attn_paged_decode_workspace_size",
            "attn_paged_evict", "attn_paged_evict_workspace_size", "attn_norm_rope", "attn_norm_rope_bwd",
            "attn_norm_rope_bwd_workspace_size", "attn_norm_rope_append", "attn_paged_reserve",
-           "attn_paged_prefix_decode", "attn_paged_prefix_decode_workspace_size", "attn_cache_get_device_status")
+           "attn_paged_prefix_decode", "attn_paged_prefix_decode_ex", "attn_paged_prefix_decode_workspace_size",
+           "attn_cache_get_device_status")
 
 
 class AttnError(RuntimeError):
@@ -239,6 +240,8 @@ def load(path: str | None = None):
             getattr(lib, name + "_workspace_size").argtypes = [vp]
         lib.attn_paged_prefix_decode.restype = i32
         lib.attn_paged_prefix_decode.argtypes = [vp, i64, vp, ctypes.c_size_t, vp]
+        lib.attn_paged_prefix_decode_ex.restype = i32
+        lib.attn_paged_prefix_decode_ex.argtypes = [vp, i64, ctypes.c_uint32, ctypes.c_uint32, vp, ctypes.c_size_t, vp]
         lib.attn_paged_prefix_decode_workspace_size.restype = ctypes.c_size_t
         lib.attn_paged_prefix_decode_workspace_size.argtypes = [vp, i64]
         lib.attn_cache_get_device_status.restype = i32
@@ -1048,7 +1051,8 @@ def _prefix_workspace_bytes(index, prefix_len, *shape):
 
 
 def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix_len: int, o=None, lse=None,
-                             round: str = "rtne", return_lse: bool = False, stream=None, workspace=None):
+                             round: str = "rtne", return_lse: bool = False, stream=None, workspace=None, wait_limit_ms: int = 0,
+                             test_hooks: int = 0):
     """:func:`attn_paged_decode` for a batch whose sequences all begin with the same ``prefix_len`` keys (one instruction,
     one document): those are read once for the whole batch, through ``block_table``'s first row.
 
@@ -1057,7 +1061,9 @@ def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix
     prefix are not read, but in the first row, which names them whatever its own length is).
     A sequence with another length or a bad page of its own is not written and is reported by
     :func:`cache_device_status`; a bad page of the prefix leaves every sequence unwritten.  ``workspace``: optional caller tensor
-    (calls that may run at the same time need one each).  Returns ``o`` or ``(o, lse)`` (lse fp32 [B, H])."""
+    (calls that may run at the same time need one each).  ``wait_limit_ms`` bounds each wait in the kernels (0: 2000 ms; rows that
+    an expired one cut off are not written, and :func:`cache_device_status` reports it); ``test_hooks`` is 0 for normal use (1 makes
+    one wait run out).  Returns ``o`` or ``(o, lse)`` (lse fp32 [B, H])."""
     import torch
     dev, pages, ps, Hkv, d, B, most, H = _check_decode(q, k_cache, v_cache, seqlens_k, block_table, o, lse, round)
     prefix_len, ws_bytes = int(prefix_len), 0
@@ -1081,8 +1087,9 @@ def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix
                                                ("page_size", ps), ("max_pages", most), ("d", d))
             if ws_bytes:
                 workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        st = (_lib or load()).attn_paged_prefix_decode(a, prefix_len, workspace.data_ptr() if ws_bytes else None, ws_bytes,
-                                                       torch._C._cuda_getCurrentRawStream(dev))
+        st = (_lib or load()).attn_paged_prefix_decode_ex(a, prefix_len, wait_limit_ms, test_hooks,
+                                                          workspace.data_ptr() if ws_bytes else None, ws_bytes,
+                                                          torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise AttnError(st, "attn_paged_prefix_decode")
     finally:

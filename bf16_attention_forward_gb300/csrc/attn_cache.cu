@@ -631,10 +631,11 @@ int launch_prefix(const PrefixParams& p, int64_t ctas, cudaStream_t stream) {
     return launch(attn_prefix_kernel<D, kSingle>, ctas, 1, PfGeo<D, kSingle>::kThreads, PfGeo<D, kSingle>::kSmem, stream, p);
 }
 
-int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* workspace, size_t workspace_bytes,
-                      cudaStream_t stream) {
+int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, uint32_t wait_limit_ms, uint32_t test_hooks, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
     int st = check_prefix_shape(a, prefix_len);
     if (st != ATTN_OK) return st;
+    if (test_hooks != 0 && test_hooks != ATTN_TEST_WITHHOLD_O_READY) return ATTN_ERR_INVALID_ARG;
     if ((st = check_decode_tensors(a)) != ATTN_OK) return st;
     int sms = 0;
     if ((st = device(&sms)) != ATTN_OK) return st;
@@ -684,7 +685,8 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, void* wor
     x.scale_log2 = j.s.scale_log2;
     x.part_o = reinterpret_cast<float*>(ws + l.x_o);
     x.part_ml = reinterpret_cast<float2*>(ws + l.x_ml);
-    x.wait_limit_ns = 2000000000ull;
+    x.wait_limit_ns = (wait_limit_ms ? wait_limit_ms : 2000u) * 1000000ull;
+    x.test_hooks = (int)test_hooks;
     j.single = plan.single;
     // several warps a row where a row has more parts than a warp has in flight, while the SMs have room (16 warps each):
     // every warp has the same arithmetic to begin with (with 40: 71.3 us for 68.0 of 768 rows with 40 parts, 61.0 for 57.9 of 2,048 with 20)
@@ -1169,7 +1171,13 @@ size_t attn_paged_prefix_decode_workspace_size(const attn_decode_args_t* args, i
 
 int attn_paged_prefix_decode(const attn_decode_args_t* args, int64_t prefix_len, void* workspace, size_t workspace_bytes,
                              attn_stream_t stream) {
-    return args ? run_prefix_decode(*args, prefix_len, workspace, workspace_bytes, (cudaStream_t)stream) : ATTN_ERR_INVALID_ARG;
+    return attn_paged_prefix_decode_ex(args, prefix_len, 0, 0, workspace, workspace_bytes, stream);
+}
+
+int attn_paged_prefix_decode_ex(const attn_decode_args_t* args, int64_t prefix_len, uint32_t wait_limit_ms, uint32_t test_hooks,
+                                void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+    return args ? run_prefix_decode(*args, prefix_len, wait_limit_ms, test_hooks, workspace, workspace_bytes, (cudaStream_t)stream)
+                : ATTN_ERR_INVALID_ARG;
 }
 
 int attn_cache_get_device_status(attn_stream_t stream, int32_t* site) {

@@ -57,8 +57,9 @@ struct PrefixParams {
     int slots;                     // parts that a CTA may leave
     float scale_log2;              // log2(e) / sqrt(d)
     float* part_o;                 // [ctas][slots][2][128][d]
-    float2* part_ml;               // [ctas][slots][2][128]: (m in logits, l); l = -1: a bad page
+    float2* part_ml;               // [ctas][slots][2][128]: (m in logits, l); l = -1: a bad page, or an expired wait
     unsigned long long wait_limit_ns;
+    int test_hooks;                // ATTN_TEST_WITHHOLD_O_READY: CTA 0 skips its first share's output-ready signal of tile 0
     // the line has fewer than 2^30 places (the host checks)
     __device__ __forceinline__ int start(int c) const { return per * c + min(c, more); }
     __device__ __forceinline__ int cta_of(int u) const {
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
                         if (!ok) break;
                         ptx::tc_fence_after();
                         issue_o(t, vs, jj == 0);
-                        if (!more) ptx::mma_commit(bar(G::kOFull + t));
+                        if (!more && !(p.test_hooks && n == 0 && t == 0 && blockIdx.x == 0)) ptx::mma_commit(bar(G::kOFull + t));
                         if (kSingle || t == 1) release(vt);
                         if (more) {
                             const uint32_t ks = kSingle || t == 0 ? landed(kt) : kt % G::kStages;
@@ -445,12 +446,12 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
         uint32_t count = 0;                                        // steps before this share
         bool ok = true;
 #pragma unroll 1
-        for (uint32_t n = 0; ok && walk.next(p, w); ++n) {
+        for (uint32_t n = 0; walk.next(p, w); ++n) {               // (once a wait has given up: only to mark the parts that are owed)
         const int at = w.rb * (kSingle ? kPfTile : 2 * kPfTile) + (kSingle ? row : t * kPfTile + row);
         // warps without a row keep every wait and arrival, and skip the rest: a row is its own lane of TMEM
         const bool live = at - lane < p.rows;
         float m = -INFINITY, l = 0.0f;
-        if (!live) {
+        if (ok && !live) {
 #pragma unroll 1
             for (int j = w.j0; j < w.j1; ++j, ++count) {
                 ok = pf_wait(bar(G::kSFull + t), count & 1u, abort_flag, lim);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(bar(G::kPFull + t));
             }
-        } else {
+        } else if (ok) {
 #pragma unroll 1
             for (int j = w.j0; j < w.j1; ++j, ++count) {
                 ok = pf_wait(bar(G::kSFull + t), count & 1u, abort_flag, lim);
@@ -553,16 +554,19 @@ __global__ void __launch_bounds__(PfGeo<D, kSingle>::kThreads, 1) attn_prefix_ke
                 ptx::mbar_arrive(bar(G::kPFull + t));
             }
         }
-        if (!ok) break;
-        ok = pf_wait(bar(G::kOFull + t), n & 1u, abort_flag, lim);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        ptx::tc_fence_after();
+        ok = ok && pf_wait(bar(G::kOFull + t), n & 1u, abort_flag, lim);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!live) continue;
         // the warp's 32 rows, 32 columns at a time, through its room: each store then takes four whole 128-byte lines
         // (a thread's own row in 16-byte pieces took 4 us more)
         const long long part0 = (((long long)blockIdx.x * p.slots + n) * 2 + t) * kPfTile + quarter * 32;
         const uint32_t room = sbase + (uint32_t)(G::kRoom + warp * 4096);
         const int rows = min(32, p.rows - (at - lane));
+        if (!ok) {                     // a part that is not there: the join leaves its rows unwritten
+            if (lane < rows) p.part_ml[part0 + lane] = make_float2(-INFINITY, kBadPart);
+            continue;
+        }
+        ptx::tc_fence_after();
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t o[32];

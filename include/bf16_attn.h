@@ -471,7 +471,8 @@ int attn_bwd_varlen(const attn_bwd_varlen_args_t* args, void* workspace, size_t 
 #define ATTN_CACHE_SITE_EVICT 23    /* a bad length, or of a sequence to be cut a bad page or one used twice: it stays */
 #define ATTN_CACHE_SITE_SLOTS 24    /* a slot outside the cache (other than -1): k, v not written               */
 #define ATTN_CACHE_SITE_RESERVE 25  /* bad lengths, offsets, counts, or too few free pages: nothing is reserved */
-#define ATTN_CACHE_SITE_PREFIX 26   /* a bad page of the shared prefix (or a wait that expired): no outputs     */
+#define ATTN_CACHE_SITE_PREFIX 26   /* a bad page of the shared prefix: no outputs; with ATTN_ERR_DEVICE_TIMEOUT: a wait
+                                       expired, and the rows that it cut off are not written                  */
 
 /* Which elements of a head form pair p of `pairs`: 2p and 2p + 1, or p and p + pairs. */
 typedef enum { ATTN_ROPE_ADJACENT = 0, ATTN_ROPE_HALVES = 1 } attn_rope_pairing_t;
@@ -764,6 +765,16 @@ int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
 size_t attn_paged_prefix_decode_workspace_size(const attn_decode_args_t* args, int64_t prefix_len);
 int attn_paged_prefix_decode(const attn_decode_args_t* args, int64_t prefix_len, void* workspace, size_t workspace_bytes,
                              attn_stream_t stream);
+
+/*
+ * attn_paged_prefix_decode_ex -- the same with the bound on any single wait inside the kernels and the hook that makes one run out.
+ *   wait_limit_ms  0: 2000 ms.  A wait that expires is reported as ATTN_ERR_DEVICE_TIMEOUT at ATTN_CACHE_SITE_PREFIX; rows that lack
+ *                  a part of the prefix because of it are not written
+ *   test_hooks     0 for normal use; ATTN_TEST_WITHHOLD_O_READY makes the first CTA of the prefix's kernel skip one signal that its output
+ *                  accumulator is complete, so that the wait for it expires.  (A call that goes to attn_paged_decode's kernel has no waits.)
+ */
+int attn_paged_prefix_decode_ex(const attn_decode_args_t* args, int64_t prefix_len, uint32_t wait_limit_ms, uint32_t test_hooks,
+                                void* workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /* Synchronize `stream`, then read and clear the current device's status word of these calls' kernels (all from attn_rope
  * on). */

@@ -5,7 +5,8 @@
 //   r = 1 / sqrt(sum x_i^2 / d + eps),  n = r x,  y = R(n * w),
 // R the rotation of rope.cuh (pair p by pos[axis[p]] * freq[p]).  Of the gradient dy, with g = R^T dy:
 //   dw = sum over heads and tokens of g * n,  dx = r (g * w - n (sum (g * w)_i n_i) / d).
-// All of it in fp32, y and dx rounded once.  (The squares' sum is fp32 too: elements past 10^19 overflow it, r is 0.)
+// All of it in fp32, y and dx rounded once.  (The squares' sum is fp32 too: elements past 10^18 may overflow it, then r is 0 and
+// so are n, y and dx.  Squares that underflow are taken of 2^80 x.)
 //
 // Bound: HBM bytes; x read and y written once (backward: x and dy read, dx written).  A warp takes a token, whose angles it
 // computes once; D / 16 lanes take a head, 16 elements each (two 16-byte chunks, so that a pair's elements meet in one thread),
@@ -215,6 +216,23 @@ __device__ __forceinline__ float head_dot(const float2 (&x)[8], const float2 (&y
     for (int off = 1; off < kL; off <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
     return v;
 }
+// r of a head.  kSmall: where the mean and eps are below 2^-80, the squares may have underflowed: x comes back times `up` = 2^80 (else 1),
+// and so does 1 / r, whose squares then lie between 2^-106 and 2^94.  there: whether the head is one (others' numbers count for nothing).
+// Looked for only where eps allows such heads: the vote keeps the heads of a step from running side by side (32,760 tokens of 24
+// heads: 65.7 us, without 63.8).
+constexpr float kNormSmall = 0x1p-80f;
+template <int D, bool kSmall>
+__device__ __forceinline__ float head_root(float2 (&x)[8], float eps, bool there, float& up) {
+    float mean = head_dot<D / 16>(x, x) * (1.0f / D) + eps;
+    up = 1.0f;
+    if (kSmall && __any_sync(0xFFFFFFFFu, there && mean < kNormSmall)) {
+        up = mean < kNormSmall ? 0x1p80f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], make_float2(up, up));
+        mean = head_dot<D / 16>(x, x) * (1.0f / D) + eps * up * up;
+    }
+    return rsqrtf(mean);
+}
 // 16 bytes global -> shared
 __device__ __forceinline__ void cp_async16_plain(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -349,7 +367,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
                 place.take(cs[warp], c, sn);
                 place.factors(w, c, sn, A, B);
             }
-            auto heads = [&](auto all) {       // all: every word of the warp turns
+            auto heads = [&](auto all, auto small) {       // all: every word of the warp turns; small: see head_root
 #pragma unroll 1
                 for (int h = h0 + sub; h - sub < h1; h += kNormHeads * kSub) {
                     cp_async_wait<kNormStages - 2>();
@@ -366,12 +384,14 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
                         if (!kAppend || t < 2) {
                             float2 x[8], y[8];
                             unpack16(xa[u], xb[u], x);
-                            const float r = rsqrtf(head_dot<kL>(x, x) * (1.0f / D) + p.eps);
+                            float up;
+                            const float r = head_root<D, small.value>(x, p.eps, h + u * kSub < h1, up);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], both(r));      // (before the factors, which may be large)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 y[i] = __fmul2_rn(x[i], A[i]);
                                 if (all.value || place.turned(turns, i)) y[i] = __ffma2_rn(place.partners(x, i), B[i], y[i]);
-                                y[i] = __fmul2_rn(y[i], both(r));
                             }
                             pack16(y, xa[u], xb[u]);
                         }
@@ -383,8 +403,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
                     }
                 }
             };
-            if (all_turn) heads(std::true_type());
-            else heads(std::false_type());
+            if (p.eps < kNormSmall) heads(std::false_type(), std::true_type());
+            else if (all_turn) heads(std::true_type(), std::false_type());
+            else heads(std::false_type(), std::false_type());
         }
     }
     cp_async_wait<0>();
@@ -460,7 +481,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_b
         table.angles(p, at.b, at.s, cs[warp]);
         float c[8], sn[8];
         place.take(cs[warp], c, sn);
-        auto tensor = [&](int t, float2 (&dw)[8]) {
+        auto tensor = [&](int t, float2 (&dw)[8], auto small) {
             char* dst = p.x[t].dst + (long long)at.b * p.x[t].dst_b + (long long)at.s * p.x[t].dst_t + sub * p.x[t].dst_h;
             const long long step = kSub * p.x[t].dst_h;
             const int heads = p.x[t].heads;
@@ -472,8 +493,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_b
                 unpack16(ring[stage][2][threadIdx.x], ring[stage][3][threadIdx.x], g);
                 load(stage == 0 ? kNormBwdStages - 1 : stage - 1);     // (the stage read in the step before)
                 place.template turn<true>(g, c, sn, turns);
-                const float r = rsqrtf(head_dot<kL>(x, x) * (1.0f / D) + p.eps);
                 const bool there = h < heads;                          // (what an absent head's place holds is another's)
+                float up;
+                const float r = head_root<D, small.value>(x, p.eps, there, up);
                 weights16(w_s[t], place.ca, place.cb, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -485,6 +507,9 @@ __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_b
                 if (there) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) g[e] = __fmul2_rn(__ffma2_rn(x[e], both(-dot), g[e]), both(r));
+                    if (small.value && up != 1.0f)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) g[e] = __fmul2_rn(g[e], both(up));
                     uint4 oa, ob;
                     pack16(g, oa, ob);
                     *reinterpret_cast<uint4*>(dst + place.ca * 16) = oa;
@@ -494,12 +519,15 @@ __global__ void __launch_bounds__(kNormThreads, kNormBwdBlocks) attn_norm_rope_b
                 stage = stage + 1 == kNormBwdStages ? 0 : stage + 1;
             }
         };
-        tensor(0, dq);
+        const bool small = p.eps < kNormSmall;
+        if (small) tensor(0, dq, std::true_type());
+        else tensor(0, dq, std::false_type());
         if (p.x[1].heads > 0) {
             float2 dk[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) dk[e] = make_float2(0.0f, 0.0f);
-            tensor(1, dk);
+            if (small) tensor(1, dk, std::true_type());
+            else tensor(1, dk, std::false_type());
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float4 v = dk_s[i][threadIdx.x];

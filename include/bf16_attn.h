@@ -626,7 +626,8 @@ int attn_paged_evict(const attn_evict_args_t* args, void* workspace, size_t work
  *   q_weight, k_weight   [d], fp32 or bf16 (weight_bf16 = 1); NULL: ones
  *   eps           >= 0, finite
  *   pairs         0 .. d / 2; 0: no rotation, positions, freqs and axes are ignored (num_axes >= 1 all the same)
- * The squares are summed in fp32: heads with elements past about 10^19 come out zero (NaN where they are infinite).
+ * The squares are summed in fp32: a head whose sum overflows (elements past about 10^18) comes out zero, NaN where an element is infinite.
+ * Small heads, whose squares underflow, come out right (with eps = 0 too; then a head of zeros is 0 / 0, NaN).
  */
 typedef struct {
     const void* q;

@@ -981,11 +981,12 @@ int run_norm_rope_bwd(const attn_norm_rope_bwd_args_t& g, void* workspace, size_
     p.part = reinterpret_cast<float*>(workspace);
     p.dw[0] = g.dq_weight;
     p.dw[1] = g.dk_weight;
-    p.blocks = norm_bwd_blocks(a, sms);
+    p.blocks = a.S > 0 ? norm_bwd_blocks(a, sms) : 0;      // (no tokens: the weights' gradients are sums of nothing)
+    if (a.S == 0) p.pairs = 0;
     const bool halves = a.pairs && a.pairing == ATTN_ROPE_HALVES;
     auto* kernel = a.d == 128 ? (halves ? attn_norm_rope_bwd_kernel<128, true> : attn_norm_rope_bwd_kernel<128, false>)
                               : (halves ? attn_norm_rope_bwd_kernel<64, true> : attn_norm_rope_bwd_kernel<64, false>);
-    if ((st = launch(kernel, p.blocks, 1, kNormThreads, 0, stream, p)) != ATTN_OK) return st;
+    if (a.S > 0 && (st = launch(kernel, p.blocks, 1, kNormThreads, 0, stream, p)) != ATTN_OK) return st;
     if (!p.dw[0] && !p.dw[1]) return ATTN_OK;
     const int64_t grid = (a.k ? 2 : 1) * (a.d / 32);
     return a.d == 128 ? launch(attn_norm_rope_dw_kernel<128>, grid, 1, 32 * kDwRows, 0, stream, p)

@@ -198,6 +198,7 @@ bool meet(const View& a, const View& b) {
 
 // no two elements of a view on one address: its extents nest
 bool nested(const View& v) {
+    if (!v.span()) return true;
     int order[3] = {0, 1, 2};
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 2 - i; ++j)

@@ -567,13 +567,18 @@ int run_decode(const attn_decode_args_t& a, void* workspace, size_t workspace_by
 
 // ------------------------------------------------------------------------------ shared prefix
 // Where a batch's tiles of the prefix, and two a row for its own keys and its end, are few, the decoding kernel itself reads the
-// prefix's pages for each sequence: one or two kernels instead of three.  us a call in a graph, d = 128, again / shared:
-// 16 sequences of 600 shared keys, 8 K/V heads (896 tiles) 10.1 / 23.0;  64 of 200 (2,048) 21.6 / 27.3;  16 of 2,000 (2,304)
-// 22.4 / 24.6;  2 of 20,000 (2,544) 26.3 / 29.5;  4 of 10,000 (2,592) 25.3 / 24.9;  64 of 5,000, one K/V head (2,688)
-// 25.6 / 23.0;  64 of 600 (3,584) 30.6 / 27.3;  4 of 16,384 (4,160) 35.6 / 28.9;  256 of 32 (6,144) 44.3 / 29.6.
+// prefix's pages for each sequence: one or two kernels instead of three.  A tile costs it the more the more query heads it takes with one, but a
+// batch whose rows it does not split pays a CTA's tiles only.  us a call in a graph, 16 to 100 own keys, again / shared:
+//   blocks of 8 heads, d = 128: 16 sequences of 600 shared keys, 8 K/V heads (896 tiles) 9.2 / 22.9;  64 of 200 (2,048) 20.2 / 26.0;  16 of 2,000
+//   (2,304) 21.8 / 23.3;  2 of 20,000 (2,544) 27.7 / 28.6;  4 of 10,000 (2,592) 25.3 / 23.4;  64 of 600 (3,584) 29.3 / 26.4;  16 of 4,000 (4,352)
+//   35.1 / 24.0.  d = 64: 2,304 16.7 / 20.0;  2,592 18.3 / 19.1;  3,584 22.8 / 21.1.
+//   16 heads, d = 128: 16 of 2,000, 4 K/V heads (1,152) 20.2 / 22.4;  4 of 5,000, 8 (1,344) 22.3 / 21.0;  4 of 6,000 (1,568) 24.5 / 21.6;  16 of 1,500
+//   (1,792) 25.4 / 26.6;  64 of 200 (2,048) 32.0 / 30.2;  16 of 4,000, 4 (2,176) 27.4 / 23.3.  d = 64: 17.2 / 17.0 at 1,344, 20.6 / 18.3 at 2,176.
+//   32 heads, d = 128: 2 of 4,000, 8 K/V heads (544) 28.1 / 21.1;  4 of 2,000 (576) 26.5 / 20.1;  4 of 3,000 (832) 30.1 / 21.7;  4 of 8,000, one of 71
+//   heads (780) 33.1 / 20.2;  not split: 16 of 600 (896) 18.7 / 29.6, 16 of 1,000 (1,280) 24.1 / 30.9.  d = 64: 21.6 / 16.6 at 544, 16.7 / 23.6 at 1,280.
 bool prefix_again(const attn_decode_args_t& a, int64_t prefix_len, int sms) {
-    const int64_t group = a.H / a.Hkv, rows = a.B * a.Hkv * cdiv(group, 8 * head_tiles(group));
-    return a.B == 1 || rows * (cdiv(prefix_len, kDecTile) + 2) <= 17 * sms;
+    const int64_t nh = head_tiles(a.H / a.Hkv), rows = a.B * a.Hkv * cdiv(a.H / a.Hkv, 8 * nh);
+    return a.B == 1 || decode_whole(a, sms) || 2 * rows * (cdiv(prefix_len, kDecTile) + 2) <= (nh == 1 ? 34 : nh == 2 ? 20 : 7) * sms;
 }
 
 // How the prefix's kernel divides: row blocks, and a line of steps over the CTAs.

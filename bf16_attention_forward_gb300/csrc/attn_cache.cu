@@ -75,9 +75,14 @@ int device(int* sms) {
 }
 
 // Each kernel is launched as the programmatic dependent of the one before it in the stream, waits for that one before
-// it touches global memory and before it ends, and only then lets the next one start.  One reads earlier: eviction's
-// select kernel reads lengths and weights while the prepare kernel runs, which only reads them too; what ran before that
+// it touches global memory and before it ends, and only then lets the next one start.  Two differ.
+// Eviction's select kernel reads lengths and weights while the prepare kernel runs, which only reads them too; what ran before that
 // is complete by then, because the prepare kernel's CTAs let select start behind their own wait.
+// The own keys' kernel behind a shared prefix (attn_decode_kernel<.., kOwnKeys>) lets the join start at once, reads lengths, table, queries and
+// caches and writes its parts of the workspace, all before its wait.  That holds as long as the prefix's kernel is the launch directly before it
+// and lets it start only behind a wait of its own (so that what ran before is complete, the last call's join among it, which read
+// that workspace), writes nothing of what it reads or writes, and as long as each of its exits passes its wait (so that the join, which waits
+// for this kernel, has the prefix's parts too).
 // cluster: CTAs of a cluster.
 template <class P>
 int launch_clusters(void (*kernel)(P), int64_t grid, int cluster, int threads, size_t smem, cudaStream_t stream,

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(32 * (kKeys == kOwnKeys ? kOwnWarps<NH> : kDec
     float* red = reinterpret_cast<float*>(smem + G::kRing);
 
     // (kShared: what it reads was complete before the prefix's kernel, all of whose CTAs let this one start behind their
-    // own wait, and what it writes only the join reads)
+    // own wait, and what it writes only the join reads, which waits until every exit below has waited: see launch_clusters)
     if (!kShared) pdl_wait();
     pdl_launch();
     const int rows = p.Hkv * p.head_blocks;

@@ -1054,7 +1054,8 @@ def attn_paged_prefix_decode(q, k_cache, v_cache, seqlens_k, block_table, prefix
                              round: str = "rtne", return_lse: bool = False, stream=None, workspace=None, wait_limit_ms: int = 0,
                              test_hooks: int = 0):
     """:func:`attn_paged_decode` for a batch whose sequences all begin with the same ``prefix_len`` keys (one instruction,
-    one document): those are read once for the whole batch, through ``block_table``'s first row.
+    one document): those are read once for the whole batch (for every 256 of a K/V head's rows, sequences times query heads, again), through
+    ``block_table``'s first row.
 
     Arguments as there; ``seqlens_k`` holds whole lengths (prefix_len or more, or 0: a sequence that has ended gets NaN and -inf),
     and a row's entries from the page that the prefix ends in on are its own (its entries of pages that end inside the

@@ -700,7 +700,7 @@ int run_prefix_decode(const attn_decode_args_t& a, int64_t prefix_len, uint32_t 
     x.test_hooks = (int)test_hooks;
     j.single = plan.single;
     // several warps a row where a row has more parts than a warp has in flight, while the SMs have room (16 warps each):
-    // every warp has the same arithmetic to begin with (with 40: 71.3 us for 68.0 of 768 rows with 40 parts, 61.0 for 57.9 of 2,048 with 20)
+    // every warp has the same arithmetic to begin with (with 40: 66.3 us for 63.8 of 768 rows with 40 parts, 63.4 for 61.3 of 2,048 with 20)
     const int64_t parts = (cdiv(plan.steps - 1, x.per) + 1) * (plan.single ? 2 : 1);
     j.warps = 1;
     while (j.warps < kPfJoinWarps && parts > 8 * j.warps && a.B * a.H * j.warps <= 16 * sms) j.warps *= 2;

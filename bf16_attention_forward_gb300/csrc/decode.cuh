@@ -270,7 +270,7 @@ __device__ __forceinline__ float rescale(float m, float to, float c) {
 
 // kOwnKeys: the own keys behind a shared prefix, as a line of 16-key tiles that the WARPS divide: own keys are often few, and
 // a row's end then costs a warp a few stores instead of a block its barriers (512 sequences of 1 to 200 own keys, 8 K/V
-// heads, 210 MB: 41 us, and 98 with a CTA's rows one after another).  Every row leaves (m, l, o) for the prefix's join.
+// heads, 210 MB: 37 us, and 98 with a CTA's rows one after another).  Every row leaves (m, l, o) for the prefix's join.
 template <int D, int NH, bool kWeights, int kKeys = kAllKeys>
 __global__ void __launch_bounds__(32 * (kKeys == kOwnKeys ? kOwnWarps<NH> : kDecWarps), 1) attn_decode_kernel(const __grid_constant__ DecodeParams p) {
     using G = DecGeo<D>;

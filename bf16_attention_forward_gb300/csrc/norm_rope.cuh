@@ -262,7 +262,7 @@ struct NormStride {
 // Each thread copies its own 16-byte chunks into shared memory two steps ahead and reads only those back: nothing but its own
 // wait_group stands between.  At HBM's rate the SMs have 350 instructions for a warp's kSub heads, so the loop is kept
 // short: weights, cosines and sines multiplied once a token, two products an instruction, addresses by addition.
-// 32,760 tokens of 24 heads (403 MB): 63 us, 95 % of a copy; with the next heads in registers 72, with more steps ahead or more
+// 32,760 tokens of 24 heads (403 MB): 63.6 us, 95 % of a copy; with the next heads in registers 72, with more steps ahead or more
 // blocks 64 to 75 (more rows of the memory are open then).
 constexpr int kNormStages = 3;
 constexpr int kNormHeads = 2;      // of a thread at a time
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks) attn_norm_rope_kern
 
 // The gradient.  A warp takes a token's q heads, then its k heads; a thread sums its 16 elements of q's dw over all of its heads
 // in registers, of k's in shared memory, a block adds up its threads' in a fixed order, and attn_norm_rope_dw_kernel the blocks'.
-// 16,384 tokens of 40 heads (503 MB): 82 us both kernels, 91 % of a copy's rate; q and k in blocks of their own took 93 (a token's
+// 16,384 tokens of 40 heads (503 MB): 83 us both kernels, 91 % of a copy's rate; q and k in blocks of their own took 93 (a token's
 // angles, which wait for its position, take as long as some heads' steps), the next head in registers 105.
 constexpr int kNormBwdStages = 3;
 template <int D, bool kHalves>

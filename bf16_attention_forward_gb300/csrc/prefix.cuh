@@ -12,8 +12,10 @@
 // contiguous range, and leaves one part for each unit that it meets.  Behind each unit's steps the line has kPfEnd more places,
 // for the change of units, which takes as long (without them the CTAs that met one ended 6 to 10 us after the others).
 //
-// Bound.  Every key of the prefix is read once for the batch (2 * d * 2 bytes) and costs 4 * d * B * G flops: with some
-// 285 rows and more the tensor pipe bounds it, with fewer HBM.  So the products run on tcgen05, with queries as the 128
+// Bound.  Every key of the prefix is read once for a block of 256 rows, and from HBM once for the batch while the prefix fits in
+// the L2 (2 * d * 2 bytes); it costs 6 * d * B * G flops (P V twice, below): with some 190 rows and more the tensor pipe bounds it, with fewer
+// HBM.  512 sequences of 40 heads, 8 K/V heads, us of this kernel: 4,000 keys 57, 8,000 98, 16,000 178, 32,000 (131 MB) 351: 2.5 a step of
+// 25 MFLOP a CTA, 80 % of the measured peak, and 15 for first loads, changes of units and last parts.  So the products run on tcgen05, with queries as the 128
 // rows of a tile, S and O in TMEM, P written over S.  Two tiles of P are in work at a time, one softmax warpgroup each,
 // so that the products of one run beside the exponentials of the other:
 //   more than 128 rows: two tiles of rows against one tile of keys;
@@ -75,8 +77,8 @@ constexpr uint32_t kPfTmemCols = 512;          // S0 | S1 | O0 | O1
 template <int D, bool kSingle>
 struct PfGeo {
     // Warpgroups 0, 1: softmax; warp 9 issues the products, and of the other warps those of other schedulers than its own load: three,
-    // or with one tile of rows, where HBM bounds, six in a block of 512 threads (24 sequences of 32 heads, 65,500 keys: 69.3 us,
-    // with three 76.5; but 64 sequences, 16,384 keys, two tiles of rows: 60.6, with three 58.4).
+    // or with one tile of rows, where HBM bounds, six in a block of 512 threads (24 sequences of 32 heads, 65,500 keys: 64.1 us,
+    // with three 70.2; with two tiles of rows no gain: 512 sequences of 40 heads, 8,000 keys: 152.6, with three 151.0).
     static constexpr int kLoaders = kSingle ? 6 : 3, kThreads = kSingle ? 512 : 384;
     static constexpr uint32_t kRegsSoftmax = kSingle ? 160 : 176, kRegsOther = kSingle ? 96 : 128;
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= 65536 / kThreads / 8 * 8 * kThreads, "more registers than at launch");
@@ -604,8 +606,8 @@ struct PrefixJoin {
 // prefix's parts and of the own keys', and are joined through shared memory.  The prefix's parts lie where arithmetic says, so
 // they are on their way while the row's length and span are read.
 constexpr int kPfJoinWarps = 8;
-// kU: parts in flight; 4 where a row has no more, for more rows on an SM.  20,480 rows of 1 or 2 parts of the prefix: 13 us; 2,048
-// rows of 20: 7.
+// kU: parts in flight; 4 where a row has no more, for more rows on an SM.  20,480 rows of 1 or 2 parts of the prefix: 15 us, with 8
+// in flight 19; 2,048 rows of 20: 7.
 template <int D, int kU>
 __global__ void __launch_bounds__(32 * kPfJoinWarps, kU > 4 ? 2 : 3) attn_prefix_join_kernel(const __grid_constant__ PrefixJoin p) {
     constexpr int kQ = D / 64, kC = 4 * kQ;            // a lane's elements: 4 of each 64

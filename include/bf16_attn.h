@@ -748,7 +748,7 @@ int attn_paged_reserve(const attn_reserve_args_t* args, attn_stream_t stream);
 
 /*
  * attn_paged_prefix_decode -- attn_paged_decode for a batch whose sequences all begin with the same prefix_len keys: those
- * are read once for the whole batch, and the products with them run on tiles of all sequences' queries.
+ * are read once for every 256 rows (sequences times a K/V head's query heads), and the products with them run on tiles of all sequences' queries.
  *   q, caches, o, lse, seqlens_k, block_table, round_mode   as in attn_paged_decode (weights: NULL)
  *   prefix_len       1 .. max_pages * page_size: keys 0 .. prefix_len - 1 of every sequence are those of sequence 0, and are
  *                    read through block_table's first row; the other rows' entries of pages that end inside the prefix

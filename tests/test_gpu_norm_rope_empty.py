@@ -18,9 +18,10 @@ def test_gradient_of_no_tokens(attn, d, B, k, weights):  # noqa: F811
     dw = torch.full((2, d + 64), 7.0, device="cuda")
     w = torch.ones(d, device="cuda")
     a = attn.NormRopeBwdArgs()
-    a.q, a.q_out, a.dq, a.q_weight = t.data_ptr(), t.data_ptr() + 1024, t.data_ptr() + 2048, w.data_ptr()
+    at = [t[512 * i:].data_ptr() for i in range(6)]
+    a.q, a.q_out, a.dq, a.q_weight = *at[:3], w.data_ptr()
     if k:
-        a.k, a.k_out, a.dk, a.k_weight = t.data_ptr() + 3072, t.data_ptr() + 4096, t.data_ptr() + 5120, w.data_ptr()
+        a.k, a.k_out, a.dk, a.k_weight = *at[3:], w.data_ptr()
     a.positions, a.freqs, a.axes = pos.data_ptr(), freqs.data_ptr(), axes.data_ptr()
     a.B, a.S, a.H, a.Hkv, a.d, a.pairs, a.num_axes, a.eps = B, 0, 2, 1, d, d // 2, 1, 1e-6
     for s in ("q_stride", "q_out_stride", "k_stride", "k_out_stride", "dq_stride", "dk_stride"):
